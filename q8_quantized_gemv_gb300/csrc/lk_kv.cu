@@ -1,0 +1,208 @@
+// New keys and values into a paged cache, with the per-head norm and the
+// rotation of q and k on the way (include/lk_attn.h, lk_kv_append).
+//
+// A warp takes one head of one row: lane l holds the values l + 32 c, so a
+// rotation pair (i, i + rot/2) is in one lane (rot/2 is a multiple of 32), a
+// neighbour pair in lanes l and l ^ 1, and a Q8 group of 32 values is one
+// value per lane.  Every operation is rounded as the header writes it, so
+// the results are bit-fixed.  A few KB a row: the call is bound by its launch
+// and one chain of dependent loads (lens -> table, beside the row itself).
+#include <cuda_bf16.h>
+
+#include "lk_attn.cuh"
+
+using namespace lk;
+using namespace lkh;
+
+namespace {
+
+struct AppendArgs {
+  const float* q;
+  const float* k;
+  const float* v;
+  long ld;
+  int n_q, n_kv, page_log2, n_pages;
+  void* ck;
+  void* cv;
+  __half* cks;
+  __half* cvs;
+  const int* table;
+  int table_w;
+  const int* lens;
+  int R, p0;
+  const float* cosines;
+  const float* sines;
+  int n_pos, rot, paired;
+  const float* q_gain;
+  const float* k_gain;
+  float eps;
+  float* qr;
+  long heads;  // rows * (n_q + 2 n_kv)
+};
+
+template <int TYPE, int D>
+__device__ __forceinline__ void store_head(void* base, __half* scales, long row, const float (&x)[D / 32], int lane) {
+#pragma unroll
+  for (int c = 0; c < D / 32; ++c) {
+    const long i = row * D + 32 * c + lane;
+    if constexpr (TYPE == LK_KV_F16) ((__half*)base)[i] = __float2half_rn(x[c]);
+    if constexpr (TYPE == LK_KV_BF16) ((__nv_bfloat16*)base)[i] = __float2bfloat16_rn(x[c]);
+    if constexpr (TYPE == LK_KV_Q8) {
+      const __half s = __float2half_rn(fminf(div127(warp_absmax(x[c])), 65504.0f));
+      const float f = __half2float(s);
+      const int z = f > 0.0f ? __float2int_rn(fminf(fmaxf(__fdiv_rn(x[c], f), -127.0f), 127.0f)) : 0;
+      ((int8_t*)base)[i] = (int8_t)z;
+      if (lane == 0) scales[row * (D / 32) + c] = s;
+    }
+  }
+}
+
+template <int TYPE, int D>
+__global__ void __launch_bounds__(256) kv_append_kernel(const AppendArgs a) {
+  constexpr int C = D / 32;
+  asm volatile("griddepcontrol.launch_dependents;" :::);
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const long w = (long)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
+  if (w >= a.heads) return;  // whole warps
+  const int lane = threadIdx.x & 31, per = a.n_q + 2 * a.n_kv;
+  const int t = (int)(w / per), h = (int)(w - (long)t * per);
+  const bool is_q = h < a.n_q, is_v = h >= a.n_q + a.n_kv;
+  const int hh = is_q ? h : is_v ? h - a.n_q - a.n_kv : h - a.n_q;
+  const float* src = (is_q ? a.q : is_v ? a.v : a.k) + t * a.ld + (long)hh * D;
+  // the row itself, beside the chain lens -> table (all in bounds whether or not
+  // the row is left out)
+  float x[C];
+#pragma unroll
+  for (int c = 0; c < C; ++c) x[c] = __ldcg(src + 32 * c + lane);
+  const int b = t / a.R, r = t - b * a.R;
+  const int len = __ldcg(a.lens + b);
+  const int p = len - a.R + r;
+  if (len <= 0 || p < 0 || (p >> a.page_log2) >= a.table_w) return;
+  if (a.rot && p >= a.n_pos - a.p0) return;
+  const int pid = __ldcg(a.table + (long)b * a.table_w + (p >> a.page_log2));
+  if ((unsigned)pid >= (unsigned)a.n_pages) return;
+  if (!is_v) {
+    const float* gain = is_q ? a.q_gain : a.k_gain;
+    if (gain) {
+      double ss = 0.0;
+#pragma unroll
+      for (int c = 0; c < C; ++c) ss = __fma_rn((double)x[c], (double)x[c], ss);
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(FULL, ss, o);
+      const double den = __dsqrt_rn(ss / D + (double)a.eps);
+#pragma unroll
+      for (int c = 0; c < C; ++c)
+        x[c] = __double2float_rn(__ddiv_rn((double)x[c] * (double)__ldg(gain + 32 * c + lane), den));
+    }
+    if (a.rot) {
+      const long at = (long)(a.p0 + p) * (a.rot >> 1);
+      if (a.paired) {
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+          if (32 * c >= a.rot) continue;
+          const int i = (32 * c + lane) >> 1;
+          const float cs = __ldg(a.cosines + at + i), sn = __ldg(a.sines + at + i);
+          const float o = __shfl_xor_sync(FULL, x[c], 1);
+          const float u = __fmul_rn(x[c], cs), z = __fmul_rn(o, sn);
+          x[c] = (lane & 1) ? __fadd_rn(u, z) : __fsub_rn(u, z);
+        }
+      } else {
+        const int hc = a.rot >> 6;  // registers between the values of a pair
+#pragma unroll
+        for (int c = 0; c < C / 2; ++c) {
+          if (c >= hc) continue;
+          const float cs = __ldg(a.cosines + at + 32 * c + lane), sn = __ldg(a.sines + at + 32 * c + lane);
+          // partner register c + hc: hc is 1 (rot 64) or 2 (rot 128)
+          const float y = C == 4 && hc == 2 ? x[(c + 2) % C] : x[(c + 1) % C];
+          const float u = __fsub_rn(__fmul_rn(x[c], cs), __fmul_rn(y, sn));
+          const float z = __fadd_rn(__fmul_rn(y, cs), __fmul_rn(x[c], sn));
+          x[c] = u;
+          if (C == 4 && hc == 2) x[(c + 2) % C] = z;
+          else x[(c + 1) % C] = z;
+        }
+      }
+    }
+  }
+  if (is_q) {
+    float* dst = a.qr + ((long)t * a.n_q + hh) * D;
+#pragma unroll
+    for (int c = 0; c < C; ++c) dst[32 * c + lane] = x[c];
+    return;
+  }
+  const long row = (((long)pid * a.n_kv + hh) << a.page_log2) + (p & ((1 << a.page_log2) - 1));
+  if (is_v) store_head<TYPE, D>(a.cv, a.cvs, row, x, lane);
+  else store_head<TYPE, D>(a.ck, a.cks, row, x, lane);
+}
+
+// rows x span floats at pitch ld from p, against n dense floats from q
+bool rows_overlap(const float* p, long ld, int rows, long span, const float* q, long n) {
+  const float* end = p + (rows - 1) * ld + span;
+  return p < q + n && q < end;
+}
+
+template <int TYPE>
+void launch_append(const AppendArgs& a, int D, int pdl, cudaStream_t stream) {
+  const dim3 grid((unsigned)((a.heads + 7) / 8)), block(256);
+  if (D == 128) launch_pdl(kv_append_kernel<TYPE, 128>, grid, block, stream, pdl, a);
+  else launch_pdl(kv_append_kernel<TYPE, 64>, grid, block, stream, pdl, a);
+}
+
+}  // namespace
+
+extern "C" lk_status lk_kv_append(const lk_kv_cache* cache, const float* q, const float* k, const float* v, long ld,
+                                  int n_q, const int32_t* table, int table_w, const int32_t* lens, int B, int R,
+                                  int p0, const float* cosines, const float* sines, int n_pos, int rot, int paired,
+                                  const float* q_gain, const float* k_gain, float eps, float* qr,
+                                  const lk_launch_cfg* cfg, cudaStream_t stream) {
+  if (check_launch_cfg(cfg)) return LK_ERR_ARG;
+  lk_status st = lkattn::check_cache(cache, n_q);
+  if (st) return st;
+  if ((st = lkattn::check_rows(cache, table, table_w, lens, B, R))) return st;
+  const int D = cache->head_dim;
+  if ((rot != 0 && rot != 64 && rot != 128) || rot > D || p0 < 0 || n_pos < 0) return LK_ERR_SHAPE;
+  const long M = (long)B * R;
+  if (M == 0) return LK_OK;
+  if (!q || !k || !v || !qr || (rot && n_pos && (!cosines || !sines))) return LK_ERR_ARG;
+  if (ld < (long)n_q * D || ld < (long)cache->n_kv * D) return LK_ERR_SHAPE;
+  if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(qr, 16) || ld % 4) return LK_ERR_ALIGN;
+  if ((cosines && !aligned(cosines, 4)) || (sines && !aligned(sines, 4)) || (q_gain && !aligned(q_gain, 4)) ||
+      (k_gain && !aligned(k_gain, 4)))
+    return LK_ERR_ALIGN;
+  const long nq = M * n_q * D;
+  if (rows_overlap(q, ld, (int)M, (long)n_q * D, qr, nq) || rows_overlap(k, ld, (int)M, (long)cache->n_kv * D, qr, nq) ||
+      rows_overlap(v, ld, (int)M, (long)cache->n_kv * D, qr, nq))
+    return LK_ERR_ARG;
+  AppendArgs a;
+  a.q = q;
+  a.k = k;
+  a.v = v;
+  a.ld = ld;
+  a.n_q = n_q;
+  a.n_kv = cache->n_kv;
+  a.page_log2 = lkattn::log2_of(cache->page);
+  a.n_pages = cache->n_pages;
+  a.ck = cache->k;
+  a.cv = cache->v;
+  a.cks = (__half*)cache->ks;
+  a.cvs = (__half*)cache->vs;
+  a.table = table;
+  a.table_w = table_w;
+  a.lens = lens;
+  a.R = R;
+  a.p0 = p0;
+  a.cosines = cosines;
+  a.sines = sines;
+  a.n_pos = n_pos;
+  a.rot = rot;
+  a.paired = paired;
+  a.q_gain = q_gain;
+  a.k_gain = k_gain;
+  a.eps = eps;
+  a.qr = qr;
+  a.heads = M * (n_q + 2 * cache->n_kv);
+  const int pdl = cfg_pdl(cfg);
+  if (cache->type == LK_KV_F16) launch_append<LK_KV_F16>(a, D, pdl, stream);
+  else if (cache->type == LK_KV_BF16) launch_append<LK_KV_BF16>(a, D, pdl, stream);
+  else launch_append<LK_KV_Q8>(a, D, pdl, stream);
+  return launch_status();
+}

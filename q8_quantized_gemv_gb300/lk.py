@@ -1,4 +1,5 @@
-"""Thin ctypes binding of liblk.so (the C ABI declared in include/lk.h).
+"""Thin ctypes binding of liblk.so (the C ABI declared in include/lk.h and,
+for the attention step, include/lk_attn.h).
 
 Each ``lk_*`` function here has the name and argument order of the C entry
 point; it only checks and marshals torch tensors (dtype, device, contiguity,
@@ -118,6 +119,10 @@ def _load():
         "lk_add_rmsnorm_quant": ([P, P, P, I, I, F, I, P, P, P, P, P, P, P], I),
         "lk_swiglu_quant": ([P, P, I, I, L, I, P, P, P, P, P, P], I),
         "lk_gemv_q8_glu": ([P, P, P, P, I, I, I, P, P, P, P, I, P, P, P, P, P, P, P, P], I),
+        "lk_kv_append": ([P, P, P, P, L, I, P, I, P, I, I, I, P, P, I, I, I, P, P, F, P, P, P], I),
+        "lk_attn": ([P, P, I, P, I, P, I, I, F, I, P, P, P, P, P, S, P, P], I),
+        "lk_attn_shared": ([P, P, I, P, I, I, P, I, P, I, I, F, I, P, P, P, P, P, S, P, P], I),
+        "lk_attn_workspace_bytes": ([I, I, I, I, I, I], S),
     }
     for name, (args, res) in sig.items():
         fn = getattr(lib, name)
@@ -135,6 +140,11 @@ def exported_symbols():
             "lk_rmsnorm_quant_gemv_q8", "lk_chain_sync_bytes", "lk_gemv_chain", "lk_trace_read",
             "lk_argmax_noalloc", "lk_gemv_q8_group", "lk_add_rmsnorm_quant", "lk_swiglu_quant",
             "lk_gemv_q8_glu", "lk_splitk_chunks_for", "lk_format_row_bytes", "lk_gemv_blk", "lk_dequant_blk"]
+
+
+def attn_symbols():
+    """The entry points of include/lk_attn.h."""
+    return ["lk_kv_append", "lk_attn", "lk_attn_shared", "lk_attn_workspace_bytes"]
 
 
 def _ok(st, where):
@@ -449,3 +459,155 @@ def lk_dequant_blk(fmt, w, K, out, stream=None):
     """The decoded weights f32 [N, K] of a block-format matrix (test hook)."""
     _ok(_load().lk_dequant_blk(_fmt(fmt), _ptr(w, torch.uint8, "w"), w.shape[0], K, _ptr(out, _F32, "out"),
                                _stream(stream)), "lk_dequant_blk")
+
+
+# ---- the attention step: paged cache, append, attention (include/lk_attn.h) ----------
+
+LK_KV_F16, LK_KV_BF16, LK_KV_Q8 = 0, 1, 2
+_KV_TYPES = {torch.float16: LK_KV_F16, torch.bfloat16: LK_KV_BF16, torch.int8: LK_KV_Q8}
+_I32 = torch.int32
+
+
+class LkKvCache(ctypes.Structure):
+    """The C struct lk_kv_cache."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("ks", ctypes.c_void_p), ("vs", ctypes.c_void_p),
+                ("type", ctypes.c_int), ("n_kv", ctypes.c_int), ("head_dim", ctypes.c_int), ("page", ctypes.c_int),
+                ("n_pages", ctypes.c_int), ("reserved", ctypes.c_int)]
+
+
+class KvCache:
+    """A paged key/value cache over the caller's tensors: k, v [n_pages, n_kv,
+    page, head_dim] in float16, bfloat16, or int8 levels with their float16
+    scales ks, vs [n_pages, n_kv, page, head_dim / 32].  Marshalled once; the
+    tensors are kept alive with it."""
+
+    def __init__(self, k, v, ks=None, vs=None):
+        self.k, self.v, self.ks, self.vs = k, v, ks, vs
+        if not isinstance(k, torch.Tensor) or k.dtype not in _KV_TYPES:
+            raise TypeError("k must be a float16, bfloat16 or int8 tensor")
+        if k.dim() != 4:
+            raise ValueError("k must be [n_pages, n_kv, page, head_dim]")
+        kp, vp = _ptr(k, k.dtype, "k"), _ptr(v, k.dtype, "v")
+        if v.shape != k.shape or v.device != k.device:
+            raise ValueError("v must have the shape and device of k")
+        if (k.dtype == torch.int8) != (ks is not None) or (ks is None) != (vs is None):
+            raise ValueError("ks and vs go with int8 levels")
+        self.device, self.n_kv, self.head_dim = k.device, k.shape[1], k.shape[3]
+        if ks is not None:
+            for name, t in (("ks", ks), ("vs", vs)):
+                if tuple(t.shape) != (*k.shape[:3], k.shape[3] // 32) or t.device != k.device:
+                    raise ValueError(f"{name} must be [n_pages, n_kv, page, head_dim / 32] on the device of k")
+        self.c = LkKvCache(kp, vp, _ptr(ks, torch.float16, "ks"), _ptr(vs, torch.float16, "vs"), _KV_TYPES[k.dtype],
+                           k.shape[1], k.shape[3], k.shape[2], k.shape[0], 0)
+        self.ref = ctypes.byref(self.c)
+
+
+def _on(dev, t, dtype, name, shape=None):
+    """Pointer of a contiguous tensor of that dtype (and shape) on the cache's device."""
+    if t is None:
+        return None
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype:
+        raise TypeError(f"{name} must be a {dtype} tensor")
+    if t.device != dev:
+        raise ValueError(f"{name} must be on {dev}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    return t.data_ptr()
+
+
+def _kv_rows(cache, table, lens, R):
+    """Checks of the arguments every call on a cache takes: (table pointer,
+    table width, lens pointer, B)."""
+    dev = cache.device
+    if torch.cuda.current_device() != dev.index:
+        raise ValueError(f"the cache is on {dev}, which is not the current device")
+    if table.dim() != 2:
+        raise ValueError("table must be [B, pages]")
+    B, w = table.shape
+    if R < 0:
+        raise ValueError("R must not be negative")
+    return _on(dev, table, _I32, "table") if w else None, w, _on(dev, lens, _I32, "lens", (B,)), B
+
+
+def lk_kv_append(cache: KvCache, q, k, v, table, lens, cosines, sines, qr, R=1, p0=0, paired=False, q_gain=None,
+                 k_gain=None, eps=1e-6, stream=None, cfg=None):
+    """Append the rows' keys and values to the cache, rotated, and write the
+    rotated queries to qr [M, n_q * head_dim] (see include/lk_attn.h).  q, k, v: f32
+    rows of one pitch (column ranges of one fused projection output, say);
+    table int32 [B, pages], lens int32 [B] with the R new tokens of each
+    sequence counted; cosines, sines f32 [positions, rot / 2] or None (no
+    rotation)."""
+    tp, tw, lp, B = _kv_rows(cache, table, lens, R)
+    dev, D, M = cache.device, cache.head_dim, B * R
+    ptrs, ld = [], None
+    for name, t in (("q", q), ("k", k), ("v", v)):
+        if not isinstance(t, torch.Tensor) or t.dtype is not _F32 or t.dim() != 2:
+            raise TypeError(f"{name} must be a 2-D float32 tensor")
+        if t.device != dev or t.shape[0] != M or (t.shape[1] > 1 and t.stride(1) != 1):
+            raise ValueError(f"{name} must be {M} rows of contiguous values on {dev}")
+        if M > 1:
+            if ld is not None and t.stride(0) != ld:
+                raise ValueError("q, k and v must have the same row pitch")
+            ld = t.stride(0)
+        ptrs.append(t.data_ptr())
+    if k.shape[1] != cache.n_kv * D or v.shape[1] != cache.n_kv * D or q.shape[1] % D:
+        raise ValueError("q, k and v rows must be heads of head_dim values, k and v n_kv of them")
+    if M <= 1:
+        ld = q.shape[1]
+    rot = n_pos = 0
+    if cosines is not None:
+        if cosines.dim() != 2:
+            raise ValueError("cosines must be [positions, rot / 2]")
+        n_pos, rot = cosines.shape[0], 2 * cosines.shape[1]
+    elif sines is not None:
+        raise ValueError("cosines and sines go together")
+    for name, t in (("q_gain", q_gain), ("k_gain", k_gain)):
+        if t is not None and t.shape != (D,):
+            raise ValueError(f"{name} must be [head_dim]")
+    _ok(_load().lk_kv_append(cache.ref, *ptrs, ld, q.shape[1] // D, tp, tw, lp, B, R, p0,
+                             _on(dev, cosines, _F32, "cosines"),
+                             _on(dev, sines, _F32, "sines", cosines.shape) if cosines is not None else None, n_pos,
+                             rot, 1 if paired else 0, _on(dev, q_gain, _F32, "q_gain"),
+                             _on(dev, k_gain, _F32, "k_gain"), eps, _on(dev, qr, _F32, "qr", q.shape), _cfg(cfg),
+                             _stream(stream)), "lk_kv_append")
+
+
+def lk_attn_workspace_bytes(n_q, n_kv, head_dim, B, R=1, shared=False) -> int:
+    return _load().lk_attn_workspace_bytes(n_q, n_kv, head_dim, B, R, 1 if shared else 0)
+
+
+def _attn_tail(cache, q, M, scale, mode, out, hq, hl, hs, ws):
+    dev, N = cache.device, q.shape[1]
+    qp = _on(dev, q, _F32, "q")
+    if q.shape[0] != M or N % cache.head_dim:
+        raise ValueError(f"q must be {M} rows of heads of head_dim values")
+    if scale is None:
+        scale = cache.head_dim ** -0.5
+    return qp, N // cache.head_dim, (
+        scale, _mode(mode), _on(dev, out, _F32, "out", (M, N)), _on(dev, hq, _I8, "hq", (M, N)),
+        _on(dev, hl, _I8, "hl", (M, N)), _on(dev, hs, _F32, "hs", (M, N // 32)), _on(dev, ws, torch.uint8, "ws"),
+        ws.numel())
+
+
+def lk_attn(cache: KvCache, q, table, lens, ws, R=1, scale=None, mode=LK_DEQUANT, out=None, hq=None, hl=None, hs=None,
+            stream=None, cfg=None):
+    """Attention of the rows q [B * R, n_q * head_dim] over their sequences'
+    cached tokens (see include/lk_attn.h): f32 rows in out and / or, by mode, the
+    next projection's words hq, hl and scales hs.  ws: uint8 workspace of
+    lk_attn_workspace_bytes.  scale None: 1 / sqrt(head_dim)."""
+    tp, tw, lp, B = _kv_rows(cache, table, lens, R)
+    qp, n_q, tail = _attn_tail(cache, q, B * R, scale, mode, out, hq, hl, hs, ws)
+    _ok(_load().lk_attn(cache.ref, qp, n_q, tp, tw, lp, B, R, *tail, _cfg(cfg), _stream(stream)), "lk_attn")
+
+
+def lk_attn_shared(cache: KvCache, q, prefix_table, prefix_len, table, lens, ws, R=1, scale=None, mode=LK_DEQUANT,
+                   out=None, hq=None, hl=None, hs=None, stream=None, cfg=None):
+    """lk_attn for sequences that continue one prefix of prefix_len tokens in
+    the pages prefix_table (int32); table and lens are the sequences' own."""
+    tp, tw, lp, B = _kv_rows(cache, table, lens, R)
+    qp, n_q, tail = _attn_tail(cache, q, B * R, scale, mode, out, hq, hl, hs, ws)
+    _ok(_load().lk_attn_shared(cache.ref, qp, n_q, _on(cache.device, prefix_table, _I32, "prefix_table"),
+                               0 if prefix_table is None else prefix_table.numel(), prefix_len, tp, tw, lp, B, R,
+                               *tail, _cfg(cfg), _stream(stream)), "lk_attn_shared")
