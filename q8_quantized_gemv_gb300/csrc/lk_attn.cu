@@ -1,14 +1,10 @@
 // Attention over the paged cache (include/lk_attn.h): lk_attn,
 // lk_attn_shared.
 //
-// Work.  An item is one key/value head of one sequence with up to 8 of the
-// query rows that read it (row i of a head's R * G: token i / G, query head
-// i % G); a shared prefix is one more sequence with the rows of all others.
-// Its keys come in units of 32.  All units of all items, in a fixed order, are
-// dealt to the blocks in equal contiguous shares, whatever the lengths are;
-// a block's part of an item (a segment) leaves a partial result (running
-// maximum, sum, weighted values) in the workspace, in slot block + item,
-// which no other segment has; a second launch joins the partials of a row.
+// The work and its deal to the blocks are in lk_attn.cuh.  This file has the
+// streaming kernel (up to 8 query rows to a key/value head and unit of keys;
+// the cache's bytes set its time) and the join of the partials; lk_tile.cu has
+// the kernel for many rows on the same keys.
 //
 // Mathematics.  Scores and weighted sums run on m16n8k16 MMAs whose 16 rows
 // are 8 query rows twice: rows 0..7 the high and rows 8..15 the low 16-bit
@@ -39,76 +35,6 @@ using namespace lkh;
 
 namespace lkattn {
 
-constexpr int UNIT = 32;          // keys of a unit
-constexpr int TR = 8;             // query rows of an item
-constexpr int kMaxWorkers = 512;  // blocks of a launch, at most
-constexpr int kMaxSeq = LK_MAX_BATCH + 1;
-
-struct AttnArgs {
-  const float* q;
-  int n_q, n_kv, G;
-  const void* k;
-  const void* v;
-  const __half* ks;
-  const __half* vs;
-  int page_log2, n_pages;
-  const int* table;
-  int table_w;
-  const int* lens;
-  int B, R;
-  const int* ptable;  // prefix: page list, length, tokens it has room for
-  int plen, pcap;
-  int shared;
-  float qscale;  // scale * log2(e)
-  float* ml;     // partials: [slot][TR][2] maximum and sum,
-  float* o;      //           [slot][TR][D] weighted values
-  int W;         // blocks
-};
-
-// The deal of the units: sequence s has un[s] units per item, items before it
-// item0(s), units before it cum[s]; cum[nseq] is their total.
-struct Deal {
-  long cum[kMaxSeq + 1];
-  int un[kMaxSeq];
-  int n[kMaxSeq];
-};
-
-__device__ __forceinline__ int rows_of(const AttnArgs& a, int s) { return (s == a.B ? a.B * a.R : a.R) * a.G; }
-__device__ __forceinline__ int tiles_of(const AttnArgs& a, int s) { return (rows_of(a, s) + TR - 1) / TR; }
-__device__ __forceinline__ int item0(const AttnArgs& a, int s) { return s * a.n_kv * tiles_of(a, 0); }
-
-// Blocks that have a share: none is empty, so an item's segments are in
-// consecutive blocks.
-__device__ __forceinline__ long shares(const AttnArgs& a, long T) { return T < a.W ? T : a.W; }
-
-// By the block's first warp; the caller synchronizes.
-__device__ __forceinline__ void make_deal(const AttnArgs& a, Deal& d) {
-  if (threadIdx.x >= 32) return;
-  const int lane = threadIdx.x, nseq = a.B + a.shared;
-  const int cap = a.table_w << a.page_log2;
-  long run = 0;
-  for (int s0 = 0; s0 < nseq; s0 += 32) {
-    const int s = s0 + lane;
-    int n = 0;
-    long u = 0;
-    if (s < nseq) {
-      n = s == a.B ? min(a.plen, a.pcap) : min(max(__ldcg(a.lens + s), 0), cap);
-      d.n[s] = n;
-      d.un[s] = (n + UNIT - 1) / UNIT;
-      u = (long)d.un[s] * a.n_kv * tiles_of(a, s);
-    }
-    long sum = u;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long up = __shfl_up_sync(FULL, sum, o);
-      if (lane >= o) sum += up;
-    }
-    if (s < nseq) d.cum[s] = run + sum - u;
-    run += __shfl_sync(FULL, sum, 31);
-  }
-  if (lane == 0) d.cum[nseq] = run;
-}
-
 // ---- MMA and copies -----------------------------------------------------------------
 template <int TYPE>
 __device__ __forceinline__ void mma16(float (&c)[4], unsigned a0, unsigned a1, unsigned a2, unsigned a3, unsigned b0,
@@ -123,38 +49,8 @@ __device__ __forceinline__ void mma16(float (&c)[4], unsigned a0, unsigned a1, u
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// (x, y) rounded to the type, packed, and what the rounding left of them
-template <int TYPE>
-__device__ __forceinline__ unsigned split2(float& x, float& y) {
-  if constexpr (TYPE == LK_KV_BF16) {
-    const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
-    x -= __low2float(h);
-    y -= __high2float(h);
-    return *(const unsigned*)&h;
-  } else {
-    const __half2 h = __floats2half2_rn(x, y);
-    x -= __low2float(h);
-    y -= __high2float(h);
-    return *(const unsigned*)&h;
-  }
-}
-
 __device__ __forceinline__ unsigned prmt(unsigned a, unsigned b, unsigned s) { return __byte_perm(a, b, s); }
 
-// 16 bytes global -> shared; with bytes 0 nothing is read and zeros are written
-__device__ __forceinline__ void cp16(unsigned dst, const void* src, int bytes) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-}
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-__device__ __forceinline__ float ex2(float x) {
-  float r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-  return r;
-}
 __device__ __forceinline__ uint4 lds128(unsigned a) {
   uint4 r;
   asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "r"(a));
@@ -204,11 +100,11 @@ __global__ void __launch_bounds__(32 * Cfg<TYPE, D>::NW, 1) attn_kernel(const At
   __shared__ float wml[C::NW][TR][2];
   asm volatile("griddepcontrol.launch_dependents;" :::);
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  make_deal(a, deal);
+  if (threadIdx.x < 32) make_deal<false>(a, deal);
   __syncthreads();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
   const int nseq = a.B + a.shared;
-  const long T = deal.cum[nseq], W = shares(a, T);
+  const long T = deal.cum[nseq], W = shares(a.W, T);
   if (blockIdx.x >= W) return;
   long u0 = T * blockIdx.x / W;
   const long u1 = T * (blockIdx.x + 1) / W;
@@ -221,8 +117,8 @@ __global__ void __launch_bounds__(32 * Cfg<TYPE, D>::NW, 1) attn_kernel(const At
     const int li = (int)(rel / un), ub = (int)(rel - (long)li * un);
     const int ue = (int)min((long)un, ub + (u1 - u0));
     u0 += ue - ub;
-    const int tiles = tiles_of(a, s), kvh = li / tiles, tile = li - kvh * tiles;
-    const int slot = (int)blockIdx.x + item0(a, s) + li;
+    const int tiles = groups_of<false>(a, s), kvh = li / tiles, tile = li - kvh * tiles;
+    const int slot = (int)blockIdx.x + item0<false>(a, s) + li;
     const bool pre = s == a.B;
     const int nrows = min(TR, rows_of(a, s) - tile * TR);
     const int* table = pre ? a.ptable : a.table + (long)s * a.table_w;
@@ -253,22 +149,20 @@ __global__ void __launch_bounds__(32 * Cfg<TYPE, D>::NW, 1) attn_kernel(const At
       if constexpr (TYPE != LK_KV_BF16) {
         amax = fmaxf(amax, __shfl_xor_sync(FULL, amax, 1));
         amax = fmaxf(amax, __shfl_xor_sync(FULL, amax, 2));
-        const int e = min(max((int)(__float_as_uint(amax) >> 23), 27), 227) - 127;  // amax in [2^e, 2^(e+1))
-        rs = __uint_as_float((unsigned)(127 + e - 10) << 23);
-        const float up = __uint_as_float((unsigned)(127 - e + 10) << 23);
+        const float up = row_shift(amax, rs);
 #pragma unroll
         for (int i = 0; i < D / 4; ++i) x[i] *= up;
       }
       // k-step k: registers 4 k .. 4 k + 3 are the lane's four inner indices
 #pragma unroll
       for (int k = 0; k < KS; ++k) {
-        qa[k][0] = split2<TYPE>(x[4 * k], x[4 * k + 1]);
-        qa[k][2] = split2<TYPE>(x[4 * k + 2], x[4 * k + 3]);
-        qa[k][1] = split2<TYPE>(x[4 * k], x[4 * k + 1]);
-        qa[k][3] = split2<TYPE>(x[4 * k + 2], x[4 * k + 3]);
+        qa[k][0] = split2<TYPE == LK_KV_BF16>(x[4 * k], x[4 * k + 1]);
+        qa[k][2] = split2<TYPE == LK_KV_BF16>(x[4 * k + 2], x[4 * k + 3]);
+        qa[k][1] = split2<TYPE == LK_KV_BF16>(x[4 * k], x[4 * k + 1]);
+        qa[k][3] = split2<TYPE == LK_KV_BF16>(x[4 * k + 2], x[4 * k + 3]);
         if constexpr (QT == 3) {
-          qc[k][0] = split2<TYPE>(x[4 * k], x[4 * k + 1]);
-          qc[k][1] = split2<TYPE>(x[4 * k + 2], x[4 * k + 3]);
+          qc[k][0] = split2<TYPE == LK_KV_BF16>(x[4 * k], x[4 * k + 1]);
+          qc[k][1] = split2<TYPE == LK_KV_BF16>(x[4 * k + 2], x[4 * k + 3]);
         }
       }
     }
@@ -462,10 +356,10 @@ __global__ void __launch_bounds__(32 * Cfg<TYPE, D>::NW, 1) attn_kernel(const At
         unsigned ph[2][4];
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-          ph[k][0] = split2<TYPE>(p[2 * k][0], p[2 * k][1]);
-          ph[k][2] = split2<TYPE>(p[2 * k + 1][0], p[2 * k + 1][1]);
-          ph[k][1] = split2<TYPE>(p[2 * k][0], p[2 * k][1]);
-          ph[k][3] = split2<TYPE>(p[2 * k + 1][0], p[2 * k + 1][1]);
+          ph[k][0] = split2<TYPE == LK_KV_BF16>(p[2 * k][0], p[2 * k][1]);
+          ph[k][2] = split2<TYPE == LK_KV_BF16>(p[2 * k + 1][0], p[2 * k + 1][1]);
+          ph[k][1] = split2<TYPE == LK_KV_BF16>(p[2 * k][0], p[2 * k][1]);
+          ph[k][3] = split2<TYPE == LK_KV_BF16>(p[2 * k + 1][0], p[2 * k + 1][1]);
         }
 #pragma unroll
         for (int h = 0; h < D / 64; ++h) {
@@ -523,10 +417,10 @@ __global__ void __launch_bounds__(32 * Cfg<TYPE, D>::NW, 1) attn_kernel(const At
               y[2 * i] = p[2 * k + i][0] * (e0 * dsc);
               y[2 * i + 1] = p[2 * k + i][1] * (e1 * dsc);
             }
-            ph[k][0] = split2<TYPE>(y[0], y[1]);
-            ph[k][2] = split2<TYPE>(y[2], y[3]);
-            ph[k][1] = split2<TYPE>(y[0], y[1]);
-            ph[k][3] = split2<TYPE>(y[2], y[3]);
+            ph[k][0] = split2<TYPE == LK_KV_BF16>(y[0], y[1]);
+            ph[k][2] = split2<TYPE == LK_KV_BF16>(y[2], y[3]);
+            ph[k][1] = split2<TYPE == LK_KV_BF16>(y[0], y[1]);
+            ph[k][3] = split2<TYPE == LK_KV_BF16>(y[2], y[3]);
           }
           unsigned w[8];
 #pragma unroll
@@ -623,63 +517,100 @@ struct JoinArgs {
   float* hs;
 };
 
+// Partials of a row from one item: entry i (0 <= i < n) has its maximum and
+// sum at ml + 2 r and its values at o + r * D, r = first + (i / per) * step + (i % per) *
+// hop; flip: the values' 16-byte pieces are permuted by this (tile partials).
+struct Source {
+  const float* ml;
+  const float* o;
+  long first;
+  int n, per, step, hop, flip;
+  __device__ __forceinline__ long at(int i) const {
+    const int j = per == 1 ? i : i >> 1;
+    return first + (long)j * step + (i - j * per) * hop;
+  }
+};
+
+// Row i of key/value head kvh in sequence s of the streaming (tile) deal.
+template <bool TILED>
+__device__ __forceinline__ Source source(const AttnArgs& a, const Deal& d, int s, int kvh, int i) {
+  Source r = {};
+  const int un = d.un[s];
+  if (un == 0) return r;
+  constexpr int N = TILED ? TROWS : TR;
+  const long T = d.cum[a.B + a.shared], W = shares(TILED ? a.TW : a.W, T);
+  const int group = i / N, li = kvh * groups_of<TILED>(a, s) + group, ig = i - group * N;
+  const long ub = d.cum[s] + (long)li * un;
+  // the last w with T * w / W <= u has unit u
+  const int w0 = (int)(((ub + 1) * W - 1) / T), w1 = (int)(((ub + un) * W - 1) / T);
+  const long slot = w0 + item0<TILED>(a, s) + li;
+  r.n = w1 - w0 + 1;
+  r.per = 1;
+  if constexpr (TILED) {
+    const int rows = rows_of(a, s), rg = min(TROWS, rows - group * TROWS), which = s == a.B ? 1 : 0;
+    r.step = tile_slot_rows(rows);
+    r.ml = a.tml[which];
+    r.o = a.to[which];
+    r.flip = rg > 128 ? ig & 127 & 7 : ig & 7;
+    if (rg <= 128) r.per = 2, r.hop = rg, r.n *= 2;
+  } else {
+    r.step = TR;
+    r.ml = a.ml;
+    r.o = a.o;
+  }
+  r.first = slot * r.step + ig;
+  return r;
+}
+
 template <int Q, int D>
 __global__ void __launch_bounds__(128) attn_join_kernel(const JoinArgs j) {
   const AttnArgs& a = j.a;
-  __shared__ Deal deal;
+  __shared__ Deal deal, tdeal;
   asm volatile("griddepcontrol.launch_dependents;" :::);
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  make_deal(a, deal);
+  if (threadIdx.x < 32) make_deal<false>(a, deal);
+  else if (threadIdx.x < 64 && (a.own_tiled || a.pre_tiled)) make_deal<true>(a, tdeal);
   __syncthreads();
   const int lane = threadIdx.x & 31;
   const long w = (long)blockIdx.x * 4 + (threadIdx.x >> 5);
   if (w >= (long)a.B * a.R * a.n_q) return;
   const int row = (int)(w / a.n_q), h = (int)(w - (long)row * a.n_q), kvh = h / a.G, hg = h - kvh * a.G;
   const int b = row / a.R, r = row - b * a.R;
-  const long T = deal.cum[a.B + a.shared], W = shares(a, T);
-  // the slots of the row's own item, then of its prefix item
-  int first[2] = {0, 0}, count[2] = {0, 0}, rt[2] = {0, 0};
-#pragma unroll
-  for (int x = 0; x < 2; ++x) {
-    const int s = x == 0 ? b : a.B;
-    if (x == 1 && (!a.shared || __ldcg(a.lens + b) < 0)) continue;
-    const int un = deal.un[s];
-    if (un == 0) continue;
-    const int i = (x == 0 ? r : row) * a.G + hg;
-    const int li = kvh * tiles_of(a, s) + i / TR;
-    const long ub = deal.cum[s] + (long)li * un;
-    // the last w with T * w / W <= u has unit u
-    const int w0 = (int)(((ub + 1) * W - 1) / T), w1 = (int)(((ub + un) * W - 1) / T);
-    first[x] = w0 + item0(a, s) + li;
-    count[x] = w1 - w0 + 1;
-    rt[x] = i % TR;
-  }
-  const int total = count[0] + count[1];
-  auto at = [&](int i) -> long {
-    return i < count[0] ? (long)(first[0] + i) * TR + rt[0] : (long)(first[1] + i - count[0]) * TR + rt[1];
-  };
+  // the row's own item, then its prefix item
+  Source src[2] = {};
+  const int io = r * a.G + hg, ip = row * a.G + hg;
+  src[0] = a.own_tiled ? source<true>(a, tdeal, b, kvh, io) : source<false>(a, deal, b, kvh, io);
+  if (a.shared && __ldcg(a.lens + b) >= 0)
+    src[1] = a.pre_tiled ? source<true>(a, tdeal, a.B, kvh, ip) : source<false>(a, deal, a.B, kvh, ip);
   float M = -INFINITY;
-  for (int i = lane; i < total; i += 32) M = fmaxf(M, __ldcg(a.ml + at(i) * 2));
+#pragma unroll
+  for (int x = 0; x < 2; ++x)
+    for (int i = lane; i < src[x].n; i += 32) M = fmaxf(M, __ldcg(src[x].ml + src[x].at(i) * 2));
   M = warp_max_xor(M);
   const float ref = M == -INFINITY ? 0.0f : M;
   float acc[D / 32], ls = 0.0f;
 #pragma unroll
   for (int c = 0; c < D / 32; ++c) acc[c] = 0.0f;
-  for (int i0 = 0; i0 < total; i0 += 32) {
-    float f = 0.0f, lf = 0.0f;
-    if (i0 + lane < total) {
-      const long p = at(i0 + lane) * 2;
-      f = ex2(__ldcg(a.ml + p) - ref);
-      lf = f * __ldcg(a.ml + p + 1);
-    }
-    const int n = min(32, total - i0);
-#pragma unroll 4
-    for (int i = 0; i < n; ++i) {
-      const float fi = __shfl_sync(FULL, f, i);
-      ls += __shfl_sync(FULL, lf, i);
-      const float* o = a.o + at(i0 + i) * D + lane;
 #pragma unroll
-      for (int c = 0; c < D / 32; ++c) acc[c] = fmaf(fi, __ldcg(o + 32 * c), acc[c]);
+  for (int x = 0; x < 2; ++x) {
+    const Source& z = src[x];
+    const int dl = lane ^ (z.flip << 2);  // the lane's place within 32 values
+    for (int i0 = 0; i0 < z.n; i0 += 32) {
+      float f = 0.0f, lf = 0.0f;
+      if (i0 + lane < z.n) {
+        const float2 p = __ldcg((const float2*)(z.ml + z.at(i0 + lane) * 2));
+        f = ex2(p.x - ref);
+        lf = f * p.y;
+      }
+      const int n = min(32, z.n - i0);
+#pragma unroll 4
+      for (int i = 0; i < n; ++i) {
+        const float fi = __shfl_sync(FULL, f, i);
+        ls += __shfl_sync(FULL, lf, i);
+        const float* o = z.o + z.at(i0 + i) * D + dl;
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) acc[c] = fmaf(fi, __ldcg(o + 32 * c), acc[c]);
+      }
     }
   }
 #pragma unroll
@@ -691,69 +622,78 @@ __global__ void __launch_bounds__(128) attn_join_kernel(const JoinArgs j) {
 }
 
 // ---- host --------------------------------------------------------------------------
-long items_of(int n_q, int n_kv, int B, int R, int shared) {
-  const int G = n_q / n_kv;
-  long n = (long)B * n_kv * ((R * G + TR - 1) / TR);
-  if (shared) n += (long)n_kv * (((long)B * R * G + TR - 1) / TR);
-  return n;
+// Whether rows on the same keys go to the tile kernel.
+bool tiled(long rows, int type) { return type != LK_KV_Q8 && rows > 16; }
+
+struct Plan {
+  long slots, tslots[2];  // streaming partials; tile partials of sequences, prefix
+  int tsr[2];             // rows of a tile slot
+};
+
+Plan plan(int n_q, int n_kv, int B, int R, int shared, int type) {
+  const long G = n_q / n_kv, rows[2] = {R * G, (long)B * R * G}, many[2] = {(long)B * n_kv, shared ? n_kv : 0};
+  Plan p = {};
+  p.slots = kMaxWorkers;
+  for (int x = 0; x < 2; ++x) {
+    p.slots += many[x] * ((rows[x] + TR - 1) / TR);
+    if (!many[x] || !tiled(rows[x], type)) continue;
+    p.tsr[x] = tile_slot_rows(rows[x]);
+    p.tslots[x] = kTileWorkers + many[x] * ((rows[x] + TROWS - 1) / TROWS);
+  }
+  return p;
 }
 
-template <typename F>
-bool allow_shared(F f, std::atomic<int> (&done)[kMaxDevices], int bytes) {
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return false;
-  if (done[dev].load(std::memory_order_acquire)) return true;
-  if (cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) return false;
-  done[dev].store(1, std::memory_order_release);
-  return true;
-}
+size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 
-template <typename A>
-cudaError_t launch(void (*f)(A), dim3 grid, dim3 block, int smem, int pdl, cudaStream_t stream, const A& args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = block;
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = pdl ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, f, args);
+// Byte offsets of the workspace's parts; returns its size.
+size_t layout(const Plan& p, int D, size_t (&ml)[3], size_t (&o)[3]) {
+  size_t at = 0;
+  for (int x = 0; x < 3; ++x) {
+    const size_t rows = x == 0 ? (size_t)p.slots * TR : (size_t)p.tslots[x - 1] * p.tsr[x - 1];
+    ml[x] = at;
+    at += up256(rows * 8);
+    o[x] = at;
+    at += up256(rows * D * 4);
+  }
+  return at;
 }
 
 template <int TYPE, int D>
 lk_status run_type(const AttnArgs& a, int pdl, cudaStream_t stream) {
   static std::atomic<int> done[kMaxDevices];
   typedef Cfg<TYPE, D> C;
-  if (!allow_shared(attn_kernel<TYPE, D>, done, C::RING)) return LK_ERR_CUDA;
-  if (launch(attn_kernel<TYPE, D>, dim3(a.W), dim3(32 * C::NW), C::RING, pdl, stream, a) != cudaSuccess) {
-    cudaGetLastError();
-    return LK_ERR_CUDA;
-  }
-  return LK_OK;
+  if (!prepare_kernel(attn_kernel<TYPE, D>, done, C::RING)) return LK_ERR_CUDA;
+  return launch(attn_kernel<TYPE, D>, dim3(a.W), dim3(32 * C::NW), C::RING, pdl, stream, a) == cudaSuccess
+             ? LK_OK
+             : LK_ERR_CUDA;
+}
+
+template <int Q, int D>
+lk_status run_join(const JoinArgs& j, cudaStream_t stream) {
+  static std::atomic<int> done[kMaxDevices];
+  if (!prepare_kernel(attn_join_kernel<Q, D>, done, 0)) return LK_ERR_CUDA;
+  const long heads = (long)j.a.B * j.a.R * j.a.n_q;
+  return launch(attn_join_kernel<Q, D>, dim3((unsigned)((heads + 3) / 4)), dim3(128), 0, 1, stream, j) == cudaSuccess
+             ? LK_OK
+             : LK_ERR_CUDA;
 }
 
 template <int D>
 lk_status run_d(const AttnArgs& a, int type, lk_mode mode, const JoinArgs& j, int pdl, cudaStream_t stream) {
-  const lk_status st = type == LK_KV_F16    ? run_type<LK_KV_F16, D>(a, pdl, stream)
-                       : type == LK_KV_BF16 ? run_type<LK_KV_BF16, D>(a, pdl, stream)
-                                            : run_type<LK_KV_Q8, D>(a, pdl, stream);
-  if (st) return st;
-  const long heads = (long)a.B * a.R * a.n_q;
-  const dim3 grid((unsigned)((heads + 3) / 4)), block(128);
-  const cudaError_t e = mode == LK_DEQUANT   ? launch(attn_join_kernel<0, D>, grid, block, 0, 1, stream, j)
-                        : mode == LK_INT8ACT ? launch(attn_join_kernel<1, D>, grid, block, 0, 1, stream, j)
-                                             : launch(attn_join_kernel<2, D>, grid, block, 0, 1, stream, j);
-  if (e != cudaSuccess) {
-    cudaGetLastError();
-    return LK_ERR_CUDA;
+  lk_status st = LK_OK;
+  // the launches after the first are dependents of the one before
+  if (!a.own_tiled || (a.shared && !a.pre_tiled)) {
+    st = type == LK_KV_F16    ? run_type<LK_KV_F16, D>(a, pdl, stream)
+         : type == LK_KV_BF16 ? run_type<LK_KV_BF16, D>(a, pdl, stream)
+                              : run_type<LK_KV_Q8, D>(a, pdl, stream);
+    pdl = 1;
   }
-  return LK_OK;
+  if (!st && (a.own_tiled || a.pre_tiled)) st = launch_tiles(a, type, D, pdl, stream);
+  if (st) return st;
+  return mode == LK_DEQUANT   ? run_join<0, D>(j, stream)
+         : mode == LK_INT8ACT ? run_join<1, D>(j, stream)
+                              : run_join<2, D>(j, stream);
 }
-
-size_t ml_bytes(long slots) { return ((size_t)slots * TR * 8 + 255) / 256 * 256; }
 
 }  // namespace lkattn
 
@@ -764,8 +704,8 @@ extern "C" {
 size_t lk_attn_workspace_bytes(int n_q, int n_kv, int head_dim, int B, int R, int shared) {
   if ((head_dim != 64 && head_dim != 128) || n_kv < 1 || n_q < n_kv || n_q % n_kv || n_q > 4096) return 0;
   if (B < 0 || R < 0 || B > LK_MAX_BATCH || R > LK_MAX_BATCH || B * R > LK_MAX_BATCH) return 0;
-  const long slots = kMaxWorkers + items_of(n_q, n_kv, B, R, shared != 0);
-  return ml_bytes(slots) + (size_t)slots * TR * head_dim * 4;
+  size_t ml[3], o[3];
+  return layout(plan(n_q, n_kv, B, R, shared != 0, LK_KV_F16), head_dim, ml, o);  // of any type's the largest
 }
 
 lk_status lk_attn_shared(const lk_kv_cache* cache, const float* q, int n_q, const int32_t* prefix_table,
@@ -810,13 +750,24 @@ lk_status lk_attn_shared(const lk_kv_cache* cache, const float* q, int n_q, cons
   a.R = R;
   a.ptable = prefix_table;
   a.plen = prefix_len;
-  a.pcap = prefix_len;
   a.shared = shared;
   a.qscale = scale * 1.44269504088896340736f;
+  const Plan p = plan(n_q, cache->n_kv, B, R, shared, cache->type);
+  size_t ml[3], o[3];
+  layout(p, cache->head_dim, ml, o);
+  a.own_tiled = p.tslots[0] > 0;
+  a.pre_tiled = p.tslots[1] > 0;
+  a.ml = (float*)((char*)ws + ml[0]);
+  a.o = (float*)((char*)ws + o[0]);
+  for (int x = 0; x < 2; ++x) {
+    a.tml[x] = (float*)((char*)ws + ml[x + 1]);
+    a.to[x] = (float*)((char*)ws + o[x + 1]);
+  }
   a.W = d->sm_count < kMaxWorkers ? d->sm_count : kMaxWorkers;
-  const long slots = kMaxWorkers + items_of(n_q, cache->n_kv, B, R, shared);
-  a.ml = (float*)ws;
-  a.o = (float*)((char*)ws + ml_bytes(slots));
+  a.TW = d->sm_count < kTileWorkers ? d->sm_count : kTileWorkers;
+  a.wait_ns = opt_wait_us > 0 ? (unsigned long long)opt_wait_us * 1000ull : 2000000000ull;
+  a.err = error_word_ptr();
+  if (!a.err) return LK_ERR_CUDA;
   JoinArgs j;
   j.a = a;
   j.out = out;

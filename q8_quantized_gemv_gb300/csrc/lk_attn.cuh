@@ -1,6 +1,8 @@
 // Host checks and work partition shared by the attention step's kernels.
 #pragma once
 
+#include <cuda_bf16.h>
+
 #include "lk_attn.h"
 #include "lk_device.cuh"
 #include "lk_host.h"
@@ -35,5 +37,183 @@ inline lk_status check_rows(const lk_kv_cache* c, const int32_t* table, int tabl
   if (!lkh::aligned(lens, 4) || (table && !lkh::aligned(table, 4))) return LK_ERR_ALIGN;
   return LK_OK;
 }
+
+// ---- the work of a call and its deal ---------------------------------------------------
+// An item is one key/value head of one sequence (a shared prefix is one more,
+// number B) with a group of the query rows that read it: row i of a head's
+// R * G (prefix: B * R * G): token i / G, query head i % G.  The streaming
+// kernel's items have up to 8 rows and their keys come in units of 32, the tile
+// kernel's 256 rows and units of 128.  A sequence belongs to one of the two.
+// All units of a kernel's items, in a fixed order, are dealt to its blocks in
+// equal contiguous shares, whatever the lengths are; a block's part of an
+// item (a segment) leaves a partial result (running maximum, sum, weighted
+// values) in the workspace, in slot block + item, which no other segment has;
+// a last launch joins the partials of a row.
+constexpr int UNIT = 32;           // keys of a unit, streaming kernel
+constexpr int TR = 8;              // its query rows of an item
+constexpr int TUNIT = 128;         // keys of a unit, tile kernel
+constexpr int TROWS = 256;         // its query rows of an item
+constexpr int kMaxWorkers = 512;   // blocks of the streaming launch, at most
+constexpr int kTileWorkers = 192;  // blocks of a tile launch, at most
+constexpr int kMaxSeq = LK_MAX_BATCH + 1;
+
+// Rows of a tile slot: with up to 128 query rows the keys' tiles are halved
+// between two streams, each with a partial of the rows.
+__host__ __device__ inline int tile_slot_rows(long rows) { return rows <= 128 ? 2 * (int)rows : TROWS; }
+
+struct AttnArgs {
+  const float* q;
+  int n_q, n_kv, G;
+  const void* k;
+  const void* v;
+  const __half* ks;
+  const __half* vs;
+  int page_log2, n_pages;
+  const int* table;
+  int table_w;
+  const int* lens;
+  int B, R;
+  const int* ptable;  // prefix: page list, length
+  int plen;
+  int shared;
+  float qscale;       // scale * log2(e)
+  int own_tiled, pre_tiled;  // which kernel has the sequences, the prefix
+  float* ml;          // streaming partials: [slot][TR][2] maximum and sum,
+  float* o;           //   [slot][TR][D] weighted values
+  float* tml[2];      // tile partials of the sequences, the prefix: [slot][slot rows][2],
+  float* to[2];       //   [slot][slot rows][D], 16-byte pieces permuted in 128 bytes by row & 7
+  int W, TW;          // blocks of the streaming and of the tile launch
+  unsigned long long wait_ns;
+  int* err;
+};
+
+// Sequence s has un[s] units per item (0 where the other kernel has it) and
+// n[s] keys; units before it cum[s]; cum[nseq] is their total.
+struct Deal {
+  long cum[kMaxSeq + 1];
+  int un[kMaxSeq];
+  int n[kMaxSeq];
+};
+
+__device__ __forceinline__ int rows_of(const AttnArgs& a, int s) { return (s == a.B ? a.B * a.R : a.R) * a.G; }
+template <bool TILED>
+__device__ __forceinline__ int groups_of(const AttnArgs& a, int s) {
+  constexpr int N = TILED ? TROWS : TR;
+  return (rows_of(a, s) + N - 1) / N;
+}
+// Items before sequence s: of the streaming kernel in one row, of the tile
+// kernel the prefix's apart.
+template <bool TILED>
+__device__ __forceinline__ int item0(const AttnArgs& a, int s) {
+  if (TILED && s == a.B) return 0;
+  return s * a.n_kv * groups_of<TILED>(a, 0);
+}
+
+// Blocks that have a share: none is empty, so an item's segments are in
+// consecutive blocks.
+__device__ __forceinline__ long shares(int W, long T) { return T < W ? T : W; }
+
+// By one whole warp; the caller synchronizes.
+template <bool TILED>
+__device__ __forceinline__ void make_deal(const AttnArgs& a, Deal& d) {
+  const int lane = threadIdx.x & 31, nseq = a.B + a.shared;
+  const int cap = a.table_w << a.page_log2;
+  long run = 0;
+  for (int s0 = 0; s0 < nseq; s0 += 32) {
+    const int s = s0 + lane;
+    long u = 0;
+    if (s < nseq) {
+      const int n = s == a.B ? a.plen : min(max(__ldcg(a.lens + s), 0), cap);
+      constexpr int U = TILED ? TUNIT : UNIT;
+      const bool mine = ((s == a.B ? a.pre_tiled : a.own_tiled) != 0) == TILED;
+      d.n[s] = n;
+      d.un[s] = mine ? (n + U - 1) / U : 0;
+      u = (long)d.un[s] * a.n_kv * groups_of<TILED>(a, s);
+    }
+    long sum = u;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long up = __shfl_up_sync(lk::FULL, sum, o);
+      if (lane >= o) sum += up;
+    }
+    if (s < nseq) d.cum[s] = run + sum - u;
+    run += __shfl_sync(lk::FULL, sum, 31);
+  }
+  if (lane == 0) d.cum[nseq] = run;
+}
+
+// ---- instructions both kernels use ----------------------------------------------------
+// (x, y) rounded to the 16-bit type, packed, and what the rounding left of them
+template <bool BF>
+__device__ __forceinline__ unsigned split2(float& x, float& y) {
+  if constexpr (BF) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
+    x -= __low2float(h);
+    y -= __high2float(h);
+    return *(const unsigned*)&h;
+  } else {
+    const __half2 h = __floats2half2_rn(x, y);
+    x -= __low2float(h);
+    y -= __high2float(h);
+    return *(const unsigned*)&h;
+  }
+}
+// 16 bytes global -> shared; with bytes 0 nothing is read and zeros are written
+__device__ __forceinline__ void cp16(unsigned dst, const void* src, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ float ex2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+// Shift of a row's queries before f16 splitting: 2^10 / amax's power of two
+// (returned), and its inverse for the scores.
+__device__ __forceinline__ float row_shift(float amax, float& back) {
+  const int e = min(max((int)(__float_as_uint(amax) >> 23), 27), 227) - 127;  // amax in [2^e, 2^(e+1))
+  back = __uint_as_float((unsigned)(127 + e - 10) << 23);
+  return __uint_as_float((unsigned)(127 - e + 10) << 23);
+}
+
+// ---- host -------------------------------------------------------------------------------
+template <typename A>
+cudaError_t launch(void (*f)(A), dim3 grid, dim3 block, int smem, int pdl, cudaStream_t stream, const A& args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = pdl ? 1 : 0;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, f, args);
+  if (e != cudaSuccess) cudaGetLastError();
+  return e;
+}
+
+// Once per kernel and device: its dynamic shared memory (0: none) and the
+// carveout of the GEMV kernels around it.
+template <typename F>
+bool prepare_kernel(F f, std::atomic<int> (&done)[lkh::kMaxDevices], int smem) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= lkh::kMaxDevices) return false;
+  if (done[dev].load(std::memory_order_acquire)) return true;
+  if (smem && cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return false;
+  if (cudaFuncSetAttribute(f, cudaFuncAttributePreferredSharedMemoryCarveout, (int)cudaSharedmemCarveoutMaxShared) !=
+      cudaSuccess)
+    return false;
+  done[dev].store(1, std::memory_order_release);
+  return true;
+}
+
+// The tile kernel (lk_tile.cu): launched for the sequences that a marks as tiled.
+lk_status launch_tiles(const AttnArgs& a, int type, int D, int pdl, cudaStream_t stream);
 
 }  // namespace lkattn

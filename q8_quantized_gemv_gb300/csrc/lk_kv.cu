@@ -141,10 +141,12 @@ bool rows_overlap(const float* p, long ld, int rows, long span, const float* q, 
 }
 
 template <int TYPE>
-void launch_append(const AppendArgs& a, int D, int pdl, cudaStream_t stream) {
+lk_status launch_append(const AppendArgs& a, int D, int pdl, cudaStream_t stream) {
   const dim3 grid((unsigned)((a.heads + 7) / 8)), block(256);
-  if (D == 128) launch_pdl(kv_append_kernel<TYPE, 128>, grid, block, stream, pdl, a);
-  else launch_pdl(kv_append_kernel<TYPE, 64>, grid, block, stream, pdl, a);
+  static std::atomic<int> done[2][kMaxDevices];
+  const auto f = D == 128 ? kv_append_kernel<TYPE, 128> : kv_append_kernel<TYPE, 64>;
+  if (!lkattn::prepare_kernel(f, done[D == 128], 0)) return LK_ERR_CUDA;
+  return lkattn::launch(f, grid, block, 0, pdl, stream, a) == cudaSuccess ? LK_OK : LK_ERR_CUDA;
 }
 
 }  // namespace
@@ -201,8 +203,7 @@ extern "C" lk_status lk_kv_append(const lk_kv_cache* cache, const float* q, cons
   a.qr = qr;
   a.heads = M * (n_q + 2 * cache->n_kv);
   const int pdl = cfg_pdl(cfg);
-  if (cache->type == LK_KV_F16) launch_append<LK_KV_F16>(a, D, pdl, stream);
-  else if (cache->type == LK_KV_BF16) launch_append<LK_KV_BF16>(a, D, pdl, stream);
-  else launch_append<LK_KV_Q8>(a, D, pdl, stream);
-  return launch_status();
+  if (cache->type == LK_KV_F16) return launch_append<LK_KV_F16>(a, D, pdl, stream);
+  if (cache->type == LK_KV_BF16) return launch_append<LK_KV_BF16>(a, D, pdl, stream);
+  return launch_append<LK_KV_Q8>(a, D, pdl, stream);
 }

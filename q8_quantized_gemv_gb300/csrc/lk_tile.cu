@@ -1,0 +1,460 @@
+// Attention for many query rows on the same keys (include/lk_attn.h): a
+// shared prefix, or several new tokens of a sequence, on the fifth-generation
+// tensor cores.
+//
+// With up to 256 query rows to a key/value head the products, not the cache's
+// bytes, set the time: a block takes 256 rows and walks over its share of the
+// keys in tiles of 128.  Two streams, each with an S tile (scores, then the
+// weights in its place) and an O tile (128 columns each) in tensor memory, and
+// a warpgroup of 128 threads, a thread to a row, keep the tensor pipe busy in
+// turn: while one stream's warpgroup turns scores into weights, the pipe has
+// the other's products.  More than 128 rows: a stream has 128 of the rows and
+// both use each tile; else both have the same rows and take the tiles in turn.
+//
+// Precision as in the streaming kernel: keys and values enter as stored,
+// queries and weights as two 16-bit terms (the low term's MMAs accumulate on
+// the high term's); a tile's weighted values start a fresh accumulator and are
+// added in f32 registers, 128 keys at a time.
+//
+// Roles: warp 0 issues the MMAs (one thread), warps 2 and 3 fill a ring of
+// tile buffers with 16-byte asynchronous copies (pages of any size from 16;
+// absent and trailing tokens become zeros) in the 128-byte swizzle of the MMA
+// operands, keys as a K-major and values as an MN-major B operand; warpgroups
+// 1 and 2 are the streams.  Every wait is bounded (option "wait_us"); one that
+// runs out raises the device error word and ends the block.
+#include "lk_attn.cuh"
+#include "lk_tc.cuh"
+
+using namespace lk;
+using namespace lkh;
+using namespace lktc;
+
+namespace lkattn {
+
+constexpr int ERR_TILE_WAIT = 32;
+
+template <int D>
+struct TCfg {
+  static constexpr int HALF = TUNIT * 128;          // 128 rows of 64 16-bit values
+  static constexpr int BUF = (D / 64) * HALF;       // a tile of keys or values
+  static constexpr int QS = 2 * BUF;                // a stream's queries, high and low terms
+  static constexpr int NB = D == 128 ? 3 : 8;       // ring buffers
+  static constexpr int SMEM = 2 * QS + NB * BUF + 1024;
+  static constexpr int THREADS = 384;
+  // Registers: the launch has THREADS * LAUNCH of them; the streams take
+  // 2 * 128 * STREAM and leave 128 * REST, the same sum.
+  static constexpr int LAUNCH = 168, STREAM = 224, REST = 56;
+  static_assert(THREADS * LAUNCH == 2 * 128 * STREAM + 128 * REST, "register split");
+};
+
+// Where a tile's K and V are in a segment's order of ring fills (nt tiles):
+// the order in which the MMAs use them.
+__device__ __forceinline__ int k_at(bool both, int t) { return both ? 2 * t : t == 0 ? 0 : 2 * t - 1; }
+__device__ __forceinline__ int v_at(bool both, int t, int nt) {
+  return both ? 2 * t + 1 : t == nt - 1 ? 2 * nt - 1 : 2 * t + 2;
+}
+
+struct Segment {
+  int s, n, kvh, group, ub, nt, rows, slot;
+  bool both;  // more than 128 rows: both streams use each tile
+};
+
+// The next segment of the share [u0, u1), u0 moved behind it.
+__device__ __forceinline__ Segment next_segment(const AttnArgs& a, const Deal& d, int& s, long& u0, long u1) {
+  Segment g;
+  while (d.cum[s + 1] <= u0) ++s;
+  const int un = d.un[s], groups = groups_of<true>(a, s);
+  const long rel = u0 - d.cum[s];
+  const int li = (int)(rel / un);
+  g.s = s;
+  g.n = d.n[s];
+  g.ub = (int)(rel - (long)li * un);
+  g.nt = (int)min((long)(un - g.ub), u1 - u0);
+  g.kvh = li / groups;
+  g.group = li - g.kvh * groups;
+  g.rows = min(TROWS, rows_of(a, s) - g.group * TROWS);
+  g.both = g.rows > 128;
+  g.slot = (int)blockIdx.x + item0<true>(a, s) + li;
+  u0 += g.nt;
+  return g;
+}
+
+// The 128 threads of stream x.
+__device__ __forceinline__ void group_sync(int x) {
+  if (x == 0) asm volatile("bar.sync 1, 128;" ::: "memory");
+  else asm volatile("bar.sync 2, 128;" ::: "memory");
+}
+
+template <bool BF, int D>
+__global__ void __launch_bounds__(TCfg<D>::THREADS) __maxnreg__(TCfg<D>::LAUNCH) attn_tile_kernel(const AttnArgs a) {
+  typedef TCfg<D> C;
+  extern __shared__ unsigned char raw[];
+  __shared__ Deal deal;
+  __shared__ __align__(8) unsigned long long bars[2 * C::NB + 9];
+  __shared__ unsigned tmem_slot;
+  __shared__ int abort_flag;
+  const unsigned base = (smem_addr(raw) + 1023u) & ~1023u;
+  const unsigned ring = base + 2 * C::QS;
+  const unsigned bar0 = smem_addr(bars);
+  const unsigned b_full = bar0, b_free = bar0 + 8 * C::NB, b_q = bar0 + 16 * C::NB, b_s = b_q + 16, b_p = b_s + 16,
+                 b_o = b_p + 16, b_drain = b_o + 16;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < C::NB; ++i) bar_init(b_full + 8 * i, 2), bar_init(b_free + 8 * i, 1);
+    for (int x = 0; x < 2; ++x) {
+      bar_init(b_q + 8 * x, 128);
+      bar_init(b_s + 8 * x, 1);
+      bar_init(b_p + 8 * x, 128);
+      bar_init(b_o + 8 * x, 1);
+    }
+    bar_init(b_drain, 1);
+    abort_flag = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 0) tm_alloc(smem_addr(&tmem_slot), 512);
+  asm volatile("griddepcontrol.launch_dependents;" :::);
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (warp == 1) make_deal<true>(a, deal);
+  tm_before();
+  __syncthreads();
+  tm_after();
+  const unsigned tmem = *(volatile unsigned*)&tmem_slot;
+  const long T = deal.cum[a.B + a.shared], W = shares(a.TW, T);
+  long u0 = 0, u1 = 0;
+  if (blockIdx.x < W) u0 = T * blockIdx.x / W, u1 = T * (blockIdx.x + 1) / W;
+  int s = 0;
+  auto wait = [&](unsigned bar, unsigned parity) -> bool {
+    if (bar_wait(bar, parity & 1u, a.wait_ns, &abort_flag)) return true;
+    if (!*(volatile int*)&abort_flag) {
+      *(volatile int*)&abort_flag = 1;
+      atomicOr(a.err, ERR_TILE_WAIT);
+    }
+    return false;
+  };
+
+  if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::REST));
+    if (warp == 0) {
+      // ---- MMA issue ---------------------------------------------------------------
+      if (lane == 0) {
+        constexpr unsigned id_qk = inst_desc(BF, false, 128, TUNIT), id_pv = inst_desc(BF, true, 128, D);
+        unsigned nb = 0, seg = 0, np[2] = {0, 0};
+        bool ok = true;
+        while (u0 < u1 && ok) {
+          const Segment g = next_segment(a, deal, s, u0, u1);
+          const int cnt[2] = {g.both ? g.nt : (g.nt + 1) / 2, g.both ? g.nt : g.nt / 2};
+          // scores of stream x's tile j
+          auto qk = [&](int x, int j) -> bool {
+            const unsigned f = nb + k_at(g.both, g.both ? j : 2 * j + x), buf = f % C::NB;
+            if (!wait(b_full + 8 * buf, f / C::NB)) return false;
+            tm_after();
+            const unsigned q = base + x * C::QS, k = ring + buf * C::BUF;
+#pragma unroll 1
+            for (int term = 0; term < 2; ++term)
+#pragma unroll 4
+              for (int i = 0; i < D / 16; ++i) {
+                const unsigned off = (i >> 2) * C::HALF + (i & 3) * 32;
+                mma_ss(tmem + x * 128, smem_desc(q + term * C::BUF + off, 16, 1024), smem_desc(k + off, 16, 1024),
+                       id_qk, term > 0 || i > 0);
+              }
+            mma_commit(b_s + 8 * x);
+            if (!g.both || x == 1) mma_commit(b_free + 8 * buf);
+            return true;
+          };
+          // weighted values of stream x's tile j
+          auto pv = [&](int x, int j) -> bool {
+            const unsigned f = nb + v_at(g.both, g.both ? j : 2 * j + x, g.nt), buf = f % C::NB;
+            if (!wait(b_full + 8 * buf, f / C::NB) || !wait(b_p + 8 * x, np[x])) return false;
+            ++np[x];
+            tm_after();
+            const unsigned p = tmem + x * 128, v = ring + buf * C::BUF;
+#pragma unroll 1
+            for (int term = 0; term < 2; ++term)
+#pragma unroll 4
+              for (int i = 0; i < TUNIT / 16; ++i)
+                // 32 columns hold the two terms of 32 keys' weights
+                mma_ts(tmem + 256 + x * 128, p + (i >> 1) * 32 + term * 16 + (i & 1) * 8,
+                       smem_desc(v + i * 2048, C::HALF, 1024), id_pv, term > 0 || i > 0);
+            mma_commit(b_o + 8 * x);
+            if (!g.both || x == 1) mma_commit(b_free + 8 * buf);
+            return true;
+          };
+          for (int x = 0; x < 2 && ok; ++x)
+            if (cnt[x]) ok = wait(b_q + 8 * x, seg) && qk(x, 0);
+            else ok = wait(b_q + 8 * x, seg);
+          for (int j = 0; j < cnt[0] && ok; ++j)
+            for (int x = 0; x < 2 && ok; ++x) {
+              if (j < cnt[x]) ok = pv(x, j);
+              if (ok && j + 1 < cnt[x]) ok = qk(x, j + 1);
+            }
+          nb += 2 * g.nt;
+          ++seg;
+        }
+        // nothing of this block is in flight when its tensor memory is freed
+        mma_commit(b_drain);
+        const unsigned long long t0 = now_ns();
+        while (!bar_try(b_drain, 0))
+          if (now_ns() - t0 > a.wait_ns) {
+            atomicOr(a.err, ERR_TILE_WAIT);
+            break;
+          }
+      }
+      __syncwarp();
+    } else if (warp >= 2) {
+      // ---- the ring's fills ----------------------------------------------------------
+      const int tid = threadIdx.x - 64;
+      constexpr int PP = D / 8;            // 16-byte pieces of a token
+      constexpr int RS = 64 / PP;          // tokens of a pass
+      const int pc = tid % PP, r_in = tid / PP;
+      unsigned f = 0, told = 0;  // fills begun, fills reported
+      bool ok = true;
+      constexpr unsigned LAG = C::NB - 1;
+      auto tell = [&](unsigned upto) {
+        fence_async();
+        __syncwarp();
+        for (; told != upto; ++told)
+          if (lane == 0) bar_arrive(b_full + 8 * (told % C::NB));
+      };
+      while (u0 < u1 && ok) {
+        const Segment g = next_segment(a, deal, s, u0, u1);
+        const int* table = g.s == a.B ? a.ptable : a.table + (long)g.s * a.table_w;
+        for (int i = 0; i < 2 * g.nt && ok; ++i, ++f) {
+          // fill i of the segment: which tile, keys or values
+          bool is_v;
+          int t;
+          if (g.both) is_v = i & 1, t = i >> 1;
+          else if (i == 0) is_v = false, t = 0;
+          else if (i == 2 * g.nt - 1) is_v = true, t = g.nt - 1;
+          else is_v = !(i & 1), t = is_v ? (i - 2) >> 1 : (i + 1) >> 1;
+          const int key0 = (g.ub + t) * TUNIT;
+          // pages of the tile's eight groups of 16 tokens
+          int pg = -1;
+          if (lane < 8 && key0 + 16 * lane < g.n) pg = __ldg(table + ((key0 + 16 * lane) >> a.page_log2));
+          const unsigned buf = f % C::NB;
+          if (!__all_sync(FULL, bar_try(b_free + 8 * buf, ((f / C::NB) & 1u) ^ 1u))) {
+            cp_wait<0>();
+            tell(f);
+            ok = __all_sync(FULL, wait(b_free + 8 * buf, (f / C::NB) ^ 1u));
+            if (!ok) break;
+          }
+          const char* src0 = (const char*)(is_v ? a.v : a.k);
+          const unsigned dst0 = ring + buf * C::BUF + (pc >> 3) * C::HALF;
+#pragma unroll 2
+          for (int h = 0; h < 8; ++h) {
+            const int p = __shfl_sync(FULL, pg, h);
+            const int k0 = key0 + 16 * h;
+            const int left = (unsigned)p < (unsigned)a.n_pages ? g.n - k0 : 0;
+            const long r0 = (((long)(left > 0 ? p : 0) * a.n_kv + g.kvh) << a.page_log2) + (k0 & ((1 << a.page_log2) - 1));
+            const char* src = src0 + r0 * (2 * D) + pc * 16;
+#pragma unroll
+            for (int m = 0; m < 16 / RS; ++m) {
+              const int kk = m * RS + r_in, row = 16 * h + kk;
+              cp16(dst0 + row * 128 + (((pc & 7) ^ (row & 7)) << 4), src + kk * (2 * D), kk < left ? 16 : 0);
+            }
+          }
+          cp_commit();
+          if (f + 1 - told > LAG) {
+            cp_wait<LAG>();
+            tell(f + 1 - LAG);
+          }
+        }
+      }
+      cp_wait<0>();
+      if (ok) tell(f);
+    }
+  } else {
+    // ---- a stream: a thread to a row ---------------------------------------------------
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::STREAM));
+    const int x = (warp >> 2) - 1, wq = warp & 3, me = threadIdx.x & 127;
+    const unsigned tw = tmem + ((unsigned)(32 * wq) << 16);  // the warp's lanes
+    const unsigned ts = tw + x * 128, to = tw + 256 + x * 128;
+    const unsigned qs = base + x * C::QS;
+    constexpr float UP = BF ? 0.0f : 14.0f;
+    unsigned nt = 0;  // tiles so far
+    bool ok = true, stored = false;
+    while (u0 < u1 && ok) {
+      const Segment g = next_segment(a, deal, s, u0, u1);
+      const bool pre = g.s == a.B;
+      const int* table = pre ? a.ptable : a.table + (long)g.s * a.table_w;
+      const int r_first = g.group * TROWS + (g.both ? 128 * x : 0);  // row of the head that is the stream's row 0
+      const int nr = g.both ? min(128, g.rows - 128 * x) : g.rows;
+      const int cnt = g.both ? g.nt : x == 0 ? (g.nt + 1) / 2 : g.nt / 2;
+      if (stored) {  // the last segment's rows have left the queries' place
+        if (me == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+        group_sync(x);
+      }
+      // queries: a warp loads its 32 rows one after the other, D / 32 values a
+      // lane, and writes their two terms swizzled
+      float rs = 1.0f;
+#pragma unroll 4
+      for (int i = 0; i < 32; ++i) {
+        const int lr = 32 * wq + i;
+        float v[D / 32];
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) v[c] = 0.0f;
+        if (lr < nr) {
+          const int ri = r_first + lr, tok = ri / a.G, row = pre ? tok : g.s * a.R + tok;
+          const float* q = a.q + ((long)row * a.n_q + g.kvh * a.G + (ri - tok * a.G)) * D + lane * (D / 32);
+          if constexpr (D == 128) {
+            const float4 f = __ldcg((const float4*)q);
+            v[0] = f.x, v[1] = f.y, v[2] = f.z, v[3] = f.w;
+          } else {
+            const float2 f = __ldcg((const float2*)q);
+            v[0] = f.x, v[1] = f.y;
+          }
+        }
+        float am = 0.0f;
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) v[c] *= a.qscale, am = fmaxf(am, fabsf(v[c]));
+        if constexpr (!BF) {
+          float back;
+          const float up = row_shift(warp_absmax(am), back);
+          if (lane == i) rs = back;
+#pragma unroll
+          for (int c = 0; c < D / 32; ++c) v[c] *= up;
+        }
+        // values lane * D/32 ...: 16-byte piece and place in it
+        const int d0 = lane * (D / 32), piece = (d0 & 63) >> 3;
+        const unsigned at = qs + (d0 >> 6) * C::HALF + lr * 128 + ((piece ^ (lr & 7)) << 4) + (d0 & 7) * 2;
+#pragma unroll
+        for (int term = 0; term < 2; ++term) {
+          const unsigned w0 = split2<BF>(v[0], v[1]);
+          if constexpr (D == 128) {
+            const unsigned w1 = split2<BF>(v[2], v[3]);
+            asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(at + term * C::BUF), "r"(w0), "r"(w1) : "memory");
+          } else {
+            asm volatile("st.shared.u32 [%0], %1;" ::"r"(at + term * C::BUF), "r"(w0) : "memory");
+          }
+        }
+      }
+      fence_async();
+      bar_arrive(b_q + 8 * x);
+
+      int vis = g.n;  // keys that the thread's row sees
+      if (!pre && me < nr) {
+        const int tok = (r_first + me) / a.G;
+        vis = min(g.n, max(0, __ldcg(a.lens + g.s) - a.R + 1 + tok));
+      }
+      float O[D], m = -INFINITY, l = 0.0f;
+#pragma unroll
+      for (int i = 0; i < D; ++i) O[i] = 0.0f;
+      for (int j = 0; j < cnt; ++j, ++nt) {
+        const int key0 = (g.ub + (g.both ? j : 2 * j + x)) * TUNIT;
+        int pg = -1;
+        if (lane < 8 && key0 + 16 * lane < g.n) pg = __ldg(table + ((key0 + 16 * lane) >> a.page_log2));
+        const unsigned there = __ballot_sync(FULL, (unsigned)pg < (unsigned)a.n_pages);
+        const bool whole = __all_sync(FULL, key0 + TUNIT <= vis) && there == 0xffu;
+        ok = __all_sync(FULL, wait(b_s + 8 * x, nt));
+        if (!ok) break;
+        tm_after();
+        auto seen = [&](int k) { return key0 + k < vis && ((there >> (k >> 4)) & 1u); };
+        float mx = -INFINITY;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          unsigned r[32];
+          tm_ld32(ts + 32 * c, r);
+          tm_ld_wait(r);
+          if (whole) {
+#pragma unroll
+            for (int k = 0; k < 32; ++k) mx = fmaxf(mx, __uint_as_float(r[k]));
+          } else {
+#pragma unroll
+            for (int k = 0; k < 32; ++k)
+              if (seen(32 * c + k)) mx = fmaxf(mx, __uint_as_float(r[k]));
+          }
+        }
+        const float mn = fmaxf(m, mx * rs);
+        const float ref = mn == -INFINITY ? 0.0f : mn;
+        const float al = ex2(m - ref);
+        m = mn;
+        float sum = 0.0f;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          unsigned r[32], w[32];
+          tm_ld32(ts + 32 * c, r);
+          tm_ld_wait(r);
+#pragma unroll
+          for (int k = 0; k < 32; k += 2) {
+            float p0 = ex2(fmaf(__uint_as_float(r[k]), rs, UP - ref));
+            float p1 = ex2(fmaf(__uint_as_float(r[k + 1]), rs, UP - ref));
+            if (!whole) {
+              if (!seen(32 * c + k)) p0 = 0.0f;
+              if (!seen(32 * c + k + 1)) p1 = 0.0f;
+            }
+            sum += p0 + p1;
+            w[k >> 1] = split2<BF>(p0, p1);
+            w[16 + (k >> 1)] = split2<BF>(p0, p1);
+          }
+          tm_st32(ts + 32 * c, w);
+        }
+        l = fmaf(l, al, sum);
+        tm_st_wait();
+        tm_before();
+        bar_arrive(b_p + 8 * x);
+        ok = __all_sync(FULL, wait(b_o + 8 * x, nt));
+        if (!ok) break;
+        tm_after();
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) {
+          unsigned r[32];
+          tm_ld32(to + 32 * c, r);
+          tm_ld_wait(r);
+#pragma unroll
+          for (int k = 0; k < 32; ++k) O[32 * c + k] = fmaf(O[32 * c + k], al, __uint_as_float(r[k]));
+        }
+        tm_before();
+      }
+      if (!ok) break;
+      // the rows' partials: staged where the queries were (their last product
+      // is done), then one bulk store
+      const int which = pre ? 1 : 0, sr = tile_slot_rows(rows_of(a, g.s)), row0 = x * (g.both ? 128 : g.rows);
+      const long at = (long)g.slot * sr + row0;
+      if (me < nr) {
+#pragma unroll
+        for (int c = 0; c < D / 4; ++c)
+          asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(qs + me * (D * 4) + ((c ^ (me & 7)) << 4)),
+                       "f"(O[4 * c]), "f"(O[4 * c + 1]), "f"(O[4 * c + 2]), "f"(O[4 * c + 3])
+                       : "memory");
+        __stcg((float2*)(a.tml[which] + (at + me) * 2), make_float2(m, l));
+      }
+      fence_async();
+      group_sync(x);
+      if (me == 0) {
+        asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(a.to[which] + at * D), "r"(qs),
+                     "r"(nr * D * 4)
+                     : "memory");
+        asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+      }
+      stored = true;
+    }
+    if (me == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+  }
+  tm_before();
+  __syncthreads();
+  tm_after();
+  if (warp == 0) tm_free(tmem, 512);
+}
+
+template <bool BF, int D>
+lk_status run_tiles(const AttnArgs& a, int pdl, cudaStream_t stream) {
+  typedef TCfg<D> C;
+  static std::atomic<int> done[kMaxDevices], regs;
+  if (!prepare_kernel(attn_tile_kernel<BF, D>, done, C::SMEM)) return LK_ERR_CUDA;
+  if (!regs.load(std::memory_order_acquire)) {
+    // the register split waits forever on a launch with fewer than it assumes
+    cudaFuncAttributes fa;
+    if (cudaFuncGetAttributes(&fa, attn_tile_kernel<BF, D>) != cudaSuccess || fa.numRegs != C::LAUNCH)
+      return LK_ERR_CUDA;
+    regs.store(1, std::memory_order_release);
+  }
+  return launch(attn_tile_kernel<BF, D>, dim3(a.TW), dim3(C::THREADS), C::SMEM, pdl, stream, a) == cudaSuccess
+             ? LK_OK
+             : LK_ERR_CUDA;
+}
+
+lk_status launch_tiles(const AttnArgs& a, int type, int D, int pdl, cudaStream_t stream) {
+  if (type == LK_KV_BF16) return D == 128 ? run_tiles<true, 128>(a, pdl, stream) : run_tiles<true, 64>(a, pdl, stream);
+  return D == 128 ? run_tiles<false, 128>(a, pdl, stream) : run_tiles<false, 64>(a, pdl, stream);
+}
+
+}  // namespace lkattn
