@@ -20,18 +20,21 @@
 // more than 32 keys.
 //
 // Data.  Every warp streams its own units through its own stages of shared
-// memory with 16-byte asynchronous copies.  A lane of the 16-bit kernels
-// copies exactly the pieces that it will use as MMA operands (the order of the
-// inner index of a product is free, so a lane's 8 consecutive values serve two
-// k-steps), so stages need no barrier and reads no shuffle; the Q8 kernels
-// read 4- and 8-byte pieces, staged with their 16-byte pieces permuted against
-// bank conflicts.
+// memory: one thread asks for a unit with a few tensor copies (128-byte pieces
+// of its tokens' rows, 128-byte swizzle), every lane then reads the operands
+// it needs as 16-byte pieces (Q8: 8 and 4 bytes).  The order of the inner index
+// of a product is free, so a lane's 8 consecutive values serve two k-steps and
+// no value changes lanes.  Copies by the threads themselves (cp.async) were
+// measured slower: a warp gets one 512-byte copy instruction through per
+// ~190 cycles, 5.1 TB/s with 7 warps.
 #include <cuda_bf16.h>
 
 #include "lk_attn.cuh"
+#include "lk_tc.cuh"
 
 using namespace lk;
 using namespace lkh;
+using namespace lktc;
 
 namespace lkattn {
 
@@ -75,29 +78,43 @@ __device__ __forceinline__ unsigned level_pair(unsigned u, unsigned sel) {
   return *(const unsigned*)&h;
 }
 
+constexpr int ERR_ATTN_WAIT = 32;
+
 template <int TYPE, int D>
 struct Cfg {
   static constexpr int EB = TYPE == LK_KV_Q8 ? 1 : 2;              // bytes of a stored value
   static constexpr int KV = UNIT * D * EB;                         // bytes of a unit's keys
   static constexpr int SC = TYPE == LK_KV_Q8 ? UNIT * D / 16 : 0;  // bytes of their scales
-  static constexpr int STAGE = 2 * (KV + SC);
+  static constexpr int STAGE = (2 * (KV + SC) + 1023) / 1024 * 1024;
+  static constexpr int ROW = EB * D < 128 ? EB * D : 128;          // bytes of a box row
+  static constexpr int PARTS = EB * D / ROW;                       // boxes of a token's row
   static constexpr int NW = TYPE != LK_KV_Q8 && D == 128 ? 7 : 8;  // warps
   static constexpr int ST = TYPE != LK_KV_Q8 && D == 128 ? 2 : 3;  // stages a warp
-  static constexpr int RING = NW * ST * STAGE;
+  static constexpr int RING = NW * ST * STAGE + 1024;  // and the base's alignment
   static_assert(STAGE * ST >= TR * (D + 4) * 4, "a warp's partial fits in its stages");
-  static_assert(RING + 2048 <= 232448, "shared memory of a block");
+  static_assert(NW * ST <= 32 && RING + 2048 <= 232448, "shared memory of a block");
 };
 
 template <int TYPE, int D>
-__global__ void __launch_bounds__(32 * Cfg<TYPE, D>::NW, 1) attn_kernel(const AttnArgs a) {
+__global__ void __launch_bounds__(32 * Cfg<TYPE, D>::NW, 1) attn_kernel(const __grid_constant__ AttnArgs a) {
   typedef Cfg<TYPE, D> C;
   constexpr bool Q8 = TYPE == LK_KV_Q8;
   constexpr int KS = D / 16;                       // k-steps of a score
   constexpr int QT = TYPE == LK_KV_BF16 ? 3 : 2;   // terms of a query
   constexpr int NT = D / 8;                        // n-tiles of the output
-  extern __shared__ __align__(128) unsigned char smem[];
+  extern __shared__ unsigned char raw[];
   __shared__ Deal deal;
   __shared__ float wml[C::NW][TR][2];
+  __shared__ __align__(8) unsigned long long bars[C::NW * C::ST];
+  __shared__ int abort_flag;
+  unsigned char* smem = raw + ((1024u - (smem_addr(raw) & 1023u)) & 1023u);
+  if (threadIdx.x < C::NW * C::ST) bar_init(smem_addr(bars + threadIdx.x), 1);
+  if (threadIdx.x == 0) {
+    abort_flag = 0;
+    map_prefetch(&a.kmap);
+    map_prefetch(&a.vmap);
+  }
+  asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" :::);
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (threadIdx.x < 32) make_deal<false>(a, deal);
@@ -108,7 +125,8 @@ __global__ void __launch_bounds__(32 * Cfg<TYPE, D>::NW, 1) attn_kernel(const At
   if (blockIdx.x >= W) return;
   long u0 = T * blockIdx.x / W;
   const long u1 = T * (blockIdx.x + 1) / W;
-  const unsigned ring = (unsigned)__cvta_generic_to_shared(smem) + warp * C::ST * C::STAGE;
+  const unsigned ring = smem_addr(smem) + warp * C::ST * C::STAGE, bar0 = smem_addr(bars) + 8 * warp * C::ST;
+  unsigned phases = 0;  // bit i: the parity stage i's copies complete next
   int s = 0;
   while (u0 < u1) {
     while (deal.cum[s + 1] <= u0) ++s;
@@ -179,56 +197,31 @@ __global__ void __launch_bounds__(32 * Cfg<TYPE, D>::NW, 1) attn_kernel(const At
         }
       }
     };
-    // start the copies of unit u into a stage; one commit group
+    // ask for unit u (one thread of the warp); a.box is 16 or 32 rows
     auto issue = [&](int u, const int (&pg)[2], int stage) {
-      const unsigned st = ring + stage * C::STAGE;
-#pragma unroll
-      for (int hf = 0; hf < 2; ++hf) {
+      if (lane != 0) return;
+      const unsigned st = ring + stage * C::STAGE, bar = bar0 + 8 * stage;
+      const int n_box = a.box == 32 ? 1 : 2;
+      unsigned bytes = 0;
+      for (int hf = 0; hf < n_box; ++hf)
+        if (pg[hf] >= 0) bytes += 2 * a.box * (D * C::EB + (Q8 ? D / 16 : 0));
+      bar_expect(bar, bytes);
+      for (int hf = 0; hf < n_box; ++hf) {
+        if (pg[hf] < 0) continue;
         const int key0 = u * UNIT + 16 * hf;
-        const int left = pg[hf] < 0 ? 0 : min(16, n - key0);  // tokens there are
-        const long r0 =
-            (((long)max(pg[hf], 0) * a.n_kv + kvh) << a.page_log2) + (key0 & ((1 << a.page_log2) - 1));
-        const char* k = (const char*)a.k + r0 * D * C::EB;
-        const char* v = (const char*)a.v + r0 * D * C::EB;
-        if constexpr (!Q8) {
+        const int r0 = ((pg[hf] * a.n_kv + kvh) << a.page_log2) + (key0 & ((1 << a.page_log2) - 1));
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const int kk = 8 * i + g;
-#pragma unroll
-            for (int j = 0; j < D / 32; ++j)
-              cp16(st + (((2 * hf + i) * (D / 32) + j) * 32 + lane) * 16, k + kk * (D * 2) + j * 64 + t * 16,
-                   kk < left ? 16 : 0);
-          }
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int kk = 2 * t + (e & 1) + 8 * (e >> 1);
-#pragma unroll
-            for (int h = 0; h < D / 64; ++h)
-              cp16(st + C::KV + (((4 * hf + e) * (D / 64) + h) * 32 + lane) * 16, v + kk * (D * 2) + h * 128 + g * 16,
-                   kk < left ? 16 : 0);
-          }
-        } else {
-          constexpr int PP = D / 16;  // 16-byte pieces of a token
-#pragma unroll
-          for (int i = 0; i < 16 * PP / 32; ++i) {
-            const int c = i * 32 + lane, kk = c / PP, pc = c % PP;
-            const int fk = PP == 8 ? 2 * (kk & 3) : kk & 2, fv = PP == 8 ? kk & 6 : kk & 2;
-            const int ok = kk < left ? 16 : 0;
-            cp16(st + (16 * hf + kk) * D + ((pc ^ fk) * 16), k + c * 16, ok);
-            cp16(st + C::KV + (16 * hf + kk) * D + ((pc ^ fv) * 16), v + c * 16, ok);
-          }
-          // scales: D bytes of each half's keys and as many of its values,
-          // 16 / (D / 16) tokens to a piece
-          constexpr int SP = D / 16;
-          if (lane < 2 * SP) {
-            const int pc = lane % SP;
-            const char* sc = (const char*)(lane < SP ? a.ks : a.vs) + r0 * (D / 16);
-            cp16(st + 2 * C::KV + (lane < SP ? 0 : C::SC) + hf * D + pc * 16, sc + pc * 16,
-                 pc * 16 < left * (D / 16) ? 16 : 0);
-          }
+        for (int p = 0; p < C::PARTS; ++p) {
+          const unsigned at = st + p * UNIT * C::ROW + 16 * hf * C::ROW;
+          tma_2d(at, &a.kmap, p * (C::ROW / C::EB), r0, bar);
+          tma_2d(at + C::KV, &a.vmap, p * (C::ROW / C::EB), r0, bar);
+        }
+        if constexpr (Q8) {
+          const unsigned at = st + 2 * C::KV + hf * D, n = a.box * (D / 16);
+          bulk_in(at, (const char*)a.ks + (long)r0 * (D / 16), n, bar);
+          bulk_in(at + C::SC, (const char*)a.vs + (long)r0 * (D / 16), n, bar);
         }
       }
-      cp_commit();
     };
 
     float O[NT][2], m = -INFINITY, l = 0.0f, dvm = 0.0f, dsc = 1.0f;
@@ -243,13 +236,18 @@ __global__ void __launch_bounds__(32 * Cfg<TYPE, D>::NW, 1) attn_kernel(const At
 #pragma unroll
     for (int i = 0; i < C::ST; ++i) {
       if (uw + i * C::NW < ue) issue(uw + i * C::NW, pgq[i], i);
-      else cp_commit();
     }
     pages(uw + C::ST * C::NW, pgn);
-    int stage = 0;
-    for (int u = uw; u < ue; u += C::NW) {
-      cp_wait<C::ST - 1>();
-      if constexpr (Q8) __syncwarp();
+    int stage = 0, u = uw;
+    for (; u < ue; u += C::NW) {
+      if (!bar_wait(bar0 + 8 * stage, (phases >> stage) & 1u, a.wait_ns, &abort_flag)) {
+        if (lane == 0 && !*(volatile int*)&abort_flag) {
+          *(volatile int*)&abort_flag = 1;
+          atomicOr(a.err, ERR_ATTN_WAIT);
+        }
+      }
+      if (__any_sync(FULL, *(volatile int*)&abort_flag)) break;
+      phases ^= 1u << stage;
       const unsigned st = ring + stage * C::STAGE;
       // ---- scores: lane (g, t) has row g with keys 8 i + 2 t, + 1
       float sc[4][2];
@@ -259,7 +257,8 @@ __global__ void __launch_bounds__(32 * Cfg<TYPE, D>::NW, 1) attn_kernel(const At
           float c[4] = {0.f, 0.f, 0.f, 0.f}, c3[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
           for (int j = 0; j < D / 32; ++j) {
-            const uint4 w = lds128(st + ((i * (D / 32) + j) * 32 + lane) * 16);
+            // piece 4 (j & 1) + t of the token's part j >> 1
+            const uint4 w = lds128(st + (j >> 1) * (UNIT * 128) + (8 * i + g) * 128 + (((4 * (j & 1) + t) ^ g) << 4));
             mma16<TYPE>(c, qa[2 * j][0], qa[2 * j][1], qa[2 * j][2], qa[2 * j][3], w.x, w.y);
             mma16<TYPE>(c, qa[2 * j + 1][0], qa[2 * j + 1][1], qa[2 * j + 1][2], qa[2 * j + 1][3], w.z, w.w);
             if constexpr (QT == 3) {
@@ -270,7 +269,7 @@ __global__ void __launch_bounds__(32 * Cfg<TYPE, D>::NW, 1) attn_kernel(const At
           sc[i][0] = (c[0] + (c[2] + c3[0])) * rs;
           sc[i][1] = (c[1] + (c[3] + c3[1])) * rs;
         } else {
-          const int key = 8 * i + g, fk = D == 128 ? 2 * (key & 3) : key & 2;
+          const int key = 8 * i + g, fk = D == 128 ? g : (key >> 1) & 3;  // the swizzle
           // scales of keys 8 i + 2 t, + 1
           __half2 d0[D / 64], d1[D / 64];
           if constexpr (D == 128) {
@@ -336,7 +335,7 @@ __global__ void __launch_bounds__(32 * Cfg<TYPE, D>::NW, 1) attn_kernel(const At
         for (int i = 0; i < HW; ++i) {
           const int w = i * 32 + lane;
           unsigned x = lds32(st + 2 * C::KV + C::SC + w * 4) & 0x7fff7fffu;
-          if (u * UNIT + w / HW >= n) x = 0;
+          if (u * UNIT + w / HW >= n || (w / HW < 16 ? pg0 : pg1) < 0) x = 0;
           mx = max(mx, max(x & 0xffffu, x >> 16));
         }
         mx = __reduce_max_sync(FULL, mx);
@@ -366,7 +365,10 @@ __global__ void __launch_bounds__(32 * Cfg<TYPE, D>::NW, 1) attn_kernel(const At
           unsigned w[8][4];
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
-            const uint4 x = lds128(st + C::KV + ((e * (D / 64) + h) * 32 + lane) * 16);
+            const int key = 16 * (e >> 2) + 2 * t + (e & 1) + 8 * ((e >> 1) & 1);
+            uint4 x = lds128(st + C::KV + h * (UNIT * 128) + key * 128 + ((g ^ (key & 7)) << 4));
+            // what lies behind the tokens may be anything: 0 * NaN is not 0
+            if (!whole && (u * UNIT + key >= n || (e < 4 ? pg0 : pg1) < 0)) x = make_uint4(0, 0, 0, 0);
             w[e][0] = x.x, w[e][1] = x.y, w[e][2] = x.z, w[e][3] = x.w;
           }
 #pragma unroll
@@ -399,8 +401,8 @@ __global__ void __launch_bounds__(32 * Cfg<TYPE, D>::NW, 1) attn_kernel(const At
           if (!whole) {
 #pragma unroll
             for (int x = 0; x < D / 64; ++x) {
-              if (key >= n) d0[i][x] = __half2half2(__ushort_as_half(0));
-              if (key + 1 >= n) d1[i][x] = __half2half2(__ushort_as_half(0));
+              if (key >= n || (i < 2 ? pg0 : pg1) < 0) d0[i][x] = __half2half2(__ushort_as_half(0));
+              if (key + 1 >= n || (i < 2 ? pg0 : pg1) < 0) d1[i][x] = __half2half2(__ushort_as_half(0));
             }
           }
         }
@@ -426,7 +428,7 @@ __global__ void __launch_bounds__(32 * Cfg<TYPE, D>::NW, 1) attn_kernel(const At
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
             const int key = 16 * (e >> 2) + 2 * t + (e & 1) + 8 * ((e >> 1) & 1);
-            const int fv = D == 128 ? key & 6 : key & 2;
+            const int fv = D == 128 ? key & 7 : (key >> 1) & 3;
             w[e] = lds32(st + C::KV + key * D + (((2 * b + (g >> 2)) ^ fv) * 16) + (g & 3) * 4) ^ 0x80808080u;
           }
           unsigned z[2][2][2];  // [k-step][half][values 0,1 / 2,3 of the two tokens]
@@ -449,20 +451,21 @@ __global__ void __launch_bounds__(32 * Cfg<TYPE, D>::NW, 1) attn_kernel(const At
             O[4 * b + j][1] += c[1] + c[3];
           }
         }
-        __syncwarp();  // every lane is done with the stage
       }
       // ---- the stage's next unit
       const int nu = u + C::ST * C::NW;
 #pragma unroll
       for (int i = 0; i + 1 < C::ST; ++i) pgq[i][0] = pgq[i + 1][0], pgq[i][1] = pgq[i + 1][1];
       pgq[C::ST - 1][0] = pgn[0], pgq[C::ST - 1][1] = pgn[1];
+      __syncwarp();  // every lane is done with the stage
       if (nu < ue) issue(nu, pgn, stage);
-      else cp_commit();
       pages(nu + C::NW, pgn);
       stage = stage + 1 == C::ST ? 0 : stage + 1;
     }
-    cp_wait<0>();
-    __syncwarp();
+    // a warp that gave up: nothing of its copies is in flight when the block ends
+    for (int i = 0; u < ue && i < C::ST; ++i, u += C::NW, stage = stage + 1 == C::ST ? 0 : stage + 1)
+      if (!bar_drain(bar0 + 8 * stage, (phases >> stage) & 1u, a.wait_ns) && lane == 0) atomicOr(a.err, ERR_ATTN_WAIT);
+    if (__syncthreads_or(abort_flag)) return;
 
     // ---- the warps' partials of the segment, joined in warp order
     if constexpr (Q8) {
@@ -504,6 +507,7 @@ __global__ void __launch_bounds__(32 * Cfg<TYPE, D>::NW, 1) attn_kernel(const At
         __stcg(a.ml + ((long)slot * TR + r) * 2 + 1, ls);
       }
     }
+    fence_async();  // the next segment's copies come after these accesses
     __syncthreads();
   }
 }
@@ -658,6 +662,37 @@ size_t layout(const Plan& p, int D, size_t (&ml)[3], size_t (&o)[3]) {
   return at;
 }
 
+lk_status make_maps(AttnArgs& a, int type, int D, int box) {
+  typedef CUresult (*encode_fn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                                const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+  static std::atomic<encode_fn> known;
+  encode_fn encode = known.load(std::memory_order_acquire);
+  if (!encode) {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult r;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &r) != cudaSuccess ||
+        r != cudaDriverEntryPointSuccess || !f) {
+      cudaGetLastError();
+      return LK_ERR_CUDA;
+    }
+    encode = (encode_fn)f;
+    known.store(encode, std::memory_order_release);
+  }
+  const int eb = type == LK_KV_Q8 ? 1 : 2, row = D * eb < 128 ? D * eb : 128;
+  const cuuint64_t dim[2] = {(cuuint64_t)D, ((cuuint64_t)a.n_pages * a.n_kv) << a.page_log2};
+  const cuuint64_t pitch[1] = {(cuuint64_t)D * eb};
+  const cuuint32_t shape[2] = {(cuuint32_t)(row / eb), (cuuint32_t)box}, step[2] = {1, 1};
+  for (int x = 0; x < 2; ++x)
+    if (encode(x ? &a.vmap : &a.kmap, eb == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_UINT16, 2,
+               const_cast<void*>(x ? a.v : a.k), dim, pitch, shape, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               row == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+      return LK_ERR_CUDA;
+  a.box = box;
+  return LK_OK;
+}
+
 template <int TYPE, int D>
 lk_status run_type(const AttnArgs& a, int pdl, cudaStream_t stream) {
   static std::atomic<int> done[kMaxDevices];
@@ -679,16 +714,22 @@ lk_status run_join(const JoinArgs& j, cudaStream_t stream) {
 }
 
 template <int D>
-lk_status run_d(const AttnArgs& a, int type, lk_mode mode, const JoinArgs& j, int pdl, cudaStream_t stream) {
+lk_status run_d(AttnArgs& a, int type, lk_mode mode, const JoinArgs& j, int pdl, cudaStream_t stream) {
   lk_status st = LK_OK;
+  const int page = 1 << a.page_log2;
   // the launches after the first are dependents of the one before
   if (!a.own_tiled || (a.shared && !a.pre_tiled)) {
+    if ((st = make_maps(a, type, D, page < UNIT ? page : UNIT))) return st;
     st = type == LK_KV_F16    ? run_type<LK_KV_F16, D>(a, pdl, stream)
          : type == LK_KV_BF16 ? run_type<LK_KV_BF16, D>(a, pdl, stream)
                               : run_type<LK_KV_Q8, D>(a, pdl, stream);
     pdl = 1;
   }
-  if (!st && (a.own_tiled || a.pre_tiled)) st = launch_tiles(a, type, D, pdl, stream);
+  if (!st && (a.own_tiled || a.pre_tiled)) {
+    const int part = D == 128 ? TUNIT : TUNIT / 2;  // tokens that a warp of the tile kernel fetches
+    if ((st = make_maps(a, type, D, page < part ? page : part))) return st;
+    st = launch_tiles(a, type, D, pdl, stream);
+  }
   if (st) return st;
   return mode == LK_DEQUANT   ? run_join<0, D>(j, stream)
          : mode == LK_INT8ACT ? run_join<1, D>(j, stream)

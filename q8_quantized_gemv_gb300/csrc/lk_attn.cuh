@@ -1,6 +1,7 @@
 // Host checks and work partition shared by the attention step's kernels.
 #pragma once
 
+#include <cuda.h>
 #include <cuda_bf16.h>
 
 #include "lk_attn.h"
@@ -20,6 +21,8 @@ inline lk_status check_cache(const lk_kv_cache* c, int n_q) {
   if (c->type < LK_KV_F16 || c->type > LK_KV_Q8) return LK_ERR_ARG;
   if (c->head_dim != 64 && c->head_dim != 128) return LK_ERR_SHAPE;
   if (c->page < 16 || c->page > 1024 || (c->page & (c->page - 1))) return LK_ERR_SHAPE;
+  // rows of the cache are coordinates of a tensor map
+  if ((long)c->n_pages * c->page > 0x7fffffffL / (c->n_kv > 0 ? c->n_kv : 1)) return LK_ERR_SHAPE;
   if (c->n_kv < 1 || c->n_pages < 1 || n_q < c->n_kv || n_q % c->n_kv || n_q > 4096) return LK_ERR_SHAPE;
   if (!c->k || !c->v || (c->type == LK_KV_Q8 && (!c->ks || !c->vs))) return LK_ERR_ARG;
   if (!lkh::aligned(c->k, 16) || !lkh::aligned(c->v, 16)) return LK_ERR_ALIGN;
@@ -62,6 +65,8 @@ constexpr int kMaxSeq = LK_MAX_BATCH + 1;
 __host__ __device__ inline int tile_slot_rows(long rows) { return rows <= 128 ? 2 * (int)rows : TROWS; }
 
 struct AttnArgs {
+  CUtensorMap kmap, vmap;  // [pages * heads * page rows][D], boxes of 128 bytes (Q8, D 64: 64) by box rows
+  int box;
   const float* q;
   int n_q, n_kv, G;
   const void* k;
@@ -212,6 +217,10 @@ bool prepare_kernel(F f, std::atomic<int> (&done)[lkh::kMaxDevices], int smem) {
   done[dev].store(1, std::memory_order_release);
   return true;
 }
+
+// Tensor maps of a's keys and values with boxes of `box` rows: 128-byte
+// pieces of a row in the 128-byte swizzle (rows of 64 bytes: the 64-byte one).
+lk_status make_maps(AttnArgs& a, int type, int D, int box);
 
 // The tile kernel (lk_tile.cu): launched for the sequences that a marks as tiled.
 lk_status launch_tiles(const AttnArgs& a, int type, int D, int pdl, cudaStream_t stream);

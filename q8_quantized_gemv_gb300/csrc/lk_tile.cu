@@ -17,11 +17,12 @@
 // added in f32 registers, 128 keys at a time.
 //
 // Roles: warp 0 issues the MMAs (one thread), warps 2 and 3 fill a ring of
-// tile buffers with 16-byte asynchronous copies (pages of any size from 16;
-// absent and trailing tokens become zeros) in the 128-byte swizzle of the MMA
-// operands, keys as a K-major and values as an MN-major B operand; warpgroups
+// tile buffers with tensor copies in the 128-byte swizzle of the MMA operands,
+// keys as a K-major and values as an MN-major B operand; warpgroups
 // 1 and 2 are the streams.  Every wait is bounded (option "wait_us"); one that
 // runs out raises the device error word and ends the block.
+#include <type_traits>
+
 #include "lk_attn.cuh"
 #include "lk_tc.cuh"
 
@@ -43,7 +44,7 @@ struct TCfg {
   static constexpr int THREADS = 384;
   // Registers: the launch has THREADS * LAUNCH of them; the streams take
   // 2 * 128 * STREAM and leave 128 * REST, the same sum.
-  static constexpr int LAUNCH = 168, STREAM = 224, REST = 56;
+  static constexpr int LAUNCH = 168, STREAM = 216, REST = 72;
   static_assert(THREADS * LAUNCH == 2 * 128 * STREAM + 128 * REST, "register split");
 };
 
@@ -86,7 +87,7 @@ __device__ __forceinline__ void group_sync(int x) {
 }
 
 template <bool BF, int D>
-__global__ void __launch_bounds__(TCfg<D>::THREADS) __maxnreg__(TCfg<D>::LAUNCH) attn_tile_kernel(const AttnArgs a) {
+__global__ void __launch_bounds__(TCfg<D>::THREADS) __maxnreg__(TCfg<D>::LAUNCH) attn_tile_kernel(const __grid_constant__ AttnArgs a) {
   typedef TCfg<D> C;
   extern __shared__ unsigned char raw[];
   __shared__ Deal deal;
@@ -100,6 +101,8 @@ __global__ void __launch_bounds__(TCfg<D>::THREADS) __maxnreg__(TCfg<D>::LAUNCH)
                  b_o = b_p + 16, b_drain = b_o + 16;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   if (threadIdx.x == 0) {
+    map_prefetch(&a.kmap);
+    map_prefetch(&a.vmap);
     for (int i = 0; i < C::NB; ++i) bar_init(b_full + 8 * i, 2), bar_init(b_free + 8 * i, 1);
     for (int x = 0; x < 2; ++x) {
       bar_init(b_q + 8 * x, 128);
@@ -138,11 +141,11 @@ __global__ void __launch_bounds__(TCfg<D>::THREADS) __maxnreg__(TCfg<D>::LAUNCH)
       // ---- MMA issue ---------------------------------------------------------------
       if (lane == 0) {
         constexpr unsigned id_qk = inst_desc(BF, false, 128, TUNIT), id_pv = inst_desc(BF, true, 128, D);
-        unsigned nb = 0, seg = 0, np[2] = {0, 0};
+        unsigned nb = 0, seg = 0, np0 = 0, np1 = 0;
         bool ok = true;
         while (u0 < u1 && ok) {
           const Segment g = next_segment(a, deal, s, u0, u1);
-          const int cnt[2] = {g.both ? g.nt : (g.nt + 1) / 2, g.both ? g.nt : g.nt / 2};
+          const int cnt0 = g.both ? g.nt : (g.nt + 1) / 2, cnt1 = g.both ? g.nt : g.nt / 2;
           // scores of stream x's tile j
           auto qk = [&](int x, int j) -> bool {
             const unsigned f = nb + k_at(g.both, g.both ? j : 2 * j + x), buf = f % C::NB;
@@ -164,29 +167,27 @@ __global__ void __launch_bounds__(TCfg<D>::THREADS) __maxnreg__(TCfg<D>::LAUNCH)
           // weighted values of stream x's tile j
           auto pv = [&](int x, int j) -> bool {
             const unsigned f = nb + v_at(g.both, g.both ? j : 2 * j + x, g.nt), buf = f % C::NB;
-            if (!wait(b_full + 8 * buf, f / C::NB) || !wait(b_p + 8 * x, np[x])) return false;
-            ++np[x];
+            if (!wait(b_full + 8 * buf, f / C::NB) || !wait(b_p + 8 * x, x ? np1 : np0)) return false;
+            x ? ++np1 : ++np0;
             tm_after();
             const unsigned p = tmem + x * 128, v = ring + buf * C::BUF;
 #pragma unroll 1
             for (int term = 0; term < 2; ++term)
 #pragma unroll 4
               for (int i = 0; i < TUNIT / 16; ++i)
-                // 32 columns hold the two terms of 32 keys' weights
-                mma_ts(tmem + 256 + x * 128, p + (i >> 1) * 32 + term * 16 + (i & 1) * 8,
+                // 16 columns hold the two terms of 16 keys' weights
+                mma_ts(tmem + 256 + x * 128, p + i * 16 + term * 8,
                        smem_desc(v + i * 2048, C::HALF, 1024), id_pv, term > 0 || i > 0);
             mma_commit(b_o + 8 * x);
             if (!g.both || x == 1) mma_commit(b_free + 8 * buf);
             return true;
           };
-          for (int x = 0; x < 2 && ok; ++x)
-            if (cnt[x]) ok = wait(b_q + 8 * x, seg) && qk(x, 0);
-            else ok = wait(b_q + 8 * x, seg);
-          for (int j = 0; j < cnt[0] && ok; ++j)
-            for (int x = 0; x < 2 && ok; ++x) {
-              if (j < cnt[x]) ok = pv(x, j);
-              if (ok && j + 1 < cnt[x]) ok = qk(x, j + 1);
-            }
+          ok = wait(b_q, seg) && qk(0, 0) && wait(b_q + 8, seg) && (!cnt1 || qk(1, 0));
+          for (int i = 0; i < 2 * cnt0 && ok; ++i) {
+            const int x = i & 1, j = i >> 1, cnt = x ? cnt1 : cnt0;
+            if (j < cnt) ok = pv(x, j);
+            if (ok && j + 1 < cnt) ok = qk(x, j + 1);
+          }
           nb += 2 * g.nt;
           ++seg;
         }
@@ -202,19 +203,14 @@ __global__ void __launch_bounds__(TCfg<D>::THREADS) __maxnreg__(TCfg<D>::LAUNCH)
       __syncwarp();
     } else if (warp >= 2) {
       // ---- the ring's fills ----------------------------------------------------------
-      const int tid = threadIdx.x - 64;
-      constexpr int PP = D / 8;            // 16-byte pieces of a token
-      constexpr int RS = 64 / PP;          // tokens of a pass
-      const int pc = tid % PP, r_in = tid / PP;
-      unsigned f = 0, told = 0;  // fills begun, fills reported
+      // Warp 2 + h fills part h: of D 128 half h of every token, of D 64 half the
+      // tokens.  A tile whose tokens are all there comes by tensor copies; one with
+      // trailing or absent tokens by copies of the threads, which write zeros there.
+      const int part = warp - 2;
+      constexpr int TOK = D == 128 ? TUNIT : TUNIT / 2;  // tokens of a part
+      const int tok0 = D == 128 ? 0 : part * TOK;
+      unsigned f = 0;
       bool ok = true;
-      constexpr unsigned LAG = C::NB - 1;
-      auto tell = [&](unsigned upto) {
-        fence_async();
-        __syncwarp();
-        for (; told != upto; ++told)
-          if (lane == 0) bar_arrive(b_full + 8 * (told % C::NB));
-      };
       while (u0 < u1 && ok) {
         const Segment g = next_segment(a, deal, s, u0, u1);
         const int* table = g.s == a.B ? a.ptable : a.table + (long)g.s * a.table_w;
@@ -226,41 +222,53 @@ __global__ void __launch_bounds__(TCfg<D>::THREADS) __maxnreg__(TCfg<D>::LAUNCH)
           else if (i == 0) is_v = false, t = 0;
           else if (i == 2 * g.nt - 1) is_v = true, t = g.nt - 1;
           else is_v = !(i & 1), t = is_v ? (i - 2) >> 1 : (i + 1) >> 1;
-          const int key0 = (g.ub + t) * TUNIT;
-          // pages of the tile's eight groups of 16 tokens
+          const int key0 = (g.ub + t) * TUNIT + tok0;
+          // pages of the part's groups of 16 tokens
           int pg = -1;
-          if (lane < 8 && key0 + 16 * lane < g.n) pg = __ldg(table + ((key0 + 16 * lane) >> a.page_log2));
-          const unsigned buf = f % C::NB;
-          if (!__all_sync(FULL, bar_try(b_free + 8 * buf, ((f / C::NB) & 1u) ^ 1u))) {
-            cp_wait<0>();
-            tell(f);
-            ok = __all_sync(FULL, wait(b_free + 8 * buf, (f / C::NB) ^ 1u));
-            if (!ok) break;
+          if (lane < TOK / 16 && key0 + 16 * lane < g.n) {
+            pg = __ldg(table + ((key0 + 16 * lane) >> a.page_log2));
+            if ((unsigned)pg >= (unsigned)a.n_pages) pg = -1;
           }
-          const char* src0 = (const char*)(is_v ? a.v : a.k);
-          const unsigned dst0 = ring + buf * C::BUF + (pc >> 3) * C::HALF;
-#pragma unroll 2
-          for (int h = 0; h < 8; ++h) {
-            const int p = __shfl_sync(FULL, pg, h);
-            const int k0 = key0 + 16 * h;
-            const int left = (unsigned)p < (unsigned)a.n_pages ? g.n - k0 : 0;
-            const long r0 = (((long)(left > 0 ? p : 0) * a.n_kv + g.kvh) << a.page_log2) + (k0 & ((1 << a.page_log2) - 1));
-            const char* src = src0 + r0 * (2 * D) + pc * 16;
+          const bool all = __all_sync(FULL, lane >= TOK / 16 || pg >= 0) && key0 + TOK <= g.n;
+          const unsigned buf = f % C::NB, bar = b_full + 8 * buf;
+          const unsigned dst0 = ring + buf * C::BUF + (D == 128 ? part * C::HALF : tok0 * 128);
+          ok = __all_sync(FULL, wait(b_free + 8 * buf, (f / C::NB) ^ 1u));
+          if (!ok) break;
+          if (all) {
+            if (lane == 0) bar_expect(bar, TOK * 128);
+            __syncwarp();
+            // group l's first token begins a box, if the box is not another's
+            const int k0 = key0 + 16 * lane, in = k0 & (a.box - 1);
+            if (lane < TOK / 16 && in == 0)
+              tma_2d(dst0 + lane * 2048, is_v ? &a.vmap : &a.kmap, D == 128 ? part * 64 : 0,
+                     ((pg * a.n_kv + g.kvh) << a.page_log2) + (k0 & ((1 << a.page_log2) - 1)), bar);
+          } else {
+            const char* src0 = (const char*)(is_v ? a.v : a.k) + (D == 128 ? part * 128 : 0);
+            const int pc = lane & 7, r_in = lane >> 3;
+#pragma unroll 1
+            for (int h = 0; h < TOK / 16; ++h) {
+              const int p = __shfl_sync(FULL, pg, h), k0 = key0 + 16 * h, left = p >= 0 ? g.n - k0 : 0;
+              const long r0 = (((long)max(p, 0) * a.n_kv + g.kvh) << a.page_log2) + (k0 & ((1 << a.page_log2) - 1));
 #pragma unroll
-            for (int m = 0; m < 16 / RS; ++m) {
-              const int kk = m * RS + r_in, row = 16 * h + kk;
-              cp16(dst0 + row * 128 + (((pc & 7) ^ (row & 7)) << 4), src + kk * (2 * D), kk < left ? 16 : 0);
+              for (int m = 0; m < 4; ++m) {
+                const int kk = 4 * m + r_in, row = 16 * h + kk;
+                cp16(dst0 + row * 128 + ((pc ^ (row & 7)) << 4), src0 + (r0 + kk) * (2 * D) + pc * 16,
+                     kk < left ? 16 : 0);
+              }
             }
-          }
-          cp_commit();
-          if (f + 1 - told > LAG) {
-            cp_wait<LAG>();
-            tell(f + 1 - LAG);
+            cp_commit();
+            cp_wait<0>();
+            fence_async();
+            __syncwarp();
+            if (lane == 0) bar_arrive(bar);
           }
         }
       }
-      cp_wait<0>();
-      if (ok) tell(f);
+      // a block that gave up: its copies have landed before it ends
+      if (!ok)
+        for (unsigned i = 0; i < C::NB && i < f; ++i)
+          if (lane == 0 && !bar_drain(b_full + 8 * ((f - 1 - i) % C::NB), ((f - 1 - i) / C::NB) & 1u, a.wait_ns))
+            atomicOr(a.err, ERR_TILE_WAIT);
     }
   } else {
     // ---- a stream: a thread to a row ---------------------------------------------------
@@ -347,46 +355,51 @@ __global__ void __launch_bounds__(TCfg<D>::THREADS) __maxnreg__(TCfg<D>::LAUNCH)
         ok = __all_sync(FULL, wait(b_s + 8 * x, nt));
         if (!ok) break;
         tm_after();
-        auto seen = [&](int k) { return key0 + k < vis && ((there >> (k >> 4)) & 1u); };
-        float mx = -INFINITY;
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          unsigned r[32];
-          tm_ld32(ts + 32 * c, r);
-          tm_ld_wait(r);
-          if (whole) {
-#pragma unroll
-            for (int k = 0; k < 32; ++k) mx = fmaxf(mx, __uint_as_float(r[k]));
-          } else {
+        // the scores' maximum, then the weights in their place; CUT: some keys
+        // are absent or not seen by some row
+        float mx = -INFINITY, sum = 0.0f, al, ref;
+        const auto weights = [&](auto cut) {
+          constexpr bool CUT = decltype(cut)::value;
+#pragma unroll 1
+          for (int c = 0; c < 4; ++c) {
+            unsigned r[32];
+            tm_ld32(ts + 32 * c, r);
+            tm_ld_wait(r);
+            const int left = CUT ? vis - key0 - 32 * c : 32;
 #pragma unroll
             for (int k = 0; k < 32; ++k)
-              if (seen(32 * c + k)) mx = fmaxf(mx, __uint_as_float(r[k]));
+              if (!CUT || (k < left && ((there >> (2 * c + (k >> 4))) & 1u))) mx = fmaxf(mx, __uint_as_float(r[k]));
           }
-        }
-        const float mn = fmaxf(m, mx * rs);
-        const float ref = mn == -INFINITY ? 0.0f : mn;
-        const float al = ex2(m - ref);
-        m = mn;
-        float sum = 0.0f;
+          const float mn = fmaxf(m, mx * rs);
+          ref = mn == -INFINITY ? 0.0f : mn;
+          al = ex2(m - ref);
+          m = mn;
+          const float shift = UP - ref;
+#pragma unroll 1
+          for (int c = 0; c < 8; ++c) {
+            unsigned r[16], w[16];
+            tm_ld16(ts + 16 * c, r);
+            tm_ld_wait(r);
+            const int left = !CUT ? 16 : (there >> c) & 1u ? vis - key0 - 16 * c : 0;
+            float s0 = 0.0f, s1 = 0.0f;
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          unsigned r[32], w[32];
-          tm_ld32(ts + 32 * c, r);
-          tm_ld_wait(r);
-#pragma unroll
-          for (int k = 0; k < 32; k += 2) {
-            float p0 = ex2(fmaf(__uint_as_float(r[k]), rs, UP - ref));
-            float p1 = ex2(fmaf(__uint_as_float(r[k + 1]), rs, UP - ref));
-            if (!whole) {
-              if (!seen(32 * c + k)) p0 = 0.0f;
-              if (!seen(32 * c + k + 1)) p1 = 0.0f;
+            for (int k = 0; k < 16; k += 2) {
+              float p0 = ex2(fmaf(__uint_as_float(r[k]), rs, shift));
+              float p1 = ex2(fmaf(__uint_as_float(r[k + 1]), rs, shift));
+              if constexpr (CUT) {
+                p0 = k < left ? p0 : 0.0f;
+                p1 = k + 1 < left ? p1 : 0.0f;
+              }
+              s0 += p0, s1 += p1;
+              w[k >> 1] = split2<BF>(p0, p1);
+              w[8 + (k >> 1)] = split2<BF>(p0, p1);
             }
-            sum += p0 + p1;
-            w[k >> 1] = split2<BF>(p0, p1);
-            w[16 + (k >> 1)] = split2<BF>(p0, p1);
+            sum += s0 + s1;
+            tm_st16(ts + 16 * c, w);
           }
-          tm_st32(ts + 32 * c, w);
-        }
+        };
+        if (whole) weights(std::false_type{});
+        else weights(std::true_type{});
         l = fmaf(l, al, sum);
         tm_st_wait();
         tm_before();
