@@ -519,6 +519,7 @@ struct JoinArgs {
   int8_t* hq;
   int8_t* hl;
   float* hs;
+  int wide;  // out takes a lane's values in one store
 };
 
 // Partials of a row from one item: entry i (0 <= i < n) has its maximum and
@@ -586,42 +587,69 @@ __global__ void __launch_bounds__(128) attn_join_kernel(const JoinArgs j) {
   src[0] = a.own_tiled ? source<true>(a, tdeal, b, kvh, io) : source<false>(a, deal, b, kvh, io);
   if (a.shared && __ldcg(a.lens + b) >= 0)
     src[1] = a.pre_tiled ? source<true>(a, tdeal, a.B, kvh, ip) : source<false>(a, deal, a.B, kvh, ip);
-  float M = -INFINITY;
+  // A lane has V neighbouring values.  Partials come in batches of NB whose
+  // loads are all in flight at once, the values' not waiting for the maxima's.
+  constexpr int V = D / 32, NB = 8;
+  float M = -INFINITY, acc[V], ls = 0.0f;
 #pragma unroll
-  for (int x = 0; x < 2; ++x)
-    for (int i = lane; i < src[x].n; i += 32) M = fmaxf(M, __ldcg(src[x].ml + src[x].at(i) * 2));
-  M = warp_max_xor(M);
-  const float ref = M == -INFINITY ? 0.0f : M;
-  float acc[D / 32], ls = 0.0f;
-#pragma unroll
-  for (int c = 0; c < D / 32; ++c) acc[c] = 0.0f;
-#pragma unroll
+  for (int c = 0; c < V; ++c) acc[c] = 0.0f;
+#pragma unroll 1
   for (int x = 0; x < 2; ++x) {
-    const Source& z = src[x];
-    const int dl = lane ^ (z.flip << 2);  // the lane's place within 32 values
-    for (int i0 = 0; i0 < z.n; i0 += 32) {
-      float f = 0.0f, lf = 0.0f;
-      if (i0 + lane < z.n) {
-        const float2 p = __ldcg((const float2*)(z.ml + z.at(i0 + lane) * 2));
-        f = ex2(p.x - ref);
-        lf = f * p.y;
+    const Source z = x ? src[1] : src[0];
+    const int at = V == 4 ? (lane ^ z.flip) * 4 : ((lane >> 1) ^ z.flip) * 4 + (lane & 1) * 2;
+#pragma unroll 1
+    for (int i0 = 0; i0 < z.n; i0 += NB) {
+      float o[NB][V];
+#pragma unroll
+      for (int i = 0; i < NB; ++i) {
+        const float* p = z.o + z.at(min(i0 + i, z.n - 1)) * D + at;
+        if constexpr (V == 4) *(float4*)o[i] = __ldcg((const float4*)p);
+        else *(float2*)o[i] = __ldcg((const float2*)p);
       }
-      const int n = min(32, z.n - i0);
-#pragma unroll 4
-      for (int i = 0; i < n; ++i) {
+      // lane i < NB: partial i0 + i's maximum and sum
+      const bool in = lane < NB && i0 + lane < z.n;
+      const float2 p = in ? __ldcg((const float2*)(z.ml + z.at(i0 + lane) * 2)) : make_float2(-INFINITY, 0.0f);
+      const float m = fmaxf(M, warp_max_xor(p.x)), ref = m == -INFINITY ? 0.0f : m;
+      const float al = ex2(M - ref), f = ex2(p.x - ref), lf = f * p.y;
+      M = m;
+      ls *= al;
+#pragma unroll
+      for (int c = 0; c < V; ++c) acc[c] *= al;
+#pragma unroll
+      for (int i = 0; i < NB; ++i) {
         const float fi = __shfl_sync(FULL, f, i);
         ls += __shfl_sync(FULL, lf, i);
-        const float* o = z.o + z.at(i0 + i) * D + dl;
+        if (i0 + i < z.n) {
 #pragma unroll
-        for (int c = 0; c < D / 32; ++c) acc[c] = fmaf(fi, __ldcg(o + 32 * c), acc[c]);
+          for (int c = 0; c < V; ++c) acc[c] = fmaf(fi, o[i][c], acc[c]);
+        }
       }
     }
   }
 #pragma unroll
-  for (int c = 0; c < D / 32; ++c) {
-    const float y = ls > 0.0f ? __fdiv_rn(acc[c], ls) : 0.0f;
-    if (j.out) j.out[w * D + 32 * c + lane] = y;
-    if constexpr (Q > 0) quant_lane<Q>(y, j.hq, j.hl, j.hs, w * (D / 32) + c, lane);
+  for (int c = 0; c < V; ++c) acc[c] = ls > 0.0f ? __fdiv_rn(acc[c], ls) : 0.0f;
+  if (j.out) {
+    float* y = j.out + w * D + lane * V;
+    if (j.wide) {
+      if constexpr (V == 4) *(float4*)y = *(const float4*)acc;
+      else *(float2*)y = *(const float2*)acc;
+    } else {
+#pragma unroll
+      for (int c = 0; c < V; ++c) y[c] = acc[c];
+    }
+  }
+  if constexpr (Q > 0) {
+#pragma unroll
+    for (int c = 0; c < V; ++c) {
+      // value 32 c + lane is in lane (32 c + lane) / V
+      float y = 0.0f;
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        const float t = __shfl_sync(FULL, acc[e], (32 * c + lane) / V);
+        y = lane % V == e ? t : y;
+      }
+      quant_lane<Q>(y, j.hq, j.hl, j.hs, w * (D / 32) + c, lane);
+    }
   }
 }
 
@@ -812,6 +840,7 @@ lk_status lk_attn_shared(const lk_kv_cache* cache, const float* q, int n_q, cons
   JoinArgs j;
   j.a = a;
   j.out = out;
+  j.wide = aligned(out, 16);
   j.hq = hq;
   j.hl = mode == LK_TWOPASS ? hl : nullptr;
   j.hs = hs;

@@ -56,6 +56,13 @@ __device__ __forceinline__ bool bar_drain(unsigned bar, unsigned parity, unsigne
   return true;
 }
 
+// True in one thread of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  unsigned e;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(e));
+  return e != 0;
+}
+
 // ---- copies to shared memory ------------------------------------------------------
 // A box of a 2-D tensor map at (x, y) in elements and rows; x is a multiple of 16 bytes.
 __device__ __forceinline__ void tma_2d(unsigned dst, const void* map, int x, int y, unsigned bar) {
@@ -132,6 +139,10 @@ __device__ __forceinline__ void tm_before() { asm volatile("tcgen05.fence::befor
 __device__ __forceinline__ void tm_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 
 // ---- MMA ----------------------------------------------------------------------------
+// Issued by one elected thread of a warp whose loop and operands are uniform:
+// then the operands stay in uniform registers and an MMA of 128 x 128 x 16
+// issues every 65 cycles, the pipe's rate (measured; from a loop of one
+// divergent thread, 100 to 300).
 // Shared-memory operand descriptor, 128-byte swizzle (8 rows of 128 bytes to an
 // atom of 1024): start address, leading and stride offsets in bytes.  K-major:
 // stride = 1024 between groups of 8 rows, leading unused.  MN-major: leading =

@@ -99,7 +99,7 @@ __global__ void __launch_bounds__(TCfg<D>::THREADS) __maxnreg__(TCfg<D>::LAUNCH)
   const unsigned bar0 = smem_addr(bars);
   const unsigned b_full = bar0, b_free = bar0 + 8 * C::NB, b_q = bar0 + 16 * C::NB, b_s = b_q + 16, b_p = b_s + 16,
                  b_o = b_p + 16, b_drain = b_o + 16;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31, warp = __shfl_sync(FULL, threadIdx.x >> 5, 0);
   if (threadIdx.x == 0) {
     map_prefetch(&a.kmap);
     map_prefetch(&a.vmap);
@@ -121,7 +121,7 @@ __global__ void __launch_bounds__(TCfg<D>::THREADS) __maxnreg__(TCfg<D>::LAUNCH)
   tm_before();
   __syncthreads();
   tm_after();
-  const unsigned tmem = *(volatile unsigned*)&tmem_slot;
+  const unsigned tmem = __shfl_sync(FULL, *(volatile unsigned*)&tmem_slot, 0);
   const long T = deal.cum[a.B + a.shared], W = shares(a.TW, T);
   long u0 = 0, u1 = 0;
   if (blockIdx.x < W) u0 = T * blockIdx.x / W, u1 = T * (blockIdx.x + 1) / W;
@@ -138,69 +138,69 @@ __global__ void __launch_bounds__(TCfg<D>::THREADS) __maxnreg__(TCfg<D>::LAUNCH)
   if (warp < 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::REST));
     if (warp == 0) {
-      // ---- MMA issue ---------------------------------------------------------------
-      if (lane == 0) {
-        constexpr unsigned id_qk = inst_desc(BF, false, 128, TUNIT), id_pv = inst_desc(BF, true, 128, D);
-        unsigned nb = 0, seg = 0, np0 = 0, np1 = 0;
-        bool ok = true;
-        while (u0 < u1 && ok) {
-          const Segment g = next_segment(a, deal, s, u0, u1);
-          const int cnt0 = g.both ? g.nt : (g.nt + 1) / 2, cnt1 = g.both ? g.nt : g.nt / 2;
-          // scores of stream x's tile j
-          auto qk = [&](int x, int j) -> bool {
-            const unsigned f = nb + k_at(g.both, g.both ? j : 2 * j + x), buf = f % C::NB;
-            if (!wait(b_full + 8 * buf, f / C::NB)) return false;
-            tm_after();
-            const unsigned q = base + x * C::QS, k = ring + buf * C::BUF;
-#pragma unroll 1
-            for (int term = 0; term < 2; ++term)
-#pragma unroll 4
-              for (int i = 0; i < D / 16; ++i) {
-                const unsigned off = (i >> 2) * C::HALF + (i & 3) * 32;
-                mma_ss(tmem + x * 128, smem_desc(q + term * C::BUF + off, 16, 1024), smem_desc(k + off, 16, 1024),
-                       id_qk, term > 0 || i > 0);
-              }
+      // ---- MMA issue: the warp stays together, one elected thread issues ---------------
+      constexpr unsigned id_qk = inst_desc(BF, false, 128, TUNIT), id_pv = inst_desc(BF, true, 128, D);
+      const bool el = elect_one();
+      const unsigned long long q_desc = smem_desc(base, 16, 1024), k_desc = smem_desc(ring, 16, 1024),
+                               v_desc = smem_desc(ring, C::HALF, 1024);
+      unsigned nb = 0, seg = 0, np0 = 0, np1 = 0;
+      bool ok = true;
+      while (u0 < u1 && ok) {
+        const Segment g = next_segment(a, deal, s, u0, u1);
+        const int cnt0 = g.both ? g.nt : (g.nt + 1) / 2, cnt1 = g.both ? g.nt : g.nt / 2;
+        // scores of stream x's tile j
+        auto qk = [&](int x, int j) -> bool {
+          const unsigned f = nb + k_at(g.both, g.both ? j : 2 * j + x), buf = f % C::NB;
+          if (!__all_sync(FULL, wait(b_full + 8 * buf, f / C::NB))) return false;
+          tm_after();
+          const unsigned long long q = q_desc + ((x * C::QS) >> 4), k = k_desc + ((buf * C::BUF) >> 4);
+          const unsigned dst = tmem + x * 128;
+          if (el) {
+#pragma unroll
+            for (int i = 0; i < 2 * (D / 16); ++i) {
+              const int term = i / (D / 16), st = i % (D / 16), off = (st >> 2) * C::HALF + (st & 3) * 32;
+              mma_ss(dst, q + ((term * C::BUF + off) >> 4), k + (off >> 4), id_qk, i > 0);
+            }
             mma_commit(b_s + 8 * x);
             if (!g.both || x == 1) mma_commit(b_free + 8 * buf);
-            return true;
-          };
-          // weighted values of stream x's tile j
-          auto pv = [&](int x, int j) -> bool {
-            const unsigned f = nb + v_at(g.both, g.both ? j : 2 * j + x, g.nt), buf = f % C::NB;
-            if (!wait(b_full + 8 * buf, f / C::NB) || !wait(b_p + 8 * x, x ? np1 : np0)) return false;
-            x ? ++np1 : ++np0;
-            tm_after();
-            const unsigned p = tmem + x * 128, v = ring + buf * C::BUF;
-#pragma unroll 1
-            for (int term = 0; term < 2; ++term)
-#pragma unroll 4
-              for (int i = 0; i < TUNIT / 16; ++i)
-                // 16 columns hold the two terms of 16 keys' weights
-                mma_ts(tmem + 256 + x * 128, p + i * 16 + term * 8,
-                       smem_desc(v + i * 2048, C::HALF, 1024), id_pv, term > 0 || i > 0);
+          }
+          __syncwarp();
+          return true;
+        };
+        // weighted values of stream x's tile j
+        auto pv = [&](int x, int j) -> bool {
+          const unsigned f = nb + v_at(g.both, g.both ? j : 2 * j + x, g.nt), buf = f % C::NB;
+          if (!__all_sync(FULL, wait(b_full + 8 * buf, f / C::NB) && wait(b_p + 8 * x, x ? np1 : np0))) return false;
+          x ? ++np1 : ++np0;
+          tm_after();
+          const unsigned long long v = v_desc + ((buf * C::BUF) >> 4);
+          const unsigned p = tmem + x * 128, dst = tmem + 256 + x * 128;
+          if (el) {
+#pragma unroll
+            for (int i = 0; i < 2 * (TUNIT / 16); ++i) {
+              // 16 columns hold the two terms of 16 keys' weights
+              const int term = i / (TUNIT / 16), st = i % (TUNIT / 16);
+              mma_ts(dst, p + st * 16 + term * 8, v + ((st * 2048) >> 4), id_pv, i > 0);
+            }
             mma_commit(b_o + 8 * x);
             if (!g.both || x == 1) mma_commit(b_free + 8 * buf);
-            return true;
-          };
-          ok = wait(b_q, seg) && qk(0, 0) && wait(b_q + 8, seg) && (!cnt1 || qk(1, 0));
-          for (int i = 0; i < 2 * cnt0 && ok; ++i) {
-            const int x = i & 1, j = i >> 1, cnt = x ? cnt1 : cnt0;
-            if (j < cnt) ok = pv(x, j);
-            if (ok && j + 1 < cnt) ok = qk(x, j + 1);
           }
-          nb += 2 * g.nt;
-          ++seg;
+          __syncwarp();
+          return true;
+        };
+        ok = __all_sync(FULL, wait(b_q, seg)) && qk(0, 0) && __all_sync(FULL, wait(b_q + 8, seg)) && (!cnt1 || qk(1, 0));
+        for (int i = 0; i < 2 * cnt0 && ok; ++i) {
+          const int x = i & 1, j = i >> 1, cnt = x ? cnt1 : cnt0;
+          if (j < cnt) ok = pv(x, j);
+          if (ok && j + 1 < cnt) ok = qk(x, j + 1);
         }
-        // nothing of this block is in flight when its tensor memory is freed
-        mma_commit(b_drain);
-        const unsigned long long t0 = now_ns();
-        while (!bar_try(b_drain, 0))
-          if (now_ns() - t0 > a.wait_ns) {
-            atomicOr(a.err, ERR_TILE_WAIT);
-            break;
-          }
+        nb += 2 * g.nt;
+        ++seg;
       }
+      // nothing of this block is in flight when its tensor memory is freed
+      if (el) mma_commit(b_drain);
       __syncwarp();
+      if (!bar_drain(b_drain, 0, a.wait_ns) && lane == 0) atomicOr(a.err, ERR_TILE_WAIT);
     } else if (warp >= 2) {
       // ---- the ring's fills ----------------------------------------------------------
       // Warp 2 + h fills part h: of D 128 half h of every token, of D 64 half the
@@ -291,47 +291,53 @@ __global__ void __launch_bounds__(TCfg<D>::THREADS) __maxnreg__(TCfg<D>::LAUNCH)
         if (me == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
         group_sync(x);
       }
-      // queries: a warp loads its 32 rows one after the other, D / 32 values a
-      // lane, and writes their two terms swizzled
+      // queries: a warp takes its 32 rows, D / 32 values a lane, all loads first,
+      // and writes their two terms swizzled
       float rs = 1.0f;
-#pragma unroll 4
-      for (int i = 0; i < 32; ++i) {
-        const int lr = 32 * wq + i;
-        float v[D / 32];
+      {
+        // a lane finds its own row's place, rows without a query are zeros
+        int off = -1;
+        if (me < nr) {
+          const int ri = r_first + me, tok = ri / a.G;
+          off = (pre ? tok : g.s * a.R + tok) * a.n_q + g.kvh * a.G + (ri - tok * a.G);
+        }
+        float v[32][D / 32];
 #pragma unroll
-        for (int c = 0; c < D / 32; ++c) v[c] = 0.0f;
-        if (lr < nr) {
-          const int ri = r_first + lr, tok = ri / a.G, row = pre ? tok : g.s * a.R + tok;
-          const float* q = a.q + ((long)row * a.n_q + g.kvh * a.G + (ri - tok * a.G)) * D + lane * (D / 32);
-          if constexpr (D == 128) {
-            const float4 f = __ldcg((const float4*)q);
-            v[0] = f.x, v[1] = f.y, v[2] = f.z, v[3] = f.w;
-          } else {
-            const float2 f = __ldcg((const float2*)q);
-            v[0] = f.x, v[1] = f.y;
+        for (int i = 0; i < 32; ++i) {
+          const int at = __shfl_sync(FULL, off, i);
+          const float* q = a.q + (long)at * D + lane * (D / 32);
+          float4 f = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+          if (at >= 0) {
+            if constexpr (D == 128) f = __ldcg((const float4*)q);
+            else *(float2*)&f = __ldcg((const float2*)q);
           }
+          v[i][0] = f.x, v[i][1] = f.y;
+          if constexpr (D == 128) v[i][2] = f.z, v[i][3] = f.w;
         }
-        float am = 0.0f;
 #pragma unroll
-        for (int c = 0; c < D / 32; ++c) v[c] *= a.qscale, am = fmaxf(am, fabsf(v[c]));
-        if constexpr (!BF) {
-          float back;
-          const float up = row_shift(warp_absmax(am), back);
-          if (lane == i) rs = back;
+        for (int i = 0; i < 32; ++i) {
+          float am = 0.0f;
 #pragma unroll
-          for (int c = 0; c < D / 32; ++c) v[c] *= up;
-        }
-        // values lane * D/32 ...: 16-byte piece and place in it
-        const int d0 = lane * (D / 32), piece = (d0 & 63) >> 3;
-        const unsigned at = qs + (d0 >> 6) * C::HALF + lr * 128 + ((piece ^ (lr & 7)) << 4) + (d0 & 7) * 2;
+          for (int c = 0; c < D / 32; ++c) v[i][c] *= a.qscale, am = fmaxf(am, fabsf(v[i][c]));
+          if constexpr (!BF) {
+            float back;
+            const float up = row_shift(warp_absmax(am), back);
+            if (lane == i) rs = back;
 #pragma unroll
-        for (int term = 0; term < 2; ++term) {
-          const unsigned w0 = split2<BF>(v[0], v[1]);
-          if constexpr (D == 128) {
-            const unsigned w1 = split2<BF>(v[2], v[3]);
-            asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(at + term * C::BUF), "r"(w0), "r"(w1) : "memory");
-          } else {
-            asm volatile("st.shared.u32 [%0], %1;" ::"r"(at + term * C::BUF), "r"(w0) : "memory");
+            for (int c = 0; c < D / 32; ++c) v[i][c] *= up;
+          }
+          // values lane * D/32 ...: 16-byte piece and place in it
+          const int lr = 32 * wq + i, d0 = lane * (D / 32), piece = (d0 & 63) >> 3;
+          const unsigned at = qs + (d0 >> 6) * C::HALF + lr * 128 + ((piece ^ (lr & 7)) << 4) + (d0 & 7) * 2;
+#pragma unroll
+          for (int term = 0; term < 2; ++term) {
+            const unsigned w0 = split2<BF>(v[i][0], v[i][1]);
+            if constexpr (D == 128) {
+              const unsigned w1 = split2<BF>(v[i][2], v[i][3]);
+              asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(at + term * C::BUF), "r"(w0), "r"(w1) : "memory");
+            } else {
+              asm volatile("st.shared.u32 [%0], %1;" ::"r"(at + term * C::BUF), "r"(w0) : "memory");
+            }
           }
         }
       }
@@ -375,17 +381,20 @@ __global__ void __launch_bounds__(TCfg<D>::THREADS) __maxnreg__(TCfg<D>::LAUNCH)
           al = ex2(m - ref);
           m = mn;
           const float shift = UP - ref;
-#pragma unroll 1
+          unsigned r[2][16];
+          tm_ld16(ts, r[0]);
+          tm_ld_wait(r[0]);
+#pragma unroll
           for (int c = 0; c < 8; ++c) {
-            unsigned r[16], w[16];
-            tm_ld16(ts + 16 * c, r);
-            tm_ld_wait(r);
+            unsigned(&y)[16] = r[c & 1];
+            if (c < 7) tm_ld16(ts + 16 * (c + 1), r[(c + 1) & 1]);
             const int left = !CUT ? 16 : (there >> c) & 1u ? vis - key0 - 16 * c : 0;
             float s0 = 0.0f, s1 = 0.0f;
+            unsigned w[16];
 #pragma unroll
             for (int k = 0; k < 16; k += 2) {
-              float p0 = ex2(fmaf(__uint_as_float(r[k]), rs, shift));
-              float p1 = ex2(fmaf(__uint_as_float(r[k + 1]), rs, shift));
+              float p0 = ex2(fmaf(__uint_as_float(y[k]), rs, shift));
+              float p1 = ex2(fmaf(__uint_as_float(y[k + 1]), rs, shift));
               if constexpr (CUT) {
                 p0 = k < left ? p0 : 0.0f;
                 p1 = k + 1 < left ? p1 : 0.0f;
@@ -395,6 +404,7 @@ __global__ void __launch_bounds__(TCfg<D>::THREADS) __maxnreg__(TCfg<D>::LAUNCH)
               w[8 + (k >> 1)] = split2<BF>(p0, p1);
             }
             sum += s0 + s1;
+            if (c < 7) tm_ld_wait(r[(c + 1) & 1]);
             tm_st16(ts + 16 * c, w);
           }
         };
