@@ -91,17 +91,51 @@ struct Cfg {
   static constexpr int NW = TYPE != LK_KV_Q8 && D == 128 ? 7 : 8;  // warps
   static constexpr int ST = TYPE != LK_KV_Q8 && D == 128 ? 2 : 3;  // stages a warp
   static constexpr int RING = NW * ST * STAGE + 1024;  // and the base's alignment
-  static_assert(STAGE * ST >= TR * (D + 4) * 4, "a warp's partial fits in its stages");
+  static_assert(STAGE * ST >= TR * (D + 4) * 4 && NW <= kMaxWarps, "a warp's partial fits in its stages");
   static_assert(NW * ST <= 32 && RING + 2048 <= 232448, "shared memory of a block");
 };
+
+// Where a warp is: unit u of item li (of that sequence) of sequence s, whose
+// items have un units and n keys.
+struct Cursor {
+  int s, li, u, un, n;
+};
+
+// By a whole warp.
+__device__ __forceinline__ Cursor cursor_at(const AttnArgs& a, const Deal& d, long unit) {
+  const int lane = threadIdx.x & 31, nseq = a.B + a.shared;
+  Cursor c;
+  c.s = 0;
+  for (int s0 = 0; s0 < nseq; s0 += 32)
+    c.s += __popc(__ballot_sync(FULL, s0 + lane < nseq && d.cum[s0 + lane + 1] <= unit));
+  c.un = d.un[c.s];
+  c.n = d.n[c.s];
+  const long rel = unit - d.cum[c.s];
+  c.li = (int)(rel / c.un);
+  c.u = (int)(rel - (long)c.li * c.un);
+  return c;
+}
+
+// To the next unit; behind the last one s is the number of sequences.
+__device__ __forceinline__ void advance(const AttnArgs& a, const Deal& d, Cursor& c) {
+  if (++c.u < c.un) return;
+  c.u = 0;
+  if (++c.li < a.n_kv * groups_of<false>(a, c.s)) return;
+  c.li = 0;
+  const int nseq = a.B + a.shared;
+  while (++c.s < nseq)
+    if ((c.un = d.un[c.s]) > 0) {
+      c.n = d.n[c.s];
+      return;
+    }
+}
 
 template <int TYPE, int D>
 __global__ void __launch_bounds__(32 * Cfg<TYPE, D>::NW, 1) attn_kernel(const __grid_constant__ AttnArgs a) {
   typedef Cfg<TYPE, D> C;
   constexpr bool Q8 = TYPE == LK_KV_Q8;
-  constexpr int KS = D / 16;                       // k-steps of a score
-  constexpr int QT = TYPE == LK_KV_BF16 ? 3 : 2;   // terms of a query
-  constexpr int NT = D / 8;                        // n-tiles of the output
+  constexpr int KS = D / 16;  // k-steps of a score
+  constexpr int NT = D / 8;   // n-tiles of the output
   extern __shared__ unsigned char raw[];
   __shared__ Deal deal;
   __shared__ float wml[C::NW][TR][2];
@@ -115,39 +149,106 @@ __global__ void __launch_bounds__(32 * Cfg<TYPE, D>::NW, 1) attn_kernel(const __
     map_prefetch(&a.vmap);
   }
   asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-  asm volatile("griddepcontrol.launch_dependents;" :::);
+  // the launch after this one may read what this one's predecessors wrote
+  // before it waits for this one (the join's deal): so the wait comes first
   asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" :::);
   if (threadIdx.x < 32) make_deal<false>(a, deal);
   __syncthreads();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
-  const int nseq = a.B + a.shared;
-  const long T = deal.cum[nseq], W = shares(a.W, T);
+  const int lane = threadIdx.x & 31, warp = __shfl_sync(FULL, threadIdx.x >> 5, 0), g = lane >> 2, t = lane & 3;
+  const long T = deal.cum[a.B + a.shared], W = stream_blocks(a.W, C::NW, T);
   if (blockIdx.x >= W) return;
-  long u0 = T * blockIdx.x / W;
-  const long u1 = T * (blockIdx.x + 1) / W;
+  const long ca = T * blockIdx.x / W;
+  const int cn = (int)(T * (blockIdx.x + 1) / W - ca), we = min(C::NW, cn);
+  const int wa = warp < we ? (int)((long)cn * warp / we) : cn;
+  int left = (warp < we ? (int)((long)cn * (warp + 1) / we) : cn) - wa;  // units the warp has to do
+  Cursor cc = cursor_at(a, deal, ca);
+  const bool one = cc.u + cn <= cc.un;  // the block's units are all one item's: its warps join their parts
+  if (one) cc.u += wa;
+  else if (left > 0) cc = cursor_at(a, deal, ca + wa);
   const unsigned ring = smem_addr(smem) + warp * C::ST * C::STAGE, bar0 = smem_addr(bars) + 8 * warp * C::ST;
+
+  // pages of a unit's two halves (-1: none)
+  auto pages = [&](const Cursor& c, int (&pg)[2]) {
+    const int* table = c.s == a.B ? a.ptable : a.table + (long)c.s * a.table_w;
+#pragma unroll
+    for (int hf = 0; hf < 2; ++hf) {
+      const int key = c.u * UNIT + 16 * hf;
+      pg[hf] = -1;
+      if (key < c.n) {
+        const int p = __ldg(table + (key >> a.page_log2));
+        if ((unsigned)p < (unsigned)a.n_pages) pg[hf] = p;
+      }
+    }
+  };
+  unsigned there = 0;  // bits 2 i, 2 i + 1: stage i's halves have pages
+  unsigned asked = 0;  // bit i: stage i has a unit that was not waited for
+  // ask for a unit (one thread of the warp); a.box is 16 or 32 rows
+  auto issue = [&](const Cursor& c, const int (&pg)[2], int stage) {
+    there = (there & ~(3u << (2 * stage))) | ((pg[0] >= 0 ? 1u : 0u) | (pg[1] >= 0 ? 2u : 0u)) << (2 * stage);
+    asked |= 1u << stage;
+    const int kvh = c.li / groups_of<false>(a, c.s);
+    if (lane != 0) return;
+    const unsigned st = ring + stage * C::STAGE, bar = bar0 + 8 * stage;
+    const int n_box = a.box == 32 ? 1 : 2;
+    unsigned bytes = 0;
+    for (int hf = 0; hf < n_box; ++hf)
+      if (pg[hf] >= 0) bytes += 2 * a.box * (D * C::EB + (Q8 ? D / 16 : 0));
+    bar_expect(bar, bytes);
+    for (int hf = 0; hf < n_box; ++hf) {
+      if (pg[hf] < 0) continue;
+      const int key0 = c.u * UNIT + 16 * hf;
+      const int r0 = ((pg[hf] * a.n_kv + kvh) << a.page_log2) + (key0 & ((1 << a.page_log2) - 1));
+#pragma unroll
+      for (int p = 0; p < C::PARTS; ++p) {
+        const unsigned at = st + p * UNIT * C::ROW + 16 * hf * C::ROW;
+        tma_2d(at, &a.kmap, p * (C::ROW / C::EB), r0, bar);
+        tma_2d(at + C::KV, &a.vmap, p * (C::ROW / C::EB), r0, bar);
+      }
+      if constexpr (Q8) {
+        const unsigned at = st + 2 * C::KV + hf * D, n = a.box * (D / 16);
+        bulk_in(at, (const char*)a.ks + (long)r0 * (D / 16), n, bar);
+        bulk_in(at + C::SC, (const char*)a.vs + (long)r0 * (D / 16), n, bar);
+      }
+    }
+  };
+
+  // The ring's first units; ac: the unit to ask for next, with its pages.
+  Cursor ac = cc;
+  int ask = left, pg[2] = {-1, -1};
+  {
+    Cursor c[C::ST];
+    int p[C::ST][2];
+#pragma unroll
+    for (int i = 0; i < C::ST; ++i) {
+      c[i] = ac;
+      if (i < ask) {
+        pages(ac, p[i]);
+        advance(a, deal, ac);
+      }
+    }
+    if (ask > C::ST) pages(ac, pg);
+#pragma unroll
+    for (int i = 0; i < C::ST; ++i)
+      if (i < ask) issue(c[i], p[i], i);
+    ask -= min(ask, C::ST);
+  }
   unsigned phases = 0;  // bit i: the parity stage i's copies complete next
-  int s = 0;
-  while (u0 < u1) {
-    while (deal.cum[s + 1] <= u0) ++s;
-    const int un = deal.un[s], n = deal.n[s];
-    const long rel = u0 - deal.cum[s];
-    const int li = (int)(rel / un), ub = (int)(rel - (long)li * un);
-    const int ue = (int)min((long)un, ub + (u1 - u0));
-    u0 += ue - ub;
-    const int tiles = groups_of<false>(a, s), kvh = li / tiles, tile = li - kvh * tiles;
-    const int slot = (int)blockIdx.x + item0<false>(a, s) + li;
+  int stage = 0;
+  bool fail = false;
+  while (left > 0) {
+    // ---- an item
+    const int s = cc.s, n = cc.n, tiles = groups_of<false>(a, s), kvh = cc.li / tiles, tile = cc.li - kvh * tiles;
     const bool pre = s == a.B;
     const int nrows = min(TR, rows_of(a, s) - tile * TR);
-    const int* table = pre ? a.ptable : a.table + (long)s * a.table_w;
-
+    const long slot = (long)blockIdx.x * C::NW + (one ? 0 : warp) + item0<false>(a, s) + cc.li;
     // the lane's query row (the last row again where there are fewer)
     const int ri = tile * TR + min(g, nrows - 1);
     const int tok = ri / a.G;  // row of the batch (prefix) or of the sequence
     const int row = pre ? tok : s * a.R + tok;
     int vis = n;  // keys that the row sees
     if (!pre) vis = min(n, max(0, __ldcg(a.lens + s) - a.R + 1 + tok));
-    unsigned qa[KS][4], qc[QT == 3 ? KS : 1][2];
+    unsigned qa[KS][4];
     float rs = 1.0f;
     {
       const float* q = a.q + ((long)row * a.n_q + kvh * a.G + (ri - tok * a.G)) * D + t * 8;
@@ -178,96 +279,42 @@ __global__ void __launch_bounds__(32 * Cfg<TYPE, D>::NW, 1) attn_kernel(const __
         qa[k][2] = split2<TYPE == LK_KV_BF16>(x[4 * k + 2], x[4 * k + 3]);
         qa[k][1] = split2<TYPE == LK_KV_BF16>(x[4 * k], x[4 * k + 1]);
         qa[k][3] = split2<TYPE == LK_KV_BF16>(x[4 * k + 2], x[4 * k + 3]);
-        if constexpr (QT == 3) {
-          qc[k][0] = split2<TYPE == LK_KV_BF16>(x[4 * k], x[4 * k + 1]);
-          qc[k][1] = split2<TYPE == LK_KV_BF16>(x[4 * k + 2], x[4 * k + 3]);
-        }
       }
     }
-
-    // pages of the unit's two halves (-1: none)
-    auto pages = [&](int u, int (&pg)[2]) {
-#pragma unroll
-      for (int hf = 0; hf < 2; ++hf) {
-        const int key = u * UNIT + 16 * hf;
-        pg[hf] = -1;
-        if (u < ue && key < n) {
-          const int p = __ldg(table + (key >> a.page_log2));
-          if ((unsigned)p < (unsigned)a.n_pages) pg[hf] = p;
-        }
-      }
-    };
-    // ask for unit u (one thread of the warp); a.box is 16 or 32 rows
-    auto issue = [&](int u, const int (&pg)[2], int stage) {
-      if (lane != 0) return;
-      const unsigned st = ring + stage * C::STAGE, bar = bar0 + 8 * stage;
-      const int n_box = a.box == 32 ? 1 : 2;
-      unsigned bytes = 0;
-      for (int hf = 0; hf < n_box; ++hf)
-        if (pg[hf] >= 0) bytes += 2 * a.box * (D * C::EB + (Q8 ? D / 16 : 0));
-      bar_expect(bar, bytes);
-      for (int hf = 0; hf < n_box; ++hf) {
-        if (pg[hf] < 0) continue;
-        const int key0 = u * UNIT + 16 * hf;
-        const int r0 = ((pg[hf] * a.n_kv + kvh) << a.page_log2) + (key0 & ((1 << a.page_log2) - 1));
-#pragma unroll
-        for (int p = 0; p < C::PARTS; ++p) {
-          const unsigned at = st + p * UNIT * C::ROW + 16 * hf * C::ROW;
-          tma_2d(at, &a.kmap, p * (C::ROW / C::EB), r0, bar);
-          tma_2d(at + C::KV, &a.vmap, p * (C::ROW / C::EB), r0, bar);
-        }
-        if constexpr (Q8) {
-          const unsigned at = st + 2 * C::KV + hf * D, n = a.box * (D / 16);
-          bulk_in(at, (const char*)a.ks + (long)r0 * (D / 16), n, bar);
-          bulk_in(at + C::SC, (const char*)a.vs + (long)r0 * (D / 16), n, bar);
-        }
-      }
-    };
 
     float O[NT][2], m = -INFINITY, l = 0.0f, dvm = 0.0f, dsc = 1.0f;
 #pragma unroll
     for (int i = 0; i < NT; ++i) O[i][0] = O[i][1] = 0.0f;
-    int pgq[C::ST][2], pgn[2];
-    const int uw = ub + warp;
-#pragma unroll
-    for (int i = 0; i < C::ST; ++i) {
-      pages(uw + i * C::NW, pgq[i]);
-    }
-#pragma unroll
-    for (int i = 0; i < C::ST; ++i) {
-      if (uw + i * C::NW < ue) issue(uw + i * C::NW, pgq[i], i);
-    }
-    pages(uw + C::ST * C::NW, pgn);
-    int stage = 0, u = uw;
-    for (; u < ue; u += C::NW) {
+    const int ue = min(cc.un, cc.u + left);
+    left -= ue - cc.u;
+    for (int u = cc.u; u < ue; ++u) {
       if (!bar_wait(bar0 + 8 * stage, (phases >> stage) & 1u, a.wait_ns, &abort_flag)) {
         if (lane == 0 && !*(volatile int*)&abort_flag) {
           *(volatile int*)&abort_flag = 1;
           atomicOr(a.err, ERR_ATTN_WAIT);
         }
+        fail = true;
       }
-      if (__any_sync(FULL, *(volatile int*)&abort_flag)) break;
+      fail = __any_sync(FULL, fail);
+      if (fail) break;
       phases ^= 1u << stage;
+      asked &= ~(1u << stage);
       const unsigned st = ring + stage * C::STAGE;
       // ---- scores: lane (g, t) has row g with keys 8 i + 2 t, + 1
       float sc[4][2];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         if constexpr (!Q8) {
-          float c[4] = {0.f, 0.f, 0.f, 0.f}, c3[4] = {0.f, 0.f, 0.f, 0.f};
+          float c[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
           for (int j = 0; j < D / 32; ++j) {
             // piece 4 (j & 1) + t of the token's part j >> 1
             const uint4 w = lds128(st + (j >> 1) * (UNIT * 128) + (8 * i + g) * 128 + (((4 * (j & 1) + t) ^ g) << 4));
             mma16<TYPE>(c, qa[2 * j][0], qa[2 * j][1], qa[2 * j][2], qa[2 * j][3], w.x, w.y);
             mma16<TYPE>(c, qa[2 * j + 1][0], qa[2 * j + 1][1], qa[2 * j + 1][2], qa[2 * j + 1][3], w.z, w.w);
-            if constexpr (QT == 3) {
-              mma16<TYPE>(c3, qc[2 * j][0], 0u, qc[2 * j][1], 0u, w.x, w.y);
-              mma16<TYPE>(c3, qc[2 * j + 1][0], 0u, qc[2 * j + 1][1], 0u, w.z, w.w);
-            }
           }
-          sc[i][0] = (c[0] + (c[2] + c3[0])) * rs;
-          sc[i][1] = (c[1] + (c[3] + c3[1])) * rs;
+          sc[i][0] = (c[0] + c[2]) * rs;
+          sc[i][1] = (c[1] + c[3]) * rs;
         } else {
           const int key = 8 * i + g, fk = D == 128 ? g : (key >> 1) & 3;  // the swizzle
           // scales of keys 8 i + 2 t, + 1
@@ -300,14 +347,14 @@ __global__ void __launch_bounds__(32 * Cfg<TYPE, D>::NW, 1) attn_kernel(const __
         }
       }
       // ---- what the row does not see
-      const int pg0 = pgq[0][0], pg1 = pgq[0][1];
-      const bool whole = (u + 1) * UNIT <= n && pg0 >= 0 && pg1 >= 0;
+      const bool in0 = (there >> (2 * stage)) & 1u, in1 = (there >> (2 * stage + 1)) & 1u;  // the halves' pages
+      const bool whole = (u + 1) * UNIT <= n && in0 && in1;
       if (!__all_sync(FULL, whole && (u + 1) * UNIT <= vis)) {
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
           for (int x = 0; x < 2; ++x)
-            if (u * UNIT + 8 * i + 2 * t + x >= vis || (i < 2 ? pg0 : pg1) < 0) sc[i][x] = -INFINITY;
+            if (u * UNIT + 8 * i + 2 * t + x >= vis || !(i < 2 ? in0 : in1)) sc[i][x] = -INFINITY;
       }
       // ---- running maximum, weights
       float mt = fmaxf(fmaxf(fmaxf(sc[0][0], sc[0][1]), fmaxf(sc[1][0], sc[1][1])),
@@ -335,7 +382,7 @@ __global__ void __launch_bounds__(32 * Cfg<TYPE, D>::NW, 1) attn_kernel(const __
         for (int i = 0; i < HW; ++i) {
           const int w = i * 32 + lane;
           unsigned x = lds32(st + 2 * C::KV + C::SC + w * 4) & 0x7fff7fffu;
-          if (u * UNIT + w / HW >= n || (w / HW < 16 ? pg0 : pg1) < 0) x = 0;
+          if (u * UNIT + w / HW >= n || !(w / HW < 16 ? in0 : in1)) x = 0;
           mx = max(mx, max(x & 0xffffu, x >> 16));
         }
         mx = __reduce_max_sync(FULL, mx);
@@ -368,7 +415,7 @@ __global__ void __launch_bounds__(32 * Cfg<TYPE, D>::NW, 1) attn_kernel(const __
             const int key = 16 * (e >> 2) + 2 * t + (e & 1) + 8 * ((e >> 1) & 1);
             uint4 x = lds128(st + C::KV + h * (UNIT * 128) + key * 128 + ((g ^ (key & 7)) << 4));
             // what lies behind the tokens may be anything: 0 * NaN is not 0
-            if (!whole && (u * UNIT + key >= n || (e < 4 ? pg0 : pg1) < 0)) x = make_uint4(0, 0, 0, 0);
+            if (!whole && (u * UNIT + key >= n || !(e < 4 ? in0 : in1))) x = make_uint4(0, 0, 0, 0);
             w[e][0] = x.x, w[e][1] = x.y, w[e][2] = x.z, w[e][3] = x.w;
           }
 #pragma unroll
@@ -401,8 +448,8 @@ __global__ void __launch_bounds__(32 * Cfg<TYPE, D>::NW, 1) attn_kernel(const __
           if (!whole) {
 #pragma unroll
             for (int x = 0; x < D / 64; ++x) {
-              if (key >= n || (i < 2 ? pg0 : pg1) < 0) d0[i][x] = __half2half2(__ushort_as_half(0));
-              if (key + 1 >= n || (i < 2 ? pg0 : pg1) < 0) d1[i][x] = __half2half2(__ushort_as_half(0));
+              if (key >= n || !(i < 2 ? in0 : in1)) d0[i][x] = __half2half2(__ushort_as_half(0));
+              if (key + 1 >= n || !(i < 2 ? in0 : in1)) d1[i][x] = __half2half2(__ushort_as_half(0));
             }
           }
         }
@@ -453,21 +500,19 @@ __global__ void __launch_bounds__(32 * Cfg<TYPE, D>::NW, 1) attn_kernel(const __
         }
       }
       // ---- the stage's next unit
-      const int nu = u + C::ST * C::NW;
-#pragma unroll
-      for (int i = 0; i + 1 < C::ST; ++i) pgq[i][0] = pgq[i + 1][0], pgq[i][1] = pgq[i + 1][1];
-      pgq[C::ST - 1][0] = pgn[0], pgq[C::ST - 1][1] = pgn[1];
       __syncwarp();  // every lane is done with the stage
-      if (nu < ue) issue(nu, pgn, stage);
-      pages(nu + C::NW, pgn);
+      if (ask > 0) {
+        issue(ac, pg, stage);
+        advance(a, deal, ac);
+        if (--ask > 0) pages(ac, pg);
+      }
       stage = stage + 1 == C::ST ? 0 : stage + 1;
     }
-    // a warp that gave up: nothing of its copies is in flight when the block ends
-    for (int i = 0; u < ue && i < C::ST; ++i, u += C::NW, stage = stage + 1 == C::ST ? 0 : stage + 1)
-      if (!bar_drain(bar0 + 8 * stage, (phases >> stage) & 1u, a.wait_ns) && lane == 0) atomicOr(a.err, ERR_ATTN_WAIT);
-    if (__syncthreads_or(abort_flag)) return;
+    if (fail) break;
+    cc.u = ue - 1;
+    if (left > 0) advance(a, deal, cc);
 
-    // ---- the warps' partials of the segment, joined in warp order
+    // ---- its partial
     if constexpr (Q8) {
       const float back = 1.0f / dsc;
 #pragma unroll
@@ -475,40 +520,52 @@ __global__ void __launch_bounds__(32 * Cfg<TYPE, D>::NW, 1) attn_kernel(const __
     }
     l += __shfl_xor_sync(FULL, l, 1);
     l += __shfl_xor_sync(FULL, l, 2);
-    float* mine = (float*)(smem + (size_t)warp * C::ST * C::STAGE);  // [TR][D + 4]
     if (g < nrows) {
+      // of several items to a block, straight to the workspace; of one, beside
+      // the other warps' in the stages, which are done with
+      float* to = one ? (float*)(smem + (size_t)warp * C::ST * C::STAGE) + g * (D + 4) : a.o + (slot * TR + g) * D;
+      constexpr int E = Q8 ? 4 : 8;  // neighbouring values of a lane
 #pragma unroll
-      for (int i = 0; i < NT; ++i)
+      for (int b = 0; b < NT / E; ++b)
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          const int d = Q8 ? (i >> 2) * 32 + (2 * t + x) * 4 + (i & 3) : (i >> 3) * 64 + (2 * t + x) * 8 + (i & 7);
-          mine[g * (D + 4) + d] = O[i][x];
-        }
-      if (t == 0) wml[warp][g][0] = m, wml[warp][g][1] = l;
+        for (int x = 0; x < 2; ++x)
+#pragma unroll
+          for (int i = 0; i < E; i += 4)
+            *(float4*)(to + b * 8 * E + (2 * t + x) * E + i) =
+                make_float4(O[b * E + i][x], O[b * E + i + 1][x], O[b * E + i + 2][x], O[b * E + i + 3][x]);
+      if (t == 0) {
+        if (one) wml[warp][g][0] = m, wml[warp][g][1] = l;
+        else *(float2*)(a.ml + (slot * TR + g) * 2) = make_float2(m, l);
+      }
     }
-    __syncthreads();
+  }
+  if (fail) {
+    // nothing of the warp's copies is in flight when the block ends
+    for (int i = 0; i < C::ST; ++i)
+      if ((asked >> i) & 1u) bar_drain(bar0 + 8 * i, (phases >> i) & 1u, a.wait_ns);
+  }
+  if (!one || __syncthreads_or(abort_flag)) return;
+
+  // ---- one item: the warps' partials, joined in warp order
+  {
+    const int s = cc.s, tiles = groups_of<false>(a, s), tile = cc.li % tiles;
+    const int nrows = min(TR, rows_of(a, s) - tile * TR);
+    const long slot = (long)blockIdx.x * C::NW + item0<false>(a, s) + cc.li;
     for (int i = threadIdx.x; i < nrows * D; i += 32 * C::NW) {
       const int r = i / D, d = i - r * D;
-      float M = wml[0][r][0];
-#pragma unroll
-      for (int w = 1; w < C::NW; ++w) M = fmaxf(M, wml[w][r][0]);
+      float M = -INFINITY;
+      for (int w = 0; w < we; ++w) M = fmaxf(M, wml[w][r][0]);
       const float ref = M == -INFINITY ? 0.0f : M;
       float acc = 0.0f, ls = 0.0f;
-#pragma unroll
-      for (int w = 0; w < C::NW; ++w) {
+      for (int w = 0; w < we; ++w) {
         const float f = ex2(wml[w][r][0] - ref);
         const float ov = *(const float*)(smem + (size_t)w * C::ST * C::STAGE + (size_t)(r * (D + 4) + d) * 4);
         acc = fmaf(f, ov, acc);
         ls = fmaf(f, wml[w][r][1], ls);
       }
-      __stcg(a.o + ((long)slot * TR + r) * D + d, acc);
-      if (d == 0) {
-        __stcg(a.ml + ((long)slot * TR + r) * 2, M);
-        __stcg(a.ml + ((long)slot * TR + r) * 2 + 1, ls);
-      }
+      a.o[(slot * TR + r) * D + d] = acc;
+      if (d == 0) *(float2*)(a.ml + (slot * TR + r) * 2) = make_float2(M, ls);
     }
-    fence_async();  // the next segment's copies come after these accesses
-    __syncthreads();
   }
 }
 
@@ -523,47 +580,79 @@ struct JoinArgs {
 };
 
 // Partials of a row from one item: entry i (0 <= i < n) has its maximum and
-// sum at ml + 2 r and its values at o + r * D, r = first + (i / per) * step + (i % per) *
-// hop; flip: the values' 16-byte pieces are permuted by this (tile partials).
+// sum at ml + 2 at(i), its values at o + D at(i); the values' 16-byte pieces are
+// permuted by flip (tile partials).  Streaming: n0 warps of the item's first
+// block, nm blocks that have nothing else, warps of its last block.  Tile: a
+// block each, with `per` partials of the row.
 struct Source {
   const float* ml;
   const float* o;
-  long first;
-  int n, per, step, hop, flip;
+  long first, mid, last;
+  int n, n0, nm, step, per, hop, flip;
   __device__ __forceinline__ long at(int i) const {
+    if (i < n0) return first + (long)i * TR;
+    i -= n0;
     const int j = per == 1 ? i : i >> 1;
-    return first + (long)j * step + (i - j * per) * hop;
+    if (j < nm) return mid + (long)j * step + (i - j * per) * hop;
+    return last + (long)(i - nm) * TR;
   }
 };
 
-// Row i of key/value head kvh in sequence s of the streaming (tile) deal.
-template <bool TILED>
-__device__ __forceinline__ Source source(const AttnArgs& a, const Deal& d, int s, int kvh, int i) {
+// Row i of key/value head kvh in sequence s of the streaming deal.
+__device__ __forceinline__ Source stream_source(const AttnArgs& a, const Deal& d, int s, int kvh, int i) {
   Source r = {};
   const int un = d.un[s];
   if (un == 0) return r;
-  constexpr int N = TILED ? TROWS : TR;
-  const long T = d.cum[a.B + a.shared], W = shares(TILED ? a.TW : a.W, T);
-  const int group = i / N, li = kvh * groups_of<TILED>(a, s) + group, ig = i - group * N;
-  const long ub = d.cum[s] + (long)li * un;
-  // the last w with T * w / W <= u has unit u
-  const int w0 = (int)(((ub + 1) * W - 1) / T), w1 = (int)(((ub + un) * W - 1) / T);
-  const long slot = w0 + item0<TILED>(a, s) + li;
-  r.n = w1 - w0 + 1;
+  const long T = d.cum[a.B + a.shared], W = stream_blocks(a.W, a.NW, T);
+  const int tile = i / TR, li = kvh * groups_of<false>(a, s) + tile, item = item0<false>(a, s) + li;
+  const long ib = d.cum[s] + (long)li * un, ie = ib + un;  // the item's units
+  // the last c with T * c / W <= u has unit u
+  const int c0 = (int)(((ib + 1) * W - 1) / T), c1 = (int)((ie * W - 1) / T);
+  // entries of block c: one if it has nothing else, else one of each warp with units of the item
+  const auto part = [&](int c, long& at, int& n) {
+    const long ca = T * c / W, cb = T * (c + 1) / W;
+    int w0 = 0, w1 = 0;
+    if (ca < ib || cb > ie) {
+      const int cn = (int)(cb - ca), we = min(a.NW, cn);
+      const long ua = max(ca, ib) - ca, ub = min(cb, ie) - ca;
+      w0 = (int)(((ua + 1) * we - 1) / cn);
+      w1 = (int)((ub * we - 1) / cn);
+    }
+    at = ((long)c * a.NW + w0 + item) * TR + i % TR;
+    n = w1 - w0 + 1;
+  };
+  int n2 = 0;
+  part(c0, r.first, r.n0);
+  if (c1 > c0) part(c1, r.last, n2);
+  r.nm = c1 > c0 ? c1 - c0 - 1 : 0;
+  r.mid = ((long)(c0 + 1) * a.NW + item) * TR + i % TR;
+  r.step = a.NW * TR;
   r.per = 1;
-  if constexpr (TILED) {
-    const int rows = rows_of(a, s), rg = min(TROWS, rows - group * TROWS), which = s == a.B ? 1 : 0;
-    r.step = tile_slot_rows(rows);
-    r.ml = a.tml[which];
-    r.o = a.to[which];
-    r.flip = rg > 128 ? ig & 127 & 7 : ig & 7;
-    if (rg <= 128) r.per = 2, r.hop = rg, r.n *= 2;
-  } else {
-    r.step = TR;
-    r.ml = a.ml;
-    r.o = a.o;
-  }
-  r.first = slot * r.step + ig;
+  r.n = r.n0 + r.nm + n2;
+  r.ml = a.ml;
+  r.o = a.o;
+  return r;
+}
+
+// The same of the tile deal.
+__device__ __forceinline__ Source tile_source(const AttnArgs& a, const Deal& d, int s, int kvh, int i) {
+  Source r = {};
+  const int un = d.un[s];
+  if (un == 0) return r;
+  const long T = d.cum[a.B + a.shared], W = shares(a.TW, T);
+  const int group = i / TROWS, li = kvh * groups_of<true>(a, s) + group, ig = i - group * TROWS;
+  const long ub = d.cum[s] + (long)li * un;
+  const int w0 = (int)(((ub + 1) * W - 1) / T), w1 = (int)(((ub + un) * W - 1) / T);
+  const int rows = rows_of(a, s), rg = min(TROWS, rows - group * TROWS), which = s == a.B ? 1 : 0;
+  r.step = tile_slot_rows(rows);
+  r.mid = (long)(w0 + item0<true>(a, s) + li) * r.step + ig;
+  r.nm = w1 - w0 + 1;
+  r.per = rg <= 128 ? 2 : 1;
+  r.hop = rg;
+  r.n = r.nm * r.per;
+  r.ml = a.tml[which];
+  r.o = a.to[which];
+  r.flip = ig & 7;
   return r;
 }
 
@@ -572,21 +661,26 @@ __global__ void __launch_bounds__(128) attn_join_kernel(const JoinArgs j) {
   const AttnArgs& a = j.a;
   __shared__ Deal deal, tdeal;
   asm volatile("griddepcontrol.launch_dependents;" :::);
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  // the deal before the wait for the partials: lens was there before the launches
+  // that write them began
   if (threadIdx.x < 32) make_deal<false>(a, deal);
   else if (threadIdx.x < 64 && (a.own_tiled || a.pre_tiled)) make_deal<true>(a, tdeal);
   __syncthreads();
   const int lane = threadIdx.x & 31;
   const long w = (long)blockIdx.x * 4 + (threadIdx.x >> 5);
-  if (w >= (long)a.B * a.R * a.n_q) return;
+  if (w >= (long)a.B * a.R * a.n_q) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    return;
+  }
   const int row = (int)(w / a.n_q), h = (int)(w - (long)row * a.n_q), kvh = h / a.G, hg = h - kvh * a.G;
   const int b = row / a.R, r = row - b * a.R;
   // the row's own item, then its prefix item
   Source src[2] = {};
   const int io = r * a.G + hg, ip = row * a.G + hg;
-  src[0] = a.own_tiled ? source<true>(a, tdeal, b, kvh, io) : source<false>(a, deal, b, kvh, io);
+  src[0] = a.own_tiled ? tile_source(a, tdeal, b, kvh, io) : stream_source(a, deal, b, kvh, io);
   if (a.shared && __ldcg(a.lens + b) >= 0)
-    src[1] = a.pre_tiled ? source<true>(a, tdeal, a.B, kvh, ip) : source<false>(a, deal, a.B, kvh, ip);
+    src[1] = a.pre_tiled ? tile_source(a, tdeal, a.B, kvh, ip) : stream_source(a, deal, a.B, kvh, ip);
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   // A lane has V neighbouring values.  Partials come in batches of NB whose
   // loads are all in flight at once, the values' not waiting for the maxima's.
   constexpr int V = D / 32, NB = 8;
@@ -665,7 +759,7 @@ struct Plan {
 Plan plan(int n_q, int n_kv, int B, int R, int shared, int type) {
   const long G = n_q / n_kv, rows[2] = {R * G, (long)B * R * G}, many[2] = {(long)B * n_kv, shared ? n_kv : 0};
   Plan p = {};
-  p.slots = kMaxWorkers;
+  p.slots = (long)kMaxWorkers * kMaxWarps;
   for (int x = 0; x < 2; ++x) {
     p.slots += many[x] * ((rows[x] + TR - 1) / TR);
     if (!many[x] || !tiled(rows[x], type)) continue;
@@ -742,8 +836,10 @@ lk_status run_join(const JoinArgs& j, cudaStream_t stream) {
 }
 
 template <int D>
-lk_status run_d(AttnArgs& a, int type, lk_mode mode, const JoinArgs& j, int pdl, cudaStream_t stream) {
+lk_status run_d(JoinArgs& j, int type, lk_mode mode, int pdl, cudaStream_t stream) {
+  AttnArgs& a = j.a;
   lk_status st = LK_OK;
+  a.NW = type == LK_KV_Q8 ? Cfg<LK_KV_Q8, D>::NW : Cfg<LK_KV_F16, D>::NW;
   const int page = 1 << a.page_log2;
   // the launches after the first are dependents of the one before
   if (!a.own_tiled || (a.shared && !a.pre_tiled)) {
@@ -752,6 +848,7 @@ lk_status run_d(AttnArgs& a, int type, lk_mode mode, const JoinArgs& j, int pdl,
          : type == LK_KV_BF16 ? run_type<LK_KV_BF16, D>(a, pdl, stream)
                               : run_type<LK_KV_Q8, D>(a, pdl, stream);
     pdl = 1;
+    a.late = 1;
   }
   if (!st && (a.own_tiled || a.pre_tiled)) {
     const int part = D == 128 ? TUNIT : TUNIT / 2;  // tokens that a warp of the tile kernel fetches
@@ -845,8 +942,8 @@ lk_status lk_attn_shared(const lk_kv_cache* cache, const float* q, int n_q, cons
   j.hl = mode == LK_TWOPASS ? hl : nullptr;
   j.hs = hs;
   const int pdl = cfg_pdl(cfg);
-  return cache->head_dim == 128 ? run_d<128>(a, cache->type, mode, j, pdl, stream)
-                                : run_d<64>(a, cache->type, mode, j, pdl, stream);
+  return cache->head_dim == 128 ? run_d<128>(j, cache->type, mode, pdl, stream)
+                                : run_d<64>(j, cache->type, mode, pdl, stream);
 }
 
 lk_status lk_attn(const lk_kv_cache* cache, const float* q, int n_q, const int32_t* table, int table_w,

@@ -48,15 +48,18 @@ inline lk_status check_rows(const lk_kv_cache* c, const int32_t* table, int tabl
 // kernel's items have up to 8 rows and their keys come in units of 32, the tile
 // kernel's 256 rows and units of 128.  A sequence belongs to one of the two.
 // All units of a kernel's items, in a fixed order, are dealt to its blocks in
-// equal contiguous shares, whatever the lengths are; a block's part of an
-// item (a segment) leaves a partial result (running maximum, sum, weighted
-// values) in the workspace, in slot block + item, which no other segment has;
-// a last launch joins the partials of a row.
+// equal contiguous shares, whatever the lengths are, and a streaming block's
+// share to its warps in the same way; the part of an item that a block (warp)
+// has, a segment, leaves a partial result (running maximum, sum, weighted
+// values) in the workspace, in slot block (warp) + item, which no other segment
+// has; a last launch joins the partials of a row.  A streaming block whose
+// whole share is one item's joins its warps' partials itself.
 constexpr int UNIT = 32;           // keys of a unit, streaming kernel
 constexpr int TR = 8;              // its query rows of an item
 constexpr int TUNIT = 128;         // keys of a unit, tile kernel
 constexpr int TROWS = 256;         // its query rows of an item
-constexpr int kMaxWorkers = 512;   // blocks of the streaming launch, at most
+constexpr int kMaxWorkers = 192;   // blocks of the streaming launch, at most
+constexpr int kMaxWarps = 8;       // and their warps
 constexpr int kTileWorkers = 192;  // blocks of a tile launch, at most
 constexpr int kMaxSeq = LK_MAX_BATCH + 1;
 
@@ -87,7 +90,8 @@ struct AttnArgs {
   float* o;           //   [slot][TR][D] weighted values
   float* tml[2];      // tile partials of the sequences, the prefix: [slot][slot rows][2],
   float* to[2];       //   [slot][slot rows][D], 16-byte pieces permuted in 128 bytes by row & 7
-  int W, TW;          // blocks of the streaming and of the tile launch
+  int W, NW, TW;      // blocks and warps of the streaming launch, blocks of the tile launch
+  int late;           // the tile launch comes after a streaming one of the same call
   unsigned long long wait_ns;
   int* err;
 };
@@ -117,6 +121,10 @@ __device__ __forceinline__ int item0(const AttnArgs& a, int s) {
 // Blocks that have a share: none is empty, so an item's segments are in
 // consecutive blocks.
 __device__ __forceinline__ long shares(int W, long T) { return T < W ? T : W; }
+
+// The streaming kernel deals a block's units on to its warps: blocks as many
+// as leave each warp a unit.
+__device__ __forceinline__ long stream_blocks(int W, int NW, long T) { return min((long)W, (T + NW - 1) / NW); }
 
 // By one whole warp; the caller synchronizes.
 template <bool TILED>

@@ -115,8 +115,11 @@ __global__ void __launch_bounds__(TCfg<D>::THREADS) __maxnreg__(TCfg<D>::LAUNCH)
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == 0) tm_alloc(smem_addr(&tmem_slot), 512);
+  // A launch behind this call's streaming kernel needs nothing of that one's,
+  // and what both need was there when that one let it start: it waits for it
+  // only at its end, for the join's sake.
+  if (!a.late) asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" :::);
-  asm volatile("griddepcontrol.wait;" ::: "memory");
   if (warp == 1) make_deal<true>(a, deal);
   tm_before();
   __syncthreads();
@@ -452,6 +455,7 @@ __global__ void __launch_bounds__(TCfg<D>::THREADS) __maxnreg__(TCfg<D>::LAUNCH)
     }
     if (me == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
   }
+  if (a.late) asm volatile("griddepcontrol.wait;" ::: "memory");
   tm_before();
   __syncthreads();
   tm_after();
