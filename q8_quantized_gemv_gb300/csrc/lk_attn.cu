@@ -95,10 +95,11 @@ struct Cfg {
   static_assert(NW * ST <= 32 && RING + 2048 <= 232448, "shared memory of a block");
 };
 
-// Where a warp is: unit u of item li (of that sequence) of sequence s, whose
-// items have un units and n keys.
+// Where a warp is: unit u of the item of row tile `tile` (of `tiles`) and
+// key/value head kvh of sequence s, whose items have un units and n keys.
 struct Cursor {
-  int s, li, u, un, n;
+  int s, kvh, tile, tiles, u, un, n;
+  __device__ __forceinline__ int item() const { return kvh * tiles + tile; }
 };
 
 // By a whole warp.
@@ -111,8 +112,11 @@ __device__ __forceinline__ Cursor cursor_at(const AttnArgs& a, const Deal& d, lo
   c.un = d.un[c.s];
   c.n = d.n[c.s];
   const long rel = unit - d.cum[c.s];
-  c.li = (int)(rel / c.un);
-  c.u = (int)(rel - (long)c.li * c.un);
+  const int li = (int)(rel / c.un);
+  c.u = (int)(rel - (long)li * c.un);
+  c.tiles = groups_of<false>(a, c.s);
+  c.kvh = li / c.tiles;
+  c.tile = li - c.kvh * c.tiles;
   return c;
 }
 
@@ -120,12 +124,15 @@ __device__ __forceinline__ Cursor cursor_at(const AttnArgs& a, const Deal& d, lo
 __device__ __forceinline__ void advance(const AttnArgs& a, const Deal& d, Cursor& c) {
   if (++c.u < c.un) return;
   c.u = 0;
-  if (++c.li < a.n_kv * groups_of<false>(a, c.s)) return;
-  c.li = 0;
+  if (++c.tile < c.tiles) return;
+  c.tile = 0;
+  if (++c.kvh < a.n_kv) return;
+  c.kvh = 0;
   const int nseq = a.B + a.shared;
   while (++c.s < nseq)
     if ((c.un = d.un[c.s]) > 0) {
       c.n = d.n[c.s];
+      c.tiles = groups_of<false>(a, c.s);
       return;
     }
 }
@@ -187,7 +194,6 @@ __global__ void __launch_bounds__(32 * Cfg<TYPE, D>::NW, 1) attn_kernel(const __
   auto issue = [&](const Cursor& c, const int (&pg)[2], int stage) {
     there = (there & ~(3u << (2 * stage))) | ((pg[0] >= 0 ? 1u : 0u) | (pg[1] >= 0 ? 2u : 0u)) << (2 * stage);
     asked |= 1u << stage;
-    const int kvh = c.li / groups_of<false>(a, c.s);
     if (lane != 0) return;
     const unsigned st = ring + stage * C::STAGE, bar = bar0 + 8 * stage;
     const int n_box = a.box == 32 ? 1 : 2;
@@ -198,7 +204,7 @@ __global__ void __launch_bounds__(32 * Cfg<TYPE, D>::NW, 1) attn_kernel(const __
     for (int hf = 0; hf < n_box; ++hf) {
       if (pg[hf] < 0) continue;
       const int key0 = c.u * UNIT + 16 * hf;
-      const int r0 = ((pg[hf] * a.n_kv + kvh) << a.page_log2) + (key0 & ((1 << a.page_log2) - 1));
+      const int r0 = ((pg[hf] * a.n_kv + c.kvh) << a.page_log2) + (key0 & ((1 << a.page_log2) - 1));
 #pragma unroll
       for (int p = 0; p < C::PARTS; ++p) {
         const unsigned at = st + p * UNIT * C::ROW + 16 * hf * C::ROW;
@@ -238,10 +244,10 @@ __global__ void __launch_bounds__(32 * Cfg<TYPE, D>::NW, 1) attn_kernel(const __
   bool fail = false;
   while (left > 0) {
     // ---- an item
-    const int s = cc.s, n = cc.n, tiles = groups_of<false>(a, s), kvh = cc.li / tiles, tile = cc.li - kvh * tiles;
+    const int s = cc.s, n = cc.n, kvh = cc.kvh, tile = cc.tile;
     const bool pre = s == a.B;
     const int nrows = min(TR, rows_of(a, s) - tile * TR);
-    const long slot = (long)blockIdx.x * C::NW + (one ? 0 : warp) + item0<false>(a, s) + cc.li;
+    const long slot = (long)blockIdx.x * C::NW + (one ? 0 : warp) + item0<false>(a, s) + cc.item();
     // the lane's query row (the last row again where there are fewer)
     const int ri = tile * TR + min(g, nrows - 1);
     const int tok = ri / a.G;  // row of the batch (prefix) or of the sequence
@@ -548,9 +554,8 @@ __global__ void __launch_bounds__(32 * Cfg<TYPE, D>::NW, 1) attn_kernel(const __
 
   // ---- one item: the warps' partials, joined in warp order
   {
-    const int s = cc.s, tiles = groups_of<false>(a, s), tile = cc.li % tiles;
-    const int nrows = min(TR, rows_of(a, s) - tile * TR);
-    const long slot = (long)blockIdx.x * C::NW + item0<false>(a, s) + cc.li;
+    const int s = cc.s, nrows = min(TR, rows_of(a, s) - cc.tile * TR);
+    const long slot = (long)blockIdx.x * C::NW + item0<false>(a, s) + cc.item();
     for (int i = threadIdx.x; i < nrows * D; i += 32 * C::NW) {
       const int r = i / D, d = i - r * D;
       float M = -INFINITY;
