@@ -13,9 +13,8 @@
 // integer levels, exact in f16, the scales applied in f32 to the scores and
 // folded into the weights).  f16 operands are shifted by powers of two so
 // that the low terms stay normal: queries to a row maximum of 2^10, weights by
-// 2^14 (Q8: after dividing out the unit's largest scale's power of two).  A
-// bf16 query has three terms: with two, scores of a few hundred would lose
-// the weights' fifth digit.  Each unit's weighted values are summed in a fresh
+// 2^14 (Q8: by 2^10, their scales by what brings the largest to 8 .. 16, and the
+// product of the two again as two terms).  Each unit's weighted values are summed in a fresh
 // accumulator and added in f32, so the MMA's own accumulation never runs over
 // more than 32 keys.
 //
@@ -88,11 +87,11 @@ struct Cfg {
   static constexpr int STAGE = (2 * (KV + SC) + 1023) / 1024 * 1024;
   static constexpr int ROW = EB * D < 128 ? EB * D : 128;          // bytes of a box row
   static constexpr int PARTS = EB * D / ROW;                       // boxes of a token's row
-  static constexpr int NW = TYPE != LK_KV_Q8 && D == 128 ? 7 : 8;  // warps
-  static constexpr int ST = TYPE != LK_KV_Q8 && D == 128 ? 2 : 3;  // stages a warp
+  static constexpr int NW = TYPE != LK_KV_Q8 && D == 128 ? 7 : 12;  // warps
+  static constexpr int ST = TYPE == LK_KV_Q8 && D == 64 ? 3 : 2;     // stages a warp
   static constexpr int RING = NW * ST * STAGE + 1024;  // and the base's alignment
   static_assert(STAGE * ST >= TR * (D + 4) * 4 && NW <= kMaxWarps, "a warp's partial fits in its stages");
-  static_assert(NW * ST <= 32 && RING + 2048 <= 232448, "shared memory of a block");
+  static_assert(RING + 2048 <= 232448, "shared memory of a block");
 };
 
 // Where a warp is: unit u of the item of row tile `tile` (of `tiles`) and
@@ -371,7 +370,7 @@ __global__ void __launch_bounds__(32 * Cfg<TYPE, D>::NW, 1) attn_kernel(const __
       const float ref = mn == -INFINITY ? 0.0f : mn;
       float al = ex2(m - ref);  // 0 from an empty start
       m = mn;
-      constexpr float UP = TYPE == LK_KV_BF16 ? 0.0f : Q8 ? 13.0f : 14.0f;
+      constexpr float UP = TYPE == LK_KV_BF16 ? 0.0f : Q8 ? 10.0f : 14.0f;
       float p[4][2];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -395,7 +394,9 @@ __global__ void __launch_bounds__(32 * Cfg<TYPE, D>::NW, 1) attn_kernel(const __
         const float dm = __half2float(__ushort_as_half((unsigned short)mx));
         if (dm > dvm) {  // warp-uniform
           dvm = dm;
-          const float ns = __uint_as_float((254u - (__float_as_uint(dm) >> 23)) << 23);
+          // as an f16 factor that brings the largest scale to 8 .. 16 (2^14 at
+          // most): smaller ones stay normal down to 2^-18 of it
+          const float ns = fminf(__uint_as_float((257u - (__float_as_uint(dm) >> 23)) << 23), 16384.0f);
           al *= ns / dsc;  // powers of two; O is 0 before the first
           dsc = ns;
         }
@@ -437,9 +438,18 @@ __global__ void __launch_bounds__(32 * Cfg<TYPE, D>::NW, 1) attn_kernel(const __
           }
         }
       } else {
-        // value scales of keys 8 i + 2 t, + 1, times dsc; 0 for absent tokens
-        // (their scales may be anything)
+        // weights as two f16 terms, keys 8 i + 2 t, + 1 in a pair
+        __half2 p_hi[4], p_lo[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const unsigned h = split2<false>(p[i][0], p[i][1]), r = split2<false>(p[i][0], p[i][1]);
+          p_hi[i] = *(const __half2*)&h;
+          p_lo[i] = *(const __half2*)&r;
+        }
+        // value scales of those keys times dsc (exact above 2^-24); 0 for absent
+        // tokens, whose scales may be anything
         __half2 d0[4][D / 64], d1[4][D / 64];
+        const __half2 ds2 = __float2half2_rn(dsc);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           if constexpr (D == 128) {
@@ -451,31 +461,28 @@ __global__ void __launch_bounds__(32 * Cfg<TYPE, D>::NW, 1) attn_kernel(const __
             d0[i][0] = *(const __half2*)&w.x, d1[i][0] = *(const __half2*)&w.y;
           }
           const int key = u * UNIT + 8 * i + 2 * t;
-          if (!whole) {
 #pragma unroll
-            for (int x = 0; x < D / 64; ++x) {
+          for (int x = 0; x < D / 64; ++x) {
+            if (!whole) {
               if (key >= n || !(i < 2 ? in0 : in1)) d0[i][x] = __half2half2(__ushort_as_half(0));
               if (key + 1 >= n || !(i < 2 ? in0 : in1)) d1[i][x] = __half2half2(__ushort_as_half(0));
             }
+            d0[i][x] = __hmul2(d0[i][x], ds2);
+            d1[i][x] = __hmul2(d1[i][x], ds2);
           }
         }
 #pragma unroll
         for (int b = 0; b < D / 32; ++b) {
+          // weight times scale, again as two terms: the high one rounded, the
+          // low one what that left (exact) and the weight's low term
           unsigned ph[2][4];
 #pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            float y[4];
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              const float e0 = b & 1 ? __high2float(d0[2 * k + i][b >> 1]) : __low2float(d0[2 * k + i][b >> 1]);
-              const float e1 = b & 1 ? __high2float(d1[2 * k + i][b >> 1]) : __low2float(d1[2 * k + i][b >> 1]);
-              y[2 * i] = p[2 * k + i][0] * (e0 * dsc);
-              y[2 * i + 1] = p[2 * k + i][1] * (e1 * dsc);
-            }
-            ph[k][0] = split2<TYPE == LK_KV_BF16>(y[0], y[1]);
-            ph[k][2] = split2<TYPE == LK_KV_BF16>(y[2], y[3]);
-            ph[k][1] = split2<TYPE == LK_KV_BF16>(y[0], y[1]);
-            ph[k][3] = split2<TYPE == LK_KV_BF16>(y[2], y[3]);
+          for (int i = 0; i < 4; ++i) {
+            const __half2 e = b & 1 ? __highs2half2(d0[i][b >> 1], d1[i][b >> 1]) : __lows2half2(d0[i][b >> 1], d1[i][b >> 1]);
+            const __half2 hi = __hmul2(p_hi[i], e);
+            const __half2 lo = __hfma2(p_lo[i], e, __hfma2(p_hi[i], e, __hneg2(hi)));
+            ph[i >> 1][2 * (i & 1)] = *(const unsigned*)&hi;
+            ph[i >> 1][2 * (i & 1) + 1] = *(const unsigned*)&lo;
           }
           unsigned w[8];
 #pragma unroll

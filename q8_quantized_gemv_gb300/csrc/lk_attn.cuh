@@ -59,7 +59,7 @@ constexpr int TR = 8;              // its query rows of an item
 constexpr int TUNIT = 128;         // keys of a unit, tile kernel
 constexpr int TROWS = 256;         // its query rows of an item
 constexpr int kMaxWorkers = 192;   // blocks of the streaming launch, at most
-constexpr int kMaxWarps = 8;       // and their warps
+constexpr int kMaxWarps = 12;      // and their warps
 constexpr int kTileWorkers = 192;  // blocks of a tile launch, at most
 constexpr int kMaxSeq = LK_MAX_BATCH + 1;
 

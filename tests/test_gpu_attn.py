@@ -4,9 +4,7 @@ the formula in 64 bits.
 
 Tolerance of the attention (derived, not fitted).  An f32 operand enters the
 MMAs as 16-bit terms: the rest after two bf16 terms is at most 2^-8 * 2^-8 =
-2^-16 of it (half a step each), after two f16 terms 2^-22, after three bf16
-terms 2^-24.  Queries against bf16 keys have three terms in the streaming
-kernel and two in the tile kernel (many rows on the same keys).  A score is a sum of D <= 128 products in 8 chained MMA steps (each
+2^-16 of it (half a step each), after two f16 terms 2^-22.  A score is a sum of D <= 128 products in 8 chained MMA steps (each
 at worst truncating at 2^-22 of the absolute sum) and a few f32 operations:
 off by at most 2^-18 * A with A = scale * sum_i |q_i k_i|, in natural units, and
 a weight by that relative to itself.  Weights enter numerator and denominator
@@ -14,7 +12,16 @@ a weight by that relative to itself.  Weights enter numerator and denominator
 accumulator, then f32 additions in a tree or over at most a few hundred units)
 stay below 2^-16.  So |out - exact| <= (2^-15 + c * A) * W, W = sum p |v| / sum p,
 with the row's largest A and c = 2 * 2^-18 (f16, Q8: at most 2^-22 from the
-queries' terms) or, against bf16 keys, 2 * (2^-18 + 2^-16) <= 2^-14."""
+queries' terms) or, against bf16 keys, 2 * (2^-18 + 2^-16) <= 2^-14.
+
+f16 terms also end at 2^-24, which counts where W is far below the largest
+value (a winner whose own value is 0): weights are shifted to at least 2^10 at
+the row's largest, so a weight's low term is off by at most 2^-25 / 2^10 of it;
+Q8 multiplies that by a scale of at most 16, brought to 8 .. 16 at the largest,
+and rounds the product's low term once more: (16 + 1) 2^-25 / (2^10 * 8) < 2^-33
+of 127 times the largest scale, which is below 2 max|v|: 2^-32 max|v| a key.  A
+scale below 2^-18 of the largest is off by 2^-25 / 8 of that: 2^-28 * 127 scales, below
+2^-27 max|v| over all weights.  Together (2^-27 + N 2^-32) max|v| for N keys."""
 import numpy as np
 import pytest
 
@@ -91,6 +98,7 @@ def reference(kd, vd, q, table, lens, R, scale, prefix=None, bf16=True):
     q = q.double().view(M, n_kv, G, D)
     out = torch.zeros((M, n_kv, G, D), dtype=torch.float64, device=DEV)
     A, W = torch.zeros((M, n_kv, G, 1), dtype=torch.float64, device=DEV), torch.zeros_like(out)
+    F = torch.zeros((M, n_kv, 1, 1), dtype=torch.float64, device=DEV)
 
     def tokens(pages, n):
         t = pages.long()
@@ -113,9 +121,10 @@ def reference(kd, vd, q, table, lens, R, scale, prefix=None, bf16=True):
         p = torch.softmax(s, -1)
         out[m] = torch.einsum("hgn,nhd->hgd", p, v)
         W[m] = torch.einsum("hgn,nhd->hgd", p, v.abs())
+        F[m] = (2.0 ** -27 + k.shape[0] * 2.0 ** -32) * v.abs().amax((0, 2))[:, None, None]
         A[m] = (torch.einsum("hgd,nhd->hgn", q[m].abs(), k.abs()) * abs(scale)).amax(-1, keepdim=True)
     c = 2.0 ** -14 if bf16 else 2.0 ** -17
-    return out.view(M, -1), (2.0 ** -15 + c * A).expand_as(W).reshape(M, -1) * W.reshape(M, -1)
+    return out.view(M, -1), ((2.0 ** -15 + c * A) * W + F).reshape(M, -1)
 
 
 def workspace(cache, n_q, B, R, shared=False):
