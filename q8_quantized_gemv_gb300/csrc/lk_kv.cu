@@ -57,6 +57,87 @@ __device__ __forceinline__ void store_head(void* base, __half* scales, long row,
   }
 }
 
+// ---- the per-head norm ----------------------------------------------------------------
+// x[i] = RN32(x[i] g[i] / sqrt(mean(x^2) + eps)) with everything inside in f64.
+template <int C>
+__device__ __forceinline__ void norm_f64(float (&x)[C], const float (&g)[C], float eps) {
+  double ss = 0.0;
+#pragma unroll
+  for (int c = 0; c < C; ++c) ss = __fma_rn((double)x[c], (double)x[c], ss);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(FULL, ss, o);
+  const double den = __dsqrt_rn(ss / (32 * C) + (double)eps);
+#pragma unroll
+  for (int c = 0; c < C; ++c) x[c] = __double2float_rn(__ddiv_rn((double)x[c] * (double)g[c], den));
+}
+
+// The same values from pairs of f32 (unevaluated sums hi + lo, T. J. Dekker,
+// Numer. Math. 18, 1971), about 2^-44 accurate: the f64 pipe issues a warp's
+// instruction in 16 cycles and the 45 of a head took 14 of the 17 us of 64
+// rows.  Returns whether the lane's results are certainly the f64 form's: no
+// value within 2^-40 of a rounding boundary, and magnitudes far from the
+// ends of the range, where the pairs' low parts would vanish.
+__device__ __forceinline__ void two_sum(float a, float b, float& s, float& e) {
+  s = __fadd_rn(a, b);
+  const float t = __fsub_rn(s, a);
+  e = __fadd_rn(__fsub_rn(a, __fsub_rn(s, t)), __fsub_rn(b, t));
+}
+__device__ __forceinline__ void two_prod(float a, float b, float& p, float& e) {
+  p = __fmul_rn(a, b);
+  e = __fmaf_rn(a, b, -p);
+}
+template <int C>
+__device__ __forceinline__ bool norm_pairs(const float (&x)[C], const float (&g)[C], float eps, float (&out)[C]) {
+  float h = 0.0f, l = 0.0f;
+#pragma unroll
+  for (int c = 0; c < C; ++c) {
+    float p, e, s, f;
+    two_prod(x[c], x[c], p, e);
+    two_sum(h, p, s, f);
+    l = __fadd_rn(l, __fadd_rn(e, f));
+    h = s;
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    const float ho = __shfl_xor_sync(FULL, h, o), lo = __shfl_xor_sync(FULL, l, o);
+    float s, f;
+    two_sum(h, ho, s, f);
+    l = __fadd_rn(__fadd_rn(l, lo), f);
+    h = s;
+  }
+  // mean (a power of two) plus eps, brought to hi + lo with |lo| <= ulp(hi) / 2
+  float m, f, r;
+  two_sum(h * (1.0f / (32 * C)), eps, m, f);
+  f = __fadd_rn(f, l * (1.0f / (32 * C)));
+  two_sum(m, f, h, l);
+  // 1 / sqrt(h + l) = y + z: one Newton step from y, its residual 1 - (h + l) y^2 in pairs
+  const float y = rsqrtf(h);
+  float a, b, c0, d;
+  two_prod(y, y, a, b);
+  two_prod(h, a, c0, d);
+  d = __fadd_rn(d, __fmaf_rn(h, b, __fmul_rn(l, a)));
+  r = __fsub_rn(__fsub_rn(1.0f, c0), d);
+  const float z = __fmul_rn(y, __fmaf_rn(__fmul_rn(0.375f, r), r, __fmul_rn(0.5f, r)));
+  bool sure = h > 0x1p-60f && h < 0x1p60f;
+#pragma unroll
+  for (int c = 0; c < C; ++c) {
+    float p, e, q, w, t, u;
+    two_prod(x[c], g[c], p, e);
+    two_prod(p, y, q, w);
+    w = __fadd_rn(w, __fmaf_rn(p, z, __fmul_rn(e, y)));
+    two_sum(q, w, t, u);  // t = RN(q + w), u what that left
+    // half the distance to t's neighbour below and above (they differ at a power of two)
+    const float at = fabsf(t), up = __fmul_rn(0.5f, __fsub_rn(__uint_as_float(__float_as_uint(at) + 1), at)),
+                dn = __fmul_rn(0.5f, __fsub_rn(at, __uint_as_float(__float_as_uint(at) - 1)));
+    const float au = fabsf(u), near = __fmul_rn(at, 0x1p-40f);
+    const bool fine = at > 0x1p-60f && at < 0x1p60f && fabsf(p) > 0x1p-60f && fabsf(__fsub_rn(au, up)) > near &&
+                      fabsf(__fsub_rn(au, dn)) > near;
+    sure = sure && (fine || x[c] == 0.0f);
+    out[c] = x[c] == 0.0f ? p : t;  // a zero keeps its sign
+  }
+  return sure;
+}
+
 template <int TYPE, int D>
 __global__ void __launch_bounds__(256) kv_append_kernel(const AppendArgs a) {
   constexpr int C = D / 32;
@@ -84,15 +165,16 @@ __global__ void __launch_bounds__(256) kv_append_kernel(const AppendArgs a) {
   if (!is_v) {
     const float* gain = is_q ? a.q_gain : a.k_gain;
     if (gain) {
-      double ss = 0.0;
+      float gv[C];
 #pragma unroll
-      for (int c = 0; c < C; ++c) ss = __fma_rn((double)x[c], (double)x[c], ss);
+      for (int c = 0; c < C; ++c) gv[c] = __ldg(gain + 32 * c + lane);
+      float y[C];
+      if (__all_sync(FULL, norm_pairs<C>(x, gv, a.eps, y))) {
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(FULL, ss, o);
-      const double den = __dsqrt_rn(ss / D + (double)a.eps);
-#pragma unroll
-      for (int c = 0; c < C; ++c)
-        x[c] = __double2float_rn(__ddiv_rn((double)x[c] * (double)__ldg(gain + 32 * c + lane), den));
+        for (int c = 0; c < C; ++c) x[c] = y[c];
+      } else {
+        norm_f64<C>(x, gv, a.eps);
+      }
     }
     if (a.rot) {
       const long at = (long)(a.p0 + p) * (a.rot >> 1);

@@ -492,7 +492,7 @@ class KvCache:
             raise ValueError("v must have the shape and device of k")
         if (k.dtype == torch.int8) != (ks is not None) or (ks is None) != (vs is None):
             raise ValueError("ks and vs go with int8 levels")
-        self.device, self.n_kv, self.head_dim = k.device, k.shape[1], k.shape[3]
+        self.device, self.dev, self.n_kv, self.head_dim = k.device, k.get_device(), k.shape[1], k.shape[3]
         if ks is not None:
             for name, t in (("ks", ks), ("vs", vs)):
                 if tuple(t.shape) != (*k.shape[:3], k.shape[3] // 32) or t.device != k.device:
@@ -503,13 +503,14 @@ class KvCache:
 
 
 def _on(dev, t, dtype, name, shape=None):
-    """Pointer of a contiguous tensor of that dtype (and shape) on the cache's device."""
+    """Pointer of a contiguous tensor of that dtype (and shape) on device
+    number dev."""
     if t is None:
         return None
     if not isinstance(t, torch.Tensor) or t.dtype is not dtype:
         raise TypeError(f"{name} must be a {dtype} tensor")
-    if t.device != dev:
-        raise ValueError(f"{name} must be on {dev}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be on cuda:{dev}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     if shape is not None and t.shape != shape:
@@ -518,17 +519,22 @@ def _on(dev, t, dtype, name, shape=None):
 
 
 def _kv_rows(cache, table, lens, R):
-    """Checks of the arguments every call on a cache takes: (table pointer,
-    table width, lens pointer, B)."""
-    dev = cache.device
-    if torch.cuda.current_device() != dev.index:
-        raise ValueError(f"the cache is on {dev}, which is not the current device")
+    """Checks of the arguments every call on a cache takes: (device number,
+    table pointer, table width, lens pointer, B)."""
+    dev = cache.dev
+    if torch.cuda.current_device() != dev:
+        raise ValueError(f"the cache is on cuda:{dev}, which is not the current device")
     if table.dim() != 2:
         raise ValueError("table must be [B, pages]")
     B, w = table.shape
     if R < 0:
         raise ValueError("R must not be negative")
-    return _on(dev, table, _I32, "table") if w else None, w, _on(dev, lens, _I32, "lens", (B,)), B
+    return dev, _on(dev, table, _I32, "table") if w else None, w, _on(dev, lens, _I32, "lens", (B,)), B
+
+
+def _on_stream(stream, dev):
+    """The raw stream: the device's current one without the object around it."""
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
 
 
 def lk_kv_append(cache: KvCache, q, k, v, table, lens, cosines, sines, qr, R=1, p0=0, paired=False, q_gain=None,
@@ -539,23 +545,18 @@ def lk_kv_append(cache: KvCache, q, k, v, table, lens, cosines, sines, qr, R=1, 
     table int32 [B, pages], lens int32 [B] with the R new tokens of each
     sequence counted; cosines, sines f32 [positions, rot / 2] or None (no
     rotation)."""
-    tp, tw, lp, B = _kv_rows(cache, table, lens, R)
-    dev, D, M = cache.device, cache.head_dim, B * R
-    ptrs, ld = [], None
-    for name, t in (("q", q), ("k", k), ("v", v)):
+    dev, tp, tw, lp, B = _kv_rows(cache, table, lens, R)
+    D, M, N = cache.head_dim, B * R, q.shape[-1]
+    ld = q.stride(0) if M > 1 else N
+    for name, t, n in (("q", q, N), ("k", k, cache.n_kv * D), ("v", v, cache.n_kv * D)):
         if not isinstance(t, torch.Tensor) or t.dtype is not _F32 or t.dim() != 2:
             raise TypeError(f"{name} must be a 2-D float32 tensor")
-        if t.device != dev or t.shape[0] != M or (t.shape[1] > 1 and t.stride(1) != 1):
-            raise ValueError(f"{name} must be {M} rows of contiguous values on {dev}")
-        if M > 1:
-            if ld is not None and t.stride(0) != ld:
-                raise ValueError("q, k and v must have the same row pitch")
-            ld = t.stride(0)
-        ptrs.append(t.data_ptr())
-    if k.shape[1] != cache.n_kv * D or v.shape[1] != cache.n_kv * D or q.shape[1] % D:
-        raise ValueError("q, k and v rows must be heads of head_dim values, k and v n_kv of them")
-    if M <= 1:
-        ld = q.shape[1]
+        if t.get_device() != dev or t.shape != (M, n) or t.stride(1) != 1:
+            raise ValueError(f"{name} must be [{M}, {n}] with contiguous rows on cuda:{dev}")
+        if M > 1 and t.stride(0) != ld:
+            raise ValueError("q, k and v must have the same row pitch")
+    if N % D:
+        raise ValueError("q rows must be heads of head_dim values")
     rot = n_pos = 0
     if cosines is not None:
         if cosines.dim() != 2:
@@ -566,12 +567,12 @@ def lk_kv_append(cache: KvCache, q, k, v, table, lens, cosines, sines, qr, R=1, 
     for name, t in (("q_gain", q_gain), ("k_gain", k_gain)):
         if t is not None and t.shape != (D,):
             raise ValueError(f"{name} must be [head_dim]")
-    _ok(_load().lk_kv_append(cache.ref, *ptrs, ld, q.shape[1] // D, tp, tw, lp, B, R, p0,
+    _ok(_load().lk_kv_append(cache.ref, q.data_ptr(), k.data_ptr(), v.data_ptr(), ld, N // D, tp, tw, lp, B, R, p0,
                              _on(dev, cosines, _F32, "cosines"),
                              _on(dev, sines, _F32, "sines", cosines.shape) if cosines is not None else None, n_pos,
                              rot, 1 if paired else 0, _on(dev, q_gain, _F32, "q_gain"),
-                             _on(dev, k_gain, _F32, "k_gain"), eps, _on(dev, qr, _F32, "qr", q.shape), _cfg(cfg),
-                             _stream(stream)), "lk_kv_append")
+                             _on(dev, k_gain, _F32, "k_gain"), eps, _on(dev, qr, _F32, "qr", (M, N)), _cfg(cfg),
+                             _on_stream(stream, dev)), "lk_kv_append")
 
 
 def lk_attn_workspace_bytes(n_q, n_kv, head_dim, B, R=1, shared=False) -> int:
@@ -579,10 +580,10 @@ def lk_attn_workspace_bytes(n_q, n_kv, head_dim, B, R=1, shared=False) -> int:
 
 
 def _attn_tail(cache, q, M, scale, mode, out, hq, hl, hs, ws):
-    dev, N = cache.device, q.shape[1]
-    qp = _on(dev, q, _F32, "q")
-    if q.shape[0] != M or N % cache.head_dim:
-        raise ValueError(f"q must be {M} rows of heads of head_dim values")
+    dev, N = cache.dev, q.shape[-1]
+    qp = _on(dev, q, _F32, "q", (M, N))
+    if N % cache.head_dim:
+        raise ValueError("q rows must be heads of head_dim values")
     if scale is None:
         scale = cache.head_dim ** -0.5
     return qp, N // cache.head_dim, (
@@ -597,17 +598,18 @@ def lk_attn(cache: KvCache, q, table, lens, ws, R=1, scale=None, mode=LK_DEQUANT
     cached tokens (see include/lk_attn.h): f32 rows in out and / or, by mode, the
     next projection's words hq, hl and scales hs.  ws: uint8 workspace of
     lk_attn_workspace_bytes.  scale None: 1 / sqrt(head_dim)."""
-    tp, tw, lp, B = _kv_rows(cache, table, lens, R)
+    dev, tp, tw, lp, B = _kv_rows(cache, table, lens, R)
     qp, n_q, tail = _attn_tail(cache, q, B * R, scale, mode, out, hq, hl, hs, ws)
-    _ok(_load().lk_attn(cache.ref, qp, n_q, tp, tw, lp, B, R, *tail, _cfg(cfg), _stream(stream)), "lk_attn")
+    _ok(_load().lk_attn(cache.ref, qp, n_q, tp, tw, lp, B, R, *tail, _cfg(cfg),
+                        _on_stream(stream, dev)), "lk_attn")
 
 
 def lk_attn_shared(cache: KvCache, q, prefix_table, prefix_len, table, lens, ws, R=1, scale=None, mode=LK_DEQUANT,
                    out=None, hq=None, hl=None, hs=None, stream=None, cfg=None):
     """lk_attn for sequences that continue one prefix of prefix_len tokens in
     the pages prefix_table (int32); table and lens are the sequences' own."""
-    tp, tw, lp, B = _kv_rows(cache, table, lens, R)
+    dev, tp, tw, lp, B = _kv_rows(cache, table, lens, R)
     qp, n_q, tail = _attn_tail(cache, q, B * R, scale, mode, out, hq, hl, hs, ws)
-    _ok(_load().lk_attn_shared(cache.ref, qp, n_q, _on(cache.device, prefix_table, _I32, "prefix_table"),
+    _ok(_load().lk_attn_shared(cache.ref, qp, n_q, _on(dev, prefix_table, _I32, "prefix_table"),
                                0 if prefix_table is None else prefix_table.numel(), prefix_len, tp, tw, lp, B, R,
-                               *tail, _cfg(cfg), _stream(stream)), "lk_attn_shared")
+                               *tail, _cfg(cfg), _on_stream(stream, dev)), "lk_attn_shared")

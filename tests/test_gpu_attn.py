@@ -239,6 +239,24 @@ def test_append_bits(case):
             assert np.array_equal(host(t_.float()), w)
 
 
+def test_append_norm_bits():
+    """The norm's quick form against its definition in 64 bits, over wide
+    magnitudes (where it hands over to the f64 form) and signed zeros."""
+    g = gen(6)
+    cache, _, _ = make_cache("f16", 70, 1, 16, 128, g)
+    table = torch.arange(64, dtype=torch.int32, device=DEV).view(64, 1)
+    lens = torch.ones((64,), dtype=torch.int32, device=DEV)
+    for spread, gain in ((1.0, 1.0), (1e-3, 1.0), (300.0, 1e-4), (1e-25, 1.0), (1e25, 1.0), (1e-6, 1e9)):
+        x = torch.randn((64, 34 * 128), generator=g, device=DEV) * spread
+        x[:, ::7] = 0.0
+        x[:, 3::11] = -0.0
+        qg = torch.randn((128,), generator=g, device=DEV) * gain
+        qr = torch.empty((64, 32 * 128), device=DEV)
+        lk.lk_kv_append(cache, *x.split((4096, 128, 128), 1), table, lens, None, None, qr, q_gain=qg, k_gain=qg)
+        want = np.stack([host_append(r.reshape(32, 128), None, None, 0, False, host(qg)).ravel() for r in host(x[:, :4096])])
+        assert np.array_equal(bits(host(qr)), bits(want)), (spread, gain)
+
+
 def test_append_leaves_out_what_has_no_place():
     """Tokens past the table, in pages outside the cache or past the rotation
     table change nothing."""
