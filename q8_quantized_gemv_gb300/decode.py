@@ -14,10 +14,14 @@ glu=False (the default: the projections alone):
     output the next layer's norm, with no residual add.
 Then RMSNorm -> quantize -> lm-head with the argmax epilogue -> argmax.
 
-Attention is not part of the projection path, so the input it would produce
-for the o projection is a fixed seeded vector (N(0,1) with 1% x20 outliers,
-one per layer) quantized every token; with glu=False the down projection's
-input is such a vector too.
+By default attention is not part of the projection path, so the input it would
+produce for the o projection is a fixed seeded vector (N(0,1) with 1% x20
+outliers, one per layer) quantized every token; with glu=False the down
+projection's input is such a vector too.  attn=Attention(...) (with glu=True)
+puts the attention step there instead: the new token's key and value are
+appended to the layer's paged cache with the per-head norms and the rotation
+(lk_kv_append), the attention over the cache (lk_attn, or lk_attn_shared for
+a batch on one prefix) writes the o projection's quantized activation.
 
 Weights live on the device for the life of the object (about 8 GB for the
 36-layer, hidden-4096 configuration); every buffer is allocated once here and
@@ -30,11 +34,101 @@ import torch
 from . import lk, synth
 
 
+class Attention:
+    """The attention step of a DecodeStack: what its caches are, and after the
+    stack is built their state.
+
+    kv       "f16", "bf16" or "q8": the cache's type
+    page     tokens of a page;  capacity  tokens a sequence has room for
+    tokens   tokens already in each sequence's cache (one number, or one per
+             sequence), seeded synthetic keys and values; -1: no sequence there
+    prefix   tokens of a prefix that all sequences continue, held once
+    qk_norm  per-head RMSNorm of q and k;  rope_base  of the rotation's angles
+
+    State: lens (int32 [batch], the sequences' own tokens, advanced by one at
+    the start of every token where a sequence is), table int32 [batch, pages],
+    prefix_table, caches (one lk.KvCache per layer)."""
+
+    def __init__(self, kv="f16", head_dim=128, page=64, capacity=4096, tokens=0, prefix=0, qk_norm=True,
+                 rope_base=1e6):
+        if kv not in ("f16", "bf16", "q8"):
+            raise ValueError("kv must be f16, bf16 or q8")
+        self.kv, self.D, self.page, self.capacity = kv, head_dim, page, capacity
+        self.tokens, self.prefix, self.qk_norm, self.rope_base = tokens, prefix, qk_norm, rope_base
+
+    def build(self, layers, q_dim, kv_dim, batch, seed, dev):
+        D, page, B = self.D, self.page, batch
+        if q_dim % D or kv_dim % D or (q_dim // D) % (kv_dim // D):
+            raise ValueError("q_dim and kv_dim must be heads of head_dim, the query heads a multiple of the others")
+        self.n_q, self.n_kv = q_dim // D, kv_dim // D
+        tokens = [self.tokens] * B if isinstance(self.tokens, int) else list(self.tokens)
+        if len(tokens) != B or max(tokens) >= self.capacity:
+            raise ValueError("tokens: one number per sequence, below capacity")
+        width, p_pages = -(-self.capacity // page), -(-self.prefix // page)
+        n_pages = p_pages + B * width
+        g = torch.Generator(device=dev)
+        g.manual_seed(seed)
+        order = torch.randperm(n_pages, generator=g, device=dev).to(torch.int32)
+        self.prefix_table = order[:p_pages].contiguous()
+        self.table = order[p_pages:].view(B, width).contiguous()
+        self.live = torch.tensor([1 if t >= 0 else 0 for t in tokens], dtype=torch.int32, device=dev)
+        self.lens = torch.tensor(tokens, dtype=torch.int32, device=dev)
+        self.lens0 = self.lens.clone()
+        n_pos = self.prefix + self.capacity
+        ang = torch.arange(n_pos, dtype=torch.float64, device=dev)[:, None] * torch.pow(
+            torch.tensor(float(self.rope_base), dtype=torch.float64, device=dev),
+            -torch.arange(0, D, 2, dtype=torch.float64, device=dev) / D)
+        self.cos, self.sin = ang.cos().float(), ang.sin().float()
+        self.caches, self.gains = [], []
+        shape = (n_pages, self.n_kv, page, D)
+        for l in range(layers):
+            parts = []
+            for _ in range(2):
+                if self.kv == "q8":
+                    parts.append((torch.randint(-127, 128, shape, generator=g, device=dev, dtype=torch.int16).to(torch.int8),
+                                  torch.rand((*shape[:3], D // 32), generator=g, device=dev).mul_(0.02).half()))
+                else:
+                    x = torch.randn(shape, generator=g, device=dev)
+                    parts.append((x.to(torch.float16 if self.kv == "f16" else torch.bfloat16), None))
+            (k, ks), (v, vs) = parts
+            self.caches.append(lk.KvCache(k, v, ks, vs))
+            self.gains.append(tuple(synth.norm_gain_torch(D, seed + 1 + 2 * l + i, dev) for i in range(2))
+                              if self.qk_norm else (None, None))
+        self.qr = torch.zeros((B, q_dim), dtype=torch.float32, device=dev)
+        self.out = torch.zeros((B, q_dim), dtype=torch.float32, device=dev)
+        self.ws = torch.empty((lk.lk_attn_workspace_bytes(self.n_q, self.n_kv, D, B, 1, self.prefix > 0),),
+                              dtype=torch.uint8, device=dev)
+
+    def restart(self):
+        """Back to the tokens the caches began with."""
+        self.lens.copy_(self.lens0)
+
+    def step(self, l, q, k, v, mode, act, eps, cfg):
+        """Layer l's append and attention; returns the o projection's
+        activation arguments."""
+        qg, kg = self.gains[l]
+        lk.lk_kv_append(self.caches[l], q, k, v, self.table, self.lens, self.cos, self.sin, self.qr, p0=self.prefix,
+                        q_gain=qg, k_gain=kg, eps=eps, cfg=cfg)
+        to = dict(out=self.out) if mode == lk.LK_DEQUANT else dict(hq=act["xq"], hl=act.get("xl"), hs=act["xs"])
+        if self.prefix:
+            lk.lk_attn_shared(self.caches[l], self.qr, self.prefix_table, self.prefix, self.table, self.lens, self.ws,
+                              mode=mode, cfg=cfg, **to)
+        else:
+            lk.lk_attn(self.caches[l], self.qr, self.table, self.lens, self.ws, mode=mode, cfg=cfg, **to)
+        return {"x": self.out} if mode == lk.LK_DEQUANT else act
+
+    def launches(self):
+        """Of one layer: append, attention (two kernels where a prefix's many
+        rows go to the tile kernel), join."""
+        tiled = self.prefix and self.kv != "q8" and self.lens.numel() * self.n_q // self.n_kv > 16
+        return 4 if tiled else 3
+
+
 class DecodeStack:
     def __init__(self, layers=36, hidden=4096, q_dim=4096, kv_dim=1024, ffn=12288, vocab=151936,
                  batch=1, mode=lk.LK_INT8ACT, seed=synth.SEED_BASE + 4, device="cuda", eps=1e-6,
                  fused=False, chain=False, group_qkv=True, prefill=None, glu=False, fused_qkv=True, pdl=False,
-                 path=0, tune=None, splitk=True):
+                 path=0, tune=None, splitk=True, attn=None):
         self.L, self.H, self.Q, self.KV, self.F, self.V = layers, hidden, q_dim, kv_dim, ffn, vocab
         self.B, self.mode, self.eps, self.dev = batch, lk._mode(mode), eps, torch.device(device)
         # per projection (qkv, o, gu, down, lm): warps of a GEMV block that
@@ -51,6 +145,11 @@ class DecodeStack:
         # the gated pair runs as one fused launch; the chain and fused-prologue
         # forms keep the projections-alone dataflow
         self.glu = bool(glu) and not chain and not fused
+        self.attn = attn
+        if attn is not None:
+            if not self.glu or not fused_qkv:
+                raise ValueError("attn needs the decoder dataflow (glu=True) and the fused q|k|v matrix")
+            attn.build(layers, q_dim, kv_dim, batch, s + 777_000, dev)
         self.shapes = {"q": (q_dim, hidden), "k": (kv_dim, hidden), "v": (kv_dim, hidden),
                        "o": (hidden, q_dim), "gu": (2 * ffn, hidden), "down": (hidden, ffn)}
         # fused_qkv: q, k and v are row ranges of one [q + 2 kv, hidden]
@@ -244,11 +343,17 @@ class DecodeStack:
             return fn() if hook is None else hook(name, fn)
 
         m, B, L = self.mode, self.B, self.L
+        if self.attn is not None:
+            self.attn.lens.add_(self.attn.live)
         a_h = self._norm(self.x_buf, self.layers[0]["g_attn"])
         h_cur = self.x_buf
         for l, w in enumerate(self.layers):
             launch("qkv", self._qkv_launch(w, a_h))
-            a_o = self._quant(w["o_in"])
+            if self.attn is None:
+                a_o = self._quant(w["o_in"])
+            else:
+                a_o = launch("attn", lambda l=l: self.attn.step(
+                    l, *(self.qkv_views[n] for n in ("q", "k", "v")), m, self.acts[self.Q], self.eps, self._cfg()))
             launch("o", lambda w=w, a=a_o: self._gemv(w["o"], self.out["o"], a, name="o"))
             h_mid = self.hbuf[0]
             a_m = self._add_norm(self.out["o"], h_cur, h_mid, w["g_mlp"])
@@ -345,10 +450,11 @@ class DecodeStack:
         if self.chain is not None:
             return 1
         if self.glu:
-            # first norm; per layer q/k/v, [quantize], o, add+norm, gate/up
+            # first norm; per layer q/k/v, [quantize, or the attention step], o, add+norm, gate/up
             # pair, down, add+norm (and a combine per split-K projection);
             # lm-head, argmax
-            per_layer = 5 + (0 if self.mode == lk.LK_DEQUANT else 1) + self.glu_launches() + len(self.splitk)
+            o_in = self.attn.launches() if self.attn is not None else 0 if self.mode == lk.LK_DEQUANT else 1
+            per_layer = 5 + o_in + self.glu_launches() + len(self.splitk)
             return 1 + self.L * per_layer + 2
         n = 1  # argmax reduce
         f = self.fused
