@@ -69,14 +69,6 @@ __device__ __forceinline__ unsigned lds32(unsigned a) {
   return r;
 }
 
-// Bytes c, c+1 (selector) of u = levels ^ 0x80 as a pair of f16 levels: 1024 + u is
-// exact in the low mantissa bits of 0x64xx, less 1152.
-__device__ __forceinline__ unsigned level_pair(unsigned u, unsigned sel) {
-  const unsigned b = prmt(u, 0x64646464u, sel);
-  const __half2 h = __hsub2(*(const __half2*)&b, __half2half2(__ushort_as_half(0x6480)));
-  return *(const unsigned*)&h;
-}
-
 constexpr int ERR_ATTN_WAIT = 32;
 
 template <int TYPE, int D>
@@ -370,7 +362,7 @@ __global__ void __launch_bounds__(32 * Cfg<TYPE, D>::NW, 1) attn_kernel(const __
       const float ref = mn == -INFINITY ? 0.0f : mn;
       float al = ex2(m - ref);  // 0 from an empty start
       m = mn;
-      constexpr float UP = TYPE == LK_KV_BF16 ? 0.0f : Q8 ? 10.0f : 14.0f;
+      constexpr float UP = weight_shift(TYPE);
       float p[4][2];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -761,7 +753,7 @@ __global__ void __launch_bounds__(128) attn_join_kernel(const JoinArgs j) {
 
 // ---- host --------------------------------------------------------------------------
 // Whether rows on the same keys go to the tile kernel.
-bool tiled(long rows, int type) { return type != LK_KV_Q8 && rows > 16; }
+bool tiled(long rows, int type) { return rows > 16; }
 
 struct Plan {
   long slots, tslots[2];  // streaming partials; tile partials of sequences, prefix
@@ -863,8 +855,8 @@ lk_status run_d(JoinArgs& j, int type, lk_mode mode, int pdl, cudaStream_t strea
     a.late = 1;
   }
   if (!st && (a.own_tiled || a.pre_tiled)) {
-    const int part = D == 128 ? TUNIT : TUNIT / 2;  // tokens that a warp of the tile kernel fetches
-    if ((st = make_maps(a, type, D, page < part ? page : part))) return st;
+    const int part = D == 128 ? 128 : 64;  // tokens that a warp of the tile kernel fetches
+    if (type != LK_KV_Q8 && (st = make_maps(a, type, D, page < part ? page : part))) return st;
     st = launch_tiles(a, type, D, pdl, stream);
   }
   if (st) return st;
@@ -941,6 +933,7 @@ lk_status lk_attn_shared(const lk_kv_cache* cache, const float* q, int n_q, cons
     a.tml[x] = (float*)((char*)ws + ml[x + 1]);
     a.to[x] = (float*)((char*)ws + o[x + 1]);
   }
+  a.tunit = cache->type == LK_KV_Q8 ? 64 : 128;
   a.W = d->sm_count < kMaxWorkers ? d->sm_count : kMaxWorkers;
   a.TW = d->sm_count < kTileWorkers ? d->sm_count : kTileWorkers;
   a.wait_ns = opt_wait_us > 0 ? (unsigned long long)opt_wait_us * 1000ull : 2000000000ull;

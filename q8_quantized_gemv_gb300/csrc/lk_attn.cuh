@@ -46,7 +46,7 @@ inline lk_status check_rows(const lk_kv_cache* c, const int32_t* table, int tabl
 // number B) with a group of the query rows that read it: row i of a head's
 // R * G (prefix: B * R * G): token i / G, query head i % G.  The streaming
 // kernel's items have up to 8 rows and their keys come in units of 32, the tile
-// kernel's 256 rows and units of 128.  A sequence belongs to one of the two.
+// kernel's 256 rows and units of 128 (Q8: 64).  A sequence belongs to one of the two.
 // All units of a kernel's items, in a fixed order, are dealt to its blocks in
 // equal contiguous shares, whatever the lengths are, and a streaming block's
 // share to its warps in the same way; the part of an item that a block (warp)
@@ -56,7 +56,6 @@ inline lk_status check_rows(const lk_kv_cache* c, const int32_t* table, int tabl
 // whole share is one item's joins its warps' partials itself.
 constexpr int UNIT = 32;           // keys of a unit, streaming kernel
 constexpr int TR = 8;              // its query rows of an item
-constexpr int TUNIT = 128;         // keys of a unit, tile kernel
 constexpr int TROWS = 256;         // its query rows of an item
 constexpr int kMaxWorkers = 192;   // blocks of the streaming launch, at most
 constexpr int kMaxWarps = 12;      // and their warps
@@ -91,6 +90,7 @@ struct AttnArgs {
   float* tml[2];      // tile partials of the sequences, the prefix: [slot][slot rows][2],
   float* to[2];       //   [slot][slot rows][D], 16-byte pieces permuted in 128 bytes by row & 7
   int W, NW, TW;      // blocks and warps of the streaming launch, blocks of the tile launch
+  int tunit;          // keys of a unit of the tile kernel
   int late;           // the tile launch comes after a streaming one of the same call
   unsigned long long wait_ns;
   int* err;
@@ -137,7 +137,7 @@ __device__ __forceinline__ void make_deal(const AttnArgs& a, Deal& d) {
     long u = 0;
     if (s < nseq) {
       const int n = s == a.B ? a.plen : min(max(__ldcg(a.lens + s), 0), cap);
-      constexpr int U = TILED ? TUNIT : UNIT;
+      const int U = TILED ? a.tunit : UNIT;
       const bool mine = ((s == a.B ? a.pre_tiled : a.own_tiled) != 0) == TILED;
       d.n[s] = n;
       d.un[s] = mine ? (n + U - 1) / U : 0;
@@ -184,6 +184,18 @@ __device__ __forceinline__ float ex2(float x) {
   float r;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
+}
+// Bytes of u = levels ^ 0x80 that the selector names as a pair of f16 levels: 1024 + u
+// is exact in the low mantissa bits of 0x64xx, less 1152.
+__device__ __forceinline__ unsigned level_pair(unsigned u, unsigned sel) {
+  const unsigned b = __byte_perm(u, 0x64646464u, sel);
+  const __half2 h = __hsub2(*(const __half2*)&b, __half2half2(__ushort_as_half(0x6480)));
+  return *(const unsigned*)&h;
+}
+// log2 of what a row's largest weight is, sums and weighted values with it: the
+// two kernels' partials are joined as they are.
+__host__ __device__ constexpr float weight_shift(int type) {
+  return type == LK_KV_BF16 ? 0.0f : type == LK_KV_Q8 ? 10.0f : 14.0f;
 }
 // Shift of a row's queries before f16 splitting: 2^10 / amax's power of two
 // (returned), and its inverse for the scores.

@@ -33,19 +33,21 @@ using namespace lktc;
 namespace lkattn {
 
 constexpr int ERR_TILE_WAIT = 32;
+constexpr int kTileThreads = 384, kTileRegs = 168;
 
-template <int D>
+template <int TYPE, int D>
 struct TCfg {
-  static constexpr int HALF = TUNIT * 128;          // 128 rows of 64 16-bit values
+  static constexpr bool BF = TYPE == LK_KV_BF16, Q8 = TYPE == LK_KV_Q8;
+  static constexpr int KT = Q8 ? 64 : 128;          // keys of a tile
+  static constexpr int HALF = 128 * 128;            // 128 rows of 64 16-bit values
   static constexpr int BUF = (D / 64) * HALF;       // a tile of keys or values
   static constexpr int QS = 2 * BUF;                // a stream's queries, high and low terms
   static constexpr int NB = D == 128 ? 3 : 8;       // ring buffers
   static constexpr int SMEM = 2 * QS + NB * BUF + 1024;
-  static constexpr int THREADS = 384;
-  // Registers: the launch has THREADS * LAUNCH of them; the streams take
-  // 2 * 128 * STREAM and leave 128 * REST, the same sum.
-  static constexpr int LAUNCH = 168, STREAM = 216, REST = 72;
-  static_assert(THREADS * LAUNCH == 2 * 128 * STREAM + 128 * REST, "register split");
+  // Registers: the launch has kTileThreads * kTileRegs of them; the streams
+  // take 2 * 128 * STREAM and leave 128 * REST, the same sum.
+  static constexpr int STREAM = 216, REST = 72;
+  static_assert(kTileThreads * kTileRegs == 2 * 128 * STREAM + 128 * REST, "register split");
 };
 
 // Where a tile's K and V are in a segment's order of ring fills (nt tiles):
@@ -80,15 +82,50 @@ __device__ __forceinline__ Segment next_segment(const AttnArgs& a, const Deal& d
   return g;
 }
 
+// Fill i of a segment: its tile, and whether it is the values'.
+__device__ __forceinline__ int tile_of_fill(const Segment& g, int i, bool& is_v) {
+  if (g.both) return is_v = i & 1, i >> 1;
+  if (i == 0) return is_v = false, 0;
+  if (i == 2 * g.nt - 1) return is_v = true, g.nt - 1;
+  is_v = !(i & 1);
+  return is_v ? (i - 2) >> 1 : (i + 1) >> 1;
+}
+
+// Q8: the power of two that brings the largest scale of a 64-token tile to 64 ..
+// 128.  pg: lanes 0..3 have the pages of its groups of 16 tokens (-1: none).
+template <int D>
+__device__ __forceinline__ float scale_shift(const AttnArgs& a, const __half* sc, int pg, int key0, int n, int kvh) {
+  constexpr int LPG = D / 16, TP = 16 / LPG, WT = D / 64;  // lanes of a group, tokens of a lane, words of a token
+  const int lane = threadIdx.x & 31, grp = lane / LPG, k0 = key0 + 16 * grp, p = __shfl_sync(FULL, pg, grp & 3);
+  unsigned mx = 0;
+  if (grp < 4 && p >= 0 && k0 < n) {
+    const long r = (((long)p * a.n_kv + kvh) << a.page_log2) + (k0 & ((1 << a.page_log2) - 1));
+    const uint4 w = __ldg((const uint4*)(sc + r * (D / 32)) + lane % LPG);
+    const unsigned x[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (k0 + (lane % LPG) * TP + i / WT < n) mx = max(mx, max(x[i] & 0x7fffu, (x[i] >> 16) & 0x7fffu));
+  }
+  mx = __reduce_max_sync(FULL, mx);
+  const float m = __half2float(__ushort_as_half((unsigned short)mx));  // 0, or at least 2^-24
+  return mx ? __uint_as_float((260u - (__float_as_uint(m) >> 23)) << 23) : 1.0f;
+}
+
+__device__ __forceinline__ void sts128(unsigned at, const unsigned* r) {
+  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]) : "memory");
+}
+
 // The 128 threads of stream x.
 __device__ __forceinline__ void group_sync(int x) {
   if (x == 0) asm volatile("bar.sync 1, 128;" ::: "memory");
   else asm volatile("bar.sync 2, 128;" ::: "memory");
 }
 
-template <bool BF, int D>
-__global__ void __launch_bounds__(TCfg<D>::THREADS) __maxnreg__(TCfg<D>::LAUNCH) attn_tile_kernel(const __grid_constant__ AttnArgs a) {
-  typedef TCfg<D> C;
+template <int TYPE, int D>
+__global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid_constant__ AttnArgs a) {
+  typedef TCfg<TYPE, D> C;
+  constexpr bool BF = C::BF, Q8 = C::Q8;
+  constexpr int KT = C::KT;
   extern __shared__ unsigned char raw[];
   __shared__ Deal deal;
   __shared__ __align__(8) unsigned long long bars[2 * C::NB + 9];
@@ -101,9 +138,11 @@ __global__ void __launch_bounds__(TCfg<D>::THREADS) __maxnreg__(TCfg<D>::LAUNCH)
                  b_o = b_p + 16, b_drain = b_o + 16;
   const int lane = threadIdx.x & 31, warp = __shfl_sync(FULL, threadIdx.x >> 5, 0);
   if (threadIdx.x == 0) {
-    map_prefetch(&a.kmap);
-    map_prefetch(&a.vmap);
-    for (int i = 0; i < C::NB; ++i) bar_init(b_full + 8 * i, 2), bar_init(b_free + 8 * i, 1);
+    if constexpr (!Q8) {
+      map_prefetch(&a.kmap);
+      map_prefetch(&a.vmap);
+    }
+    for (int i = 0; i < C::NB; ++i) bar_init(b_full + 8 * i, Q8 ? 1 : 2), bar_init(b_free + 8 * i, 1);
     for (int x = 0; x < 2; ++x) {
       bar_init(b_q + 8 * x, 128);
       bar_init(b_s + 8 * x, 1);
@@ -142,7 +181,7 @@ __global__ void __launch_bounds__(TCfg<D>::THREADS) __maxnreg__(TCfg<D>::LAUNCH)
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::REST));
     if (warp == 0) {
       // ---- MMA issue: the warp stays together, one elected thread issues ---------------
-      constexpr unsigned id_qk = inst_desc(BF, false, 128, TUNIT), id_pv = inst_desc(BF, true, 128, D);
+      constexpr unsigned id_qk = inst_desc(BF, false, 128, 128), id_pv = inst_desc(BF, true, 128, D);
       const bool el = elect_one();
       const unsigned long long q_desc = smem_desc(base, 16, 1024), k_desc = smem_desc(ring, 16, 1024),
                                v_desc = smem_desc(ring, C::HALF, 1024);
@@ -179,11 +218,21 @@ __global__ void __launch_bounds__(TCfg<D>::THREADS) __maxnreg__(TCfg<D>::LAUNCH)
           const unsigned long long v = v_desc + ((buf * C::BUF) >> 4);
           const unsigned p = tmem + x * 128, dst = tmem + 256 + x * 128;
           if (el) {
+            // 16 columns hold the two terms of 16 keys' weights
+            if constexpr (Q8) {
+              // rows 0..63 of the tile are the values' high terms, 64..127 the low
+              // ones; low times low is left out (2^-22)
 #pragma unroll
-            for (int i = 0; i < 2 * (TUNIT / 16); ++i) {
-              // 16 columns hold the two terms of 16 keys' weights
-              const int term = i / (TUNIT / 16), st = i % (TUNIT / 16);
-              mma_ts(dst, p + st * 16 + term * 8, v + ((st * 2048) >> 4), id_pv, i > 0);
+              for (int i = 0; i < 12; ++i) {
+                const int st = i & 3, term = i >> 2;
+                mma_ts(dst, p + st * 16 + (term == 1 ? 8 : 0), v + (((term == 2 ? 4 + st : st) * 2048) >> 4), id_pv, i > 0);
+              }
+            } else {
+#pragma unroll
+              for (int i = 0; i < 16; ++i) {
+                const int term = i / 8, st = i % 8;
+                mma_ts(dst, p + st * 16 + term * 8, v + ((st * 2048) >> 4), id_pv, i > 0);
+              }
             }
             mma_commit(b_o + 8 * x);
             if (!g.both || x == 1) mma_commit(b_free + 8 * buf);
@@ -204,13 +253,86 @@ __global__ void __launch_bounds__(TCfg<D>::THREADS) __maxnreg__(TCfg<D>::LAUNCH)
       if (el) mma_commit(b_drain);
       __syncwarp();
       if (!bar_drain(b_drain, 0, a.wait_ns) && lane == 0) atomicOr(a.err, ERR_TILE_WAIT);
+    } else if (Q8) {
+      // ---- the ring's fills, Q8 ------------------------------------------------------
+      // Warps 1 to 3 take the fills in turn, so that one's loads run beside the
+      // others' conversions: 64 tokens' levels times scales as two f16 terms, the
+      // high one rounded, the low one what that left (exact), rows 0..63 and 64..127
+      // of the tile.  Scales are first shifted so that the tile's largest is 64 ..
+      // 128; the streams shift back.
+      constexpr int CPR = D / 16, KN = 64 * CPR / 32, GB = 4;  // 16-byte pieces of a token, of a lane, of a batch
+      unsigned f = 0;
+      bool ok = true;
+      while (u0 < u1 && ok) {
+        const Segment g = next_segment(a, deal, s, u0, u1);
+        const int* table = g.s == a.B ? a.ptable : a.table + (long)g.s * a.table_w;
+        for (int i = 0; i < 2 * g.nt && ok; ++i, ++f) {
+          if (f % 3 != (unsigned)warp - 1) continue;
+          bool is_v;
+          const int t = tile_of_fill(g, i, is_v), key0 = (g.ub + t) * KT;
+          int pg = -1;
+          if (lane < 4 && key0 + 16 * lane < g.n) {
+            pg = __ldg(table + ((key0 + 16 * lane) >> a.page_log2));
+            if ((unsigned)pg >= (unsigned)a.n_pages) pg = -1;
+          }
+          const char* lv = (const char*)(is_v ? a.v : a.k);
+          const __half* sc = is_v ? a.vs : a.ks;
+          uint4 w[2][GB];
+          __half e[2][GB];
+          const auto load = [&](int b, uint4(&wb)[GB], __half(&eb)[GB]) {
+#pragma unroll
+            for (int j = 0; j < GB; ++j) {
+              const int c = lane + 32 * (b * GB + j), row = c / CPR, grp = (b * GB + j) * (32 / CPR) / 16;
+              const int p = __shfl_sync(FULL, pg, grp);
+              const bool in = p >= 0 && key0 + row < g.n;
+              const int k0 = key0 + 16 * grp;
+              const long r = (((long)max(p, 0) * a.n_kv + g.kvh) << a.page_log2) + (k0 & ((1 << a.page_log2) - 1)) + (row & 15);
+              wb[j] = in ? __ldg((const uint4*)(lv + r * D + (c % CPR) * 16)) : make_uint4(0, 0, 0, 0);
+              eb[j] = in ? __ldg(sc + r * (D / 32) + (c % CPR) / 2) : __ushort_as_half(0);
+            }
+          };
+          load(0, w[0], e[0]);
+          const float up = scale_shift<D>(a, sc, pg, key0, g.n, g.kvh);
+          const unsigned buf = f % C::NB, dst0 = ring + buf * C::BUF;
+          ok = __all_sync(FULL, wait(b_free + 8 * buf, (f / C::NB) ^ 1u));
+          if (!ok) break;
+#pragma unroll
+          for (int b = 0; b < KN / GB; ++b) {
+            if (b + 1 < KN / GB) load(b + 1, w[(b + 1) & 1], e[(b + 1) & 1]);
+#pragma unroll
+            for (int j = 0; j < GB; ++j) {
+              const int c = lane + 32 * (b * GB + j), row = c / CPR, ch = c % CPR;
+              const __half2 e2 = __half2half2(__float2half_rn(__half2float(e[b & 1][j]) * up));
+              const unsigned x[4] = {w[b & 1][j].x, w[b & 1][j].y, w[b & 1][j].z, w[b & 1][j].w};
+              unsigned hi[8], lo[8];
+#pragma unroll
+              for (int q = 0; q < 8; ++q) {
+                const unsigned pr = level_pair(x[q >> 1] ^ 0x80808080u, q & 1 ? 0x4342 : 0x4140);
+                const __half2 l2 = *(const __half2*)&pr, h2 = __hmul2(l2, e2), r2 = __hfma2(l2, e2, __hneg2(h2));
+                hi[q] = *(const unsigned*)&h2;
+                lo[q] = *(const unsigned*)&r2;
+              }
+              const unsigned at = dst0 + (ch >> 2) * C::HALF + row * 128;
+#pragma unroll
+              for (int q = 0; q < 2; ++q) {
+                const unsigned pc = ((2 * (ch & 3) + q) ^ (row & 7)) << 4;
+                sts128(at + pc, hi + 4 * q);
+                sts128(at + 64 * 128 + pc, lo + 4 * q);
+              }
+            }
+          }
+          fence_async();
+          __syncwarp();
+          if (lane == 0) bar_arrive(b_full + 8 * buf);
+        }
+      }
     } else if (warp >= 2) {
       // ---- the ring's fills ----------------------------------------------------------
       // Warp 2 + h fills part h: of D 128 half h of every token, of D 64 half the
       // tokens.  A tile whose tokens are all there comes by tensor copies; one with
       // trailing or absent tokens by copies of the threads, which write zeros there.
       const int part = warp - 2;
-      constexpr int TOK = D == 128 ? TUNIT : TUNIT / 2;  // tokens of a part
+      constexpr int TOK = D == 128 ? KT : KT / 2;  // tokens of a part
       const int tok0 = D == 128 ? 0 : part * TOK;
       unsigned f = 0;
       bool ok = true;
@@ -218,14 +340,8 @@ __global__ void __launch_bounds__(TCfg<D>::THREADS) __maxnreg__(TCfg<D>::LAUNCH)
         const Segment g = next_segment(a, deal, s, u0, u1);
         const int* table = g.s == a.B ? a.ptable : a.table + (long)g.s * a.table_w;
         for (int i = 0; i < 2 * g.nt && ok; ++i, ++f) {
-          // fill i of the segment: which tile, keys or values
           bool is_v;
-          int t;
-          if (g.both) is_v = i & 1, t = i >> 1;
-          else if (i == 0) is_v = false, t = 0;
-          else if (i == 2 * g.nt - 1) is_v = true, t = g.nt - 1;
-          else is_v = !(i & 1), t = is_v ? (i - 2) >> 1 : (i + 1) >> 1;
-          const int key0 = (g.ub + t) * TUNIT + tok0;
+          const int t = tile_of_fill(g, i, is_v), key0 = (g.ub + t) * KT + tok0;
           // pages of the part's groups of 16 tokens
           int pg = -1;
           if (lane < TOK / 16 && key0 + 16 * lane < g.n) {
@@ -280,7 +396,7 @@ __global__ void __launch_bounds__(TCfg<D>::THREADS) __maxnreg__(TCfg<D>::LAUNCH)
     const unsigned tw = tmem + ((unsigned)(32 * wq) << 16);  // the warp's lanes
     const unsigned ts = tw + x * 128, to = tw + 256 + x * 128;
     const unsigned qs = base + x * C::QS;
-    constexpr float UP = BF ? 0.0f : 14.0f;
+    constexpr float UP = weight_shift(TYPE);
     unsigned nt = 0;  // tiles so far
     bool ok = true, stored = false;
     while (u0 < u1 && ok) {
@@ -356,11 +472,17 @@ __global__ void __launch_bounds__(TCfg<D>::THREADS) __maxnreg__(TCfg<D>::LAUNCH)
 #pragma unroll
       for (int i = 0; i < D; ++i) O[i] = 0.0f;
       for (int j = 0; j < cnt; ++j, ++nt) {
-        const int key0 = (g.ub + (g.both ? j : 2 * j + x)) * TUNIT;
+        const int key0 = (g.ub + (g.both ? j : 2 * j + x)) * KT;
         int pg = -1;
-        if (lane < 8 && key0 + 16 * lane < g.n) pg = __ldg(table + ((key0 + 16 * lane) >> a.page_log2));
-        const unsigned there = __ballot_sync(FULL, (unsigned)pg < (unsigned)a.n_pages);
-        const bool whole = __all_sync(FULL, key0 + TUNIT <= vis) && there == 0xffu;
+        if (lane < KT / 16 && key0 + 16 * lane < g.n) pg = __ldg(table + ((key0 + 16 * lane) >> a.page_log2));
+        if ((unsigned)pg >= (unsigned)a.n_pages) pg = -1;
+        const unsigned there = __ballot_sync(FULL, pg >= 0);
+        const bool whole = __all_sync(FULL, key0 + KT <= vis) && there == (1u << (KT / 16)) - 1;
+        float rt = rs, vt = 1.0f;  // what the scores and the values are multiplied with
+        if constexpr (Q8) {
+          rt = rs / scale_shift<D>(a, a.ks, pg, key0, g.n, g.kvh);
+          vt = 1.0f / scale_shift<D>(a, a.vs, pg, key0, g.n, g.kvh);
+        }
         ok = __all_sync(FULL, wait(b_s + 8 * x, nt));
         if (!ok) break;
         tm_after();
@@ -370,34 +492,54 @@ __global__ void __launch_bounds__(TCfg<D>::THREADS) __maxnreg__(TCfg<D>::LAUNCH)
         const auto weights = [&](auto cut) {
           constexpr bool CUT = decltype(cut)::value;
 #pragma unroll 1
-          for (int c = 0; c < 4; ++c) {
+          for (int c = 0; c < KT / 32; ++c) {
             unsigned r[32];
             tm_ld32(ts + 32 * c, r);
-            tm_ld_wait(r);
+            if constexpr (Q8) {
+              unsigned r2[32];
+              tm_ld32(ts + 64 + 32 * c, r2);
+              tm_ld_wait(r2);
+              tm_ld_wait(r);
+#pragma unroll
+              for (int k = 0; k < 32; ++k) r[k] = __float_as_uint(__uint_as_float(r[k]) + __uint_as_float(r2[k]));
+            } else {
+              tm_ld_wait(r);
+            }
             const int left = CUT ? vis - key0 - 32 * c : 32;
 #pragma unroll
             for (int k = 0; k < 32; ++k)
               if (!CUT || (k < left && ((there >> (2 * c + (k >> 4))) & 1u))) mx = fmaxf(mx, __uint_as_float(r[k]));
           }
-          const float mn = fmaxf(m, mx * rs);
+          const float mn = fmaxf(m, mx * rt);
           ref = mn == -INFINITY ? 0.0f : mn;
           al = ex2(m - ref);
           m = mn;
           const float shift = UP - ref;
           unsigned r[2][16];
-          tm_ld16(ts, r[0]);
-          tm_ld_wait(r[0]);
+          const auto scores = [&](int c, unsigned(&y)[16]) {
+            tm_ld16(ts + 16 * c, y);
+            if constexpr (Q8) {
+              unsigned y2[16];
+              tm_ld16(ts + 64 + 16 * c, y2);
+              tm_ld_wait(y2);
+              tm_ld_wait(y);
 #pragma unroll
-          for (int c = 0; c < 8; ++c) {
+              for (int k = 0; k < 16; ++k) y[k] = __float_as_uint(__uint_as_float(y[k]) + __uint_as_float(y2[k]));
+            }
+          };
+          scores(0, r[0]);
+          if constexpr (!Q8) tm_ld_wait(r[0]);
+#pragma unroll
+          for (int c = 0; c < KT / 16; ++c) {
             unsigned(&y)[16] = r[c & 1];
-            if (c < 7) tm_ld16(ts + 16 * (c + 1), r[(c + 1) & 1]);
+            if (c + 1 < KT / 16) scores(c + 1, r[(c + 1) & 1]);
             const int left = !CUT ? 16 : (there >> c) & 1u ? vis - key0 - 16 * c : 0;
             float s0 = 0.0f, s1 = 0.0f;
             unsigned w[16];
 #pragma unroll
             for (int k = 0; k < 16; k += 2) {
-              float p0 = ex2(fmaf(__uint_as_float(y[k]), rs, shift));
-              float p1 = ex2(fmaf(__uint_as_float(y[k + 1]), rs, shift));
+              float p0 = ex2(fmaf(__uint_as_float(y[k]), rt, shift));
+              float p1 = ex2(fmaf(__uint_as_float(y[k + 1]), rt, shift));
               if constexpr (CUT) {
                 p0 = k < left ? p0 : 0.0f;
                 p1 = k + 1 < left ? p1 : 0.0f;
@@ -407,7 +549,7 @@ __global__ void __launch_bounds__(TCfg<D>::THREADS) __maxnreg__(TCfg<D>::LAUNCH)
               w[8 + (k >> 1)] = split2<BF>(p0, p1);
             }
             sum += s0 + s1;
-            if (c < 7) tm_ld_wait(r[(c + 1) & 1]);
+            if (!Q8 && c + 1 < KT / 16) tm_ld_wait(r[(c + 1) & 1]);
             tm_st16(ts + 16 * c, w);
           }
         };
@@ -426,7 +568,8 @@ __global__ void __launch_bounds__(TCfg<D>::THREADS) __maxnreg__(TCfg<D>::LAUNCH)
           tm_ld32(to + 32 * c, r);
           tm_ld_wait(r);
 #pragma unroll
-          for (int k = 0; k < 32; ++k) O[32 * c + k] = fmaf(O[32 * c + k], al, __uint_as_float(r[k]));
+          for (int k = 0; k < 32; ++k)
+            O[32 * c + k] = fmaf(O[32 * c + k], al, Q8 ? __uint_as_float(r[k]) * vt : __uint_as_float(r[k]));
         }
         tm_before();
       }
@@ -462,26 +605,31 @@ __global__ void __launch_bounds__(TCfg<D>::THREADS) __maxnreg__(TCfg<D>::LAUNCH)
   if (warp == 0) tm_free(tmem, 512);
 }
 
-template <bool BF, int D>
+template <int TYPE, int D>
 lk_status run_tiles(const AttnArgs& a, int pdl, cudaStream_t stream) {
-  typedef TCfg<D> C;
+  typedef TCfg<TYPE, D> C;
   static std::atomic<int> done[kMaxDevices], regs;
-  if (!prepare_kernel(attn_tile_kernel<BF, D>, done, C::SMEM)) return LK_ERR_CUDA;
+  if (!prepare_kernel(attn_tile_kernel<TYPE, D>, done, C::SMEM)) return LK_ERR_CUDA;
   if (!regs.load(std::memory_order_acquire)) {
     // the register split waits forever on a launch with fewer than it assumes
     cudaFuncAttributes fa;
-    if (cudaFuncGetAttributes(&fa, attn_tile_kernel<BF, D>) != cudaSuccess || fa.numRegs != C::LAUNCH)
+    if (cudaFuncGetAttributes(&fa, attn_tile_kernel<TYPE, D>) != cudaSuccess || fa.numRegs != kTileRegs)
       return LK_ERR_CUDA;
     regs.store(1, std::memory_order_release);
   }
-  return launch(attn_tile_kernel<BF, D>, dim3(a.TW), dim3(C::THREADS), C::SMEM, pdl, stream, a) == cudaSuccess
+  return launch(attn_tile_kernel<TYPE, D>, dim3(a.TW), dim3(kTileThreads), C::SMEM, pdl, stream, a) == cudaSuccess
              ? LK_OK
              : LK_ERR_CUDA;
 }
 
 lk_status launch_tiles(const AttnArgs& a, int type, int D, int pdl, cudaStream_t stream) {
-  if (type == LK_KV_BF16) return D == 128 ? run_tiles<true, 128>(a, pdl, stream) : run_tiles<true, 64>(a, pdl, stream);
-  return D == 128 ? run_tiles<false, 128>(a, pdl, stream) : run_tiles<false, 64>(a, pdl, stream);
+  if (D == 128)
+    return type == LK_KV_F16    ? run_tiles<LK_KV_F16, 128>(a, pdl, stream)
+           : type == LK_KV_BF16 ? run_tiles<LK_KV_BF16, 128>(a, pdl, stream)
+                                : run_tiles<LK_KV_Q8, 128>(a, pdl, stream);
+  return type == LK_KV_F16    ? run_tiles<LK_KV_F16, 64>(a, pdl, stream)
+         : type == LK_KV_BF16 ? run_tiles<LK_KV_BF16, 64>(a, pdl, stream)
+                              : run_tiles<LK_KV_Q8, 64>(a, pdl, stream);
 }
 
 }  // namespace lkattn
