@@ -644,10 +644,10 @@ __device__ __forceinline__ Source tile_source(const AttnArgs& a, const Deal& d, 
   const int un = d.un[s];
   if (un == 0) return r;
   const long T = d.cum[a.B + a.shared], W = shares(a.TW, T);
-  const int group = i / TROWS, li = kvh * groups_of<true>(a, s) + group, ig = i - group * TROWS;
+  const int group = i / a.trows, li = kvh * groups_of<true>(a, s) + group, ig = i - group * a.trows;
   const long ub = d.cum[s] + (long)li * un;
   const int w0 = (int)(((ub + 1) * W - 1) / T), w1 = (int)(((ub + un) * W - 1) / T);
-  const int rows = rows_of(a, s), rg = min(TROWS, rows - group * TROWS), which = s == a.B ? 1 : 0;
+  const int rows = rows_of(a, s), rg = min(a.trows, rows - group * a.trows), which = s == a.B ? 1 : 0;
   r.step = tile_slot_rows(rows);
   r.mid = (long)(w0 + item0<true>(a, s) + li) * r.step + ig;
   r.nm = w1 - w0 + 1;
@@ -656,7 +656,7 @@ __device__ __forceinline__ Source tile_source(const AttnArgs& a, const Deal& d, 
   r.n = r.nm * r.per;
   r.ml = a.tml[which];
   r.o = a.to[which];
-  r.flip = ig & 7;
+  r.flip = a.tflip ? ig & 7 : 0;
   return r;
 }
 
@@ -768,7 +768,7 @@ Plan plan(int n_q, int n_kv, int B, int R, int shared, int type) {
     p.slots += many[x] * ((rows[x] + TR - 1) / TR);
     if (!many[x] || !tiled(rows[x], type)) continue;
     p.tsr[x] = tile_slot_rows(rows[x]);
-    p.tslots[x] = kTileWorkers + many[x] * ((rows[x] + TROWS - 1) / TROWS);
+    p.tslots[x] = kTileWorkers + many[x] * ((rows[x] + 127) / 128);  // items of 128 rows or of 256
   }
   return p;
 }
@@ -934,6 +934,8 @@ lk_status lk_attn_shared(const lk_kv_cache* cache, const float* q, int n_q, cons
     a.to[x] = (float*)((char*)ws + o[x + 1]);
   }
   a.tunit = cache->type == LK_KV_Q8 ? 64 : 128;
+  a.trows = cache->type == LK_KV_Q8 ? 128 : 256;
+  a.tflip = cache->type != LK_KV_Q8;
   a.W = d->sm_count < kMaxWorkers ? d->sm_count : kMaxWorkers;
   a.TW = d->sm_count < kTileWorkers ? d->sm_count : kTileWorkers;
   a.wait_ns = opt_wait_us > 0 ? (unsigned long long)opt_wait_us * 1000ull : 2000000000ull;

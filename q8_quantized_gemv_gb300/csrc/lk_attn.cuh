@@ -46,7 +46,7 @@ inline lk_status check_rows(const lk_kv_cache* c, const int32_t* table, int tabl
 // number B) with a group of the query rows that read it: row i of a head's
 // R * G (prefix: B * R * G): token i / G, query head i % G.  The streaming
 // kernel's items have up to 8 rows and their keys come in units of 32, the tile
-// kernel's 256 rows and units of 128 (Q8: 64).  A sequence belongs to one of the two.
+// kernel's 256 rows (Q8: 128) and units of 128 (Q8: 64).  A sequence belongs to one of the two.
 // All units of a kernel's items, in a fixed order, are dealt to its blocks in
 // equal contiguous shares, whatever the lengths are, and a streaming block's
 // share to its warps in the same way; the part of an item that a block (warp)
@@ -56,15 +56,14 @@ inline lk_status check_rows(const lk_kv_cache* c, const int32_t* table, int tabl
 // whole share is one item's joins its warps' partials itself.
 constexpr int UNIT = 32;           // keys of a unit, streaming kernel
 constexpr int TR = 8;              // its query rows of an item
-constexpr int TROWS = 256;         // its query rows of an item
 constexpr int kMaxWorkers = 192;   // blocks of the streaming launch, at most
 constexpr int kMaxWarps = 12;      // and their warps
 constexpr int kTileWorkers = 192;  // blocks of a tile launch, at most
 constexpr int kMaxSeq = LK_MAX_BATCH + 1;
 
-// Rows of a tile slot: with up to 128 query rows the keys' tiles are halved
-// between two streams, each with a partial of the rows.
-__host__ __device__ inline int tile_slot_rows(long rows) { return rows <= 128 ? 2 * (int)rows : TROWS; }
+// Rows of a tile slot: of more than 128 query rows each has one partial, else
+// the keys' tiles are halved between two streams with a partial of the rows each.
+__host__ __device__ inline int tile_slot_rows(long rows) { return rows <= 128 ? 2 * (int)rows : 256; }
 
 struct AttnArgs {
   CUtensorMap kmap, vmap;  // [pages * heads * page rows][D], boxes of 128 bytes (Q8, D 64: 64) by box rows
@@ -88,9 +87,10 @@ struct AttnArgs {
   float* ml;          // streaming partials: [slot][TR][2] maximum and sum,
   float* o;           //   [slot][TR][D] weighted values
   float* tml[2];      // tile partials of the sequences, the prefix: [slot][slot rows][2],
-  float* to[2];       //   [slot][slot rows][D], 16-byte pieces permuted in 128 bytes by row & 7
+  float* to[2];       //   [slot][slot rows][D], tflip: 16-byte pieces permuted in 128 bytes by row & 7
   int W, NW, TW;      // blocks and warps of the streaming launch, blocks of the tile launch
-  int tunit;          // keys of a unit of the tile kernel
+  int tunit, trows;   // keys of a unit, rows of an item of the tile kernel
+  int tflip;          // whether its partials' pieces are permuted
   int late;           // the tile launch comes after a streaming one of the same call
   unsigned long long wait_ns;
   int* err;
@@ -107,7 +107,7 @@ struct Deal {
 __device__ __forceinline__ int rows_of(const AttnArgs& a, int s) { return (s == a.B ? a.B * a.R : a.R) * a.G; }
 template <bool TILED>
 __device__ __forceinline__ int groups_of(const AttnArgs& a, int s) {
-  constexpr int N = TILED ? TROWS : TR;
+  const int N = TILED ? a.trows : TR;
   return (rows_of(a, s) + N - 1) / N;
 }
 // Items before sequence s: of the streaming kernel in one row, of the tile

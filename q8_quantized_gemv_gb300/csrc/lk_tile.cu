@@ -43,7 +43,11 @@ struct TCfg {
   static constexpr int BUF = (D / 64) * HALF;       // a tile of keys or values
   static constexpr int QS = 2 * BUF;                // a stream's queries, high and low terms
   static constexpr int NB = D == 128 ? 3 : 8;       // ring buffers
-  static constexpr int SMEM = 2 * QS + NB * BUF + 1024;
+  // Q8: levels and scales of 64 tokens as they come, two for each of the three
+  // warps that convert them; the streams share the queries
+  static constexpr int RAW = Q8 ? 64 * D + 64 * D / 16 : 0, NRAW = Q8 ? 6 : 0;
+  static constexpr int QX = Q8 ? 0 : QS;            // from stream 0's queries to stream 1's
+  static constexpr int SMEM = QS + QX + NB * BUF + NRAW * RAW + 1024;
   // Registers: the launch has kTileThreads * kTileRegs of them; the streams
   // take 2 * 128 * STREAM and leave 128 * REST, the same sum.
   static constexpr int STREAM = 216, REST = 72;
@@ -75,7 +79,7 @@ __device__ __forceinline__ Segment next_segment(const AttnArgs& a, const Deal& d
   g.nt = (int)min((long)(un - g.ub), u1 - u0);
   g.kvh = li / groups;
   g.group = li - g.kvh * groups;
-  g.rows = min(TROWS, rows_of(a, s) - g.group * TROWS);
+  g.rows = min(a.trows, rows_of(a, s) - g.group * a.trows);
   g.both = g.rows > 128;
   g.slot = (int)blockIdx.x + item0<true>(a, s) + li;
   u0 += g.nt;
@@ -92,33 +96,53 @@ __device__ __forceinline__ int tile_of_fill(const Segment& g, int i, bool& is_v)
 }
 
 // Q8: the power of two that brings the largest scale of a 64-token tile to 64 ..
-// 128.  pg: lanes 0..3 have the pages of its groups of 16 tokens (-1: none).
+// 128.  A lane has 16 bytes of the scales (`in`: of tokens that are there), of
+// which tokens up to `left` from the tile's first count.
 template <int D>
-__device__ __forceinline__ float scale_shift(const AttnArgs& a, const __half* sc, int pg, int key0, int n, int kvh) {
-  constexpr int LPG = D / 16, TP = 16 / LPG, WT = D / 64;  // lanes of a group, tokens of a lane, words of a token
-  const int lane = threadIdx.x & 31, grp = lane / LPG, k0 = key0 + 16 * grp, p = __shfl_sync(FULL, pg, grp & 3);
+__device__ __forceinline__ float scale_shift(bool in, uint4 w, int left) {
+  constexpr int LPG = D / 16, TP = 16 / LPG, WT = D / 64;  // lanes of 16 tokens, tokens of a lane, words of a token
+  const int lane = threadIdx.x & 31, k0 = 16 * (lane / LPG) + (lane % LPG) * TP;
   unsigned mx = 0;
-  if (grp < 4 && p >= 0 && k0 < n) {
-    const long r = (((long)p * a.n_kv + kvh) << a.page_log2) + (k0 & ((1 << a.page_log2) - 1));
-    const uint4 w = __ldg((const uint4*)(sc + r * (D / 32)) + lane % LPG);
+  if (in) {
     const unsigned x[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      if (k0 + (lane % LPG) * TP + i / WT < n) mx = max(mx, max(x[i] & 0x7fffu, (x[i] >> 16) & 0x7fffu));
+      if (k0 + i / WT < left) mx = max(mx, max(x[i] & 0x7fffu, (x[i] >> 16) & 0x7fffu));
   }
   mx = __reduce_max_sync(FULL, mx);
   const float m = __half2float(__ushort_as_half((unsigned short)mx));  // 0, or at least 2^-24
   return mx ? __uint_as_float((260u - (__float_as_uint(m) >> 23)) << 23) : 1.0f;
 }
 
-__device__ __forceinline__ void sts128(unsigned at, const unsigned* r) {
-  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]) : "memory");
+// The same from the cache.  pg: lanes 0..3 have the pages of the tile's groups of
+// 16 tokens (-1: none).
+template <int D>
+__device__ __forceinline__ uint4 tile_scales(const AttnArgs& a, const uint16_t* sc, int pg, int key0, int kvh, bool& in) {
+  constexpr int LPG = D / 16;
+  const int lane = threadIdx.x & 31, grp = lane / LPG, k0 = key0 + 16 * grp, p = __shfl_sync(FULL, pg, grp & 3);
+  in = grp < 4 && p >= 0;
+  const long r = (((long)max(p, 0) * a.n_kv + kvh) << a.page_log2) + (k0 & ((1 << a.page_log2) - 1));
+  return in ? __ldg((const uint4*)(sc + r * (D / 32)) + lane % LPG) : make_uint4(0, 0, 0, 0);
 }
 
-// The 128 threads of stream x.
-__device__ __forceinline__ void group_sync(int x) {
-  if (x == 0) asm volatile("bar.sync 1, 128;" ::: "memory");
-  else asm volatile("bar.sync 2, 128;" ::: "memory");
+__device__ __forceinline__ uint4 lds128(unsigned at) {
+  uint4 r;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "r"(at) : "memory");
+  return r;
+}
+__device__ __forceinline__ float lds_half(unsigned at) {
+  unsigned short r;
+  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(r) : "r"(at) : "memory");
+  return __half2float(__ushort_as_half(r));
+}
+// 32 bytes to global memory
+__device__ __forceinline__ void stg256(float* p, const float* v) {
+  asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "f"(v[0]), "f"(v[1]), "f"(v[2]),
+               "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
+               : "memory");
+}
+__device__ __forceinline__ void sts128(unsigned at, const unsigned* r) {
+  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]) : "memory");
 }
 
 template <int TYPE, int D>
@@ -128,14 +152,14 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
   constexpr int KT = C::KT;
   extern __shared__ unsigned char raw[];
   __shared__ Deal deal;
-  __shared__ __align__(8) unsigned long long bars[2 * C::NB + 9];
+  __shared__ __align__(8) unsigned long long bars[2 * C::NB + 11 + C::NRAW];
   __shared__ unsigned tmem_slot;
   __shared__ int abort_flag;
   const unsigned base = (smem_addr(raw) + 1023u) & ~1023u;
-  const unsigned ring = base + 2 * C::QS;
+  const unsigned ring = base + C::QS + C::QX, raws = ring + C::NB * C::BUF;
   const unsigned bar0 = smem_addr(bars);
   const unsigned b_full = bar0, b_free = bar0 + 8 * C::NB, b_q = bar0 + 16 * C::NB, b_s = b_q + 16, b_p = b_s + 16,
-                 b_o = b_p + 16, b_drain = b_o + 16;
+                 b_o = b_p + 16, b_drain = b_o + 16, b_meet = b_drain + 8, b_raw = b_meet + 16;
   const int lane = threadIdx.x & 31, warp = __shfl_sync(FULL, threadIdx.x >> 5, 0);
   if (threadIdx.x == 0) {
     if constexpr (!Q8) {
@@ -150,6 +174,9 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
       bar_init(b_o + 8 * x, 1);
     }
     bar_init(b_drain, 1);
+    // Q8: of both streams; else of each
+    bar_init(b_meet, Q8 ? 256 : 128), bar_init(b_meet + 8, 128);
+    for (int i = 0; i < C::NRAW; ++i) bar_init(b_raw + 8 * i, 1);
     abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -195,7 +222,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
           const unsigned f = nb + k_at(g.both, g.both ? j : 2 * j + x), buf = f % C::NB;
           if (!__all_sync(FULL, wait(b_full + 8 * buf, f / C::NB))) return false;
           tm_after();
-          const unsigned long long q = q_desc + ((x * C::QS) >> 4), k = k_desc + ((buf * C::BUF) >> 4);
+          const unsigned long long q = q_desc + ((x * C::QX) >> 4), k = k_desc + ((buf * C::BUF) >> 4);
           const unsigned dst = tmem + x * 128;
           if (el) {
 #pragma unroll
@@ -255,14 +282,54 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
       if (!bar_drain(b_drain, 0, a.wait_ns) && lane == 0) atomicOr(a.err, ERR_TILE_WAIT);
     } else if (Q8) {
       // ---- the ring's fills, Q8 ------------------------------------------------------
-      // Warps 1 to 3 take the fills in turn, so that one's loads run beside the
-      // others' conversions: 64 tokens' levels times scales as two f16 terms, the
-      // high one rounded, the low one what that left (exact), rows 0..63 and 64..127
-      // of the tile.  Scales are first shifted so that the tile's largest is 64 ..
-      // 128; the streams shift back.
-      constexpr int CPR = D / 16, KN = 64 * CPR / 32, GB = 4;  // 16-byte pieces of a token, of a lane, of a batch
-      unsigned f = 0;
+      // Warps 1 to 3 take the fills in turn: 64 tokens' levels and scales come by
+      // bulk copies, a fill ahead, and are written as two f16 terms of level times
+      // scale, the high one rounded, the low one what that left (exact), rows 0..63
+      // and 64..127 of the tile.  Scales are first shifted so that the tile's largest
+      // is 64 .. 128; the streams shift back.
+      constexpr int CPR = D / 16, KN = 64 * CPR / 32;  // 16-byte pieces of a token, of a lane
+      const unsigned raw0 = raws + (warp - 1) * 2 * C::RAW, raw_bar = b_raw + 16 * (warp - 1);
+      unsigned f = 0, n_raw = 0;      // fills, fills of this warp
+      unsigned of = 0, o_there = 0;   // the fill before: its number, its groups of 16 tokens that are there,
+      int o_left = 0;                 // tokens from its first
       bool ok = true;
+      // convert this warp's fill number n
+      const auto convert = [&](unsigned n) {
+        const unsigned src = raw0 + (n & 1) * C::RAW, buf = of % C::NB, dst0 = ring + buf * C::BUF;
+        ok = __all_sync(FULL, wait(raw_bar + 8 * (n & 1), n >> 1));
+        if (!ok) return;
+        const bool in = lane < 4 * (D / 16) && ((o_there >> (lane / (D / 16))) & 1u);
+        const float up = scale_shift<D>(in, in ? lds128(src + 64 * D + lane * 16) : make_uint4(0, 0, 0, 0), o_left);
+        ok = __all_sync(FULL, wait(b_free + 8 * buf, (of / C::NB) ^ 1u));
+        if (!ok) return;
+#pragma unroll 4
+        for (int k = 0; k < KN; ++k) {
+          const int c = lane + 32 * k, row = c / CPR, ch = c % CPR;
+          const bool have = row < o_left && ((o_there >> (row >> 4)) & 1u);
+          const uint4 w = lds128(src + c * 16);
+          const float e = lds_half(src + 64 * D + (row * (D / 32) + (ch >> 1)) * 2);
+          const __half2 e2 = __half2half2(__float2half_rn(have ? e * up : 0.0f));
+          const unsigned x[4] = {w.x, w.y, w.z, w.w};
+          const unsigned at = dst0 + (ch >> 2) * C::HALF + row * 128;
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {  // 8 values: 16 bytes of each term
+            unsigned hi[4], lo[4];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+              const unsigned pr = level_pair(x[2 * q + (r >> 1)] ^ 0x80808080u, r & 1 ? 0x4342 : 0x4140);
+              const __half2 l2 = *(const __half2*)&pr, h2 = __hmul2(l2, e2), r2 = __hfma2(l2, e2, __hneg2(h2));
+              hi[r] = *(const unsigned*)&h2;
+              lo[r] = *(const unsigned*)&r2;
+            }
+            const unsigned pc = at + (((2 * (ch & 3) + q) ^ (row & 7)) << 4);
+            sts128(pc, hi);
+            sts128(pc + 64 * 128, lo);
+          }
+        }
+        fence_async();
+        __syncwarp();
+        if (lane == 0) bar_arrive(b_full + 8 * buf);
+      };
       while (u0 < u1 && ok) {
         const Segment g = next_segment(a, deal, s, u0, u1);
         const int* table = g.s == a.B ? a.ptable : a.table + (long)g.s * a.table_w;
@@ -275,57 +342,25 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
             pg = __ldg(table + ((key0 + 16 * lane) >> a.page_log2));
             if ((unsigned)pg >= (unsigned)a.n_pages) pg = -1;
           }
-          const char* lv = (const char*)(is_v ? a.v : a.k);
-          const __half* sc = is_v ? a.vs : a.ks;
-          uint4 w[2][GB];
-          __half e[2][GB];
-          const auto load = [&](int b, uint4(&wb)[GB], __half(&eb)[GB]) {
-#pragma unroll
-            for (int j = 0; j < GB; ++j) {
-              const int c = lane + 32 * (b * GB + j), row = c / CPR, grp = (b * GB + j) * (32 / CPR) / 16;
-              const int p = __shfl_sync(FULL, pg, grp);
-              const bool in = p >= 0 && key0 + row < g.n;
-              const int k0 = key0 + 16 * grp;
-              const long r = (((long)max(p, 0) * a.n_kv + g.kvh) << a.page_log2) + (k0 & ((1 << a.page_log2) - 1)) + (row & 15);
-              wb[j] = in ? __ldg((const uint4*)(lv + r * D + (c % CPR) * 16)) : make_uint4(0, 0, 0, 0);
-              eb[j] = in ? __ldg(sc + r * (D / 32) + (c % CPR) / 2) : __ushort_as_half(0);
-            }
-          };
-          load(0, w[0], e[0]);
-          const float up = scale_shift<D>(a, sc, pg, key0, g.n, g.kvh);
-          const unsigned buf = f % C::NB, dst0 = ring + buf * C::BUF;
-          ok = __all_sync(FULL, wait(b_free + 8 * buf, (f / C::NB) ^ 1u));
-          if (!ok) break;
-#pragma unroll
-          for (int b = 0; b < KN / GB; ++b) {
-            if (b + 1 < KN / GB) load(b + 1, w[(b + 1) & 1], e[(b + 1) & 1]);
-#pragma unroll
-            for (int j = 0; j < GB; ++j) {
-              const int c = lane + 32 * (b * GB + j), row = c / CPR, ch = c % CPR;
-              const __half2 e2 = __half2half2(__float2half_rn(__half2float(e[b & 1][j]) * up));
-              const unsigned x[4] = {w[b & 1][j].x, w[b & 1][j].y, w[b & 1][j].z, w[b & 1][j].w};
-              unsigned hi[8], lo[8];
-#pragma unroll
-              for (int q = 0; q < 8; ++q) {
-                const unsigned pr = level_pair(x[q >> 1] ^ 0x80808080u, q & 1 ? 0x4342 : 0x4140);
-                const __half2 l2 = *(const __half2*)&pr, h2 = __hmul2(l2, e2), r2 = __hfma2(l2, e2, __hneg2(h2));
-                hi[q] = *(const unsigned*)&h2;
-                lo[q] = *(const unsigned*)&r2;
-              }
-              const unsigned at = dst0 + (ch >> 2) * C::HALF + row * 128;
-#pragma unroll
-              for (int q = 0; q < 2; ++q) {
-                const unsigned pc = ((2 * (ch & 3) + q) ^ (row & 7)) << 4;
-                sts128(at + pc, hi + 4 * q);
-                sts128(at + 64 * 128 + pc, lo + 4 * q);
-              }
-            }
-          }
-          fence_async();
+          const unsigned there = __ballot_sync(FULL, pg >= 0), bar = raw_bar + 8 * (n_raw & 1);
+          const unsigned dst = raw0 + (n_raw & 1) * C::RAW;
+          if (lane == 0) bar_expect(bar, __popc(there) * 17 * D);
           __syncwarp();
-          if (lane == 0) bar_arrive(b_full + 8 * buf);
+          if (pg >= 0) {
+            const int k0 = key0 + 16 * lane;
+            const long r = (((long)pg * a.n_kv + g.kvh) << a.page_log2) + (k0 & ((1 << a.page_log2) - 1));
+            bulk_in(dst + lane * 16 * D, (const char*)(is_v ? a.v : a.k) + r * D, 16 * D, bar);
+            bulk_in(dst + 64 * D + lane * D, (is_v ? a.vs : a.ks) + r * (D / 32), D, bar);
+          }
+          if (n_raw > 0) convert(n_raw - 1);
+          of = f, o_there = there, o_left = g.n - key0;
+          ++n_raw;
         }
       }
+      if (ok && n_raw > 0) convert(n_raw - 1);
+      // a block that gave up: its copies have landed before it ends
+      if (!ok)
+        for (unsigned n = n_raw > 2 ? n_raw - 2 : 0; n < n_raw; ++n) bar_drain(raw_bar + 8 * (n & 1), (n >> 1) & 1u, a.wait_ns);
     } else if (warp >= 2) {
       // ---- the ring's fills ----------------------------------------------------------
       // Warp 2 + h fills part h: of D 128 half h of every token, of D 64 half the
@@ -395,20 +430,30 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
     const int x = (warp >> 2) - 1, wq = warp & 3, me = threadIdx.x & 127;
     const unsigned tw = tmem + ((unsigned)(32 * wq) << 16);  // the warp's lanes
     const unsigned ts = tw + x * 128, to = tw + 256 + x * 128;
-    const unsigned qs = base + x * C::QS;
+    const unsigned qs = base + x * C::QX;
     constexpr float UP = weight_shift(TYPE);
     unsigned nt = 0;  // tiles so far
     bool ok = true, stored = false;
+    // the threads of the stream (Q8: of both) meet; a bounded wait as every other
+    unsigned met = 0;
+    const auto meet = [&]() -> bool {
+      const unsigned bar = b_meet + (Q8 ? 0 : 8 * x);
+      bar_arrive(bar);
+      return __all_sync(FULL, wait(bar, met++));
+    };
     while (u0 < u1 && ok) {
       const Segment g = next_segment(a, deal, s, u0, u1);
       const bool pre = g.s == a.B;
       const int* table = pre ? a.ptable : a.table + (long)g.s * a.table_w;
-      const int r_first = g.group * TROWS + (g.both ? 128 * x : 0);  // row of the head that is the stream's row 0
+      const int r_first = g.group * a.trows + (g.both ? 128 * x : 0);  // row of the head that is the stream's row 0
       const int nr = g.both ? min(128, g.rows - 128 * x) : g.rows;
       const int cnt = g.both ? g.nt : x == 0 ? (g.nt + 1) / 2 : g.nt / 2;
-      if (stored) {  // the last segment's rows have left the queries' place
-        if (me == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-        group_sync(x);
+      if (stored) {
+        // the last segment's rows have left the queries' place (Q8: both streams
+        // are done with the queries)
+        if (!Q8 && me == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+        ok = meet();
+        if (!ok) break;
       }
       // queries: a warp takes its 32 rows, D / 32 values a lane, all loads first,
       // and writes their two terms swizzled
@@ -450,6 +495,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
           const unsigned at = qs + (d0 >> 6) * C::HALF + lr * 128 + ((piece ^ (lr & 7)) << 4) + (d0 & 7) * 2;
 #pragma unroll
           for (int term = 0; term < 2; ++term) {
+            if (Q8 && x == 1) break;  // stream 0 writes the queries of both
             const unsigned w0 = split2<BF>(v[i][0], v[i][1]);
             if constexpr (D == 128) {
               const unsigned w1 = split2<BF>(v[i][2], v[i][3]);
@@ -471,18 +517,29 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
       float O[D], m = -INFINITY, l = 0.0f;
 #pragma unroll
       for (int i = 0; i < D; ++i) O[i] = 0.0f;
-      for (int j = 0; j < cnt; ++j, ++nt) {
-        const int key0 = (g.ub + (g.both ? j : 2 * j + x)) * KT;
+      // what a tile needs beside its products, a tile ahead: its first key, which
+      // groups of 16 tokens are there, the powers of two of its scores and values
+      int key0 = 0;
+      unsigned there = 0;
+      float rt = rs, vt = 1.0f;
+      const auto look = [&](int j) {
+        key0 = (g.ub + (g.both ? j : 2 * j + x)) * KT;
         int pg = -1;
         if (lane < KT / 16 && key0 + 16 * lane < g.n) pg = __ldg(table + ((key0 + 16 * lane) >> a.page_log2));
         if ((unsigned)pg >= (unsigned)a.n_pages) pg = -1;
-        const unsigned there = __ballot_sync(FULL, pg >= 0);
-        const bool whole = __all_sync(FULL, key0 + KT <= vis) && there == (1u << (KT / 16)) - 1;
-        float rt = rs, vt = 1.0f;  // what the scores and the values are multiplied with
-        if constexpr (Q8) {
-          rt = rs / scale_shift<D>(a, a.ks, pg, key0, g.n, g.kvh);
-          vt = 1.0f / scale_shift<D>(a, a.vs, pg, key0, g.n, g.kvh);
+        there = __ballot_sync(FULL, pg >= 0);
+        if constexpr (Q8) {  // reciprocals of powers of two
+          bool in;
+          const uint4 ks = tile_scales<D>(a, (const uint16_t*)a.ks, pg, key0, g.kvh, in);
+          const uint4 vs = tile_scales<D>(a, (const uint16_t*)a.vs, pg, key0, g.kvh, in);
+          rt = rs * __frcp_rn(scale_shift<D>(in, ks, g.n - key0));
+          vt = __frcp_rn(scale_shift<D>(in, vs, g.n - key0));
         }
+      };
+      if (cnt > 0) look(0);
+      for (int j = 0; j < cnt; ++j, ++nt) {
+        const bool whole = __all_sync(FULL, key0 + KT <= vis) && there == (1u << (KT / 16)) - 1;
+        const float vt_now = vt;
         ok = __all_sync(FULL, wait(b_s + 8 * x, nt));
         if (!ok) break;
         tm_after();
@@ -491,24 +548,30 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
         float mx = -INFINITY, sum = 0.0f, al, ref;
         const auto weights = [&](auto cut) {
           constexpr bool CUT = decltype(cut)::value;
+          if constexpr (Q8) {
 #pragma unroll 1
-          for (int c = 0; c < KT / 32; ++c) {
-            unsigned r[32];
-            tm_ld32(ts + 32 * c, r);
-            if constexpr (Q8) {
-              unsigned r2[32];
-              tm_ld32(ts + 64 + 32 * c, r2);
+            for (int c = 0; c < KT / 16; ++c) {
+              unsigned r[16], r2[16];
+              tm_ld16(ts + 16 * c, r);
+              tm_ld16(ts + 64 + 16 * c, r2);
+              tm_ld_wait(r);
               tm_ld_wait(r2);
-              tm_ld_wait(r);
+              const int left = !CUT ? 16 : (there >> c) & 1u ? vis - key0 - 16 * c : 0;
 #pragma unroll
-              for (int k = 0; k < 32; ++k) r[k] = __float_as_uint(__uint_as_float(r[k]) + __uint_as_float(r2[k]));
-            } else {
-              tm_ld_wait(r);
+              for (int k = 0; k < 16; ++k)
+                if (!CUT || k < left) mx = fmaxf(mx, __uint_as_float(r[k]) + __uint_as_float(r2[k]));
             }
-            const int left = CUT ? vis - key0 - 32 * c : 32;
+          } else {
+#pragma unroll 1
+            for (int c = 0; c < KT / 32; ++c) {
+              unsigned r[32];
+              tm_ld32(ts + 32 * c, r);
+              tm_ld_wait(r);
+              const int left = CUT ? vis - key0 - 32 * c : 32;
 #pragma unroll
-            for (int k = 0; k < 32; ++k)
-              if (!CUT || (k < left && ((there >> (2 * c + (k >> 4))) & 1u))) mx = fmaxf(mx, __uint_as_float(r[k]));
+              for (int k = 0; k < 32; ++k)
+                if (!CUT || (k < left && ((there >> (2 * c + (k >> 4))) & 1u))) mx = fmaxf(mx, __uint_as_float(r[k]));
+            }
           }
           const float mn = fmaxf(m, mx * rt);
           ref = mn == -INFINITY ? 0.0f : mn;
@@ -559,6 +622,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
         tm_st_wait();
         tm_before();
         bar_arrive(b_p + 8 * x);
+        if (j + 1 < cnt) look(j + 1);
         ok = __all_sync(FULL, wait(b_o + 8 * x, nt));
         if (!ok) break;
         tm_after();
@@ -569,7 +633,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
           tm_ld_wait(r);
 #pragma unroll
           for (int k = 0; k < 32; ++k)
-            O[32 * c + k] = fmaf(O[32 * c + k], al, Q8 ? __uint_as_float(r[k]) * vt : __uint_as_float(r[k]));
+            O[32 * c + k] = fmaf(O[32 * c + k], al, Q8 ? __uint_as_float(r[k]) * vt_now : __uint_as_float(r[k]));
         }
         tm_before();
       }
@@ -578,21 +642,27 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
       // is done), then one bulk store
       const int which = pre ? 1 : 0, sr = tile_slot_rows(rows_of(a, g.s)), row0 = x * (g.both ? 128 : g.rows);
       const long at = (long)g.slot * sr + row0;
-      if (me < nr) {
+      if (me < nr) __stcg((float2*)(a.tml[which] + (at + me) * 2), make_float2(m, l));
+      if constexpr (Q8) {  // the queries' place is the other stream's too: each row by its thread
+        if (me < nr)
 #pragma unroll
-        for (int c = 0; c < D / 4; ++c)
-          asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(qs + me * (D * 4) + ((c ^ (me & 7)) << 4)),
-                       "f"(O[4 * c]), "f"(O[4 * c + 1]), "f"(O[4 * c + 2]), "f"(O[4 * c + 3])
+          for (int c = 0; c < D / 8; ++c) stg256(a.to[which] + (at + me) * D + 8 * c, O + 8 * c);
+      } else {
+        if (me < nr)
+#pragma unroll
+          for (int c = 0; c < D / 4; ++c)
+            asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(qs + me * (D * 4) + ((c ^ (me & 7)) << 4)),
+                         "f"(O[4 * c]), "f"(O[4 * c + 1]), "f"(O[4 * c + 2]), "f"(O[4 * c + 3])
+                         : "memory");
+        fence_async();
+        ok = meet();
+        if (!ok) break;
+        if (me == 0) {
+          asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(a.to[which] + at * D), "r"(qs),
+                       "r"(nr * D * 4)
                        : "memory");
-        __stcg((float2*)(a.tml[which] + (at + me) * 2), make_float2(m, l));
-      }
-      fence_async();
-      group_sync(x);
-      if (me == 0) {
-        asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(a.to[which] + at * D), "r"(qs),
-                     "r"(nr * D * 4)
-                     : "memory");
-        asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+          asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+        }
       }
       stored = true;
     }
