@@ -268,6 +268,10 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
           return true;
         };
         ok = __all_sync(FULL, wait(b_q, seg)) && qk(0, 0) && __all_sync(FULL, wait(b_q + 8, seg)) && (!cnt1 || qk(1, 0));
+        // a stream without a tile is told all the same: it must not run ahead and
+        // complete a second phase of its queries' barrier
+        if (!cnt1 && el) mma_commit(b_s + 8);
+        __syncwarp();
         for (int i = 0; i < 2 * cnt0 && ok; ++i) {
           const int x = i & 1, j = i >> 1, cnt = x ? cnt1 : cnt0;
           if (j < cnt) ok = pv(x, j);
@@ -432,7 +436,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
     const unsigned ts = tw + x * 128, to = tw + 256 + x * 128;
     const unsigned qs = base + x * C::QX;
     constexpr float UP = weight_shift(TYPE);
-    unsigned nt = 0;  // tiles so far
+    unsigned ns = 0, no = 0;  // score and output tiles so far
     bool ok = true, stored = false;
     // the threads of the stream (Q8: of both) meet; a bounded wait as every other
     unsigned met = 0;
@@ -537,10 +541,11 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
         }
       };
       if (cnt > 0) look(0);
-      for (int j = 0; j < cnt; ++j, ++nt) {
+      if (cnt == 0) ok = __all_sync(FULL, wait(b_s + 8 * x, ns++));
+      for (int j = 0; j < cnt; ++j) {
         const bool whole = __all_sync(FULL, key0 + KT <= vis) && there == (1u << (KT / 16)) - 1;
         const float vt_now = vt;
-        ok = __all_sync(FULL, wait(b_s + 8 * x, nt));
+        ok = __all_sync(FULL, wait(b_s + 8 * x, ns++));
         if (!ok) break;
         tm_after();
         // the scores' maximum, then the weights in their place; CUT: some keys
@@ -623,7 +628,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
         tm_before();
         bar_arrive(b_p + 8 * x);
         if (j + 1 < cnt) look(j + 1);
-        ok = __all_sync(FULL, wait(b_o + 8 * x, nt));
+        ok = __all_sync(FULL, wait(b_o + 8 * x, no++));
         if (!ok) break;
         tm_after();
 #pragma unroll

@@ -339,6 +339,17 @@ def test_attn_several_new_tokens(type_, R, lens):
 
 
 @pytest.mark.parametrize("type_", list(TYPES))
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("n_q", [32, 72])
+def test_attn_many_pieces_to_a_block(type_, D, n_q):
+    """Several new tokens of sequences from one tile to many, so that a block
+    has the end of one, whole ones of a single tile and the start of another."""
+    lens = [30, 700, 5, 64, 128, 2000, 129, 90, 65, 10, 300, 127]
+    run_attn(type_, D, n_q, 8, 32, 5, lens)
+    run_attn(type_, D, n_q, 8, 32, 5, lens, prefix=200)
+
+
+@pytest.mark.parametrize("type_", list(TYPES))
 def test_attn_long_ragged_batch(type_):
     """One long context among short ones and padding: split over the blocks."""
     out, want = run_attn(type_, 128, 32, 8, 64, 1, [20000, 1, 0, 300, 4097, 64, -3, 2000])
