@@ -469,43 +469,46 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
           const int ri = r_first + me, tok = ri / a.G;
           off = (pre ? tok : g.s * a.R + tok) * a.n_q + g.kvh * a.G + (ri - tok * a.G);
         }
-        float v[32][D / 32];
+        float v[16][D / 32];
+#pragma unroll 1
+        for (int i0 = 0; i0 < 32; i0 += 16) {
 #pragma unroll
-        for (int i = 0; i < 32; ++i) {
-          const int at = __shfl_sync(FULL, off, i);
-          const float* q = a.q + (long)at * D + lane * (D / 32);
-          float4 f = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-          if (at >= 0) {
-            if constexpr (D == 128) f = __ldcg((const float4*)q);
-            else *(float2*)&f = __ldcg((const float2*)q);
+          for (int i = 0; i < 16; ++i) {
+            const int at = __shfl_sync(FULL, off, i0 + i);
+            const float* q = a.q + (long)at * D + lane * (D / 32);
+            float4 f = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            if (at >= 0) {
+              if constexpr (D == 128) f = __ldcg((const float4*)q);
+              else *(float2*)&f = __ldcg((const float2*)q);
+            }
+            v[i][0] = f.x, v[i][1] = f.y;
+            if constexpr (D == 128) v[i][2] = f.z, v[i][3] = f.w;
           }
-          v[i][0] = f.x, v[i][1] = f.y;
-          if constexpr (D == 128) v[i][2] = f.z, v[i][3] = f.w;
-        }
 #pragma unroll
-        for (int i = 0; i < 32; ++i) {
-          float am = 0.0f;
+          for (int i = 0; i < 16; ++i) {
+            float am = 0.0f;
 #pragma unroll
-          for (int c = 0; c < D / 32; ++c) v[i][c] *= a.qscale, am = fmaxf(am, fabsf(v[i][c]));
-          if constexpr (!BF) {
-            float back;
-            const float up = row_shift(warp_absmax(am), back);
-            if (lane == i) rs = back;
+            for (int c = 0; c < D / 32; ++c) v[i][c] *= a.qscale, am = fmaxf(am, fabsf(v[i][c]));
+            if constexpr (!BF) {
+              float back;
+              const float up = row_shift(warp_absmax(am), back);
+              if (lane == i0 + i) rs = back;
 #pragma unroll
-            for (int c = 0; c < D / 32; ++c) v[i][c] *= up;
-          }
-          // values lane * D/32 ...: 16-byte piece and place in it
-          const int lr = 32 * wq + i, d0 = lane * (D / 32), piece = (d0 & 63) >> 3;
-          const unsigned at = qs + (d0 >> 6) * C::HALF + lr * 128 + ((piece ^ (lr & 7)) << 4) + (d0 & 7) * 2;
+              for (int c = 0; c < D / 32; ++c) v[i][c] *= up;
+            }
+            // values lane * D/32 ...: 16-byte piece and place in it
+            const int lr = 32 * wq + i0 + i, d0 = lane * (D / 32), piece = (d0 & 63) >> 3;
+            const unsigned at = qs + (d0 >> 6) * C::HALF + lr * 128 + ((piece ^ (lr & 7)) << 4) + (d0 & 7) * 2;
 #pragma unroll
-          for (int term = 0; term < 2; ++term) {
-            if (Q8 && x == 1) break;  // stream 0 writes the queries of both
-            const unsigned w0 = split2<BF>(v[i][0], v[i][1]);
-            if constexpr (D == 128) {
-              const unsigned w1 = split2<BF>(v[i][2], v[i][3]);
-              asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(at + term * C::BUF), "r"(w0), "r"(w1) : "memory");
-            } else {
-              asm volatile("st.shared.u32 [%0], %1;" ::"r"(at + term * C::BUF), "r"(w0) : "memory");
+            for (int term = 0; term < 2; ++term) {
+              if (Q8 && x == 1) break;  // stream 0 writes the queries of both
+              const unsigned w0 = split2<BF>(v[i][0], v[i][1]);
+              if constexpr (D == 128) {
+                const unsigned w1 = split2<BF>(v[i][2], v[i][3]);
+                asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(at + term * C::BUF), "r"(w0), "r"(w1) : "memory");
+              } else {
+                asm volatile("st.shared.u32 [%0], %1;" ::"r"(at + term * C::BUF), "r"(w0) : "memory");
+              }
             }
           }
         }
@@ -548,81 +551,94 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
         ok = __all_sync(FULL, wait(b_s + 8 * x, ns++));
         if (!ok) break;
         tm_after();
-        // the scores' maximum, then the weights in their place; CUT: some keys
-        // are absent or not seen by some row
-        float mx = -INFINITY, sum = 0.0f, al, ref;
-        const auto weights = [&](auto cut) {
-          constexpr bool CUT = decltype(cut)::value;
-          if constexpr (Q8) {
+        // The scores' maximum; where some keys are absent or not seen by some row,
+        // their scores become -inf on the way.  (Rolled loops: a block runs this
+        // code a dozen times, and what is not in the instruction cache yet costs
+        // the first tile as much as two later ones.)
+        float mx = -INFINITY;
+        if (whole) {
 #pragma unroll 1
-            for (int c = 0; c < KT / 16; ++c) {
-              unsigned r[16], r2[16];
-              tm_ld16(ts + 16 * c, r);
-              tm_ld16(ts + 64 + 16 * c, r2);
-              tm_ld_wait(r);
-              tm_ld_wait(r2);
-              const int left = !CUT ? 16 : (there >> c) & 1u ? vis - key0 - 16 * c : 0;
+          for (int c = 0; c < KT / 32; ++c) {
+            unsigned r[32];
+            tm_ld32(ts + 32 * c, r);
+            if constexpr (Q8) {
+              unsigned r2[16];
 #pragma unroll
-              for (int k = 0; k < 16; ++k)
-                if (!CUT || k < left) mx = fmaxf(mx, __uint_as_float(r[k]) + __uint_as_float(r2[k]));
-            }
-          } else {
-#pragma unroll 1
-            for (int c = 0; c < KT / 32; ++c) {
-              unsigned r[32];
-              tm_ld32(ts + 32 * c, r);
-              tm_ld_wait(r);
-              const int left = CUT ? vis - key0 - 32 * c : 32;
+              for (int h = 0; h < 2; ++h) {
+                tm_ld16(ts + 64 + 32 * c + 16 * h, r2);
+                tm_ld_wait(r2);
+                if (h == 0) tm_ld_wait(r);
 #pragma unroll
-              for (int k = 0; k < 32; ++k)
-                if (!CUT || (k < left && ((there >> (2 * c + (k >> 4))) & 1u))) mx = fmaxf(mx, __uint_as_float(r[k]));
+                for (int k = 0; k < 16; ++k) mx = fmaxf(mx, __uint_as_float(r[16 * h + k]) + __uint_as_float(r2[k]));
+              }
+            } else {
+              tm_ld_wait(r);
+#pragma unroll
+              for (int k = 0; k < 32; ++k) mx = fmaxf(mx, __uint_as_float(r[k]));
             }
           }
-          const float mn = fmaxf(m, mx * rt);
-          ref = mn == -INFINITY ? 0.0f : mn;
-          al = ex2(m - ref);
-          m = mn;
-          const float shift = UP - ref;
-          unsigned r[2][16];
-          const auto scores = [&](int c, unsigned(&y)[16]) {
-            tm_ld16(ts + 16 * c, y);
-            if constexpr (Q8) {
-              unsigned y2[16];
-              tm_ld16(ts + 64 + 16 * c, y2);
-              tm_ld_wait(y2);
-              tm_ld_wait(y);
-#pragma unroll
-              for (int k = 0; k < 16; ++k) y[k] = __float_as_uint(__uint_as_float(y[k]) + __uint_as_float(y2[k]));
-            }
-          };
-          scores(0, r[0]);
-          if constexpr (!Q8) tm_ld_wait(r[0]);
-#pragma unroll
+        } else {
+#pragma unroll 1
           for (int c = 0; c < KT / 16; ++c) {
-            unsigned(&y)[16] = r[c & 1];
-            if (c + 1 < KT / 16) scores(c + 1, r[(c + 1) & 1]);
-            const int left = !CUT ? 16 : (there >> c) & 1u ? vis - key0 - 16 * c : 0;
-            float s0 = 0.0f, s1 = 0.0f;
-            unsigned w[16];
+            unsigned r[16], r2[16];
+            tm_ld16(ts + 16 * c, r);
+            if constexpr (Q8) tm_ld16(ts + 64 + 16 * c, r2);
+            tm_ld_wait(r);
+            if constexpr (Q8) tm_ld_wait(r2);
+            const int left = (there >> c) & 1u ? vis - key0 - 16 * c : 0;
 #pragma unroll
-            for (int k = 0; k < 16; k += 2) {
-              float p0 = ex2(fmaf(__uint_as_float(y[k]), rt, shift));
-              float p1 = ex2(fmaf(__uint_as_float(y[k + 1]), rt, shift));
-              if constexpr (CUT) {
-                p0 = k < left ? p0 : 0.0f;
-                p1 = k + 1 < left ? p1 : 0.0f;
-              }
-              s0 += p0, s1 += p1;
-              w[k >> 1] = split2<BF>(p0, p1);
-              w[8 + (k >> 1)] = split2<BF>(p0, p1);
+            for (int k = 0; k < 16; ++k) {
+              if (k >= left) r[k] = 0xff800000u;
+              mx = fmaxf(mx, Q8 ? __uint_as_float(r[k]) + __uint_as_float(r2[k]) : __uint_as_float(r[k]));
             }
-            sum += s0 + s1;
-            if (!Q8 && c + 1 < KT / 16) tm_ld_wait(r[(c + 1) & 1]);
-            tm_st16(ts + 16 * c, w);
+            tm_st16(ts + 16 * c, r);
+          }
+          tm_st_wait();
+        }
+        const float mn = fmaxf(m, mx * rt);
+        const float ref = mn == -INFINITY ? 0.0f : mn, al = ex2(m - ref), shift = UP - ref;
+        m = mn;
+        // the weights in their place, 16 keys at a time, the next 16 on their way
+        float sum = 0.0f;
+        const auto scores = [&](int c, unsigned(&y)[16]) {
+          tm_ld16(ts + 16 * c, y);
+          if constexpr (Q8) {
+            unsigned y2[16];
+            tm_ld16(ts + 64 + 16 * c, y2);
+            tm_ld_wait(y2);
+            tm_ld_wait(y);
+#pragma unroll
+            for (int k = 0; k < 16; ++k) y[k] = __float_as_uint(__uint_as_float(y[k]) + __uint_as_float(y2[k]));
           }
         };
-        if (whole) weights(std::false_type{});
-        else weights(std::true_type{});
+        const auto weights = [&](int c, const unsigned(&y)[16]) {
+          float s0 = 0.0f, s1 = 0.0f;
+          unsigned w[16];
+#pragma unroll
+          for (int k = 0; k < 16; k += 2) {
+            float p0 = ex2(fmaf(__uint_as_float(y[k]), rt, shift));
+            float p1 = ex2(fmaf(__uint_as_float(y[k + 1]), rt, shift));
+            s0 += p0, s1 += p1;
+            w[k >> 1] = split2<BF>(p0, p1);
+            w[8 + (k >> 1)] = split2<BF>(p0, p1);
+          }
+          sum += s0 + s1;
+          tm_st16(ts + 16 * c, w);
+        };
+        {
+          unsigned ya[16], yb[16];
+          scores(0, ya);
+          if constexpr (!Q8) tm_ld_wait(ya);
+#pragma unroll 1
+          for (int c = 0; c < KT / 16; c += 2) {
+            scores(c + 1, yb);
+            weights(c, ya);
+            if constexpr (!Q8) tm_ld_wait(yb);
+            if (c + 2 < KT / 16) scores(c + 2, ya);
+            weights(c + 1, yb);
+            if constexpr (!Q8) tm_ld_wait(ya);
+          }
+        }
         l = fmaf(l, al, sum);
         tm_st_wait();
         tm_before();
