@@ -103,7 +103,7 @@ __device__ __forceinline__ Cursor cursor_at(const AttnArgs& a, const Deal& d, lo
   c.un = d.un[c.s];
   c.n = d.n[c.s];
   const long rel = unit - d.cum[c.s];
-  const int li = (int)(rel / c.un);
+  const int li = (int)quot(rel, c.un);
   c.u = (int)(rel - (long)li * c.un);
   c.tiles = groups_of<false>(a, c.s);
   c.kvh = li / c.tiles;
@@ -156,10 +156,10 @@ __global__ void __launch_bounds__(32 * Cfg<TYPE, D>::NW, 1) attn_kernel(const __
   const int lane = threadIdx.x & 31, warp = __shfl_sync(FULL, threadIdx.x >> 5, 0), g = lane >> 2, t = lane & 3;
   const long T = deal.cum[a.B + a.shared], W = stream_blocks(a.W, C::NW, T);
   if (blockIdx.x >= W) return;
-  const long ca = T * blockIdx.x / W;
-  const int cn = (int)(T * (blockIdx.x + 1) / W - ca), we = min(C::NW, cn);
-  const int wa = warp < we ? (int)((long)cn * warp / we) : cn;
-  int left = (warp < we ? (int)((long)cn * (warp + 1) / we) : cn) - wa;  // units the warp has to do
+  const long ca = quot(T * blockIdx.x, (int)W);
+  const int cn = (int)(quot(T * (blockIdx.x + 1), (int)W) - ca), we = min(C::NW, cn);
+  const int wa = warp < we ? (int)quot((long)cn * warp, we) : cn;
+  int left = (warp < we ? (int)quot((long)cn * (warp + 1), we) : cn) - wa;  // units the warp has to do
   Cursor cc = cursor_at(a, deal, ca);
   const bool one = cc.u + cn <= cc.un;  // the block's units are all one item's: its warps join their parts
   if (one) cc.u += wa;
@@ -602,6 +602,12 @@ struct Source {
   }
 };
 
+// The block with unit u: the last c with T * c / W <= u.
+__device__ __forceinline__ int holder(long u, long W, long T) {
+  const long a = (u + 1) * W - 1;
+  return ((a | T) >> 31) == 0 ? (int)a / (int)T : (int)(a / T);
+}
+
 // Row i of key/value head kvh in sequence s of the streaming deal.
 __device__ __forceinline__ Source stream_source(const AttnArgs& a, const Deal& d, int s, int kvh, int i) {
   Source r = {};
@@ -610,11 +616,10 @@ __device__ __forceinline__ Source stream_source(const AttnArgs& a, const Deal& d
   const long T = d.cum[a.B + a.shared], W = stream_blocks(a.W, a.NW, T);
   const int tile = i / TR, li = kvh * groups_of<false>(a, s) + tile, item = item0<false>(a, s) + li;
   const long ib = d.cum[s] + (long)li * un, ie = ib + un;  // the item's units
-  // the last c with T * c / W <= u has unit u
-  const int c0 = (int)(((ib + 1) * W - 1) / T), c1 = (int)((ie * W - 1) / T);
+  const int c0 = holder(ib, W, T), c1 = holder(ie - 1, W, T);
   // entries of block c: one if it has nothing else, else one of each warp with units of the item
   const auto part = [&](int c, long& at, int& n) {
-    const long ca = T * c / W, cb = T * (c + 1) / W;
+    const long ca = quot(T * c, (int)W), cb = quot(T * (c + 1), (int)W);
     int w0 = 0, w1 = 0;
     if (ca < ib || cb > ie) {
       const int cn = (int)(cb - ca), we = min(a.NW, cn);
@@ -646,7 +651,7 @@ __device__ __forceinline__ Source tile_source(const AttnArgs& a, const Deal& d, 
   const long T = d.cum[a.B + a.shared], W = shares(a.TW, T);
   const int group = i / a.trows, li = kvh * groups_of<true>(a, s) + group, ig = i - group * a.trows;
   const long ub = d.cum[s] + (long)li * un;
-  const int w0 = (int)(((ub + 1) * W - 1) / T), w1 = (int)(((ub + un) * W - 1) / T);
+  const int w0 = holder(ub, W, T), w1 = holder(ub + un - 1, W, T);
   const int rows = rows_of(a, s), rg = min(a.trows, rows - group * a.trows), which = s == a.B ? 1 : 0;
   r.step = tile_slot_rows(rows);
   r.mid = (long)(w0 + item0<true>(a, s) + li) * r.step + ig;

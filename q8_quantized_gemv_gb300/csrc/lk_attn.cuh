@@ -171,6 +171,29 @@ __device__ __forceinline__ unsigned split2(float& x, float& y) {
     return *(const unsigned*)&h;
   }
 }
+// The rounded pair as two f32.
+template <bool BF>
+__device__ __forceinline__ lk::f32x2 widen2(unsigned h) {
+  if constexpr (BF) return lk::f2_pack(__uint_as_float(h << 16), __uint_as_float(h & 0xffff0000u));
+  const __half2 v = *(const __half2*)&h;
+  return lk::f2_pack(__low2float(v), __high2float(v));
+}
+template <bool BF>
+__device__ __forceinline__ unsigned round2(float x, float y) {
+  if constexpr (BF) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
+    return *(const unsigned*)&h;
+  }
+  const __half2 h = __floats2half2_rn(x, y);
+  return *(const unsigned*)&h;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+// a / b; a 64-bit division only where a needs one
+__device__ __forceinline__ long quot(long a, int b) { return (a >> 31) == 0 ? (long)((int)a / b) : a / b; }
 // 16 bytes global -> shared; with bytes 0 nothing is read and zeros are written
 __device__ __forceinline__ void cp16(unsigned dst, const void* src, int bytes) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");

@@ -72,7 +72,7 @@ __device__ __forceinline__ Segment next_segment(const AttnArgs& a, const Deal& d
   while (d.cum[s + 1] <= u0) ++s;
   const int un = d.un[s], groups = groups_of<true>(a, s);
   const long rel = u0 - d.cum[s];
-  const int li = (int)(rel / un);
+  const int li = (int)quot(rel, un);
   g.s = s;
   g.n = d.n[s];
   g.ub = (int)(rel - (long)li * un);
@@ -193,7 +193,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
   const unsigned tmem = __shfl_sync(FULL, *(volatile unsigned*)&tmem_slot, 0);
   const long T = deal.cum[a.B + a.shared], W = shares(a.TW, T);
   long u0 = 0, u1 = 0;
-  if (blockIdx.x < W) u0 = T * blockIdx.x / W, u1 = T * (blockIdx.x + 1) / W;
+  if (blockIdx.x < W) u0 = quot(T * blockIdx.x, (int)W), u1 = quot(T * (blockIdx.x + 1), (int)W);
   int s = 0;
   auto wait = [&](unsigned bar, unsigned parity) -> bool {
     if (bar_wait(bar, parity & 1u, a.wait_ns, &abort_flag)) return true;
@@ -547,7 +547,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
       if (cnt == 0) ok = __all_sync(FULL, wait(b_s + 8 * x, ns++));
       for (int j = 0; j < cnt; ++j) {
         const bool whole = __all_sync(FULL, key0 + KT <= vis) && there == (1u << (KT / 16)) - 1;
-        const float vt_now = vt;
+        const f32x2 vt2 = f2_pack(vt, vt);
         ok = __all_sync(FULL, wait(b_s + 8 * x, ns++));
         if (!ok) break;
         tm_after();
@@ -555,7 +555,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
         // their scores become -inf on the way.  (Rolled loops: a block runs this
         // code a dozen times, and what is not in the instruction cache yet costs
         // the first tile as much as two later ones.)
-        float mx = -INFINITY;
+        float mx = -INFINITY, mx1 = -INFINITY;
         if (whole) {
 #pragma unroll 1
           for (int c = 0; c < KT / 32; ++c) {
@@ -574,7 +574,10 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
             } else {
               tm_ld_wait(r);
 #pragma unroll
-              for (int k = 0; k < 32; ++k) mx = fmaxf(mx, __uint_as_float(r[k]));
+              for (int k = 0; k < 32; k += 4) {
+                mx = max3(mx, __uint_as_float(r[k]), __uint_as_float(r[k + 1]));
+                mx1 = max3(mx1, __uint_as_float(r[k + 2]), __uint_as_float(r[k + 3]));
+              }
             }
           }
         } else {
@@ -595,11 +598,13 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
           }
           tm_st_wait();
         }
-        const float mn = fmaxf(m, mx * rt);
+        const float mn = fmaxf(m, fmaxf(mx, mx1) * rt);
         const float ref = mn == -INFINITY ? 0.0f : mn, al = ex2(m - ref), shift = UP - ref;
         m = mn;
+        const f32x2 al2 = f2_pack(al, al);
         // the weights in their place, 16 keys at a time, the next 16 on their way
-        float sum = 0.0f;
+        f32x2 sum2[2] = {f2_pack(0.0f, 0.0f), f2_pack(0.0f, 0.0f)};
+        const f32x2 rt2 = f2_pack(rt, rt), shift2 = f2_pack(shift, shift), minus1 = f2_pack(-1.0f, -1.0f);
         const auto scores = [&](int c, unsigned(&y)[16]) {
           tm_ld16(ts + 16 * c, y);
           if constexpr (Q8) {
@@ -612,17 +617,19 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
           }
         };
         const auto weights = [&](int c, const unsigned(&y)[16]) {
-          float s0 = 0.0f, s1 = 0.0f;
           unsigned w[16];
 #pragma unroll
           for (int k = 0; k < 16; k += 2) {
-            float p0 = ex2(fmaf(__uint_as_float(y[k]), rt, shift));
-            float p1 = ex2(fmaf(__uint_as_float(y[k + 1]), rt, shift));
-            s0 += p0, s1 += p1;
-            w[k >> 1] = split2<BF>(p0, p1);
-            w[8 + (k >> 1)] = split2<BF>(p0, p1);
+            // pairs: one instruction for both halves
+            float x0, x1;
+            f2_unpack(f2_fma(f2_pack(__uint_as_float(y[k]), __uint_as_float(y[k + 1])), rt2, shift2), x0, x1);
+            x0 = ex2(x0), x1 = ex2(x1);
+            const f32x2 p = f2_pack(x0, x1);
+            sum2[(k >> 1) & 1] = f2_add(sum2[(k >> 1) & 1], p);
+            w[k >> 1] = round2<BF>(x0, x1);
+            f2_unpack(f2_fma(widen2<BF>(w[k >> 1]), minus1, p), x0, x1);
+            w[8 + (k >> 1)] = round2<BF>(x0, x1);
           }
-          sum += s0 + s1;
           tm_st16(ts + 16 * c, w);
         };
         {
@@ -639,7 +646,9 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
             if constexpr (!Q8) tm_ld_wait(ya);
           }
         }
-        l = fmaf(l, al, sum);
+        float sum0, sum1;
+        f2_unpack(f2_add(sum2[0], sum2[1]), sum0, sum1);
+        l = fmaf(l, al, sum0 + sum1);
         tm_st_wait();
         tm_before();
         bar_arrive(b_p + 8 * x);
@@ -653,8 +662,11 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
           tm_ld32(to + 32 * c, r);
           tm_ld_wait(r);
 #pragma unroll
-          for (int k = 0; k < 32; ++k)
-            O[32 * c + k] = fmaf(O[32 * c + k], al, Q8 ? __uint_as_float(r[k]) * vt_now : __uint_as_float(r[k]));
+          for (int k = 0; k < 32; k += 2) {
+            f32x2 z = f2_pack(__uint_as_float(r[k]), __uint_as_float(r[k + 1]));
+            if constexpr (Q8) z = f2_mul(z, vt2);
+            f2_unpack(f2_fma(f2_pack(O[32 * c + k], O[32 * c + k + 1]), al2, z), O[32 * c + k], O[32 * c + k + 1]);
+          }
         }
         tm_before();
       }
