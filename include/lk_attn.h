@@ -17,7 +17,7 @@
  *
  * The cache.  k and v are pages of `page` tokens:
  *     [n_pages][n_kv][page][head_dim]
- * of f16, bf16 or int8 levels; LK_KV_Q8 holds one f16 scale per 32 values of
+ * of f16, bf16 or int8 levels (n_pages * n_kv * page < 2^31); LK_KV_Q8 holds one f16 scale per 32 values of
  * a token's head in ks, vs [n_pages][n_kv][page][head_dim/32] (NULL for the
  * other types), the value being scale * level.  k, v, ks and vs are 16-byte
  * aligned; head_dim is 64 or 128; page a power of two, 16 .. 1024.  Token j of
@@ -91,12 +91,15 @@ lk_status lk_kv_append(const lk_kv_cache* cache, const float* q, const float* k,
  * n = min(lens[b] - R + 1 + r, table_w * page) tokens of sequence b (itself
  * and what came before it), absent tokens excepted:
  *   out = sum_j p_j v_j / sum_j p_j,  p_j = exp(scale * q.k_j - max)
- * and zeros where it sees none.  Sums and statistics are f32; keys and
- * values enter exactly as stored, queries and weights as sums of two 16-bit
- * terms (three for queries against bf16 keys), so out is within about 2^-16 of
- * the exact value relative to sum_j p_j |v_j| / sum_j p_j, plus the effect of
- * an error of 2^-20 * scale * sum_i |q_i k_ji| in the scores.  The result does
- * not depend on timing: the same call gives the same bits.
+ * and zeros where it sees none.  Sums and statistics are f32.  Keys and values
+ * enter as stored (Q8 under many rows: as two f16 terms, to 2^-22), queries and
+ * weights as two 16-bit terms of the cache's type (Q8: f16).  With W = sum_j p_j
+ * |v_j| / sum_j p_j and A the largest scale * sum_i |q_i k_ji| of the row, out is
+ * within (2^-15 + c A) W of the exact value, c = 2^-17 (f16, Q8) or 2^-14 (bf16),
+ * plus (2^-27 + N 2^-32) max|v| over its N tokens; on the whole far nearer (about
+ * 2^-20 of its norm).  The result does not depend on timing: the same call gives
+ * the same bits.  The same row may differ in its last bits between calls of
+ * other B, R or lens (the keys are split between blocks by all of them).
  *   q     f32 [M][n_q*head_dim], 16-byte aligned
  *   mode, out, hq, hl, hs   the result for the next projection, as
  *         lk_swiglu_quant gives it: out f32 [M][n_q*head_dim] (required under
@@ -131,6 +134,12 @@ lk_status lk_attn_shared(const lk_kv_cache* cache, const float* q, int n_q, cons
 /* Bytes of the workspace of lk_attn (shared 0) or lk_attn_shared (shared 1);
  * 0 for arguments those calls refuse. */
 size_t lk_attn_workspace_bytes(int n_q, int n_kv, int head_dim, int B, int R, int shared);
+
+/* Kernels that such a call launches (lk_attn: prefix_len 0): the streaming
+ * kernel (up to 8 query rows on each read of the keys) and / or the tile kernel
+ * (tcgen05, up to 256; chosen by rows, type and prefix length), and the join of
+ * their partial results.  0 for arguments the calls refuse and for no rows. */
+int lk_attn_launches(int type, int n_q, int n_kv, int head_dim, int B, int R, int prefix_len);
 
 #ifdef __cplusplus
 }

@@ -683,22 +683,22 @@ __global__ void __launch_bounds__(128) attn_join_kernel(const JoinArgs j) {
   }
   const int row = (int)(w / a.n_q), h = (int)(w - (long)row * a.n_q), kvh = h / a.G, hg = h - kvh * a.G;
   const int b = row / a.R, r = row - b * a.R;
-  // the row's own item, then its prefix item
-  Source src[2] = {};
-  const int io = r * a.G + hg, ip = row * a.G + hg;
-  src[0] = a.own_tiled ? tile_source(a, tdeal, b, kvh, io) : stream_source(a, deal, b, kvh, io);
-  if (a.shared && __ldcg(a.lens + b) >= 0)
-    src[1] = a.pre_tiled ? tile_source(a, tdeal, a.B, kvh, ip) : stream_source(a, deal, a.B, kvh, ip);
-  asm volatile("griddepcontrol.wait;" ::: "memory");
   // A lane has V neighbouring values.  Partials come in batches of NB whose
   // loads are all in flight at once, the values' not waiting for the maxima's.
   constexpr int V = D / 32, NB = 8;
   float M = -INFINITY, acc[V], ls = 0.0f;
 #pragma unroll
   for (int c = 0; c < V; ++c) acc[c] = 0.0f;
+  // the row's own item, then its prefix item (a rolled loop: this code runs
+  // once, and what it takes to fetch it counts)
+  bool waited = false;
 #pragma unroll 1
   for (int x = 0; x < 2; ++x) {
-    const Source z = x ? src[1] : src[0];
+    if (x == 1 && (!a.shared || __ldcg(a.lens + b) < 0)) break;
+    const int s = x ? a.B : b, i = (x ? row : r) * a.G + hg;
+    const Source z = (x ? a.pre_tiled : a.own_tiled) ? tile_source(a, tdeal, s, kvh, i) : stream_source(a, deal, s, kvh, i);
+    if (!waited) asm volatile("griddepcontrol.wait;" ::: "memory");
+    waited = true;
     const int at = V == 4 ? (lane ^ z.flip) * 4 : ((lane >> 1) ^ z.flip) * 4 + (lane & 1) * 2;
 #pragma unroll 1
     for (int i0 = 0; i0 < z.n; i0 += NB) {
@@ -757,21 +757,37 @@ __global__ void __launch_bounds__(128) attn_join_kernel(const JoinArgs j) {
 }
 
 // ---- host --------------------------------------------------------------------------
-// Whether rows on the same keys go to the tile kernel.
-bool tiled(long rows, int type) { return rows > 16; }
+// Whether rows on the same keys go to the tile kernel.  The streaming kernel
+// reads the keys once per 8 rows (from L2), the tile kernel once, at a fixed
+// cost of some 10 us; a sequence's length is not known here, a prefix's is.
+// Measured (whole call, streaming / tile, us; 8 kv heads):
+//   sequences, f16 D 128: 24 rows 1 x 8000 21.6 / 21.3, 4 x 8000 51.9 / 39.6, 20
+//     rows 8 x 1000 20.7 / 21.5; 64 rows 1 x 8000 36.9 / 23.0, 1 x 1000 15.1 / 14.2
+//   Q8 D 128: 24 rows 4 x 8000 48.6 / 60.4, 36 rows 72.3 / 62.0, 64 rows 105 / 64
+//   prefix, f16 D 128: 96 rows 2000 25.6 / 26.7, 128 rows 29.8 / 27.1; 32 rows 8000
+//     28.2 / 29.8, 48 rows 35.8 / 30.9; 24 rows 32000 59.8 / 45.8
+//   D 64: 64 rows 8000 28.0 / 28.2; 24 rows 32000 37.5 / 36.4
+//   Q8 D 128: 256 rows 2000 42.9 / 41.5, 48 rows 8000 34.5 / 37.1, 64 rows 42.2 /
+//     37.2; D 64: 96 rows 8000 39.3 / 32.6, 64 rows 28.9 / 31.8
+bool tiled(long rows, int type, int D, long keys) {
+  const bool q8 = type == LK_KV_Q8;
+  if (rows <= (q8 ? 32 : 16)) return false;
+  return keys < 0 || rows * keys * D >= (q8 ? 1L << 26 : 1L << 25);
+}
 
 struct Plan {
   long slots, tslots[2];  // streaming partials; tile partials of sequences, prefix
   int tsr[2];             // rows of a tile slot
 };
 
-Plan plan(int n_q, int n_kv, int B, int R, int shared, int type) {
-  const long G = n_q / n_kv, rows[2] = {R * G, (long)B * R * G}, many[2] = {(long)B * n_kv, shared ? n_kv : 0};
+// type < 0: the most that any call of the sizes takes.
+Plan plan(int n_q, int n_kv, int B, int R, int type, int D, long prefix) {
+  const long G = n_q / n_kv, rows[2] = {R * G, (long)B * R * G}, many[2] = {(long)B * n_kv, prefix ? n_kv : 0};
   Plan p = {};
   p.slots = (long)kMaxWorkers * kMaxWarps;
   for (int x = 0; x < 2; ++x) {
     p.slots += many[x] * ((rows[x] + TR - 1) / TR);
-    if (!many[x] || !tiled(rows[x], type)) continue;
+    if (!many[x] || !(type < 0 ? rows[x] > 16 : tiled(rows[x], type, D, x ? prefix : -1))) continue;
     p.tsr[x] = tile_slot_rows(rows[x]);
     p.tslots[x] = kTileWorkers + many[x] * ((rows[x] + 127) / 128);  // items of 128 rows or of 256
   }
@@ -880,7 +896,15 @@ size_t lk_attn_workspace_bytes(int n_q, int n_kv, int head_dim, int B, int R, in
   if ((head_dim != 64 && head_dim != 128) || n_kv < 1 || n_q < n_kv || n_q % n_kv || n_q > 4096) return 0;
   if (B < 0 || R < 0 || B > LK_MAX_BATCH || R > LK_MAX_BATCH || B * R > LK_MAX_BATCH) return 0;
   size_t ml[3], o[3];
-  return layout(plan(n_q, n_kv, B, R, shared != 0, LK_KV_F16), head_dim, ml, o);  // of any type's the largest
+  return layout(plan(n_q, n_kv, B, R, -1, head_dim, shared != 0), head_dim, ml, o);
+}
+
+int lk_attn_launches(int type, int n_q, int n_kv, int head_dim, int B, int R, int prefix_len) {
+  if (type < LK_KV_F16 || type > LK_KV_Q8 || prefix_len < 0 || !lk_attn_workspace_bytes(n_q, n_kv, head_dim, B, R, 0)) return 0;
+  if (B == 0 || R == 0) return 0;
+  const Plan p = plan(n_q, n_kv, B, R, type, head_dim, prefix_len);
+  const bool tile = p.tslots[0] || p.tslots[1], stream = !p.tslots[0] || (prefix_len && !p.tslots[1]);
+  return 1 + tile + stream;
 }
 
 lk_status lk_attn_shared(const lk_kv_cache* cache, const float* q, int n_q, const int32_t* prefix_table,
@@ -927,7 +951,7 @@ lk_status lk_attn_shared(const lk_kv_cache* cache, const float* q, int n_q, cons
   a.plen = prefix_len;
   a.shared = shared;
   a.qscale = scale * 1.44269504088896340736f;
-  const Plan p = plan(n_q, cache->n_kv, B, R, shared, cache->type);
+  const Plan p = plan(n_q, cache->n_kv, B, R, cache->type, cache->head_dim, prefix_len);
   size_t ml[3], o[3];
   layout(p, cache->head_dim, ml, o);
   a.own_tiled = p.tslots[0] > 0;

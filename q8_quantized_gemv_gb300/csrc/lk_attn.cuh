@@ -129,30 +129,41 @@ __device__ __forceinline__ long stream_blocks(int W, int NW, long T) { return mi
 // By one whole warp; the caller synchronizes.
 template <bool TILED>
 __device__ __forceinline__ void make_deal(const AttnArgs& a, Deal& d) {
-  const int lane = threadIdx.x & 31, nseq = a.B + a.shared;
-  const int cap = a.table_w << a.page_log2;
-  long run = 0;
-  for (int s0 = 0; s0 < nseq; s0 += 32) {
-    const int s = s0 + lane;
-    long u = 0;
-    if (s < nseq) {
-      const int n = s == a.B ? a.plen : min(max(__ldcg(a.lens + s), 0), cap);
-      const int U = TILED ? a.tunit : UNIT;
-      const bool mine = ((s == a.B ? a.pre_tiled : a.own_tiled) != 0) == TILED;
-      d.n[s] = n;
-      d.un[s] = mine ? (n + U - 1) / U : 0;
-      u = (long)d.un[s] * a.n_kv * groups_of<TILED>(a, s);
-    }
-    long sum = u;
+  const int lane = threadIdx.x & 31, cap = a.table_w << a.page_log2, U = TILED ? a.tunit : UNIT;
+  static_assert(LK_MAX_BATCH <= 64, "two sequences to a lane");
+  // lane l: sequences 2 l and 2 l + 1
+  int n[2];
+  long u[2] = {0, 0};
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long up = __shfl_up_sync(lk::FULL, sum, o);
-      if (lane >= o) sum += up;
-    }
-    if (s < nseq) d.cum[s] = run + sum - u;
-    run += __shfl_sync(lk::FULL, sum, 31);
+  for (int i = 0; i < 2; ++i) n[i] = 2 * lane + i < a.B ? __ldcg(a.lens + 2 * lane + i) : 0;
+  const bool own = (a.own_tiled != 0) == TILED, pre = (a.pre_tiled != 0) == TILED;
+  const int items = a.n_kv * groups_of<TILED>(a, 0);
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int s = 2 * lane + i;
+    n[i] = min(max(n[i], 0), cap);
+    const int un = own ? (n[i] + U - 1) / U : 0;
+    if (s < a.B) d.n[s] = n[i], d.un[s] = un;
+    u[i] = (long)un * items;
   }
-  if (lane == 0) d.cum[nseq] = run;
+  long sum = u[0] + u[1];
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long up = __shfl_up_sync(lk::FULL, sum, o);
+    if (lane >= o) sum += up;
+  }
+  const long before = sum - u[0] - u[1], total = __shfl_sync(lk::FULL, sum, 31);
+  if (2 * lane < a.B) d.cum[2 * lane] = before;
+  if (2 * lane + 1 < a.B) d.cum[2 * lane + 1] = before + u[0];
+  if (lane == 0) {
+    d.cum[a.B] = total;
+    if (a.shared) {
+      const int un = pre ? (a.plen + U - 1) / U : 0;
+      d.n[a.B] = a.plen;
+      d.un[a.B] = un;
+      d.cum[a.B + 1] = total + (long)un * a.n_kv * groups_of<TILED>(a, a.B);
+    }
+  }
 }
 
 // ---- instructions both kernels use ----------------------------------------------------

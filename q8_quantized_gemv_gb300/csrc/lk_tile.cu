@@ -306,28 +306,38 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
         const float up = scale_shift<D>(in, in ? lds128(src + 64 * D + lane * 16) : make_uint4(0, 0, 0, 0), o_left);
         ok = __all_sync(FULL, wait(b_free + 8 * buf, (of / C::NB) ^ 1u));
         if (!ok) return;
-#pragma unroll 4
-        for (int k = 0; k < KN; ++k) {
-          const int c = lane + 32 * k, row = c / CPR, ch = c % CPR;
-          const bool have = row < o_left && ((o_there >> (row >> 4)) & 1u);
-          const uint4 w = lds128(src + c * 16);
-          const float e = lds_half(src + 64 * D + (row * (D / 32) + (ch >> 1)) * 2);
-          const __half2 e2 = __half2half2(__float2half_rn(have ? e * up : 0.0f));
-          const unsigned x[4] = {w.x, w.y, w.z, w.w};
-          const unsigned at = dst0 + (ch >> 2) * C::HALF + row * 128;
+        constexpr int GB = 4;  // pieces read together
+#pragma unroll 1
+        for (int k0 = 0; k0 < KN; k0 += GB) {
+          uint4 w[GB];
+          float e[GB];
 #pragma unroll
-          for (int q = 0; q < 2; ++q) {  // 8 values: 16 bytes of each term
-            unsigned hi[4], lo[4];
+          for (int k = 0; k < GB; ++k) {
+            const int c = lane + 32 * (k0 + k), row = c / CPR;
+            w[k] = lds128(src + c * 16);
+            e[k] = lds_half(src + 64 * D + (row * (D / 32) + ((c % CPR) >> 1)) * 2);
+          }
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-              const unsigned pr = level_pair(x[2 * q + (r >> 1)] ^ 0x80808080u, r & 1 ? 0x4342 : 0x4140);
-              const __half2 l2 = *(const __half2*)&pr, h2 = __hmul2(l2, e2), r2 = __hfma2(l2, e2, __hneg2(h2));
-              hi[r] = *(const unsigned*)&h2;
-              lo[r] = *(const unsigned*)&r2;
+          for (int k = 0; k < GB; ++k) {
+            const int c = lane + 32 * (k0 + k), row = c / CPR, ch = c % CPR;
+            const bool have = row < o_left && ((o_there >> (row >> 4)) & 1u);
+            const __half2 e2 = __half2half2(__float2half_rn(have ? e[k] * up : 0.0f));
+            const unsigned x[4] = {w[k].x, w[k].y, w[k].z, w[k].w};
+            const unsigned at = dst0 + (ch >> 2) * C::HALF + row * 128;
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {  // 8 values: 16 bytes of each term
+              unsigned hi[4], lo[4];
+#pragma unroll
+              for (int r = 0; r < 4; ++r) {
+                const unsigned pr = level_pair(x[2 * q + (r >> 1)] ^ 0x80808080u, r & 1 ? 0x4342 : 0x4140);
+                const __half2 l2 = *(const __half2*)&pr, h2 = __hmul2(l2, e2), r2 = __hfma2(l2, e2, __hneg2(h2));
+                hi[r] = *(const unsigned*)&h2;
+                lo[r] = *(const unsigned*)&r2;
+              }
+              const unsigned pc = at + (((2 * (ch & 3) + q) ^ (row & 7)) << 4);
+              sts128(pc, hi);
+              sts128(pc + 64 * 128, lo);
             }
-            const unsigned pc = at + (((2 * (ch & 3) + q) ^ (row & 7)) << 4);
-            sts128(pc, hi);
-            sts128(pc + 64 * 128, lo);
           }
         }
         fence_async();

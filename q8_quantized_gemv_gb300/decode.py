@@ -118,10 +118,8 @@ class Attention:
         return {"x": self.out} if mode == lk.LK_DEQUANT else act
 
     def launches(self):
-        """Of one layer: append, attention (two kernels where a prefix's many
-        rows go to the tile kernel), join."""
-        tiled = self.prefix and self.kv != "q8" and self.lens.numel() * self.n_q // self.n_kv > 16
-        return 4 if tiled else 3
+        """Of one layer: the append and the attention's."""
+        return 1 + lk.lk_attn_launches(self.caches[0], self.n_q, self.lens.numel(), 1, self.prefix)
 
 
 class DecodeStack:

@@ -123,6 +123,7 @@ def _load():
         "lk_attn": ([P, P, I, P, I, P, I, I, F, I, P, P, P, P, P, S, P, P], I),
         "lk_attn_shared": ([P, P, I, P, I, I, P, I, P, I, I, F, I, P, P, P, P, P, S, P, P], I),
         "lk_attn_workspace_bytes": ([I, I, I, I, I, I], S),
+        "lk_attn_launches": ([I, I, I, I, I, I, I], I),
     }
     for name, (args, res) in sig.items():
         fn = getattr(lib, name)
@@ -144,7 +145,7 @@ def exported_symbols():
 
 def attn_symbols():
     """The entry points of include/lk_attn.h."""
-    return ["lk_kv_append", "lk_attn", "lk_attn_shared", "lk_attn_workspace_bytes"]
+    return ["lk_kv_append", "lk_attn", "lk_attn_shared", "lk_attn_workspace_bytes", "lk_attn_launches"]
 
 
 def _ok(st, where):
@@ -577,6 +578,11 @@ def lk_kv_append(cache: KvCache, q, k, v, table, lens, cosines, sines, qr, R=1, 
 
 def lk_attn_workspace_bytes(n_q, n_kv, head_dim, B, R=1, shared=False) -> int:
     return _load().lk_attn_workspace_bytes(n_q, n_kv, head_dim, B, R, 1 if shared else 0)
+
+
+def lk_attn_launches(cache, n_q, B, R=1, prefix_len=0) -> int:
+    """Kernels that lk_attn (lk_attn_shared) on this cache launches."""
+    return _load().lk_attn_launches(cache.c.type, n_q, cache.n_kv, cache.head_dim, B, R, prefix_len)
 
 
 def _attn_tail(cache, q, M, scale, mode, out, hq, hl, hs, ws):

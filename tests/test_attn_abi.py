@@ -112,6 +112,17 @@ def test_workspace_bytes(lib):
     assert f(32, 8, 64, 4) < f(32, 8, 128, 4)
 
 
+def test_launches(lib):
+    f = lib.lk_attn_launches
+    assert f(0, 32, 8, 128, 1, 1, 0) == 2                 # streaming, join
+    assert f(0, 32, 8, 128, 1, 64, 0) == 2                # tile, join
+    assert f(1, 32, 8, 128, 64, 1, 32768) == 3            # tile (prefix), streaming (own), join
+    assert f(1, 32, 8, 128, 64, 1, 100) == 2              # a short prefix streams too
+    assert f(2, 32, 8, 64, 4, 8, 0) == 2 and f(2, 32, 8, 64, 4, 9, 50000) == 2
+    assert f(3, 32, 8, 128, 1, 1, 0) == 0 and f(0, 32, 5, 128, 1, 1, 0) == 0 and f(0, 32, 8, 128, 65, 1, 0) == 0
+    assert f(0, 32, 8, 128, 0, 1, 0) == 0 and f(0, 32, 8, 128, 1, 1, -1) == 0
+
+
 def test_binding_refusals():
     k = torch.zeros((4, 2, 16, 64), dtype=torch.float16)
     with pytest.raises(ValueError):

@@ -391,7 +391,8 @@ def test_attn_lens_past_the_table():
 
 @pytest.mark.parametrize("type_", list(TYPES))
 @pytest.mark.parametrize("B,R,n_q,n_kv,prefix", [(1, 1, 4, 4, 1), (3, 1, 8, 2, 31), (5, 2, 4, 1, 500),
-                                                 (64, 1, 8, 2, 1029), (16, 4, 10, 2, 4000), (2, 1, 32, 8, 9000)])
+                                                 (64, 1, 8, 2, 1029), (16, 4, 10, 2, 4000), (2, 1, 32, 8, 9000),
+                                                 (5, 2, 8, 2, 14001), (7, 1, 28, 4, 22000), (64, 1, 8, 2, 4099)])
 def test_shared_prefix(type_, B, R, n_q, n_kv, prefix):
     lens = [(R + 13 * b) % 70 for b in range(B)]
     run_attn(type_, 128, n_q, n_kv, 16, R, lens, prefix=prefix)
@@ -404,6 +405,7 @@ def test_shared_prefix_padding_and_empty():
     """lens 0: the prefix alone; lens < 0: zeros; prefix_len 0: lk_attn."""
     for type_ in TYPES:
         run_attn(type_, 128, 8, 2, 32, 1, [0, -1, 5, -2 ** 31, 0], prefix=77)
+        run_attn(type_, 128, 16, 2, 32, 1, [0, -1, 5, -2 ** 31, 0], prefix=20000)
     g = gen(9)
     cache, _, _ = make_cache("bf16", 8, 2, 16, 64, g)
     table = make_table(2, 3, 8, g)
