@@ -109,7 +109,9 @@ lk_status lk_kv_append(const lk_kv_cache* cache, const float* q, const float* k,
  *         content needs no preparation and means nothing after the call.
  *         Calls that may run at the same time need separate ones
  *   scale finite (1/sqrt(head_dim) as a rule)
- * Rows behind the last sequence are not touched.
+ * Rows behind the last sequence are not touched.  LK_ERR_SHAPE also where the
+ * key units of all items together, n_kv * B * ceil(R * n_q/n_kv / 8) * ceil(table_w *
+ * page / 32) (and the prefix's), pass 2^31.
  */
 lk_status lk_attn(const lk_kv_cache* cache, const float* q, int n_q, const int32_t* table, int table_w,
                   const int32_t* lens, int B, int R, float scale, lk_mode mode, float* out, int8_t* hq, int8_t* hl,

@@ -94,7 +94,7 @@ struct Cursor {
 };
 
 // By a whole warp.
-__device__ __forceinline__ Cursor cursor_at(const AttnArgs& a, const Deal& d, long unit) {
+__device__ __forceinline__ Cursor cursor_at(const AttnArgs& a, const Deal& d, int unit) {
   const int lane = threadIdx.x & 31, nseq = a.B + a.shared;
   Cursor c;
   c.s = 0;
@@ -102,9 +102,8 @@ __device__ __forceinline__ Cursor cursor_at(const AttnArgs& a, const Deal& d, lo
     c.s += __popc(__ballot_sync(FULL, s0 + lane < nseq && d.cum[s0 + lane + 1] <= unit));
   c.un = d.un[c.s];
   c.n = d.n[c.s];
-  const long rel = unit - d.cum[c.s];
-  const int li = (int)quot(rel, c.un);
-  c.u = (int)(rel - (long)li * c.un);
+  const int rel = unit - d.cum[c.s], li = rel / c.un;
+  c.u = rel - li * c.un;
   c.tiles = groups_of<false>(a, c.s);
   c.kvh = li / c.tiles;
   c.tile = li - c.kvh * c.tiles;
@@ -154,12 +153,13 @@ __global__ void __launch_bounds__(32 * Cfg<TYPE, D>::NW, 1) attn_kernel(const __
   if (threadIdx.x < 32) make_deal<false>(a, deal);
   __syncthreads();
   const int lane = threadIdx.x & 31, warp = __shfl_sync(FULL, threadIdx.x >> 5, 0), g = lane >> 2, t = lane & 3;
-  const long T = deal.cum[a.B + a.shared], W = stream_blocks(a.W, C::NW, T);
-  if (blockIdx.x >= W) return;
-  const long ca = quot(T * blockIdx.x, (int)W);
-  const int cn = (int)(quot(T * (blockIdx.x + 1), (int)W) - ca), we = min(C::NW, cn);
-  const int wa = warp < we ? (int)quot((long)cn * warp, we) : cn;
-  int left = (warp < we ? (int)quot((long)cn * (warp + 1), we) : cn) - wa;  // units the warp has to do
+  const int T = deal.cum[a.B + a.shared], W = stream_blocks(a, C::NW, T);
+  if ((int)blockIdx.x >= W) return;
+  const Shares blocks(T, W);
+  const int ca = blocks.begin(blockIdx.x), cn = blocks.size(blockIdx.x), we = min(C::NW, cn);
+  const Shares warps(cn, we);
+  const int wa = warp < we ? warps.begin(warp) : cn;
+  int left = warp < we ? warps.size(warp) : 0;  // units the warp has to do
   Cursor cc = cursor_at(a, deal, ca);
   const bool one = cc.u + cn <= cc.un;  // the block's units are all one item's: its warps join their parts
   if (one) cc.u += wa;
@@ -602,39 +602,33 @@ struct Source {
   }
 };
 
-// The block with unit u: the last c with T * c / W <= u.
-__device__ __forceinline__ int holder(long u, long W, long T) {
-  const long a = (u + 1) * W - 1;
-  return ((a | T) >> 31) == 0 ? (int)a / (int)T : (int)(a / T);
-}
-
 // Row i of key/value head kvh in sequence s of the streaming deal.
 __device__ __forceinline__ Source stream_source(const AttnArgs& a, const Deal& d, int s, int kvh, int i) {
   Source r = {};
   const int un = d.un[s];
   if (un == 0) return r;
-  const long T = d.cum[a.B + a.shared], W = stream_blocks(a.W, a.NW, T);
+  const int T = d.cum[a.B + a.shared];
+  const Shares blocks(T, stream_blocks(a, a.NW, T));
   const int tile = i / TR, li = kvh * groups_of<false>(a, s) + tile, item = item0<false>(a, s) + li;
-  const long ib = d.cum[s] + (long)li * un, ie = ib + un;  // the item's units
-  const int c0 = holder(ib, W, T), c1 = holder(ie - 1, W, T);
+  const int ib = d.cum[s] + li * un, ie = ib + un;  // the item's units
+  const int c0 = blocks.holder(ib), c1 = blocks.holder(ie - 1);
   // entries of block c: one if it has nothing else, else one of each warp with units of the item
   const auto part = [&](int c, long& at, int& n) {
-    const long ca = quot(T * c, (int)W), cb = quot(T * (c + 1), (int)W);
+    const int ca = blocks.begin(c), cn = blocks.size(c);
     int w0 = 0, w1 = 0;
-    if (ca < ib || cb > ie) {
-      const int cn = (int)(cb - ca), we = min(a.NW, cn);
-      const long ua = max(ca, ib) - ca, ub = min(cb, ie) - ca;
-      w0 = (int)(((ua + 1) * we - 1) / cn);
-      w1 = (int)((ub * we - 1) / cn);
+    if (ca < ib || ca + cn > ie) {
+      const Shares warps(cn, min(a.NW, cn));
+      w0 = warps.holder(max(ca, ib) - ca);
+      w1 = warps.holder(min(ca + cn, ie) - ca - 1);
     }
-    at = ((long)c * a.NW + w0 + item) * TR + i % TR;
+    at = (long)(c * a.NW + w0 + item) * TR + i % TR;
     n = w1 - w0 + 1;
   };
   int n2 = 0;
   part(c0, r.first, r.n0);
   if (c1 > c0) part(c1, r.last, n2);
   r.nm = c1 > c0 ? c1 - c0 - 1 : 0;
-  r.mid = ((long)(c0 + 1) * a.NW + item) * TR + i % TR;
+  r.mid = (long)((c0 + 1) * a.NW + item) * TR + i % TR;
   r.step = a.NW * TR;
   r.per = 1;
   r.n = r.n0 + r.nm + n2;
@@ -648,11 +642,11 @@ __device__ __forceinline__ Source tile_source(const AttnArgs& a, const Deal& d, 
   Source r = {};
   const int un = d.un[s];
   if (un == 0) return r;
-  const long T = d.cum[a.B + a.shared], W = shares(a.TW, T);
-  const int group = i / a.trows, li = kvh * groups_of<true>(a, s) + group, ig = i - group * a.trows;
-  const long ub = d.cum[s] + (long)li * un;
-  const int w0 = holder(ub, W, T), w1 = holder(ub + un - 1, W, T);
-  const int rows = rows_of(a, s), rg = min(a.trows, rows - group * a.trows), which = s == a.B ? 1 : 0;
+  const int T = d.cum[a.B + a.shared], trows = 1 << a.trows_log2;
+  const Shares blocks(T, tile_blocks(a, T));
+  const int group = i >> a.trows_log2, li = kvh * groups_of<true>(a, s) + group, ig = i - group * trows;
+  const int ub = d.cum[s] + li * un, w0 = blocks.holder(ub), w1 = blocks.holder(ub + un - 1);
+  const int rows = rows_of(a, s), rg = min(trows, rows - group * trows), which = s == a.B ? 1 : 0;
   r.step = tile_slot_rows(rows);
   r.mid = (long)(w0 + item0<true>(a, s) + li) * r.step + ig;
   r.nm = w1 - w0 + 1;
@@ -926,6 +920,11 @@ lk_status lk_attn_shared(const lk_kv_cache* cache, const float* q, int n_q, cons
   if (out && !aligned(out, 4)) return LK_ERR_ALIGN;
   if (mode != LK_DEQUANT && (st = check_act_out(mode, hq, hl, hs))) return st;
   const int shared = prefix_len > 0;
+  // units of 32 keys, all items' together, are 32-bit numbers
+  const long cap_units = ((long)table_w * cache->page + UNIT - 1) / UNIT, pre_units = ((long)prefix_len + UNIT - 1) / UNIT;
+  const long G = n_q / cache->n_kv;
+  if (cache->n_kv * (B * ((R * G + TR - 1) / TR) * cap_units + (B * R * G + TR - 1) / TR * pre_units) > 0x7fffffffL)
+    return LK_ERR_SHAPE;
   if (!ws || ws_bytes < lk_attn_workspace_bytes(n_q, cache->n_kv, cache->head_dim, B, R, shared))
     return LK_ERR_WORKSPACE;
   if (!aligned(ws, 16)) return LK_ERR_ALIGN;
@@ -962,8 +961,8 @@ lk_status lk_attn_shared(const lk_kv_cache* cache, const float* q, int n_q, cons
     a.tml[x] = (float*)((char*)ws + ml[x + 1]);
     a.to[x] = (float*)((char*)ws + o[x + 1]);
   }
-  a.tunit = cache->type == LK_KV_Q8 ? 64 : 128;
-  a.trows = cache->type == LK_KV_Q8 ? 128 : 256;
+  a.tunit_log2 = cache->type == LK_KV_Q8 ? 6 : 7;
+  a.trows_log2 = cache->type == LK_KV_Q8 ? 7 : 8;
   a.tflip = cache->type != LK_KV_Q8;
   a.W = d->sm_count < kMaxWorkers ? d->sm_count : kMaxWorkers;
   a.TW = d->sm_count < kTileWorkers ? d->sm_count : kTileWorkers;

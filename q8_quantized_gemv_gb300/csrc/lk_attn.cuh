@@ -89,7 +89,7 @@ struct AttnArgs {
   float* tml[2];      // tile partials of the sequences, the prefix: [slot][slot rows][2],
   float* to[2];       //   [slot][slot rows][D], tflip: 16-byte pieces permuted in 128 bytes by row & 7
   int W, NW, TW;      // blocks and warps of the streaming launch, blocks of the tile launch
-  int tunit, trows;   // keys of a unit, rows of an item of the tile kernel
+  int tunit_log2, trows_log2;  // keys of a unit, rows of an item of the tile kernel
   int tflip;          // whether its partials' pieces are permuted
   int late;           // the tile launch comes after a streaming one of the same call
   unsigned long long wait_ns;
@@ -97,9 +97,11 @@ struct AttnArgs {
 };
 
 // Sequence s has un[s] units per item (0 where the other kernel has it) and
-// n[s] keys; units before it cum[s]; cum[nseq] is their total.
+// n[s] keys; units before it cum[s]; cum[nseq] is their total.  32 bits: the
+// host refuses sizes whose units could pass them (64-bit quotients would be half
+// the time of a short call).
 struct Deal {
-  long cum[kMaxSeq + 1];
+  int cum[kMaxSeq + 1];
   int un[kMaxSeq];
   int n[kMaxSeq];
 };
@@ -107,8 +109,9 @@ struct Deal {
 __device__ __forceinline__ int rows_of(const AttnArgs& a, int s) { return (s == a.B ? a.B * a.R : a.R) * a.G; }
 template <bool TILED>
 __device__ __forceinline__ int groups_of(const AttnArgs& a, int s) {
-  const int N = TILED ? a.trows : TR;
-  return (rows_of(a, s) + N - 1) / N;
+  const int lg = TILED ? a.trows_log2 : 3;
+  static_assert(TR == 8, "3 is its logarithm");
+  return (rows_of(a, s) + (1 << lg) - 1) >> lg;
 }
 // Items before sequence s: of the streaming kernel in one row, of the tile
 // kernel the prefix's apart.
@@ -118,22 +121,31 @@ __device__ __forceinline__ int item0(const AttnArgs& a, int s) {
   return s * a.n_kv * groups_of<TILED>(a, 0);
 }
 
-// Blocks that have a share: none is empty, so an item's segments are in
-// consecutive blocks.
-__device__ __forceinline__ long shares(int W, long T) { return T < W ? T : W; }
-
-// The streaming kernel deals a block's units on to its warps: blocks as many
-// as leave each warp a unit.
-__device__ __forceinline__ long stream_blocks(int W, int NW, long T) { return min((long)W, (T + NW - 1) / NW); }
+// T units dealt to W >= 1 holders in equal contiguous shares, the first T % W
+// holders having one more.  With W <= T none is empty, so an item's segments are
+// in consecutive holders.
+struct Shares {
+  int base, more;
+  __device__ __forceinline__ Shares(int T, int W) : base(T / W), more(T - base * W) {}
+  __device__ __forceinline__ int begin(int c) const { return c * base + min(c, more); }
+  __device__ __forceinline__ int size(int c) const { return base + (c < more ? 1 : 0); }
+  __device__ __forceinline__ int holder(int u) const {
+    const int first = more * (base + 1);
+    return u < first ? u / (base + 1) : more + (u - first) / base;
+  }
+};
+// Blocks of the tile deal; blocks of the streaming deal, as many as leave each of
+// their warps a unit.
+__device__ __forceinline__ int tile_blocks(const AttnArgs& a, int T) { return min(a.TW, T); }
+__device__ __forceinline__ int stream_blocks(const AttnArgs& a, int NW, int T) { return min(a.W, (T + NW - 1) / NW); }
 
 // By one whole warp; the caller synchronizes.
 template <bool TILED>
 __device__ __forceinline__ void make_deal(const AttnArgs& a, Deal& d) {
-  const int lane = threadIdx.x & 31, cap = a.table_w << a.page_log2, U = TILED ? a.tunit : UNIT;
-  static_assert(LK_MAX_BATCH <= 64, "two sequences to a lane");
+  const int lane = threadIdx.x & 31, cap = a.table_w << a.page_log2, lu = TILED ? a.tunit_log2 : 5;
+  static_assert(LK_MAX_BATCH <= 64 && UNIT == 32, "two sequences to a lane");
   // lane l: sequences 2 l and 2 l + 1
-  int n[2];
-  long u[2] = {0, 0};
+  int n[2], u[2];
 #pragma unroll
   for (int i = 0; i < 2; ++i) n[i] = 2 * lane + i < a.B ? __ldcg(a.lens + 2 * lane + i) : 0;
   const bool own = (a.own_tiled != 0) == TILED, pre = (a.pre_tiled != 0) == TILED;
@@ -142,26 +154,26 @@ __device__ __forceinline__ void make_deal(const AttnArgs& a, Deal& d) {
   for (int i = 0; i < 2; ++i) {
     const int s = 2 * lane + i;
     n[i] = min(max(n[i], 0), cap);
-    const int un = own ? (n[i] + U - 1) / U : 0;
+    const int un = own ? (n[i] + (1 << lu) - 1) >> lu : 0;
     if (s < a.B) d.n[s] = n[i], d.un[s] = un;
-    u[i] = (long)un * items;
+    u[i] = un * items;
   }
-  long sum = u[0] + u[1];
+  int sum = u[0] + u[1];
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const long up = __shfl_up_sync(lk::FULL, sum, o);
+    const int up = __shfl_up_sync(lk::FULL, sum, o);
     if (lane >= o) sum += up;
   }
-  const long before = sum - u[0] - u[1], total = __shfl_sync(lk::FULL, sum, 31);
+  const int before = sum - u[0] - u[1];
   if (2 * lane < a.B) d.cum[2 * lane] = before;
   if (2 * lane + 1 < a.B) d.cum[2 * lane + 1] = before + u[0];
-  if (lane == 0) {
-    d.cum[a.B] = total;
+  if (lane == 31) {
+    d.cum[a.B] = sum;
     if (a.shared) {
-      const int un = pre ? (a.plen + U - 1) / U : 0;
+      const int un = pre ? (a.plen + (1 << lu) - 1) >> lu : 0;
       d.n[a.B] = a.plen;
       d.un[a.B] = un;
-      d.cum[a.B + 1] = total + (long)un * a.n_kv * groups_of<TILED>(a, a.B);
+      d.cum[a.B + 1] = sum + un * a.n_kv * groups_of<TILED>(a, a.B);
     }
   }
 }
@@ -203,8 +215,6 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
 }
-// a / b; a 64-bit division only where a needs one
-__device__ __forceinline__ long quot(long a, int b) { return (a >> 31) == 0 ? (long)((int)a / b) : a / b; }
 // 16 bytes global -> shared; with bytes 0 nothing is read and zeros are written
 __device__ __forceinline__ void cp16(unsigned dst, const void* src, int bytes) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");

@@ -67,19 +67,17 @@ struct Segment {
 };
 
 // The next segment of the share [u0, u1), u0 moved behind it.
-__device__ __forceinline__ Segment next_segment(const AttnArgs& a, const Deal& d, int& s, long& u0, long u1) {
+__device__ __forceinline__ Segment next_segment(const AttnArgs& a, const Deal& d, int& s, int& u0, int u1) {
   Segment g;
   while (d.cum[s + 1] <= u0) ++s;
-  const int un = d.un[s], groups = groups_of<true>(a, s);
-  const long rel = u0 - d.cum[s];
-  const int li = (int)quot(rel, un);
+  const int un = d.un[s], groups = groups_of<true>(a, s), rel = u0 - d.cum[s], li = rel / un;
   g.s = s;
   g.n = d.n[s];
-  g.ub = (int)(rel - (long)li * un);
-  g.nt = (int)min((long)(un - g.ub), u1 - u0);
+  g.ub = rel - li * un;
+  g.nt = min(un - g.ub, u1 - u0);
   g.kvh = li / groups;
   g.group = li - g.kvh * groups;
-  g.rows = min(a.trows, rows_of(a, s) - g.group * a.trows);
+  g.rows = min(1 << a.trows_log2, rows_of(a, s) - (g.group << a.trows_log2));
   g.both = g.rows > 128;
   g.slot = (int)blockIdx.x + item0<true>(a, s) + li;
   u0 += g.nt;
@@ -191,9 +189,12 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
   __syncthreads();
   tm_after();
   const unsigned tmem = __shfl_sync(FULL, *(volatile unsigned*)&tmem_slot, 0);
-  const long T = deal.cum[a.B + a.shared], W = shares(a.TW, T);
-  long u0 = 0, u1 = 0;
-  if (blockIdx.x < W) u0 = quot(T * blockIdx.x, (int)W), u1 = quot(T * (blockIdx.x + 1), (int)W);
+  const int T = deal.cum[a.B + a.shared], W = tile_blocks(a, T);
+  int u0 = 0, u1 = 0;
+  if ((int)blockIdx.x < W) {
+    const Shares blocks(T, W);
+    u0 = blocks.begin(blockIdx.x), u1 = u0 + blocks.size(blockIdx.x);
+  }
   int s = 0;
   auto wait = [&](unsigned bar, unsigned parity) -> bool {
     if (bar_wait(bar, parity & 1u, a.wait_ns, &abort_flag)) return true;
@@ -459,7 +460,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
       const Segment g = next_segment(a, deal, s, u0, u1);
       const bool pre = g.s == a.B;
       const int* table = pre ? a.ptable : a.table + (long)g.s * a.table_w;
-      const int r_first = g.group * a.trows + (g.both ? 128 * x : 0);  // row of the head that is the stream's row 0
+      const int r_first = (g.group << a.trows_log2) + (g.both ? 128 * x : 0);  // row of the head that is the stream's row 0
       const int nr = g.both ? min(128, g.rows - 128 * x) : g.rows;
       const int cnt = g.both ? g.nt : x == 0 ? (g.nt + 1) / 2 : g.nt / 2;
       if (stored) {

@@ -87,6 +87,7 @@ def test_attn_refusals(lib):
     assert call(n_q=5) == -3
     assert call(B=64, R=2) == -3 and call(B=-1) == -3 and call(tw=-1) == -3
     assert call(pl=-1) == -3 and call(pl=65) == -3 and call(pw=-1) == -3 and call(pw=1 << 30) == -3
+    assert call(tw=1 << 26, B=64, R=1, wsb=1 << 40) == -3     # more key units than 32 bits
     assert call(scale=math.inf) == -1 and call(scale=math.nan) == -1
     assert call(mode=3) == -1 and call(mode=-1) == -1
     for name in ("q", "pt", "table", "lens"):
