@@ -153,9 +153,10 @@ __global__ void __launch_bounds__(32 * Cfg<TYPE, D>::NW, 1) attn_kernel(const __
   if (threadIdx.x < 32) make_deal<false>(a, deal);
   __syncthreads();
   const int lane = threadIdx.x & 31, warp = __shfl_sync(FULL, threadIdx.x >> 5, 0), g = lane >> 2, t = lane & 3;
-  const int T = deal.cum[a.B + a.shared], W = stream_blocks(a, C::NW, T);
-  if ((int)blockIdx.x >= W) return;
-  const Shares blocks(T, W);
+  const int T = deal.cum[a.B + a.shared];
+  if (T == 0) return;
+  const Shares blocks = stream_blocks(a, C::NW, T);
+  if (blocks.begin(blockIdx.x) >= T) return;
   const int ca = blocks.begin(blockIdx.x), cn = blocks.size(blockIdx.x), we = min(C::NW, cn);
   const Shares warps(cn, we);
   const int wa = warp < we ? warps.begin(warp) : cn;
@@ -591,14 +592,13 @@ struct JoinArgs {
 struct Source {
   const float* ml;
   const float* o;
-  long first, mid, last;
+  int first, mid, last;
   int n, n0, nm, step, per, hop, flip;
-  __device__ __forceinline__ long at(int i) const {
-    if (i < n0) return first + (long)i * TR;
-    i -= n0;
-    const int j = per == 1 ? i : i >> 1;
-    if (j < nm) return mid + (long)j * step + (i - j * per) * hop;
-    return last + (long)(i - nm) * TR;
+  __device__ __forceinline__ int at(int i) const {  // (rows of the workspace: 32 bits)
+    const int k = i - n0, j = per == 1 ? k : k >> 1;
+    const int x = first + i * TR, y = mid + j * step + (k - j * per) * hop, w = last + (k - nm) * TR;
+    const int yw = j < nm ? y : w;
+    return i < n0 ? x : yw;
   }
 };
 
@@ -608,12 +608,12 @@ __device__ __forceinline__ Source stream_source(const AttnArgs& a, const Deal& d
   const int un = d.un[s];
   if (un == 0) return r;
   const int T = d.cum[a.B + a.shared];
-  const Shares blocks(T, stream_blocks(a, a.NW, T));
+  const Shares blocks = stream_blocks(a, a.NW, T);
   const int tile = i / TR, li = kvh * groups_of<false>(a, s) + tile, item = item0<false>(a, s) + li;
   const int ib = d.cum[s] + li * un, ie = ib + un;  // the item's units
   const int c0 = blocks.holder(ib), c1 = blocks.holder(ie - 1);
   // entries of block c: one if it has nothing else, else one of each warp with units of the item
-  const auto part = [&](int c, long& at, int& n) {
+  const auto part = [&](int c, int& at, int& n) {
     const int ca = blocks.begin(c), cn = blocks.size(c);
     int w0 = 0, w1 = 0;
     if (ca < ib || ca + cn > ie) {
@@ -621,14 +621,14 @@ __device__ __forceinline__ Source stream_source(const AttnArgs& a, const Deal& d
       w0 = warps.holder(max(ca, ib) - ca);
       w1 = warps.holder(min(ca + cn, ie) - ca - 1);
     }
-    at = (long)(c * a.NW + w0 + item) * TR + i % TR;
+    at = (c * a.NW + w0 + item) * TR + i % TR;
     n = w1 - w0 + 1;
   };
   int n2 = 0;
   part(c0, r.first, r.n0);
   if (c1 > c0) part(c1, r.last, n2);
   r.nm = c1 > c0 ? c1 - c0 - 1 : 0;
-  r.mid = (long)((c0 + 1) * a.NW + item) * TR + i % TR;
+  r.mid = ((c0 + 1) * a.NW + item) * TR + i % TR;
   r.step = a.NW * TR;
   r.per = 1;
   r.n = r.n0 + r.nm + n2;
@@ -643,12 +643,12 @@ __device__ __forceinline__ Source tile_source(const AttnArgs& a, const Deal& d, 
   const int un = d.un[s];
   if (un == 0) return r;
   const int T = d.cum[a.B + a.shared], trows = 1 << a.trows_log2;
-  const Shares blocks(T, tile_blocks(a, T));
+  const Shares blocks = tile_blocks(a, T);
   const int group = i >> a.trows_log2, li = kvh * groups_of<true>(a, s) + group, ig = i - group * trows;
   const int ub = d.cum[s] + li * un, w0 = blocks.holder(ub), w1 = blocks.holder(ub + un - 1);
   const int rows = rows_of(a, s), rg = min(trows, rows - group * trows), which = s == a.B ? 1 : 0;
   r.step = tile_slot_rows(rows);
-  r.mid = (long)(w0 + item0<true>(a, s) + li) * r.step + ig;
+  r.mid = (w0 + item0<true>(a, s) + li) * r.step + ig;
   r.nm = w1 - w0 + 1;
   r.per = rg <= 128 ? 2 : 1;
   r.hop = rg;
@@ -657,6 +657,15 @@ __device__ __forceinline__ Source tile_source(const AttnArgs& a, const Deal& d, 
   r.o = a.to[which];
   r.flip = a.tflip ? ig & 7 : 0;
   return r;
+}
+
+// Values through L2; volatile, so that a batch of loads stays together ahead of
+// its sums (moved down to them, each waits alone: 14.8 against 9.9 us).
+__device__ __forceinline__ void ld_cg(const float* p, float (&v)[4]) {
+  asm volatile("ld.global.cg.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]) : "l"(p));
+}
+__device__ __forceinline__ void ld_cg(const float* p, float (&v)[2]) {
+  asm volatile("ld.global.cg.v2.f32 {%0, %1}, [%2];" : "=f"(v[0]), "=f"(v[1]) : "l"(p));
 }
 
 template <int Q, int D>
@@ -679,7 +688,7 @@ __global__ void __launch_bounds__(128) attn_join_kernel(const JoinArgs j) {
   const int b = row / a.R, r = row - b * a.R;
   // A lane has V neighbouring values.  Partials come in batches of NB whose
   // loads are all in flight at once, the values' not waiting for the maxima's.
-  constexpr int V = D / 32, NB = 8;
+  constexpr int V = D / 32, NB = 16;
   float M = -INFINITY, acc[V], ls = 0.0f;
 #pragma unroll
   for (int c = 0; c < V; ++c) acc[c] = 0.0f;
@@ -696,16 +705,15 @@ __global__ void __launch_bounds__(128) attn_join_kernel(const JoinArgs j) {
     const int at = V == 4 ? (lane ^ z.flip) * 4 : ((lane >> 1) ^ z.flip) * 4 + (lane & 1) * 2;
 #pragma unroll 1
     for (int i0 = 0; i0 < z.n; i0 += NB) {
+      // lane i < NB: partial i0 + i's place, maximum and sum
+      const bool in = lane < NB && i0 + lane < z.n;
+      const int mine = z.at(min(i0 + (lane & (NB - 1)), z.n - 1));
+      const float2 p = in ? __ldcg((const float2*)(z.ml + (long)mine * 2)) : make_float2(-INFINITY, 0.0f);
       float o[NB][V];
 #pragma unroll
       for (int i = 0; i < NB; ++i) {
-        const float* p = z.o + z.at(min(i0 + i, z.n - 1)) * D + at;
-        if constexpr (V == 4) *(float4*)o[i] = __ldcg((const float4*)p);
-        else *(float2*)o[i] = __ldcg((const float2*)p);
+        ld_cg(z.o + (long)__shfl_sync(FULL, mine, i) * D + at, o[i]);
       }
-      // lane i < NB: partial i0 + i's maximum and sum
-      const bool in = lane < NB && i0 + lane < z.n;
-      const float2 p = in ? __ldcg((const float2*)(z.ml + z.at(i0 + lane) * 2)) : make_float2(-INFINITY, 0.0f);
       const float m = fmaxf(M, warp_max_xor(p.x)), ref = m == -INFINITY ? 0.0f : m;
       const float al = ex2(M - ref), f = ex2(p.x - ref), lf = f * p.y;
       M = m;

@@ -121,23 +121,39 @@ __device__ __forceinline__ int item0(const AttnArgs& a, int s) {
   return s * a.n_kv * groups_of<TILED>(a, 0);
 }
 
-// T units dealt to W >= 1 holders in equal contiguous shares, the first T % W
-// holders having one more.  With W <= T none is empty, so an item's segments are
-// in consecutive holders.
+// Units dealt to holders in contiguous shares: groups of G units to k holders
+// each, the first G % k of them having one more.  One group of all units is the
+// general deal; where all items are one sequence's, a group is an item, and no
+// share has pieces of two (a second piece costs the tile kernel some 5 us).
+// With k <= G no share is empty, so an item's segments are in consecutive holders.
 struct Shares {
-  int base, more;
-  __device__ __forceinline__ Shares(int T, int W) : base(T / W), more(T - base * W) {}
-  __device__ __forceinline__ int begin(int c) const { return c * base + min(c, more); }
-  __device__ __forceinline__ int size(int c) const { return base + (c < more ? 1 : 0); }
+  int G, k, base, more;
+  __device__ __forceinline__ Shares(int G, int k) : G(G), k(k), base(G / k), more(G - base * k) {}
+  __device__ __forceinline__ int begin(int c) const {
+    const int i = c / k, j = c - i * k;
+    return i * G + j * base + min(j, more);
+  }
+  __device__ __forceinline__ int size(int c) const { return base + (c % k < more ? 1 : 0); }
   __device__ __forceinline__ int holder(int u) const {
-    const int first = more * (base + 1);
-    return u < first ? u / (base + 1) : more + (u - first) / base;
+    const int i = u / G, r = u - i * G, first = more * (base + 1);
+    return i * k + (r < first ? r / (base + 1) : more + (r - first) / base);
   }
 };
-// Blocks of the tile deal; blocks of the streaming deal, as many as leave each of
-// their warps a unit.
-__device__ __forceinline__ int tile_blocks(const AttnArgs& a, int T) { return min(a.TW, T); }
-__device__ __forceinline__ int stream_blocks(const AttnArgs& a, int NW, int T) { return min(a.W, (T + NW - 1) / NW); }
+// The deal of T units to at most W blocks, each with at least `least` units
+// where there are enough; `one`: they are one sequence's, in `items` equal items.
+__device__ __forceinline__ Shares deal_blocks(int T, int W, int least, bool one, int items) {
+  const bool each = one && items <= W;
+  const int G = each ? T / items : T;
+  return Shares(G, min(each ? W / items : W, (G + least - 1) / least));
+}
+__device__ __forceinline__ Shares tile_blocks(const AttnArgs& a, int T) {
+  const bool pre = !a.own_tiled;
+  return deal_blocks(T, a.TW, 1, pre || (a.B == 1 && !a.pre_tiled), a.n_kv * groups_of<true>(a, pre ? a.B : 0));
+}
+// (a unit for each of a block's warps)
+__device__ __forceinline__ Shares stream_blocks(const AttnArgs& a, int NW, int T) {
+  return deal_blocks(T, a.W, NW, a.B == 1 && (a.pre_tiled || !a.shared) && !a.own_tiled, a.n_kv * groups_of<false>(a, 0));
+}
 
 // By one whole warp; the caller synchronizes.
 template <bool TILED>

@@ -50,7 +50,7 @@ struct TCfg {
   static constexpr int SMEM = QS + QX + NB * BUF + NRAW * RAW + 1024;
   // Registers: the launch has kTileThreads * kTileRegs of them; the streams
   // take 2 * 128 * STREAM and leave 128 * REST, the same sum.
-  static constexpr int STREAM = 216, REST = 72;
+  static constexpr int STREAM = Q8 ? 224 : 232, REST = Q8 ? 56 : 40;
   static_assert(kTileThreads * kTileRegs == 2 * 128 * STREAM + 128 * REST, "register split");
 };
 
@@ -189,11 +189,12 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
   __syncthreads();
   tm_after();
   const unsigned tmem = __shfl_sync(FULL, *(volatile unsigned*)&tmem_slot, 0);
-  const int T = deal.cum[a.B + a.shared], W = tile_blocks(a, T);
+  const int T = deal.cum[a.B + a.shared];
   int u0 = 0, u1 = 0;
-  if ((int)blockIdx.x < W) {
-    const Shares blocks(T, W);
-    u0 = blocks.begin(blockIdx.x), u1 = u0 + blocks.size(blockIdx.x);
+  if (T > 0) {
+    const Shares blocks = tile_blocks(a, T);
+    u0 = blocks.begin(blockIdx.x);
+    u1 = u0 < T ? u0 + blocks.size(blockIdx.x) : u0;
   }
   int s = 0;
   auto wait = [&](unsigned bar, unsigned parity) -> bool {
