@@ -14,7 +14,9 @@
 // folded into the weights).  f16 operands are shifted by powers of two so
 // that the low terms stay normal: queries to a row maximum of 2^10, weights by
 // 2^14 (Q8: by 2^10, their scales by what brings the largest to 8 .. 16, and the
-// product of the two again as two terms).  Each unit's weighted values are summed in a fresh
+// product of the two again as two terms).  bf16 has too few bits for two terms
+// of a query (errors of 3e-6 of the result's norm where f32 arithmetic has 7e-7): a third
+// one has MMAs of its own.  Each unit's weighted values are summed in a fresh
 // accumulator and added in f32, so the MMA's own accumulation never runs over
 // more than 32 keys.
 //
@@ -133,6 +135,7 @@ __global__ void __launch_bounds__(32 * Cfg<TYPE, D>::NW, 1) attn_kernel(const __
   constexpr bool Q8 = TYPE == LK_KV_Q8;
   constexpr int KS = D / 16;  // k-steps of a score
   constexpr int NT = D / 8;   // n-tiles of the output
+  constexpr bool QT = TYPE == LK_KV_BF16;  // a third term of the queries
   extern __shared__ unsigned char raw[];
   __shared__ Deal deal;
   __shared__ float wml[C::NW][TR][2];
@@ -246,7 +249,7 @@ __global__ void __launch_bounds__(32 * Cfg<TYPE, D>::NW, 1) attn_kernel(const __
     const int row = pre ? tok : s * a.R + tok;
     int vis = n;  // keys that the row sees
     if (!pre) vis = min(n, max(0, __ldcg(a.lens + s) - a.R + 1 + tok));
-    unsigned qa[KS][4];
+    unsigned qa[KS][4], qc[QT ? KS : 1][2];
     float rs = 1.0f;
     {
       const float* q = a.q + ((long)row * a.n_q + kvh * a.G + (ri - tok * a.G)) * D + t * 8;
@@ -277,6 +280,10 @@ __global__ void __launch_bounds__(32 * Cfg<TYPE, D>::NW, 1) attn_kernel(const __
         qa[k][2] = split2<TYPE == LK_KV_BF16>(x[4 * k + 2], x[4 * k + 3]);
         qa[k][1] = split2<TYPE == LK_KV_BF16>(x[4 * k], x[4 * k + 1]);
         qa[k][3] = split2<TYPE == LK_KV_BF16>(x[4 * k + 2], x[4 * k + 3]);
+        if constexpr (QT) {
+          qc[k][0] = round2<true>(x[4 * k], x[4 * k + 1]);
+          qc[k][1] = round2<true>(x[4 * k + 2], x[4 * k + 3]);
+        }
       }
     }
 
@@ -303,16 +310,20 @@ __global__ void __launch_bounds__(32 * Cfg<TYPE, D>::NW, 1) attn_kernel(const __
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         if constexpr (!Q8) {
-          float c[4] = {0.f, 0.f, 0.f, 0.f};
+          float c[4] = {0.f, 0.f, 0.f, 0.f}, c3[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
           for (int j = 0; j < D / 32; ++j) {
             // piece 4 (j & 1) + t of the token's part j >> 1
             const uint4 w = lds128(st + (j >> 1) * (UNIT * 128) + (8 * i + g) * 128 + (((4 * (j & 1) + t) ^ g) << 4));
             mma16<TYPE>(c, qa[2 * j][0], qa[2 * j][1], qa[2 * j][2], qa[2 * j][3], w.x, w.y);
             mma16<TYPE>(c, qa[2 * j + 1][0], qa[2 * j + 1][1], qa[2 * j + 1][2], qa[2 * j + 1][3], w.z, w.w);
+            if constexpr (QT) {
+              mma16<TYPE>(c3, qc[2 * j][0], 0u, qc[2 * j][1], 0u, w.x, w.y);
+              mma16<TYPE>(c3, qc[2 * j + 1][0], 0u, qc[2 * j + 1][1], 0u, w.z, w.w);
+            }
           }
-          sc[i][0] = (c[0] + c[2]) * rs;
-          sc[i][1] = (c[1] + c[3]) * rs;
+          sc[i][0] = (c[0] + (c[2] + c3[0])) * rs;
+          sc[i][1] = (c[1] + (c[3] + c3[1])) * rs;
         } else {
           const int key = 8 * i + g, fk = D == 128 ? g : (key >> 1) & 3;  // the swizzle
           // scales of keys 8 i + 2 t, + 1

@@ -11,9 +11,11 @@
 // the other's products.  More than 128 rows: a stream has 128 of the rows and
 // both use each tile; else both have the same rows and take the tiles in turn.
 //
-// Precision as in the streaming kernel: keys and values enter as stored,
-// queries and weights as two 16-bit terms (the low term's MMAs accumulate on
-// the high term's); a tile's weighted values start a fresh accumulator and are
+// Precision as in the streaming kernel, but for bf16's queries: keys and values
+// enter as stored, queries and weights as two 16-bit terms (the low term's MMAs
+// accumulate on the high term's; a third bf16 term of the queries would take the
+// room of the second stream's, or of the ring, for errors of 2e-6 of the result's
+// norm that long f32 sums have too); a tile's weighted values start a fresh accumulator and are
 // added in f32 registers, 128 keys at a time.
 //
 // Roles: warp 0 issues the MMAs (one thread), warps 2 and 3 fill a ring of
