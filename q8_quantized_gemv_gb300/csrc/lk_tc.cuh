@@ -48,11 +48,12 @@ __device__ __forceinline__ void bar_expect(unsigned bar, unsigned bytes) {  // o
   asm volatile("{\n\t.reg .b64 st;\n\tmbarrier.arrive.expect_tx.shared::cta.b64 st, [%0], %1;\n\t}" ::"r"(bar), "r"(bytes)
                : "memory");
 }
-// The same without the limit's early end by other threads: drains copies.
+// For copies and products in flight when a block gives up: no early end by other
+// threads, and a second at least, however short the waits' limit is.
 __device__ __forceinline__ bool bar_drain(unsigned bar, unsigned parity, unsigned long long limit_ns) {
-  const unsigned long long t0 = now_ns();
+  const unsigned long long t0 = now_ns(), limit = limit_ns > 1000000000ull ? limit_ns : 1000000000ull;
   while (!bar_try(bar, parity))
-    if (now_ns() - t0 > limit_ns) return false;
+    if (now_ns() - t0 > limit) return false;
   return true;
 }
 
