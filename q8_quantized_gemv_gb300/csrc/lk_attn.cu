@@ -178,7 +178,7 @@ __global__ void __launch_bounds__(32 * Cfg<TYPE, D>::NW, 1) attn_kernel(const __
       const int key = c.u * UNIT + 16 * hf;
       pg[hf] = -1;
       if (key < c.n) {
-        const int p = __ldg(table + (key >> a.page_log2));
+        const int p = __ldca(table + (key >> a.page_log2));
         if ((unsigned)p < (unsigned)a.n_pages) pg[hf] = p;
       }
     }

@@ -122,7 +122,7 @@ __device__ __forceinline__ uint4 tile_scales(const AttnArgs& a, const uint16_t* 
   const int lane = threadIdx.x & 31, grp = lane / LPG, k0 = key0 + 16 * grp, p = __shfl_sync(FULL, pg, grp & 3);
   in = grp < 4 && p >= 0;
   const long r = (((long)max(p, 0) * a.n_kv + kvh) << a.page_log2) + (k0 & ((1 << a.page_log2) - 1));
-  return in ? __ldg((const uint4*)(sc + r * (D / 32)) + lane % LPG) : make_uint4(0, 0, 0, 0);
+  return in ? __ldca((const uint4*)(sc + r * (D / 32)) + lane % LPG) : make_uint4(0, 0, 0, 0);
 }
 
 __device__ __forceinline__ uint4 lds128(unsigned at) {
@@ -357,7 +357,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
           const int t = tile_of_fill(g, i, is_v), key0 = (g.ub + t) * KT;
           int pg = -1;
           if (lane < 4 && key0 + 16 * lane < g.n) {
-            pg = __ldg(table + ((key0 + 16 * lane) >> a.page_log2));
+            pg = __ldca(table + ((key0 + 16 * lane) >> a.page_log2));
             if ((unsigned)pg >= (unsigned)a.n_pages) pg = -1;
           }
           const unsigned there = __ballot_sync(FULL, pg >= 0), bar = raw_bar + 8 * (n_raw & 1);
@@ -398,7 +398,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
           // pages of the part's groups of 16 tokens
           int pg = -1;
           if (lane < TOK / 16 && key0 + 16 * lane < g.n) {
-            pg = __ldg(table + ((key0 + 16 * lane) >> a.page_log2));
+            pg = __ldca(table + ((key0 + 16 * lane) >> a.page_log2));
             if ((unsigned)pg >= (unsigned)a.n_pages) pg = -1;
           }
           const bool all = __all_sync(FULL, lane >= TOK / 16 || pg >= 0) && key0 + TOK <= g.n;
@@ -546,7 +546,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
       const auto look = [&](int j) {
         key0 = (g.ub + (g.both ? j : 2 * j + x)) * KT;
         int pg = -1;
-        if (lane < KT / 16 && key0 + 16 * lane < g.n) pg = __ldg(table + ((key0 + 16 * lane) >> a.page_log2));
+        if (lane < KT / 16 && key0 + 16 * lane < g.n) pg = __ldca(table + ((key0 + 16 * lane) >> a.page_log2));
         if ((unsigned)pg >= (unsigned)a.n_pages) pg = -1;
         there = __ballot_sync(FULL, pg >= 0);
         if constexpr (Q8) {  // reciprocals of powers of two
