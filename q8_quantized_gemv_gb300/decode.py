@@ -47,7 +47,9 @@ class Attention:
 
     State: lens (int32 [batch], the sequences' own tokens, advanced by one at
     the start of every token where a sequence is), table int32 [batch, pages],
-    prefix_table, caches (one lk.KvCache per layer)."""
+    prefix_table, caches (one lk.KvCache per layer).  It belongs to one stack.
+    A sequence at its capacity takes no further token: what the stack computes
+    for it then means nothing.  room() says how many tokens all still take."""
 
     def __init__(self, kv="f16", head_dim=128, page=64, capacity=4096, tokens=0, prefix=0, qk_norm=True,
                  rope_base=1e6):
@@ -58,6 +60,8 @@ class Attention:
 
     def build(self, layers, q_dim, kv_dim, batch, seed, dev):
         D, page, B = self.D, self.page, batch
+        if hasattr(self, "caches"):
+            raise ValueError("this Attention has the caches of another stack")
         if q_dim % D or kv_dim % D or (q_dim // D) % (kv_dim // D):
             raise ValueError("q_dim and kv_dim must be heads of head_dim, the query heads a multiple of the others")
         self.n_q, self.n_kv = q_dim // D, kv_dim // D
@@ -102,6 +106,10 @@ class Attention:
     def restart(self):
         """Back to the tokens the caches began with."""
         self.lens.copy_(self.lens0)
+
+    def room(self):
+        """Tokens that every sequence still takes (waits for the device)."""
+        return self.capacity - max(0, int(self.lens.max()))
 
     def step(self, l, q, k, v, mode, act, eps, cfg):
         """Layer l's append and attention; returns the o projection's

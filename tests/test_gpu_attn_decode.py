@@ -124,3 +124,21 @@ def test_attention_needs_its_dataflow():
         DecodeStack(**SMALL, attn=Attention(capacity=64, tokens=64))
     with pytest.raises(ValueError):
         Attention(kv="f32")
+
+
+def test_attention_belongs_to_one_stack():
+    at = Attention(page=16, capacity=34, tokens=[30, -1])
+    st = DecodeStack(**SMALL, batch=2, attn=at)
+    with pytest.raises(ValueError):
+        DecodeStack(**SMALL, batch=2, attn=at)
+    for left in (4, 3, 2, 1):
+        assert at.room() == left
+        st.run_token()
+    assert at.room() == 0
+    # what a full sequence does not take changes nothing in the cache
+    before = [t.clone() for c in at.caches for t in (c.k, c.v)]
+    st.run_token()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, t) for a, t in zip(before, [t for c in at.caches for t in (c.k, c.v)]))
+    at.restart()
+    assert at.room() == 4
