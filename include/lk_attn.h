@@ -7,6 +7,11 @@
  * The conventions of lk.h hold: device pointers owned by the caller, nothing
  * allocated, asynchronous on the given stream, arguments checked before
  * anything is launched, cfg as everywhere (these calls use its pdl field).
+ * Make the first call on a device before any stream capture there (it looks up
+ * addresses and sets kernel attributes).  Device-side waits are bounded (option
+ * "wait_us"); one that runs out ends its kernel and sets the error word
+ * (lk_device_error), the results being then undefined.
+ *
  * The pages the other entry points cite have no counterpart of these; they
  * are the library's own.
  *
@@ -17,10 +22,11 @@
  *
  * The cache.  k and v are pages of `page` tokens:
  *     [n_pages][n_kv][page][head_dim]
- * of f16, bf16 or int8 levels (n_pages * n_kv * page < 2^31); LK_KV_Q8 holds one f16 scale per 32 values of
- * a token's head in ks, vs [n_pages][n_kv][page][head_dim/32] (NULL for the
- * other types), the value being scale * level.  k, v, ks and vs are 16-byte
- * aligned; head_dim is 64 or 128; page a power of two, 16 .. 1024.  Token j of
+ * of f16, bf16 or int8 levels (n_pages * n_kv * page < 2^31); LK_KV_Q8 holds
+ * one f16 scale per 32 values of a token's head in ks, vs
+ * [n_pages][n_kv][page][head_dim/32] (NULL for the other types), the value
+ * being scale * level.  k, v, ks and vs are 16-byte aligned; head_dim is 64 or
+ * 128; page a power of two, 16 .. 1024.  Token j of
  * sequence b lies in page table[b*table_w + j/page] (int32, device), slot
  * j % page.  The table is B rows of table_w page numbers; a sequence has room
  * for table_w * page tokens.  A page number outside [0, n_pages) is never
@@ -77,7 +83,8 @@ typedef struct {
  *            a prefix that the sequences share)
  * A row is left out, nothing of it written (qr and cache), if p < 0
  * (a padding sequence has lens[b] <= 0), if p0 + p >= n_pos (rot > 0), or if
- * token p has no page.  n_q is a positive multiple of n_kv.
+ * token p has no page (a full sequence: what attention then makes of the old qr
+ * means nothing).  n_q is a positive multiple of n_kv, at most 4096.
  */
 lk_status lk_kv_append(const lk_kv_cache* cache, const float* q, const float* k, const float* v, long ld, int n_q,
                        const int32_t* table, int table_w, const int32_t* lens, int B, int R, int p0,
@@ -100,7 +107,8 @@ lk_status lk_kv_append(const lk_kv_cache* cache, const float* q, const float* k,
  * 2^-20 of its norm).  The result does not depend on timing: the same call gives
  * the same bits.  The same row may differ in its last bits between calls of
  * other B, R or lens (the keys are split between blocks by all of them).
- *   q     f32 [M][n_q*head_dim], 16-byte aligned
+ *   q     f32 [M][n_q*head_dim], 16-byte aligned, finite (a row that is not
+ *         changes no other row's result)
  *   mode, out, hq, hl, hs   the result for the next projection, as
  *         lk_swiglu_quant gives it: out f32 [M][n_q*head_dim] (required under
  *         LK_DEQUANT, else optional; may be q), under LK_INT8ACT / LK_TWOPASS

@@ -480,6 +480,100 @@ def test_offsets_past_32_bits():
         torch.cuda.empty_cache()
 
 
+@pytest.mark.parametrize("type_", list(TYPES))
+@pytest.mark.parametrize("R", [1, 12])
+def test_attn_nothing_to_see(type_, R):
+    """No sequence has a token."""
+    out, _ = run_attn(type_, 128, 8, 2, 16, R, [0, -1, 0])
+    assert (out == 0).all()
+    run_attn(type_, 64, 8, 2, 1024, R, [0, 0], prefix=3)
+
+
+@pytest.mark.parametrize("type_", list(TYPES))
+def test_attn_many_rows_on_large_pages(type_):
+    run_attn(type_, 128, 8, 2, 1024, 64, [1500])
+    run_attn(type_, 64, 8, 2, 256, 16, [999, 20, 256])
+
+
+@pytest.mark.parametrize("type_", list(TYPES))
+@pytest.mark.parametrize("R", [1, 16])
+def test_attn_a_bad_row_changes_no_other(type_, R):
+    """Padding rows may hold anything: NaN and infinity stay in their rows."""
+    g = gen(61)
+    cache, _, _ = make_cache(type_, 60, 2, 16, 128, g)
+    table = make_table(3, 12, 60, g)
+    lens = torch.tensor([150, 0, 77], dtype=torch.int32, device=DEV)
+    q = torch.randn((3 * R, 16 * 128), generator=g, device=DEV)
+    ws, want, out = workspace(cache, 16, 3, R), torch.empty_like(q), torch.empty_like(q)
+    lk.lk_attn(cache, q, table, lens, ws, R=R, out=want)
+    bad = q.clone()
+    bad[R:2 * R] = float("nan")
+    bad[0, :128], bad[0, 128:256] = float("inf"), float("nan")
+    lk.lk_attn(cache, bad, table, lens, ws, R=R, out=out)
+    assert (out[R:2 * R] == 0).all()
+    assert torch.equal(out[0, 256:], want[0, 256:])
+    assert torch.equal(out[1:R], want[1:R]) and torch.equal(out[2 * R:], want[2 * R:])
+
+
+def test_one_workspace_for_calls_in_a_row():
+    """Dependent launches of different calls on one stream share a workspace."""
+    g = gen(71)
+    cfg = lk.launch_cfg(pdl=1)
+    cache, _, _ = make_cache("f16", 700, 4, 32, 128, g)
+    ptable = torch.arange(600, 700, dtype=torch.int32, device=DEV)
+    calls, n = [], 0
+    for B, R, shared in ((4, 1, False), (2, 20, False), (8, 1, True), (64, 1, True), (1, 3, False)):
+        table = torch.randint(0, 600, (B, 40), generator=g, device=DEV, dtype=torch.int32)
+        lens = torch.randint(R, 1280, (B,), generator=g, device=DEV, dtype=torch.int32)
+        q = torch.randn((B * R, 16 * 128), generator=g, device=DEV)
+        n = max(n, lk.lk_attn_workspace_bytes(16, 4, 128, B, R, shared))
+        calls.append((B, R, shared, table, lens, q, torch.empty_like(q), torch.empty_like(q)))
+    ws = torch.empty((n,), dtype=torch.uint8, device=DEV)
+
+    def run(c, out, cfg=None):
+        B, R, shared, table, lens, q = c[:6]
+        if shared:
+            lk.lk_attn_shared(cache, q, ptable, 3190, table, lens, ws, R=R, out=out, cfg=cfg)
+        else:
+            lk.lk_attn(cache, q, table, lens, ws, R=R, out=out, cfg=cfg)
+
+    for c in calls:
+        run(c, c[6])
+        torch.cuda.synchronize()
+    for _ in range(10):
+        for c in calls:
+            run(c, c[7], cfg)
+    torch.cuda.synchronize()
+    for c in calls:
+        assert torch.equal(c[6], c[7])
+
+
+def test_shortest_wait_limit():
+    """Under the shortest limit a call either keeps it and gives its result or
+    raises the error word; the context and the next calls are as they were."""
+    for type_ in TYPES:
+        g = gen(81)
+        cache, _, _ = make_cache(type_, 500, 2, 64, 128, g)
+        table = make_table(2, 200, 500, g)
+        lens = torch.tensor([12000, 9000], dtype=torch.int32, device=DEV)
+        for R in (1, 24):
+            q = torch.randn((2 * R, 8 * 128), generator=g, device=DEV)
+            ws, want, out = workspace(cache, 8, 2, R), torch.empty_like(q), torch.empty_like(q)
+            lk.lk_attn(cache, q, table, lens, ws, R=R, out=want)
+            torch.cuda.synchronize()
+            assert lk.lk_device_error(reset=True) == 0
+            lk.lk_set_option("wait_us", 1)
+            try:
+                lk.lk_attn(cache, q, table, lens, ws, R=R, out=out)
+                torch.cuda.synchronize()
+            finally:
+                lk.lk_set_option("wait_us", 0)
+            assert lk.lk_device_error(reset=True) != 0 or torch.equal(out, want)
+            lk.lk_attn(cache, q, table, lens, ws, R=R, out=out)
+            torch.cuda.synchronize()
+            assert lk.lk_device_error(reset=True) == 0 and torch.equal(out, want)
+
+
 # ---- a run of them together ------------------------------------------------------------
 
 @pytest.mark.parametrize("type_", list(TYPES))
