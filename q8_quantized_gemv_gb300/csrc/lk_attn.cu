@@ -15,8 +15,8 @@
 // that the low terms stay normal: queries to a row maximum of 2^10, weights by
 // 2^14 (Q8: by 2^10, their scales by what brings the largest to 8 .. 16, and the
 // product of the two again as two terms).  bf16 has too few bits for two terms
-// of a query (errors of 3e-6 of the result's norm where f32 arithmetic has 7e-7): a third
-// one has MMAs of its own.  Each unit's weighted values are summed in a fresh
+// of a query (errors of 3e-6 of the result's norm where f32 arithmetic has 7e-7):
+// a third one has MMAs of its own.  Each unit's weighted values are summed in a fresh
 // accumulator and added in f32, so the MMA's own accumulation never runs over
 // more than 32 keys.
 //
@@ -28,6 +28,12 @@
 // no value changes lanes.  Copies by the threads themselves (cp.async) were
 // measured slower: a warp gets one 512-byte copy instruction through per
 // ~190 cycles, 5.1 TB/s with 7 warps.
+//
+// Measured (GPU time of a whole call, with its join): 64 x 8192 tokens f16, 32 query /
+// 8 key heads of 128: 322 us, 6.67 TB/s; 16 ragged up to 16384 bf16 100 us, 5.7
+// TB/s (98 us with two query terms); 1 x 131071 Q8 63 us, 4.5 TB/s, bound by the
+// issue of its instructions (58 % of the slots), not by memory; 1 x 1023 f16 9.4
+// us, launches and dependent reads.
 #include <cuda_bf16.h>
 
 #include "lk_attn.cuh"
