@@ -106,7 +106,7 @@ lk_status lk_kv_append(const lk_kv_cache* cache, const float* q, const float* k,
  * plus (2^-27 + N 2^-32) max|v| over its N tokens; on the whole far nearer (about
  * 2^-20 of its norm).  The result does not depend on timing: the same call gives
  * the same bits.  The same row may differ in its last bits between calls of
- * other B, R or lens (the keys are split between blocks by all of them).
+ * other B, R, lens or table_w (the keys are split between blocks by all of them).
  *   q     f32 [M][n_q*head_dim], 16-byte aligned, finite (a row that is not
  *         changes no other row's result)
  *   mode, out, hq, hl, hs   the result for the next projection, as
@@ -148,8 +148,10 @@ size_t lk_attn_workspace_bytes(int n_q, int n_kv, int head_dim, int B, int R, in
 /* Kernels that such a call launches (lk_attn: prefix_len 0): the streaming
  * kernel (up to 8 query rows on each read of the keys) and / or the tile kernel
  * (tcgen05, up to 256; chosen by rows, type and prefix length), and the join of
- * their partial results.  0 for arguments the calls refuse and for no rows. */
-int lk_attn_launches(int type, int n_q, int n_kv, int head_dim, int B, int R, int prefix_len);
+ * their partial results; few sequences with little room (table_w * page tokens)
+ * take the streaming kernel in clusters, which join their own.  0 for arguments
+ * the calls refuse and for no rows. */
+int lk_attn_launches(int type, int n_q, int n_kv, int head_dim, int B, int R, int prefix_len, int room);
 
 #ifdef __cplusplus
 }

@@ -29,12 +29,17 @@
 // measured slower: a warp gets one 512-byte copy instruction through per
 // ~190 cycles, 5.1 TB/s with 7 warps.
 //
+// Few sequences with little room take the same kernel in clusters of up to 8 blocks to
+// an item, whose partials stay in shared memory (cluster_size).
+//
 // Measured (GPU time of a whole call, with its join): 64 x 8192 tokens f16, 32 query /
 // 8 key heads of 128: 322 us, 6.67 TB/s; 16 ragged up to 16384 bf16 100 us, 5.7
 // TB/s (98 us with two query terms); 1 x 131071 Q8 63 us, 4.5 TB/s, bound by the
-// issue of its instructions (58 % of the slots), not by memory; 1 x 1023 f16 9.4
-// us, launches and dependent reads.
+// issue of its instructions (58 % of the slots), not by memory; 1 x 1023 f16 in
+// clusters 6.2 us (9.3 by the deal and the join), a launch and dependent reads.
 #include <cuda_bf16.h>
+
+#include <type_traits>
 
 #include "lk_attn.cuh"
 #include "lk_tc.cuh"
@@ -78,6 +83,30 @@ __device__ __forceinline__ unsigned lds32(unsigned a) {
 }
 
 constexpr int ERR_ATTN_WAIT = 32;
+
+// ---- clusters ---------------------------------------------------------------------------
+constexpr int kMaxCluster = 8;
+// All threads of all blocks of the cluster; every block comes here, whatever
+// became of its own waits, which are bounded.
+__device__ __forceinline__ void cluster_meet() {
+  __syncwarp();
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ unsigned cluster_addr(unsigned at, unsigned rank) {
+  unsigned r;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(at), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ void ld_far(unsigned at, float& x, float& y) {
+  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(x), "=f"(y) : "r"(at) : "memory");
+}
+__device__ __forceinline__ void ld_far(unsigned at, float (&v)[2]) { ld_far(at, v[0], v[1]); }
+__device__ __forceinline__ void ld_far(unsigned at, float (&v)[4]) {
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3])
+               : "r"(at)
+               : "memory");
+}
 
 template <int TYPE, int D>
 struct Cfg {
@@ -135,18 +164,64 @@ __device__ __forceinline__ void advance(const AttnArgs& a, const Deal& d, Cursor
     }
 }
 
-template <int TYPE, int D>
-__global__ void __launch_bounds__(32 * Cfg<TYPE, D>::NW, 1) attn_kernel(const __grid_constant__ AttnArgs a) {
+// What both ways of joining write: rows, and / or words and scales.
+struct JoinArgs {
+  AttnArgs a;
+  float* out;
+  int8_t* hq;
+  int8_t* hl;
+  float* hs;
+  int mode;
+  int wide;  // out takes a lane's values in one store
+};
+
+// Row and head w (row * n_q + head): a lane's D / 32 neighbouring sums over the
+// weights' sum, as f32 and / or quantized.
+template <int Q, int D>
+__device__ __forceinline__ void finish(const JoinArgs& j, long w, float (&acc)[D / 32], float ls, int lane) {
+  constexpr int V = D / 32;
+#pragma unroll
+  for (int c = 0; c < V; ++c) acc[c] = ls > 0.0f ? __fdiv_rn(acc[c], ls) : 0.0f;
+  if (j.out) {
+    float* y = j.out + w * D + lane * V;
+    if (j.wide) {
+      if constexpr (V == 4) *(float4*)y = *(const float4*)acc;
+      else *(float2*)y = *(const float2*)acc;
+    } else {
+#pragma unroll
+      for (int c = 0; c < V; ++c) y[c] = acc[c];
+    }
+  }
+  if constexpr (Q > 0) {
+#pragma unroll
+    for (int c = 0; c < V; ++c) {
+      // value 32 c + lane is in lane (32 c + lane) / V
+      float y = 0.0f;
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        const float t = __shfl_sync(FULL, acc[e], (32 * c + lane) / V);
+        y = lane % V == e ? t : y;
+      }
+      quant_lane<Q>(y, j.hq, j.hl, j.hs, w * (D / 32) + c, lane);
+    }
+  }
+}
+
+// CL: the blocks of an item are a cluster and join their parts themselves (j);
+// else a is all, and parts go to the workspace.
+template <int TYPE, int D, bool CL>
+__device__ __forceinline__ void attn_body(const AttnArgs& a, const JoinArgs* j) {
   typedef Cfg<TYPE, D> C;
   constexpr bool Q8 = TYPE == LK_KV_Q8;
   constexpr int KS = D / 16;  // k-steps of a score
   constexpr int NT = D / 8;   // n-tiles of the output
   constexpr bool QT = TYPE == LK_KV_BF16;  // a third term of the queries
   extern __shared__ unsigned char raw[];
-  __shared__ Deal deal;
+  __shared__ std::conditional_t<CL, int, Deal> deal_place;
   __shared__ float wml[C::NW][TR][2];
   __shared__ __align__(8) unsigned long long bars[C::NW * C::ST];
   __shared__ int abort_flag;
+  __shared__ __align__(8) float cml[CL ? TR : 1][2];
   unsigned char* smem = raw + ((1024u - (smem_addr(raw) & 1023u)) & 1023u);
   if (threadIdx.x < C::NW * C::ST) bar_init(smem_addr(bars + threadIdx.x), 1);
   if (threadIdx.x == 0) {
@@ -159,21 +234,50 @@ __global__ void __launch_bounds__(32 * Cfg<TYPE, D>::NW, 1) attn_kernel(const __
   // before it waits for this one (the join's deal): so the wait comes first
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" :::);
-  if (threadIdx.x < 32) make_deal<false>(a, deal);
+  if constexpr (!CL)
+    if (threadIdx.x < 32) make_deal<false>(a, deal_place);
   __syncthreads();
   const int lane = threadIdx.x & 31, warp = __shfl_sync(FULL, threadIdx.x >> 5, 0), g = lane >> 2, t = lane & 3;
-  const int T = deal.cum[a.B + a.shared];
-  if (T == 0) return;
-  const Shares blocks = stream_blocks(a, C::NW, T);
-  if (blocks.begin(blockIdx.x) >= T) return;
-  const int ca = blocks.begin(blockIdx.x), cn = blocks.size(blockIdx.x), we = min(C::NW, cn);
-  const Shares warps(cn, we);
-  const int wa = warp < we ? warps.begin(warp) : cn;
-  int left = warp < we ? warps.size(warp) : 0;  // units the warp has to do
-  Cursor cc = cursor_at(a, deal, ca);
-  const bool one = cc.u + cn <= cc.un;  // the block's units are all one item's: its warps join their parts
+  int cn, we, wa, left;  // units of the block, its warps with units; the warp's first and their number
+  Cursor cc;
+  bool one;  // the block's units are all one item's: its warps join their parts
+  if constexpr (CL) {
+    const int item = (int)blockIdx.x / a.C, rank = (int)blockIdx.x - item * a.C;
+    cc.tiles = groups_of<false>(a, 0);
+    const int items = a.n_kv * cc.tiles, li = item - item / items * items;
+    cc.s = item / items;
+    cc.kvh = li / cc.tiles;
+    cc.tile = li - cc.kvh * cc.tiles;
+    cc.n = min(max(__ldcg(a.lens + cc.s), 0), a.table_w << a.page_log2);
+    cc.un = (cc.n + UNIT - 1) / UNIT;
+    cc.u = cn = 0;
+    if (cc.un > 0) {
+      const Shares blocks(cc.un, min(a.C, cc.un));
+      cc.u = rank < blocks.k ? blocks.begin(rank) : cc.un;
+      cn = rank < blocks.k ? blocks.size(rank) : 0;
+    }
+    one = true;
+  } else {
+    const Deal& deal = deal_place;
+    const int T = deal.cum[a.B + a.shared];
+    if (T == 0) return;
+    const Shares blocks = stream_blocks(a, C::NW, T);
+    if (blocks.begin(blockIdx.x) >= T) return;
+    cn = blocks.size(blockIdx.x);
+    cc = cursor_at(a, deal, blocks.begin(blockIdx.x));
+    one = cc.u + cn <= cc.un;
+  }
+  we = min(C::NW, cn);
+  const Shares warps(cn, max(we, 1));
+  wa = warp < we ? warps.begin(warp) : cn;
+  left = warp < we ? warps.size(warp) : 0;
   if (one) cc.u += wa;
-  else if (left > 0) cc = cursor_at(a, deal, ca + wa);
+  else if constexpr (!CL)
+    if (left > 0) cc = cursor_at(a, deal_place, stream_blocks(a, C::NW, deal_place.cum[a.B + a.shared]).begin(blockIdx.x) + wa);
+  const auto next = [&](Cursor& c) {
+    if constexpr (CL) ++c.u;
+    else advance(a, deal_place, c);
+  };
   const unsigned ring = smem_addr(smem) + warp * C::ST * C::STAGE, bar0 = smem_addr(bars) + 8 * warp * C::ST;
 
   // pages of a unit's two halves (-1: none)
@@ -231,7 +335,7 @@ __global__ void __launch_bounds__(32 * Cfg<TYPE, D>::NW, 1) attn_kernel(const __
       c[i] = ac;
       if (i < ask) {
         pages(ac, p[i]);
-        advance(a, deal, ac);
+        next(ac);
       }
     }
     if (ask > C::ST) pages(ac, pg);
@@ -526,14 +630,14 @@ __global__ void __launch_bounds__(32 * Cfg<TYPE, D>::NW, 1) attn_kernel(const __
       __syncwarp();  // every lane is done with the stage
       if (ask > 0) {
         issue(ac, pg, stage);
-        advance(a, deal, ac);
+        next(ac);
         if (--ask > 0) pages(ac, pg);
       }
       stage = stage + 1 == C::ST ? 0 : stage + 1;
     }
     if (fail) break;
     cc.u = ue - 1;
-    if (left > 0) advance(a, deal, cc);
+    if (left > 0) next(cc);
 
     // ---- its partial
     if constexpr (Q8) {
@@ -567,12 +671,13 @@ __global__ void __launch_bounds__(32 * Cfg<TYPE, D>::NW, 1) attn_kernel(const __
     for (int i = 0; i < C::ST; ++i)
       if ((asked >> i) & 1u) bar_drain(bar0 + 8 * i, (phases >> i) & 1u, a.wait_ns);
   }
-  if (!one || __syncthreads_or(abort_flag)) return;
+  if constexpr (CL) __syncthreads();
+  else if (!one || __syncthreads_or(abort_flag)) return;
 
   // ---- one item: the warps' partials, joined in warp order
   {
     const int s = cc.s, nrows = min(TR, rows_of(a, s) - cc.tile * TR);
-    const long slot = (long)blockIdx.x * C::NW + item0<false>(a, s) + cc.item();
+    const long slot = CL ? 0 : (long)blockIdx.x * C::NW + item0<false>(a, s) + cc.item();
     for (int i = threadIdx.x; i < nrows * D; i += 32 * C::NW) {
       const int r = i / D, d = i - r * D;
       float M = -INFINITY;
@@ -585,22 +690,62 @@ __global__ void __launch_bounds__(32 * Cfg<TYPE, D>::NW, 1) attn_kernel(const __
         acc = fmaf(f, ov, acc);
         ls = fmaf(f, wml[w][r][1], ls);
       }
-      a.o[(slot * TR + r) * D + d] = acc;
-      if (d == 0) *(float2*)(a.ml + (slot * TR + r) * 2) = make_float2(M, ls);
+      if constexpr (CL) {
+        // in the first warp's place: each value's only reader is its writer
+        *(float*)(smem + (size_t)(r * (D + 4) + d) * 4) = acc;
+        if (d == 0) cml[r][0] = M, cml[r][1] = ls;
+      } else {
+        a.o[(slot * TR + r) * D + d] = acc;
+        if (d == 0) *(float2*)(a.ml + (slot * TR + r) * 2) = make_float2(M, ls);
+      }
+    }
+    if constexpr (CL) {
+      // ---- the cluster's partials, joined in rank order: row r by block r % C
+      cluster_meet();
+      for (int r = (int)blockIdx.x % a.C + warp * a.C; r < nrows; r += C::NW * a.C) {
+        constexpr int V = D / 32;
+        float m[kMaxCluster], l[kMaxCluster], o[kMaxCluster][V], M = -INFINITY;
+#pragma unroll
+        for (int c = 0; c < kMaxCluster; ++c) {
+          // (a rank that is not there: the last one's again, with weight 0)
+          const unsigned from = min(c, a.C - 1);
+          ld_far(cluster_addr(smem_addr(&cml[r][0]), from), m[c], l[c]);
+          ld_far(cluster_addr(smem_addr(smem) + (r * (D + 4) + lane * V) * 4, from), o[c]);
+          if (c >= a.C) m[c] = -INFINITY;
+          M = fmaxf(M, m[c]);
+        }
+        const float ref = M == -INFINITY ? 0.0f : M;
+        float acc[V], ls = 0.0f;
+#pragma unroll
+        for (int e = 0; e < V; ++e) acc[e] = 0.0f;
+#pragma unroll
+        for (int c = 0; c < kMaxCluster; ++c) {
+          const float f = ex2(m[c] - ref);
+          ls = fmaf(f, l[c], ls);
+#pragma unroll
+          for (int e = 0; e < V; ++e) acc[e] = fmaf(f, o[c][e], acc[e]);
+        }
+        const int ri = cc.tile * TR + r, tok = ri / a.G;
+        const long w = (long)(s * a.R + tok) * a.n_q + cc.kvh * a.G + (ri - tok * a.G);
+        if (j->mode == LK_DEQUANT) finish<0, D>(*j, w, acc, ls, lane);
+        else if (j->mode == LK_INT8ACT) finish<1, D>(*j, w, acc, ls, lane);
+        else finish<2, D>(*j, w, acc, ls, lane);
+      }
+      cluster_meet();  // a block's parts are there until all have read them
     }
   }
 }
 
-// ---- the join: one warp per row and query head ---------------------------------------
-struct JoinArgs {
-  AttnArgs a;
-  float* out;
-  int8_t* hq;
-  int8_t* hl;
-  float* hs;
-  int wide;  // out takes a lane's values in one store
-};
+template <int TYPE, int D>
+__global__ void __launch_bounds__(32 * Cfg<TYPE, D>::NW, 1) attn_kernel(const __grid_constant__ AttnArgs a) {
+  attn_body<TYPE, D, false>(a, nullptr);
+}
+template <int TYPE, int D>
+__global__ void __launch_bounds__(32 * Cfg<TYPE, D>::NW, 1) attn_cluster_kernel(const __grid_constant__ JoinArgs j) {
+  attn_body<TYPE, D, true>(j.a, &j);
+}
 
+// ---- the join: one warp per row and query head ---------------------------------------
 // Partials of a row from one item: entry i (0 <= i < n) has its maximum and
 // sum at ml + 2 at(i), its values at o + D at(i); the values' 16-byte pieces are
 // permuted by flip (tile partials).  Streaming: n0 warps of the item's first
@@ -748,31 +893,7 @@ __global__ void __launch_bounds__(128) attn_join_kernel(const JoinArgs j) {
       }
     }
   }
-#pragma unroll
-  for (int c = 0; c < V; ++c) acc[c] = ls > 0.0f ? __fdiv_rn(acc[c], ls) : 0.0f;
-  if (j.out) {
-    float* y = j.out + w * D + lane * V;
-    if (j.wide) {
-      if constexpr (V == 4) *(float4*)y = *(const float4*)acc;
-      else *(float2*)y = *(const float2*)acc;
-    } else {
-#pragma unroll
-      for (int c = 0; c < V; ++c) y[c] = acc[c];
-    }
-  }
-  if constexpr (Q > 0) {
-#pragma unroll
-    for (int c = 0; c < V; ++c) {
-      // value 32 c + lane is in lane (32 c + lane) / V
-      float y = 0.0f;
-#pragma unroll
-      for (int e = 0; e < V; ++e) {
-        const float t = __shfl_sync(FULL, acc[e], (32 * c + lane) / V);
-        y = lane % V == e ? t : y;
-      }
-      quant_lane<Q>(y, j.hq, j.hl, j.hs, w * (D / 32) + c, lane);
-    }
-  }
+  finish<Q, D>(j, w, acc, ls, lane);
 }
 
 // ---- host --------------------------------------------------------------------------
@@ -794,6 +915,24 @@ bool tiled(long rows, int type, int D, long keys) {
   return keys < 0 || rows * keys * D >= (q8 ? 1L << 26 : 1L << 25);
 }
 
+// Blocks of an item (up to 8 rows of one key/value head and sequence) where they
+// are a cluster that joins its own partials: one launch, no deal.  0 where the
+// equal deal to all SMs and the join launch do better.  `room`: tokens the table
+// has room for; how many there are is not known here.  64 blocks in clusters
+// of 8 or 128 in smaller ones run at once (128 in eights took two rounds: 5.8
+// us became 10.1).  Measured (GPU time, cluster / deal and join, us; 8 kv heads
+// of 128, 4 query heads each; f16, Q8 nearly the same):
+//   B 1, C 8: 256 tokens 5.5 / 8.3, 1000 6.2 / 9.3, 4000 9.5 / 12.3, 8000 12.7 / 15.9
+//   B 4, C 4: 256 5.9 / 9.4, 1000 8.3 / 10.5, 4000 13.6 / 17.8
+//   B 16, C 1: 256 8.3 / 12.2, 1000 13.3 / 17.5
+// one sequence full, the others 100: B 4 4000 12.6 / 14.1, B 16 1000 12.6 / 10.1: a
+// long sequence among short ones loses at small C, and more so beyond this room.
+int cluster_size(long items, long room, bool alone) {
+  if (!alone) return 0;
+  const int C = items <= 8 ? 8 : items <= 32 ? 4 : items <= 64 ? 2 : items <= 128 ? 1 : 0;
+  return room <= 1024L * C ? C : 0;
+}
+
 struct Plan {
   long slots, tslots[2];  // streaming partials; tile partials of sequences, prefix
   int tsr[2];             // rows of a tile slot
@@ -811,6 +950,10 @@ Plan plan(int n_q, int n_kv, int B, int R, int type, int D, long prefix) {
     p.tslots[x] = kTileWorkers + many[x] * ((rows[x] + 127) / 128);  // items of 128 rows or of 256
   }
   return p;
+}
+
+int clusters(const Plan& p, long G, int n_kv, int B, int R, long prefix, long room) {
+  return cluster_size((long)B * n_kv * ((R * G + TR - 1) / TR), room, !prefix && !p.tslots[0]);
 }
 
 size_t up256(size_t n) { return (n + 255) / 256 * 256; }
@@ -869,6 +1012,18 @@ lk_status run_type(const AttnArgs& a, int pdl, cudaStream_t stream) {
              : LK_ERR_CUDA;
 }
 
+template <int TYPE, int D>
+lk_status run_cluster(const JoinArgs& j, int pdl, cudaStream_t stream) {
+  static std::atomic<int> done[kMaxDevices];
+  typedef Cfg<TYPE, D> C;
+  if (!prepare_kernel(attn_cluster_kernel<TYPE, D>, done, C::RING)) return LK_ERR_CUDA;
+  const int items = j.a.B * j.a.n_kv * (int)((j.a.R * j.a.G + TR - 1) / TR);
+  return launch(attn_cluster_kernel<TYPE, D>, dim3(items * j.a.C), dim3(32 * C::NW), C::RING, pdl, stream, j, j.a.C) ==
+                 cudaSuccess
+             ? LK_OK
+             : LK_ERR_CUDA;
+}
+
 template <int Q, int D>
 lk_status run_join(const JoinArgs& j, cudaStream_t stream) {
   static std::atomic<int> done[kMaxDevices];
@@ -885,6 +1040,12 @@ lk_status run_d(JoinArgs& j, int type, lk_mode mode, int pdl, cudaStream_t strea
   lk_status st = LK_OK;
   a.NW = type == LK_KV_Q8 ? Cfg<LK_KV_Q8, D>::NW : Cfg<LK_KV_F16, D>::NW;
   const int page = 1 << a.page_log2;
+  if (a.C) {
+    if ((st = make_maps(a, type, D, page < UNIT ? page : UNIT))) return st;
+    return type == LK_KV_F16    ? run_cluster<LK_KV_F16, D>(j, pdl, stream)
+           : type == LK_KV_BF16 ? run_cluster<LK_KV_BF16, D>(j, pdl, stream)
+                                : run_cluster<LK_KV_Q8, D>(j, pdl, stream);
+  }
   // the launches after the first are dependents of the one before
   if (!a.own_tiled || (a.shared && !a.pre_tiled)) {
     if ((st = make_maps(a, type, D, page < UNIT ? page : UNIT))) return st;
@@ -918,12 +1079,12 @@ size_t lk_attn_workspace_bytes(int n_q, int n_kv, int head_dim, int B, int R, in
   return layout(plan(n_q, n_kv, B, R, -1, head_dim, shared != 0), head_dim, ml, o);
 }
 
-int lk_attn_launches(int type, int n_q, int n_kv, int head_dim, int B, int R, int prefix_len) {
-  if (type < LK_KV_F16 || type > LK_KV_Q8 || prefix_len < 0 || !lk_attn_workspace_bytes(n_q, n_kv, head_dim, B, R, 0)) return 0;
+int lk_attn_launches(int type, int n_q, int n_kv, int head_dim, int B, int R, int prefix_len, int room) {
+  if (type < LK_KV_F16 || type > LK_KV_Q8 || prefix_len < 0 || room < 0 || !lk_attn_workspace_bytes(n_q, n_kv, head_dim, B, R, 0)) return 0;
   if (B == 0 || R == 0) return 0;
   const Plan p = plan(n_q, n_kv, B, R, type, head_dim, prefix_len);
   const bool tile = p.tslots[0] || p.tslots[1], stream = !p.tslots[0] || (prefix_len && !p.tslots[1]);
-  return 1 + tile + stream;
+  return clusters(p, n_q / n_kv, n_kv, B, R, prefix_len, room) ? 1 : 1 + tile + stream;
 }
 
 lk_status lk_attn_shared(const lk_kv_cache* cache, const float* q, int n_q, const int32_t* prefix_table,
@@ -980,6 +1141,7 @@ lk_status lk_attn_shared(const lk_kv_cache* cache, const float* q, int n_q, cons
   layout(p, cache->head_dim, ml, o);
   a.own_tiled = p.tslots[0] > 0;
   a.pre_tiled = p.tslots[1] > 0;
+  a.C = clusters(p, a.G, a.n_kv, B, R, prefix_len, (long)table_w * cache->page);
   a.ml = (float*)((char*)ws + ml[0]);
   a.o = (float*)((char*)ws + o[0]);
   for (int x = 0; x < 2; ++x) {
@@ -1001,6 +1163,7 @@ lk_status lk_attn_shared(const lk_kv_cache* cache, const float* q, int n_q, cons
   j.hq = hq;
   j.hl = mode == LK_TWOPASS ? hl : nullptr;
   j.hs = hs;
+  j.mode = mode;
   const int pdl = cfg_pdl(cfg);
   return cache->head_dim == 128 ? run_d<128>(j, cache->type, mode, pdl, stream)
                                 : run_d<64>(j, cache->type, mode, pdl, stream);

@@ -88,6 +88,7 @@ struct AttnArgs {
   float* o;           //   [slot][TR][D] weighted values
   float* tml[2];      // tile partials of the sequences, the prefix: [slot][slot rows][2],
   float* to[2];       //   [slot][slot rows][D], tflip: 16-byte pieces permuted in 128 bytes by row & 7
+  int C;              // blocks of a cluster (attn_cluster_kernel), else 0
   int W, NW, TW;      // blocks and warps of the streaming launch, blocks of the tile launch
   int tunit_log2, trows_log2;  // keys of a unit, rows of an item of the tile kernel
   int tflip;          // whether its partials' pieces are permuted
@@ -267,17 +268,27 @@ __device__ __forceinline__ float row_shift(float amax, float& back) {
 
 // ---- host -------------------------------------------------------------------------------
 template <typename A>
-cudaError_t launch(void (*f)(A), dim3 grid, dim3 block, int smem, int pdl, cudaStream_t stream, const A& args) {
+cudaError_t launch(void (*f)(A), dim3 grid, dim3 block, int smem, int pdl, cudaStream_t stream, const A& args,
+                   int cluster = 0) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = block;
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchAttribute attr[2];
+  int n = 0;
+  if (pdl) {
+    attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[n++].val.programmaticStreamSerializationAllowed = 1;
+  }
+  if (cluster) {
+    attr[n].id = cudaLaunchAttributeClusterDimension;
+    attr[n].val.clusterDim.x = cluster;
+    attr[n].val.clusterDim.y = attr[n].val.clusterDim.z = 1;
+    ++n;
+  }
   cfg.attrs = attr;
-  cfg.numAttrs = pdl ? 1 : 0;
+  cfg.numAttrs = n;
   const cudaError_t e = cudaLaunchKernelEx(&cfg, f, args);
   if (e != cudaSuccess) cudaGetLastError();
   return e;

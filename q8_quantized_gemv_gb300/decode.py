@@ -127,7 +127,7 @@ class Attention:
 
     def launches(self):
         """Of one layer: the append and the attention's."""
-        return 1 + lk.lk_attn_launches(self.caches[0], self.n_q, self.lens.numel(), 1, self.prefix)
+        return 1 + lk.lk_attn_launches(self.caches[0], self.n_q, *self.table.shape, 1, self.prefix)
 
 
 class DecodeStack:

@@ -123,7 +123,7 @@ def _load():
         "lk_attn": ([P, P, I, P, I, P, I, I, F, I, P, P, P, P, P, S, P, P], I),
         "lk_attn_shared": ([P, P, I, P, I, I, P, I, P, I, I, F, I, P, P, P, P, P, S, P, P], I),
         "lk_attn_workspace_bytes": ([I, I, I, I, I, I], S),
-        "lk_attn_launches": ([I, I, I, I, I, I, I], I),
+        "lk_attn_launches": ([I, I, I, I, I, I, I, I], I),
     }
     for name, (args, res) in sig.items():
         fn = getattr(lib, name)
@@ -580,9 +580,11 @@ def lk_attn_workspace_bytes(n_q, n_kv, head_dim, B, R=1, shared=False) -> int:
     return _load().lk_attn_workspace_bytes(n_q, n_kv, head_dim, B, R, 1 if shared else 0)
 
 
-def lk_attn_launches(cache, n_q, B, R=1, prefix_len=0) -> int:
-    """Kernels that lk_attn (lk_attn_shared) on this cache launches."""
-    return _load().lk_attn_launches(cache.c.type, n_q, cache.n_kv, cache.head_dim, B, R, prefix_len)
+def lk_attn_launches(cache, n_q, B, table_w, R=1, prefix_len=0) -> int:
+    """Kernels that lk_attn (lk_attn_shared) on this cache launches, with tables
+    of table_w pages."""
+    return _load().lk_attn_launches(cache.c.type, n_q, cache.n_kv, cache.head_dim, B, R, prefix_len,
+                                    table_w * cache.c.page)
 
 
 def _attn_tail(cache, q, M, scale, mode, out, hq, hl, hs, ws):

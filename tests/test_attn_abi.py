@@ -114,14 +114,18 @@ def test_workspace_bytes(lib):
 
 
 def test_launches(lib):
-    f = lib.lk_attn_launches
-    assert f(0, 32, 8, 128, 1, 1, 0) == 2                 # streaming, join
-    assert f(0, 32, 8, 128, 1, 64, 0) == 2                # tile, join
-    assert f(1, 32, 8, 128, 64, 1, 32768) == 3            # tile (prefix), streaming (own), join
-    assert f(1, 32, 8, 128, 64, 1, 100) == 2              # a short prefix streams too
-    assert f(2, 32, 8, 64, 4, 8, 0) == 2 and f(2, 32, 8, 64, 4, 9, 50000) == 2
-    assert f(3, 32, 8, 128, 1, 1, 0) == 0 and f(0, 32, 5, 128, 1, 1, 0) == 0 and f(0, 32, 8, 128, 65, 1, 0) == 0
-    assert f(0, 32, 8, 128, 0, 1, 0) == 0 and f(0, 32, 8, 128, 1, 1, -1) == 0
+    f, much = lib.lk_attn_launches, 1 << 20
+    assert f(0, 32, 8, 128, 1, 1, 0, much) == 2                 # streaming, join
+    assert f(0, 32, 8, 128, 1, 64, 0, 1000) == 2                # tile, join
+    assert f(1, 32, 8, 128, 64, 1, 32768, 1000) == 3            # tile (prefix), streaming (own), join
+    assert f(1, 32, 8, 128, 64, 1, 100, 1000) == 2              # a short prefix streams too
+    assert f(2, 32, 8, 64, 4, 8, 0, much) == 2 and f(2, 32, 8, 64, 4, 9, 50000, much) == 2
+    assert f(0, 32, 8, 128, 1, 1, 0, 1024) == 1                 # clusters
+    assert f(0, 32, 8, 128, 1, 1, 10, 1024) == 2
+    assert f(0, 32, 8, 128, 64, 1, 0, 1024) == 2
+    assert f(3, 32, 8, 128, 1, 1, 0, 1) == 0 and f(0, 32, 5, 128, 1, 1, 0, 1) == 0
+    assert f(0, 32, 8, 128, 65, 1, 0, 1) == 0 and f(0, 32, 8, 128, 0, 1, 0, 1) == 0
+    assert f(0, 32, 8, 128, 1, 1, -1, 1) == 0 and f(0, 32, 8, 128, 1, 1, 0, -1) == 0
 
 
 def test_binding_refusals():

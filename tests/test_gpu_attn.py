@@ -74,6 +74,11 @@ def make_table(B, width, n_pages, g, first=0):
     return (torch.randperm(n_pages - first, generator=g, device=DEV)[:B * width] + first).to(torch.int32).view(B, width)
 
 
+def roomy(table, page):
+    """The table with room for 5000 tokens more (no pages there)."""
+    return torch.cat([table, torch.full((table.shape[0], -(-5000 // page)), -1, device=DEV, dtype=torch.int32)], 1)
+
+
 def poison(cache, table, lens, page):
     """Everything of the sequences' pages behind their tokens becomes NaN (the
     levels of a Q8 cache -128, its scales NaN)."""
@@ -306,6 +311,11 @@ def run_attn(type_, D, n_q, n_kv, page, R, lens, seed=3, prefix=0, spread=1.0, s
     assert (out[-1] == 9.0).all()
     want, tol = reference(kd, vd, q, table, lens, R, sc, (ptable, prefix) if prefix else None, type_ == "bf16")
     check(out[:-1], want, tol)
+    if not prefix:  # with room for more, the keys are split in another way
+        lk.lk_attn(cache, q, roomy(table, page), lt, ws, R=R, scale=scale, out=out[:-1])
+        torch.cuda.synchronize()
+        assert (out[-1] == 9.0).all()
+        check(out[:-1], want, tol)
     return out[:-1], want
 
 
@@ -419,11 +429,14 @@ def test_shared_prefix_padding_and_empty():
 
 @pytest.mark.parametrize("mode", [1, 2])
 @pytest.mark.parametrize("D", [64, 128])
-def test_attn_quantized_output(mode, D):
+@pytest.mark.parametrize("room", [False, True])
+def test_attn_quantized_output(mode, D, room):
     """The words are the quantizer's of the f32 rows, which they do not change."""
     g = gen(21)
     cache, _, _ = make_cache("q8", 40, 2, 32, D, g)
     table = make_table(4, 8, 40, g)
+    if room:
+        table = roomy(table, 32)
     lens = torch.tensor([200, 0, 1, 77], dtype=torch.int32, device=DEV)
     N = 8 * D
     q = torch.randn((4, N), generator=g, device=DEV)
@@ -496,12 +509,15 @@ def test_attn_many_rows_on_large_pages(type_):
 
 
 @pytest.mark.parametrize("type_", list(TYPES))
+@pytest.mark.parametrize("room", [False, True])
 @pytest.mark.parametrize("R", [1, 16])
-def test_attn_a_bad_row_changes_no_other(type_, R):
+def test_attn_a_bad_row_changes_no_other(type_, R, room):
     """Padding rows may hold anything: NaN and infinity stay in their rows."""
     g = gen(61)
     cache, _, _ = make_cache(type_, 60, 2, 16, 128, g)
     table = make_table(3, 12, 60, g)
+    if room:
+        table = roomy(table, 16)
     lens = torch.tensor([150, 0, 77], dtype=torch.int32, device=DEV)
     q = torch.randn((3 * R, 16 * 128), generator=g, device=DEV)
     ws, want, out = workspace(cache, 16, 3, R), torch.empty_like(q), torch.empty_like(q)
@@ -522,7 +538,7 @@ def test_one_workspace_for_calls_in_a_row():
     cache, _, _ = make_cache("f16", 700, 4, 32, 128, g)
     ptable = torch.arange(600, 700, dtype=torch.int32, device=DEV)
     calls, n = [], 0
-    for B, R, shared in ((4, 1, False), (2, 20, False), (8, 1, True), (64, 1, True), (1, 3, False)):
+    for B, R, shared in ((4, 1, False), (2, 20, False), (8, 1, True), (64, 1, True), (1, 3, False), (9, 1, False)):
         table = torch.randint(0, 600, (B, 40), generator=g, device=DEV, dtype=torch.int32)
         lens = torch.randint(R, 1280, (B,), generator=g, device=DEV, dtype=torch.int32)
         q = torch.randn((B * R, 16 * 128), generator=g, device=DEV)
@@ -554,9 +570,9 @@ def test_shortest_wait_limit():
     for type_ in TYPES:
         g = gen(81)
         cache, _, _ = make_cache(type_, 500, 2, 64, 128, g)
-        table = make_table(2, 200, 500, g)
         lens = torch.tensor([12000, 9000], dtype=torch.int32, device=DEV)
-        for R in (1, 24):
+        for R, width in ((1, 200), (24, 200), (1, 100)):
+            table = make_table(2, width, 500, g)
             q = torch.randn((2 * R, 8 * 128), generator=g, device=DEV)
             ws, want, out = workspace(cache, 8, 2, R), torch.empty_like(q), torch.empty_like(q)
             lk.lk_attn(cache, q, table, lens, ws, R=R, out=want)
@@ -641,12 +657,15 @@ def test_append_and_attend_token_by_token(type_, pdl):
         assert torch.equal(out, got[i])
 
 
-def test_two_streams_with_a_workspace_each():
+@pytest.mark.parametrize("room", [False, True])
+def test_two_streams_with_a_workspace_each(room):
     g = gen(41)
     cache, _, _ = make_cache("bf16", 300, 4, 32, 128, g)
     sets = []
     for i in range(2):
         table = make_table(4, 64, 300, g)
+        if room:
+            table = roomy(table, 32)
         lens = torch.tensor([2000, 100 + i, 33, 1500], dtype=torch.int32, device=DEV)
         q = torch.randn((4, 16 * 128), generator=g, device=DEV)
         sets.append((table, lens, q, workspace(cache, 16, 4, 1), torch.empty_like(q), torch.empty_like(q),
