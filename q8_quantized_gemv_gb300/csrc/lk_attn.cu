@@ -16,7 +16,10 @@
 // 2^14 (Q8: by 2^10, their scales by what brings the largest to 8 .. 16, and the
 // product of the two again as two terms).  bf16 has too few bits for two terms
 // of a query (errors of 3e-6 of the result's norm where f32 arithmetic has 7e-7):
-// a third one has MMAs of its own.  Each unit's weighted values are summed in a fresh
+// a third one has MMAs of its own.  So has a third one of the weights where the
+// table has room for few keys (2e-7 instead of 1e-6 to 2e-6); over long
+// sequences f32 sums have 5e-7 and more, and it would cost 6 % (16 ragged to
+// 16384 100 -> 106 us).  Each unit's weighted values are summed in a fresh
 // accumulator and added in f32, so the MMA's own accumulation never runs over
 // more than 32 keys.
 //
@@ -209,13 +212,14 @@ __device__ __forceinline__ void finish(const JoinArgs& j, long w, float (&acc)[D
 
 // CL: the blocks of an item are a cluster and join their parts themselves (j);
 // else a is all, and parts go to the workspace.
-template <int TYPE, int D, bool CL>
+template <int TYPE, int D, bool CL, bool FINE>
 __device__ __forceinline__ void attn_body(const AttnArgs& a, const JoinArgs* j) {
   typedef Cfg<TYPE, D> C;
   constexpr bool Q8 = TYPE == LK_KV_Q8;
   constexpr int KS = D / 16;  // k-steps of a score
   constexpr int NT = D / 8;   // n-tiles of the output
   constexpr bool QT = TYPE == LK_KV_BF16;  // a third term of the queries
+  constexpr bool WT = QT && FINE;          // and of the weights
   extern __shared__ unsigned char raw[];
   __shared__ std::conditional_t<CL, int, Deal> deal_place;
   __shared__ float wml[C::NW][TR][2];
@@ -520,13 +524,17 @@ __device__ __forceinline__ void attn_body(const AttnArgs& a, const JoinArgs* j) 
         for (int i = 0; i < NT; ++i) O[i][0] *= al, O[i][1] *= al;
       }
       if constexpr (!Q8) {
-        unsigned ph[2][4];
+        unsigned ph[2][4], pc[WT ? 2 : 1][2];
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
           ph[k][0] = split2<TYPE == LK_KV_BF16>(p[2 * k][0], p[2 * k][1]);
           ph[k][2] = split2<TYPE == LK_KV_BF16>(p[2 * k + 1][0], p[2 * k + 1][1]);
           ph[k][1] = split2<TYPE == LK_KV_BF16>(p[2 * k][0], p[2 * k][1]);
           ph[k][3] = split2<TYPE == LK_KV_BF16>(p[2 * k + 1][0], p[2 * k + 1][1]);
+          if constexpr (WT) {
+            pc[k][0] = round2<true>(p[2 * k][0], p[2 * k][1]);
+            pc[k][1] = round2<true>(p[2 * k + 1][0], p[2 * k + 1][1]);
+          }
         }
 #pragma unroll
         for (int h = 0; h < D / 64; ++h) {
@@ -544,9 +552,12 @@ __device__ __forceinline__ void attn_body(const AttnArgs& a, const JoinArgs* j) 
             const unsigned sel = j & 1 ? 0x7632 : 0x5410;
             float c[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-            for (int k = 0; k < 2; ++k)
-              mma16<TYPE>(c, ph[k][0], ph[k][1], ph[k][2], ph[k][3], prmt(w[4 * k][j >> 1], w[4 * k + 1][j >> 1], sel),
-                          prmt(w[4 * k + 2][j >> 1], w[4 * k + 3][j >> 1], sel));
+            for (int k = 0; k < 2; ++k) {
+              const unsigned b0 = prmt(w[4 * k][j >> 1], w[4 * k + 1][j >> 1], sel),
+                             b1 = prmt(w[4 * k + 2][j >> 1], w[4 * k + 3][j >> 1], sel);
+              mma16<TYPE>(c, ph[k][0], ph[k][1], ph[k][2], ph[k][3], b0, b1);
+              if constexpr (WT) mma16<TYPE>(c, pc[k][0], 0u, pc[k][1], 0u, b0, b1);
+            }
             O[8 * h + j][0] += c[0] + c[2];
             O[8 * h + j][1] += c[1] + c[3];
           }
@@ -736,13 +747,13 @@ __device__ __forceinline__ void attn_body(const AttnArgs& a, const JoinArgs* j) 
   }
 }
 
-template <int TYPE, int D>
+template <int TYPE, int D, bool FINE>
 __global__ void __launch_bounds__(32 * Cfg<TYPE, D>::NW, 1) attn_kernel(const __grid_constant__ AttnArgs a) {
-  attn_body<TYPE, D, false>(a, nullptr);
+  attn_body<TYPE, D, false, FINE>(a, nullptr);
 }
 template <int TYPE, int D>
 __global__ void __launch_bounds__(32 * Cfg<TYPE, D>::NW, 1) attn_cluster_kernel(const __grid_constant__ JoinArgs j) {
-  attn_body<TYPE, D, true>(j.a, &j);
+  attn_body<TYPE, D, true, true>(j.a, &j);
 }
 
 // ---- the join: one warp per row and query head ---------------------------------------
@@ -925,35 +936,39 @@ bool tiled(long rows, int type, int D, long keys) {
 //   B 1, C 8: 256 tokens 5.5 / 8.3, 1000 6.2 / 9.3, 4000 9.5 / 12.3, 8000 12.7 / 15.9
 //   B 4, C 4: 256 5.9 / 9.4, 1000 8.3 / 10.5, 4000 13.6 / 17.8
 //   B 16, C 1: 256 8.3 / 12.2, 1000 13.3 / 17.5
+// and against the tile kernel, rows on the same keys (its join included):
+//   32 rows, C 4: f16 500 7.3 / 12.4, 4000 14.7 / 18.1; Q8 4000 14.4 / 17.1
+//   64 rows, C 2: f16 500 9.3 / 12.8, 2000 14.8 / 16.3; bf16 16.6 / 15.8; Q8 14.2 / 19.8
+//   256 rows, 2 kv heads, C 2: f16 500 9.1 / 14.9, 2000 14.2 / 15.6; Q8 14.0 / 23.3
 // one sequence full, the others 100: B 4 4000 12.6 / 14.1, B 16 1000 12.6 / 10.1: a
 // long sequence among short ones loses at small C, and more so beyond this room.
-int cluster_size(long items, long room, bool alone) {
-  if (!alone) return 0;
+int cluster_size(long items, long room) {
   const int C = items <= 8 ? 8 : items <= 32 ? 4 : items <= 64 ? 2 : items <= 128 ? 1 : 0;
   return room <= 1024L * C ? C : 0;
 }
 
+// Up to as many keys bf16's weights have a third term too.
+constexpr long kFineKeys = 4096;
+
 struct Plan {
   long slots, tslots[2];  // streaming partials; tile partials of sequences, prefix
   int tsr[2];             // rows of a tile slot
+  int C;                  // blocks of a cluster, 0: no clusters
 };
 
 // type < 0: the most that any call of the sizes takes.
-Plan plan(int n_q, int n_kv, int B, int R, int type, int D, long prefix) {
+Plan plan(int n_q, int n_kv, int B, int R, int type, int D, long prefix, long room) {
   const long G = n_q / n_kv, rows[2] = {R * G, (long)B * R * G}, many[2] = {(long)B * n_kv, prefix ? n_kv : 0};
   Plan p = {};
+  if (type >= 0 && !prefix) p.C = cluster_size(many[0] * ((rows[0] + TR - 1) / TR), room);
   p.slots = (long)kMaxWorkers * kMaxWarps;
   for (int x = 0; x < 2; ++x) {
     p.slots += many[x] * ((rows[x] + TR - 1) / TR);
-    if (!many[x] || !(type < 0 ? rows[x] > 16 : tiled(rows[x], type, D, x ? prefix : -1))) continue;
+    if (!many[x] || p.C || !(type < 0 ? rows[x] > 16 : tiled(rows[x], type, D, x ? prefix : -1))) continue;
     p.tsr[x] = tile_slot_rows(rows[x]);
     p.tslots[x] = kTileWorkers + many[x] * ((rows[x] + 127) / 128);  // items of 128 rows or of 256
   }
   return p;
-}
-
-int clusters(const Plan& p, long G, int n_kv, int B, int R, long prefix, long room) {
-  return cluster_size((long)B * n_kv * ((R * G + TR - 1) / TR), room, !prefix && !p.tslots[0]);
 }
 
 size_t up256(size_t n) { return (n + 255) / 256 * 256; }
@@ -1002,12 +1017,12 @@ lk_status make_maps(AttnArgs& a, int type, int D, int box) {
   return LK_OK;
 }
 
-template <int TYPE, int D>
+template <int TYPE, int D, bool FINE>
 lk_status run_type(const AttnArgs& a, int pdl, cudaStream_t stream) {
   static std::atomic<int> done[kMaxDevices];
   typedef Cfg<TYPE, D> C;
-  if (!prepare_kernel(attn_kernel<TYPE, D>, done, C::RING)) return LK_ERR_CUDA;
-  return launch(attn_kernel<TYPE, D>, dim3(a.W), dim3(32 * C::NW), C::RING, pdl, stream, a) == cudaSuccess
+  if (!prepare_kernel(attn_kernel<TYPE, D, FINE>, done, C::RING)) return LK_ERR_CUDA;
+  return launch(attn_kernel<TYPE, D, FINE>, dim3(a.W), dim3(32 * C::NW), C::RING, pdl, stream, a) == cudaSuccess
              ? LK_OK
              : LK_ERR_CUDA;
 }
@@ -1049,9 +1064,12 @@ lk_status run_d(JoinArgs& j, int type, lk_mode mode, int pdl, cudaStream_t strea
   // the launches after the first are dependents of the one before
   if (!a.own_tiled || (a.shared && !a.pre_tiled)) {
     if ((st = make_maps(a, type, D, page < UNIT ? page : UNIT))) return st;
-    st = type == LK_KV_F16    ? run_type<LK_KV_F16, D>(a, pdl, stream)
-         : type == LK_KV_BF16 ? run_type<LK_KV_BF16, D>(a, pdl, stream)
-                              : run_type<LK_KV_Q8, D>(a, pdl, stream);
+    // (beside the tile kernel's partials, which have two, it would be lost)
+    const bool fine = !a.own_tiled && !a.pre_tiled && (long)a.table_w << a.page_log2 <= kFineKeys && a.plen <= kFineKeys;
+    st = type == LK_KV_F16  ? run_type<LK_KV_F16, D, false>(a, pdl, stream)
+         : type == LK_KV_Q8 ? run_type<LK_KV_Q8, D, false>(a, pdl, stream)
+         : fine             ? run_type<LK_KV_BF16, D, true>(a, pdl, stream)
+                            : run_type<LK_KV_BF16, D, false>(a, pdl, stream);
     pdl = 1;
     a.late = 1;
   }
@@ -1076,15 +1094,15 @@ size_t lk_attn_workspace_bytes(int n_q, int n_kv, int head_dim, int B, int R, in
   if ((head_dim != 64 && head_dim != 128) || n_kv < 1 || n_q < n_kv || n_q % n_kv || n_q > 4096) return 0;
   if (B < 0 || R < 0 || B > LK_MAX_BATCH || R > LK_MAX_BATCH || B * R > LK_MAX_BATCH) return 0;
   size_t ml[3], o[3];
-  return layout(plan(n_q, n_kv, B, R, -1, head_dim, shared != 0), head_dim, ml, o);
+  return layout(plan(n_q, n_kv, B, R, -1, head_dim, shared != 0, 0), head_dim, ml, o);
 }
 
 int lk_attn_launches(int type, int n_q, int n_kv, int head_dim, int B, int R, int prefix_len, int room) {
   if (type < LK_KV_F16 || type > LK_KV_Q8 || prefix_len < 0 || room < 0 || !lk_attn_workspace_bytes(n_q, n_kv, head_dim, B, R, 0)) return 0;
   if (B == 0 || R == 0) return 0;
-  const Plan p = plan(n_q, n_kv, B, R, type, head_dim, prefix_len);
+  const Plan p = plan(n_q, n_kv, B, R, type, head_dim, prefix_len, room);
   const bool tile = p.tslots[0] || p.tslots[1], stream = !p.tslots[0] || (prefix_len && !p.tslots[1]);
-  return clusters(p, n_q / n_kv, n_kv, B, R, prefix_len, room) ? 1 : 1 + tile + stream;
+  return p.C ? 1 : 1 + tile + stream;
 }
 
 lk_status lk_attn_shared(const lk_kv_cache* cache, const float* q, int n_q, const int32_t* prefix_table,
@@ -1136,12 +1154,12 @@ lk_status lk_attn_shared(const lk_kv_cache* cache, const float* q, int n_q, cons
   a.plen = prefix_len;
   a.shared = shared;
   a.qscale = scale * 1.44269504088896340736f;
-  const Plan p = plan(n_q, cache->n_kv, B, R, cache->type, cache->head_dim, prefix_len);
+  const Plan p = plan(n_q, cache->n_kv, B, R, cache->type, cache->head_dim, prefix_len, (long)table_w * cache->page);
   size_t ml[3], o[3];
   layout(p, cache->head_dim, ml, o);
   a.own_tiled = p.tslots[0] > 0;
   a.pre_tiled = p.tslots[1] > 0;
-  a.C = clusters(p, a.G, a.n_kv, B, R, prefix_len, (long)table_w * cache->page);
+  a.C = p.C;
   a.ml = (float*)((char*)ws + ml[0]);
   a.o = (float*)((char*)ws + o[0]);
   for (int x = 0; x < 2; ++x) {
