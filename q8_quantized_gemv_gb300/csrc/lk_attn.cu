@@ -244,6 +244,7 @@ __device__ __forceinline__ void attn_body(const AttnArgs& a, const JoinArgs* j) 
   const int lane = threadIdx.x & 31, warp = __shfl_sync(FULL, threadIdx.x >> 5, 0), g = lane >> 2, t = lane & 3;
   int cn, we, wa, left;  // units of the block, its warps with units; the warp's first and their number
   Cursor cc;
+  int pu = 0;  // clusters: units of the prefix, which come before the sequence's own
   bool one;  // the block's units are all one item's: its warps join their parts
   if constexpr (CL) {
     const int item = (int)blockIdx.x / a.C, rank = (int)blockIdx.x - item * a.C;
@@ -252,8 +253,10 @@ __device__ __forceinline__ void attn_body(const AttnArgs& a, const JoinArgs* j) 
     cc.s = item / items;
     cc.kvh = li / cc.tiles;
     cc.tile = li - cc.kvh * cc.tiles;
-    cc.n = min(max(__ldcg(a.lens + cc.s), 0), a.table_w << a.page_log2);
-    cc.un = (cc.n + UNIT - 1) / UNIT;
+    const int len = __ldcg(a.lens + cc.s);
+    cc.n = min(max(len, 0), a.table_w << a.page_log2);
+    if (a.shared && len >= 0) pu = (a.plen + UNIT - 1) / UNIT;
+    cc.un = pu + (cc.n + UNIT - 1) / UNIT;
     cc.u = cn = 0;
     if (cc.un > 0) {
       const Shares blocks(cc.un, min(a.C, cc.un));
@@ -286,12 +289,14 @@ __device__ __forceinline__ void attn_body(const AttnArgs& a, const JoinArgs* j) 
 
   // pages of a unit's two halves (-1: none)
   auto pages = [&](const Cursor& c, int (&pg)[2]) {
-    const int* table = c.s == a.B ? a.ptable : a.table + (long)c.s * a.table_w;
+    const bool pre = CL ? c.u < pu : c.s == a.B;
+    const int* table = pre ? a.ptable : a.table + (long)c.s * a.table_w;
+    const int n = CL && pre ? a.plen : c.n, key0 = (CL && !pre ? c.u - pu : c.u) * UNIT;
 #pragma unroll
     for (int hf = 0; hf < 2; ++hf) {
-      const int key = c.u * UNIT + 16 * hf;
+      const int key = key0 + 16 * hf;
       pg[hf] = -1;
-      if (key < c.n) {
+      if (key < n) {
         const int p = __ldca(table + (key >> a.page_log2));
         if ((unsigned)p < (unsigned)a.n_pages) pg[hf] = p;
       }
@@ -312,7 +317,7 @@ __device__ __forceinline__ void attn_body(const AttnArgs& a, const JoinArgs* j) 
     bar_expect(bar, bytes);
     for (int hf = 0; hf < n_box; ++hf) {
       if (pg[hf] < 0) continue;
-      const int key0 = c.u * UNIT + 16 * hf;
+      const int key0 = (CL && c.u >= pu ? c.u - pu : c.u) * UNIT + 16 * hf;
       const int r0 = ((pg[hf] * a.n_kv + c.kvh) << a.page_log2) + (key0 & ((1 << a.page_log2) - 1));
 #pragma unroll
       for (int p = 0; p < C::PARTS; ++p) {
@@ -353,7 +358,7 @@ __device__ __forceinline__ void attn_body(const AttnArgs& a, const JoinArgs* j) 
   bool fail = false;
   while (left > 0) {
     // ---- an item
-    const int s = cc.s, n = cc.n, kvh = cc.kvh, tile = cc.tile;
+    const int s = cc.s, kvh = cc.kvh, tile = cc.tile;
     const bool pre = s == a.B;
     const int nrows = min(TR, rows_of(a, s) - tile * TR);
     const long slot = (long)blockIdx.x * C::NW + (one ? 0 : warp) + item0<false>(a, s) + cc.item();
@@ -361,8 +366,8 @@ __device__ __forceinline__ void attn_body(const AttnArgs& a, const JoinArgs* j) 
     const int ri = tile * TR + min(g, nrows - 1);
     const int tok = ri / a.G;  // row of the batch (prefix) or of the sequence
     const int row = pre ? tok : s * a.R + tok;
-    int vis = n;  // keys that the row sees
-    if (!pre) vis = min(n, max(0, __ldcg(a.lens + s) - a.R + 1 + tok));
+    int row_vis = cc.n;  // keys that the row sees
+    if (!pre) row_vis = min(cc.n, max(0, __ldcg(a.lens + s) - a.R + 1 + tok));
     unsigned qa[KS][4], qc[QT ? KS : 1][2];
     float rs = 1.0f;
     {
@@ -471,13 +476,15 @@ __device__ __forceinline__ void attn_body(const AttnArgs& a, const JoinArgs* j) 
       }
       // ---- what the row does not see
       const bool in0 = (there >> (2 * stage)) & 1u, in1 = (there >> (2 * stage + 1)) & 1u;  // the halves' pages
-      const bool whole = (u + 1) * UNIT <= n && in0 && in1;
-      if (!__all_sync(FULL, whole && (u + 1) * UNIT <= vis)) {
+      const bool of_pre = CL && u < pu;
+      const int k0 = (CL && !of_pre ? u - pu : u) * UNIT, n = of_pre ? a.plen : cc.n, vis = of_pre ? a.plen : row_vis;
+      const bool whole = k0 + UNIT <= n && in0 && in1;
+      if (!__all_sync(FULL, whole && k0 + UNIT <= vis)) {
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
           for (int x = 0; x < 2; ++x)
-            if (u * UNIT + 8 * i + 2 * t + x >= vis || !(i < 2 ? in0 : in1)) sc[i][x] = -INFINITY;
+            if (k0 + 8 * i + 2 * t + x >= vis || !(i < 2 ? in0 : in1)) sc[i][x] = -INFINITY;
       }
       // ---- running maximum, weights
       float mt = fmaxf(fmaxf(fmaxf(sc[0][0], sc[0][1]), fmaxf(sc[1][0], sc[1][1])),
@@ -505,7 +512,7 @@ __device__ __forceinline__ void attn_body(const AttnArgs& a, const JoinArgs* j) 
         for (int i = 0; i < HW; ++i) {
           const int w = i * 32 + lane;
           unsigned x = lds32(st + 2 * C::KV + C::SC + w * 4) & 0x7fff7fffu;
-          if (u * UNIT + w / HW >= n || !(w / HW < 16 ? in0 : in1)) x = 0;
+          if (k0 + w / HW >= n || !(w / HW < 16 ? in0 : in1)) x = 0;
           mx = max(mx, max(x & 0xffffu, x >> 16));
         }
         mx = __reduce_max_sync(FULL, mx);
@@ -544,7 +551,7 @@ __device__ __forceinline__ void attn_body(const AttnArgs& a, const JoinArgs* j) 
             const int key = 16 * (e >> 2) + 2 * t + (e & 1) + 8 * ((e >> 1) & 1);
             uint4 x = lds128(st + C::KV + h * (UNIT * 128) + key * 128 + ((g ^ (key & 7)) << 4));
             // what lies behind the tokens may be anything: 0 * NaN is not 0
-            if (!whole && (u * UNIT + key >= n || !(e < 4 ? in0 : in1))) x = make_uint4(0, 0, 0, 0);
+            if (!whole && (k0 + key >= n || !(e < 4 ? in0 : in1))) x = make_uint4(0, 0, 0, 0);
             w[e][0] = x.x, w[e][1] = x.y, w[e][2] = x.z, w[e][3] = x.w;
           }
 #pragma unroll
@@ -585,7 +592,7 @@ __device__ __forceinline__ void attn_body(const AttnArgs& a, const JoinArgs* j) 
             const uint2 w = lds64(st + 2 * C::KV + C::SC + (8 * i + 2 * t) * 4);
             d0[i][0] = *(const __half2*)&w.x, d1[i][0] = *(const __half2*)&w.y;
           }
-          const int key = u * UNIT + 8 * i + 2 * t;
+          const int key = k0 + 8 * i + 2 * t;
 #pragma unroll
           for (int x = 0; x < D / 64; ++x) {
             if (!whole) {
@@ -927,7 +934,8 @@ bool tiled(long rows, int type, int D, long keys) {
 }
 
 // Blocks of an item (up to 8 rows of one key/value head and sequence) where they
-// are a cluster that joins its own partials: one launch, no deal.  0 where the
+// are a cluster that joins its own partials: one launch, no deal (and a shared
+// prefix is read by every sequence, from L2).  0 where the
 // equal deal to all SMs and the join launch do better.  `room`: tokens the table
 // has room for; how many there are is not known here.  64 blocks in clusters
 // of 8 or 128 in smaller ones run at once (128 in eights took two rounds: 5.8
@@ -960,7 +968,7 @@ struct Plan {
 Plan plan(int n_q, int n_kv, int B, int R, int type, int D, long prefix, long room) {
   const long G = n_q / n_kv, rows[2] = {R * G, (long)B * R * G}, many[2] = {(long)B * n_kv, prefix ? n_kv : 0};
   Plan p = {};
-  if (type >= 0 && !prefix) p.C = cluster_size(many[0] * ((rows[0] + TR - 1) / TR), room);
+  if (type >= 0) p.C = cluster_size(many[0] * ((rows[0] + TR - 1) / TR), prefix + room);
   p.slots = (long)kMaxWorkers * kMaxWarps;
   for (int x = 0; x < 2; ++x) {
     p.slots += many[x] * ((rows[x] + TR - 1) / TR);

@@ -75,8 +75,8 @@ def make_table(B, width, n_pages, g, first=0):
 
 
 def roomy(table, page):
-    """The table with room for 5000 tokens more (no pages there)."""
-    return torch.cat([table, torch.full((table.shape[0], -(-5000 // page)), -1, device=DEV, dtype=torch.int32)], 1)
+    """The table with room for 9000 tokens more (no pages there)."""
+    return torch.cat([table, torch.full((table.shape[0], -(-9000 // page)), -1, device=DEV, dtype=torch.int32)], 1)
 
 
 def poison(cache, table, lens, page):
@@ -311,11 +311,15 @@ def run_attn(type_, D, n_q, n_kv, page, R, lens, seed=3, prefix=0, spread=1.0, s
     assert (out[-1] == 9.0).all()
     want, tol = reference(kd, vd, q, table, lens, R, sc, (ptable, prefix) if prefix else None, type_ == "bf16")
     check(out[:-1], want, tol)
-    if not prefix:  # with room for more, the keys are split in another way
-        lk.lk_attn(cache, q, roomy(table, page), lt, ws, R=R, scale=scale, out=out[:-1])
-        torch.cuda.synchronize()
-        assert (out[-1] == 9.0).all()
-        check(out[:-1], want, tol)
+    # with room for more, the keys are split in another way
+    wide = roomy(table, page)
+    if prefix:
+        lk.lk_attn_shared(cache, q, ptable, prefix, wide, lt, ws, R=R, scale=scale, out=out[:-1])
+    else:
+        lk.lk_attn(cache, q, wide, lt, ws, R=R, scale=scale, out=out[:-1])
+    torch.cuda.synchronize()
+    assert (out[-1] == 9.0).all()
+    check(out[:-1], want, tol)
     return out[:-1], want
 
 
