@@ -121,7 +121,7 @@ def test_launches(lib):
     assert f(1, 32, 8, 128, 64, 1, 100, 1000) == 2              # a short prefix streams too
     assert f(2, 32, 8, 64, 4, 8, 0, much) == 2 and f(2, 32, 8, 64, 4, 9, 50000, much) == 2
     assert f(0, 32, 8, 128, 1, 1, 0, 1024) == 1                 # clusters
-    assert f(0, 32, 8, 128, 1, 1, 10, 1024) == 1 and f(0, 32, 8, 128, 1, 1, 9000, 1024) == 2
+    assert f(0, 32, 8, 128, 1, 1, 10, 1024) == 1 and f(0, 32, 8, 128, 1, 1, 20000, 1024) == 2
     assert f(0, 32, 8, 128, 64, 1, 0, 1024) == 2
     assert f(3, 32, 8, 128, 1, 1, 0, 1) == 0 and f(0, 32, 5, 128, 1, 1, 0, 1) == 0
     assert f(0, 32, 8, 128, 65, 1, 0, 1) == 0 and f(0, 32, 8, 128, 0, 1, 0, 1) == 0
