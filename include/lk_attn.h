@@ -132,7 +132,8 @@ lk_status lk_attn(const lk_kv_cache* cache, const float* q, int n_q, const int32
  * describe each sequence's own tokens, which follow the prefix.  Row b*R + r
  * sees the whole prefix and the first lens[b] - R + 1 + r own tokens (none if
  * that is not positive); a sequence with lens[b] < 0 is padding and gets
- * zeros.  The prefix's keys and values are read for all rows together.
+ * zeros.  The prefix's keys and values are read for all rows together (a short
+ * one by each sequence, where that is faster).
  * The other arguments are lk_attn's; prefix_len 0 is lk_attn (prefix_table
  * may then be NULL).
  */
