@@ -937,24 +937,34 @@ bool tiled(long rows, int type, int D, long keys) {
 // are a cluster that joins its own partials: one launch, no deal, and a shared
 // prefix is read by every sequence, from L2.  0 where the equal deal to all SMs
 // and the join launch, or the tile kernel, do better.  `room`: tokens the table
-// has room for; how many there are is not known here.  64 blocks in clusters
-// of 8 or 128 in smaller ones run at once (128 in eights took two rounds: 5.8
-// us became 10.1).  Measured (GPU time, cluster / deal and join, us; 8 kv heads of
+// has room for; how many there are is not known here.  All clusters run at
+// once: a block has an SM, and 15 clusters of 8, 23 of 6, 28 of 5, 36 of 4, 46 of 3,
+// 76 of 2 fit (cudaOccupancyMaxActiveClusters; 16 of 8 took two rounds: 5.8 us
+// became 10.1).  Measured (GPU time, cluster / deal and join, us; 8 kv heads of
 // 128, 4 query heads each; f16, Q8 nearly the same where it is not named):
 //   B 1, C 8: 256 tokens 5.5 / 8.3, 1000 6.2 / 9.3, 4000 9.5 / 12.3, 8000 12.7 / 15.9,
 //     12700 17.2 / 17.4; D 64 12700 f16 10.2 / 13.6, Q8 12.3 / 11.6, 20000 f16 12.8 / 14.8
+//   B 2, C 6: 250 6.1 / 9.4, 1000 6.9 / 9.7, 4000 10.4 / 15.2 (12.8 with C 4)
 //   B 4, C 4: 256 5.9 / 9.4, 1000 8.3 / 10.5, 4000 13.6 / 17.8
+//   B 5, C 3: 250 6.3 / 9.4, 1000 8.6 / 13.1, 2000 11.0 / 15.3
 //   B 16, C 1: 256 8.3 / 12.2, 1000 13.3 / 17.5
 // against the tile kernel and its join, rows on the same keys:
 //   32 rows, C 4: f16 500 7.3 / 12.4, 4000 14.7 / 18.1; Q8 4000 14.4 / 17.1
 //   64 rows, C 2: f16 500 9.3 / 12.8, 2000 14.8 / 16.3; bf16 16.6 / 15.8; Q8 14.2 / 19.8
 //   256 rows, 2 kv heads, C 2: f16 500 9.1 / 14.9, 2000 14.2 / 15.6; Q8 14.0 / 23.3
-// on a prefix, 5 sequences of 77, C 2: f16 300 7.0 / 14.0, 1900 12.9 / 16.5, 2900
-//   16.3 / 18.8; bf16 1900 15.4 / 16.8; Q8 2900 16.4 / 20.6; D 64 f16 2900 9.8 / 18.2
+// on a prefix, 8 sequences of 77, C 2: f16 300 7.2 / 14.6, 1900 13.1 / 18.1, 2900
+//   16.4 / 19.7; bf16 1900 15.6 / 18.4; Q8 2900 16.6 / 21.8; D 64 f16 2900 10.1 / 18.9
 // One sequence full, the others 100: B 4 4000 12.6 / 14.1, B 16 1000 12.6 / 10.1: a
 // long sequence among short ones loses at small C, and more so beyond that room.
 int cluster_size(long items, bool alone, int type, int D, long prefix, long room) {
-  const long C = items <= 8 ? 8 : items <= 32 ? 4 : items <= 64 ? 2 : items <= 128 ? 1 : 0;
+  const long C = items <= 14   ? 8
+                 : items <= 22 ? 6
+                 : items <= 27 ? 5
+                 : items <= 34 ? 4
+                 : items <= 44 ? 3
+                 : items <= 74 ? 2
+                 : items <= 150 ? 1
+                                : 0;
   const bool half = D == 64 && type != LK_KV_Q8;  // half the time a token; Q8's is not the bytes'
   const long most = (type == LK_KV_BF16 ? 1024 : type == LK_KV_Q8 ? 1400 : 1600) * (half ? 2 : 1) * C;
   return room + prefix <= most && (alone || room <= (half ? 1536 : 1024) * C) ? (int)C : 0;
