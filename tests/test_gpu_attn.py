@@ -498,6 +498,16 @@ def test_offsets_past_32_bits():
 
 
 @pytest.mark.parametrize("type_", list(TYPES))
+@pytest.mark.parametrize("items", [1, 14, 15, 22, 23, 27, 28, 34, 35, 44, 45, 74, 75, 150, 151])
+def test_attn_cluster_sizes(type_, items):
+    """The numbers of key/value heads and sequences where the split changes."""
+    n_kv, B = next((k, items // k) for k in (1, 2, 3, 5, 23, 37, 75, 151) if items % k == 0 and items // k <= 22)
+    lens = [(97 * b + 700) % 901 for b in range(B)]
+    run_attn(type_, 64, 3 * n_kv, n_kv, 32, 1, lens)
+    run_attn(type_, 128, n_kv, n_kv, 64, 1, lens, prefix=45)
+
+
+@pytest.mark.parametrize("type_", list(TYPES))
 @pytest.mark.parametrize("R", [1, 12])
 def test_attn_nothing_to_see(type_, R):
     """No sequence has a token."""
