@@ -269,7 +269,7 @@ __device__ __forceinline__ void attn_body(const AttnArgs& a, const JoinArgs* j) 
     const int T = deal.cum[a.B + a.shared];
     if (T == 0) return;
     const Shares blocks = stream_blocks(a, C::NW, T);
-    if (blocks.begin(blockIdx.x) >= T) return;
+    if ((int)blockIdx.x >= blocks.n) return;
     cn = blocks.size(blockIdx.x);
     cc = cursor_at(a, deal, blocks.begin(blockIdx.x));
     one = cc.u + cn <= cc.un;

@@ -127,25 +127,29 @@ __device__ __forceinline__ int item0(const AttnArgs& a, int s) {
 // general deal; where all items are one sequence's, a group is an item, and no
 // share has pieces of two (a second piece costs the tile kernel some 5 us).
 // With k <= G no share is empty, so an item's segments are in consecutive holders.
+// There are n holders; begin and size are theirs (behind the last one begin
+// would be up to twice the units, which can pass 32 bits).
 struct Shares {
-  int G, k, base, more;
-  __device__ __forceinline__ Shares(int G, int k) : G(G), k(k), base(G / k), more(G - base * k) {}
-  __device__ __forceinline__ int begin(int c) const {
+  int G, k, n, base, more;
+  __host__ __device__ __forceinline__ Shares(int G, int k, int groups = 1)
+      : G(G), k(k), n(groups * k), base(G / k), more(G - base * k) {}
+  __host__ __device__ __forceinline__ int begin(int c) const {
     const int i = c / k, j = c - i * k;
-    return i * G + j * base + min(j, more);
+    return i * G + j * base + (j < more ? j : more);
   }
-  __device__ __forceinline__ int size(int c) const { return base + (c % k < more ? 1 : 0); }
-  __device__ __forceinline__ int holder(int u) const {
+  __host__ __device__ __forceinline__ int size(int c) const { return base + (c % k < more ? 1 : 0); }
+  __host__ __device__ __forceinline__ int holder(int u) const {
     const int i = u / G, r = u - i * G, first = more * (base + 1);
     return i * k + (r < first ? r / (base + 1) : more + (r - first) / base);
   }
 };
 // The deal of T units to at most W blocks, each with at least `least` units
 // where there are enough; `one`: they are one sequence's, in `items` equal items.
-__device__ __forceinline__ Shares deal_blocks(int T, int W, int least, bool one, int items) {
+// T is any number up to 2^31 - 1, but not 0.
+__host__ __device__ __forceinline__ Shares deal_blocks(int T, int W, int least, bool one, int items) {
   const bool each = one && items <= W;
-  const int G = each ? T / items : T;
-  return Shares(G, min(each ? W / items : W, (G + least - 1) / least));
+  const int G = each ? T / items : T, most = each ? W / items : W, full = (G - 1) / least + 1;
+  return Shares(G, most < full ? most : full, each ? items : 1);
 }
 __device__ __forceinline__ Shares tile_blocks(const AttnArgs& a, int T) {
   const bool pre = !a.own_tiled;

@@ -202,8 +202,10 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
   int u0 = 0, u1 = 0;
   if (T > 0) {
     const Shares blocks = tile_blocks(a, T);
-    u0 = blocks.begin(blockIdx.x);
-    u1 = u0 < T ? u0 + blocks.size(blockIdx.x) : u0;
+    if ((int)blockIdx.x < blocks.n) {
+      u0 = blocks.begin(blockIdx.x);
+      u1 = u0 + blocks.size(blockIdx.x);
+    }
   }
   int s = 0;
   auto wait = [&](unsigned bar, unsigned parity) -> bool {
