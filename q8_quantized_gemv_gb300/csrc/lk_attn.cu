@@ -234,8 +234,8 @@ __device__ __forceinline__ void attn_body(const AttnArgs& a, const JoinArgs* j) 
     map_prefetch(&a.vmap);
   }
   asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-  // the launch after this one may read what this one's predecessors wrote
-  // before it waits for this one (the join's deal): so the wait comes first
+  // (a dependent has next to nothing to do before its own wait: started earlier
+  // it would only hold its share of the SMs)
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" :::);
   if constexpr (!CL)
@@ -853,17 +853,13 @@ __global__ void __launch_bounds__(128) attn_join_kernel(const JoinArgs j) {
   const AttnArgs& a = j.a;
   __shared__ Deal deal, tdeal;
   asm volatile("griddepcontrol.launch_dependents;" :::);
-  // the deal before the wait for the partials: lens was there before the launches
-  // that write them began
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   if (threadIdx.x < 32) make_deal<false>(a, deal);
   else if (threadIdx.x < 64 && (a.own_tiled || a.pre_tiled)) make_deal<true>(a, tdeal);
   __syncthreads();
   const int lane = threadIdx.x & 31;
   const long w = (long)blockIdx.x * 4 + (threadIdx.x >> 5);
-  if (w >= (long)a.B * a.R * a.n_q) {
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    return;
-  }
+  if (w >= (long)a.B * a.R * a.n_q) return;
   const int row = (int)(w / a.n_q), h = (int)(w - (long)row * a.n_q), kvh = h / a.G, hg = h - kvh * a.G;
   const int b = row / a.R, r = row - b * a.R;
   // A lane has V neighbouring values.  Partials come in batches of NB whose
@@ -874,14 +870,11 @@ __global__ void __launch_bounds__(128) attn_join_kernel(const JoinArgs j) {
   for (int c = 0; c < V; ++c) acc[c] = 0.0f;
   // the row's own item, then its prefix item (a rolled loop: this code runs
   // once, and what it takes to fetch it counts)
-  bool waited = false;
 #pragma unroll 1
   for (int x = 0; x < 2; ++x) {
     if (x == 1 && (!a.shared || __ldcg(a.lens + b) < 0)) break;
     const int s = x ? a.B : b, i = (x ? row : r) * a.G + hg;
     const Source z = (x ? a.pre_tiled : a.own_tiled) ? tile_source(a, tdeal, s, kvh, i) : stream_source(a, deal, s, kvh, i);
-    if (!waited) asm volatile("griddepcontrol.wait;" ::: "memory");
-    waited = true;
     const int at = V == 4 ? (lane ^ z.flip) * 4 : ((lane >> 1) ^ z.flip) * 4 + (lane & 1) * 2;
 #pragma unroll 1
     for (int i0 = 0; i0 < z.n; i0 += NB) {
@@ -1094,7 +1087,6 @@ lk_status run_d(JoinArgs& j, int type, lk_mode mode, int pdl, cudaStream_t strea
          : fine             ? run_type<LK_KV_BF16, D, true>(a, pdl, stream)
                             : run_type<LK_KV_BF16, D, false>(a, pdl, stream);
     pdl = 1;
-    a.late = 1;
   }
   if (!st && (a.own_tiled || a.pre_tiled)) {
     const int part = D == 128 ? 128 : 64;  // tokens that a warp of the tile kernel fetches

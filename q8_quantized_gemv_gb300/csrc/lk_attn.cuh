@@ -92,7 +92,6 @@ struct AttnArgs {
   int W, NW, TW;      // blocks and warps of the streaming launch, blocks of the tile launch
   int tunit_log2, trows_log2;  // keys of a unit, rows of an item of the tile kernel
   int tflip;          // whether its partials' pieces are permuted
-  int late;           // the tile launch comes after a streaming one of the same call
   unsigned long long wait_ns;
   int* err;
 };

@@ -188,10 +188,10 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == 0) tm_alloc(smem_addr(&tmem_slot), 512);
-  // A launch behind this call's streaming kernel needs nothing of that one's,
-  // and what both need was there when that one let it start: it waits for it
-  // only at its end, for the join's sake.
-  if (!a.late) asm volatile("griddepcontrol.wait;" ::: "memory");
+  // Nothing of the caller's is read before this wait, behind the call's streaming
+  // launch either: that one's having waited for the caller's work before it let
+  // this one start says nothing of what this one sees.
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" :::);
   if (warp == 1) make_deal<true>(a, deal);
   tm_before();
@@ -724,7 +724,6 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
     }
     if (me == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
   }
-  if (a.late) asm volatile("griddepcontrol.wait;" ::: "memory");
   tm_before();
   __syncthreads();
   tm_after();

@@ -1,0 +1,34 @@
+"""What the attention step's kernels must not do under dependent launches, read
+from their source: a kernel that may start while its predecessors run
+(programmatic dependent launch) sees their writes only behind its own
+griddepcontrol.wait.  A stale read shows in no result as long as the timing is
+kind, so the order in the source is the test.  No GPU."""
+import os
+import re
+
+import pytest
+
+from q8_quantized_gemv_gb300 import build
+
+# where each kernel first reads what a caller's earlier launch may have written
+KERNELS = [("lk_attn.cu", "attn_body(", "make_deal"), ("lk_attn.cu", "attn_body(", "a.lens"),
+           ("lk_attn.cu", "attn_body(", "a.q"), ("lk_attn.cu", "attn_join_kernel(", "make_deal"),
+           ("lk_attn.cu", "attn_join_kernel(", "a.lens"), ("lk_tile.cu", "attn_tile_kernel(", "make_deal"),
+           ("lk_tile.cu", "attn_tile_kernel(", "a.q"), ("lk_kv.cu", "kv_append_kernel(", "__ldcg"),
+           ("lk_kv.cu", "kv_append_kernel(", "a.lens")]
+
+
+def source(name):
+    with open(os.path.join(build.CSRC, name)) as f:
+        return re.sub(r"//[^\n]*", "", f.read())
+
+
+@pytest.mark.parametrize("file,kernel,read", KERNELS)
+def test_waits_before_it_reads(file, kernel, read):
+    s = source(file)
+    at = s.index(kernel)
+    body = s[at:s.index("\n}\n", at)]
+    wait = body.index("griddepcontrol.wait")
+    assert wait < re.search(re.escape(read) + r"(?![a-z0-9_])", body).start()
+    line = body[body.rindex("\n", 0, wait):wait]
+    assert "if" not in line, "the wait is not conditional: " + line
