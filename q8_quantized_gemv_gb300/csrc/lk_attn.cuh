@@ -159,15 +159,19 @@ __device__ __forceinline__ Shares stream_blocks(const AttnArgs& a, int NW, int T
   return deal_blocks(T, a.W, NW, a.B == 1 && (a.pre_tiled || !a.shared) && !a.own_tiled, a.n_kv * groups_of<false>(a, 0));
 }
 
+// The lengths of sequences 2 l and 2 l + 1 in lane l.
+__device__ __forceinline__ int2 lens_pair(const AttnArgs& a) {
+  static_assert(LK_MAX_BATCH <= 64, "two sequences to a lane");
+  const int s = 2 * (threadIdx.x & 31);
+  return make_int2(s < a.B ? __ldcg(a.lens + s) : 0, s + 1 < a.B ? __ldcg(a.lens + s + 1) : 0);
+}
+
 // By one whole warp; the caller synchronizes.
 template <bool TILED>
-__device__ __forceinline__ void make_deal(const AttnArgs& a, Deal& d) {
+__device__ __forceinline__ void make_deal(const AttnArgs& a, Deal& d, int2 lens) {
   const int lane = threadIdx.x & 31, cap = a.table_w << a.page_log2, lu = TILED ? a.tunit_log2 : 5;
-  static_assert(LK_MAX_BATCH <= 64 && UNIT == 32, "two sequences to a lane");
-  // lane l: sequences 2 l and 2 l + 1
-  int n[2], u[2];
-#pragma unroll
-  for (int i = 0; i < 2; ++i) n[i] = 2 * lane + i < a.B ? __ldcg(a.lens + 2 * lane + i) : 0;
+  static_assert(UNIT == 32, "5 is its logarithm");
+  int n[2] = {lens.x, lens.y}, u[2];
   const bool own = (a.own_tiled != 0) == TILED, pre = (a.pre_tiled != 0) == TILED;
   const int items = a.n_kv * groups_of<TILED>(a, 0);
 #pragma unroll

@@ -193,7 +193,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
   // this one start says nothing of what this one sees.
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" :::);
-  if (warp == 1) make_deal<true>(a, deal);
+  if (warp == 1) make_deal<true>(a, deal, lens_pair(a));
   tm_before();
   __syncthreads();
   tm_after();

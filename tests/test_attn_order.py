@@ -12,8 +12,8 @@ from q8_quantized_gemv_gb300 import build
 
 # where each kernel first reads what a caller's earlier launch may have written
 KERNELS = [("lk_attn.cu", "attn_body(", "make_deal"), ("lk_attn.cu", "attn_body(", "a.lens"),
-           ("lk_attn.cu", "attn_body(", "a.q"), ("lk_attn.cu", "attn_join_kernel(", "make_deal"),
-           ("lk_attn.cu", "attn_join_kernel(", "a.lens"), ("lk_tile.cu", "attn_tile_kernel(", "make_deal"),
+           ("lk_attn.cu", "attn_body(", "a.q"), ("lk_attn.cu", "attn_join_kernel(", "z.ml"),
+           ("lk_attn.cu", "attn_join_kernel(", "z.o"), ("lk_tile.cu", "attn_tile_kernel(", "make_deal"),
            ("lk_tile.cu", "attn_tile_kernel(", "a.q"), ("lk_kv.cu", "kv_append_kernel(", "__ldcg"),
            ("lk_kv.cu", "kv_append_kernel(", "a.lens")]
 
@@ -23,12 +23,25 @@ def source(name):
         return re.sub(r"//[^\n]*", "", f.read())
 
 
-@pytest.mark.parametrize("file,kernel,read", KERNELS)
-def test_waits_before_it_reads(file, kernel, read):
+def kernel_body(file, kernel):
     s = source(file)
     at = s.index(kernel)
-    body = s[at:s.index("\n}\n", at)]
+    return s[at:s.index("\n}\n", at)]
+
+
+@pytest.mark.parametrize("file,kernel,read", KERNELS)
+def test_waits_before_it_reads(file, kernel, read):
+    body = kernel_body(file, kernel)
     wait = body.index("griddepcontrol.wait")
     assert wait < re.search(re.escape(read) + r"(?![a-z0-9_])", body).start()
     line = body[body.rindex("\n", 0, wait):wait]
     assert "if" not in line, "the wait is not conditional: " + line
+
+
+def test_join_reads_the_lengths_again():
+    """The join works its deal out ahead of the wait; what it does behind it
+    follows from lengths that it read there."""
+    body = kernel_body("lk_attn.cu", "attn_join_kernel(")
+    after = body[body.index("griddepcontrol.wait"):]
+    again = re.search(r"const int2 now = lens_pair\(a\);.*?if \(__syncthreads_or\(other\)\) \{\s*lens = now;\s*deals\(\);", after, re.S)
+    assert again and again.end() < after.index("ld_cg")
