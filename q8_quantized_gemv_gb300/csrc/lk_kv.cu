@@ -164,12 +164,13 @@ __global__ void __launch_bounds__(256) kv_append_kernel(const AppendArgs a) {
   if (a.rot && p >= a.n_pos - a.p0) return;
   const int pid = __ldcg(a.table + (long)b * a.table_w + (p >> a.page_log2));
   if ((unsigned)pid >= (unsigned)a.n_pages) return;
+  // (gains and tables too may be a launch before's: no loads by the read-only path)
   if (!is_v) {
     const float* gain = is_q ? a.q_gain : a.k_gain;
     if (gain) {
       float gv[C];
 #pragma unroll
-      for (int c = 0; c < C; ++c) gv[c] = __ldg(gain + 32 * c + lane);
+      for (int c = 0; c < C; ++c) gv[c] = __ldcg(gain + 32 * c + lane);
       float y[C];
       if (__all_sync(FULL, norm_pairs<C>(x, gv, a.eps, y))) {
 #pragma unroll
@@ -185,7 +186,7 @@ __global__ void __launch_bounds__(256) kv_append_kernel(const AppendArgs a) {
         for (int c = 0; c < C; ++c) {
           if (32 * c >= a.rot) continue;
           const int i = (32 * c + lane) >> 1;
-          const float cs = __ldg(a.cosines + at + i), sn = __ldg(a.sines + at + i);
+          const float cs = __ldcg(a.cosines + at + i), sn = __ldcg(a.sines + at + i);
           const float o = __shfl_xor_sync(FULL, x[c], 1);
           const float u = __fmul_rn(x[c], cs), z = __fmul_rn(o, sn);
           x[c] = (lane & 1) ? __fadd_rn(u, z) : __fsub_rn(u, z);
@@ -195,7 +196,7 @@ __global__ void __launch_bounds__(256) kv_append_kernel(const AppendArgs a) {
 #pragma unroll
         for (int c = 0; c < C / 2; ++c) {
           if (c >= hc) continue;
-          const float cs = __ldg(a.cosines + at + 32 * c + lane), sn = __ldg(a.sines + at + 32 * c + lane);
+          const float cs = __ldcg(a.cosines + at + 32 * c + lane), sn = __ldcg(a.sines + at + 32 * c + lane);
           // partner register c + hc: hc is 1 (rot 64) or 2 (rot 128)
           const float y = C == 4 && hc == 2 ? x[(c + 2) % C] : x[(c + 1) % C];
           const float u = __fsub_rn(__fmul_rn(x[c], cs), __fmul_rn(y, sn));

@@ -45,3 +45,11 @@ def test_join_reads_the_lengths_again():
     after = body[body.index("griddepcontrol.wait"):]
     again = re.search(r"const int2 now = lens_pair\(a\);.*?if \(__syncthreads_or\(other\)\) \{\s*lens = now;\s*deals\(\);", after, re.S)
     assert again and again.end() < after.index("ld_cg")
+
+
+@pytest.mark.parametrize("file", ["lk_kv.cu", "lk_attn.cu", "lk_tile.cu", "lk_attn.cuh", "lk_tc.cuh"])
+def test_no_loads_by_the_read_only_path(file):
+    """That path promises that nobody writes for the kernel's whole life, which
+    begins while its predecessors run."""
+    s = source(file)
+    assert "__ldg(" not in s and ".nc" not in s and "__restrict__" not in s

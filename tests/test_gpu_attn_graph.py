@@ -6,13 +6,15 @@ attention reads; lengths advance inside the graph; inputs and page-table
 entries change between replays.  Two layers share the workspace.  Results are
 held to the formula in 64 bits, and to the bits of the same calls with the
 device idle before each."""
+import numpy as np
 import pytest
 
 torch = pytest.importorskip("torch")
 
-from gpuhelp import host  # noqa: E402
+from gpuhelp import bits, host  # noqa: E402
 from q8_quantized_gemv_gb300 import build, lk  # noqa: E402
-from test_gpu_attn import DEV, TYPES, check, gen, make_cache, reference, workspace  # noqa: E402
+from test_gpu_attn import (DEV, TYPES, check, gen, host_append, host_quant, make_cache, make_table, reference,  # noqa: E402
+                           workspace)
 
 pytestmark = pytest.mark.gpu
 
@@ -135,3 +137,51 @@ def test_token_by_token(path, type_, pdl):
     for c, e in zip(caches, end):
         for t, b in zip((c.k, c.v, c.ks, c.vs), e):
             assert t is None or torch.equal(t, b)
+
+
+@pytest.mark.parametrize("paired", [False, True])
+def test_append_reads_tables_and_gains_of_the_launch_before(paired):
+    """Rotation table and gains written by the launches just before a dependent
+    append, new ones in every replay."""
+    B, n_q, n_kv, D, page = 3, 8, 2, 128, 16
+    g = gen(95)
+    cache, _, _ = make_cache("q8", 8, n_kv, page, D, g)
+    table = make_table(B, 2, 8, g)
+    lens = torch.tensor([1, 17, 30], dtype=torch.int32, device=DEV)
+    x = torch.randn((B, (n_q + 2 * n_kv) * D), generator=g, device=DEV)
+    q, k, v = x.split((n_q * D, n_kv * D, n_kv * D), 1)
+    new = torch.zeros((4, 30, D // 2), device=DEV)
+    cos, sin = torch.zeros((30, D // 2), device=DEV), torch.zeros((30, D // 2), device=DEV)
+    gains = torch.zeros((2, D), device=DEV)
+    qr = torch.zeros((B, n_q * D), device=DEV)
+    cfg = lk.launch_cfg(pdl=1)
+
+    def step():
+        cos.copy_(new[0])
+        gains[0].copy_(new[2, :2].flatten())
+        gains[1].copy_(new[3, :2].flatten())
+        sin.copy_(new[1])
+        for _ in range(2):  # the second one a dependent of a kernel that lets it start early
+            lk.lk_kv_append(cache, q, k, v, table, lens, cos, sin, qr, paired=paired, q_gain=gains[0], k_gain=gains[1],
+                            cfg=cfg)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        step()
+    hx, ht = host(x).reshape(B, -1, D), host(table)
+    for _ in range(4):
+        new.copy_(torch.randn(new.shape, generator=g, device=DEV))
+        graph.replay()
+        torch.cuda.synchronize()
+        n = host(new)
+        for b, ln in enumerate(host(lens).tolist()):
+            want = host_append(hx[b, :n_q], n[0], n[1], ln - 1, paired, n[2, :2].ravel())
+            assert np.array_equal(bits(host(qr[b]).reshape(n_q, D)), bits(want))
+            kw, ks = host_quant(host_append(hx[b, n_q:n_q + n_kv], n[0], n[1], ln - 1, paired, n[3, :2].ravel()))
+            at = (int(ht[b, (ln - 1) // page]), slice(None), (ln - 1) % page)
+            assert np.array_equal(host(cache.k)[at], kw) and np.array_equal(host(cache.ks)[at], ks)
