@@ -32,7 +32,9 @@
  * for table_w * page tokens.  A page number outside [0, n_pages) is never
  * followed: its tokens count as absent.  Sequences may share pages, except
  * those that an append writes.  Stored values below lens[b] must be finite,
- * scales finite and not negative; what lies behind them may be anything.
+ * scales finite and not negative; what lies behind them may be anything.  An
+ * infinite value below lens[b] (what an append rounds past 65504 to f16) makes
+ * results infinite or NaN, on its head and in the sequences that hold it only.
  */
 #ifndef LK_ATTN_H
 #define LK_ATTN_H
@@ -107,8 +109,9 @@ lk_status lk_kv_append(const lk_kv_cache* cache, const float* q, const float* k,
  * 2^-20 of its norm).  The result does not depend on timing: the same call gives
  * the same bits.  The same row may differ in its last bits between calls of
  * other B, R, lens or table_w (the keys are split between blocks by all of them).
- *   q     f32 [M][n_q*head_dim], 16-byte aligned, finite (a row that is not
- *         changes no other row's result)
+ *   q     f32 [M][n_q*head_dim], 16-byte aligned, finite.  A head of a row that
+ *         is not comes out as NaN if it sees a token, zeros if it sees none, and
+ *         changes no other result (quantized words of NaN are unspecified)
  *   mode, out, hq, hl, hs   the result for the next projection, as
  *         lk_swiglu_quant gives it: out f32 [M][n_q*head_dim] (required under
  *         LK_DEQUANT, else optional; may be q), under LK_INT8ACT / LK_TWOPASS

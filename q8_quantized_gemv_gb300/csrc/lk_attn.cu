@@ -179,12 +179,13 @@ struct JoinArgs {
 };
 
 // Row and head w (row * n_q + head): a lane's D / 32 neighbouring sums over the
-// weights' sum, as f32 and / or quantized.
+// weights' sum, as f32 and / or quantized.  A sum of 0: the row sees nothing.  One
+// that is not a number (the maxima drop such scores, the sums do not) stays so.
 template <int Q, int D>
 __device__ __forceinline__ void finish(const JoinArgs& j, long w, float (&acc)[D / 32], float ls, int lane) {
   constexpr int V = D / 32;
 #pragma unroll
-  for (int c = 0; c < V; ++c) acc[c] = ls > 0.0f ? __fdiv_rn(acc[c], ls) : 0.0f;
+  for (int c = 0; c < V; ++c) acc[c] = ls != 0.0f ? __fdiv_rn(acc[c], ls) : 0.0f;
   if (j.out) {
     float* y = j.out + w * D + lane * V;
     if (j.wide) {

@@ -614,10 +614,14 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
             const int left = (there >> c) & 1u ? vis - key0 - 16 * c : 0;
 #pragma unroll
             for (int k = 0; k < 16; ++k) {
-              if (k >= left) r[k] = 0xff800000u;
+              if (k >= left) {
+                r[k] = 0xff800000u;
+                if constexpr (Q8) r2[k] = 0u;  // (not a number where the query is none)
+              }
               mx = fmaxf(mx, Q8 ? __uint_as_float(r[k]) + __uint_as_float(r2[k]) : __uint_as_float(r[k]));
             }
             tm_st16(ts + 16 * c, r);
+            if constexpr (Q8) tm_st16(ts + 64 + 16 * c, r2);
           }
           tm_st_wait();
         }
