@@ -119,6 +119,8 @@ lk_status lk_kv_append(const lk_kv_cache* cache, const float* q, const float* k,
  *   ws    ws_bytes >= lk_attn_workspace_bytes(...), 16-byte aligned; its
  *         content needs no preparation and means nothing after the call.
  *         Calls that may run at the same time need separate ones
+ *   What is written (out, hq, hl, hs, ws) must not overlap each other or
+ *         anything that is read, but for out == q (LK_ERR_ARG)
  *   scale finite (1/sqrt(head_dim) as a rule)
  * Rows behind the last sequence are not touched.  LK_ERR_SHAPE also where the
  * key units of all items together, n_kv * B * ceil(R * n_q/n_kv / 8) * ceil(table_w *

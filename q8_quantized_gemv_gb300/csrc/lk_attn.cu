@@ -1121,6 +1121,23 @@ lk_status run_d(JoinArgs& j, int type, lk_mode mode, int pdl, cudaStream_t strea
                               : run_join<2, D>(j, stream);
 }
 
+// n bytes at p, where there are any
+struct Span {
+  const void* p;
+  size_t n;
+};
+bool overlap(const Span& x, const Span& y) {
+  const uintptr_t a = (uintptr_t)x.p, b = (uintptr_t)y.p;
+  return x.p && y.p && x.n && y.n && a < b + y.n && b < a + x.n;
+}
+// Whether one of the `nw` written spans, which come first, overlaps another of the n.
+bool spans_clash(const Span* s, int nw, int n) {
+  for (int i = 0; i < nw; ++i)
+    for (int k = i + 1; k < n; ++k)
+      if (overlap(s[i], s[k])) return true;
+  return false;
+}
+
 }  // namespace lkattn
 
 using namespace lkattn;
@@ -1169,6 +1186,25 @@ lk_status lk_attn_shared(const lk_kv_cache* cache, const float* q, int n_q, cons
   if (!ws || ws_bytes < lk_attn_workspace_bytes(n_q, cache->n_kv, cache->head_dim, B, R, shared))
     return LK_ERR_WORKSPACE;
   if (!aligned(ws, 16)) return LK_ERR_ALIGN;
+  // what is written apart from all else that is given (out in place of q excepted:
+  // a row's head is written by those that read it, when they have)
+  const size_t rows = (size_t)B * R * n_q * cache->head_dim, tokens = (size_t)cache->n_pages * cache->n_kv * cache->page;
+  const size_t kv = tokens * cache->head_dim * (cache->type == LK_KV_Q8 ? 1 : 2), sc = tokens * (cache->head_dim / 32) * 2;
+  const bool words = mode != LK_DEQUANT, q8 = cache->type == LK_KV_Q8;
+  const Span spans[] = {{out, rows * 4},
+                        {words ? hq : nullptr, rows},
+                        {mode == LK_TWOPASS ? hl : nullptr, rows},
+                        {words ? hs : nullptr, rows / 8},
+                        {ws, lk_attn_workspace_bytes(n_q, cache->n_kv, cache->head_dim, B, R, shared)},
+                        {out == q ? nullptr : q, rows * 4},
+                        {cache->k, kv},
+                        {cache->v, kv},
+                        {q8 ? cache->ks : nullptr, sc},
+                        {q8 ? cache->vs : nullptr, sc},
+                        {table, (size_t)B * table_w * 4},
+                        {lens, (size_t)B * 4},
+                        {shared ? prefix_table : nullptr, (size_t)prefix_w * 4}};
+  if (spans_clash(spans, 5, sizeof spans / sizeof *spans)) return LK_ERR_ARG;
   const DeviceInfo* d = device_info(nullptr);
   if (!d) return LK_ERR_CUDA;
   AttnArgs a = {};
