@@ -9,8 +9,9 @@
  * anything is launched, cfg as everywhere (these calls use its pdl field).
  * Make the first call on a device before any stream capture there (it looks up
  * addresses and sets kernel attributes).  Device-side waits are bounded (option
- * "wait_us"); one that runs out ends its kernel and sets the error word
- * (lk_device_error), the results being then undefined.
+ * "wait_us"); one that runs out ends its kernel and sets a bit of the error word
+ * (lk_device_error): 64 in the streaming kernel, 128 in the tile kernel (which
+ * is which: lk_attn_launches), the results being then undefined.
  *
  * The pages the other entry points cite have no counterpart of these; they
  * are the library's own.

@@ -85,8 +85,6 @@ __device__ __forceinline__ unsigned lds32(unsigned a) {
   return r;
 }
 
-constexpr int ERR_ATTN_WAIT = 32;
-
 // ---- clusters ---------------------------------------------------------------------------
 constexpr int kMaxCluster = 8;
 // All threads of all blocks of the cluster; every block comes here, whatever

@@ -10,6 +10,11 @@
 
 namespace lkattn {
 
+// Bits of the device error word that a wait which ran out sets: the streaming
+// kernel's (clusters included) and the tile kernel's (1 to 16 are the GEMV
+// kernels', 32 the chain's barrier).
+constexpr int ERR_ATTN_WAIT = 64, ERR_TILE_WAIT = 128;
+
 inline int log2_of(int p) {
   int n = 0;
   while ((1 << n) < p) ++n;

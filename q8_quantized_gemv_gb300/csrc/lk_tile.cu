@@ -41,7 +41,6 @@ using namespace lktc;
 
 namespace lkattn {
 
-constexpr int ERR_TILE_WAIT = 32;
 constexpr int kTileThreads = 384, kTileRegs = 168;
 
 template <int TYPE, int D>

@@ -3,6 +3,7 @@ from their source: a kernel that may start while its predecessors run
 (programmatic dependent launch) sees their writes only behind its own
 griddepcontrol.wait.  A stale read shows in no result as long as the timing is
 kind, so the order in the source is the test.  No GPU."""
+import glob
 import os
 import re
 
@@ -53,3 +54,18 @@ def test_no_loads_by_the_read_only_path(file):
     begins while its predecessors run."""
     s = source(file)
     assert "__ldg(" not in s and ".nc" not in s and "__restrict__" not in s
+
+
+def test_error_bits_tell_the_waits_apart():
+    """Every wait of the library that can run out has a bit of its own in the
+    device error word."""
+    bits = {}
+    for f in glob.glob(os.path.join(build.CSRC, "*.cu*")):
+        for name, v in re.findall(r"\b(ERR_[A-Z_]+) = (\d+)", source(os.path.basename(f))):
+            bits[f"{os.path.basename(f)} {name}"] = int(v)
+    assert len(bits) >= 8 and all(v & (v - 1) == 0 for v in bits.values())
+    assert len(set(bits.values())) == len(bits), bits
+    with open(os.path.join(build.INCLUDE, "lk_attn.h")) as f:
+        doc = f.read()
+    for name in ("ERR_ATTN_WAIT", "ERR_TILE_WAIT"):
+        assert f"{bits['lk_attn.cuh ' + name]} in the" in doc
