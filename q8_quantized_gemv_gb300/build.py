@@ -6,6 +6,7 @@ from __future__ import annotations
 import concurrent.futures as cf
 import glob
 import os
+import re
 import subprocess
 import sys
 
@@ -68,14 +69,42 @@ def _stale(target, deps):
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+# Kernels that move registers between their warps at run time: the split is made
+# for one number of registers at launch, which is the compiler's to choose (the
+# library refuses to launch them with another).
+SPLIT_KERNELS = {"lk_tile.cu": ("attn_tile_kernel", "kTileRegs")}
+
+
+def check_registers(name, source, ptxas):
+    """Raise if ptxas (its -v output) gave a kernel of SPLIT_KERNELS[name] another
+    number of registers than the source's split is made for."""
+    kernel, const = SPLIT_KERNELS[name]
+    want = int(re.search(rf"\b{const} = (\d+)", source).group(1))
+    got = re.findall(rf"entry function '([^']*{kernel}[^']*)'.*?Used (\d+) registers", ptxas, re.S)
+    if not got:
+        raise RuntimeError(f"{name}: no register counts of {kernel} in the output of ptxas")
+    for fn, n in got:
+        if int(n) != want:
+            raise RuntimeError(f"{name}: {fn} has {n} registers at launch, its split is made for {want} ({const}): "
+                               "with this compiler the split has to be made anew")
+
+
 def _compile(src, verbose_ptxas):
     obj = os.path.join(BUILD, os.path.basename(src)[:-3] + ".o")
     if not _stale(obj, [src] + _headers() + [__file__]):
         return obj, ""
-    cmd = [nvcc()] + NVCC_FLAGS + (["-Xptxas", "-v"] if verbose_ptxas else []) + ["-c", src, "-o", obj]
+    split = os.path.basename(src) in SPLIT_KERNELS
+    cmd = [nvcc()] + NVCC_FLAGS + (["-Xptxas", "-v"] if verbose_ptxas or split else []) + ["-c", src, "-o", obj]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"nvcc failed for {src}:\n{r.stdout}\n{r.stderr}")
+    if split:
+        try:
+            with open(src) as f:
+                check_registers(os.path.basename(src), f.read(), r.stderr)
+        except RuntimeError:
+            os.remove(obj)
+            raise
     return obj, r.stderr
 
 
