@@ -104,12 +104,14 @@ lk_status lk_kv_append(const lk_kv_cache* cache, const float* q, const float* k,
  * and zeros where it sees none.  Sums and statistics are f32.  Keys and values
  * enter as stored (Q8 under many rows: as two f16 terms, to 2^-22), queries and
  * weights as two 16-bit terms of the cache's type (Q8: f16).  With W = sum_j p_j
- * |v_j| / sum_j p_j and A the largest scale * sum_i |q_i k_ji| of the row, out is
+ * |v_j| / sum_j p_j and A the largest scale * sum_i |q_i k_ji| of the row (f16, Q8:
+ * with no |q_i| taken below 2^-17 of the row's largest, the terms end there), out is
  * within (2^-15 + c A) W of the exact value, c = 2^-17 (f16, Q8) or 2^-14 (bf16),
  * plus (2^-27 + N 2^-32) max|v| over its N tokens; on the whole far nearer (about
- * 2^-20 of its norm).  The result does not depend on timing: the same call gives
- * the same bits.  The same row may differ in its last bits between calls of
- * other B, R, lens or table_w (the keys are split between blocks by all of them).
+ * 2^-20 of its norm; 2^-18 where a bf16 cache goes through the tile kernel).
+ * The result does not depend on timing: the same call gives the same bits.  The
+ * same row may differ in its last bits between calls of other B, R, lens or
+ * table_w (the keys are split between blocks by all of them).
  *   q     f32 [M][n_q*head_dim], 16-byte aligned, finite.  A head of a row that
  *         is not comes out as NaN if it sees a token, zeros if it sees none, and
  *         changes no other result (quantized words of NaN are unspecified)

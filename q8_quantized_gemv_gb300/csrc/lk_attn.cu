@@ -36,10 +36,10 @@
 // an item, whose partials stay in shared memory (cluster_size).
 //
 // Measured (GPU time of a whole call, with its join): 64 x 8192 tokens f16, 32 query /
-// 8 key heads of 128: 322 us, 6.67 TB/s; 16 ragged up to 16384 bf16 100 us, 5.7
-// TB/s (98 us with two query terms); 1 x 131071 Q8 63 us, 4.5 TB/s, bound by the
+// 8 key heads of 128: 327 us, 6.6 TB/s; 16 ragged up to 16384 bf16 101 us, 5.6
+// TB/s (99 us with two query terms); 1 x 131071 Q8 63 us, 4.5 TB/s, bound by the
 // issue of its instructions (58 % of the slots), not by memory; 1 x 1023 f16 in
-// clusters 6.2 us (9.3 by the deal and the join), a launch and dependent reads.
+// clusters 6.2 us (9.1 by the deal and the join), a launch and dependent reads.
 #include <cuda_bf16.h>
 
 #include <type_traits>
@@ -932,14 +932,15 @@ __global__ void __launch_bounds__(128) attn_join_kernel(const JoinArgs j) {
 // reads the keys once per 8 rows (from L2), the tile kernel once, at a fixed
 // cost of some 10 us; a sequence's length is not known here, a prefix's is.
 // Measured (whole call, streaming / tile, us; 8 kv heads):
-//   sequences, f16 D 128: 24 rows 1 x 8000 21.6 / 21.3, 4 x 8000 51.9 / 39.6, 20
-//     rows 8 x 1000 20.7 / 21.5; 64 rows 1 x 8000 36.9 / 23.0, 1 x 1000 15.1 / 14.2
-//   Q8 D 128: 24 rows 4 x 8000 48.6 / 60.4, 36 rows 72.3 / 62.0, 64 rows 105 / 64
-//   prefix, f16 D 128: 96 rows 2000 25.6 / 26.7, 128 rows 29.8 / 27.1; 32 rows 8000
-//     28.2 / 29.8, 48 rows 35.8 / 30.9; 24 rows 32000 59.8 / 45.8
-//   D 64: 64 rows 8000 28.0 / 28.2; 24 rows 32000 37.5 / 36.4
-//   Q8 D 128: 256 rows 2000 42.9 / 41.5, 48 rows 8000 34.5 / 37.1, 64 rows 42.2 /
-//     37.2; D 64: 96 rows 8000 39.3 / 32.6, 64 rows 28.9 / 31.8
+//   sequences, f16 D 128: 24 rows 1 x 8000 20.2 / 21.0, 4 x 8000 48.6 / 38.9, 20
+//     rows 8 x 1000 21.0 / 20.3; 64 rows 1 x 8000 39.4 / 21.9, 1 x 1000 13.9 / 14.0
+//   Q8 D 128: 24 rows 4 x 8000 48.0 / 60.9, 36 rows 67.9 / 61.7, 64 rows 101 / 64
+//   prefix, f16 D 128: 96 rows 2000 25.5 / 27.8, 128 rows 29.5 / 28.5; 32 rows 8000
+//     27.9 / 31.1, 48 rows 34.3 / 32.1; 24 rows 32000 55.5 / 48.5; bf16 96 rows 2000
+//     29.9 / 27.1, 32 rows 8000 29.4 / 30.0
+//   D 64: 64 rows 8000 26.8 / 26.6; 24 rows 32000 32.8 / 34.6
+//   Q8 D 128: 256 rows 2000 42.9 / 37.9, 48 rows 8000 34.4 / 38.8, 64 rows 41.1 /
+//     39.6; D 64: 96 rows 8000 38.3 / 32.2, 64 rows 26.8 / 30.9
 bool tiled(long rows, int type, int D, long keys) {
   const bool q8 = type == LK_KV_Q8;
   if (rows <= (q8 ? 32 : 16)) return false;

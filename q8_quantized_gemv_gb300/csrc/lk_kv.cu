@@ -7,8 +7,11 @@
 // value per lane.  Every operation is rounded as the header writes it, so
 // the results are bit-fixed.  A few KB a row: the call is bound by its launch
 // and one chain of dependent loads (lens -> table, beside the row itself): 2.1 us
-// for one row of 32 + 8 + 8 heads of 128, 5.4 us for 64 rows with the norm to Q8
-// (3 MB, 0.4 us of memory time; f64 in the norm made it 16.6).
+// for one row of 32 + 8 + 8 heads of 128, 3.4 us for 64 rows to Q8, 5.5 with the
+// norm (3 MB, 0.4 us of memory time; f64 for every head made it 16.6): of its 2560
+// normed heads some 7 have a value so near a rounding boundary that the f64 form
+// decides (378 f64 instructions counted), and the call waits for that one's chain of
+// a sum, a root and quotients, some 2.5 us.  One row's 40 mostly have none.
 #include <cuda_bf16.h>
 
 #include "lk_attn.cuh"

@@ -19,11 +19,11 @@
 // fresh accumulator and are added in f32 registers, 128 keys at a time.
 //
 // Measured (GPU time of a whole call, 32 query / 8 key heads of 128): 64 new
-// tokens behind 32768 in bf16 54 us: 1.27 PFLOP/s of products, twice the plain
+// tokens behind 32768 in bf16 55 us: 1.25 PFLOP/s of products, twice the plain
 // count for the second terms (tensor pipe 57 % busy in the kernel: a 4.9 k cycle
 // period of 4.2 k cycles of MMAs, and the first and last tiles).  24 sequences on
-// a Q8 prefix of 16384: 54 us with their own tokens, the kernel 38, bound by the
-// conversion of levels to f16 terms.
+// a Q8 prefix of 16384: 56 us with their own tokens' launch before it, the kernel 38,
+// bound by the conversion of levels to f16 terms.
 //
 // Roles: warp 0 issues the MMAs (one thread), warps 2 and 3 fill a ring of
 // tile buffers with tensor copies in the 128-byte swizzle of the MMA operands,
