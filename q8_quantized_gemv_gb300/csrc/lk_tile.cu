@@ -186,16 +186,19 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
     abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (warp == 0) tm_alloc(smem_addr(&tmem_slot), 512);
   // Nothing of the caller's is read before this wait, behind the call's streaming
   // launch either: that one's having waited for the caller's work before it let
   // this one start says nothing of what this one sees.
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  asm volatile("griddepcontrol.launch_dependents;" :::);
+  // Tensor memory is taken behind the wait and ahead of the dependents' start: a
+  // launch before or after that wants some on this SM too would wait for this one's,
+  // and this one for its end, or for what it took first.
+  if (warp == 0) tm_alloc(smem_addr(&tmem_slot), 512);
   if (warp == 1) make_deal<true>(a, deal, lens_pair(a));
   tm_before();
   __syncthreads();
   tm_after();
+  asm volatile("griddepcontrol.launch_dependents;" :::);
   const unsigned tmem = __shfl_sync(FULL, *(volatile unsigned*)&tmem_slot, 0);
   const int T = deal.cum[a.B + a.shared];
   int u0 = 0, u1 = 0;

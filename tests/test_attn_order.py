@@ -11,11 +11,12 @@ import pytest
 
 from q8_quantized_gemv_gb300 import build
 
-# where each kernel first reads what a caller's earlier launch may have written
+# where each kernel first reads what a caller's earlier launch may have written, or
+# takes what such a launch may still be waiting for (tensor memory)
 KERNELS = [("lk_attn.cu", "attn_body(", "make_deal"), ("lk_attn.cu", "attn_body(", "a.lens"),
            ("lk_attn.cu", "attn_body(", "a.q"), ("lk_attn.cu", "attn_join_kernel(", "z.ml"),
            ("lk_attn.cu", "attn_join_kernel(", "z.o"), ("lk_tile.cu", "attn_tile_kernel(", "make_deal"),
-           ("lk_tile.cu", "attn_tile_kernel(", "a.q"), ("lk_kv.cu", "kv_append_kernel(", "__ldcg"),
+           ("lk_tile.cu", "attn_tile_kernel(", "a.q"), ("lk_tile.cu", "attn_tile_kernel(", "tm_alloc"), ("lk_kv.cu", "kv_append_kernel(", "__ldcg"),
            ("lk_kv.cu", "kv_append_kernel(", "a.lens")]
 
 
@@ -37,6 +38,15 @@ def test_waits_before_it_reads(file, kernel, read):
     assert wait < re.search(re.escape(read) + r"(?![a-z0-9_])", body).start()
     line = body[body.rindex("\n", 0, wait):wait]
     assert "if" not in line, "the wait is not conditional: " + line
+
+
+def test_tensor_memory_is_taken_before_dependents_start():
+    """One that wants some too and got it first would wait for this launch, and this
+    launch for it."""
+    body = kernel_body("lk_tile.cu", "attn_tile_kernel(")
+    assert body.count("griddepcontrol.launch_dependents") == 1
+    taken = body.index("tm_alloc")
+    assert taken < body.index("__syncthreads();", taken) < body.index("griddepcontrol.launch_dependents")
 
 
 def test_join_reads_the_lengths_again():
