@@ -968,13 +968,15 @@ bool tiled(long rows, int type, int D, long keys) {
 //   256 rows, 2 kv heads, C 2: f16 500 9.1 / 14.9, 2000 14.2 / 15.6; Q8 14.0 / 23.3
 // on a prefix, 8 sequences of 77, C 2: f16 300 7.2 / 14.6, 1900 13.1 / 18.1, 2900
 //   16.4 / 19.7; bf16 1900 15.6 / 18.4; Q8 2900 16.6 / 21.8; D 64 f16 2900 10.1 / 18.9
-// fewer than 8 items, to which clusters give 8 blocks each and the deal all SMs (so
-// their number bounds the tokens too; number: tokens, f16 where not named): 1: 4000 9.5 / 10.1, 6000 10.9 / 10.2, 8000 12.6 / 11.1, 12700
-//   17.1 / 12.4; 2: 6000 11.1 / 10.6, 12700 17.2 / 13.5; 4: 8000 12.7 / 12.9, 12700 17.1 /
-//   15.7; 6: 10000 14.3 / 14.6, 12700 17.3 / 15.7; bf16 1: 3000 9.9 / 9.3, 6000 12.8 /
-//   10.5, 4: 4000 10.9 / 11.1, 6000 13.0 / 11.9; Q8 1: 6000 11.1 / 11.0, 10000 14.9 / 12.2;
-//   D 64 f16 1: 10000 8.9 / 8.7, 18000 11.8 / 10.0, 4: 18000 11.9 / 12.7; Q8 D 64 1: 8000
-//   8.9 / 9.4, 10000 10.3 / 9.8 (its bound is near enough as it is)
+// fewer than 8 items, to which clusters give 8 blocks each and the deal all SMs, so
+// their number bounds the tokens too (number: tokens; f16 where not named):
+//   1: 4000 9.5 / 10.1, 6000 10.9 / 10.2, 8000 12.6 / 11.1, 12700 17.1 / 12.4
+//   2: 6000 11.1 / 10.6, 12700 17.2 / 13.5; 4: 8000 12.7 / 12.9, 12700 17.1 / 15.7
+//   6: 10000 14.3 / 14.6, 12700 17.3 / 15.7
+//   bf16 1: 3000 9.9 / 9.3, 6000 12.8 / 10.5; 4: 4000 10.9 / 11.1, 6000 13.0 / 11.9
+//   Q8 1: 6000 11.1 / 11.0, 10000 14.9 / 12.2
+//   D 64 f16 1: 10000 8.9 / 8.7, 18000 11.8 / 10.0; 4: 18000 11.9 / 12.7; Q8 1: 8000
+//     8.9 / 9.4, 10000 10.3 / 9.8 (its bound is near enough as it is)
 // One sequence full, the others 100: B 4 4000 12.6 / 14.1, B 16 1000 12.6 / 10.1: a
 // long sequence among short ones loses at small C, and more so beyond that room.
 int cluster_size(long items, bool alone, int type, int D, long prefix, long room) {
