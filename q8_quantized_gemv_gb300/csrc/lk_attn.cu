@@ -45,6 +45,7 @@
 #include <type_traits>
 
 #include "lk_attn.cuh"
+#include "lk_spans.h"
 #include "lk_tc.cuh"
 
 using namespace lk;
@@ -1128,23 +1129,6 @@ lk_status run_d(JoinArgs& j, int type, lk_mode mode, int pdl, cudaStream_t strea
   return mode == LK_DEQUANT   ? run_join<0, D>(j, stream)
          : mode == LK_INT8ACT ? run_join<1, D>(j, stream)
                               : run_join<2, D>(j, stream);
-}
-
-// n bytes at p, where there are any
-struct Span {
-  const void* p;
-  size_t n;
-};
-bool overlap(const Span& x, const Span& y) {
-  const uintptr_t a = (uintptr_t)x.p, b = (uintptr_t)y.p;
-  return x.p && y.p && x.n && y.n && a < b + y.n && b < a + x.n;
-}
-// Whether one of the `nw` written spans, which come first, overlaps another of the n.
-bool spans_clash(const Span* s, int nw, int n) {
-  for (int i = 0; i < nw; ++i)
-    for (int k = i + 1; k < n; ++k)
-      if (overlap(s[i], s[k])) return true;
-  return false;
 }
 
 }  // namespace lkattn

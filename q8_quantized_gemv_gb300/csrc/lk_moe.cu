@@ -1,0 +1,512 @@
+// The experts' products of a mixture-of-experts token (include/lk_moe.h):
+// lk_moe_glu_q8, lk_moe_down_q8.
+//
+// Bound: the chosen experts' weights, read once from HBM.  Like the ring GEMV,
+// a block has a share of rows, every warp streams its own groups of four rows
+// ("quads") by bulk copies into its own shared-memory stages and refills a
+// stage when it has consumed it; the activation stays in shared memory.  The
+// rows' arithmetic is lk_gemv_q8's (8 lanes to a row, lane pair b mod 4 with
+// block b's exact dot, (p0 + p2) + (p1 + p3)), so each product has its bits.
+//
+// Gate/up: a quad is the gate rows and the up rows of two neighbouring outputs
+// of one pair, so the warp that has them has what the SwiGLU needs.  A row's
+// pairs lie one after the other, and its blocks share their outputs evenly.  The
+// words of h need 32 outputs: after its last quad a block quantizes the groups
+// of 32 it has whole, and a group that it has in part if it is the last of its
+// blocks to count in (cnt).
+//
+// Down: a quad is four output rows, which the warp takes through all the pairs
+// of the row of activations, one expert's four rows after the other's, and adds
+// them up in the order of the pairs: no partial results, no second launch.
+#include "lk_moe.h"
+#include "lk_ring_kernel.cuh"
+#include "lk_spans.h"
+
+using namespace lk;
+using namespace lkh;
+using namespace lkring;
+
+namespace {
+
+constexpr int ERR_MOE_WAIT = 256;  // bit of the device error word
+
+constexpr int NW = 12;             // warps of a block
+constexpr int SLICE = 4096;        // bytes of K in a stage at most
+constexpr int DEPTH = 8;           // stages of a warp at most
+constexpr int kStatic = 2048;      // static shared memory, at most
+
+struct MoeArgs {
+  const int8_t* wa;            // gate, or down
+  const unsigned char* sa;     // f16 scales, as bytes
+  const int8_t* wb;            // up
+  const unsigned char* sb;
+  int E, rows, K;              // a matrix: [rows][K]
+  const float* x;              // activation rows: M (gate/up) or M * k (down)
+  const int8_t* xq;
+  const int8_t* xl;
+  const float* xs;
+  const int* ids;
+  const float* weights;
+  int k;
+  float* out;                  // h [M * k][rows], or y [M][rows]
+  int8_t* hq;
+  int8_t* hl;
+  float* hs;
+  int* cnt;
+  int tk, nsl;                 // bytes of K in a stage, stages of a row
+  int depth;
+  unsigned srow, s_off, stage_bytes, ring_off;
+  unsigned long long wait_ns;
+  int* err;
+};
+
+template <int Q>
+__host__ __device__ constexpr unsigned act_bytes(unsigned len) {
+  return Q == 0 ? 4u * len : len * Q + len / 8u;
+}
+
+// The activation row `row` into `dst`: words, low words and scales, or f32 values.
+template <int Q>
+__device__ __forceinline__ void load_row(unsigned char* dst, const MoeArgs& a, long row) {
+  const int K = a.K;
+  auto copy = [&](const void* src, unsigned char* to, int bytes) {
+    for (int i = threadIdx.x * 16; i < bytes; i += blockDim.x * 16) *(uint4*)(to + i) = ld_cg16((const char*)src + i);
+  };
+  if constexpr (Q == 0) {
+    copy(a.x + row * K, dst, 4 * K);
+  } else {
+    copy(a.xq + row * K, dst, K);
+    if constexpr (Q == 2) copy(a.xl + row * K, dst + K, K);
+    copy(a.xs + row * (K >> 5), dst + K * Q, K >> 3);
+  }
+}
+
+// A stage's part of four rows against the activation at `act` (K its whole length).
+template <int Q>
+__device__ __forceinline__ void quad_stage(typename part_t<Q>::t& p, const unsigned char* st, const MoeArgs& a, int k0,
+                                           int len, const unsigned (&sh)[2], const unsigned char* act, int lane) {
+  const int nseg = len >> 7;
+  if constexpr (Q == 0) {
+    // lane l has values 4l .. 4l + 3 of a segment, of all four rows (as the ring kernel)
+    const float* X = (const float*)act + k0 + 4 * lane;
+    const unsigned char* W = st + 4 * lane;
+    const unsigned char* S = st + a.s_off + 2 * (lane >> 3);
+    const f32x2 neg = f2_pack(-8388736.0f, -8388736.0f);
+    f32x2 acc[QR];
+#pragma unroll
+    for (int r = 0; r < QR; ++r) acc[r] = f2_pack(0.f, 0.f);
+#pragma unroll 4
+    for (int seg = 0; seg < nseg; ++seg) {
+      const float4 xx = *(const float4*)(X + 128 * seg);
+      const f32x2 x01 = f2_pack(xx.x, xx.y), x23 = f2_pack(xx.z, xx.w);
+#pragma unroll
+      for (int r = 0; r < QR; ++r) {
+        const unsigned u = *(const unsigned*)(W + r * a.tk + 128 * seg) ^ 0x80808080u;
+        const float ws = __half2float(*(const __half*)(S + r * a.srow + sh[r & 1] + 8 * seg));
+        const f32x2 w01 = f2_add(f2_pack(i8_bits_f32(u, 0), i8_bits_f32(u, 1)), neg);
+        const f32x2 w23 = f2_add(f2_pack(i8_bits_f32(u, 2), i8_bits_f32(u, 3)), neg);
+        acc[r] = f2_fma(f2_pack(ws, ws), f2_fma(w23, x23, f2_mul(w01, x01)), acc[r]);
+      }
+    }
+#pragma unroll
+    for (int r = 0; r < QR; ++r) {
+      float a0, a1;
+      f2_unpack(acc[r], a0, a1);
+      float v = __fadd_rn(a0, a1);
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) v = __fadd_rn(v, __shfl_xor_sync(FULL, v, o));
+      if (lane == 8 * r) p = __dadd_rn((double)p, (double)v);
+    }
+  } else {
+    const int rr = lane >> 3, j = lane & 7, q = j >> 1;
+    const unsigned char* W = st + rr * a.tk + 16 * j;
+    const unsigned char* S = st + a.s_off + rr * a.srow + sh[rr & 1] + 2 * q;
+    const unsigned char* XQ = act + k0 + 16 * j;
+    const float* XS = (const float*)(act + (size_t)a.K * Q) + (k0 >> 5) + q;
+#pragma unroll 8
+    for (int seg = 0; seg < nseg; ++seg) {
+      const int4 w = *(const int4*)(W + 128 * seg);
+      const float ws = __half2float(*(const __half*)(S + 8 * seg));
+      int d = dot16(w, *(const int4*)(XQ + 128 * seg));
+      d += __shfl_xor_sync(FULL, d, 1);
+      int e = 0;
+      if constexpr (Q == 2) {
+        e = dot16(w, *(const int4*)(XQ + a.K + 128 * seg));
+        e += __shfl_xor_sync(FULL, e, 1);
+      }
+      p = q8_step<Q>((float)p, ws, XS[4 * seg], d, e);
+    }
+  }
+}
+
+// (p0 + p2) + (p1 + p3) of each row, in lane 8 r for row r.
+template <typename P>
+__device__ __forceinline__ float row_sum(P p) {
+  p = p + __shfl_down_sync(FULL, p, 4);
+  p = p + __shfl_down_sync(FULL, p, 2);
+  return sizeof(P) == 8 ? __double2float_rn((double)p) : (float)p;
+}
+
+template <int Q, bool GLU>
+__global__ void __launch_bounds__(NW * 32, 1) moe_kernel(const MoeArgs a) {
+  extern __shared__ __align__(128) unsigned char smem[];
+  __shared__ unsigned long long bars[NW * DEPTH];
+  __shared__ int pair_of[LK_MOE_MAX_K], expert_of[LK_MOE_MAX_K];
+  __shared__ float weight_of[LK_MOE_MAX_K];
+  __shared__ int n_pairs;
+  __shared__ int aborted;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const long t = blockIdx.y;
+  volatile int* abort_flag = &aborted;
+  unsigned char* ring = smem + a.ring_off + (size_t)warp * a.depth * a.stage_bytes;
+  const unsigned full0 = smem_u32(bars + warp * DEPTH);
+  if (lane == 0)
+    for (int s = 0; s < a.depth; ++s) mbar_init(full0 + 8 * s, 1);
+  if (threadIdx.x == 0) {
+    aborted = 0;
+    asm volatile("griddepcontrol.launch_dependents;" :::);
+  }
+  asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  griddep_wait();
+
+  // the row's pairs that are there
+  if (warp == 0) {
+    const int e = lane < a.k ? __ldcg(a.ids + t * a.k + lane) : -1;
+    const unsigned there = __ballot_sync(FULL, (unsigned)e < (unsigned)a.E);
+    if ((there >> lane) & 1u) {
+      const int i = __popc(there & ((1u << lane) - 1u));
+      pair_of[i] = lane;
+      expert_of[i] = e;
+      if (!GLU) weight_of[i] = __ldcg(a.weights + t * a.k + lane);
+    }
+    if (lane == 0) n_pairs = __popc(there);
+  }
+  __syncthreads();
+  const int np = n_pairs;
+  if (GLU) {
+    if (np) load_row<Q>(smem, a, t);
+  } else {
+    for (int i = 0; i < np; ++i) load_row<Q>(smem + i * act_bytes<Q>(a.K), a, t * a.k + pair_of[i]);
+  }
+
+  // this block's quads: gate/up, of all pairs' outputs; down, of the rows
+  const int per = GLU ? a.rows / 2 : a.rows / 4;  // quads of a pair, of the output
+  const long quads = GLU ? (long)np * per : per;
+  const int q0 = (int)(quads * blockIdx.x / gridDim.x), q1 = (int)(quads * (blockIdx.x + 1) / gridDim.x);
+  // stages of a quad (a row without pairs has none)
+  const int spq = GLU ? a.nsl : np * a.nsl;
+
+  struct Cursor {
+    int q, i, c;  // quad, pair (down), slice
+  };
+  auto next = [&](Cursor& s) {
+    if (++s.c < a.nsl) return;
+    s.c = 0;
+    if (!GLU && ++s.i < np) return;
+    s.i = 0;
+    s.q += NW;
+  };
+  const int nb = a.K >> 5;
+  // matrix row r of the quad: its row in the stack
+  auto stack_row = [&](const Cursor& s, int r) -> long {
+    if (GLU) {
+      const int i = s.q / per, o = 2 * (s.q - i * per);
+      return (long)expert_of[i] * a.rows + o + (r & 1);
+    }
+    return (long)expert_of[s.i] * a.rows + 4 * s.q + r;
+  };
+  auto issue = [&](const Cursor& s, int slot) {
+    const int k0 = s.c * a.tk, len = a.K - k0 < a.tk ? a.K - k0 : a.tk;
+    const unsigned bar = full0 + 8 * slot;
+    unsigned char* st = ring + (size_t)slot * a.stage_bytes;
+    const int r = lane & 3;
+    const long row = lane < 8 ? stack_row(s, r) : 0;
+    const bool up = GLU && r >= 2;
+    const unsigned long long off = ((unsigned long long)row * nb + (k0 >> 5)) * 2;
+    const unsigned slen = ((unsigned)len / 16 + (unsigned)(off & 15) + 15u) & ~15u;  // 16-byte superset
+    unsigned mine = lane < 4 ? (unsigned)len : lane < 8 ? slen : 0u;
+    mine = __reduce_add_sync(FULL, mine);
+    if (lane == 0) mbar_arrive_expect_tx(bar, mine);
+    __syncwarp();
+    if (lane < 4)
+      bulk(st + r * a.tk, (up ? a.wb : a.wa) + row * a.K + k0, len, bar, 0);
+    else if (lane < 8)
+      bulk(st + a.s_off + r * a.srow, (up ? a.sb : a.sa) + (off & ~15ull), slen, bar, 0);
+    __syncwarp();
+  };
+  typedef typename part_t<Q>::t P;
+  Cursor head{q0 + warp, 0, 0}, at = head;
+  const int total = q0 + warp < q1 ? ((q1 - 1 - q0 - warp) / NW + 1) * spq : 0;
+  int issued = 0;
+  for (; issued < total && issued < a.depth; ++issued, next(head)) issue(head, issued);
+  __syncthreads();  // the activation
+
+  bool ok = true;
+  P p = (P)0;
+  float y = 0.f;
+  int n = 0, slot = 0;
+  unsigned phase = 0;
+  for (; n < total; ++n) {
+    if (!__all_sync(FULL, mbar_wait(full0 + 8 * slot, phase, a.wait_ns, abort_flag))) {
+      if (lane == 0) raise_error(a.err, ERR_MOE_WAIT, abort_flag);
+      ok = false;
+      break;
+    }
+    const int k0 = at.c * a.tk, len = a.K - k0 < a.tk ? a.K - k0 : a.tk;
+    unsigned char* st = ring + (size_t)slot * a.stage_bytes;
+    unsigned sh[2];
+#pragma unroll
+    for (int r = 0; r < 2; ++r)
+      sh[r] = (unsigned)((((unsigned long long)stack_row(at, r) * nb + (k0 >> 5)) * 2) & 15);
+    quad_stage<Q>(p, st, a, k0, len, sh, smem + (GLU ? 0 : at.i * act_bytes<Q>(a.K)), lane);
+    __syncwarp();
+    if (issued < total) {
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      issue(head, slot);
+      next(head);
+      ++issued;
+    }
+    if (at.c == a.nsl - 1) {
+      const float v = row_sum(p);
+      p = (P)0;
+      if (GLU) {
+        const float u = __shfl_down_sync(FULL, v, 16);
+        const int i = at.q / per, o = 2 * (at.q - i * per) + (lane >> 3);
+        if (lane == 0 || lane == 8) a.out[(t * a.k + pair_of[i]) * a.rows + o] = swiglu(v, u);
+      } else {
+        y = __fmaf_rn(weight_of[at.i], v, y);
+        if (at.i == np - 1) {
+          if ((lane & 7) == 0) a.out[t * a.rows + 4 * at.q + (lane >> 3)] = y;
+          y = 0.f;
+        }
+      }
+    }
+    next(at);
+    if (++slot == a.depth) {
+      slot = 0;
+      phase ^= 1u;
+    }
+  }
+  // copies in flight land before the block may end
+  for (int m = n; m < issued; ++m) {
+    if (lane == 0) drain_wait(full0 + 8 * slot, phase, a.wait_ns, a.err);
+    if (++slot == a.depth) {
+      slot = 0;
+      phase ^= 1u;
+    }
+  }
+  if (!GLU && np == 0)
+    for (int o = 4 * q0 + threadIdx.x; o < 4 * q1; o += blockDim.x) a.out[t * a.rows + o] = 0.f;
+  if constexpr (GLU && Q > 0) {
+    if (!a.hq) return;
+    __threadfence();  // this block's h before its counts
+    __syncthreads();
+    if (!ok || *abort_flag || q1 <= q0) return;
+    for (int g = q0 / 16 + warp; g <= (q1 - 1) / 16; g += NW) {
+      const int lo = q0 > 16 * g ? q0 : 16 * g, hi = q1 < 16 * g + 16 ? q1 : 16 * g + 16;
+      const int i = g / (per / 16), gi = g - i * (per / 16);
+      const long pair = t * a.k + pair_of[i];
+      if (hi - lo < 16) {
+        int old = 0;
+        int* cnt = a.cnt + pair * (a.rows >> 5) + gi;
+        if (lane == 0) old = atomicAdd(cnt, hi - lo);
+        old = __shfl_sync(FULL, old, 0);
+        if (old + hi - lo != 16) continue;  // another block finishes it
+        if (lane == 0) *cnt = 0;
+        __threadfence();  // the others' h after their counts
+      }
+      quant_lane<Q>(__ldcg(a.out + pair * a.rows + 32 * gi + lane), a.hq + pair * a.rows,
+                    Q == 2 ? a.hl + pair * a.rows : nullptr, a.hs + pair * (a.rows >> 5), gi, lane);
+    }
+  }
+}
+
+// ---- host --------------------------------------------------------------------------
+
+// Stages: rows in equal slices of at most SLICE bytes, a multiple of 128, and as
+// many stages a warp as fit; more, shorter slices only where clearly more bytes
+// are in flight with them.
+bool fit(MoeArgs& a, int mode, int rows_held, int smem_optin, int* smem) {
+  const unsigned act = mode == 0 ? 4u * a.K : (unsigned)a.K * mode + a.K / 8u;
+  if ((unsigned long long)act * rows_held > 200000u) return false;
+  a.ring_off = (act * rows_held + 127u) & ~127u;
+  const int room = smem_optin - kStatic - (int)a.ring_off;
+  int best = 0;
+  for (int n = (a.K + SLICE - 1) / SLICE; n <= a.K / 128; ++n) {
+    const int tk = ((a.K + n - 1) / n + 127) & ~127;
+    const unsigned srow = (tk / 16u + 23u) & ~15u;  // a row's scales and half of 16 bytes, to 16
+    const unsigned bytes = (4u * tk + 4u * srow + 127u) & ~127u;
+    int depth = room / (int)(NW * bytes);
+    if (depth > DEPTH) depth = DEPTH;
+    if (depth * tk <= best + best / 8) continue;
+    best = depth * tk;
+    a.tk = tk;
+    a.nsl = (a.K + tk - 1) / tk;
+    a.srow = srow;
+    a.s_off = 4u * tk;
+    a.stage_bytes = bytes;
+    a.depth = depth;
+    *smem = (int)a.ring_off + NW * depth * (int)bytes;
+  }
+  return best > 0;
+}
+
+template <int Q, bool GLU>
+lk_status run(const MoeArgs& a, dim3 grid, int smem, int optin, int pdl, cudaStream_t stream) {
+  static std::atomic<int> done[kMaxDevices];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return LK_ERR_CUDA;
+  if (!done[dev].load(std::memory_order_acquire)) {
+    if (cudaFuncSetAttribute(moe_kernel<Q, GLU>, cudaFuncAttributeMaxDynamicSharedMemorySize, optin - kStatic) !=
+        cudaSuccess)
+      return LK_ERR_CUDA;
+    carveout_max_shared(moe_kernel<Q, GLU>);
+    done[dev].store(1, std::memory_order_release);
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(NW * 32);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = pdl ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, moe_kernel<Q, GLU>, a) == cudaSuccess ? LK_OK : LK_ERR_CUDA;
+}
+
+template <bool GLU>
+lk_status launch_moe(MoeArgs& a, int mode, int M, int held, const lk_launch_cfg* cfg, cudaStream_t stream) {
+  const DeviceInfo* d = device_info(nullptr);
+  if (!d) return LK_ERR_CUDA;
+  int smem = 0;
+  if (!fit(a, mode, held, d->smem_optin, &smem)) return LK_ERR_SHAPE;
+  a.wait_ns = opt_wait_us > 0 ? (unsigned long long)opt_wait_us * 1000ull : 2000000000ull;
+  a.err = error_word_ptr();
+  if (!a.err) return LK_ERR_CUDA;
+  const dim3 grid(M < d->sm_count ? (d->sm_count + M - 1) / M : 1, M);
+  const int pdl = cfg_pdl(cfg);
+  return mode == 0   ? run<0, GLU>(a, grid, smem, d->smem_optin, pdl, stream)
+         : mode == 1 ? run<1, GLU>(a, grid, smem, d->smem_optin, pdl, stream)
+                     : run<2, GLU>(a, grid, smem, d->smem_optin, pdl, stream);
+}
+
+// Checks that both calls make of a stack's shape, the mode, the rows and k.
+lk_status check_shape(int E, int rows, int K, lk_mode mode, int M, int k, const lk_launch_cfg* cfg) {
+  if (mode < LK_DEQUANT || mode > LK_TWOPASS || check_launch_cfg(cfg)) return LK_ERR_ARG;
+  if (E < 1 || E > LK_MOE_MAX_E || rows < 128 || rows % 128 || K < 128 || K % 128 || M < 0 || M > LK_MAX_BATCH ||
+      k < 1 || k > LK_MOE_MAX_K)
+    return LK_ERR_SHAPE;
+  // rows of a stack, and quads of a row's pairs, are 32-bit numbers
+  if ((long)E * rows > 0x7fffffffL || (long)k * rows > 0x3fffffffL) return LK_ERR_SHAPE;
+  return LK_OK;
+}
+// Activation rows by mode: present and aligned.
+lk_status check_act_in(lk_mode mode, const float* x, const int8_t* xq, const int8_t* xl, const float* xs) {
+  if (mode == LK_DEQUANT ? !x : (!xq || !xs || (mode == LK_TWOPASS && !xl))) return LK_ERR_ARG;
+  if (mode == LK_DEQUANT ? !aligned(x, 16) : (!aligned(xq, 16) || !aligned(xs, 16) || (mode == LK_TWOPASS && !aligned(xl, 16))))
+    return LK_ERR_ALIGN;
+  return LK_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+lk_status lk_moe_glu_q8(const int8_t* wg, const uint16_t* wsg, const int8_t* wu, const uint16_t* wsu, int E, int F,
+                        int K, lk_mode mode, const float* x, const int8_t* xq, const int8_t* xl, const float* xs, int M,
+                        const int32_t* ids, int k, float* h, int8_t* hq, int8_t* hl, float* hs, int* cnt,
+                        const lk_launch_cfg* cfg, cudaStream_t stream) {
+  lk_status st = check_shape(E, F, K, mode, M, k, cfg);
+  if (st) return st;
+  if (M == 0) return LK_OK;
+  if (!wg || !wsg || !wu || !wsu || !ids || !h) return LK_ERR_ARG;
+  if (!aligned(wg, 16) || !aligned(wsg, 16) || !aligned(wu, 16) || !aligned(wsu, 16) || !aligned(ids, 4) || !aligned(h, 16))
+    return LK_ERR_ALIGN;
+  if ((st = check_act_in(mode, x, xq, xl, xs))) return st;
+  if (mode == LK_DEQUANT) hq = nullptr;
+  if (hq) {
+    if (!hs || !cnt || (mode == LK_TWOPASS && !hl)) return LK_ERR_ARG;
+    if (!aligned(hq, 16) || !aligned(hs, 16) || !aligned(cnt, 4) || (mode == LK_TWOPASS && !aligned(hl, 16)))
+      return LK_ERR_ALIGN;
+  }
+  const size_t n = (size_t)M * k * F, mat = (size_t)E * F * K, act = (size_t)M * K;
+  const bool words = mode != LK_DEQUANT, two = mode == LK_TWOPASS;
+  const Span spans[] = {{h, n * 4},
+                        {hq, n},
+                        {hq && two ? hl : nullptr, n},
+                        {hq ? hs : nullptr, n / 8},
+                        {hq ? cnt : nullptr, n / 8},
+                        {wg, mat},
+                        {wsg, mat / 16},
+                        {wu, mat},
+                        {wsu, mat / 16},
+                        {words ? nullptr : x, act * 4},
+                        {words ? xq : nullptr, act},
+                        {two ? xl : nullptr, act},
+                        {words ? xs : nullptr, act / 8},
+                        {ids, (size_t)M * k * 4}};
+  if (spans_clash(spans, 5, sizeof spans / sizeof *spans)) return LK_ERR_ARG;
+  MoeArgs a = {};
+  a.wa = wg;
+  a.sa = (const unsigned char*)wsg;
+  a.wb = wu;
+  a.sb = (const unsigned char*)wsu;
+  a.E = E;
+  a.rows = F;
+  a.K = K;
+  a.x = x;
+  a.xq = xq;
+  a.xl = xl;
+  a.xs = xs;
+  a.ids = ids;
+  a.k = k;
+  a.out = h;
+  a.hq = hq;
+  a.hl = hl;
+  a.hs = hs;
+  a.cnt = cnt;
+  return launch_moe<true>(a, mode, M, 1, cfg, stream);
+}
+
+lk_status lk_moe_down_q8(const int8_t* wd, const uint16_t* wsd, int E, int N, int F, lk_mode mode, const float* h,
+                         const int8_t* hq, const int8_t* hl, const float* hs, int M, const int32_t* ids,
+                         const float* weights, int k, float* y, const lk_launch_cfg* cfg, cudaStream_t stream) {
+  lk_status st = check_shape(E, N, F, mode, M, k, cfg);
+  if (st) return st;
+  if (M == 0) return LK_OK;
+  if (!wd || !wsd || !ids || !weights || !y) return LK_ERR_ARG;
+  if (!aligned(wd, 16) || !aligned(wsd, 16) || !aligned(ids, 4) || !aligned(weights, 4) || !aligned(y, 16))
+    return LK_ERR_ALIGN;
+  if ((st = check_act_in(mode, h, hq, hl, hs))) return st;
+  const size_t mat = (size_t)E * N * F, act = (size_t)M * k * F;
+  const bool words = mode != LK_DEQUANT, two = mode == LK_TWOPASS;
+  const Span spans[] = {{y, (size_t)M * N * 4},
+                        {wd, mat},
+                        {wsd, mat / 16},
+                        {words ? nullptr : h, act * 4},
+                        {words ? hq : nullptr, act},
+                        {two ? hl : nullptr, act},
+                        {words ? hs : nullptr, act / 8},
+                        {ids, (size_t)M * k * 4},
+                        {weights, (size_t)M * k * 4}};
+  if (spans_clash(spans, 1, sizeof spans / sizeof *spans)) return LK_ERR_ARG;
+  MoeArgs a = {};
+  a.wa = wd;
+  a.sa = (const unsigned char*)wsd;
+  a.E = E;
+  a.rows = N;
+  a.K = F;
+  a.x = h;
+  a.xq = hq;
+  a.xl = hl;
+  a.xs = hs;
+  a.ids = ids;
+  a.weights = weights;
+  a.k = k;
+  a.out = y;
+  return launch_moe<false>(a, mode, M, k, cfg, stream);
+}
+
+}  // extern "C"

@@ -1,0 +1,263 @@
+// Routing to experts (include/lk_moe.h): lk_moe_route.
+//
+// A warp works on a row, its lanes hold the experts lane + 32 v.  The k largest
+// are taken one by one: each lane keeps its own largest, one warp maximum of
+// the values' order-preserving bits and one minimum of the holders' numbers
+// give the next, and its lane drops it.  What this costs is latency (a launch,
+// one read, k + 1 rounds of two warp reductions); there are no bytes to speak of.
+//
+// Which experts are taken is decided in f32 where f32 can: a score is within
+// 2^-19 of its value (exp's argument is rounded to 2^-24 of |l - max|, and
+// e^-x (x + 16) 2^-23 is at most 2^-19; a sigmoid is nearer), so values further
+// apart than 2^-17 (and 2^-22 of themselves, for the rounding of s + bias) are
+// in the right order.  A row where two neighbours of the order taken, or a
+// group that stays and one that does not, are nearer than that (about one row
+// in a thousand), is done again in f64, whose exp would cost every row some
+// microseconds on this GPU's narrow f64 pipe.  Without a bias the order is the
+// logits' own, and exact.
+#include <float.h>
+#include <math.h>
+
+#include "lk_device.cuh"
+#include "lk_moe.h"
+#include "lk_spans.h"
+
+using namespace lk;
+using namespace lkh;
+
+namespace {
+
+struct RouteArgs {
+  const float* logits;
+  const float* bias;
+  int E, n_group, top_group, group_sum, k;
+  int gs;          // experts of a group
+  unsigned g_inv;  // ceil(2^20 / gs): i / gs = i * g_inv >> 20 for i < 1024
+  int sigmoid, renorm;
+  float scale;
+  int* ids;
+  float* weights;
+};
+
+// ---- the two precisions ------------------------------------------------------------
+
+__device__ __forceinline__ unsigned ordered(float v) {
+  const unsigned u = __float_as_uint(v == 0.0f ? 0.0f : v);
+  return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+}
+__device__ __forceinline__ float unordered(unsigned u) {
+  return __uint_as_float((u & 0x80000000u) ? (u & 0x7FFFFFFFu) : ~u);
+}
+__device__ __forceinline__ float warp_max(float v) { return unordered(__reduce_max_sync(FULL, ordered(v))); }
+__device__ __forceinline__ double warp_max(double v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v = fmax(v, __shfl_xor_sync(FULL, v, o));
+  return v;
+}
+__device__ __forceinline__ float exp_of(float x) { return expf(x); }
+__device__ __forceinline__ double exp_of(double x) { return exp(x); }
+
+// One row in precision T: the chosen experts and their weights in lanes < k.
+// False: T (f32) does not decide it.
+template <typename T, int V>
+__device__ __forceinline__ bool route_row(const RouteArgs& a, const float (&l)[V], const float (&b)[V], int lane,
+                                          T* vals, int& id, float& weight) {
+  constexpr bool F32 = sizeof(T) == 4;
+  const T none = (T)-INFINITY;
+  const bool by_logit = a.bias == nullptr;
+  T p[V], c[V];
+  T m = none, pmax = (T)1;
+#pragma unroll
+  for (int v = 0; v < V; ++v) m = l[v] > m ? (T)l[v] : m;
+  m = warp_max(m);
+  if (m == none) m = (T)0;  // no expert at all
+  if (!a.sigmoid) {
+    T sum = (T)0;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      p[v] = l[v] > -INFINITY ? exp_of((T)l[v] - m) : (T)0;
+      sum += p[v];
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(FULL, sum, o);
+    pmax = sum > (T)0 ? (T)1 / sum : (T)1;
+#pragma unroll
+    for (int v = 0; v < V; ++v) p[v] *= pmax;
+  } else {
+#pragma unroll
+    for (int v = 0; v < V; ++v) p[v] = l[v] > -INFINITY ? (T)1 / ((T)1 + exp_of(-(T)l[v])) : (T)0;
+  }
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    const bool there = l[v] > -INFINITY && b[v] - b[v] == 0.0f;
+    c[v] = !there ? none : by_logit ? (T)l[v] : p[v] + (T)b[v];
+  }
+  const T slack = F32 ? (T)0x1p-17f * pmax : (T)0, part = F32 ? (T)0x1p-22f : (T)0;
+  bool sure = true;
+
+  if (a.n_group > 1) {
+    const bool sums = a.group_sum == 2, of_scores = by_logit && sums;
+    __syncwarp();
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const int i = lane + 32 * v;
+      if (i < a.E) vals[i] = of_scores && c[v] > none ? p[v] : c[v];
+    }
+    __syncwarp();
+    T t1 = none, t2 = none;
+    if (lane < a.n_group)
+      for (int i = lane * a.gs; i < (lane + 1) * a.gs; ++i) {
+        const T x = vals[i];
+        t2 = x > t1 ? t1 : x > t2 ? x : t2;
+        t1 = x > t1 ? x : t1;
+      }
+    const T val = sums && t2 > none ? t1 + t2 : t1;
+    int rank = 0;
+    for (int g = 0; g < a.n_group; ++g) {
+      const T w = __shfl_sync(FULL, val, g);
+      rank += w > val || (w == val && g < lane);
+    }
+    const unsigned stay = __ballot_sync(FULL, lane < a.n_group && val > none && rank < a.top_group);
+    if (F32 && !(by_logit && !sums)) {
+      for (int g = 0; g < a.n_group; ++g) {
+        const T w = __shfl_sync(FULL, val, g);
+        if (lane < a.n_group && val > none && w > none && (((stay >> g) ^ (stay >> lane)) & 1u))
+          sure = sure && fabsf((float)(w - val)) > 2.0f * (float)slack + 2.0f * (float)part * fabsf((float)val);
+      }
+      sure = __all_sync(FULL, sure);
+    }
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const unsigned i = lane + 32 * v;
+      if (!((stay >> ((i * a.g_inv) >> 20)) & 1u)) c[v] = none;
+    }
+  }
+
+  T best = none, pb = (T)0, prev = none;
+  float lb = 0.f, lmine = 0.f;
+  T pmine = (T)0;
+  int vb = 0;
+  id = -1;
+  auto own_best = [&] {
+    best = none;
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+      if (c[v] > best) {
+        best = c[v];
+        vb = v;
+        pb = p[v];
+        lb = l[v];
+      }
+  };
+  own_best();
+  const int rounds = a.k + (F32 && !by_logit ? 1 : 0);  // one more: the gap behind the last
+  for (int j = 0; j < rounds; ++j) {
+    const T top = warp_max(best);
+    if (top == none) break;
+    const unsigned i = __reduce_min_sync(FULL, best == top ? (unsigned)(lane + 32 * vb) : 0xFFFFFFFFu);
+    const int owner = (int)(i & 31u);
+    if (F32 && !by_logit && j > 0) sure = sure && prev - top > slack + part * (T)fabsf((float)prev);
+    prev = top;
+    const T pt = __shfl_sync(FULL, pb, owner);
+    const float lt = __shfl_sync(FULL, lb, owner);
+    if (lane == j && j < a.k) {
+      id = (int)i;
+      pmine = pt;
+      lmine = lt;
+    }
+    if (lane == owner) {
+#pragma unroll
+      for (int v = 0; v < V; ++v)
+        if (v == vb) c[v] = none;
+      own_best();
+    }
+  }
+
+  T w = id >= 0 ? pmine : (T)0;
+  if (a.renorm) {
+    if (!a.sigmoid) {
+      // from the chosen logits alone: the row's largest may be in no chosen group
+      const T lm = warp_max(id >= 0 ? (T)lmine : none);
+      w = id >= 0 ? exp_of((T)lmine - lm) : (T)0;
+    }
+    T sum = w;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(FULL, sum, o);
+    // sigmoids this small: their quotient needs f64's range
+    if (F32 && sum < (T)1e-30f && __any_sync(FULL, id >= 0)) return false;
+    w = sum > (T)0 ? w / sum : (T)0;
+  }
+  weight = (float)(w * (T)a.scale);
+  return sure;
+}
+
+template <int V>
+__device__ __noinline__ void route_row_f64(const RouteArgs& a, const float (&l)[V], const float (&b)[V], int lane,
+                                           double* vals, int& id, float& weight) {
+  route_row<double, V>(a, l, b, lane, vals, id, weight);
+}
+
+template <int V>
+__global__ void __launch_bounds__(32) route_kernel(const RouteArgs a) {
+  __shared__ double vals[32 * V];
+  const int lane = threadIdx.x;
+  const long row = blockIdx.x;
+  asm volatile("griddepcontrol.launch_dependents;" :::);
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  float l[V], b[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    const int i = lane + 32 * v;
+    float x = i < a.E ? __ldcg(a.logits + row * a.E + i) : -INFINITY;
+    b[v] = a.bias && i < a.E ? __ldcg(a.bias + i) : 0.0f;
+    if (!(x >= -INFINITY)) x = -INFINITY;  // NaN
+    l[v] = fminf(x, FLT_MAX);
+  }
+  int id;
+  float w;
+  if (!route_row<float, V>(a, l, b, lane, (float*)vals, id, w)) route_row_f64<V>(a, l, b, lane, vals, id, w);
+  if (lane < a.k) {
+    a.ids[row * a.k + lane] = id;
+    a.weights[row * a.k + lane] = w;
+  }
+}
+
+}  // namespace
+
+extern "C" lk_status lk_moe_route(const float* logits, const float* bias, int M, int E, lk_score score, int n_group,
+                                  int top_group, int group_sum, int k, int renorm, float scale, int32_t* ids,
+                                  float* weights, const lk_launch_cfg* cfg, cudaStream_t stream) {
+  if ((score != LK_SCORE_SOFTMAX && score != LK_SCORE_SIGMOID) || check_launch_cfg(cfg)) return LK_ERR_ARG;
+  if (!(scale - scale == 0.0f)) return LK_ERR_ARG;  // not finite
+  if (M < 0 || M > LK_MAX_BATCH || E < 1 || E > LK_MOE_MAX_E || k < 1 || k > E || k > LK_MOE_MAX_K) return LK_ERR_SHAPE;
+  if (n_group < 1 || n_group > LK_MOE_MAX_GROUPS || E % n_group || top_group < 1 || top_group > n_group ||
+      group_sum < 1 || group_sum > 2)
+    return LK_ERR_SHAPE;
+  if (M == 0) return LK_OK;
+  if (!logits || !ids || !weights) return LK_ERR_ARG;
+  if (!aligned(logits, 4) || !aligned(bias, 4) || !aligned(ids, 4) || !aligned(weights, 4)) return LK_ERR_ALIGN;
+  const size_t out = (size_t)M * k * 4;
+  const Span spans[] = {{ids, out}, {weights, out}, {logits, (size_t)M * E * 4}, {bias, (size_t)E * 4}};
+  if (spans_clash(spans, 2, 4)) return LK_ERR_ARG;
+  RouteArgs a;
+  a.logits = logits;
+  a.bias = bias;
+  a.E = E;
+  a.n_group = n_group;
+  a.top_group = top_group;
+  a.group_sum = group_sum;
+  a.k = k;
+  a.gs = E / n_group;
+  a.g_inv = ((1u << 20) + a.gs - 1) / a.gs;
+  a.sigmoid = score == LK_SCORE_SIGMOID;
+  a.renorm = renorm != 0;
+  a.scale = scale;
+  a.ids = ids;
+  a.weights = weights;
+  const int pdl = cfg_pdl(cfg);
+  // values a lane holds: the smallest of these that fit, fewer steps a round
+  if (E <= 128) launch_pdl(route_kernel<4>, dim3(M), dim3(32), stream, pdl, a);
+  else if (E <= 256) launch_pdl(route_kernel<8>, dim3(M), dim3(32), stream, pdl, a);
+  else launch_pdl(route_kernel<32>, dim3(M), dim3(32), stream, pdl, a);
+  return launch_status();
+}

@@ -1,5 +1,6 @@
 """Thin ctypes binding of liblk.so (the C ABI declared in include/lk.h and,
-for the attention step, include/lk_attn.h).
+for the attention step, include/lk_attn.h, for a mixture of experts
+include/lk_moe.h, for the drawn token include/lk_sample.h).
 
 Each ``lk_*`` function here has the name and argument order of the C entry
 point; it only checks and marshals torch tensors (dtype, device, contiguity,
@@ -124,6 +125,10 @@ def _load():
         "lk_attn_shared": ([P, P, I, P, I, I, P, I, P, I, I, F, I, P, P, P, P, P, S, P, P], I),
         "lk_attn_workspace_bytes": ([I, I, I, I, I, I], S),
         "lk_attn_launches": ([I, I, I, I, I, I, I, I], I),
+        "lk_moe_route": ([P, P, I, I, I, I, I, I, I, I, F, P, P, P, P], I),
+        "lk_moe_glu_q8": ([P, P, P, P, I, I, I, I, P, P, P, P, I, P, I, P, P, P, P, P, P, P], I),
+        "lk_moe_down_q8": ([P, P, I, I, I, I, P, P, P, P, I, P, P, I, P, P, P], I),
+        "lk_sample": ([P, I, I, P, P, P, P, P, P, P, P, P], I),
     }
     for name, (args, res) in sig.items():
         fn = getattr(lib, name)
@@ -146,6 +151,16 @@ def exported_symbols():
 def attn_symbols():
     """The entry points of include/lk_attn.h."""
     return ["lk_kv_append", "lk_attn", "lk_attn_shared", "lk_attn_workspace_bytes", "lk_attn_launches"]
+
+
+def moe_symbols():
+    """The entry points of include/lk_moe.h."""
+    return ["lk_moe_route", "lk_moe_glu_q8", "lk_moe_down_q8"]
+
+
+def sample_symbols():
+    """The entry points of include/lk_sample.h."""
+    return ["lk_sample"]
 
 
 def _ok(st, where):
@@ -621,3 +636,133 @@ def lk_attn_shared(cache: KvCache, q, prefix_table, prefix_len, table, lens, ws,
     _ok(_load().lk_attn_shared(cache.ref, qp, n_q, _on(dev, prefix_table, _I32, "prefix_table"),
                                0 if prefix_table is None else prefix_table.numel(), prefix_len, tp, tw, lp, B, R,
                                *tail, _cfg(cfg), _on_stream(stream, dev)), "lk_attn_shared")
+
+
+# ---- a mixture of experts: routing, the experts' products (include/lk_moe.h) ----------
+
+LK_MOE_MAX_E, LK_MOE_MAX_K, LK_MOE_MAX_GROUPS = 1024, 32, 32
+SCORES = {"softmax": 0, "sigmoid": 1}
+
+
+def _here(t, name):
+    """The device number of tensor t, which has to be the current device."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch tensor")
+    dev = t.get_device()
+    if dev < 0 or torch.cuda.current_device() != dev:
+        raise ValueError(f"{name} must be on the current CUDA device")
+    return dev
+
+
+def lk_moe_route(logits, ids, weights, bias=None, score="softmax", n_group=1, top_group=1, group_sum=1, renorm=True,
+                 scale=1.0, stream=None, cfg=None):
+    """The experts ids int32 [M, k] of each row of router logits f32 [M, E] and
+    their weights f32 [M, k] (see include/lk_moe.h).  score "softmax" or
+    "sigmoid"; bias f32 [E] is added for the choice alone; of n_group groups
+    of experts the top_group best stay, by the sum of their group_sum largest;
+    renorm: weights over their sum, times scale."""
+    dev = _here(logits, "logits")
+    if logits.dim() != 2 or ids.dim() != 2:
+        raise ValueError("logits must be [M, E], ids [M, k]")
+    M, E = logits.shape
+    k = ids.shape[1]
+    _ok(_load().lk_moe_route(_on(dev, logits, _F32, "logits"), _on(dev, bias, _F32, "bias", (E,)), M, E,
+                             SCORES[score] if isinstance(score, str) else int(score), n_group, top_group, group_sum,
+                             k, 1 if renorm else 0, scale, _on(dev, ids, _I32, "ids", (M, k)),
+                             _on(dev, weights, _F32, "weights", (M, k)), _cfg(cfg), _on_stream(stream, dev)),
+        "lk_moe_route")
+
+
+class Experts:
+    """Q8_0 matrices of E experts over the caller's tensors: gate and up
+    (levels int8 [E, F, K], scales float16 [E, F, K / 32]) and / or down
+    ([E, K, F], [E, K, F / 32]).  Marshalled once; the tensors are kept alive
+    with it."""
+
+    def __init__(self, gate=None, up=None, down=None):
+        if (gate is None) != (up is None) or (gate is None and down is None):
+            raise ValueError("gate and up go together; at least they or down")
+        self.gate, self.up, self.down = gate, up, down
+        first = gate or down
+        self.dev = first[0].get_device()
+        self.E = first[0].shape[0]
+        for name, pair in (("gate", gate), ("up", up), ("down", down)):
+            if pair is None:
+                continue
+            q, s = pair
+            if not isinstance(q, torch.Tensor) or q.dtype != _I8 or q.dim() != 3 or s.dtype not in _WS:
+                raise TypeError(f"{name} must be int8 levels [E, rows, K] and their float16 scales")
+            if q.shape[0] != self.E or tuple(s.shape) != (*q.shape[:2], q.shape[2] // 32):
+                raise ValueError(f"{name}'s scales must be [E, rows, K / 32], E the same for all")
+            if q.get_device() != self.dev or s.get_device() != self.dev or self.dev < 0:
+                raise ValueError("the experts' tensors must be on one CUDA device")
+            if not q.is_contiguous() or not s.is_contiguous():
+                raise ValueError(f"{name} must be contiguous")
+        if gate is not None and gate[0].shape != up[0].shape:
+            raise ValueError("gate and up must have the same shape")
+        if gate is not None and down is not None and down[0].shape[2] != gate[0].shape[1]:
+            raise ValueError("down's rows must be as long as gate has rows")
+        self._gu = None if gate is None else (*(t.data_ptr() for t in (*gate, *up)), *gate[0].shape)
+        self._down = None if down is None else (*(t.data_ptr() for t in down), *down[0].shape)
+
+
+def _pairs(experts, ids):
+    if torch.cuda.current_device() != experts.dev:
+        raise ValueError(f"the experts are on cuda:{experts.dev}, which is not the current device")
+    if ids.dim() != 2:
+        raise ValueError("ids must be [M, k]")
+    return (experts.dev, *ids.shape)
+
+
+def lk_moe_glu_q8(experts: Experts, mode, ids, h, x=None, xq=None, xl=None, xs=None, hq=None, hl=None, hs=None, cnt=None,
+                  stream=None, cfg=None):
+    """h[t * k + j] = silu(gate x_t) * (up x_t) with the matrices of expert
+    ids[t, j] (see include/lk_moe.h): h f32 [M * k, F] and, with hq, its words hq,
+    hl and scales hs for the down products (cnt: zeroed int32, M * k * F / 32 of
+    them at least).  The rows x or xq, xl, xs [M, K] by mode, as lk_gemv_q8's."""
+    dev, M, k = _pairs(experts, ids)
+    if experts._gu is None:
+        raise ValueError("these experts have no gate and up matrices")
+    *w, E, F, K = experts._gu
+    n = M * k
+    if cnt is not None and cnt.numel() < n * F // 32:
+        raise ValueError("cnt must have M * k * F / 32 entries")
+    _ok(_load().lk_moe_glu_q8(*w, E, F, K, _mode(mode), _on(dev, x, _F32, "x", (M, K)), _on(dev, xq, _I8, "xq", (M, K)),
+                              _on(dev, xl, _I8, "xl", (M, K)), _on(dev, xs, _F32, "xs", (M, K // 32)), M,
+                              _on(dev, ids, _I32, "ids"), k, _on(dev, h, _F32, "h", (n, F)),
+                              _on(dev, hq, _I8, "hq", (n, F)), _on(dev, hl, _I8, "hl", (n, F)),
+                              _on(dev, hs, _F32, "hs", (n, F // 32)), _on(dev, cnt, _I32, "cnt"), _cfg(cfg),
+                              _on_stream(stream, dev)), "lk_moe_glu_q8")
+
+
+def lk_moe_down_q8(experts: Experts, mode, ids, weights, y, h=None, hq=None, hl=None, hs=None, stream=None, cfg=None):
+    """y[t] = sum over j of weights[t, j] * (down h[t * k + j]) with the matrix
+    of expert ids[t, j] (see include/lk_moe.h); h, or hq, hl, hs by mode, as
+    lk_moe_glu_q8 gives them."""
+    dev, M, k = _pairs(experts, ids)
+    if experts._down is None:
+        raise ValueError("these experts have no down matrices")
+    *w, E, N, F = experts._down
+    n = M * k
+    _ok(_load().lk_moe_down_q8(*w, E, N, F, _mode(mode), _on(dev, h, _F32, "h", (n, F)), _on(dev, hq, _I8, "hq", (n, F)),
+                               _on(dev, hl, _I8, "hl", (n, F)), _on(dev, hs, _F32, "hs", (n, F // 32)), M,
+                               _on(dev, ids, _I32, "ids"), _on(dev, weights, _F32, "weights", (M, k)), k,
+                               _on(dev, y, _F32, "y", (M, N)), _cfg(cfg), _on_stream(stream, dev)), "lk_moe_down_q8")
+
+
+# ---- the next token drawn from the logits (include/lk_sample.h) -------------------------
+
+def lk_sample(logits, u, idx, prob=None, temperature=None, top_k=None, top_p=None, min_p=None, stream=None, cfg=None):
+    """One token idx int32 [M] for each row of logits f32 [M, N], drawn by the
+    numbers u f32 [M] in [0, 1) from what temperature, top_k, top_p and min_p
+    ([M] tensors, None: off) leave, and its probability prob f32 [M] (see
+    include/lk_sample.h)."""
+    dev = _here(logits, "logits")
+    if logits.dim() != 2:
+        raise ValueError("logits must be [M, N]")
+    M, N = logits.shape
+    _ok(_load().lk_sample(_on(dev, logits, _F32, "logits"), M, N, _on(dev, temperature, _F32, "temperature", (M,)),
+                          _on(dev, top_k, _I32, "top_k", (M,)), _on(dev, top_p, _F32, "top_p", (M,)),
+                          _on(dev, min_p, _F32, "min_p", (M,)), _on(dev, u, _F32, "u", (M,)),
+                          _on(dev, idx, _I32, "idx", (M,)), _on(dev, prob, _F32, "prob", (M,)), _cfg(cfg),
+                          _on_stream(stream, dev)), "lk_sample")
