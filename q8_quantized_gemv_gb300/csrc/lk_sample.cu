@@ -64,29 +64,34 @@ __device__ __forceinline__ Slope slope_of(float T) {
   return s;
 }
 
+// The table in shared memory: the entries, and as floats.
+struct Table {
+  u64 w[256];
+  float f[256];
+};
+
 // e = (mant 2^-n) 2^-ONE, mant in [2^ONE, 2^(ONE+1)); n 63 for what is nothing
-__device__ __forceinline__ u64 weight_parts(float l, float m, const Slope& c, const u64* table, int& n) {
+__device__ __forceinline__ u64 weight_parts(float l, float m, const Slope& c, const Table& table, int& n) {
   // l - m = d + r exactly (D. E. Knuth's two-sum)
   const float d = __fsub_rn(l, m), bb = __fsub_rn(d, l);
   const float r = __fadd_rn(__fsub_rn(l, __fsub_rn(d, bb)), __fsub_rn(-m, bb));
   const float t = __fmul_rn(d, c.hi);
-  if (!(t >= -62.0f)) {
-    n = 63;
-    return 0;
-  }
+  const bool there = t >= -62.0f;
   const float te = __fmaf_rn(d, c.hi, -t) + __fmaf_rn(d, c.lo, __fmul_rn(r, c.hi));
-  const float kf = rintf(__fmul_rn(t, 256.0f));
-  const int k = (int)kf;
+  const float big = __fmaf_rn(t, 256.0f, 12582912.0f);  // 1.5 * 2^23: the nearest whole number in the low bits
+  const float kf = __fsub_rn(big, 12582912.0f);
+  const int k = __float_as_int(big) - 0x4B400000;
   const float f = __fadd_rn(__fmaf_rn(kf, -0.00390625f, t), te);  // |f| <= 1/512
   const float q = __fmul_rn(f, fmaf(f, fmaf(f, 0.055504109f, 0.24022651f), 0.69314718f));
-  const u64 w = table[k & 255];
-  n = -(k >> 8);
-  return w + (long long)__float2int_rn(__fmul_rn((float)w, q));  // |w q| < 2^30.5
+  n = there ? -(k >> 8) : 63;
+  const int j = k & 255;
+  return table.w[j] + (long long)__float2int_rn(__fmul_rn(table.f[j], q));  // |w q| < 2^30.5
 }
-__device__ __forceinline__ u64 weight_of(float l, float m, const Slope& c, const u64* table) {
+__device__ __forceinline__ u64 weight_of(float l, float m, const Slope& c, const Table& table) {
   int n;
   const u64 w = weight_parts(l, m, c, table, n);
-  return n > ONE + 1 ? 0ull : n > 0 ? (w + (1ull << (n - 1))) >> n : w;
+  // rounded to nearest; n > ONE + 1 is nothing
+  return n > ONE + 1 ? 0ull : (w + ((1ull << n) >> 1)) >> n;
 }
 
 // ---- rows --------------------------------------------------------------------------
@@ -109,7 +114,8 @@ __device__ __forceinline__ float value_of(u64 key) {
 struct SampleArgs {
   const float* logits;
   int N;
-  int part;  // tokens of a warp's part of a row, a multiple of 32
+  int part;  // tokens of a warp's part of a row, a multiple of 128
+  int held;  // of these, in shared memory
   const float* T;
   const int* top_k;
   const float* top_p;
@@ -122,14 +128,17 @@ struct SampleArgs {
 constexpr int NW = 16;             // warps of a block
 constexpr int THREADS = 32 * NW;
 constexpr int MAX_C = 8;           // blocks of a row at most
+constexpr int kHeld = 2048;        // tokens of a warp's part in shared memory at most
 constexpr int NB = 2048;           // bins of the order
 constexpr int CAP = 4096;          // tokens near the borders that are sorted
 constexpr float REACH = 41.0f;     // log2 of the largest weight over the smallest that is not 0
-constexpr float SLACK = 1e-4f;     // of the bins' estimated sums
+constexpr float SLACK = 6e-4f;     // of the bins' estimated sums
+constexpr int PLACES = 16;         // places in a bin
+constexpr int POS_BITS = 18;       // a bin's word: the sum of its tokens' places, above it their number
 
-struct Shared {
-  u64 table[256];
-  unsigned cnt[NB], pos[NB];       // this block's tokens in each bin, and their places in it
+struct alignas(16) Shared {
+  Table table;
+  unsigned bin[NB];                // this block's tokens in each bin, and their places in it
   union {
     struct {
       unsigned cnt[NB], pos[NB];   // the row's
@@ -140,7 +149,8 @@ struct Shared {
   u64 drawn[MAX_C * NW];           // sums of the parts, of what is kept for the draw
   u64 first[MAX_C];                // of each block: its first key,
   float low[MAX_C];                // its lowest logit,
-  unsigned n_list[MAX_C];          // its tokens in list,
+  unsigned n_list[MAX_C];          // its tokens in list, and in bins,
+  unsigned n_bin[MAX_C];
   u64 kept[MAX_C], mid[MAX_C];     // its sums before and between the windows
   u64 sums[2][MAX_C];
   u64 warp[NW];
@@ -152,6 +162,9 @@ struct Shared {
   u64 goal;
   int at;
 };
+
+// (the tokens held lie behind it, read and written by 16 bytes)
+static_assert(sizeof(Shared) % 16 == 0 && sizeof(Shared) + NW * kHeld * 4 <= 227 * 1024, "shared memory");
 
 __device__ __forceinline__ u64 warp_sum(u64 v) {
 #pragma unroll
@@ -193,40 +206,113 @@ __device__ float block_before(float v, float& all, Shared& s) {
   __syncthreads();
   if (lane == 31) s.fwarp[w] = inc;
   __syncthreads();
-  float before = 0.f;
-  all = 0.f;
-  for (int i = 0; i < NW; ++i) {
-    if (i < w) before += s.fwarp[i];
-    all += s.fwarp[i];
+  const float tot = lane < NW ? s.fwarp[lane] : 0.f;
+  float before = lane < w ? tot : 0.f;
+  all = tot;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    before += __shfl_xor_sync(FULL, before, o);
+    all += __shfl_xor_sync(FULL, all, o);
   }
   return before + inc - v;
 }
 
-// Where a token lies in the order: 256 times its bin, plus its place there.
+// Sum of the values of the threads behind this one.
+__device__ float block_after(float v, Shared& s) {
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  float inc = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const float y = __shfl_down_sync(FULL, inc, o);
+    if (lane + o < 32) inc += y;
+  }
+  __syncthreads();
+  if (lane == 0) s.fwarp[w] = inc;
+  __syncthreads();
+  float after = lane > w && lane < NW ? s.fwarp[lane] : 0.f;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) after += __shfl_xor_sync(FULL, after, o);
+  return after + __shfl_down_sync(FULL, inc, 1) * (lane < 31);
+}
+
+// Where a token lies in the order: PLACES times its bin, plus its place there.
 struct Bins {
   float m, c, scale;
   __device__ __forceinline__ float depth(float l) const { return __fmul_rn(__fsub_rn(m, l), c); }  // in log2
   // any monotone function of the logit serves; all of it is finite for depth < REACH
   __device__ __forceinline__ unsigned place(float depth) const {
-    return min((unsigned)__float_as_int(__fadd_rn(__fmul_rn(depth, scale), 8388608.0f)) & 0x7FFFFFu, 256u * NB - 1u);
+    return min((unsigned)__float_as_int(__fadd_rn(__fmul_rn(depth, scale), 8388608.0f)) & 0x7FFFFFu, (unsigned)PLACES * NB - 1u);
   }
 };
 
-// The tokens of this warp's part, eight loads in flight a lane: f(logit, index).
-template <typename F>
-__device__ __forceinline__ void each(const float* x, int lo, int hi, F f) {
-  const int lane = threadIdx.x & 31;
-  for (int i0 = lo + lane; i0 - lane < hi; i0 += 256) {
-    float l[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) l[j] = i0 + 32 * j < hi ? __ldcg(x + i0 + 32 * j) : NAN;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) f(clean(l[j]), i0 + 32 * j);
+// A warp's part of a row: tokens [lo, hi), of which the first `held` are in its
+// shared memory once they have been read.  Rows need not begin at 16 bytes: the
+// part's first `skew` places (below 4) lie before it and are no tokens.
+struct Part {
+  const float* x;
+  float* mem;
+  int lo, hi, held;
+  __device__ __forceinline__ float4 load(int i) const {
+    float4 v;
+    if (i >= 0 && i + 3 < hi) {
+      v = __ldcg((const float4*)(x + i));
+    } else {
+      v.x = i >= 0 && i < hi ? __ldcg(x + i) : NAN;
+      v.y = i + 1 >= 0 && i + 1 < hi ? __ldcg(x + i + 1) : NAN;
+      v.z = i + 2 >= 0 && i + 2 < hi ? __ldcg(x + i + 2) : NAN;
+      v.w = i + 3 < hi ? __ldcg(x + i + 3) : NAN;
+    }
+    return make_float4(clean(v.x), clean(v.y), clean(v.z), clean(v.w));
   }
-}
+  // f(logit, index) of every token, and of some places that are none with -inf:
+  // from global memory, eight loads in flight a lane, to shared memory.
+  template <typename F>
+  __device__ __forceinline__ void first(F f) const {
+    const int lane = threadIdx.x & 31;
+    constexpr int U = 8;
+    for (int i0 = lo + 4 * lane; i0 - 4 * lane < hi; i0 += 128 * U) {
+      float4 v[U];
+#pragma unroll
+      for (int j = 0; j < U; ++j) v[j] = load(i0 + 128 * j);
+#pragma unroll
+      for (int j = 0; j < U; ++j) {
+        const int i = i0 + 128 * j;
+        if (i - 4 * lane >= hi) break;  // (the whole warp)
+        if (i - lo < held) *(float4*)(mem + (i - lo)) = v[j];
+        f(v[j].x, i);
+        f(v[j].y, i + 1);
+        f(v[j].z, i + 2);
+        f(v[j].w, i + 3);
+      }
+    }
+  }
+  // The same again, where the tokens are now.  The loop is rolled (f is some hundred
+  // instructions, and fetching code unrolled eight times took longer than the work),
+  // with the next two loads in flight.
+  template <typename F>
+  __device__ __forceinline__ void again(F f) const {
+    const int lane = threadIdx.x & 31;
+    auto get = [&](int i) -> float4 {
+      if (i - lo < held) return *(const float4*)(mem + (i - lo));
+      return load(i);
+    };
+    int i = lo + 4 * lane;
+    float4 v = get(i), next = get(i + 128);
+#pragma unroll 1
+    for (; i - 4 * lane < hi; i += 128) {
+      const float4 later = get(i + 256);
+      f(v.x, i);
+      f(v.y, i + 1);
+      f(v.z, i + 2);
+      f(v.w, i + 3);
+      v = next;
+      next = later;
+    }
+  }
+};
 
 __global__ void __launch_bounds__(THREADS) sample_kernel(const SampleArgs a) {
-  extern __shared__ __align__(16) unsigned char smem[];
+  extern __shared__ __align__(128) unsigned char smem[];
   Shared& s = *(Shared*)smem;
   cg::cluster_group cl = cg::this_cluster();
   const int C = (int)cl.num_blocks(), me = (int)cl.block_rank();
@@ -235,24 +321,39 @@ __global__ void __launch_bounds__(THREADS) sample_kernel(const SampleArgs a) {
     s.listed = 0;
     asm volatile("griddepcontrol.launch_dependents;" :::);
   }
-  for (int i = threadIdx.x; i < 256; i += THREADS) s.table[i] = kExp2.v[i];
-  for (int i = threadIdx.x; i < NB; i += THREADS) s.cnt[i] = s.pos[i] = 0;
+  for (int i = threadIdx.x; i < 256; i += THREADS) {
+    s.table.w[i] = kExp2.v[i];
+    s.table.f[i] = (float)kExp2.v[i];
+  }
+  for (int i = threadIdx.x; i < NB; i += THREADS) s.bin[i] = 0;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const long row = blockIdx.x / C;
   const int N = a.N;
   const float* x = a.logits + row * N;
   const int slot = me * NW + warp;
-  const int lo = min(N, slot * a.part), hi = min(N, lo + a.part);
+  // parts begin at 16 bytes: the first at up to three places before the row
+  const int skew = (int)(((uintptr_t)x >> 2) & 3);
+  Part mine;
+  mine.x = x;
+  mine.lo = min(N, slot * a.part - skew);
+  mine.hi = min(N, (slot + 1) * a.part - skew);
+  mine.held = a.held;
+  mine.mem = (float*)(smem + sizeof(Shared)) + (size_t)warp * a.held;
 
   // the first of the order, and the lowest logit
   {
     u64 first = ~0ull;
     float low = INFINITY;
-    each(x, lo, hi, [&](float l, int i) {
-      const u64 k = key_of(l, i);
-      first = l > -INFINITY && k < first ? k : first;
+    float top = -INFINITY;
+    int at = 0;
+    mine.first([&](float l, int i) {
+      if (l > top) {  // (indices ascend in a lane)
+        top = l;
+        at = i;
+      }
       low = l > -INFINITY ? fminf(low, l) : low;
     });
+    if (top > -INFINITY) first = key_of(top, at);
     first = ~warp_max_u64(~first);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) low = fminf(low, __shfl_xor_sync(FULL, low, o));
@@ -302,44 +403,51 @@ __global__ void __launch_bounds__(THREADS) sample_kernel(const SampleArgs a) {
   if (by_k || by_p) {
     // ---- the order in bins ----
     const float reach = fminf(REACH, __fmul_rn(__fsub_rn(m, low), c.hi));
-    const Bins bins = {m, c.hi, fminf(256.0f * (NB - 1) / fmaxf(reach, 1e-30f), 1e30f)};
-    each(x, lo, hi, [&](float l, int) {
+    const Bins bins = {m, c.hi, fminf((float)PLACES * (NB - 1) / fmaxf(reach, 1e-30f), 1e30f)};
+    unsigned binned = 0;
+    mine.again([&](float l, int) {
       const float d = bins.depth(l);
       if (d < REACH) {
         const unsigned p = bins.place(d);
-        atomicAdd(&s.cnt[p >> 8], 1u);
-        atomicAdd(&s.pos[p >> 8], p & 255u);
+        atomicAdd(&s.bin[p / PLACES], (1u << POS_BITS) + p % PLACES);
+        ++binned;
       }
     });
+    binned = (unsigned)block_sum(binned, s);
+    if (threadIdx.x < C) cl.map_shared_rank(&s, threadIdx.x)->n_bin[me] = binned;
     cl.sync();
     const int per = NB / C;
     for (int i = threadIdx.x; i < per; i += THREADS) {
       const int b = me * per + i;
-      unsigned n = 0, p = 0;
-      for (int q = 0; q < C; ++q) {
-        const Shared* from = cl.map_shared_rank(&s, q);
-        n += from->cnt[b];
-        p += from->pos[b];
+      unsigned v[MAX_C], n = 0, p = 0;
+#pragma unroll
+      for (int q = 0; q < MAX_C; ++q) v[q] = q < C ? cl.map_shared_rank(&s, q)->bin[b] : 0u;
+#pragma unroll
+      for (int q = 0; q < MAX_C; ++q) {
+        n += v[q] >> POS_BITS;
+        p += v[q] & ((1u << POS_BITS) - 1u);
       }
-      for (int q = 0; q < C; ++q) {
-        Shared* to = cl.map_shared_rank(&s, q);
-        to->all.cnt[b] = n;
-        to->all.pos[b] = p;
-      }
+#pragma unroll
+      for (int q = 0; q < MAX_C; ++q)
+        if (q < C) {
+          Shared* to = cl.map_shared_rank(&s, q);
+          to->all.cnt[b] = n;
+          to->all.pos[b] = p;
+        }
     }
     cl.sync();
     // ---- the windows: the bin of the top_k border, those of the top_p border ----
     // A bin's sum of weights is estimated from its tokens' mean place: within
-    // (ln2 * width)^2 / 8 of it, width at most 41 / 2047, half a place's rounding and
-    // the f32 sums: 1e-4 covers them with room.
+    // (ln2 * width)^2 / 8 of it, width at most 41 / 2047, half a place's rounding
+    // (4.4e-4) and the f32 sums: SLACK covers them.
     constexpr int PER = NB / THREADS;
     unsigned n[PER], nt = 0;
-    float w[PER], wt = 0.f;
+    float w[PER], wa[PER], wt = 0.f;
     const float step = reach / (NB - 1);
     for (int j = 0; j < PER; ++j) {
       const int b = threadIdx.x * PER + j;
       n[j] = s.all.cnt[b];
-      w[j] = n[j] ? n[j] * exp2f(-step * (b + s.all.pos[b] / (256.0f * n[j]))) : 0.f;
+      w[j] = n[j] ? n[j] * exp2f(-step * (b + s.all.pos[b] / ((float)PLACES * n[j]))) : 0.f;
       nt += n[j];
       wt += w[j];
     }
@@ -347,6 +455,10 @@ __global__ void __launch_bounds__(THREADS) sample_kernel(const SampleArgs a) {
     u64 n_all;
     u64 nb = block_before((u64)nt, n_all, s);
     float wb = block_before(wt, w_all, s);
+    // a bin of more tokens than its word counts loses some: the row is done by halving then
+    unsigned expected = 0;
+    for (int q = 0; q < C; ++q) expected += s.n_bin[q];
+    const bool full = n_all != expected;
     int* mark = s.mark;
     if (threadIdx.x == 0) {
       mark[0] = NB;      // bin of the top_k border, NB: past the last
@@ -376,16 +488,28 @@ __global__ void __launch_bounds__(THREADS) sample_kernel(const SampleArgs a) {
     if (by_p) {
       const float z_hi = (s.est[0] + (bk < NB ? s.est[1] : 0.f)) * (1.0f + SLACK);
       const float z_lo = (s.est[0] + (bk < NB ? s.est[1] * exp2f(-step) : 0.f)) * (1.0f - SLACK);
-      float ww = wb;
-      const float p = fmaxf(tp, 0.f);
+      const float p = fmaxf(tp, 0.f), rest = 1.0f - p;
+      // The border lies in no bin before the first that may reach it, in none behind
+      // the first that must have.  With no top_k the sums from the end say it too, and
+      // nearer where top_p is close to 1.
+      float after = block_after(wt, s);
+      for (int j = PER - 1; j >= 0; --j) {
+        const float w_j = w[j];
+        w[j] = after;  // behind bin j
+        after += w_j;
+        wa[j] = w_j;
+      }
+      float upto = wb;
       for (int j = 0; j < PER; ++j) {
         const int b = threadIdx.x * PER + j;
-        const float upto = ww + w[j];
-        // the border lies in no bin before the first that may reach it, in none
-        // behind the first that must have reached it
-        if (n[j] && upto * (1.0f + SLACK) >= p * z_lo) atomicMin(mark + 2, b);
-        if (n[j] && upto * (1.0f - SLACK) >= p * z_hi) atomicMin(mark + 3, b);
-        ww = upto;
+        upto += wa[j];
+        bool may = upto * (1.0f + SLACK) >= p * z_lo, must = upto * (1.0f - SLACK) >= p * z_hi;
+        if (bk == NB) {
+          may = may && w[j] * (1.0f - SLACK) <= rest * z_hi;
+          must = must || w[j] * (1.0f + SLACK) <= rest * z_lo;
+        }
+        if (n[j] && may) atomicMin(mark + 2, b);
+        if (n[j] && must) atomicMin(mark + 3, b);
       }
       __syncthreads();
     }
@@ -394,21 +518,24 @@ __global__ void __launch_bounds__(THREADS) sample_kernel(const SampleArgs a) {
     __syncthreads();
     // ---- the sums beside the windows, the tokens in them ----
     u64 part = 0, kept = 0, mid = 0;
-    each(x, lo, hi, [&](float l, int i) {
-      const float d = bins.depth(l);
-      const int b = d < REACH ? (int)(bins.place(d) >> 8) : NB;
-      if (b > bk || b == NB) return;
-      if (b < safe) {
+    if (!full)
+      mine.again([&](float l, int i) {
+        const float d = bins.depth(l);
+        const int b = d < REACH ? (int)(bins.place(d) / PLACES) : NB;
+        if (b >= NB || b > bk) return;
+        if (b == bk || (b >= p_lo && b <= p_hi)) {
+          const unsigned at = atomicAdd(&s.listed, 1u);
+          if (at < CAP) s.list[at] = key_of(l, i);
+          return;
+        }
         const u64 e = weight_of(l, m, c, s.table);
-        kept += e;
-        part += e >= least ? e : 0ull;
-      } else if (b == bk || (b >= p_lo && b <= p_hi)) {
-        const unsigned at = atomicAdd(&s.listed, 1u);
-        if (at < CAP) s.list[at] = key_of(l, i);
-      } else {
-        mid += weight_of(l, m, c, s.table);
-      }
-    });
+        if (b < safe) {
+          kept += e;
+          part += e >= least ? e : 0ull;
+        } else {
+          mid += e;
+        }
+      });
     part = warp_sum(part);
     if (lane == 0) cl.map_shared_rank(&s, 0)->drawn[slot] = part;
     kept = block_sum(kept, s);
@@ -422,17 +549,19 @@ __global__ void __launch_bounds__(THREADS) sample_kernel(const SampleArgs a) {
     cl.sync();
     unsigned listed = 0;
     for (int q = 0; q < C; ++q) listed += s.n_list[q];
-    if (listed <= CAP) {
+    if (listed <= CAP && !full) {
       summed = true;
       if (me == 0) {
         kept = mid = 0;
-        unsigned done = 0;
         for (int q = 0; q < C; ++q) {
           kept += s.kept[q];
           mid += s.mid[q];
-          const Shared* from = cl.map_shared_rank(&s, q);
-          for (unsigned i = threadIdx.x; i < s.n_list[q]; i += THREADS) s.sorted[done + i] = from->list[i];
-          done += s.n_list[q];
+        }
+        for (unsigned i = threadIdx.x; i < listed; i += THREADS) {
+          unsigned j = i;
+          int q = 0;
+          while (j >= s.n_list[q]) j -= s.n_list[q++];
+          s.sorted[i] = cl.map_shared_rank(&s, q)->list[j];
         }
         unsigned pad = 32;
         while (pad < listed) pad *= 2;
@@ -451,40 +580,41 @@ __global__ void __launch_bounds__(THREADS) sample_kernel(const SampleArgs a) {
             __syncthreads();
           }
         // the border among them: of top_k the nk-th of its bin, of top_p the first whose sum reaches
-        constexpr int EACH = CAP / THREADS;
-        u64 e[EACH], sum = 0;
-        unsigned before_k = 0;  // of the listed, those before the top_k bin
-        for (int j = 0; j < EACH; ++j) {
-          const unsigned i = threadIdx.x * EACH + j;
-          e[j] = 0;
-          if (i >= listed) continue;
+        u64* weight = s.list;  // of the sorted keys (the block's own list is in sorted[] now)
+        u64 before_k = 0;      // of the keys, those before the top_k bin
+#pragma unroll 1
+        for (unsigned i = threadIdx.x; i < listed; i += THREADS) {
           const float l = value_of(s.sorted[i]);
-          e[j] = weight_of(l, m, c, s.table);
-          before_k += (int)(bins.place(bins.depth(l)) >> 8) < bk;
+          weight[i] = weight_of(l, m, c, s.table);
+          before_k += (int)(bins.place(bins.depth(l)) / PLACES) < bk;
         }
-        const unsigned stay = by_k && bk < NB ? (unsigned)block_sum(before_k, s) + nk : listed;
-        for (int j = 0; j < EACH; ++j) sum += threadIdx.x * EACH + j < stay ? e[j] : 0ull;
-        u64 all;
-        u64 run = block_before(sum, all, s);
-        const u64 z = kept + mid + all;
-        const double want = by_p ? ceil((double)tp * (double)z) : 0.0;
-        const u64 goal = want >= 1.0 ? (u64)want : 1ull;
+        const bool k_there = by_k && bk < NB;
+        const unsigned stay = k_there ? (unsigned)block_sum(before_k, s) + nk : listed;
         if (threadIdx.x == 0) s.last = stay ? s.sorted[stay - 1] : 0ull;
-        __syncthreads();
-        if (by_p)
-          for (int j = 0; j < EACH; ++j) {
-            const unsigned i = threadIdx.x * EACH + j;
-            if (i < stay && kept + run < goal && kept + run + e[j] >= goal) s.last = s.sorted[i];
-            run += e[j];
+        if (by_p) {
+          u64 sum = 0;
+          for (unsigned i = threadIdx.x; i < stay; i += THREADS) sum += weight[i];
+          const u64 z = kept + mid + block_sum(sum, s);
+          const double want = ceil((double)tp * (double)z);
+          const u64 goal = want >= 1.0 ? (u64)want : 1ull;
+          u64 run = kept;
+#pragma unroll 1
+          for (unsigned i0 = 0; i0 < stay && run < goal; i0 += THREADS) {
+            const unsigned i = i0 + threadIdx.x;
+            const u64 v = i < stay ? weight[i] : 0ull;
+            u64 all;
+            const u64 r = run + block_before(v, all, s);
+            if (r < goal && r + v >= goal) s.last = s.sorted[i];
+            run += all;
           }
-        __syncthreads();
-        // all bins behind the top_k border's that the list does not show
-        last = !by_p && !(by_k && bk < NB) ? ~0ull : s.last;
-        for (int j = 0; j < EACH; ++j) {
-          const unsigned i = threadIdx.x * EACH + j;
-          if (i < listed && s.sorted[i] <= last && e[j] >= least)
-            atomicAdd(&s.drawn[(unsigned)(s.sorted[i] & 0xFFFFFFFFu) / (unsigned)a.part], e[j]);
         }
+        __syncthreads();
+        // all keys where no border is in the bins
+        last = !by_p && !k_there ? ~0ull : s.last;
+#pragma unroll 1
+        for (unsigned i = threadIdx.x; i < listed; i += THREADS)
+          if (s.sorted[i] <= last && weight[i] >= least)
+            atomicAdd(&s.drawn[((unsigned)(s.sorted[i] & 0xFFFFFFFFu) + skew) / (unsigned)a.part], weight[i]);
         __syncthreads();
       }
     } else {
@@ -501,7 +631,7 @@ __global__ void __launch_bounds__(THREADS) sample_kernel(const SampleArgs a) {
       };
       auto upto = [&](u64 key, bool weigh) {
         u64 v = 0;
-        each(x, lo, hi, [&](float l, int i) {
+        mine.again([&](float l, int i) {
           if (l > -INFINITY && key_of(l, i) <= key) v += weigh ? weight_of(l, m, c, s.table) : 1ull;
         });
         return whole(v);
@@ -526,7 +656,7 @@ __global__ void __launch_bounds__(THREADS) sample_kernel(const SampleArgs a) {
   }
   if (!summed) {
     u64 part = 0;
-    each(x, lo, hi, [&](float l, int i) {
+    mine.again([&](float l, int i) {
       const u64 e = key_of(l, i) <= last ? weight_of(l, m, c, s.table) : 0ull;
       part += e >= least ? e : 0ull;
     });
@@ -569,33 +699,26 @@ __global__ void __launch_bounds__(THREADS) sample_kernel(const SampleArgs a) {
   }
   __syncthreads();
   const u64 goal = s.goal, total = s.kept[0];
-  const int begin = s.at * a.part, end = min(N, begin + a.part);
-  const int len = (end - begin + THREADS - 1) / THREADS;
-  u64 sum = 0;
-  auto weight_at = [&](int i, float& l) {
-    l = clean(__ldcg(x + i));
-    const u64 e = key_of(l, i) <= last ? weight_of(l, m, c, s.table) : 0ull;
-    return e >= least ? e : 0ull;
-  };
-  const int b0 = begin + threadIdx.x * len, b1 = min(end, b0 + len);
-  float l;
-  for (int i = b0; i < b1; ++i) sum += weight_at(i, l);
-  u64 all;
-  u64 run = block_before(sum, all, s);
-  if (run <= goal && run + sum > goal)
-    for (int i = b0; i < b1; ++i) {
-      const u64 e = weight_at(i, l);
-      if (run + e > goal) {
-        a.idx[row] = i;
-        if (a.prob) {
-          int n;
-          const u64 p = weight_parts(l, m, c, s.table, n);
-          a.prob[row] = (float)(scalbn((double)p, -n) / (double)total);
-        }
-        break;
+  const int begin = max(0, s.at * a.part - skew), end = min(N, (s.at + 1) * a.part - skew);
+  u64 run = 0;
+  for (int i0 = begin; i0 < end; i0 += THREADS) {
+    const int i = i0 + threadIdx.x;
+    const float l = i < end ? clean(__ldcg(x + i)) : -INFINITY;
+    u64 e = i < end && key_of(l, i) <= last ? weight_of(l, m, c, s.table) : 0ull;
+    e = e >= least ? e : 0ull;
+    u64 all;
+    const u64 r = run + block_before(e, all, s);
+    if (r <= goal && r + e > goal) {
+      a.idx[row] = i;
+      if (a.prob) {
+        int n;
+        const u64 p = weight_parts(l, m, c, s.table, n);
+        a.prob[row] = (float)(scalbn((double)p, -n) / (double)total);
       }
-      run += e;
     }
+    run += all;
+    if (run > goal) break;
+  }
 }
 
 }  // namespace
@@ -619,7 +742,8 @@ extern "C" lk_status lk_sample(const float* logits, int M, int N, const float* t
   if (!d || cudaGetDevice(&dev) != cudaSuccess) return LK_ERR_CUDA;
   static std::atomic<int> done[kMaxDevices];
   if (!done[dev].load(std::memory_order_acquire)) {
-    if (cudaFuncSetAttribute(sample_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(Shared)) !=
+    if (cudaFuncSetAttribute(sample_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             (int)(sizeof(Shared) + NW * kHeld * 4)) !=
         cudaSuccess)
       return LK_ERR_CUDA;
     carveout_max_shared(sample_kernel);
@@ -629,11 +753,13 @@ extern "C" lk_status lk_sample(const float* logits, int M, int N, const float* t
   int C = 1;
   while (C < MAX_C && M * C * 2 <= d->sm_count && N >= C * 4096) C *= 2;
   const int parts = C * NW;
-  const SampleArgs a = {logits, N, ((N + parts - 1) / parts + 31) & ~31, temperature, top_k, top_p, min_p, u, idx, prob};
+  const int part = ((N + 3 + parts - 1) / parts + 127) & ~127, held = part < kHeld ? part : kHeld;
+  const size_t smem = sizeof(Shared) + (size_t)NW * held * 4;
+  const SampleArgs a = {logits, N, part, held, temperature, top_k, top_p, min_p, u, idx, prob};
   cudaLaunchConfig_t lc = {};
   lc.gridDim = dim3(M * C);
   lc.blockDim = dim3(THREADS);
-  lc.dynamicSmemBytes = sizeof(Shared);
+  lc.dynamicSmemBytes = smem;
   lc.stream = stream;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
