@@ -125,12 +125,13 @@ struct SampleArgs {
   float* prob;
 };
 
-constexpr int NW = 16;             // warps of a block
+constexpr int NW = 32;             // warps of a block
 constexpr int THREADS = 32 * NW;
 constexpr int MAX_C = 8;           // blocks of a row at most
-constexpr int kHeld = 2048;        // tokens of a warp's part in shared memory at most
+constexpr int kHeld = 1024;        // tokens of a warp's part in shared memory at most
 constexpr int NB = 2048;           // bins of the order
 constexpr int CAP = 4096;          // tokens near the borders that are sorted
+constexpr int FEW = 128;           // of these, sorted by counting
 constexpr float REACH = 41.0f;     // log2 of the largest weight over the smallest that is not 0
 constexpr float SLACK = 6e-4f;     // of the bins' estimated sums
 constexpr int PLACES = 16;         // places in a bin
@@ -286,9 +287,9 @@ struct Part {
       }
     }
   }
-  // The same again, where the tokens are now.  The loop is rolled (f is some hundred
-  // instructions, and fetching code unrolled eight times took longer than the work),
-  // with the next two loads in flight.
+  // The same again, where the tokens are now: f(four logits, the first one's index).
+  // The loop is rolled (f is some hundred instructions: fetching more code takes longer
+  // than the work), with the next two loads in flight.
   template <typename F>
   __device__ __forceinline__ void again(F f) const {
     const int lane = threadIdx.x & 31;
@@ -301,10 +302,8 @@ struct Part {
 #pragma unroll 1
     for (; i - 4 * lane < hi; i += 128) {
       const float4 later = get(i + 256);
-      f(v.x, i);
-      f(v.y, i + 1);
-      f(v.z, i + 2);
-      f(v.w, i + 3);
+      const float l[4] = {v.x, v.y, v.z, v.w};
+      f(l, i);
       v = next;
       next = later;
     }
@@ -405,12 +404,15 @@ __global__ void __launch_bounds__(THREADS) sample_kernel(const SampleArgs a) {
     const float reach = fminf(REACH, __fmul_rn(__fsub_rn(m, low), c.hi));
     const Bins bins = {m, c.hi, fminf((float)PLACES * (NB - 1) / fmaxf(reach, 1e-30f), 1e30f)};
     unsigned binned = 0;
-    mine.again([&](float l, int) {
-      const float d = bins.depth(l);
-      if (d < REACH) {
+    mine.again([&](const float (&l)[4], int) {
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const float d = bins.depth(l[q]);
         const unsigned p = bins.place(d);
-        atomicAdd(&s.bin[p / PLACES], (1u << POS_BITS) + p % PLACES);
-        ++binned;
+        if (d < REACH) {
+          atomicAdd(&s.bin[p / PLACES], (1u << POS_BITS) + p % PLACES);
+          ++binned;
+        }
       }
     });
     binned = (unsigned)block_sum(binned, s);
@@ -519,22 +521,27 @@ __global__ void __launch_bounds__(THREADS) sample_kernel(const SampleArgs a) {
     // ---- the sums beside the windows, the tokens in them ----
     u64 part = 0, kept = 0, mid = 0;
     if (!full)
-      mine.again([&](float l, int i) {
-        const float d = bins.depth(l);
-        const int b = d < REACH ? (int)(bins.place(d) / PLACES) : NB;
-        if (b >= NB || b > bk) return;
-        if (b == bk || (b >= p_lo && b <= p_hi)) {
-          const unsigned at = atomicAdd(&s.listed, 1u);
-          if (at < CAP) s.list[at] = key_of(l, i);
-          return;
+      mine.again([&](const float (&l)[4], int i) {
+        // (without branches: the four tokens' chains of dependent steps interleave)
+        bool near[4], some = false;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const float d = bins.depth(l[q]);
+          const int b = d < REACH ? (int)(bins.place(d) / PLACES) : NB;
+          const u64 e = weight_of(l[q], m, c, s.table);
+          near[q] = b < NB && (b == bk || (b >= p_lo && b <= p_hi));
+          some = some || near[q];
+          kept += b < safe ? e : 0ull;
+          part += b < safe && e >= least ? e : 0ull;
+          mid += b >= safe && b < bk && !near[q] ? e : 0ull;
         }
-        const u64 e = weight_of(l, m, c, s.table);
-        if (b < safe) {
-          kept += e;
-          part += e >= least ? e : 0ull;
-        } else {
-          mid += e;
-        }
+        if (some)
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            if (near[q]) {
+              const unsigned at = atomicAdd(&s.listed, 1u);
+              if (at < CAP) s.list[at] = key_of(l[q], i + q);
+            }
       });
     part = warp_sum(part);
     if (lane == 0) cl.map_shared_rank(&s, 0)->drawn[slot] = part;
@@ -563,54 +570,79 @@ __global__ void __launch_bounds__(THREADS) sample_kernel(const SampleArgs a) {
           while (j >= s.n_list[q]) j -= s.n_list[q++];
           s.sorted[i] = cl.map_shared_rank(&s, q)->list[j];
         }
-        unsigned pad = 32;
-        while (pad < listed) pad *= 2;
-        for (unsigned i = listed + threadIdx.x; i < pad; i += THREADS) s.sorted[i] = ~0ull;
         __syncthreads();
-        for (unsigned k = 2; k <= pad; k *= 2)
-          for (unsigned j = k / 2; j > 0; j /= 2) {
-            for (unsigned i = threadIdx.x; i < pad / 2; i += THREADS) {
-              const unsigned p = 2 * i - (i & (j - 1)), q = p + j;
-              const u64 y = s.sorted[p], z = s.sorted[q];
-              if ((y > z) == !(p & k)) {
-                s.sorted[p] = z;
-                s.sorted[q] = y;
-              }
-            }
-            __syncthreads();
+        if (listed <= FEW) {
+          // a thread's key goes behind as many as are smaller (the keys are distinct)
+          u64 key = 0;
+          unsigned rank = 0;
+          if (threadIdx.x < listed) {
+            key = s.sorted[threadIdx.x];
+            for (unsigned i = 0; i < listed; ++i) rank += s.sorted[i] < key;
           }
+          __syncthreads();
+          if (threadIdx.x < listed) s.sorted[rank] = key;
+        } else {
+          unsigned pad = FEW;
+          while (pad < listed) pad *= 2;
+          for (unsigned i = listed + threadIdx.x; i < pad; i += THREADS) s.sorted[i] = ~0ull;
+          __syncthreads();
+          for (unsigned k = 2; k <= pad; k *= 2)
+            for (unsigned j = k / 2; j > 0; j /= 2) {
+              for (unsigned i = threadIdx.x; i < pad / 2; i += THREADS) {
+                const unsigned p = 2 * i - (i & (j - 1)), q = p + j;
+                const u64 y = s.sorted[p], z = s.sorted[q];
+                if ((y > z) == !(p & k)) {
+                  s.sorted[p] = z;
+                  s.sorted[q] = y;
+                }
+              }
+              __syncthreads();
+            }
+        }
+        __syncthreads();
         // the border among them: of top_k the nk-th of its bin, of top_p the first whose sum reaches
         u64* weight = s.list;  // of the sorted keys (the block's own list is in sorted[] now)
-        u64 before_k = 0;      // of the keys, those before the top_k bin
-#pragma unroll 1
-        for (unsigned i = threadIdx.x; i < listed; i += THREADS) {
-          const float l = value_of(s.sorted[i]);
-          weight[i] = weight_of(l, m, c, s.table);
-          before_k += (int)(bins.place(bins.depth(l)) / PLACES) < bk;
-        }
         const bool k_there = by_k && bk < NB;
-        const unsigned stay = k_there ? (unsigned)block_sum(before_k, s) + nk : listed;
-        if (threadIdx.x == 0) s.last = stay ? s.sorted[stay - 1] : 0ull;
-        if (by_p) {
-          u64 sum = 0;
-          for (unsigned i = threadIdx.x; i < stay; i += THREADS) sum += weight[i];
-          const u64 z = kept + mid + block_sum(sum, s);
-          const double want = ceil((double)tp * (double)z);
-          const u64 goal = want >= 1.0 ? (u64)want : 1ull;
-          u64 run = kept;
 #pragma unroll 1
-          for (unsigned i0 = 0; i0 < stay && run < goal; i0 += THREADS) {
-            const unsigned i = i0 + threadIdx.x;
-            const u64 v = i < stay ? weight[i] : 0ull;
-            u64 all;
-            const u64 r = run + block_before(v, all, s);
-            if (r < goal && r + v >= goal) s.last = s.sorted[i];
-            run += all;
+        for (unsigned i = threadIdx.x; i < listed; i += THREADS) weight[i] = weight_of(value_of(s.sorted[i]), m, c, s.table);
+        __syncthreads();
+        if (warp == 0) {
+          unsigned stay = listed;
+          if (k_there) {
+            unsigned before = 0;  // of the keys, those before the top_k bin
+            for (unsigned i = lane; i < listed; i += 32)
+              before += (int)(bins.place(bins.depth(value_of(s.sorted[i]))) / PLACES) < bk;
+            stay = __reduce_add_sync(FULL, before) + nk;
           }
+          u64 key = stay ? s.sorted[stay - 1] : 0ull;
+          if (by_p) {
+            u64 z = 0;
+            for (unsigned i = lane; i < stay; i += 32) z += weight[i];
+            z = warp_sum(z) + kept + mid;
+            const double want = ceil((double)tp * (double)z);
+            const u64 goal = want >= 1.0 ? (u64)want : 1ull;
+            u64 run = kept;
+            for (unsigned i0 = 0; i0 < stay; i0 += 32) {
+              u64 inc = i0 + lane < stay ? weight[i0 + lane] : 0ull;
+#pragma unroll
+              for (int o = 1; o < 32; o <<= 1) {
+                const u64 y = __shfl_up_sync(FULL, inc, o);
+                if (lane >= o) inc += y;
+              }
+              const unsigned there = __ballot_sync(FULL, run + inc >= goal);
+              if (there) {
+                const unsigned i = i0 + __ffs(there) - 1;
+                key = s.sorted[i < stay ? i : stay - 1];
+                break;
+              }
+              run += __shfl_sync(FULL, inc, 31);
+            }
+          }
+          // all keys where no border is in the bins
+          if (lane == 0) s.last = !by_p && !k_there ? ~0ull : key;
         }
         __syncthreads();
-        // all keys where no border is in the bins
-        last = !by_p && !k_there ? ~0ull : s.last;
+        last = s.last;
 #pragma unroll 1
         for (unsigned i = threadIdx.x; i < listed; i += THREADS)
           if (s.sorted[i] <= last && weight[i] >= least)
@@ -631,8 +663,10 @@ __global__ void __launch_bounds__(THREADS) sample_kernel(const SampleArgs a) {
       };
       auto upto = [&](u64 key, bool weigh) {
         u64 v = 0;
-        mine.again([&](float l, int i) {
-          if (l > -INFINITY && key_of(l, i) <= key) v += weigh ? weight_of(l, m, c, s.table) : 1ull;
+        mine.again([&](const float (&l)[4], int i) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            if (l[q] > -INFINITY && key_of(l[q], i + q) <= key) v += weigh ? weight_of(l[q], m, c, s.table) : 1ull;
         });
         return whole(v);
       };
@@ -656,9 +690,12 @@ __global__ void __launch_bounds__(THREADS) sample_kernel(const SampleArgs a) {
   }
   if (!summed) {
     u64 part = 0;
-    mine.again([&](float l, int i) {
-      const u64 e = key_of(l, i) <= last ? weight_of(l, m, c, s.table) : 0ull;
-      part += e >= least ? e : 0ull;
+    mine.again([&](const float (&l)[4], int i) {
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const u64 e = weight_of(l[q], m, c, s.table);
+        part += e >= least && key_of(l[q], i + q) <= last ? e : 0ull;
+      }
     });
     part = warp_sum(part);
     if (lane == 0) cl.map_shared_rank(&s, 0)->drawn[slot] = part;
