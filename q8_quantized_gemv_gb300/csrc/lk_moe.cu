@@ -15,71 +15,70 @@
 // of 32 it has whole, and a group that it has in part if it is the last of its
 // blocks to count in (cnt).
 //
-// Down: a quad is four output rows, which the warp takes through all the pairs
-// of the row of activations, one expert's four rows after the other's, and adds
-// them up in the order of the pairs: no partial results, no second launch.
-#include "lk_moe.h"
-#include "lk_ring_kernel.cuh"
-#include "lk_spans.h"
+// Down: a block has a range of output rows for all pairs of the row of activations,
+// a quad is four of them of one pair's expert.  The products stay in shared memory until
+// all are there, then are added in the order of the pairs: no second launch.
+#include "lk_moe.cuh"
 
 using namespace lk;
 using namespace lkh;
 using namespace lkring;
+using namespace lkmoe;
 
 namespace {
-
-constexpr int ERR_MOE_WAIT = 256;  // bit of the device error word
 
 constexpr int NW = 12;             // warps of a block
 constexpr int SLICE = 4096;        // bytes of K in a stage at most
 constexpr int DEPTH = 8;           // stages of a warp at most
 constexpr int kStatic = 2048;      // static shared memory, at most
-
-struct MoeArgs {
-  const int8_t* wa;            // gate, or down
-  const unsigned char* sa;     // f16 scales, as bytes
-  const int8_t* wb;            // up
-  const unsigned char* sb;
-  int E, rows, K;              // a matrix: [rows][K]
-  const float* x;              // activation rows: M (gate/up) or M * k (down)
-  const int8_t* xq;
-  const int8_t* xl;
-  const float* xs;
-  const int* ids;
-  const float* weights;
-  int k;
-  float* out;                  // h [M * k][rows], or y [M][rows]
-  int8_t* hq;
-  int8_t* hl;
-  float* hs;
-  int* cnt;
-  int tk, nsl;                 // bytes of K in a stage, stages of a row
-  int depth;
-  unsigned srow, s_off, stage_bytes, ring_off;
-  unsigned long long wait_ns;
-  int* err;
-};
+constexpr int kProducts = 16384;   // down: bytes of a block's products, about
 
 template <int Q>
 __host__ __device__ constexpr unsigned act_bytes(unsigned len) {
   return Q == 0 ? 4u * len : len * Q + len / 8u;
 }
 
-// The activation row `row` into `dst`: words, low words and scales, or f32 values.
+// The activation rows of a block in shared memory, one after the other: words, low
+// words and scales, or f32 values.  All threads load 16-byte runs; batch b is runs
+// [b, b + 1) * RUNS * blockDim.x, so that the first can be under way while the first weights are
+// asked for (behind those a load would wait for all of them).
 template <int Q>
-__device__ __forceinline__ void load_row(unsigned char* dst, const MoeArgs& a, long row) {
-  const int K = a.K;
-  auto copy = [&](const void* src, unsigned char* to, int bytes) {
-    for (int i = threadIdx.x * 16; i < bytes; i += blockDim.x * 16) *(uint4*)(to + i) = ld_cg16((const char*)src + i);
-  };
-  if constexpr (Q == 0) {
-    copy(a.x + row * K, dst, 4 * K);
-  } else {
-    copy(a.xq + row * K, dst, K);
-    if constexpr (Q == 2) copy(a.xl + row * K, dst + K, K);
-    copy(a.xs + row * (K >> 5), dst + K * Q, K >> 3);
+struct ActLoad {
+  static constexpr int RUNS = 4;
+  const MoeArgs& a;
+  const int* row_of;  // the rows' numbers
+  int rows, per;      // runs of a row
+  uint4 v[RUNS];
+  __device__ __forceinline__ ActLoad(const MoeArgs& args, const int* numbers, int n)
+      : a(args), row_of(numbers), rows(n), per((int)(act_bytes<Q>(args.K) / 16)) {}
+  __device__ __forceinline__ const void* source(int i) const {
+    const int r = i / per, c = i - r * per;
+    const long row = row_of[r];
+    if constexpr (Q == 0) {
+      return a.x + row * a.K + 4 * c;
+    } else {
+      const int w = a.K / 16;
+      if (c < w) return a.xq + row * a.K + 16 * c;
+      if (Q == 2 && c < 2 * w) return a.xl + row * a.K + 16 * (c - w);
+      return a.xs + row * (a.K >> 5) + 4 * (c - Q * w);
+    }
   }
-}
+  __device__ __forceinline__ void load(int b) {
+#pragma unroll
+    for (int u = 0; u < RUNS; ++u) {
+      const int i = (b * RUNS + u) * blockDim.x + threadIdx.x;
+      if (i < rows * per) v[u] = ld_cg16(source(i));
+    }
+  }
+  __device__ __forceinline__ void store(int b, unsigned char* act) {
+#pragma unroll
+    for (int u = 0; u < RUNS; ++u) {
+      const int i = (b * RUNS + u) * blockDim.x + threadIdx.x;
+      if (i < rows * per) *(uint4*)(act + 16 * (size_t)i) = v[u];
+    }
+  }
+  __device__ __forceinline__ bool more(int b) const { return b * RUNS * (int)blockDim.x < rows * per; }
+};
 
 // A stage's part of four rows against the activation at `act` (K its whole length).
 template <int Q>
@@ -151,13 +150,14 @@ template <int Q, bool GLU>
 __global__ void __launch_bounds__(NW * 32, 1) moe_kernel(const MoeArgs a) {
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ unsigned long long bars[NW * DEPTH];
-  __shared__ int pair_of[LK_MOE_MAX_K], expert_of[LK_MOE_MAX_K];
+  __shared__ int pair_of[LK_MOE_MAX_K], expert_of[LK_MOE_MAX_K], row_of[LK_MOE_MAX_K];
   __shared__ float weight_of[LK_MOE_MAX_K];
   __shared__ int n_pairs;
   __shared__ int aborted;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const long t = blockIdx.y;
   volatile int* abort_flag = &aborted;
+  float* products = (float*)(smem + a.s_products);  // down: [pair][this block's rows]
   unsigned char* ring = smem + a.ring_off + (size_t)warp * a.depth * a.stage_bytes;
   const unsigned full0 = smem_u32(bars + warp * DEPTH);
   if (lane == 0)
@@ -177,43 +177,45 @@ __global__ void __launch_bounds__(NW * 32, 1) moe_kernel(const MoeArgs a) {
       const int i = __popc(there & ((1u << lane) - 1u));
       pair_of[i] = lane;
       expert_of[i] = e;
+      row_of[i] = (int)(GLU ? t : t * a.k + lane);
       if (!GLU) weight_of[i] = __ldcg(a.weights + t * a.k + lane);
     }
     if (lane == 0) n_pairs = __popc(there);
   }
   __syncthreads();
   const int np = n_pairs;
-  if (GLU) {
-    if (np) load_row<Q>(smem, a, t);
-  } else {
-    for (int i = 0; i < np; ++i) load_row<Q>(smem + i * act_bytes<Q>(a.K), a, t * a.k + pair_of[i]);
-  }
+  ActLoad<Q> act(a, row_of, GLU ? np > 0 : np);
+  act.load(0);
 
-  // this block's quads: gate/up, of all pairs' outputs; down, of the rows
-  const int per = GLU ? a.rows / 2 : a.rows / 4;  // quads of a pair, of the output
-  const long quads = GLU ? (long)np * per : per;
-  const int q0 = (int)(quads * blockIdx.x / gridDim.x), q1 = (int)(quads * (blockIdx.x + 1) / gridDim.x);
-  // stages of a quad (a row without pairs has none)
-  const int spq = GLU ? a.nsl : np * a.nsl;
-
+  // this block's quads: gate/up, of all pairs' outputs; down, of its rows of all pairs
+  const int per = GLU ? a.rows / 2 : a.rows / 4;  // quads of a pair
+  const int quads = GLU ? np * per : per;
+  const int q0 = (int)((long)quads * blockIdx.x / gridDim.x), q1 = (int)((long)quads * (blockIdx.x + 1) / gridDim.x);
+  const int nq = q1 - q0, items = GLU ? nq : nq * np;
   struct Cursor {
-    int q, i, c;  // quad, pair (down), slice
+    int item, c;  // item, slice
   };
   auto next = [&](Cursor& s) {
     if (++s.c < a.nsl) return;
     s.c = 0;
-    if (!GLU && ++s.i < np) return;
-    s.i = 0;
-    s.q += NW;
+    s.item += NW;
+  };
+  // an item's pair (of those that are there) and its first output row
+  auto place = [&](int item, int& i, int& row) {
+    if (GLU) {
+      i = (q0 + item) / per;
+      row = 2 * (q0 + item - i * per);
+    } else {
+      i = item / nq;
+      row = 4 * (q0 + item - i * nq);
+    }
   };
   const int nb = a.K >> 5;
   // matrix row r of the quad: its row in the stack
   auto stack_row = [&](const Cursor& s, int r) -> long {
-    if (GLU) {
-      const int i = s.q / per, o = 2 * (s.q - i * per);
-      return (long)expert_of[i] * a.rows + o + (r & 1);
-    }
-    return (long)expert_of[s.i] * a.rows + 4 * s.q + r;
+    int i, row;
+    place(s.item, i, row);
+    return (long)expert_of[i] * a.rows + row + (GLU ? r & 1 : r);
   };
   auto issue = [&](const Cursor& s, int slot) {
     const int k0 = s.c * a.tk, len = a.K - k0 < a.tk ? a.K - k0 : a.tk;
@@ -235,15 +237,19 @@ __global__ void __launch_bounds__(NW * 32, 1) moe_kernel(const MoeArgs a) {
     __syncwarp();
   };
   typedef typename part_t<Q>::t P;
-  Cursor head{q0 + warp, 0, 0}, at = head;
-  const int total = q0 + warp < q1 ? ((q1 - 1 - q0 - warp) / NW + 1) * spq : 0;
+  Cursor head{warp, 0}, at = head;
+  const int total = warp < items ? ((items - 1 - warp) / NW + 1) * a.nsl : 0;
   int issued = 0;
   for (; issued < total && issued < a.depth; ++issued, next(head)) issue(head, issued);
-  __syncthreads();  // the activation
+  act.store(0, smem);
+  for (int b = 1; act.more(b); ++b) {
+    act.load(b);
+    act.store(b, smem);
+  }
+  __syncthreads();
 
   bool ok = true;
   P p = (P)0;
-  float y = 0.f;
   int n = 0, slot = 0;
   unsigned phase = 0;
   for (; n < total; ++n) {
@@ -258,7 +264,9 @@ __global__ void __launch_bounds__(NW * 32, 1) moe_kernel(const MoeArgs a) {
 #pragma unroll
     for (int r = 0; r < 2; ++r)
       sh[r] = (unsigned)((((unsigned long long)stack_row(at, r) * nb + (k0 >> 5)) * 2) & 15);
-    quad_stage<Q>(p, st, a, k0, len, sh, smem + (GLU ? 0 : at.i * act_bytes<Q>(a.K)), lane);
+    int i, row;
+    place(at.item, i, row);
+    quad_stage<Q>(p, st, a, k0, len, sh, smem + (GLU ? 0 : i * act_bytes<Q>(a.K)), lane);
     __syncwarp();
     if (issued < total) {
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -271,14 +279,9 @@ __global__ void __launch_bounds__(NW * 32, 1) moe_kernel(const MoeArgs a) {
       p = (P)0;
       if (GLU) {
         const float u = __shfl_down_sync(FULL, v, 16);
-        const int i = at.q / per, o = 2 * (at.q - i * per) + (lane >> 3);
-        if (lane == 0 || lane == 8) a.out[(t * a.k + pair_of[i]) * a.rows + o] = swiglu(v, u);
-      } else {
-        y = __fmaf_rn(weight_of[at.i], v, y);
-        if (at.i == np - 1) {
-          if ((lane & 7) == 0) a.out[t * a.rows + 4 * at.q + (lane >> 3)] = y;
-          y = 0.f;
-        }
+        if (lane == 0 || lane == 8) a.out[(t * a.k + pair_of[i]) * a.rows + row + (lane >> 3)] = swiglu(v, u);
+      } else if ((lane & 7) == 0) {
+        products[4 * at.item + (lane >> 3)] = v;
       }
     }
     next(at);
@@ -295,8 +298,14 @@ __global__ void __launch_bounds__(NW * 32, 1) moe_kernel(const MoeArgs a) {
       phase ^= 1u;
     }
   }
-  if (!GLU && np == 0)
-    for (int o = 4 * q0 + threadIdx.x; o < 4 * q1; o += blockDim.x) a.out[t * a.rows + o] = 0.f;
+  if constexpr (!GLU) {
+    __syncthreads();
+    for (int r = threadIdx.x; r < 4 * nq; r += blockDim.x) {
+      float y = 0.f;
+      for (int i = 0; i < np; ++i) y = __fmaf_rn(weight_of[i], products[4 * nq * i + r], y);
+      a.out[t * a.rows + 4 * q0 + r] = y;
+    }
+  }
   if constexpr (GLU && Q > 0) {
     if (!a.hq) return;
     __threadfence();  // this block's h before its counts
@@ -326,10 +335,11 @@ __global__ void __launch_bounds__(NW * 32, 1) moe_kernel(const MoeArgs a) {
 // Stages: rows in equal slices of at most SLICE bytes, a multiple of 128, and as
 // many stages a warp as fit; more, shorter slices only where clearly more bytes
 // are in flight with them.
-bool fit(MoeArgs& a, int mode, int rows_held, int smem_optin, int* smem) {
+bool fit(MoeArgs& a, int mode, int rows_held, int products, int smem_optin, int* smem) {
   const unsigned act = mode == 0 ? 4u * a.K : (unsigned)a.K * mode + a.K / 8u;
   if ((unsigned long long)act * rows_held > 200000u) return false;
-  a.ring_off = (act * rows_held + 127u) & ~127u;
+  a.s_products = act * rows_held;  // (a multiple of 16)
+  a.ring_off = (a.s_products + 4u * products + 127u) & ~127u;
   const int room = smem_optin - kStatic - (int)a.ring_off;
   int best = 0;
   for (int n = (a.K + SLICE - 1) / SLICE; n <= a.K / 128; ++n) {
@@ -354,38 +364,28 @@ bool fit(MoeArgs& a, int mode, int rows_held, int smem_optin, int* smem) {
 template <int Q, bool GLU>
 lk_status run(const MoeArgs& a, dim3 grid, int smem, int optin, int pdl, cudaStream_t stream) {
   static std::atomic<int> done[kMaxDevices];
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return LK_ERR_CUDA;
-  if (!done[dev].load(std::memory_order_acquire)) {
-    if (cudaFuncSetAttribute(moe_kernel<Q, GLU>, cudaFuncAttributeMaxDynamicSharedMemorySize, optin - kStatic) !=
-        cudaSuccess)
-      return LK_ERR_CUDA;
-    carveout_max_shared(moe_kernel<Q, GLU>);
-    done[dev].store(1, std::memory_order_release);
-  }
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(NW * 32);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = pdl ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, moe_kernel<Q, GLU>, a) == cudaSuccess ? LK_OK : LK_ERR_CUDA;
+  return launch_moe_kernel(moe_kernel<Q, GLU>, done, grid, NW * 32, smem, optin - kStatic, pdl, stream, a);
 }
 
 template <bool GLU>
 lk_status launch_moe(MoeArgs& a, int mode, int M, int held, const lk_launch_cfg* cfg, cudaStream_t stream) {
   const DeviceInfo* d = device_info(nullptr);
   if (!d) return LK_ERR_CUDA;
-  int smem = 0;
-  if (!fit(a, mode, held, d->smem_optin, &smem)) return LK_ERR_SHAPE;
   a.wait_ns = opt_wait_us > 0 ? (unsigned long long)opt_wait_us * 1000ull : 2000000000ull;
   a.err = error_word_ptr();
   if (!a.err) return LK_ERR_CUDA;
-  const dim3 grid(M < d->sm_count ? (d->sm_count + M - 1) / M : 1, M);
+  if (mode != 0 && M > 1) return moe_rows(a, GLU, mode, M, cfg_pdl(cfg), stream);
+  int smem = 0;
+  // blocks of a row of activations; down: enough that a block's products are few
+  int gx = (d->sm_count + M - 1) / M;
+  if (!GLU) {
+    const int least = (int)(((long)a.k * a.rows * 4 + kProducts - 1) / kProducts);
+    if (gx < least) gx = least;
+    if (gx > a.rows / 4) gx = a.rows / 4;
+  }
+  const int products = GLU ? 0 : a.k * 4 * ((a.rows / 4 + gx - 1) / gx);
+  if (!fit(a, mode, held, products, d->smem_optin, &smem)) return LK_ERR_SHAPE;
+  const dim3 grid(gx, M);
   const int pdl = cfg_pdl(cfg);
   return mode == 0   ? run<0, GLU>(a, grid, smem, d->smem_optin, pdl, stream)
          : mode == 1 ? run<1, GLU>(a, grid, smem, d->smem_optin, pdl, stream)

@@ -1,0 +1,447 @@
+// The experts' products for several rows in the quantized modes (include/lk_moe.h),
+// on the tensor cores.
+//
+// Rows that chose the same expert share the read of its weights.  Every block
+// sorts the pairs by expert (the same sort in all of them: it takes about a
+// microsecond, nothing is handed on) into bundles of one expert's up to 8
+// pairs, and takes its share of all bundles' weight rows in order, so an expert's
+// weights come from HBM once (more than 8 pairs: again from L2).  A tile is 16 weight
+// rows x 8 pairs; a warp streams its tiles through its own shared-memory stage
+// (bulk copies of the 16 rows, their scales, and of the bundle's activation rows,
+// all of one slice of K), each row 16 bytes longer than its slice, which keeps
+// ldmatrix's eight rows in different banks.  A 32-block is one mma m16n8k32 of int8
+// levels with the exact dots as result, combined in f32 as every other kernel
+// of the library does (partial b mod 4 ascending, (p0 + p2) + (p1 + p3)):
+// the products have lk_gemv_q8's bits.
+//
+// Gate/up: a tile is 8 gate rows over the 8 up rows of the same outputs, so a lane has
+// both values of an output.  Words: groups of 32 outputs, finished by the block that
+// has them whole, or by the last of its blocks to count in.
+//
+// Down: a block has a range of output rows and streams it from every expert;
+// its products stay in shared memory until all of a row's pairs are there, then
+// are added in the order of the pairs.
+//
+// Bound: HBM for few pairs an expert.  The int8 MMA takes 16 cycles of an SM's
+// tensor pipe, 70 % of it at the copy bandwidth under Int8Act (TwoPass: 140 %).
+#include "lk_moe.cuh"
+
+using namespace lk;
+using namespace lkh;
+using namespace lkring;
+
+namespace lkmoe {
+
+namespace {
+
+constexpr int TR = 16;        // weight rows of a tile
+constexpr int TP = 8;         // pairs of a bundle
+constexpr int NW = 8;         // warps of a block
+constexpr int DEPTH = 2;      // stages of a warp at most
+constexpr int STATIC = 1024;  // static shared memory, at most
+constexpr int ROOM_D = 65536; // bytes of products that a block keeps, about
+
+struct RowsArgs {
+  MoeArgs a;
+  int M, P;                        // rows, pairs M * k
+  unsigned rs, srs, ars, xsr;      // stage: bytes of a level, scale, activation and activation-scale row
+  unsigned s_off, x_off, xl_off, xs_off;
+  unsigned o_ids, o_rank, o_order, o_cnt, o_off, o_bundle, o_d, o_ring;  // offsets in shared memory
+  int rows_d;                      // down: output rows of a pass
+};
+
+__device__ __forceinline__ void ldmatrix4(unsigned (&r)[4], unsigned addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+// d = A (16 x 32) * B (32 x 8) + 0x4B400000: as a float, 1.5 * 2^23 + the dot (|dot| < 2^20)
+__device__ __forceinline__ void dot_bits(int (&d)[4], const unsigned (&w)[4], unsigned b0, unsigned b1) {
+  constexpr int base = 0x4B400000;
+  asm("mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+      : "=r"(d[0]), "=r"(d[1]), "=r"(d[2]), "=r"(d[3])
+      : "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(b0), "r"(b1), "r"(base));
+}
+__device__ __forceinline__ float dot_of(int bits) { return __fadd_rn(__int_as_float(bits), -12582912.0f); }
+
+// A bundle: expert, its first place in the sorted pairs, pairs.
+__device__ __forceinline__ unsigned bundle_of(int e, int start, int n) {
+  return (unsigned)e | (unsigned)start << 10 | (unsigned)(n - 1) << 21;
+}
+
+template <int Q, bool GLU>
+__global__ void __launch_bounds__(NW * 32, 1) moe_rows_kernel(const RowsArgs ra) {
+  extern __shared__ __align__(128) unsigned char smem[];
+  __shared__ unsigned long long bars[NW * DEPTH];
+  __shared__ int totals[2][NW];
+  __shared__ int aborted, n_bundles;
+  const MoeArgs& a = ra.a;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int g = lane >> 2, t4 = lane & 3;
+  volatile int* abort_flag = &aborted;
+  short* ids = (short*)(smem + ra.o_ids);
+  unsigned short* rank = (unsigned short*)(smem + ra.o_rank);
+  unsigned short* order = (unsigned short*)(smem + ra.o_order);
+  unsigned short* cnt = (unsigned short*)(smem + ra.o_cnt);
+  unsigned short* off = (unsigned short*)(smem + ra.o_off);  // first place, first bundle of an expert
+  unsigned* bundle = (unsigned*)(smem + ra.o_bundle);
+  float* dd = (float*)(smem + ra.o_d);
+  unsigned char* ring = smem + ra.o_ring + (size_t)warp * a.depth * a.stage_bytes;
+  const unsigned full0 = smem_u32(bars + warp * DEPTH);
+  if (lane == 0)
+    for (int s = 0; s < a.depth; ++s) mbar_init(full0 + 8 * s, 1);
+  for (int e = threadIdx.x; e < a.E; e += blockDim.x) cnt[e] = 0;
+  if (threadIdx.x == 0) {
+    aborted = 0;
+    asm volatile("griddepcontrol.launch_dependents;" :::);
+  }
+  asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  griddep_wait();
+  for (int p = threadIdx.x; p < ra.P; p += blockDim.x) {
+    const int e = __ldcg(a.ids + p);
+    ids[p] = (unsigned)e < (unsigned)a.E ? (short)e : (short)-1;
+  }
+  __syncthreads();
+
+  // ---- the pairs by expert: how many of its expert come before each (one warp) ----
+  if (warp == 0) {
+    for (int p0 = 0; p0 < ra.P; p0 += 32) {
+      const int e = p0 + lane < ra.P ? ids[p0 + lane] : -1;
+      const unsigned same = __match_any_sync(FULL, e);
+      const int before = __popc(same & ((1u << lane) - 1u));
+      int base = 0;
+      if (e >= 0) {
+        base = cnt[e];
+        rank[p0 + lane] = (unsigned short)(base + before);
+      }
+      __syncwarp();
+      if (e >= 0 && before == 0) cnt[e] = (unsigned short)(base + __popc(same));
+      __syncwarp();
+    }
+  }
+  __syncthreads();
+  // first places and bundles: sums over the experts before (a thread has neighbours)
+  {
+    const int per = (a.E + NW * 32 - 1) / (NW * 32), e0 = min(a.E, (int)threadIdx.x * per), e1 = min(a.E, e0 + per);
+    int n = 0, b = 0;
+    for (int e = e0; e < e1; ++e) {
+      n += cnt[e];
+      b += (cnt[e] + TP - 1) / TP;
+    }
+    int in = n, ib = b;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int yn = __shfl_up_sync(FULL, in, o), yb = __shfl_up_sync(FULL, ib, o);
+      if (lane >= o) {
+        in += yn;
+        ib += yb;
+      }
+    }
+    if (lane == 31) {
+      totals[0][warp] = in;
+      totals[1][warp] = ib;
+    }
+    __syncthreads();
+    int bn = in - n, bb = ib - b;
+    for (int w = 0; w < NW; ++w) {
+      if (w < warp) {
+        bn += totals[0][w];
+        bb += totals[1][w];
+      }
+      if (threadIdx.x == 0) n_bundles = (w ? n_bundles : 0) + totals[1][w];
+    }
+    for (int e = e0; e < e1; ++e) {
+      off[e] = (unsigned short)bn;
+      for (int i = 0; i < cnt[e]; i += TP) bundle[bb++] = bundle_of(e, bn + i, min(TP, cnt[e] - i));
+      bn += cnt[e];
+    }
+  }
+  __syncthreads();
+  for (int p = threadIdx.x; p < ra.P; p += blockDim.x)
+    if (ids[p] >= 0) order[off[ids[p]] + rank[p]] = (unsigned short)p;
+  __syncthreads();
+  const int nbu = n_bundles;
+
+  const int nb = a.K >> 5, odd = (nb >> 2) & 1;
+  const int G = gridDim.x;
+  // this block's output rows (down), in passes; its tiles (gate/up)
+  const int per = a.rows / 8;  // gate/up: tiles of a bundle
+  const int r_lo = GLU ? 0 : (int)((long)a.rows * blockIdx.x / G), r_hi = GLU ? 0 : (int)((long)a.rows * (blockIdx.x + 1) / G);
+  const int t_lo = GLU ? (int)((long)nbu * per * blockIdx.x / G) : 0;
+  const int t_hi = GLU ? (int)((long)nbu * per * (blockIdx.x + 1) / G) : 0;
+  // element q of a lane: weight rows g, g + 8 x pairs 2 t4, 2 t4 + 1
+  const unsigned a_row = (lane & 15) * ra.rs + (lane >> 4) * 16;
+  const unsigned b_row = (lane & 7) * ra.ars + (lane >> 3) * 16;
+  int slot = 0;
+  unsigned phase = 0;
+  bool ok = true;
+
+  for (int r0 = r_lo; GLU ? r0 == 0 : r0 < r_hi; r0 += GLU ? 1 : ra.rows_d) {
+    const int rn = GLU ? 0 : min(ra.rows_d, r_hi - r0);  // down: rows of this pass
+    const int rt = GLU ? per : (rn + TR - 1) / TR;
+    const int lo = GLU ? t_lo : 0, hi = GLU ? t_hi : nbu * rt;
+    struct Cursor {
+      int tile, c;
+    };
+    auto next = [&](Cursor& s) {
+      if (++s.c == a.nsl) {
+        s.c = 0;
+        s.tile += NW;
+      }
+    };
+    auto issue = [&](const Cursor& s, int to) {
+      const int v = s.tile / rt, w = s.tile - v * rt;
+      const unsigned bu = bundle[v];
+      const int e = bu & 1023, start = (bu >> 10) & 2047, n = (int)(bu >> 21) + 1;
+      const int k0 = s.c * a.tk, len = a.K - k0 < a.tk ? a.K - k0 : a.tk;
+      const unsigned bar = full0 + 8 * to;
+      unsigned char* st = ring + (size_t)to * a.stage_bytes;
+      const int i = lane & 15;
+      const int rows = GLU ? TR : min(TR, rn - TR * w);
+      const long row = (long)e * a.rows + (GLU ? 8 * w + (i & 7) : r0 + TR * w + i);
+      const bool up = GLU && i >= 8;
+      const unsigned long long o = ((unsigned long long)row * nb + (k0 >> 5)) * 2;
+      const unsigned slen = ((unsigned)len / 16 + (unsigned)(o & 15) + 15u) & ~15u;
+      unsigned mine = i < rows ? (lane < 16 ? (unsigned)len : slen) : 0u;
+      if (lane < n) mine += (unsigned)len * Q + (unsigned)len / 8;
+      mine = __reduce_add_sync(FULL, mine);
+      if (lane == 0) mbar_arrive_expect_tx(bar, mine);
+      __syncwarp();
+      if (i < rows) {
+        if (lane < 16) bulk_g2s_nohint(st + i * ra.rs, (up ? a.wb : a.wa) + row * a.K + k0, len, bar);
+        else bulk_g2s_nohint(st + ra.s_off + i * ra.srs, (up ? a.sb : a.sa) + (o & ~15ull), slen, bar);
+      }
+      const int x = lane & 7;
+      if (x < n) {
+        const int p = order[start + x];
+        const long xr = GLU ? p / a.k : p;
+        if (lane < 8) bulk_g2s_nohint(st + ra.x_off + x * ra.ars, a.xq + xr * a.K + k0, len, bar);
+        else if (lane < 16) bulk_g2s_nohint(st + ra.xs_off + x * ra.xsr, a.xs + xr * nb + (k0 >> 5), len / 8, bar);
+        else if (Q == 2 && lane < 24) bulk_g2s_nohint(st + ra.xl_off + x * ra.ars, a.xl + xr * a.K + k0, len, bar);
+      }
+      __syncwarp();
+    };
+    Cursor head{lo + warp, 0}, at = head;
+    const int total = ok && lo + warp < hi ? ((hi - 1 - lo - warp) / NW + 1) * a.nsl : 0;
+    int issued = 0;
+    for (int s = slot; issued < total && issued < a.depth; ++issued, next(head)) {
+      issue(head, s);
+      if (++s == a.depth) s = 0;
+    }
+    float p[4][4];  // [partial][element]
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) p[q][e] = 0.f;
+    int n = 0;
+    for (; ok && n < total; ++n) {
+      if (!__all_sync(FULL, mbar_wait(full0 + 8 * slot, phase, a.wait_ns, abort_flag))) {
+        if (lane == 0) raise_error(a.err, ERR_MOE_WAIT, abort_flag);
+        ok = false;
+        break;
+      }
+      const int k0 = at.c * a.tk, len = a.K - k0 < a.tk ? a.K - k0 : a.tk;
+      unsigned char* st = ring + (size_t)slot * a.stage_bytes;
+      const unsigned W = smem_u32(st) + a_row, X = smem_u32(st + ra.x_off) + b_row;
+      const unsigned L = smem_u32(st + ra.xl_off) + b_row;
+      const int v = at.tile / rt, w = at.tile - v * rt;
+      // rows of a stack alternate between 0 and 8 bytes into 16 where K / 128 is odd
+      const int par = GLU ? g & 1 : (r0 + g) & 1;
+      const unsigned char* S = st + ra.s_off + g * ra.srs + ((par & odd) << 3);
+      const unsigned char* XS = st + ra.xs_off + 2 * t4 * ra.xsr;
+      const int groups = len >> 7;
+#pragma unroll 2
+      for (int gi = 0; gi < groups; ++gi) {
+        int d[4][4], f[4][4];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          unsigned xh[4], xl[4], w0[4], w1[4];
+          ldmatrix4(w0, W + 128 * gi + 64 * h);
+          ldmatrix4(w1, W + 128 * gi + 64 * h + 32);
+          ldmatrix4(xh, X + 128 * gi + 64 * h);
+          dot_bits(d[2 * h], w0, xh[0], xh[1]);
+          dot_bits(d[2 * h + 1], w1, xh[2], xh[3]);
+          if constexpr (Q == 2) {
+            ldmatrix4(xl, L + 128 * gi + 64 * h);
+            dot_bits(f[2 * h], w0, xl[0], xl[1]);
+            dot_bits(f[2 * h + 1], w1, xl[2], xl[3]);
+          }
+        }
+        const uint2 s0 = *(const uint2*)(S + 8 * gi), s8 = *(const uint2*)(S + 8 * ra.srs + 8 * gi);
+        const float4 x0 = *(const float4*)(XS + 16 * gi), x1 = *(const float4*)(XS + ra.xsr + 16 * gi);
+        const float2 wa0 = __half22float2(*(const __half2*)&s0.x), wa1 = __half22float2(*(const __half2*)&s0.y);
+        const float2 wb0 = __half22float2(*(const __half2*)&s8.x), wb1 = __half22float2(*(const __half2*)&s8.y);
+        const float ws[2][4] = {{wa0.x, wa0.y, wa1.x, wa1.y}, {wb0.x, wb0.y, wb1.x, wb1.y}};
+        const float xs[2][4] = {{x0.x, x0.y, x0.z, x0.w}, {x1.x, x1.y, x1.z, x1.w}};
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float sw = ws[e >> 1][q], sx = xs[e & 1][q], dot = dot_of(d[q][e]);
+            if constexpr (Q == 1) {
+              p[q][e] = __fmaf_rn(__fmul_rn(sw, sx), dot, p[q][e]);
+            } else {
+              const float u = __fmaf_rn(sx, dot, __fmul_rn(__fmul_rn(sx, 0.0078125f), dot_of(f[q][e])));
+              p[q][e] = __fmaf_rn(sw, u, p[q][e]);
+            }
+          }
+      }
+      __syncwarp();
+      if (issued < total) {
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        issue(head, slot);
+        next(head);
+        ++issued;
+      }
+      if (at.c == a.nsl - 1) {
+        const unsigned bu = bundle[v];
+        const int start = (bu >> 10) & 2047, np = (int)(bu >> 21) + 1;
+        float y[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          y[e] = __fadd_rn(__fadd_rn(p[0][e], p[2][e]), __fadd_rn(p[1][e], p[3][e]));
+#pragma unroll
+          for (int q = 0; q < 4; ++q) p[q][e] = 0.f;
+        }
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          if (2 * t4 + c >= np) continue;
+          const long pair = order[start + 2 * t4 + c];
+          if (GLU) {
+            a.out[pair * a.rows + 8 * w + g] = swiglu(y[c], y[2 + c]);
+          } else {
+            float* to = dd + pair * ra.rows_d + TR * w + g;
+            if (TR * w + g < rn) to[0] = y[c];
+            if (TR * w + g + 8 < rn) to[8] = y[2 + c];
+          }
+        }
+      }
+      next(at);
+      if (++slot == a.depth) {
+        slot = 0;
+        phase ^= 1u;
+      }
+    }
+    // copies in flight land before the block may end
+    for (int m = n; m < issued; ++m) {
+      if (lane == 0) drain_wait(full0 + 8 * slot, phase, a.wait_ns, a.err);
+      __syncwarp();
+      if (++slot == a.depth) {
+        slot = 0;
+        phase ^= 1u;
+      }
+    }
+    if constexpr (!GLU) {
+      __syncthreads();
+      for (int i = threadIdx.x; i < ra.M * rn; i += blockDim.x) {
+        const int t = i / rn, r = i - t * rn;
+        float y = 0.f;
+        for (int j = 0; j < a.k; ++j) {
+          const int pr = t * a.k + j;
+          if (ids[pr] >= 0) y = __fmaf_rn(__ldcg(a.weights + pr), dd[(size_t)pr * ra.rows_d + r], y);
+        }
+        a.out[(long)t * a.rows + r0 + r] = y;
+      }
+      __syncthreads();
+    }
+  }
+  if constexpr (GLU) {
+    if (!a.hq) return;
+    __threadfence();  // this block's h before its counts
+    __syncthreads();
+    if (*abort_flag || t_hi <= t_lo) return;
+    const int groups = a.rows / 32;  // of a pair
+    for (int x = t_lo / 4 + warp; x <= (t_hi - 1) / 4; x += NW) {
+      const int lo = t_lo > 4 * x ? t_lo : 4 * x, hi = t_hi < 4 * x + 4 ? t_hi : 4 * x + 4;
+      if (hi - lo < 4) {
+        int old = 0;
+        if (lane == 0) old = atomicAdd(a.cnt + x, hi - lo);
+        old = __shfl_sync(FULL, old, 0);
+        if (old + hi - lo != 4) continue;  // another block finishes it
+        if (lane == 0) a.cnt[x] = 0;
+        __threadfence();  // the others' h after their counts
+      }
+      const int v = x / groups, gi = x - v * groups;
+      const unsigned bu = bundle[v];
+      const int start = (bu >> 10) & 2047, np = (int)(bu >> 21) + 1;
+      for (int c = 0; c < np; ++c) {
+        const long pair = order[start + c];
+        quant_lane<Q>(__ldcg(a.out + pair * a.rows + 32 * gi + lane), a.hq + pair * a.rows,
+                      Q == 2 ? a.hl + pair * a.rows : nullptr, a.hs + pair * (a.rows >> 5), gi, lane);
+      }
+    }
+  }
+}
+
+unsigned up16(unsigned n) { return (n + 15u) & ~15u; }
+
+// The layout of shared memory; false where it does not fit.
+bool fit_rows(RowsArgs& r, int Q, bool glu, int blocks, int smem_optin, int* smem) {
+  MoeArgs& a = r.a;
+  unsigned o = 0;
+  auto take = [&](unsigned bytes) {
+    const unsigned at = o;
+    o = up16(o + bytes);
+    return at;
+  };
+  r.o_ids = take(2u * r.P);
+  r.o_rank = take(2u * r.P);
+  r.o_order = take(2u * r.P);
+  r.o_cnt = take(2u * a.E);
+  r.o_off = take(2u * a.E);
+  r.o_bundle = take(4u * r.P);
+  r.rows_d = 0;
+  if (!glu) {
+    // rows of a pass: all of a block's where they fit, else a multiple of a tile's
+    const int rows = (a.rows + blocks - 1) / blocks;
+    const int most = ROOM_D / (4 * r.P);  // at least 8
+    r.rows_d = rows <= most ? rows : most < TR ? most : most / TR * TR;
+  }
+  r.o_d = take(4u * r.P * r.rows_d);
+  r.o_ring = (o + 127u) & ~127u;
+  const int room = smem_optin - STATIC - (int)r.o_ring;
+  for (int tk = 1024; tk >= 256; tk /= 2) {  // (slices begin at 8 scales' multiples)
+    a.tk = tk < a.K ? tk : a.K;
+    a.nsl = (a.K + a.tk - 1) / a.tk;
+    r.rs = a.tk + 16u;
+    r.srs = up16(a.tk / 16u + 8u);
+    r.ars = a.tk + 16u;
+    r.xsr = a.tk / 8u + 16u;
+    r.s_off = TR * r.rs;
+    r.x_off = r.s_off + TR * r.srs;
+    r.xl_off = r.x_off + TP * r.ars;
+    r.xs_off = r.x_off + Q * TP * r.ars;
+    a.stage_bytes = (r.xs_off + TP * r.xsr + 127u) & ~127u;
+    a.depth = room / (int)(NW * a.stage_bytes);
+    if (a.depth > DEPTH) a.depth = DEPTH;
+    if (a.depth >= 1) break;
+  }
+  if (a.depth < 1) return false;
+  *smem = (int)r.o_ring + NW * a.depth * (int)a.stage_bytes;
+  return true;
+}
+
+template <int Q, bool GLU>
+lk_status run(RowsArgs& r, const DeviceInfo* d, int pdl, cudaStream_t stream) {
+  static std::atomic<int> done[kMaxDevices];
+  int smem = 0;
+  if (!fit_rows(r, Q, GLU, d->sm_count, d->smem_optin, &smem)) return LK_ERR_SHAPE;
+  return launch_moe_kernel(moe_rows_kernel<Q, GLU>, done, dim3(d->sm_count), NW * 32, smem, d->smem_optin - STATIC, pdl,
+                           stream, r);
+}
+
+}  // namespace
+
+lk_status moe_rows(const MoeArgs& a, bool glu, int mode, int M, int pdl, cudaStream_t stream) {
+  const DeviceInfo* d = device_info(nullptr);
+  if (!d) return LK_ERR_CUDA;
+  RowsArgs r = {};
+  r.a = a;
+  r.M = M;
+  r.P = M * a.k;
+  return glu ? (mode == 1 ? run<1, true>(r, d, pdl, stream) : run<2, true>(r, d, pdl, stream))
+             : (mode == 1 ? run<1, false>(r, d, pdl, stream) : run<2, false>(r, d, pdl, stream));
+}
+
+}  // namespace lkmoe
