@@ -33,9 +33,9 @@ extern "C" {
  *                (u >= 1: the last of them with e above 0)
  *   prob         optional f32 [M]: e_idx over that sum
  * A logit of NaN counts as -inf (never drawn), +inf as the largest f32; a row
- * without any other gets idx -1, prob 0.  The e are formed to 2^-32 relatively
+ * without any other gets idx -1, prob 0.  The e are formed to 2^-29 relatively
  * and summed as whole numbers of 2^-39: the result does not depend on any order, and
- * differs from the exact one only where u or top_p lies within about 2^-30 of a
+ * differs from the exact one only where u or top_p lies within about 2^-28 of a
  * border between tokens.
  *   u    f32 [M], >= 0 (below 0 or NaN: 0);  idx int32 [M]
  * What is written must not overlap what is read (LK_ERR_ARG).

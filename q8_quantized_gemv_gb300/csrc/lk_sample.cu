@@ -1,13 +1,13 @@
 // The next token from the logits (include/lk_sample.h): lk_sample.
 //
-// Weights.  e = exp((l - max) / T) as a whole number of 2^-39: the argument
-// (l - max) log2(e) / T as an unevaluated sum of two floats, its nearest
-// multiple of 1/256 taken out (k / 256), 2^(frac(k / 256)) from a table of 256
-// and the remaining factor, 1 + q with |q| < 2^-9.5, from a cubic in f32 (a
-// table-driven exponential after P. T. P. Tang, ACM TOMS 15(2), 1989): relative
-// error below 2^-32 where the weight is above 2^-8, else the last place.  Whole
-// numbers add to the same sum in any order, so nothing here depends on how a
-// row is split, and the largest weight is exactly 2^39.
+// Weights.  e = exp((l - max) / T) as a whole number of 2^-39: the nearest
+// multiple of 1/128 of l log2(e) / T is taken out of it (one fused multiply-add leaves the
+// rest, below 1/256, to 2^-33), 2^(frac) comes from a table of 128, and the remaining
+// factor, 1 + q with |q| < 2^-7.5, from a cubic in f32 (a table-driven exponential
+// after P. T. P. Tang, ACM TOMS 15(2), 1989): relative error below 2^-29, or
+// half a 2^-39.  Whole numbers add to the same sum in any order, so nothing here
+// depends on how a row is split, and the largest weight is exactly 2^39.  Each lane
+// has a copy of the table in its own bank.
 //
 // The order of tokens (the largest logit first, equal ones by index) is that of
 // the 64-bit keys (complement of the logit's order-preserving bits, index);
@@ -30,69 +30,82 @@ namespace {
 typedef unsigned long long u64;
 
 constexpr int ONE = 39;                         // a weight of 1 is 2^39
-constexpr double ONE_F = (double)(1ull << ONE);
 
 // ---- the weights -------------------------------------------------------------------
 
-// 2^(j/256) 2^ONE, rounded: exp's series in f64 on the host
-constexpr u64 exp2_entry(int j) {
-  const double x = 0.69314718055994530942 * j / 256;
+constexpr int TAB = 128;                        // entries of the table
+constexpr float REACH = 41.0f;                  // 2^-REACH of the largest and below is nothing
+
+// 2^(j/TAB) 2^30, rounded: exp's series in f64 on the host
+constexpr unsigned exp2_entry(int j) {
+  const double x = 0.69314718055994530942 * j / TAB;
   double sum = 1, term = 1;
   for (int n = 1; n < 24; ++n) {
     term = term * x / n;
     sum += term;
   }
-  return (u64)(sum * ONE_F + 0.5);
+  return (unsigned)(sum * (double)(1u << 30) + 0.5);
 }
 struct Exp2Table {
-  u64 v[256];
+  unsigned v[TAB];
   constexpr Exp2Table() : v() {
-    for (int j = 0; j < 256; ++j) v[j] = exp2_entry(j);
+    for (int j = 0; j < TAB; ++j) v[j] = exp2_entry(j);
   }
 };
 __device__ const Exp2Table kExp2 = Exp2Table();
 
-// log2(e) / T as two floats
-struct Slope {
-  float hi, lo;
-};
-__device__ __forceinline__ Slope slope_of(float T) {
-  const double c = fmin(1.4426950408889634074 / (double)T, 1e37);
-  Slope s;
-  s.hi = (float)c;
-  s.lo = (float)(c - (double)s.hi);
-  return s;
-}
+// The weights of a row.
+struct Weights {
+  float m;              // the largest logit
+  float hi, lo;         // log2(e) / T as two floats
+  float base;           // taken off the logits first, where they are so large that
+                        // it is needed: exactly, for all within reach of m
+  float hi_tab;         // hi * TAB
+  int k_m;              // m's multiple of 1 / TAB
+  float f_m;            // and its rest
+  const unsigned* tab;  // this lane's copy of the table, entries 32 apart
 
-// The table in shared memory: the entries, and as floats.
-struct Table {
-  u64 w[256];
-  float f[256];
+  __device__ __forceinline__ float split(float x, int& k) const {
+    const float big = __fmaf_rn(x, hi_tab, 12582912.0f);  // 1.5 * 2^23: a whole number in the low bits
+    k = __float_as_int(big) - 0x4B400000;
+    const float kf = __fsub_rn(big, 12582912.0f);
+    return __fmaf_rn(x, lo, __fmaf_rn(x, hi, __fmul_rn(kf, -1.0f / TAB)));
+  }
+  __device__ __forceinline__ Weights(float max, float T, const unsigned* table) : m(max) {
+    // (in f32: f64 divisions by all of a block's threads took microseconds)
+    constexpr float L_HI = 1.44269502f, L_LO = 1.92596300e-8f;  // log2(e)
+    const float t = fmaxf(T, 1e-34f);
+    hi = __fdiv_rn(L_HI, t);
+    lo = hi > 0.0f ? __fdiv_rn(__fadd_rn(__fmaf_rn(-hi, t, L_HI), L_LO), t) : 0.0f;
+    hi_tab = hi * TAB;
+    base = fabsf(m) * hi > 8192.0f ? m : 0.0f;
+    tab = table + (threadIdx.x & 31);
+    f_m = split(__fsub_rn(m, base), k_m);
+  }
+  // how far below the largest, in log2
+  __device__ __forceinline__ float depth(float l) const { return __fmul_rn(__fsub_rn(m, l), hi); }
+  // e = mant 2^-30 2^-n for a depth below REACH (else anything), mant from 2^30 to 2^31
+  __device__ __forceinline__ unsigned parts(float l, int& n) const {
+    int k;
+    const float f = __fsub_rn(split(__fsub_rn(l, base), k), f_m);
+    k -= k_m;
+    n = -(k >> 7);
+    const unsigned w = tab[(k & (TAB - 1)) * 32];
+    const float q = __fmul_rn(f, fmaf(f, fmaf(f, 0.055504109f, 0.24022651f), 0.69314718f));
+    return w + (unsigned)__float2int_rn(__fmul_rn((float)w, q));
+  }
+  __device__ __forceinline__ u64 of(float l, float depth) const {
+    int n;
+    const unsigned w = parts(l, n);
+    // 2^(ONE - 30 - n) w: up by at most 9 places, or down, rounded to nearest
+    const u64 up = (u64)w * (1u << ((ONE - 30 - n) & 31));
+    const unsigned down = (w + (1u << ((n - (ONE - 29)) & 31))) >> ((n - (ONE - 30)) & 31);
+    const u64 e = n > ONE - 30 ? (u64)(n > ONE + 1 ? 0u : down) : up;
+    return depth < REACH ? e : 0ull;
+  }
+  __device__ __forceinline__ u64 of(float l) const { return of(l, depth(l)); }
 };
-
-// e = (mant 2^-n) 2^-ONE, mant in [2^ONE, 2^(ONE+1)); n 63 for what is nothing
-__device__ __forceinline__ u64 weight_parts(float l, float m, const Slope& c, const Table& table, int& n) {
-  // l - m = d + r exactly (D. E. Knuth's two-sum)
-  const float d = __fsub_rn(l, m), bb = __fsub_rn(d, l);
-  const float r = __fadd_rn(__fsub_rn(l, __fsub_rn(d, bb)), __fsub_rn(-m, bb));
-  const float t = __fmul_rn(d, c.hi);
-  const bool there = t >= -62.0f;
-  const float te = __fmaf_rn(d, c.hi, -t) + __fmaf_rn(d, c.lo, __fmul_rn(r, c.hi));
-  const float big = __fmaf_rn(t, 256.0f, 12582912.0f);  // 1.5 * 2^23: the nearest whole number in the low bits
-  const float kf = __fsub_rn(big, 12582912.0f);
-  const int k = __float_as_int(big) - 0x4B400000;
-  const float f = __fadd_rn(__fmaf_rn(kf, -0.00390625f, t), te);  // |f| <= 1/512
-  const float q = __fmul_rn(f, fmaf(f, fmaf(f, 0.055504109f, 0.24022651f), 0.69314718f));
-  n = there ? -(k >> 8) : 63;
-  const int j = k & 255;
-  return table.w[j] + (long long)__float2int_rn(__fmul_rn(table.f[j], q));  // |w q| < 2^30.5
-}
-__device__ __forceinline__ u64 weight_of(float l, float m, const Slope& c, const Table& table) {
-  int n;
-  const u64 w = weight_parts(l, m, c, table, n);
-  // rounded to nearest; n > ONE + 1 is nothing
-  return n > ONE + 1 ? 0ull : (w + ((1ull << n) >> 1)) >> n;
-}
+static_assert(TAB == 128 && ONE == 39, "parts() and of() shift by these");
 
 // ---- rows --------------------------------------------------------------------------
 
@@ -132,13 +145,12 @@ constexpr int kHeld = 1024;        // tokens of a warp's part in shared memory a
 constexpr int NB = 2048;           // bins of the order
 constexpr int CAP = 4096;          // tokens near the borders that are sorted
 constexpr int FEW = 128;           // of these, sorted by counting
-constexpr float REACH = 41.0f;     // log2 of the largest weight over the smallest that is not 0
 constexpr float SLACK = 6e-4f;     // of the bins' estimated sums
 constexpr int PLACES = 16;         // places in a bin
 constexpr int POS_BITS = 18;       // a bin's word: the sum of its tokens' places, above it their number
 
 struct alignas(16) Shared {
-  Table table;
+  unsigned table[TAB * 32];
   unsigned bin[NB];                // this block's tokens in each bin, and their places in it
   union {
     struct {
@@ -238,9 +250,8 @@ __device__ float block_after(float v, Shared& s) {
 
 // Where a token lies in the order: PLACES times its bin, plus its place there.
 struct Bins {
-  float m, c, scale;
-  __device__ __forceinline__ float depth(float l) const { return __fmul_rn(__fsub_rn(m, l), c); }  // in log2
-  // any monotone function of the logit serves; all of it is finite for depth < REACH
+  float scale;
+  // any monotone function of the depth serves; it is finite below REACH
   __device__ __forceinline__ unsigned place(float depth) const {
     return min((unsigned)__float_as_int(__fadd_rn(__fmul_rn(depth, scale), 8388608.0f)) & 0x7FFFFFu, (unsigned)PLACES * NB - 1u);
   }
@@ -320,10 +331,7 @@ __global__ void __launch_bounds__(THREADS) sample_kernel(const SampleArgs a) {
     s.listed = 0;
     asm volatile("griddepcontrol.launch_dependents;" :::);
   }
-  for (int i = threadIdx.x; i < 256; i += THREADS) {
-    s.table.w[i] = kExp2.v[i];
-    s.table.f[i] = (float)kExp2.v[i];
-  }
+  for (int i = threadIdx.x; i < TAB * 32; i += THREADS) s.table[i] = kExp2.v[i / 32];
   for (int i = threadIdx.x; i < NB; i += THREADS) s.bin[i] = 0;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const long row = blockIdx.x / C;
@@ -340,10 +348,10 @@ __global__ void __launch_bounds__(THREADS) sample_kernel(const SampleArgs a) {
   mine.mem = (float*)(smem + sizeof(Shared)) + (size_t)warp * a.held;
 
   // the first of the order, and the lowest logit
+  float top = -INFINITY;  // this lane's largest
   {
     u64 first = ~0ull;
     float low = INFINITY;
-    float top = -INFINITY;
     int at = 0;
     mine.first([&](float l, int i) {
       if (l > top) {  // (indices ascend in a lane)
@@ -388,12 +396,11 @@ __global__ void __launch_bounds__(THREADS) sample_kernel(const SampleArgs a) {
     }
     return;
   }
-  const float m = value_of(first);
-  const Slope c = slope_of(T);
+  const Weights w = Weights(value_of(first), T, s.table);
   const int tk = a.top_k ? __ldcg(a.top_k + row) : 0;
   const float tp = a.top_p ? __ldcg(a.top_p + row) : 1.0f;
   const float mp0 = a.min_p ? __ldcg(a.min_p + row) : 0.0f, mp = mp0 > 0.0f ? fminf(mp0, 1.0f) : 0.0f;
-  const u64 least = mp > 0.0f ? (u64)ceil((double)mp * ONE_F) : 0ull;
+  const u64 least = mp > 0.0f ? __float2ull_ru(__fmul_rn(mp, (float)(1ull << ONE))) : 0ull;
   const bool by_k = tk > 0 && tk < N, by_p = tp < 1.0f;
   // what is kept is all keys up to `last`, with weights of `least` at least
   u64 last = ~0ull;
@@ -401,139 +408,186 @@ __global__ void __launch_bounds__(THREADS) sample_kernel(const SampleArgs a) {
 
   if (by_k || by_p) {
     // ---- the order in bins ----
-    const float reach = fminf(REACH, __fmul_rn(__fsub_rn(m, low), c.hi));
-    const Bins bins = {m, c.hi, fminf((float)PLACES * (NB - 1) / fmaxf(reach, 1e-30f), 1e30f)};
+    const float reach = fminf(REACH, w.depth(low));
+    const Bins bins = {fminf((float)PLACES * (NB - 1) / fmaxf(reach, 1e-30f), 1e30f)};
     unsigned binned = 0;
-    mine.again([&](const float (&l)[4], int) {
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const float d = bins.depth(l[q]);
-        const unsigned p = bins.place(d);
-        if (d < REACH) {
-          atomicAdd(&s.bin[p / PLACES], (1u << POS_BITS) + p % PLACES);
-          ++binned;
-        }
+    auto count = [&](float l) {
+      const float d = w.depth(l);
+      const unsigned p = bins.place(d);
+      if (d < REACH) {
+        atomicAdd(&s.bin[p / PLACES], (1u << POS_BITS) + p % PLACES);
+        ++binned;
       }
-    });
-    binned = (unsigned)block_sum(binned, s);
-    if (threadIdx.x < C) cl.map_shared_rank(&s, threadIdx.x)->n_bin[me] = binned;
-    cl.sync();
-    const int per = NB / C;
-    for (int i = threadIdx.x; i < per; i += THREADS) {
-      const int b = me * per + i;
-      unsigned v[MAX_C], n = 0, p = 0;
+    };
+    // the row's bins, in every block
+    auto merge = [&] {
+      binned = (unsigned)block_sum(binned, s);
+      if (threadIdx.x < C) cl.map_shared_rank(&s, threadIdx.x)->n_bin[me] = binned;
+      cl.sync();
+      const int per = NB / C;
+      for (int i = threadIdx.x; i < per; i += THREADS) {
+        const int b = me * per + i;
+        unsigned v[MAX_C], n = 0, p = 0;
 #pragma unroll
-      for (int q = 0; q < MAX_C; ++q) v[q] = q < C ? cl.map_shared_rank(&s, q)->bin[b] : 0u;
+        for (int q = 0; q < MAX_C; ++q) v[q] = q < C ? cl.map_shared_rank(&s, q)->bin[b] : 0u;
 #pragma unroll
-      for (int q = 0; q < MAX_C; ++q) {
-        n += v[q] >> POS_BITS;
-        p += v[q] & ((1u << POS_BITS) - 1u);
-      }
-#pragma unroll
-      for (int q = 0; q < MAX_C; ++q)
-        if (q < C) {
-          Shared* to = cl.map_shared_rank(&s, q);
-          to->all.cnt[b] = n;
-          to->all.pos[b] = p;
+        for (int q = 0; q < MAX_C; ++q) {
+          n += v[q] >> POS_BITS;
+          p += v[q] & ((1u << POS_BITS) - 1u);
         }
-    }
-    cl.sync();
-    // ---- the windows: the bin of the top_k border, those of the top_p border ----
-    // A bin's sum of weights is estimated from its tokens' mean place: within
-    // (ln2 * width)^2 / 8 of it, width at most 41 / 2047, half a place's rounding
-    // (4.4e-4) and the f32 sums: SLACK covers them.
+#pragma unroll
+        for (int q = 0; q < MAX_C; ++q)
+          if (q < C) {
+            Shared* to = cl.map_shared_rank(&s, q);
+            to->all.cnt[b] = n;
+            to->all.pos[b] = p;
+          }
+      }
+      cl.sync();
+    };
     constexpr int PER = NB / THREADS;
-    unsigned n[PER], nt = 0;
-    float w[PER], wa[PER], wt = 0.f;
-    const float step = reach / (NB - 1);
-    for (int j = 0; j < PER; ++j) {
-      const int b = threadIdx.x * PER + j;
-      n[j] = s.all.cnt[b];
-      w[j] = n[j] ? n[j] * exp2f(-step * (b + s.all.pos[b] / ((float)PLACES * n[j]))) : 0.f;
-      nt += n[j];
-      wt += w[j];
-    }
-    float w_all;
-    u64 n_all;
-    u64 nb = block_before((u64)nt, n_all, s);
-    float wb = block_before(wt, w_all, s);
-    // a bin of more tokens than its word counts loses some: the row is done by halving then
-    unsigned expected = 0;
-    for (int q = 0; q < C; ++q) expected += s.n_bin[q];
-    const bool full = n_all != expected;
+    const int b0 = threadIdx.x * PER;
     int* mark = s.mark;
-    if (threadIdx.x == 0) {
-      mark[0] = NB;      // bin of the top_k border, NB: past the last
-      mark[1] = 0;       // tokens of it that stay
-      mark[2] = NB;
-      mark[3] = NB - 1;
-      s.est[0] = w_all;
-    }
-    __syncthreads();
-    if (by_k) {
-      u64 nn = nb;
-      float ww = wb;
-      for (int j = 0; j < PER; ++j) {
-        if (nn < (u64)tk && nn + n[j] >= (u64)tk) {
-          mark[0] = threadIdx.x * PER + j;
-          mark[1] = (int)((u64)tk - nn);
-          // of its tokens the heaviest: no less than all at its far edge, no more than at its near one
-          s.est[0] = ww;
-          s.est[1] = (float)(tk - (int)nn) * exp2f(-step * (threadIdx.x * PER + j));
-        }
-        nn += n[j];
-        ww += w[j];
-      }
-    }
-    __syncthreads();
-    const int bk = mark[0], nk = mark[1];
-    if (by_p) {
-      const float z_hi = (s.est[0] + (bk < NB ? s.est[1] : 0.f)) * (1.0f + SLACK);
-      const float z_lo = (s.est[0] + (bk < NB ? s.est[1] * exp2f(-step) : 0.f)) * (1.0f - SLACK);
-      const float p = fmaxf(tp, 0.f), rest = 1.0f - p;
-      // The border lies in no bin before the first that may reach it, in none behind
-      // the first that must have.  With no top_k the sums from the end say it too, and
-      // nearer where top_p is close to 1.
-      float after = block_after(wt, s);
-      for (int j = PER - 1; j >= 0; --j) {
-        const float w_j = w[j];
-        w[j] = after;  // behind bin j
-        after += w_j;
-        wa[j] = w_j;
-      }
-      float upto = wb;
-      for (int j = 0; j < PER; ++j) {
-        const int b = threadIdx.x * PER + j;
-        upto += wa[j];
-        bool may = upto * (1.0f + SLACK) >= p * z_lo, must = upto * (1.0f - SLACK) >= p * z_hi;
-        if (bk == NB) {
-          may = may && w[j] * (1.0f - SLACK) <= rest * z_hi;
-          must = must || w[j] * (1.0f + SLACK) <= rest * z_lo;
-        }
-        if (n[j] && may) atomicMin(mark + 2, b);
-        if (n[j] && must) atomicMin(mark + 3, b);
+    unsigned n[PER];
+    u64 n_all, n_before;
+    // the bin in which the count reaches top_k, and how many of it stay
+    auto find_k = [&] {
+      unsigned nt = 0;
+      for (int j = 0; j < PER; ++j) nt += n[j] = s.all.cnt[b0 + j];
+      n_before = block_before((u64)nt, n_all, s);
+      if (threadIdx.x == 0) {
+        mark[0] = NB;  // past the last
+        mark[1] = 0;
+        mark[2] = NB;
+        mark[3] = NB - 1;
       }
       __syncthreads();
+      if (by_k) {
+        u64 nn = n_before;
+        for (int j = 0; j < PER; ++j) {
+          if (nn < (u64)tk && nn + n[j] >= (u64)tk) {
+            mark[0] = b0 + j;
+            mark[1] = (int)((u64)tk - nn);
+          }
+          nn += n[j];
+        }
+      }
+      __syncthreads();
+    };
+    int bk = NB, nk = 0, p_lo = NB, p_hi = -1, safe = 0;
+    bool full = false;
+    // Few of many: the lanes' largest alone are counted.  The bin in which theirs
+    // reach top_k is not before the true one, and with eight lanes to each there are
+    // hardly more tokens up to it than top_k: all of them are listed.
+    bool few = by_k && tk <= C * THREADS / 8 && tk <= CAP / 4;
+    if (few) {
+      if (top > -INFINITY) count(top);
+      merge();
+      find_k();
+      bk = mark[0];
+      nk = tk;
+      p_lo = 0;
+      p_hi = bk;
+      if (bk == NB) {  // too few lanes have any within reach
+        few = false;
+        for (int i = threadIdx.x; i < NB; i += THREADS) s.bin[i] = 0;
+        cl.sync();
+      }
     }
-    const int p_hi = by_p ? min(mark[3], bk) : -1, p_lo = by_p ? min(mark[2], p_hi) : NB;
-    const int safe = by_p ? min(p_lo, bk) : bk;  // bins before it stay whole
+    if (!few) {
+      binned = 0;
+      mine.again([&](const float (&l)[4], int) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) count(l[q]);
+      });
+      merge();
+      find_k();
+      bk = mark[0];
+      nk = mark[1];
+      p_lo = NB;
+      p_hi = -1;
+      // a bin of more tokens than its word counts loses some: the row is done by halving then
+      unsigned expected = 0;
+      for (int q = 0; q < C; ++q) expected += s.n_bin[q];
+      full = n_all != expected;
+      if (by_p) {
+        // ---- the bins of the top_p border ----
+        // A bin's sum of weights is estimated from its tokens' mean place: within
+        // (ln2 * width)^2 / 8 of it, width at most 41 / 2047, half a place's rounding
+        // (4.4e-4) and the f32 sums: SLACK covers them.
+        float v[PER], sum = 0.f;
+        const float step = reach / (NB - 1);
+        for (int j = 0; j < PER; ++j) {
+          v[j] = n[j] ? n[j] * exp2f(-step * (b0 + j + s.all.pos[b0 + j] / ((float)PLACES * n[j]))) : 0.f;
+          sum += v[j];
+        }
+        float all;
+        const float before = block_before(sum, all, s);
+        float after = block_after(sum, s);
+        if (threadIdx.x == 0) {
+          s.est[0] = all;
+          s.est[1] = 0.f;
+        }
+        __syncthreads();
+        if (bk >= b0 && bk < b0 + PER) {
+          float x = before;
+          for (int j = 0; j < bk - b0; ++j) x += v[j];
+          s.est[0] = x;
+          // of its tokens the heaviest: no less than all at its far edge, no more than at its near one
+          s.est[1] = (float)nk * exp2f(-step * bk);
+        }
+        __syncthreads();
+        const float z_hi = (s.est[0] + s.est[1]) * (1.0f + SLACK);
+        const float z_lo = (s.est[0] + s.est[1] * exp2f(-step)) * (1.0f - SLACK);
+        const float p = fmaxf(tp, 0.f), rest = 1.0f - p;
+        // The border lies in no bin before the first that may reach it, in none behind
+        // the first that must have.  With no top_k the sums from the end say it too, and
+        // nearer where top_p is close to 1.
+        float upto = before, left = after + sum;
+        for (int j = 0; j < PER; ++j) {
+          upto += v[j];
+          left = j + 1 < PER ? left - v[j] : after;
+          bool may = upto * (1.0f + SLACK) >= p * z_lo, must = upto * (1.0f - SLACK) >= p * z_hi;
+          if (bk == NB) {
+            // (a difference of f32 sums is off by 2^-23 of what is taken from)
+            const float blur = j + 1 < PER ? 0x1p-22f * (after + sum) : 0.f;
+            may = may && left * (1.0f - SLACK) - blur <= rest * z_hi;
+            must = must || left * (1.0f + SLACK) + blur <= rest * z_lo;
+          }
+          if (n[j] && may) atomicMin(mark + 2, b0 + j);
+          if (n[j] && must) atomicMin(mark + 3, b0 + j);
+        }
+        __syncthreads();
+        p_hi = min(mark[3], bk);
+        p_lo = min(mark[2], p_hi);
+      }
+      safe = by_p ? min(p_lo, bk) : bk;  // bins before it stay whole
+    }
     __syncthreads();
     // ---- the sums beside the windows, the tokens in them ----
     u64 part = 0, kept = 0, mid = 0;
     if (!full)
       mine.again([&](const float (&l)[4], int i) {
         // (without branches: the four tokens' chains of dependent steps interleave)
-        bool near[4], some = false;
+        float d[4];
+        int b[4];
+        bool near[4], some = false, sums = false;
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-          const float d = bins.depth(l[q]);
-          const int b = d < REACH ? (int)(bins.place(d) / PLACES) : NB;
-          const u64 e = weight_of(l[q], m, c, s.table);
-          near[q] = b < NB && (b == bk || (b >= p_lo && b <= p_hi));
+          d[q] = w.depth(l[q]);
+          b[q] = d[q] < REACH ? (int)(bins.place(d[q]) / PLACES) : NB;
+          near[q] = b[q] < NB && (b[q] == bk || (b[q] >= p_lo && b[q] <= p_hi));
           some = some || near[q];
-          kept += b < safe ? e : 0ull;
-          part += b < safe && e >= least ? e : 0ull;
-          mid += b >= safe && b < bk && !near[q] ? e : 0ull;
+          sums = sums || (b[q] < bk && !near[q]);
+        }
+        if (__any_sync(FULL, sums)) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const u64 e = w.of(l[q], d[q]);
+            kept += b[q] < safe ? e : 0ull;
+            part += b[q] < safe && e >= least ? e : 0ull;
+            mid += b[q] >= safe && b[q] < bk && !near[q] ? e : 0ull;
+          }
         }
         if (some)
 #pragma unroll
@@ -604,14 +658,15 @@ __global__ void __launch_bounds__(THREADS) sample_kernel(const SampleArgs a) {
         u64* weight = s.list;  // of the sorted keys (the block's own list is in sorted[] now)
         const bool k_there = by_k && bk < NB;
 #pragma unroll 1
-        for (unsigned i = threadIdx.x; i < listed; i += THREADS) weight[i] = weight_of(value_of(s.sorted[i]), m, c, s.table);
+        for (unsigned i = threadIdx.x; i < listed; i += THREADS) weight[i] = w.of(value_of(s.sorted[i]));
         __syncthreads();
         if (warp == 0) {
           unsigned stay = listed;
           if (k_there) {
             unsigned before = 0;  // of the keys, those before the top_k bin
-            for (unsigned i = lane; i < listed; i += 32)
-              before += (int)(bins.place(bins.depth(value_of(s.sorted[i]))) / PLACES) < bk;
+            if (!few)
+              for (unsigned i = lane; i < listed; i += 32)
+                before += (int)(bins.place(w.depth(value_of(s.sorted[i]))) / PLACES) < bk;
             stay = __reduce_add_sync(FULL, before) + nk;
           }
           u64 key = stay ? s.sorted[stay - 1] : 0ull;
@@ -666,7 +721,7 @@ __global__ void __launch_bounds__(THREADS) sample_kernel(const SampleArgs a) {
         mine.again([&](const float (&l)[4], int i) {
 #pragma unroll
           for (int q = 0; q < 4; ++q)
-            if (l[q] > -INFINITY && key_of(l[q], i + q) <= key) v += weigh ? weight_of(l[q], m, c, s.table) : 1ull;
+            if (l[q] > -INFINITY && key_of(l[q], i + q) <= key) v += weigh ? w.of(l[q]) : 1ull;
         });
         return whole(v);
       };
@@ -693,7 +748,7 @@ __global__ void __launch_bounds__(THREADS) sample_kernel(const SampleArgs a) {
     mine.again([&](const float (&l)[4], int i) {
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
-        const u64 e = weight_of(l[q], m, c, s.table);
+        const u64 e = w.of(l[q]);
         part += e >= least && key_of(l[q], i + q) <= last ? e : 0ull;
       }
     });
@@ -741,7 +796,7 @@ __global__ void __launch_bounds__(THREADS) sample_kernel(const SampleArgs a) {
   for (int i0 = begin; i0 < end; i0 += THREADS) {
     const int i = i0 + threadIdx.x;
     const float l = i < end ? clean(__ldcg(x + i)) : -INFINITY;
-    u64 e = i < end && key_of(l, i) <= last ? weight_of(l, m, c, s.table) : 0ull;
+    u64 e = i < end && key_of(l, i) <= last ? w.of(l) : 0ull;
     e = e >= least ? e : 0ull;
     u64 all;
     const u64 r = run + block_before(e, all, s);
@@ -749,8 +804,8 @@ __global__ void __launch_bounds__(THREADS) sample_kernel(const SampleArgs a) {
       a.idx[row] = i;
       if (a.prob) {
         int n;
-        const u64 p = weight_parts(l, m, c, s.table, n);
-        a.prob[row] = (float)(scalbn((double)p, -n) / (double)total);
+        const unsigned p = w.parts(l, n);
+        a.prob[row] = (float)(scalbn((double)p, ONE - 30 - n) / (double)total);
       }
     }
     run += all;
