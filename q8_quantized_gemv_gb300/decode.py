@@ -23,6 +23,11 @@ appended to the layer's paged cache with the per-head norms and the rotation
 (lk_kv_append), the attention over the cache (lk_attn, or lk_attn_shared for
 a batch on one prefix) writes the o projection's quantized activation.
 
+moe=Mixture(...) (with glu=True) puts a mixture of experts in place of the
+gate/up pair and the down projection: the router's logits (a Q8_0 matrix on the
+same normed activation), lk_moe_route, lk_moe_glu_q8 and lk_moe_down_q8.
+sample=Sampling(...) draws the token (lk_sample) instead of taking the argmax.
+
 Weights live on the device for the life of the object (about 8 GB for the
 36-layer, hidden-4096 configuration); every buffer is allocated once here and
 ``run_token`` only launches kernels, so it can be captured in a CUDA graph.
@@ -130,11 +135,88 @@ class Attention:
         return 1 + lk.lk_attn_launches(self.caches[0], self.n_q, *self.table.shape, 1, self.prefix)
 
 
+class Mixture:
+    """The mixture of experts of a DecodeStack's layers: `experts` matrices
+    each of gate, up and down, of `ffn` rows, k of them for a row; the routing's
+    settings as lk_moe_route's.  bias: one (seeded) for each expert.
+
+    State after the stack is built: ids and weights of the last layer that ran
+    ([batch, k]), stacks (one lk.Experts per layer).  It belongs to one stack."""
+
+    def __init__(self, experts=64, k=8, ffn=1024, score="softmax", bias=False, n_group=1, top_group=1, group_sum=1,
+                 renorm=True, scale=1.0):
+        self.E, self.k, self.F, self.bias = experts, k, ffn, bias
+        self.how = dict(score=score, n_group=n_group, top_group=top_group, group_sum=group_sum, renorm=renorm,
+                        scale=scale)
+
+    def build(self, layers, hidden, batch, mode, seed, dev):
+        if hasattr(self, "stacks"):
+            raise ValueError("this Mixture has the experts of another stack")
+        E, F, n = self.E, self.F, batch * self.k
+
+        def stack(rows, K, s):
+            q, sc = synth.q8_matrix_torch(E * rows, K, s, dev)
+            return q.view(E, rows, K), sc.view(E, rows, K // 32)
+        self.stacks, self.routers, self.biases = [], [], []
+        for l in range(layers):
+            s = seed + 10 * l
+            self.stacks.append(lk.Experts(gate=stack(F, hidden, s), up=stack(F, hidden, s + 1),
+                                          down=stack(hidden, F, s + 2)))
+            self.routers.append(synth.q8_matrix_torch(E, hidden, s + 3, dev))
+            self.biases.append(synth.norm_gain_torch(E, s + 4, dev) - 1 if self.bias else None)
+        self.logits = torch.empty((batch, E), dtype=torch.float32, device=dev)
+        self.ids = torch.empty((batch, self.k), dtype=torch.int32, device=dev)
+        self.weights = torch.empty((batch, self.k), dtype=torch.float32, device=dev)
+        self.h = torch.empty((n, F), dtype=torch.float32, device=dev)
+        # (zeros: the rows of pairs that are not there stay as they are)
+        self.words = {}
+        if mode != lk.LK_DEQUANT:
+            self.words = {"hq": torch.zeros((n, F), dtype=torch.int8, device=dev),
+                          "hs": torch.zeros((n, F // 32), dtype=torch.float32, device=dev)}
+            if mode == lk.LK_TWOPASS:
+                self.words["hl"] = torch.zeros((n, F), dtype=torch.int8, device=dev)
+            self.cnt = torch.zeros((n * F // 32,), dtype=torch.int32, device=dev)
+
+    def step(self, l, act, mode, y, cfg):
+        """Layer l's experts on the normed rows `act`, summed into y."""
+        lk.lk_gemv_q8(*self.routers[l], mode, self.logits, M=self.ids.shape[0], cfg=cfg, **act)
+        lk.lk_moe_route(self.logits, self.ids, self.weights, bias=self.biases[l], cfg=cfg, **self.how)
+        to = dict(self.words, cnt=self.cnt) if self.words else {}
+        act = {n: t for n, t in act.items() if t is not None}
+        lk.lk_moe_glu_q8(self.stacks[l], mode, self.ids, self.h, cfg=cfg, **act, **to)
+        lk.lk_moe_down_q8(self.stacks[l], mode, self.ids, self.weights, y, cfg=cfg,
+                          **(self.words or {"h": self.h}))
+
+
+class Sampling:
+    """How a DecodeStack draws its tokens (lk_sample): temperature, top_k,
+    top_p and min_p, each one number or one per sequence (None: off).
+
+    State after the stack is built: u float32 [batch], the random numbers in
+    [0, 1) of the next token, which the caller writes; prob float32 [batch], the
+    drawn tokens' probabilities."""
+
+    def __init__(self, temperature=None, top_k=None, top_p=None, min_p=None):
+        self.given = dict(temperature=temperature, top_k=top_k, top_p=top_p, min_p=min_p)
+
+    def build(self, batch, dev):
+        self.set = {}
+        for n, v in self.given.items():
+            if v is not None:
+                t = torch.tensor(v, dtype=torch.int32 if n == "top_k" else torch.float32, device=dev)
+                self.set[n] = t.expand(batch).contiguous()
+        self.u = torch.zeros((batch,), dtype=torch.float32, device=dev)
+        self.prob = torch.zeros((batch,), dtype=torch.float32, device=dev)
+
+    def draw(self, logits, idx, cfg):
+        lk.lk_sample(logits, self.u, idx, prob=self.prob, cfg=cfg, **self.set)
+
+
 class DecodeStack:
     def __init__(self, layers=36, hidden=4096, q_dim=4096, kv_dim=1024, ffn=12288, vocab=151936,
                  batch=1, mode=lk.LK_INT8ACT, seed=synth.SEED_BASE + 4, device="cuda", eps=1e-6,
                  fused=False, chain=False, group_qkv=True, prefill=None, glu=False, fused_qkv=True, pdl=False,
-                 path=0, tune=None, splitk=True, attn=None):
+                 path=0, tune=None, splitk=True, attn=None, moe=None, sample=None):
         self.L, self.H, self.Q, self.KV, self.F, self.V = layers, hidden, q_dim, kv_dim, ffn, vocab
         self.B, self.mode, self.eps, self.dev = batch, lk._mode(mode), eps, torch.device(device)
         # per projection (qkv, o, gu, down, lm): warps of a GEMV block that
@@ -156,6 +238,15 @@ class DecodeStack:
             if not self.glu or not fused_qkv:
                 raise ValueError("attn needs the decoder dataflow (glu=True) and the fused q|k|v matrix")
             attn.build(layers, q_dim, kv_dim, batch, s + 777_000, dev)
+        self.moe, self.sample = moe, sample
+        if moe is not None:
+            if not self.glu:
+                raise ValueError("moe needs the decoder dataflow (glu=True)")
+            moe.build(layers, hidden, batch, self.mode, s + 888_000, dev)
+        if sample is not None:
+            if not self.glu:
+                raise ValueError("sample needs the decoder dataflow (glu=True)")
+            sample.build(batch, dev)
         self.shapes = {"q": (q_dim, hidden), "k": (kv_dim, hidden), "v": (kv_dim, hidden),
                        "o": (hidden, q_dim), "gu": (2 * ffn, hidden), "down": (hidden, ffn)}
         # fused_qkv: q, k and v are row ranges of one [q + 2 kv, hidden]
@@ -172,6 +263,8 @@ class DecodeStack:
                     w[n] = (w["qkv"][0][r0:r1], w["qkv"][1][r0:r1])
             for i, (name, (N, K)) in enumerate(self.shapes.items()):
                 if name in ("q", "k", "v") and self.fused_qkv:
+                    continue
+                if self.moe is not None and name in ("gu", "down"):
                     continue
                 if name == "gu" and self.glu:
                     # the gate and up matrices of the pair (ffn rows each)
@@ -250,7 +343,7 @@ class DecodeStack:
         if self.qkv_one and not any(fq):
             cand["qkv"] = (q_dim + 2 * kv_dim, hidden)
         for n in ("o", "gu", "down"):
-            if not self.fused[n] and not (n == "gu" and self.glu):
+            if not self.fused[n] and not (n == "gu" and self.glu) and not (n == "down" and moe is not None):
                 cand[n] = self.shapes[n]
         if splitk is False or B < 2 or self.chain is not None:
             self.splitk = {}
@@ -364,14 +457,21 @@ class DecodeStack:
             h_mid = self.hbuf[0]
             a_m = self._add_norm(self.out["o"], h_cur, h_mid, w["g_mlp"])
             a_d = {"x": self.hglu} if m == lk.LK_DEQUANT else self.acts[self.F]
-            launch("gu", lambda w=w, a=a_m, d=a_d: lk.lk_gemv_q8_glu(
-                w["gate"][0], w["gate"][1], w["up"][0], w["up"][1], m, self.gu_buf, h=self.hglu,
-                hq=d.get("xq"), hl=d.get("xl"), hs=d.get("xs"), cnt=self.glu_cnt, M=B, cfg=self._cfg("gu"), **a))
-            launch("down", lambda w=w, d=a_d: self._gemv(w["down"], self.out["down"], d, name="down"))
+            if self.moe is not None:
+                launch("moe", lambda l=l, a=a_m: self.moe.step(l, a, m, self.out["down"], self._cfg()))
+            else:
+                launch("gu", lambda w=w, a=a_m, d=a_d: lk.lk_gemv_q8_glu(
+                    w["gate"][0], w["gate"][1], w["up"][0], w["up"][1], m, self.gu_buf, h=self.hglu,
+                    hq=d.get("xq"), hl=d.get("xl"), hs=d.get("xs"), cnt=self.glu_cnt, M=B, cfg=self._cfg("gu"), **a))
+                launch("down", lambda w=w, d=a_d: self._gemv(w["down"], self.out["down"], d, name="down"))
             h_next = self.hbuf[1]
             g_next = self.layers[l + 1]["g_attn"] if l + 1 < L else self.g_final
             a_h = self._add_norm(self.out["down"], h_mid, h_next, g_next)
             h_cur = h_next
+        if self.sample is not None:
+            launch("lm", lambda: self._gemv(self.lm, self.logits, a_h, name="lm"))
+            self.sample.draw(self.logits, self.idx, self._cfg())
+            return self.idx
         self.n_parts = launch("lm", lambda: self._gemv(self.lm, self.logits, a_h, self.parts, name="lm"))
         lk.lk_argmax(self.idx, B, self.V, parts=self.parts, n_parts=self.n_parts)
         return self.idx
@@ -436,14 +536,16 @@ class DecodeStack:
 
     # -- accounting ------------------------------------------------------------------------
     def weight_bytes(self, name=None):
-        """Algorithmic weight bytes (N*K levels + N*K/16 scale bytes)."""
+        """Algorithmic weight bytes (N*K levels + N*K/16 scale bytes) of the
+        dense matrices; what a mixture of experts reads depends on the routing."""
         def mb(N, K):
             return N * K + N * K // 16
         if name == "lm":
             return mb(self.V, self.H)
         if name is not None:
             return mb(*self.shapes[name])  # "gu": the gate/up pair together
-        return self.L * sum(mb(N, K) for N, K in self.shapes.values()) + mb(self.V, self.H)
+        return self.L * sum(mb(N, K) for n, (N, K) in self.shapes.items()
+                            if self.moe is None or n not in ("gu", "down")) + mb(self.V, self.H)
 
     def glu_launches(self):
         """Launches of the gate/up pair: one (the ring kernel's SwiGLU
@@ -460,7 +562,9 @@ class DecodeStack:
             # pair, down, add+norm (and a combine per split-K projection);
             # lm-head, argmax
             o_in = self.attn.launches() if self.attn is not None else 0 if self.mode == lk.LK_DEQUANT else 1
-            per_layer = 5 + o_in + self.glu_launches() + len(self.splitk)
+            # the mixture of experts: router, routing, gate/up, down
+            ffn = 4 if self.moe is not None else 1 + self.glu_launches()
+            per_layer = 4 + o_in + ffn + len(self.splitk)
             return 1 + self.L * per_layer + 2
         n = 1  # argmax reduce
         f = self.fused
