@@ -6,7 +6,9 @@
  *
  * The conventions of lk.h hold: device pointers owned by the caller, nothing
  * allocated, asynchronous on the given stream, arguments checked before
- * anything is launched, cfg as everywhere (these calls use its pdl field).
+ * anything is launched, cfg as everywhere (these calls use its pdl field; the
+ * products also path: 2 the kernel for single rows, 3 the tensor-core kernel, LK_INT8ACT
+ * and LK_TWOPASS only, 0 the library's choice, the same bits from both).
  * Make the first call on a device before any stream capture there (it looks up
  * addresses and sets kernel attributes).  Device-side waits are bounded (option
  * "wait_us"); one that runs out ends its kernel and sets bit 256 of the error

@@ -348,8 +348,10 @@ bool fit(MoeArgs& a, int mode, int rows_held, int products, int smem_optin, int*
     const unsigned bytes = (4u * tk + 4u * srow + 127u) & ~127u;
     int depth = room / (int)(NW * bytes);
     if (depth > DEPTH) depth = DEPTH;
-    if (depth * tk <= best + best / 8) continue;
-    best = depth * tk;
+    // (two stages a warp: one is used while the other's copy is under way)
+    const int score = depth * tk + (depth > 1 ? tk / 2 : 0);
+    if (score <= best + best / 8) continue;
+    best = score;
     a.tk = tk;
     a.nsl = (a.K + tk - 1) / tk;
     a.srow = srow;
@@ -374,7 +376,9 @@ lk_status launch_moe(MoeArgs& a, int mode, int M, int held, const lk_launch_cfg*
   a.wait_ns = opt_wait_us > 0 ? (unsigned long long)opt_wait_us * 1000ull : 2000000000ull;
   a.err = error_word_ptr();
   if (!a.err) return LK_ERR_CUDA;
-  if (mode != 0 && M > 1) return moe_rows(a, GLU, mode, M, cfg_pdl(cfg), stream);
+  const int path = cfg ? cfg->path : 0;
+  if (path == 1 || (path == 3 && mode == 0)) return LK_ERR_SHAPE;
+  if (path == 3 || (path == 0 && mode != 0 && M > 1)) return moe_rows(a, GLU, mode, M, cfg_pdl(cfg), stream);
   int smem = 0;
   // blocks of a row of activations; down: enough that a block's products are few
   int gx = (d->sm_count + M - 1) / M;

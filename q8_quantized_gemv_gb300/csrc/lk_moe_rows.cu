@@ -36,7 +36,7 @@ namespace {
 
 constexpr int TR = 16;        // weight rows of a tile
 constexpr int TP = 8;         // pairs of a bundle
-constexpr int NW = 8;         // warps of a block
+constexpr int NW = 16;        // warps of a block at most (TwoPass: 12, for its registers)
 constexpr int DEPTH = 2;      // stages of a warp at most
 constexpr int STATIC = 1024;  // static shared memory, at most
 constexpr int ROOM_D = 65536; // bytes of products that a block keeps, about
@@ -48,6 +48,7 @@ struct RowsArgs {
   unsigned s_off, x_off, xl_off, xs_off;
   unsigned o_ids, o_rank, o_order, o_cnt, o_off, o_bundle, o_d, o_ring;  // offsets in shared memory
   int rows_d;                      // down: output rows of a pass
+  int nw;                          // warps
 };
 
 __device__ __forceinline__ void ldmatrix4(unsigned (&r)[4], unsigned addr) {
@@ -71,13 +72,13 @@ __device__ __forceinline__ unsigned bundle_of(int e, int start, int n) {
 }
 
 template <int Q, bool GLU>
-__global__ void __launch_bounds__(NW * 32, 1) moe_rows_kernel(const RowsArgs ra) {
+__global__ void __launch_bounds__((Q == 1 ? NW : 12) * 32, 1) moe_rows_kernel(const RowsArgs ra) {
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ unsigned long long bars[NW * DEPTH];
   __shared__ int totals[2][NW];
   __shared__ int aborted, n_bundles;
   const MoeArgs& a = ra.a;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = ra.nw;
   const int g = lane >> 2, t4 = lane & 3;
   volatile int* abort_flag = &aborted;
   short* ids = (short*)(smem + ra.o_ids);
@@ -123,7 +124,7 @@ __global__ void __launch_bounds__(NW * 32, 1) moe_rows_kernel(const RowsArgs ra)
   __syncthreads();
   // first places and bundles: sums over the experts before (a thread has neighbours)
   {
-    const int per = (a.E + NW * 32 - 1) / (NW * 32), e0 = min(a.E, (int)threadIdx.x * per), e1 = min(a.E, e0 + per);
+    const int per = (a.E + nw * 32 - 1) / (nw * 32), e0 = min(a.E, (int)threadIdx.x * per), e1 = min(a.E, e0 + per);
     int n = 0, b = 0;
     for (int e = e0; e < e1; ++e) {
       n += cnt[e];
@@ -144,7 +145,7 @@ __global__ void __launch_bounds__(NW * 32, 1) moe_rows_kernel(const RowsArgs ra)
     }
     __syncthreads();
     int bn = in - n, bb = ib - b;
-    for (int w = 0; w < NW; ++w) {
+    for (int w = 0; w < nw; ++w) {
       if (w < warp) {
         bn += totals[0][w];
         bb += totals[1][w];
@@ -187,7 +188,7 @@ __global__ void __launch_bounds__(NW * 32, 1) moe_rows_kernel(const RowsArgs ra)
     auto next = [&](Cursor& s) {
       if (++s.c == a.nsl) {
         s.c = 0;
-        s.tile += NW;
+        s.tile += nw;
       }
     };
     auto issue = [&](const Cursor& s, int to) {
@@ -223,7 +224,7 @@ __global__ void __launch_bounds__(NW * 32, 1) moe_rows_kernel(const RowsArgs ra)
       __syncwarp();
     };
     Cursor head{lo + warp, 0}, at = head;
-    const int total = ok && lo + warp < hi ? ((hi - 1 - lo - warp) / NW + 1) * a.nsl : 0;
+    const int total = ok && lo + warp < hi ? ((hi - 1 - lo - warp) / nw + 1) * a.nsl : 0;
     int issued = 0;
     for (int s = slot; issued < total && issued < a.depth; ++issued, next(head)) {
       issue(head, s);
@@ -352,7 +353,7 @@ __global__ void __launch_bounds__(NW * 32, 1) moe_rows_kernel(const RowsArgs ra)
     __syncthreads();
     if (*abort_flag || t_hi <= t_lo) return;
     const int groups = a.rows / 32;  // of a pair
-    for (int x = t_lo / 4 + warp; x <= (t_hi - 1) / 4; x += NW) {
+    for (int x = t_lo / 4 + warp; x <= (t_hi - 1) / 4; x += nw) {
       const int lo = t_lo > 4 * x ? t_lo : 4 * x, hi = t_hi < 4 * x + 4 ? t_hi : 4 * x + 4;
       if (hi - lo < 4) {
         int old = 0;
@@ -401,7 +402,11 @@ bool fit_rows(RowsArgs& r, int Q, bool glu, int blocks, int smem_optin, int* sme
   r.o_d = take(4u * r.P * r.rows_d);
   r.o_ring = (o + 127u) & ~127u;
   const int room = smem_optin - STATIC - (int)r.o_ring;
-  for (int tk = 1024; tk >= 256; tk /= 2) {  // (slices begin at 8 scales' multiples)
+  // slices of 512 for as many warps as have room (two warps a scheduler left it waiting
+  // for the MMAs; slices begin at multiples of 8 scales)
+  const int most_warps = Q == 1 ? NW : 12;
+  r.nw = 0;
+  for (int tk = 512; tk >= 256 && r.nw < 8; tk /= 2) {
     a.tk = tk < a.K ? tk : a.K;
     a.nsl = (a.K + a.tk - 1) / a.tk;
     r.rs = a.tk + 16u;
@@ -413,12 +418,13 @@ bool fit_rows(RowsArgs& r, int Q, bool glu, int blocks, int smem_optin, int* sme
     r.xl_off = r.x_off + TP * r.ars;
     r.xs_off = r.x_off + Q * TP * r.ars;
     a.stage_bytes = (r.xs_off + TP * r.xsr + 127u) & ~127u;
-    a.depth = room / (int)(NW * a.stage_bytes);
+    const int fits = room / (int)a.stage_bytes;
+    r.nw = fits < most_warps ? fits : most_warps;
+    a.depth = r.nw ? fits / r.nw : 0;
     if (a.depth > DEPTH) a.depth = DEPTH;
-    if (a.depth >= 1) break;
   }
   if (a.depth < 1) return false;
-  *smem = (int)r.o_ring + NW * a.depth * (int)a.stage_bytes;
+  *smem = (int)r.o_ring + r.nw * a.depth * (int)a.stage_bytes;
   return true;
 }
 
@@ -427,7 +433,7 @@ lk_status run(RowsArgs& r, const DeviceInfo* d, int pdl, cudaStream_t stream) {
   static std::atomic<int> done[kMaxDevices];
   int smem = 0;
   if (!fit_rows(r, Q, GLU, d->sm_count, d->smem_optin, &smem)) return LK_ERR_SHAPE;
-  return launch_moe_kernel(moe_rows_kernel<Q, GLU>, done, dim3(d->sm_count), NW * 32, smem, d->smem_optin - STATIC, pdl,
+  return launch_moe_kernel(moe_rows_kernel<Q, GLU>, done, dim3(d->sm_count), r.nw * 32, smem, d->smem_optin - STATIC, pdl,
                            stream, r);
 }
 
