@@ -369,6 +369,15 @@ lk_status run(const MoeArgs& a, dim3 grid, int smem, int optin, int pdl, cudaStr
   return launch_moe_kernel(moe_kernel<Q, GLU>, done, grid, NW * 32, smem, optin - kStatic, pdl, stream, a);
 }
 
+// Whether the tensor-core kernel, which reads a shared expert once, is faster than
+// single rows at the copy rate.  Measured (gate/up, single rows / tensor cores, us): 128
+// experts 4096 x 1024, k 8, Int8Act 8 rows 84 / 105, 16 rows 165 / 162, 32 rows 302 / 209;
+// TwoPass 8 rows 86 / 108, 16 rows 173 / 168; 8 experts, k 2, 4 rows 23 / 34 and 27 / 35,
+// 8 rows 40 / 38 and 48 / 40.
+bool rows_favoured(int E, int pairs, int mode) {
+  return mode == 1 ? pairs >= E + 8 : 4 * pairs >= 3 * E + 16;
+}
+
 template <bool GLU>
 lk_status launch_moe(MoeArgs& a, int mode, int M, int held, const lk_launch_cfg* cfg, cudaStream_t stream) {
   const DeviceInfo* d = device_info(nullptr);
@@ -378,10 +387,12 @@ lk_status launch_moe(MoeArgs& a, int mode, int M, int held, const lk_launch_cfg*
   if (!a.err) return LK_ERR_CUDA;
   const int path = cfg ? cfg->path : 0;
   if (path == 1 || (path == 3 && mode == 0)) return LK_ERR_SHAPE;
-  if (path == 3 || (path == 0 && mode != 0 && M > 1)) return moe_rows(a, GLU, mode, M, cfg_pdl(cfg), stream);
+  if (path == 3 || (path == 0 && mode != 0 && rows_favoured(a.E, M * a.k, mode)))
+    return moe_rows(a, GLU, mode, M, cfg_pdl(cfg), stream);
   int smem = 0;
   // blocks of a row of activations; down: enough that a block's products are few
-  int gx = (d->sm_count + M - 1) / M;
+  int gx = d->sm_count / M;  // (all of them on the SMs at once: a second wave of blocks doubled the time)
+  if (gx < 1) gx = 1;
   if (!GLU) {
     const int least = (int)(((long)a.k * a.rows * 4 + kProducts - 1) / kProducts);
     if (gx < least) gx = least;

@@ -3,10 +3,11 @@
 //
 // Rows that chose the same expert share the read of its weights.  Every block
 // sorts the pairs by expert (the same sort in all of them: it takes about a
-// microsecond, nothing is handed on) into bundles of one expert's up to 8
-// pairs, and takes its share of all bundles' weight rows in order, so an expert's
-// weights come from HBM once (more than 8 pairs: again from L2).  A tile is 16 weight
-// rows x 8 pairs; a warp streams its tiles through its own shared-memory stage
+// microsecond, nothing is handed on) into bundles of one expert's up to 8 pairs
+// (TwoPass 4), and takes its share of all bundles' weight rows in order, so an expert's
+// weights come from HBM once (more pairs: again from L2).  A tile is 16 weight
+// rows x 8 columns, a column a pair's words (TwoPass: neighbouring columns its high and low
+// words, which the same lane then has the dots of); a warp streams its tiles through its own shared-memory stage
 // (bulk copies of the 16 rows, their scales, and of the bundle's activation rows,
 // all of one slice of K), each row 16 bytes longer than its slice, which keeps
 // ldmatrix's eight rows in different banks.  A 32-block is one mma m16n8k32 of int8
@@ -23,7 +24,7 @@
 // are added in the order of the pairs.
 //
 // Bound: HBM for few pairs an expert.  The int8 MMA takes 16 cycles of an SM's
-// tensor pipe, 70 % of it at the copy bandwidth under Int8Act (TwoPass: 140 %).
+// tensor pipe, 70 % of it at the copy bandwidth.
 #include "lk_moe.cuh"
 
 using namespace lk;
@@ -35,8 +36,8 @@ namespace lkmoe {
 namespace {
 
 constexpr int TR = 16;        // weight rows of a tile
-constexpr int TP = 8;         // pairs of a bundle
-constexpr int NW = 16;        // warps of a block at most (TwoPass: 12, for its registers)
+constexpr int TC = 8;         // columns of a tile: activation rows of a stage
+constexpr int NW = 16;        // warps of a block at most
 constexpr int DEPTH = 2;      // stages of a warp at most
 constexpr int STATIC = 1024;  // static shared memory, at most
 constexpr int ROOM_D = 65536; // bytes of products that a block keeps, about
@@ -45,17 +46,17 @@ struct RowsArgs {
   MoeArgs a;
   int M, P;                        // rows, pairs M * k
   unsigned rs, srs, ars, xsr;      // stage: bytes of a level, scale, activation and activation-scale row
-  unsigned s_off, x_off, xl_off, xs_off;
+  unsigned x_off, xs_off;
   unsigned o_ids, o_rank, o_order, o_cnt, o_off, o_bundle, o_d, o_ring;  // offsets in shared memory
   int rows_d;                      // down: output rows of a pass
   int nw;                          // warps
 };
 
 __device__ __forceinline__ void ldmatrix4(unsigned (&r)[4], unsigned addr) {
+  // (volatile: in order with the waits and the copies; no other memory is concerned)
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr)
-               : "memory");
+               : "r"(addr));
 }
 // d = A (16 x 32) * B (32 x 8) + 0x4B400000: as a float, 1.5 * 2^23 + the dot (|dot| < 2^20)
 __device__ __forceinline__ void dot_bits(int (&d)[4], const unsigned (&w)[4], unsigned b0, unsigned b1) {
@@ -72,11 +73,12 @@ __device__ __forceinline__ unsigned bundle_of(int e, int start, int n) {
 }
 
 template <int Q, bool GLU>
-__global__ void __launch_bounds__((Q == 1 ? NW : 12) * 32, 1) moe_rows_kernel(const RowsArgs ra) {
+__global__ void __launch_bounds__(NW * 32, 1) moe_rows_kernel(const RowsArgs ra) {
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ unsigned long long bars[NW * DEPTH];
   __shared__ int totals[2][NW];
   __shared__ int aborted, n_bundles;
+  constexpr int TP = TC / Q;  // pairs of a bundle
   const MoeArgs& a = ra.a;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = ra.nw;
   const int g = lane >> 2, t4 = lane & 3;
@@ -171,7 +173,6 @@ __global__ void __launch_bounds__((Q == 1 ? NW : 12) * 32, 1) moe_rows_kernel(co
   const int r_lo = GLU ? 0 : (int)((long)a.rows * blockIdx.x / G), r_hi = GLU ? 0 : (int)((long)a.rows * (blockIdx.x + 1) / G);
   const int t_lo = GLU ? (int)((long)nbu * per * blockIdx.x / G) : 0;
   const int t_hi = GLU ? (int)((long)nbu * per * (blockIdx.x + 1) / G) : 0;
-  // element q of a lane: weight rows g, g + 8 x pairs 2 t4, 2 t4 + 1
   const unsigned a_row = (lane & 15) * ra.rs + (lane >> 4) * 16;
   const unsigned b_row = (lane & 7) * ra.ars + (lane >> 3) * 16;
   int slot = 0;
@@ -211,15 +212,15 @@ __global__ void __launch_bounds__((Q == 1 ? NW : 12) * 32, 1) moe_rows_kernel(co
       __syncwarp();
       if (i < rows) {
         if (lane < 16) bulk_g2s_nohint(st + i * ra.rs, (up ? a.wb : a.wa) + row * a.K + k0, len, bar);
-        else bulk_g2s_nohint(st + ra.s_off + i * ra.srs, (up ? a.sb : a.sa) + (o & ~15ull), slen, bar);
+        else bulk_g2s_nohint(st + a.s_off + i * ra.srs, (up ? a.sb : a.sa) + (o & ~15ull), slen, bar);
       }
       const int x = lane & 7;
       if (x < n) {
         const int p = order[start + x];
         const long xr = GLU ? p / a.k : p;
-        if (lane < 8) bulk_g2s_nohint(st + ra.x_off + x * ra.ars, a.xq + xr * a.K + k0, len, bar);
+        if (lane < 8) bulk_g2s_nohint(st + ra.x_off + Q * x * ra.ars, a.xq + xr * a.K + k0, len, bar);
         else if (lane < 16) bulk_g2s_nohint(st + ra.xs_off + x * ra.xsr, a.xs + xr * nb + (k0 >> 5), len / 8, bar);
-        else if (Q == 2 && lane < 24) bulk_g2s_nohint(st + ra.xl_off + x * ra.ars, a.xl + xr * a.K + k0, len, bar);
+        else if (Q == 2 && lane < 24) bulk_g2s_nohint(st + ra.x_off + (2 * x + 1) * ra.ars, a.xl + xr * a.K + k0, len, bar);
       }
       __syncwarp();
     };
@@ -230,11 +231,16 @@ __global__ void __launch_bounds__((Q == 1 ? NW : 12) * 32, 1) moe_rows_kernel(co
       issue(head, s);
       if (++s == a.depth) s = 0;
     }
-    float p[4][4];  // [partial][element]
+    // partials of a lane's products: [partial][row g or g + 8][its pairs]: Int8Act pairs 2 t4 and
+    // 2 t4 + 1, TwoPass pair t4
+    constexpr int LP = Q == 1 ? 2 : 1;
+    float p[4][2][LP];
 #pragma unroll
     for (int q = 0; q < 4; ++q)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) p[q][e] = 0.f;
+      for (int e = 0; e < 2; ++e)
+#pragma unroll
+        for (int c = 0; c < LP; ++c) p[q][e][c] = 0.f;
     int n = 0;
     for (; ok && n < total; ++n) {
       if (!__all_sync(FULL, mbar_wait(full0 + 8 * slot, phase, a.wait_ns, abort_flag))) {
@@ -245,48 +251,61 @@ __global__ void __launch_bounds__((Q == 1 ? NW : 12) * 32, 1) moe_rows_kernel(co
       const int k0 = at.c * a.tk, len = a.K - k0 < a.tk ? a.K - k0 : a.tk;
       unsigned char* st = ring + (size_t)slot * a.stage_bytes;
       const unsigned W = smem_u32(st) + a_row, X = smem_u32(st + ra.x_off) + b_row;
-      const unsigned L = smem_u32(st + ra.xl_off) + b_row;
       const int v = at.tile / rt, w = at.tile - v * rt;
       // rows of a stack alternate between 0 and 8 bytes into 16 where K / 128 is odd
       const int par = GLU ? g & 1 : (r0 + g) & 1;
-      const unsigned char* S = st + ra.s_off + g * ra.srs + ((par & odd) << 3);
-      const unsigned char* XS = st + ra.xs_off + 2 * t4 * ra.xsr;
+      const unsigned char* S = st + a.s_off + g * ra.srs + ((par & odd) << 3);
+      const unsigned char* XS = st + ra.xs_off + LP * t4 * ra.xsr;
       const int groups = len >> 7;
-#pragma unroll 2
-      for (int gi = 0; gi < groups; ++gi) {
-        int d[4][4], f[4][4];
+      // two groups of four blocks at a time: their MMAs before the first combine
+#pragma unroll 1
+      for (int gi = 0; gi < groups; gi += 2) {
+        int d[2][4][4];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          unsigned xh[4], xl[4], w0[4], w1[4];
-          ldmatrix4(w0, W + 128 * gi + 64 * h);
-          ldmatrix4(w1, W + 128 * gi + 64 * h + 32);
-          ldmatrix4(xh, X + 128 * gi + 64 * h);
-          dot_bits(d[2 * h], w0, xh[0], xh[1]);
-          dot_bits(d[2 * h + 1], w1, xh[2], xh[3]);
-          if constexpr (Q == 2) {
-            ldmatrix4(xl, L + 128 * gi + 64 * h);
-            dot_bits(f[2 * h], w0, xl[0], xl[1]);
-            dot_bits(f[2 * h + 1], w1, xl[2], xl[3]);
+        for (int u = 0; u < 2; ++u) {
+          if (gi + u >= groups) break;
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const unsigned at = 128 * (gi + u) + 64 * h;
+            unsigned x[4], w0[4], w1[4];
+            ldmatrix4(w0, W + at);
+            ldmatrix4(w1, W + at + 32);
+            ldmatrix4(x, X + at);
+            dot_bits(d[u][2 * h], w0, x[0], x[1]);
+            dot_bits(d[u][2 * h + 1], w1, x[2], x[3]);
           }
         }
-        const uint2 s0 = *(const uint2*)(S + 8 * gi), s8 = *(const uint2*)(S + 8 * ra.srs + 8 * gi);
-        const float4 x0 = *(const float4*)(XS + 16 * gi), x1 = *(const float4*)(XS + ra.xsr + 16 * gi);
-        const float2 wa0 = __half22float2(*(const __half2*)&s0.x), wa1 = __half22float2(*(const __half2*)&s0.y);
-        const float2 wb0 = __half22float2(*(const __half2*)&s8.x), wb1 = __half22float2(*(const __half2*)&s8.y);
-        const float ws[2][4] = {{wa0.x, wa0.y, wa1.x, wa1.y}, {wb0.x, wb0.y, wb1.x, wb1.y}};
-        const float xs[2][4] = {{x0.x, x0.y, x0.z, x0.w}, {x1.x, x1.y, x1.z, x1.w}};
 #pragma unroll
-        for (int q = 0; q < 4; ++q)
+        for (int u = 0; u < 2; ++u) {
+          if (gi + u >= groups) break;
+          const uint2 s0 = *(const uint2*)(S + 8 * (gi + u)), s8 = *(const uint2*)(S + 8 * ra.srs + 8 * (gi + u));
+          const float2 wa0 = __half22float2(*(const __half2*)&s0.x), wa1 = __half22float2(*(const __half2*)&s0.y);
+          const float2 wb0 = __half22float2(*(const __half2*)&s8.x), wb1 = __half22float2(*(const __half2*)&s8.y);
+          const float ws[2][4] = {{wa0.x, wa0.y, wa1.x, wa1.y}, {wb0.x, wb0.y, wb1.x, wb1.y}};
+          float xs[LP][4];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float sw = ws[e >> 1][q], sx = xs[e & 1][q], dot = dot_of(d[q][e]);
-            if constexpr (Q == 1) {
-              p[q][e] = __fmaf_rn(__fmul_rn(sw, sx), dot, p[q][e]);
-            } else {
-              const float u = __fmaf_rn(sx, dot, __fmul_rn(__fmul_rn(sx, 0.0078125f), dot_of(f[q][e])));
-              p[q][e] = __fmaf_rn(sw, u, p[q][e]);
-            }
+          for (int c = 0; c < LP; ++c) {
+            const float4 v = *(const float4*)(XS + c * ra.xsr + 16 * (gi + u));
+            xs[c][0] = v.x;
+            xs[c][1] = v.y;
+            xs[c][2] = v.z;
+            xs[c][3] = v.w;
           }
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const int* dq = d[u][q] + 2 * e;  // columns 2 t4, 2 t4 + 1 of row g + 8 e
+              if constexpr (Q == 1) {
+#pragma unroll
+                for (int c = 0; c < 2; ++c)
+                  p[q][e][c] = __fmaf_rn(__fmul_rn(ws[e][q], xs[c][q]), dot_of(dq[c]), p[q][e][c]);
+              } else {
+                const float v = __fmaf_rn(xs[0][q], dot_of(dq[0]), __fmul_rn(__fmul_rn(xs[0][q], 0.0078125f), dot_of(dq[1])));
+                p[q][e][0] = __fmaf_rn(ws[e][q], v, p[q][e][0]);
+              }
+            }
+        }
       }
       __syncwarp();
       if (issued < total) {
@@ -298,23 +317,23 @@ __global__ void __launch_bounds__((Q == 1 ? NW : 12) * 32, 1) moe_rows_kernel(co
       if (at.c == a.nsl - 1) {
         const unsigned bu = bundle[v];
         const int start = (bu >> 10) & 2047, np = (int)(bu >> 21) + 1;
-        float y[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          y[e] = __fadd_rn(__fadd_rn(p[0][e], p[2][e]), __fadd_rn(p[1][e], p[3][e]));
+        for (int c = 0; c < LP; ++c) {
+          float y[2];
 #pragma unroll
-          for (int q = 0; q < 4; ++q) p[q][e] = 0.f;
-        }
+          for (int e = 0; e < 2; ++e) {
+            y[e] = __fadd_rn(__fadd_rn(p[0][e][c], p[2][e][c]), __fadd_rn(p[1][e][c], p[3][e][c]));
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          if (2 * t4 + c >= np) continue;
-          const long pair = order[start + 2 * t4 + c];
+            for (int q = 0; q < 4; ++q) p[q][e][c] = 0.f;
+          }
+          if (LP * t4 + c >= np) continue;
+          const long pair = order[start + LP * t4 + c];
           if (GLU) {
-            a.out[pair * a.rows + 8 * w + g] = swiglu(y[c], y[2 + c]);
+            a.out[pair * a.rows + 8 * w + g] = swiglu(y[0], y[1]);
           } else {
             float* to = dd + pair * ra.rows_d + TR * w + g;
-            if (TR * w + g < rn) to[0] = y[c];
-            if (TR * w + g + 8 < rn) to[8] = y[2 + c];
+            if (TR * w + g < rn) to[0] = y[0];
+            if (TR * w + g + 8 < rn) to[8] = y[1];
           }
         }
       }
@@ -404,7 +423,6 @@ bool fit_rows(RowsArgs& r, int Q, bool glu, int blocks, int smem_optin, int* sme
   const int room = smem_optin - STATIC - (int)r.o_ring;
   // slices of 512 for as many warps as have room (two warps a scheduler left it waiting
   // for the MMAs; slices begin at multiples of 8 scales)
-  const int most_warps = Q == 1 ? NW : 12;
   r.nw = 0;
   for (int tk = 512; tk >= 256 && r.nw < 8; tk /= 2) {
     a.tk = tk < a.K ? tk : a.K;
@@ -413,13 +431,12 @@ bool fit_rows(RowsArgs& r, int Q, bool glu, int blocks, int smem_optin, int* sme
     r.srs = up16(a.tk / 16u + 8u);
     r.ars = a.tk + 16u;
     r.xsr = a.tk / 8u + 16u;
-    r.s_off = TR * r.rs;
-    r.x_off = r.s_off + TR * r.srs;
-    r.xl_off = r.x_off + TP * r.ars;
-    r.xs_off = r.x_off + Q * TP * r.ars;
-    a.stage_bytes = (r.xs_off + TP * r.xsr + 127u) & ~127u;
+    a.s_off = TR * r.rs;
+    r.x_off = a.s_off + TR * r.srs;
+    r.xs_off = r.x_off + TC * r.ars;
+    a.stage_bytes = (r.xs_off + TC * r.xsr + 127u) & ~127u;
     const int fits = room / (int)a.stage_bytes;
-    r.nw = fits < most_warps ? fits : most_warps;
+    r.nw = fits < NW ? fits : NW;
     a.depth = r.nw ? fits / r.nw : 0;
     if (a.depth > DEPTH) a.depth = DEPTH;
   }

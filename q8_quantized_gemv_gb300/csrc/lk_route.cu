@@ -222,6 +222,19 @@ __global__ void __launch_bounds__(32) route_kernel(const RouteArgs a) {
   }
 }
 
+lk_status launch_route(void (*f)(const RouteArgs), int M, int pdl, cudaStream_t stream, const RouteArgs& a) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(M);
+  cfg.blockDim = dim3(32);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = pdl ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, f, a) == cudaSuccess ? LK_OK : LK_ERR_CUDA;
+}
+
 }  // namespace
 
 extern "C" lk_status lk_moe_route(const float* logits, const float* bias, int M, int E, lk_score score, int n_group,
@@ -256,8 +269,7 @@ extern "C" lk_status lk_moe_route(const float* logits, const float* bias, int M,
   a.weights = weights;
   const int pdl = cfg_pdl(cfg);
   // values a lane holds: the smallest of these that fit, fewer steps a round
-  if (E <= 128) launch_pdl(route_kernel<4>, dim3(M), dim3(32), stream, pdl, a);
-  else if (E <= 256) launch_pdl(route_kernel<8>, dim3(M), dim3(32), stream, pdl, a);
-  else launch_pdl(route_kernel<32>, dim3(M), dim3(32), stream, pdl, a);
-  return launch_status();
+  return E <= 128   ? launch_route(route_kernel<4>, M, pdl, stream, a)
+         : E <= 256 ? launch_route(route_kernel<8>, M, pdl, stream, a)
+                    : launch_route(route_kernel<32>, M, pdl, stream, a);
 }

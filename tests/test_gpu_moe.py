@@ -291,6 +291,35 @@ def test_step_together(lk):
     torch.cuda.current_stream().wait_stream(side)
 
 
+@pytest.mark.parametrize("mode", ["int8act", "twopass"])
+@pytest.mark.parametrize("M,E,k,F,K", CASES)
+def test_kernels_agree(lk, mode, M, E, k, F, K):
+    """The kernel for single rows and the tensor-core kernel give the same bits."""
+    ex = lk.Experts(gate=experts(E, F, K, 1, DEV), up=experts(E, F, K, 2, DEV), down=experts(E, K, F, 3, DEV))
+    m, n = lk.MODES[mode], M * k
+    ids = make_ids(M, E, k, 4)
+    acts, hs_ = quantize(x_rows(M, K, 3), m), as_h(quantize(x_rows(n, F, 5), m))
+    w = torch.rand((M, k), device=DEV)
+    got = []
+    for path in (0, 2, 3):
+        cfg = lk.launch_cfg(path=path)
+        h, y = torch.zeros((n, F), device=DEV), torch.zeros((M, K), device=DEV)
+        words = dict(hq=torch.zeros((n, F), dtype=torch.int8, device=DEV), hs=torch.zeros((n, F // 32), device=DEV),
+                     hl=torch.zeros((n, F), dtype=torch.int8, device=DEV))
+        cnt = torch.zeros((n * F // 32,), dtype=torch.int32, device=DEV)
+        lk.lk_moe_glu_q8(ex, m, ids, h, cnt=cnt, cfg=cfg, **words, **acts)
+        lk.lk_moe_down_q8(ex, m, ids, w, y, cfg=cfg, **hs_)
+        assert not bool(cnt.any())
+        got.append([bits(h), bits(y), bits(words["hs"]), words["hq"], words["hl"]])
+    for other in got[1:]:
+        assert all(torch.equal(a, b) for a, b in zip(got[0], other))
+    x = torch.zeros((M, K), device=DEV)
+    for path in (1, 3):
+        with pytest.raises(lk.LkError) as err:
+            lk.lk_moe_glu_q8(ex, "dequant", ids, h, x=x, cfg=lk.launch_cfg(path=path))
+        assert err.value.status == -3
+
+
 def test_two_streams_at_once(lk):
     """Calls on two streams, each with its own outputs and counters."""
     M, E, k, F, K, mode = 8, 12, 4, 256, 768, lk.LK_INT8ACT
