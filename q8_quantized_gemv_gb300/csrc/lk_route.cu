@@ -6,15 +6,15 @@
 // give the next, and its lane drops it.  What this costs is latency (a launch,
 // one read, k + 1 rounds of two warp reductions); there are no bytes to speak of.
 //
-// Which experts are taken is decided in f32 where f32 can: a score is within
-// 2^-19 of its value (exp's argument is rounded to 2^-24 of |l - max|, and
-// e^-x (x + 16) 2^-23 is at most 2^-19; a sigmoid is nearer), so values further
-// apart than 2^-17 (and 2^-22 of themselves, for the rounding of s + bias) are
-// in the right order.  A row where two neighbours of the order taken, or a
-// group that stays and one that does not, are nearer than that (about one row
-// in a thousand), is done again in f64, whose exp would cost every row some
-// microseconds on this GPU's narrow f64 pipe.  Without a bias the order is the
-// logits' own, and exact.
+// Which experts are taken is decided in f32 where f32 can.  A score is within
+// 2^-20 of the row's largest (exp's argument is rounded to 2^-24 of |l - max|, exp to two
+// places, and e^-x (x + 16) 2^-24 is at most that; a sigmoid is within 2^-21), so values
+// further apart than twice that (and 2^-22 of themselves, for the rounding of
+// s + bias) are in the right order.  Where two neighbours of the order taken are nearer
+// (one row in some hundreds), f64 decides, whose exp is slow on this GPU's narrow
+// f64 pipe: for sigmoids of the experts in question alone, one a lane; with a
+// softmax, whose sum takes all of them, or where it is about groups, of the whole row (some
+// 8 us for 256 experts).  Without a bias the order is the logits' own, and exact.
 #include <float.h>
 #include <math.h>
 
@@ -57,10 +57,11 @@ __device__ __forceinline__ double warp_max(double v) {
 __device__ __forceinline__ float exp_of(float x) { return expf(x); }
 __device__ __forceinline__ double exp_of(double x) { return exp(x); }
 
+enum { SURE, ALL };  // what f32 leaves open: nothing, or the whole row
+
 // One row in precision T: the chosen experts and their weights in lanes < k.
-// False: T (f32) does not decide it.
 template <typename T, int V>
-__device__ __forceinline__ bool route_row(const RouteArgs& a, const float (&l)[V], const float (&b)[V], int lane,
+__device__ __forceinline__ int route_row(const RouteArgs& a, const float (&l)[V], const float (&b)[V], int lane,
                                           T* vals, int& id, float& weight) {
   constexpr bool F32 = sizeof(T) == 4;
   const T none = (T)-INFINITY;
@@ -92,7 +93,7 @@ __device__ __forceinline__ bool route_row(const RouteArgs& a, const float (&l)[V
     const bool there = l[v] > -INFINITY && b[v] - b[v] == 0.0f;
     c[v] = !there ? none : by_logit ? (T)l[v] : p[v] + (T)b[v];
   }
-  const T slack = F32 ? (T)0x1p-17f * pmax : (T)0, part = F32 ? (T)0x1p-22f : (T)0;
+  const T slack = F32 ? (a.sigmoid ? (T)0x1p-20f : (T)0x1p-19f * pmax) : (T)0, part = F32 ? (T)0x1p-22f : (T)0;
   bool sure = true;
 
   if (a.n_group > 1) {
@@ -124,7 +125,7 @@ __device__ __forceinline__ bool route_row(const RouteArgs& a, const float (&l)[V
         if (lane < a.n_group && val > none && w > none && (((stay >> g) ^ (stay >> lane)) & 1u))
           sure = sure && fabsf((float)(w - val)) > 2.0f * (float)slack + 2.0f * (float)part * fabsf((float)val);
       }
-      sure = __all_sync(FULL, sure);
+      if (!__all_sync(FULL, sure)) return ALL;
     }
 #pragma unroll
     for (int v = 0; v < V; ++v) {
@@ -134,7 +135,7 @@ __device__ __forceinline__ bool route_row(const RouteArgs& a, const float (&l)[V
   }
 
   T best = none, pb = (T)0, prev = none;
-  float lb = 0.f, lmine = 0.f;
+  float lb = 0.f, bb = 0.f, lmine = 0.f;
   T pmine = (T)0;
   int vb = 0;
   id = -1;
@@ -147,19 +148,35 @@ __device__ __forceinline__ bool route_row(const RouteArgs& a, const float (&l)[V
         vb = v;
         pb = p[v];
         lb = l[v];
+        bb = b[v];
       }
   };
   own_best();
   const int rounds = a.k + (F32 && !by_logit ? 1 : 0);  // one more: the gap behind the last
-  for (int j = 0; j < rounds; ++j) {
+  float logit = 0.f, shift = 0.f;                       // of the lane's candidate
+  int cand = -1;
+  T last = none;  // the k-th value
+  for (int j = 0; j < 33; ++j) {
     const T top = warp_max(best);
     if (top == none) break;
+    if (j >= rounds) {
+      // the order is open: all that may be among the k, in lanes of their own
+      if (sure || last - top > slack + part * (T)fabsf((float)last)) break;
+      if (j == 32) return ALL;
+    }
     const unsigned i = __reduce_min_sync(FULL, best == top ? (unsigned)(lane + 32 * vb) : 0xFFFFFFFFu);
     const int owner = (int)(i & 31u);
     if (F32 && !by_logit && j > 0) sure = sure && prev - top > slack + part * (T)fabsf((float)prev);
+    if (F32 && j == 32 && !sure) return ALL;  // (no lane for it)
     prev = top;
+    if (j == a.k - 1) last = top;
     const T pt = __shfl_sync(FULL, pb, owner);
-    const float lt = __shfl_sync(FULL, lb, owner);
+    const float lt = __shfl_sync(FULL, lb, owner), bt = __shfl_sync(FULL, bb, owner);
+    if (lane == j) {
+      cand = (int)i;
+      logit = lt;
+      shift = bt;
+    }
     if (lane == j && j < a.k) {
       id = (int)i;
       pmine = pt;
@@ -173,6 +190,29 @@ __device__ __forceinline__ bool route_row(const RouteArgs& a, const float (&l)[V
     }
   }
 
+  if (F32 && !sure) {
+    if (!a.sigmoid) return ALL;
+    // the candidates by their values in f64 (equal ones: the lower number)
+    const double d = cand >= 0 ? 1.0 / (1.0 + exp(-(double)logit)) + (double)shift : -INFINITY;
+    int rank = 0;
+    for (int j = 0; j < 32; ++j) {
+      const double o = __shfl_sync(FULL, d, j);
+      const int n = __shfl_sync(FULL, cand, j);
+      rank += o > d || (o == d && n >= 0 && n < cand);
+    }
+    // lane j takes the candidate of rank j
+    int from = 0;
+    for (int j = 0; j < 32; ++j) {
+      const int r = __shfl_sync(FULL, rank, j), n = __shfl_sync(FULL, cand, j);
+      if (n >= 0 && r == lane) from = j;
+    }
+    const float lt = __shfl_sync(FULL, logit, from);
+    const int n = __shfl_sync(FULL, cand, from);
+    id = id >= 0 ? n : -1;
+    lmine = lt;
+    pmine = (T)1 / ((T)1 + exp_of(-(T)lt));
+  }
+
   T w = id >= 0 ? pmine : (T)0;
   if (a.renorm) {
     if (!a.sigmoid) {
@@ -184,11 +224,11 @@ __device__ __forceinline__ bool route_row(const RouteArgs& a, const float (&l)[V
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(FULL, sum, o);
     // sigmoids this small: their quotient needs f64's range
-    if (F32 && sum < (T)1e-30f && __any_sync(FULL, id >= 0)) return false;
+    if (F32 && sum < (T)1e-30f && __any_sync(FULL, id >= 0)) return ALL;
     w = sum > (T)0 ? w / sum : (T)0;
   }
   weight = (float)(w * (T)a.scale);
-  return sure;
+  return SURE;
 }
 
 template <int V>
@@ -215,7 +255,7 @@ __global__ void __launch_bounds__(32) route_kernel(const RouteArgs a) {
   }
   int id;
   float w;
-  if (!route_row<float, V>(a, l, b, lane, (float*)vals, id, w)) route_row_f64<V>(a, l, b, lane, vals, id, w);
+  if (route_row<float, V>(a, l, b, lane, (float*)vals, id, w) != SURE) route_row_f64<V>(a, l, b, lane, vals, id, w);
   if (lane < a.k) {
     a.ids[row * a.k + lane] = id;
     a.weights[row * a.k + lane] = w;

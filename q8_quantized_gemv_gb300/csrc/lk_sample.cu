@@ -1,13 +1,15 @@
 // The next token from the logits (include/lk_sample.h): lk_sample.
 //
-// Weights.  e = exp((l - max) / T) as a whole number of 2^-39: the nearest
-// multiple of 1/128 of l log2(e) / T is taken out of it (one fused multiply-add leaves the
-// rest, below 1/256, to 2^-33), 2^(frac) comes from a table of 128, and the remaining
-// factor, 1 + q with |q| < 2^-7.5, from a cubic in f32 (a table-driven exponential
-// after P. T. P. Tang, ACM TOMS 15(2), 1989): relative error below 2^-29, or
-// half a 2^-39.  Whole numbers add to the same sum in any order, so nothing here
-// depends on how a row is split, and the largest weight is exactly 2^39.  Each lane
-// has a copy of the table in its own bank.
+// Weights.  e = exp((l - max) / T): the nearest multiple of 1/64 of l log2(e) / T
+// is taken out of it (one fused multiply-add leaves the rest, below 1/128, to 2^-32),
+// 2^(frac) comes from a table of 64, and the remaining factor, 1 + q with
+// |q| < 2^-6.5, from a quartic in f32 (a table-driven exponential after P. T. P. Tang, ACM
+// TOMS 15(2), 1989): relative error below 2^-29.  Each lane has a copy of the table in its
+// own banks.  Single weights are whole numbers of 2^-39 (the largest is exactly 2^39);
+// a lane's sum over its part of a row is kept as two f32 sums, of the weights'
+// multiples of a grid that makes them exact and of the rests (whole numbers of 64 bits
+// cost three times the instructions), then rounded to a whole number: what is summed over
+// lanes and blocks does not depend on their order.
 //
 // The order of tokens (the largest logit first, equal ones by index) is that of
 // the 64-bit keys (complement of the logit's order-preserving bits, index);
@@ -33,23 +35,27 @@ constexpr int ONE = 39;                         // a weight of 1 is 2^39
 
 // ---- the weights -------------------------------------------------------------------
 
-constexpr int TAB = 128;                        // entries of the table
+constexpr int TAB = 64;                         // entries of the table
 constexpr float REACH = 41.0f;                  // 2^-REACH of the largest and below is nothing
 
-// 2^(j/TAB) 2^30, rounded: exp's series in f64 on the host
-constexpr unsigned exp2_entry(int j) {
+// 2^(j/TAB): as a float, and what it is more than that, relatively (exp's series in f64 on
+// the host, of which an f32 rest keeps enough)
+constexpr double exp2_of(int j) {
   const double x = 0.69314718055994530942 * j / TAB;
   double sum = 1, term = 1;
   for (int n = 1; n < 24; ++n) {
     term = term * x / n;
     sum += term;
   }
-  return (unsigned)(sum * (double)(1u << 30) + 0.5);
+  return sum;
 }
 struct Exp2Table {
-  unsigned v[TAB];
-  constexpr Exp2Table() : v() {
-    for (int j = 0; j < TAB; ++j) v[j] = exp2_entry(j);
+  float hi[TAB], lo[TAB];
+  constexpr Exp2Table() : hi(), lo() {
+    for (int j = 0; j < TAB; ++j) {
+      hi[j] = (float)exp2_of(j);
+      lo[j] = (float)(exp2_of(j) / (double)hi[j] - 1.0);
+    }
   }
 };
 __device__ const Exp2Table kExp2 = Exp2Table();
@@ -63,7 +69,7 @@ struct Weights {
   float hi_tab;         // hi * TAB
   int k_m;              // m's multiple of 1 / TAB
   float f_m;            // and its rest
-  const unsigned* tab;  // this lane's copy of the table, entries 32 apart
+  const float2* tab;    // this lane's copy of the table, entries 32 apart
 
   __device__ __forceinline__ float split(float x, int& k) const {
     const float big = __fmaf_rn(x, hi_tab, 12582912.0f);  // 1.5 * 2^23: a whole number in the low bits
@@ -71,7 +77,7 @@ struct Weights {
     const float kf = __fsub_rn(big, 12582912.0f);
     return __fmaf_rn(x, lo, __fmaf_rn(x, hi, __fmul_rn(kf, -1.0f / TAB)));
   }
-  __device__ __forceinline__ Weights(float max, float T, const unsigned* table) : m(max) {
+  __device__ __forceinline__ Weights(float max, float T, const float2* table) : m(max) {
     // (in f32: f64 divisions by all of a block's threads took microseconds)
     constexpr float L_HI = 1.44269502f, L_LO = 1.92596300e-8f;  // log2(e)
     const float t = fmaxf(T, 1e-34f);
@@ -84,35 +90,66 @@ struct Weights {
   }
   // how far below the largest, in log2
   __device__ __forceinline__ float depth(float l) const { return __fmul_rn(__fsub_rn(m, l), hi); }
-  // e = mant 2^-30 2^-n for a depth below REACH (else anything), mant from 2^30 to 2^31
-  __device__ __forceinline__ unsigned parts(float l, int& n) const {
+  // e = big (1 + small) for a depth below REACH (else anything)
+  __device__ __forceinline__ float parts(float l, float& small) const {
     int k;
     const float f = __fsub_rn(split(__fsub_rn(l, base), k), f_m);
     k -= k_m;
-    n = -(k >> 7);
-    const unsigned w = tab[(k & (TAB - 1)) * 32];
-    const float q = __fmul_rn(f, fmaf(f, fmaf(f, 0.055504109f, 0.24022651f), 0.69314718f));
-    return w + (unsigned)__float2int_rn(__fmul_rn((float)w, q));
+    const float2 t = tab[(k & (TAB - 1)) * 32];
+    small = fmaf(f, fmaf(f, fmaf(f, fmaf(f, 0.0096181291f, 0.055504109f), 0.24022651f), 0.69314718f), t.y);
+    return __int_as_float(__float_as_int(t.x) + (k >> 6) * (1 << 23));
   }
+  // as a whole number of 2^-ONE, rounded to nearest
   __device__ __forceinline__ u64 of(float l, float depth) const {
-    int n;
-    const unsigned w = parts(l, n);
-    // 2^(ONE - 30 - n) w: up by at most 9 places, or down, rounded to nearest
-    const u64 up = (u64)w * (1u << ((ONE - 30 - n) & 31));
-    const unsigned down = (w + (1u << ((n - (ONE - 29)) & 31))) >> ((n - (ONE - 30)) & 31);
-    const u64 e = n > ONE - 30 ? (u64)(n > ONE + 1 ? 0u : down) : up;
-    return depth < REACH ? e : 0ull;
+    float small;
+    const float big = parts(l, small);
+    // big is a multiple of 2^-64 2^-ONE, so in two steps: its integer (exact or nearest), and the rest
+    const float scaled = __fmul_rn(big, (float)(1ull << ONE)), rest = __fmul_rn(scaled, small);
+    const long long whole = __float2ll_rn(scaled);
+    const float left = __fadd_rn(__fsub_rn(scaled, __ll2float_rn(whole)), rest);
+    return depth < REACH ? (u64)(whole + __float2ll_rn(left)) : 0ull;
   }
   __device__ __forceinline__ u64 of(float l) const { return of(l, depth(l)); }
+  // e >= min_p, the same answer wherever it is asked
+  static __device__ __forceinline__ bool enough(float big, float small, float min_p) {
+    return __fmaf_rn(big, small, __fsub_rn(big, min_p)) >= 0.0f;
+  }
+  __device__ __forceinline__ bool enough(float l, float min_p) const {
+    float small;
+    const float big = parts(l, small);
+    return depth(l) < REACH && enough(big, small, min_p);
+  }
 };
-static_assert(TAB == 128 && ONE == 39, "parts() and of() shift by these");
+static_assert(TAB == 64, "parts() shifts by this");
+
+// A weight as a multiple of GRID / 2^23 and what it is more than that.
+constexpr float GRID = 256.0f;
+struct Split {
+  float multiple, rest;
+  __device__ __forceinline__ Split(float big, float small) {
+    const float r = __fmul_rn(big, small), hi = __fadd_rn(big, r), lo = __fsub_rn(r, __fsub_rn(hi, big));
+    multiple = __fsub_rn(__fadd_rn(hi, 1.5f * GRID), 1.5f * GRID);
+    rest = __fadd_rn(__fsub_rn(hi, multiple), lo);
+  }
+};
+// A lane's sum of up to GRID of them: of the multiples exactly.
+struct Sum {
+  float high = 0.f, low = 0.f;
+  u64 all = 0;
+  __device__ __forceinline__ void add(const Split& v) {
+    high = __fadd_rn(high, v.multiple);
+    low = __fadd_rn(low, v.rest);
+  }
+  __device__ __forceinline__ void flush() {
+    all += (u64)(__float2ll_rn(__fmul_rn(high, (float)(1ull << ONE))) + __float2ll_rn(__fmul_rn(low, (float)(1ull << ONE))));
+    high = low = 0.f;
+  }
+};
 
 // ---- rows --------------------------------------------------------------------------
 
-__device__ __forceinline__ float clean(float x) {
-  if (!(x >= -INFINITY)) return -INFINITY;  // NaN
-  return fminf(x, FLT_MAX);
-}
+// (the maximum with a NaN is the other)
+__device__ __forceinline__ float clean(float x) { return fminf(fmaxf(x, -INFINITY), FLT_MAX); }
 __device__ __forceinline__ unsigned down_bits(float v) {  // the larger v, the smaller
   const unsigned u = __float_as_uint(v == 0.0f ? 0.0f : v);
   return (u & 0x80000000u) ? u : ~(u | 0x80000000u);
@@ -144,13 +181,12 @@ constexpr int MAX_C = 8;           // blocks of a row at most
 constexpr int kHeld = 1024;        // tokens of a warp's part in shared memory at most
 constexpr int NB = 2048;           // bins of the order
 constexpr int CAP = 4096;          // tokens near the borders that are sorted
-constexpr int FEW = 128;           // of these, sorted by counting
 constexpr float SLACK = 6e-4f;     // of the bins' estimated sums
 constexpr int PLACES = 16;         // places in a bin
 constexpr int POS_BITS = 18;       // a bin's word: the sum of its tokens' places, above it their number
 
 struct alignas(16) Shared {
-  unsigned table[TAB * 32];
+  float2 table[TAB * 32];
   unsigned bin[NB];                // this block's tokens in each bin, and their places in it
   union {
     struct {
@@ -331,7 +367,7 @@ __global__ void __launch_bounds__(THREADS) sample_kernel(const SampleArgs a) {
     s.listed = 0;
     asm volatile("griddepcontrol.launch_dependents;" :::);
   }
-  for (int i = threadIdx.x; i < TAB * 32; i += THREADS) s.table[i] = kExp2.v[i / 32];
+  for (int i = threadIdx.x; i < TAB * 32; i += THREADS) s.table[i] = make_float2(kExp2.hi[i / 32], kExp2.lo[i / 32]);
   for (int i = threadIdx.x; i < NB; i += THREADS) s.bin[i] = 0;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const long row = blockIdx.x / C;
@@ -400,11 +436,33 @@ __global__ void __launch_bounds__(THREADS) sample_kernel(const SampleArgs a) {
   const int tk = a.top_k ? __ldcg(a.top_k + row) : 0;
   const float tp = a.top_p ? __ldcg(a.top_p + row) : 1.0f;
   const float mp0 = a.min_p ? __ldcg(a.min_p + row) : 0.0f, mp = mp0 > 0.0f ? fminf(mp0, 1.0f) : 0.0f;
-  const u64 least = mp > 0.0f ? __float2ull_ru(__fmul_rn(mp, (float)(1ull << ONE))) : 0ull;
   const bool by_k = tk > 0 && tk < N, by_p = tp < 1.0f;
-  // what is kept is all keys up to `last`, with weights of `least` at least
+  // what is kept is all keys up to `last`, with weights of mp at least
   u64 last = ~0ull;
   bool summed = false;  // drawn[] has the parts' sums
+
+  // this lane's sum of the weights (number) of the keys up to one, of those of min_p at least
+  auto sum_up_to = [&](u64 key, bool weigh, float min_p) {
+    Sum sum;
+    u64 number = 0;
+    int turns = 0;
+    mine.again([&](const float (&l)[4], int i) {
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        float small;
+        const float big = w.parts(l[q], small);
+        const bool in = l[q] > -INFINITY && key_of(l[q], i + q) <= key;
+        number += in;
+        if (in && w.depth(l[q]) < REACH && Weights::enough(big, small, min_p)) sum.add(Split(big, small));
+      }
+      if (++turns == (int)GRID / 4) {
+        turns = 0;
+        sum.flush();
+      }
+    });
+    sum.flush();
+    return weigh ? sum.all : number;
+  };
 
   if (by_k || by_p) {
     // ---- the order in bins ----
@@ -566,37 +624,56 @@ __global__ void __launch_bounds__(THREADS) sample_kernel(const SampleArgs a) {
     __syncthreads();
     // ---- the sums beside the windows, the tokens in them ----
     u64 part = 0, kept = 0, mid = 0;
-    if (!full)
+    if (!full) {
+      Sum sum_kept, sum_part, sum_mid;
+      // bins by their first places, as place() has them before it takes the whole number out
+      auto from = [&](int b) { return 8388608.0f + (float)(PLACES * b); };
+      const float t_safe = from(safe), t_lo = from(p_lo), t_hi = from(p_hi + 1), t_k = from(bk), t_k1 = from(bk + 1);
+      int turns = 0;
       mine.again([&](const float (&l)[4], int i) {
         // (without branches: the four tokens' chains of dependent steps interleave)
-        float d[4];
-        int b[4];
+        float at[4];
         bool near[4], some = false, sums = false;
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-          d[q] = w.depth(l[q]);
-          b[q] = d[q] < REACH ? (int)(bins.place(d[q]) / PLACES) : NB;
-          near[q] = b[q] < NB && (b[q] == bk || (b[q] >= p_lo && b[q] <= p_hi));
+          const float d = w.depth(l[q]);
+          at[q] = d < REACH ? __fadd_rn(__fmul_rn(d, bins.scale), 8388608.0f) : INFINITY;
+          near[q] = (at[q] >= t_lo && at[q] < t_hi) || (at[q] >= t_k && at[q] < t_k1);
           some = some || near[q];
-          sums = sums || (b[q] < bk && !near[q]);
+          sums = sums || (at[q] < t_k && !near[q]);
         }
         if (__any_sync(FULL, sums)) {
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
-            const u64 e = w.of(l[q], d[q]);
-            kept += b[q] < safe ? e : 0ull;
-            part += b[q] < safe && e >= least ? e : 0ull;
-            mid += b[q] >= safe && b[q] < bk && !near[q] ? e : 0ull;
+            float small;
+            const float big = w.parts(l[q], small);
+            const Split e(big, small);
+            if (at[q] < t_safe) sum_kept.add(e);
+            else if (at[q] < t_k && !near[q]) sum_mid.add(e);
+            if (mp > 0.0f && at[q] < t_safe && Weights::enough(big, small, mp)) sum_part.add(e);
+          }
+          if (++turns == (int)GRID / 4) {
+            turns = 0;
+            sum_kept.flush();
+            sum_part.flush();
+            sum_mid.flush();
           }
         }
         if (some)
 #pragma unroll
           for (int q = 0; q < 4; ++q)
             if (near[q]) {
-              const unsigned at = atomicAdd(&s.listed, 1u);
-              if (at < CAP) s.list[at] = key_of(l[q], i + q);
+              const unsigned n = atomicAdd(&s.listed, 1u);
+              if (n < CAP) s.list[n] = key_of(l[q], i + q);
             }
       });
+      sum_kept.flush();
+      sum_part.flush();
+      sum_mid.flush();
+      kept = sum_kept.all;
+      mid = sum_mid.all;
+      part = mp > 0.0f ? sum_part.all : kept;
+    }
     part = warp_sum(part);
     if (lane == 0) cl.map_shared_rank(&s, 0)->drawn[slot] = part;
     kept = block_sum(kept, s);
@@ -625,18 +702,29 @@ __global__ void __launch_bounds__(THREADS) sample_kernel(const SampleArgs a) {
           s.sorted[i] = cl.map_shared_rank(&s, q)->list[j];
         }
         __syncthreads();
-        if (listed <= FEW) {
-          // a thread's key goes behind as many as are smaller (the keys are distinct)
-          u64 key = 0;
-          unsigned rank = 0;
-          if (threadIdx.x < listed) {
-            key = s.sorted[threadIdx.x];
-            for (unsigned i = 0; i < listed; ++i) rank += s.sorted[i] < key;
-          }
+        if (listed <= THREADS) {
+          // a key a thread; neighbours below 32 meet by shuffles
+          const unsigned i = threadIdx.x;
+          unsigned pad = 32;
+          while (pad < listed) pad *= 2;
+          u64 v = i < listed ? s.sorted[i] : ~0ull;
+          for (unsigned k = 2; k <= pad; k *= 2)
+            for (unsigned j = k / 2; j > 0; j /= 2) {
+              u64 o;
+              if (j >= 32) {
+                __syncthreads();
+                s.sorted[i] = v;
+                __syncthreads();
+                o = s.sorted[i ^ j];
+              } else {
+                o = __shfl_xor_sync(FULL, v, j);
+              }
+              v = (((i & j) == 0) == ((i & k) == 0)) == (o < v) ? o : v;
+            }
           __syncthreads();
-          if (threadIdx.x < listed) s.sorted[rank] = key;
+          s.sorted[i] = v;
         } else {
-          unsigned pad = FEW;
+          unsigned pad = THREADS;
           while (pad < listed) pad *= 2;
           for (unsigned i = listed + threadIdx.x; i < pad; i += THREADS) s.sorted[i] = ~0ull;
           __syncthreads();
@@ -700,7 +788,7 @@ __global__ void __launch_bounds__(THREADS) sample_kernel(const SampleArgs a) {
         last = s.last;
 #pragma unroll 1
         for (unsigned i = threadIdx.x; i < listed; i += THREADS)
-          if (s.sorted[i] <= last && weight[i] >= least)
+          if (s.sorted[i] <= last && (mp == 0.0f || w.enough(value_of(s.sorted[i]), mp)))
             atomicAdd(&s.drawn[((unsigned)(s.sorted[i] & 0xFFFFFFFFu) + skew) / (unsigned)a.part], weight[i]);
         __syncthreads();
       }
@@ -717,13 +805,7 @@ __global__ void __launch_bounds__(THREADS) sample_kernel(const SampleArgs a) {
         return r;
       };
       auto upto = [&](u64 key, bool weigh) {
-        u64 v = 0;
-        mine.again([&](const float (&l)[4], int i) {
-#pragma unroll
-          for (int q = 0; q < 4; ++q)
-            if (l[q] > -INFINITY && key_of(l[q], i + q) <= key) v += weigh ? w.of(l[q]) : 1ull;
-        });
-        return whole(v);
+        return whole(sum_up_to(key, weigh, 0.0f));
       };
       auto border = [&](bool weigh, u64 want, u64 top) {
         u64 bottom = first;
@@ -744,14 +826,7 @@ __global__ void __launch_bounds__(THREADS) sample_kernel(const SampleArgs a) {
     }
   }
   if (!summed) {
-    u64 part = 0;
-    mine.again([&](const float (&l)[4], int i) {
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const u64 e = w.of(l[q]);
-        part += e >= least && key_of(l[q], i + q) <= last ? e : 0ull;
-      }
-    });
+    u64 part = sum_up_to(last, true, mp);
     part = warp_sum(part);
     if (lane == 0) cl.map_shared_rank(&s, 0)->drawn[slot] = part;
   }
@@ -792,24 +867,33 @@ __global__ void __launch_bounds__(THREADS) sample_kernel(const SampleArgs a) {
   __syncthreads();
   const u64 goal = s.goal, total = s.kept[0];
   const int begin = max(0, s.at * a.part - skew), end = min(N, (s.at + 1) * a.part - skew);
-  u64 run = 0;
-  for (int i0 = begin; i0 < end; i0 += THREADS) {
-    const int i = i0 + threadIdx.x;
-    const float l = i < end ? clean(__ldcg(x + i)) : -INFINITY;
-    u64 e = i < end && key_of(l, i) <= last ? w.of(l) : 0ull;
-    e = e >= least ? e : 0ull;
-    u64 all;
-    const u64 r = run + block_before(e, all, s);
-    if (r <= goal && r + e > goal) {
-      a.idx[row] = i;
-      if (a.prob) {
-        int n;
-        const unsigned p = w.parts(l, n);
-        a.prob[row] = (float)(scalbn((double)p, ONE - 30 - n) / (double)total);
+  // (The part's sum was rounded lane by lane: should the goal lie past what its tokens come
+  // to here, the second turn takes the last of them.)
+  u64 run = 0, want = goal;
+  for (int turn = 0; turn < 2; ++turn) {
+    run = 0;
+    for (int i0 = begin; i0 < end && run <= want; i0 += THREADS) {
+      const int i = i0 + threadIdx.x;
+      const float l = i < end ? clean(__ldcg(x + i)) : -INFINITY;
+      u64 e = i < end && key_of(l, i) <= last && (mp == 0.0f || w.enough(l, mp)) ? w.of(l) : 0ull;
+      u64 all;
+      const u64 r = run + block_before(e, all, s);
+      if (r <= want && r + e > want) {
+        a.idx[row] = i;
+        if (a.prob) {
+          float small;
+          const float big = w.parts(l, small);
+          a.prob[row] = (float)(((double)big + (double)big * small) * (double)(1ull << ONE) / (double)total);
+        }
       }
+      run += all;
     }
-    run += all;
-    if (run > goal) break;
+    if (run > want || run == 0) break;
+    want = run - 1;
+  }
+  if (run == 0 && threadIdx.x == 0) {  // nothing but weights that single tokens round to 0: the first
+    a.idx[row] = (int)(first & 0xFFFFFFFFu);
+    if (a.prob) a.prob[row] = (float)((double)(1ull << ONE) / (double)total);
   }
 }
 
