@@ -370,13 +370,12 @@ lk_status run(const MoeArgs& a, dim3 grid, int smem, int optin, int pdl, cudaStr
 }
 
 // Whether the tensor-core kernel, which reads a shared expert once, is faster than
-// single rows at the copy rate.  Measured (gate/up, single rows / tensor cores, us): 128
-// experts 4096 x 1024, k 8, Int8Act 8 rows 84 / 105, 16 rows 165 / 162, 32 rows 302 / 209;
-// TwoPass 8 rows 86 / 108, 16 rows 173 / 168; 8 experts, k 2, 4 rows 23 / 34 and 27 / 35,
-// 8 rows 40 / 38 and 48 / 40.
-bool rows_favoured(int E, int pairs, int mode) {
-  return mode == 1 ? pairs >= E + 8 : 4 * pairs >= 3 * E + 16;
-}
+// single rows at the copy rate.  Measured (gate/up, down; single rows against tensor cores,
+// us): 128 experts 4096 x 1024, k 8, Int8Act 8 rows 84 / 96 and 54 / 61, 16 rows 163 / 147 and
+// 104 / 89; TwoPass 8 rows 87 / 98 and 66 / 61; 60 experts 2048 x 1408, k 4, 16 rows 58 / 58 and
+// 38 / 38, TwoPass 8 rows 36 / 39 and 24 / 26; 8 experts, k 2, 4 rows 23 / 32 and 13 / 18,
+// 8 rows 40 / 36 and 23 / 20.
+bool rows_favoured(int E, int pairs, int mode) { return 16 * pairs >= (mode == 1 ? 15 : 9) * E + 96; }
 
 template <bool GLU>
 lk_status launch_moe(MoeArgs& a, int mode, int M, int held, const lk_launch_cfg* cfg, cudaStream_t stream) {

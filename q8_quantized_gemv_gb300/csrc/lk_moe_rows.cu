@@ -7,10 +7,12 @@
 // (TwoPass 4), and takes its share of all bundles' weight rows in order, so an expert's
 // weights come from HBM once (more pairs: again from L2).  A tile is 16 weight
 // rows x 8 columns, a column a pair's words (TwoPass: neighbouring columns its high and low
-// words, which the same lane then has the dots of); a warp streams its tiles through its own shared-memory stage
-// (bulk copies of the 16 rows, their scales, and of the bundle's activation rows,
-// all of one slice of K), each row 16 bytes longer than its slice, which keeps
-// ldmatrix's eight rows in different banks.  A 32-block is one mma m16n8k32 of int8
+// words, which the same lane then has the dots of); a warp streams its tiles through its
+// own shared-memory stages, each one slice of K: bulk copies of the 16 rows and of the
+// bundle's activation rows, and the lanes' own asynchronous copies of their scales (bulk copies
+// of 32 bytes kept the copy engine, which starts one in about 16 cycles, from the rest).
+// Each row is 16 bytes longer than its slice, which keeps ldmatrix's eight rows in
+// different banks.  A 32-block is one mma m16n8k32 of int8
 // levels with the exact dots as result, combined in f32 as every other kernel
 // of the library does (partial b mod 4 ascending, (p0 + p2) + (p1 + p3)):
 // the products have lk_gemv_q8's bits.
@@ -67,6 +69,17 @@ __device__ __forceinline__ void dot_bits(int (&d)[4], const unsigned (&w)[4], un
 }
 __device__ __forceinline__ float dot_of(int bits) { return __fadd_rn(__int_as_float(bits), -12582912.0f); }
 
+// A lane's own copies, and its arrival at `bar` when they are there.
+__device__ __forceinline__ void copy16(void* to, const void* from) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(to)), "l"(from) : "memory");
+}
+__device__ __forceinline__ void copy8(void* to, const void* from) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(smem_u32(to)), "l"(from) : "memory");
+}
+__device__ __forceinline__ void arrive_with_copies(unsigned bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
+
 // A bundle: expert, its first place in the sorted pairs, pairs.
 __device__ __forceinline__ unsigned bundle_of(int e, int start, int n) {
   return (unsigned)e | (unsigned)start << 10 | (unsigned)(n - 1) << 21;
@@ -93,7 +106,7 @@ __global__ void __launch_bounds__(NW * 32, 1) moe_rows_kernel(const RowsArgs ra)
   unsigned char* ring = smem + ra.o_ring + (size_t)warp * a.depth * a.stage_bytes;
   const unsigned full0 = smem_u32(bars + warp * DEPTH);
   if (lane == 0)
-    for (int s = 0; s < a.depth; ++s) mbar_init(full0 + 8 * s, 1);
+    for (int s = 0; s < a.depth; ++s) mbar_init(full0 + 8 * s, 33);  // the bulk copies', and each lane's
   for (int e = threadIdx.x; e < a.E; e += blockDim.x) cnt[e] = 0;
   if (threadIdx.x == 0) {
     aborted = 0;
@@ -166,7 +179,7 @@ __global__ void __launch_bounds__(NW * 32, 1) moe_rows_kernel(const RowsArgs ra)
   __syncthreads();
   const int nbu = n_bundles;
 
-  const int nb = a.K >> 5, odd = (nb >> 2) & 1;
+  const int nb = a.K >> 5, odd = (nb >> 2) & 1;  // odd: rows of scales begin at 8 bytes in turn
   const int G = gridDim.x;
   // this block's output rows (down), in passes; its tiles (gate/up)
   const int per = a.rows / 8;  // gate/up: tiles of a bundle
@@ -199,29 +212,42 @@ __global__ void __launch_bounds__(NW * 32, 1) moe_rows_kernel(const RowsArgs ra)
       const int k0 = s.c * a.tk, len = a.K - k0 < a.tk ? a.K - k0 : a.tk;
       const unsigned bar = full0 + 8 * to;
       unsigned char* st = ring + (size_t)to * a.stage_bytes;
-      const int i = lane & 15;
       const int rows = GLU ? TR : min(TR, rn - TR * w);
-      const long row = (long)e * a.rows + (GLU ? 8 * w + (i & 7) : r0 + TR * w + i);
-      const bool up = GLU && i >= 8;
-      const unsigned long long o = ((unsigned long long)row * nb + (k0 >> 5)) * 2;
-      const unsigned slen = ((unsigned)len / 16 + (unsigned)(o & 15) + 15u) & ~15u;
-      unsigned mine = i < rows ? (lane < 16 ? (unsigned)len : slen) : 0u;
-      if (lane < n) mine += (unsigned)len * Q + (unsigned)len / 8;
-      mine = __reduce_add_sync(FULL, mine);
-      if (lane == 0) mbar_arrive_expect_tx(bar, mine);
+      auto stack_row = [&](int i) { return (long)e * a.rows + (GLU ? 8 * w + (i & 7) : r0 + TR * w + i); };
+      if (lane == 0) mbar_arrive_expect_tx(bar, (unsigned)len * (rows + Q * n));
       __syncwarp();
-      if (i < rows) {
-        if (lane < 16) bulk_g2s_nohint(st + i * ra.rs, (up ? a.wb : a.wa) + row * a.K + k0, len, bar);
-        else bulk_g2s_nohint(st + a.s_off + i * ra.srs, (up ? a.sb : a.sa) + (o & ~15ull), slen, bar);
-      }
-      const int x = lane & 7;
-      if (x < n) {
-        const int p = order[start + x];
+      if (lane < 16) {
+        if (lane < rows) {
+          const bool up = GLU && lane >= 8;
+          bulk_g2s_nohint(st + lane * ra.rs, (up ? a.wb : a.wa) + stack_row(lane) * a.K + k0, len, bar);
+        }
+      } else if (lane < 16 + Q * n) {
+        const int x = (lane - 16) / Q, low = Q == 2 ? lane & 1 : 0, p = order[start + x];
         const long xr = GLU ? p / a.k : p;
-        if (lane < 8) bulk_g2s_nohint(st + ra.x_off + Q * x * ra.ars, a.xq + xr * a.K + k0, len, bar);
-        else if (lane < 16) bulk_g2s_nohint(st + ra.xs_off + x * ra.xsr, a.xs + xr * nb + (k0 >> 5), len / 8, bar);
-        else if (Q == 2 && lane < 24) bulk_g2s_nohint(st + ra.x_off + (2 * x + 1) * ra.ars, a.xl + xr * a.K + k0, len, bar);
+        bulk_g2s_nohint(st + ra.x_off + (lane - 16) * ra.ars, (low ? a.xl : a.xq) + xr * a.K + k0, len, bar);
       }
+      // scales: 2 bytes a block of a weight row, 16 or (where rows begin at 8) 8 at a time
+      if (!odd && len % 256 == 0) {
+        const int per_row = len / 256;
+        for (int c = lane; c < rows * per_row; c += 32) {
+          const int i = c / per_row, at = 16 * (c - i * per_row);
+          copy16(st + a.s_off + i * ra.srs + at, (GLU && i >= 8 ? a.sb : a.sa) + (stack_row(i) * nb + (k0 >> 5)) * 2 + at);
+        }
+      } else {
+        const int per_row = len / 128;
+        for (int c = lane; c < rows * per_row; c += 32) {
+          const int i = c / per_row, at = 8 * (c - i * per_row);
+          copy8(st + a.s_off + i * ra.srs + at, (GLU && i >= 8 ? a.sb : a.sa) + (stack_row(i) * nb + (k0 >> 5)) * 2 + at);
+        }
+      }
+      // and 4 bytes a block of an activation row
+      const int per_row = len / 128;
+      for (int c = lane; c < n * per_row; c += 32) {
+        const int x = c / per_row, at = 4 * (c - x * per_row), p = order[start + x];
+        const long xr = GLU ? p / a.k : p;
+        copy16(st + ra.xs_off + x * ra.xsr + 4 * at, a.xs + xr * nb + (k0 >> 5) + at);
+      }
+      arrive_with_copies(bar);
       __syncwarp();
     };
     Cursor head{lo + warp, 0}, at = head;
@@ -252,9 +278,7 @@ __global__ void __launch_bounds__(NW * 32, 1) moe_rows_kernel(const RowsArgs ra)
       unsigned char* st = ring + (size_t)slot * a.stage_bytes;
       const unsigned W = smem_u32(st) + a_row, X = smem_u32(st + ra.x_off) + b_row;
       const int v = at.tile / rt, w = at.tile - v * rt;
-      // rows of a stack alternate between 0 and 8 bytes into 16 where K / 128 is odd
-      const int par = GLU ? g & 1 : (r0 + g) & 1;
-      const unsigned char* S = st + a.s_off + g * ra.srs + ((par & odd) << 3);
+      const unsigned char* S = st + a.s_off + g * ra.srs;
       const unsigned char* XS = st + ra.xs_off + LP * t4 * ra.xsr;
       const int groups = len >> 7;
       // two groups of four blocks at a time: their MMAs before the first combine

@@ -146,6 +146,15 @@ struct Sum {
   }
 };
 
+// floor (ceil) of x * total, x from 0 to 1 (below 2^-40: as 2^-40's multiples)
+__device__ __forceinline__ u64 share_down(float x, u64 total) {
+  return __umul64hi(__float2ull_rz(__fmul_rn(x, 0x1p40f)) << 24, total);
+}
+__device__ __forceinline__ u64 share_up(float x, u64 total) {
+  const u64 f = __float2ull_rz(__fmul_rn(x, 0x1p40f)) << 24;
+  return __umul64hi(f, total) + (f * total != 0);
+}
+
 // ---- rows --------------------------------------------------------------------------
 
 // (the maximum with a NaN is the other)
@@ -367,7 +376,10 @@ __global__ void __launch_bounds__(THREADS) sample_kernel(const SampleArgs a) {
     s.listed = 0;
     asm volatile("griddepcontrol.launch_dependents;" :::);
   }
-  for (int i = threadIdx.x; i < TAB * 32; i += THREADS) s.table[i] = make_float2(kExp2.hi[i / 32], kExp2.lo[i / 32]);
+  // (the table's entries are under way while the row is read)
+  static_assert(TAB * 32 == 2 * THREADS, "two entries a thread");
+  const float2 entry[2] = {make_float2(kExp2.hi[threadIdx.x / 32], kExp2.lo[threadIdx.x / 32]),
+                           make_float2(kExp2.hi[TAB / 2 + threadIdx.x / 32], kExp2.lo[TAB / 2 + threadIdx.x / 32])};
   for (int i = threadIdx.x; i < NB; i += THREADS) s.bin[i] = 0;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const long row = blockIdx.x / C;
@@ -397,6 +409,8 @@ __global__ void __launch_bounds__(THREADS) sample_kernel(const SampleArgs a) {
       low = l > -INFINITY ? fminf(low, l) : low;
     });
     if (top > -INFINITY) first = key_of(top, at);
+    s.table[threadIdx.x] = entry[0];
+    s.table[THREADS + threadIdx.x] = entry[1];
     first = ~warp_max_u64(~first);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) low = fminf(low, __shfl_xor_sync(FULL, low, o));
@@ -477,10 +491,16 @@ __global__ void __launch_bounds__(THREADS) sample_kernel(const SampleArgs a) {
         ++binned;
       }
     };
+    // Few of many: the lanes' largest alone are counted.  The bin in which theirs
+    // reach top_k is not before the true one, and with eight lanes to each there are
+    // hardly more tokens up to it than top_k: all of them are listed.
+    bool few = by_k && tk <= C * THREADS / 8 && tk <= CAP / 4;
     // the row's bins, in every block
     auto merge = [&] {
-      binned = (unsigned)block_sum(binned, s);
-      if (threadIdx.x < C) cl.map_shared_rank(&s, threadIdx.x)->n_bin[me] = binned;
+      if (!few) {
+        binned = (unsigned)block_sum(binned, s);
+        if (threadIdx.x < C) cl.map_shared_rank(&s, threadIdx.x)->n_bin[me] = binned;
+      }
       cl.sync();
       const int per = NB / C;
       for (int i = threadIdx.x; i < per; i += THREADS) {
@@ -534,10 +554,6 @@ __global__ void __launch_bounds__(THREADS) sample_kernel(const SampleArgs a) {
     };
     int bk = NB, nk = 0, p_lo = NB, p_hi = -1, safe = 0;
     bool full = false;
-    // Few of many: the lanes' largest alone are counted.  The bin in which theirs
-    // reach top_k is not before the true one, and with eight lanes to each there are
-    // hardly more tokens up to it than top_k: all of them are listed.
-    bool few = by_k && tk <= C * THREADS / 8 && tk <= CAP / 4;
     if (few) {
       if (top > -INFINITY) count(top);
       merge();
@@ -624,7 +640,20 @@ __global__ void __launch_bounds__(THREADS) sample_kernel(const SampleArgs a) {
     __syncthreads();
     // ---- the sums beside the windows, the tokens in them ----
     u64 part = 0, kept = 0, mid = 0;
-    if (!full) {
+    if (few) {
+      // (a loop of its own, so short that fetching its code does not count)
+      const float t_k1 = 8388608.0f + (float)(PLACES * (bk + 1));
+      mine.again([&](const float (&l)[4], int i) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const float d = w.depth(l[q]);
+          if (d < REACH && __fadd_rn(__fmul_rn(d, bins.scale), 8388608.0f) < t_k1) {
+            const unsigned n = atomicAdd(&s.listed, 1u);
+            if (n < CAP) s.list[n] = key_of(l[q], i + q);
+          }
+        }
+      });
+    } else if (!full) {
       Sum sum_kept, sum_part, sum_mid;
       // bins by their first places, as place() has them before it takes the whole number out
       auto from = [&](int b) { return 8388608.0f + (float)(PLACES * b); };
@@ -708,7 +737,9 @@ __global__ void __launch_bounds__(THREADS) sample_kernel(const SampleArgs a) {
           unsigned pad = 32;
           while (pad < listed) pad *= 2;
           u64 v = i < listed ? s.sorted[i] : ~0ull;
+#pragma unroll 1
           for (unsigned k = 2; k <= pad; k *= 2)
+#pragma unroll 1
             for (unsigned j = k / 2; j > 0; j /= 2) {
               u64 o;
               if (j >= 32) {
@@ -728,7 +759,9 @@ __global__ void __launch_bounds__(THREADS) sample_kernel(const SampleArgs a) {
           while (pad < listed) pad *= 2;
           for (unsigned i = listed + threadIdx.x; i < pad; i += THREADS) s.sorted[i] = ~0ull;
           __syncthreads();
+#pragma unroll 1
           for (unsigned k = 2; k <= pad; k *= 2)
+#pragma unroll 1
             for (unsigned j = k / 2; j > 0; j /= 2) {
               for (unsigned i = threadIdx.x; i < pad / 2; i += THREADS) {
                 const unsigned p = 2 * i - (i & (j - 1)), q = p + j;
@@ -760,11 +793,12 @@ __global__ void __launch_bounds__(THREADS) sample_kernel(const SampleArgs a) {
           u64 key = stay ? s.sorted[stay - 1] : 0ull;
           if (by_p) {
             u64 z = 0;
+#pragma unroll 1
             for (unsigned i = lane; i < stay; i += 32) z += weight[i];
             z = warp_sum(z) + kept + mid;
-            const double want = ceil((double)tp * (double)z);
-            const u64 goal = want >= 1.0 ? (u64)want : 1ull;
+            const u64 want = share_up(fmaxf(tp, 0.f), z), goal = want ? want : 1ull;
             u64 run = kept;
+#pragma unroll 1
             for (unsigned i0 = 0; i0 < stay; i0 += 32) {
               u64 inc = i0 + lane < stay ? weight[i0 + lane] : 0ull;
 #pragma unroll
@@ -820,8 +854,8 @@ __global__ void __launch_bounds__(THREADS) sample_kernel(const SampleArgs a) {
       last = end;
       if (by_k && upto(end, false) >= (u64)tk) last = border(false, tk, end);
       if (by_p) {
-        const double want = ceil((double)tp * (double)upto(last, true));
-        last = border(true, want >= 1.0 ? (u64)want : 1ull, last);
+        const u64 want = share_up(fmaxf(tp, 0.f), upto(last, true));
+        last = border(true, want ? want : 1ull, last);
       }
     }
   }
@@ -852,7 +886,7 @@ __global__ void __launch_bounds__(THREADS) sample_kernel(const SampleArgs a) {
     const u64 total = __shfl_sync(FULL, inc, 31);
     float u = __ldcg(a.u + row);
     u = u > 0.0f ? u : 0.0f;
-    u64 goal = u < 1.0f ? (u64)((double)u * (double)total) : total;
+    u64 goal = u < 1.0f ? share_down(u, total) : total;
     goal = goal < total ? goal : total - 1;
     u64 run = inc - sum;
     for (int j = 0; j < PER; ++j) {
@@ -870,8 +904,10 @@ __global__ void __launch_bounds__(THREADS) sample_kernel(const SampleArgs a) {
   // (The part's sum was rounded lane by lane: should the goal lie past what its tokens come
   // to here, the second turn takes the last of them.)
   u64 run = 0, want = goal;
+#pragma unroll 1
   for (int turn = 0; turn < 2; ++turn) {
     run = 0;
+#pragma unroll 1
     for (int i0 = begin; i0 < end && run <= want; i0 += THREADS) {
       const int i = i0 + threadIdx.x;
       const float l = i < end ? clean(__ldcg(x + i)) : -INFINITY;
@@ -883,7 +919,7 @@ __global__ void __launch_bounds__(THREADS) sample_kernel(const SampleArgs a) {
         if (a.prob) {
           float small;
           const float big = w.parts(l, small);
-          a.prob[row] = (float)(((double)big + (double)big * small) * (double)(1ull << ONE) / (double)total);
+          a.prob[row] = __fdiv_rn(__fmul_rn(__fmaf_rn(big, small, big), (float)(1ull << ONE)), __ull2float_rn(total));
         }
       }
       run += all;
@@ -893,7 +929,7 @@ __global__ void __launch_bounds__(THREADS) sample_kernel(const SampleArgs a) {
   }
   if (run == 0 && threadIdx.x == 0) {  // nothing but weights that single tokens round to 0: the first
     a.idx[row] = (int)(first & 0xFFFFFFFFu);
-    if (a.prob) a.prob[row] = (float)((double)(1ull << ONE) / (double)total);
+    if (a.prob) a.prob[row] = __fdiv_rn((float)(1ull << ONE), __ull2float_rn(total));
   }
 }
 
