@@ -34,9 +34,10 @@ extern "C" {
  *   prob         optional f32 [M]: e_idx over that sum
  * A logit of NaN counts as -inf (never drawn), +inf as the largest f32; a row
  * without any other gets idx -1, prob 0.  The e are formed to 2^-29 relatively
- * and summed as whole numbers of 2^-39: the result does not depend on any order, and
- * differs from the exact one only where u or top_p lies within about 2^-28 of a
- * border between tokens.
+ * and summed to about 2^-37 of the largest: the token differs from the exact one only
+ * where u or top_p lies within about 2^-28 of a border between tokens (min_p within
+ * 2^-29 of a token's e).  The same call gives the same bits; the same row among others
+ * (M, or another alignment of its logits) the same token but for such borders.
  *   u    f32 [M], >= 0 (below 0 or NaN: 0);  idx int32 [M]
  * What is written must not overlap what is read (LK_ERR_ARG).
  */

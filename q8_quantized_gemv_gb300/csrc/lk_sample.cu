@@ -952,34 +952,44 @@ extern "C" lk_status lk_sample(const float* logits, int M, int N, const float* t
   const DeviceInfo* d = device_info(nullptr);
   int dev = 0;
   if (!d || cudaGetDevice(&dev) != cudaSuccess) return LK_ERR_CUDA;
-  static std::atomic<int> done[kMaxDevices];
-  if (!done[dev].load(std::memory_order_acquire)) {
-    if (cudaFuncSetAttribute(sample_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             (int)(sizeof(Shared) + NW * kHeld * 4)) !=
-        cudaSuccess)
-      return LK_ERR_CUDA;
-    carveout_max_shared(sample_kernel);
-    done[dev].store(1, std::memory_order_release);
-  }
-  // blocks of a row: as many as the SMs take at once, none with less than 2048 tokens
-  int C = 1;
-  while (C < MAX_C && M * C * 2 <= d->sm_count && N >= C * 4096) C *= 2;
-  const int parts = C * NW;
-  const int part = ((N + 3 + parts - 1) / parts + 127) & ~127, held = part < kHeld ? part : kHeld;
-  const size_t smem = sizeof(Shared) + (size_t)NW * held * 4;
-  const SampleArgs a = {logits, N, part, held, temperature, top_k, top_p, min_p, u, idx, prob};
   cudaLaunchConfig_t lc = {};
-  lc.gridDim = dim3(M * C);
   lc.blockDim = dim3(THREADS);
-  lc.dynamicSmemBytes = smem;
   lc.stream = stream;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = C;
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   lc.attrs = attr;
+  lc.numAttrs = 1;
+  constexpr size_t kMost = sizeof(Shared) + (size_t)NW * kHeld * 4;
+  // once a device: how many clusters of 2, 4 and 8 blocks it takes at once
+  static std::atomic<int> clusters[kMaxDevices];  // 10 bits each
+  int fits = clusters[dev].load(std::memory_order_acquire);
+  if (!fits) {
+    if (cudaFuncSetAttribute(sample_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMost) != cudaSuccess)
+      return LK_ERR_CUDA;
+    carveout_max_shared(sample_kernel);
+    lc.dynamicSmemBytes = kMost;
+    for (int i = 0; i < 3; ++i) {
+      int n = 0;
+      attr[0].val.clusterDim.x = 2u << i;
+      lc.gridDim = dim3(2u << i);
+      if (cudaOccupancyMaxActiveClusters(&n, sample_kernel, &lc) != cudaSuccess) return LK_ERR_CUDA;
+      fits |= (n < 1023 ? n : 1023) << (10 * i);
+    }
+    if (!fits) return LK_ERR_CUDA;
+    clusters[dev].store(fits, std::memory_order_release);
+  }
+  // blocks of a row: as many as are on the SMs at once with all rows', none with less than 2048 tokens
+  int C = 1;
+  for (int i = 0; i < 3 && M <= ((fits >> (10 * i)) & 1023) && N >= C * 4096; ++i) C *= 2;
+  const int parts = C * NW;
+  const int part = ((N + 3 + parts - 1) / parts + 127) & ~127, held = part < kHeld ? part : kHeld;
+  const SampleArgs a = {logits, N, part, held, temperature, top_k, top_p, min_p, u, idx, prob};
+  lc.gridDim = dim3(M * C);
+  lc.dynamicSmemBytes = sizeof(Shared) + (size_t)NW * held * 4;
+  attr[0].val.clusterDim.x = C;
   lc.numAttrs = cfg_pdl(cfg) ? 2 : 1;
   return cudaLaunchKernelEx(&lc, sample_kernel, a) == cudaSuccess ? LK_OK : LK_ERR_CUDA;
 }

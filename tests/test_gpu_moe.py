@@ -346,6 +346,45 @@ def test_two_streams_at_once(lk):
         assert not bool(s["cnt"].any())
 
 
+@pytest.mark.parametrize("mode", ["dequant", "int8act", "twopass"])
+def test_no_experts_at_all(lk, mode):
+    """Every pair absent: the products' rows stay, the sums are zeros."""
+    M, E, k, F, K, m = 5, 4, 3, 128, 256, lk.MODES[mode]
+    ex = lk.Experts(gate=experts(E, F, K, 1, DEV), up=experts(E, F, K, 2, DEV), down=experts(E, K, F, 3, DEV))
+    ids = torch.tensor([-1, E, 2 ** 31 - 1, -2 ** 31, 1023] * k, dtype=torch.int32, device=DEV).view(M, k)
+    acts, hidden = acts_of(x_rows(M, K, 1), m), as_h(acts_of(x_rows(M * k, F, 2), m))
+    for path in ((0, 2) if mode == "dequant" else (0, 2, 3)):
+        h, y = torch.full((M * k, F), 7.0, device=DEV), torch.full((M, K), math.nan, device=DEV)
+        cfg = lk.launch_cfg(path=path)
+        lk.lk_moe_glu_q8(ex, m, ids, h, cfg=cfg, **acts)
+        lk.lk_moe_down_q8(ex, m, ids, torch.ones((M, k), device=DEV), y, cfg=cfg, **hidden)
+        assert bool((h == 7).all()) and bool((y == 0).all())
+
+
+def test_stack_past_32_bits(lk):
+    """Matrices that begin more than 2^32 bytes into their stacks."""
+    E, F, K, k = 300, 4096, 4096, 2
+    dev = torch.device(DEV)
+    q = torch.zeros((E, F, K), dtype=torch.int8, device=dev)
+    s = torch.zeros((E, F, K // 32), dtype=torch.float16, device=dev)
+    for e in (3, E - 1):
+        for t, r in zip((q, s), experts(1, F, K, e, DEV)):
+            t[e] = r[0]
+    assert (E - 1) * F * K > 2 ** 32
+    ex = lk.Experts(gate=(q, s), up=(q, s), down=(q, s))
+    for M, path in ((1, 2), (3, 3)):
+        ids = torch.tensor([[E - 1, 3]] * M, dtype=torch.int32, device=DEV)
+        acts, cfg = quantize(x_rows(M, K, 5), lk.LK_INT8ACT), lk.launch_cfg(path=path)
+        h, y = torch.zeros((M * k, F), device=DEV), torch.zeros((M, F), device=DEV)
+        lk.lk_moe_glu_q8(ex, "int8act", ids, h, cfg=cfg, **acts)
+        want, tol = glu_ref((q, s), (q, s), acts, lk.LK_INT8ACT, ids, E)
+        assert bool(((h.double() - want).abs() <= tol).all())
+        hidden, w = quantize(x_rows(M * k, K, 6), lk.LK_INT8ACT), torch.ones((M, k), device=DEV)
+        lk.lk_moe_down_q8(ex, "int8act", ids, w, y, cfg=cfg, **as_h(hidden))
+        want, tol = down_ref((q, s), hidden, lk.LK_INT8ACT, ids, w, E)
+        assert bool(((y.double() - want).abs() <= tol).all())
+
+
 def test_limits(lk):
     """The largest activation that the header promises, and one past it."""
     e = lk.Experts(gate=experts(1, 128, 32768, 1, DEV), up=experts(1, 128, 32768, 2, DEV),

@@ -176,6 +176,67 @@ def test_shares(lk):
     assert np.all(np.abs(count - n * p) <= 1 + 1e-6)
 
 
+@pytest.mark.parametrize("M", [1, 9, 17, 19, 33, 40])
+def test_rows_of_any_alignment(lk, M):
+    """Row counts that take clusters of every size, rows that begin at any
+    multiple of 4 bytes, and tokens masked with -inf and the type's lowest value."""
+    N = 20001
+    r = np.random.default_rng(M)
+    flat = np.concatenate([np.float32([7]), vocab(1, M * N, M)[0]])
+    flat[r.integers(0, flat.size, flat.size // 4)] = -np.inf
+    flat[r.integers(0, flat.size, flat.size // 8)] = np.finfo(np.float32).min
+    u = r.random(M).astype(np.float32)
+    for shift in (0, 1):
+        logits = flat[shift:shift + M * N].reshape(M, N)
+        x = torch.from_numpy(flat).to(DEV)[shift:shift + M * N].view(M, N)
+        idx, tp = torch.zeros((M,), dtype=torch.int32, device=DEV), torch.full((M,), 0.9, device=DEV)
+        lk.lk_sample(x, torch.from_numpy(u).to(DEV), idx, top_p=tp)
+        near = 0
+        for t in range(M):
+            i, _, margin = sample_ref(logits[t], 1.0, 0, float(np.float32(0.9)), 0.0, float(u[t]))
+            near += margin < NEAR
+            assert margin < NEAR or int(idx[t]) == i
+        assert near <= 1
+
+
+def test_largest_row(lk):
+    """As many logits as a row may have, and tokens a bin too many to count."""
+    N = 1 << 21
+    x = torch.full((2, N), -2.0, device=DEV)
+    x[0, 5::7] = 1.0
+    x[1, 11] = 30.0
+    x[1, N - 1] = 30.0
+    idx, prob = torch.zeros((2,), dtype=torch.int32, device=DEV), torch.zeros((2,), device=DEV)
+    u = torch.tensor([0.5, 0.75], device=DEV)
+    lk.lk_sample(x, u, idx, prob=prob, top_k=torch.tensor([100000, 0], dtype=torch.int32, device=DEV),
+                 top_p=torch.tensor([0.5, 0.9], device=DEV))
+    # row 0: the first 100000 of the equal largest, of these 50000, of these the one at half
+    assert idx.tolist() == [5 + 7 * 25000, N - 1]
+    assert abs(float(prob[0]) * 50000 - 1) < 2.0 ** -22 and abs(float(prob[1]) * 2 - 1) < 2.0 ** -22
+    with pytest.raises(lk.LkError) as err:
+        lk.lk_sample(torch.zeros((1, N + 1), device=DEV), u[:1], idx[:1])
+    assert err.value.status == -3
+
+
+def test_two_streams_at_once(lk):
+    M, N = 12, 30011
+    sets = [(torch.from_numpy(vocab(M, N, s)).to(DEV), torch.rand((M,), device=DEV), torch.zeros((M,), dtype=torch.int32, device=DEV))
+            for s in range(2)]
+    tk = torch.full((M,), 80, dtype=torch.int32, device=DEV)
+    want = []
+    for x, u, idx in sets:
+        lk.lk_sample(x, u, idx, top_k=tk)
+        want.append(idx.clone())
+        idx.zero_()
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in sets]
+    for _ in range(20):
+        for st, (x, u, idx) in zip(streams, sets):
+            lk.lk_sample(x, u, idx, top_k=tk, stream=st)
+    torch.cuda.synchronize()
+    assert all(torch.equal(idx, w) for (_, _, idx), w in zip(sets, want))
+
+
 def test_captured(lk):
     """A captured call behind the launch that writes its logits, dependent, its
     inputs changed between replays; the same bits as a call alone."""
