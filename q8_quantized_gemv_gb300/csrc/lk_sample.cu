@@ -173,6 +173,7 @@ __device__ __forceinline__ float value_of(u64 key) {
 struct SampleArgs {
   const float* logits;
   int N;
+  int C;     // blocks of a row
   int part;  // tokens of a warp's part of a row, a multiple of 128
   int held;  // of these, in shared memory
   const float* T;
@@ -184,15 +185,29 @@ struct SampleArgs {
   float* prob;
 };
 
-constexpr int NW = 32;             // warps of a block
-constexpr int THREADS = 32 * NW;
 constexpr int MAX_C = 8;           // blocks of a row at most
-constexpr int kHeld = 1024;        // tokens of a warp's part in shared memory at most
-constexpr int NB = 2048;           // bins of the order
 constexpr int CAP = 4096;          // tokens near the borders that are sorted
-constexpr float SLACK = 6e-4f;     // of the bins' estimated sums
-constexpr int PLACES = 16;         // places in a bin
-constexpr int POS_BITS = 18;       // a bin's word: the sum of its tokens' places, above it their number
+constexpr int HELD = 32768;        // tokens of a block in shared memory at most
+
+__device__ __forceinline__ u64 warp_sum(u64 v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(FULL, v, o);
+  return v;
+}
+
+// A row's blocks, of NW warps each.  Few tokens go with few warps: most of what a block
+// runs through is run through by all of its warps, whatever they have to do.
+template <int NW>
+struct Rows {
+static constexpr int THREADS = 32 * NW;
+static constexpr int NB = 64 * NW;                  // bins of the order
+static constexpr int PLACES = 32768 / NB;           // places in a bin
+static constexpr int POS_BITS = NW == 32 ? 18 : NW == 16 ? 19 : 20;  // a bin's word: the sum of its tokens' places, above it
+                                                    // their number, below 2^(32 - POS_BITS)
+// Of the bins' estimated sums.  A bin's sum of weights is estimated from its tokens' mean
+// place: within (ln2 * width)^2 / 8 of it (width 41 / NB at most: 2.4e-5, 1e-4 or 3.9e-4), half a
+// place's rounding (4.4e-4) and the f32 sums.
+static constexpr float SLACK = NW == 8 ? 1e-3f : 6e-4f;
 
 struct alignas(16) Shared {
   float2 table[TAB * 32];
@@ -222,15 +237,10 @@ struct alignas(16) Shared {
 };
 
 // (the tokens held lie behind it, read and written by 16 bytes)
-static_assert(sizeof(Shared) % 16 == 0 && sizeof(Shared) + NW * kHeld * 4 <= 227 * 1024, "shared memory");
+static_assert(sizeof(Shared) % 16 == 0 && sizeof(Shared) + HELD * 4 <= 227 * 1024, "shared memory");
 
-__device__ __forceinline__ u64 warp_sum(u64 v) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(FULL, v, o);
-  return v;
-}
 // Sum over the block, in every thread.
-__device__ u64 block_sum(u64 v, Shared& s) {
+static __device__ u64 block_sum(u64 v, Shared& s) {
   v = warp_sum(v);
   __syncthreads();
   if ((threadIdx.x & 31) == 0) s.warp[threadIdx.x >> 5] = v;
@@ -238,7 +248,7 @@ __device__ u64 block_sum(u64 v, Shared& s) {
   return warp_sum((threadIdx.x & 31) < NW ? s.warp[threadIdx.x & 31] : 0ull);
 }
 // Sum of the values of the threads before this one; `all` gets the block's.
-__device__ u64 block_before(u64 v, u64& all, Shared& s) {
+static __device__ u64 block_before(u64 v, u64& all, Shared& s) {
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   u64 inc = v;
 #pragma unroll
@@ -253,7 +263,7 @@ __device__ u64 block_before(u64 v, u64& all, Shared& s) {
   all = warp_sum(tot);
   return warp_sum(lane < w ? tot : 0ull) + inc - v;
 }
-__device__ float block_before(float v, float& all, Shared& s) {
+static __device__ float block_before(float v, float& all, Shared& s) {
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   float inc = v;
 #pragma unroll
@@ -276,7 +286,7 @@ __device__ float block_before(float v, float& all, Shared& s) {
 }
 
 // Sum of the values of the threads behind this one.
-__device__ float block_after(float v, Shared& s) {
+static __device__ float block_after(float v, Shared& s) {
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   float inc = v;
 #pragma unroll
@@ -366,8 +376,7 @@ struct Part {
   }
 };
 
-__global__ void __launch_bounds__(THREADS) sample_kernel(const SampleArgs a) {
-  extern __shared__ __align__(128) unsigned char smem[];
+static __device__ __forceinline__ void run(const SampleArgs& a, unsigned char* smem) {
   Shared& s = *(Shared*)smem;
   cg::cluster_group cl = cg::this_cluster();
   const int C = (int)cl.num_blocks(), me = (int)cl.block_rank();
@@ -377,9 +386,10 @@ __global__ void __launch_bounds__(THREADS) sample_kernel(const SampleArgs a) {
     asm volatile("griddepcontrol.launch_dependents;" :::);
   }
   // (the table's entries are under way while the row is read)
-  static_assert(TAB * 32 == 2 * THREADS, "two entries a thread");
-  const float2 entry[2] = {make_float2(kExp2.hi[threadIdx.x / 32], kExp2.lo[threadIdx.x / 32]),
-                           make_float2(kExp2.hi[TAB / 2 + threadIdx.x / 32], kExp2.lo[TAB / 2 + threadIdx.x / 32])};
+  constexpr int ENTRIES = TAB / NW;  // of a warp
+  float2 entry[ENTRIES];
+#pragma unroll
+  for (int j = 0; j < ENTRIES; ++j) entry[j] = make_float2(kExp2.hi[j * NW + warp], kExp2.lo[j * NW + warp]);
   for (int i = threadIdx.x; i < NB; i += THREADS) s.bin[i] = 0;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const long row = blockIdx.x / C;
@@ -409,8 +419,8 @@ __global__ void __launch_bounds__(THREADS) sample_kernel(const SampleArgs a) {
       low = l > -INFINITY ? fminf(low, l) : low;
     });
     if (top > -INFINITY) first = key_of(top, at);
-    s.table[threadIdx.x] = entry[0];
-    s.table[THREADS + threadIdx.x] = entry[1];
+#pragma unroll
+    for (int j = 0; j < ENTRIES; ++j) s.table[THREADS * j + threadIdx.x] = entry[j];
     first = ~warp_max_u64(~first);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) low = fminf(low, __shfl_xor_sync(FULL, low, o));
@@ -586,9 +596,6 @@ __global__ void __launch_bounds__(THREADS) sample_kernel(const SampleArgs a) {
       full = n_all != expected;
       if (by_p) {
         // ---- the bins of the top_p border ----
-        // A bin's sum of weights is estimated from its tokens' mean place: within
-        // (ln2 * width)^2 / 8 of it, width at most 41 / 2047, half a place's rounding
-        // (4.4e-4) and the f32 sums: SLACK covers them.
         float v[PER], sum = 0.f;
         const float step = reach / (NB - 1);
         for (int j = 0; j < PER; ++j) {
@@ -933,6 +940,73 @@ __global__ void __launch_bounds__(THREADS) sample_kernel(const SampleArgs a) {
   }
 }
 
+};
+
+template <int NW>
+__global__ void __launch_bounds__(32 * NW) sample_kernel(const SampleArgs a) {
+  extern __shared__ __align__(128) unsigned char smem[];
+  Rows<NW>::run(a, smem);
+}
+
+constexpr int LARGE = 32768, SMALL = 6144;  // tokens of a block above which it has 32 (16) warps
+
+template <int NW>
+lk_status launch_rows(SampleArgs a, int M, int dev, int pdl, cudaStream_t stream) {
+  typedef Rows<NW> R;
+  cudaLaunchConfig_t lc = {};
+  lc.blockDim = dim3(R::THREADS);
+  lc.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  lc.attrs = attr;
+  lc.numAttrs = pdl ? 2 : 1;
+  static std::atomic<int> done[kMaxDevices];
+  if (!done[dev].load(std::memory_order_acquire)) {
+    if (cudaFuncSetAttribute(sample_kernel<NW>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             (int)(sizeof(typename R::Shared) + HELD * 4)) != cudaSuccess)
+      return LK_ERR_CUDA;
+    carveout_max_shared(sample_kernel<NW>);
+    done[dev].store(1, std::memory_order_release);
+  }
+  const int parts = a.C * NW;
+  a.part = ((a.N + 3 + parts - 1) / parts + 127) & ~127;
+  a.held = a.part < HELD / NW ? a.part : HELD / NW;
+  lc.gridDim = dim3(M * a.C);
+  lc.dynamicSmemBytes = sizeof(typename R::Shared) + (size_t)NW * a.held * 4;
+  attr[0].val.clusterDim.x = a.C;
+  return cudaLaunchKernelEx(&lc, sample_kernel<NW>, a) == cudaSuccess ? LK_OK : LK_ERR_CUDA;
+}
+
+// Clusters of 2, 4 and 8 blocks that the device takes at once, 10 bits each (0: an error).
+int clusters_at_once(int dev) {
+  static std::atomic<int> known[kMaxDevices];
+  int fits = known[dev].load(std::memory_order_acquire);
+  if (fits) return fits;
+  typedef Rows<32> R;
+  const size_t most = sizeof(typename R::Shared) + HELD * 4;
+  if (cudaFuncSetAttribute(sample_kernel<32>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most) != cudaSuccess) return 0;
+  cudaLaunchConfig_t lc = {};
+  lc.blockDim = dim3(R::THREADS);
+  lc.dynamicSmemBytes = most;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  lc.attrs = attr;
+  lc.numAttrs = 1;
+  for (int i = 0; i < 3; ++i) {
+    int n = 0;
+    attr[0].val.clusterDim.x = 2u << i;
+    lc.gridDim = dim3(2u << i);
+    if (cudaOccupancyMaxActiveClusters(&n, sample_kernel<32>, &lc) != cudaSuccess) return 0;
+    fits |= (n < 1023 ? n : 1023) << (10 * i);
+  }
+  known[dev].store(fits, std::memory_order_release);
+  return fits;
+}
+
 }  // namespace
 
 extern "C" lk_status lk_sample(const float* logits, int M, int N, const float* temperature, const int32_t* top_k,
@@ -949,47 +1023,16 @@ extern "C" lk_status lk_sample(const float* logits, int M, int N, const float* t
   const Span spans[] = {{idx, r},   {prob, r},  {logits, (size_t)M * N * 4}, {temperature, r},
                         {top_k, r}, {top_p, r}, {min_p, r},                  {u, r}};
   if (spans_clash(spans, 2, 8)) return LK_ERR_ARG;
-  const DeviceInfo* d = device_info(nullptr);
   int dev = 0;
-  if (!d || cudaGetDevice(&dev) != cudaSuccess) return LK_ERR_CUDA;
-  cudaLaunchConfig_t lc = {};
-  lc.blockDim = dim3(THREADS);
-  lc.stream = stream;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[1].val.programmaticStreamSerializationAllowed = 1;
-  lc.attrs = attr;
-  lc.numAttrs = 1;
-  constexpr size_t kMost = sizeof(Shared) + (size_t)NW * kHeld * 4;
-  // once a device: how many clusters of 2, 4 and 8 blocks it takes at once
-  static std::atomic<int> clusters[kMaxDevices];  // 10 bits each
-  int fits = clusters[dev].load(std::memory_order_acquire);
-  if (!fits) {
-    if (cudaFuncSetAttribute(sample_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMost) != cudaSuccess)
-      return LK_ERR_CUDA;
-    carveout_max_shared(sample_kernel);
-    lc.dynamicSmemBytes = kMost;
-    for (int i = 0; i < 3; ++i) {
-      int n = 0;
-      attr[0].val.clusterDim.x = 2u << i;
-      lc.gridDim = dim3(2u << i);
-      if (cudaOccupancyMaxActiveClusters(&n, sample_kernel, &lc) != cudaSuccess) return LK_ERR_CUDA;
-      fits |= (n < 1023 ? n : 1023) << (10 * i);
-    }
-    if (!fits) return LK_ERR_CUDA;
-    clusters[dev].store(fits, std::memory_order_release);
-  }
+  if (!device_info(&dev)) return LK_ERR_CUDA;
+  const int fits = clusters_at_once(dev);
+  if (!fits) return LK_ERR_CUDA;
   // blocks of a row: as many as are on the SMs at once with all rows', none with less than 2048 tokens
   int C = 1;
   for (int i = 0; i < 3 && M <= ((fits >> (10 * i)) & 1023) && N >= C * 4096; ++i) C *= 2;
-  const int parts = C * NW;
-  const int part = ((N + 3 + parts - 1) / parts + 127) & ~127, held = part < kHeld ? part : kHeld;
-  const SampleArgs a = {logits, N, part, held, temperature, top_k, top_p, min_p, u, idx, prob};
-  lc.gridDim = dim3(M * C);
-  lc.dynamicSmemBytes = sizeof(Shared) + (size_t)NW * held * 4;
-  attr[0].val.clusterDim.x = C;
-  lc.numAttrs = cfg_pdl(cfg) ? 2 : 1;
-  return cudaLaunchKernelEx(&lc, sample_kernel, a) == cudaSuccess ? LK_OK : LK_ERR_CUDA;
+  const SampleArgs a = {logits, N, C, 0, 0, temperature, top_k, top_p, min_p, u, idx, prob};
+  const int pdl = cfg_pdl(cfg), tokens = N / C;
+  return tokens > LARGE   ? launch_rows<32>(a, M, dev, pdl, stream)
+         : tokens > SMALL ? launch_rows<16>(a, M, dev, pdl, stream)
+                          : launch_rows<8>(a, M, dev, pdl, stream);
 }
