@@ -380,6 +380,11 @@ static __device__ __forceinline__ void run(const SampleArgs& a, unsigned char* s
   Shared& s = *(Shared*)smem;
   cg::cluster_group cl = cg::this_cluster();
   const int C = (int)cl.num_blocks(), me = (int)cl.block_rank();
+  // all threads of the row's blocks
+  auto meet = [&] {
+    if (C == 1) __syncthreads();
+    else cl.sync();
+  };
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   if (threadIdx.x == 0) {
     s.listed = 0;
@@ -441,7 +446,7 @@ static __device__ __forceinline__ void run(const SampleArgs& a, unsigned char* s
       }
     }
   }
-  cl.sync();
+  meet();
   u64 first = ~0ull;
   float low = INFINITY;
   for (int c = 0; c < C; ++c) {
@@ -511,7 +516,7 @@ static __device__ __forceinline__ void run(const SampleArgs& a, unsigned char* s
         binned = (unsigned)block_sum(binned, s);
         if (threadIdx.x < C) cl.map_shared_rank(&s, threadIdx.x)->n_bin[me] = binned;
       }
-      cl.sync();
+      meet();
       const int per = NB / C;
       for (int i = threadIdx.x; i < per; i += THREADS) {
         const int b = me * per + i;
@@ -531,7 +536,7 @@ static __device__ __forceinline__ void run(const SampleArgs& a, unsigned char* s
             to->all.pos[b] = p;
           }
       }
-      cl.sync();
+      meet();
     };
     constexpr int PER = NB / THREADS;
     const int b0 = threadIdx.x * PER;
@@ -575,7 +580,7 @@ static __device__ __forceinline__ void run(const SampleArgs& a, unsigned char* s
       if (bk == NB) {  // too few lanes have any within reach
         few = false;
         for (int i = threadIdx.x; i < NB; i += THREADS) s.bin[i] = 0;
-        cl.sync();
+        meet();
       }
     }
     if (!few) {
@@ -720,7 +725,7 @@ static __device__ __forceinline__ void run(const SampleArgs& a, unsigned char* s
       to->kept[me] = kept;
       to->mid[me] = mid;
     }
-    cl.sync();
+    meet();
     unsigned listed = 0;
     for (int q = 0; q < C; ++q) listed += s.n_list[q];
     if (listed <= CAP && !full) {
@@ -839,7 +844,7 @@ static __device__ __forceinline__ void run(const SampleArgs& a, unsigned char* s
       auto whole = [&](u64 v) {
         v = block_sum(v, s);
         if (threadIdx.x < C) cl.map_shared_rank(&s, threadIdx.x)->sums[turn][me] = v;
-        cl.sync();
+        meet();
         u64 r = 0;
         for (int q = 0; q < C; ++q) r += s.sums[turn][q];
         turn ^= 1;
@@ -872,7 +877,7 @@ static __device__ __forceinline__ void run(const SampleArgs& a, unsigned char* s
     if (lane == 0) cl.map_shared_rank(&s, 0)->drawn[slot] = part;
   }
   // (the last time that blocks look into one another)
-  cl.sync();
+  meet();
   if (me != 0) return;
 
   // ---- the draw: the part in which the running sum passes the goal, then the token ----
