@@ -74,49 +74,90 @@ struct ActLoad {
 #pragma unroll
     for (int u = 0; u < RUNS; ++u) {
       const int i = (b * RUNS + u) * blockDim.x + threadIdx.x;
-      if (i < rows * per) *(uint4*)(act + 16 * (size_t)i) = v[u];
+      if (i < rows * per) *(uint4*)(act + 16 * (size_t)place(i)) = v[u];
     }
+  }
+  // where run i goes: f32 values of a stretch of 256 so that the eight neighbours a lane
+  // takes lie in two runs, each next to those of the lanes beside it
+  __device__ __forceinline__ int place(int i) const {
+    if constexpr (Q != 0) return i;
+    const int r = i / per, c = i - r * per, j = c & 63;
+    return c < (a.K >> 8) * 64 ? i - j + (j & 1) * 32 + (j >> 1) : i;
   }
   __device__ __forceinline__ bool more(int b) const { return b * RUNS * (int)blockDim.x < rows * per; }
 };
 
-// A stage's part of four rows against the activation at `act` (K its whole length).
+// What a lane has of its item's four rows: under Dequant its part of each row, in packed
+// halves; else partial (lane & 7) / 2 of row lane / 8, in the even lanes.
 template <int Q>
-__device__ __forceinline__ void quad_stage(typename part_t<Q>::t& p, const unsigned char* st, const MoeArgs& a, int k0,
-                                           int len, const unsigned (&sh)[2], const unsigned char* act, int lane) {
-  const int nseg = len >> 7;
+struct Partial {
+  float p;
+  __device__ __forceinline__ void clear() { p = 0.f; }
+};
+template <>
+struct Partial<0> {
+  f32x2 p[QR];
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int r = 0; r < QR; ++r) p[r] = f2_pack(0.f, 0.f);
+  }
+};
+
+// Four levels (u = their bytes ^ 0x80) as f32 pairs.
+__device__ __forceinline__ void levels4(unsigned u, f32x2& w01, f32x2& w23) {
+  const f32x2 neg = f2_pack(-8388736.0f, -8388736.0f);  // 2^23 + 128, as in i8_as_f32
+  w01 = f2_add(f2_pack(i8_bits_f32(u, 0), i8_bits_f32(u, 1)), neg);
+  w23 = f2_add(f2_pack(i8_bits_f32(u, 2), i8_bits_f32(u, 3)), neg);
+}
+
+// A stage's part of four rows against the activation at `act` (K its whole length).
+// Dequant: lane l has values 8l .. 8l + 7 of a stretch of 256, of one block, of all four rows
+// (4l .. 4l + 3 of a last 128); the stage's sums are added to the item's, so a row of K
+// values has K / 256 + slices + 15 roundings at most in a chain, all in f32: within
+// 5e-6 of sum |w x| up to K 16384.
+template <int Q>
+__device__ __forceinline__ void quad_stage(Partial<Q>& p, const unsigned char* st, const MoeArgs& a, int k0, int len,
+                                           const unsigned (&sh)[2], const unsigned char* act, int lane) {
   if constexpr (Q == 0) {
-    // lane l has values 4l .. 4l + 3 of a segment, of all four rows (as the ring kernel)
     const float* X = (const float*)act + k0 + 4 * lane;
-    const unsigned char* W = st + 4 * lane;
-    const unsigned char* S = st + a.s_off + 2 * (lane >> 3);
-    const f32x2 neg = f2_pack(-8388736.0f, -8388736.0f);
+    const unsigned char* S = st + a.s_off;
     f32x2 acc[QR];
 #pragma unroll
     for (int r = 0; r < QR; ++r) acc[r] = f2_pack(0.f, 0.f);
-#pragma unroll 4
-    for (int seg = 0; seg < nseg; ++seg) {
-      const float4 xx = *(const float4*)(X + 128 * seg);
-      const f32x2 x01 = f2_pack(xx.x, xx.y), x23 = f2_pack(xx.z, xx.w);
+    const int n = len >> 8;
+#pragma unroll 2
+    for (int s = 0; s < n; ++s) {
+      const float4 xa = *(const float4*)(X + 256 * s), xb = *(const float4*)(X + 256 * s + 128);
 #pragma unroll
       for (int r = 0; r < QR; ++r) {
-        const unsigned u = *(const unsigned*)(W + r * a.tk + 128 * seg) ^ 0x80808080u;
-        const float ws = __half2float(*(const __half*)(S + r * a.srow + sh[r & 1] + 8 * seg));
-        const f32x2 w01 = f2_add(f2_pack(i8_bits_f32(u, 0), i8_bits_f32(u, 1)), neg);
-        const f32x2 w23 = f2_add(f2_pack(i8_bits_f32(u, 2), i8_bits_f32(u, 3)), neg);
-        acc[r] = f2_fma(f2_pack(ws, ws), f2_fma(w23, x23, f2_mul(w01, x01)), acc[r]);
+        const uint2 u = *(const uint2*)(st + r * a.tk + 256 * s + 8 * lane);
+        const float ws = __half2float(*(const __half*)(S + r * a.srow + sh[r & 1] + 16 * s + 2 * (lane >> 2)));
+        f32x2 w0, w1, w2, w3;
+        levels4(u.x ^ 0x80808080u, w0, w1);
+        levels4(u.y ^ 0x80808080u, w2, w3);
+        f32x2 d = f2_mul(w0, f2_pack(xa.x, xa.y));
+        d = f2_fma(w1, f2_pack(xa.z, xa.w), d);
+        d = f2_fma(w2, f2_pack(xb.x, xb.y), d);
+        d = f2_fma(w3, f2_pack(xb.z, xb.w), d);
+        acc[r] = f2_fma(f2_pack(ws, ws), d, acc[r]);
+      }
+    }
+    if (len & 128) {
+      const float4 xx = *(const float4*)(X + 256 * n);
+#pragma unroll
+      for (int r = 0; r < QR; ++r) {
+        const unsigned u = *(const unsigned*)(st + r * a.tk + 256 * n + 4 * lane);
+        const float ws = __half2float(*(const __half*)(S + r * a.srow + sh[r & 1] + 16 * n + 2 * (lane >> 3)));
+        f32x2 w0, w1;
+        levels4(u ^ 0x80808080u, w0, w1);
+        const f32x2 d = f2_fma(w1, f2_pack(xx.z, xx.w), f2_mul(w0, f2_pack(xx.x, xx.y)));
+        acc[r] = f2_fma(f2_pack(ws, ws), d, acc[r]);
       }
     }
 #pragma unroll
-    for (int r = 0; r < QR; ++r) {
-      float a0, a1;
-      f2_unpack(acc[r], a0, a1);
-      float v = __fadd_rn(a0, a1);
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) v = __fadd_rn(v, __shfl_xor_sync(FULL, v, o));
-      if (lane == 8 * r) p = __dadd_rn((double)p, (double)v);
-    }
+    for (int r = 0; r < QR; ++r) p.p[r] = f2_add(p.p[r], acc[r]);
   } else {
+    const int nseg = len >> 7;
     const int rr = lane >> 3, j = lane & 7, q = j >> 1;
     const unsigned char* W = st + rr * a.tk + 16 * j;
     const unsigned char* S = st + a.s_off + rr * a.srow + sh[rr & 1] + 2 * q;
@@ -133,17 +174,35 @@ __device__ __forceinline__ void quad_stage(typename part_t<Q>::t& p, const unsig
         e = dot16(w, *(const int4*)(XQ + a.K + 128 * seg));
         e += __shfl_xor_sync(FULL, e, 1);
       }
-      p = q8_step<Q>((float)p, ws, XS[4 * seg], d, e);
+      p.p = q8_step<Q>(p.p, ws, XS[4 * seg], d, e);
     }
   }
 }
 
-// (p0 + p2) + (p1 + p3) of each row, in lane 8 r for row r.
-template <typename P>
-__device__ __forceinline__ float row_sum(P p) {
-  p = p + __shfl_down_sync(FULL, p, 4);
-  p = p + __shfl_down_sync(FULL, p, 2);
-  return sizeof(P) == 8 ? __double2float_rn((double)p) : (float)p;
+// The product of each row r, in lane 8 r: Dequant the sum over the lanes, else
+// (p0 + p2) + (p1 + p3).
+template <int Q>
+__device__ __forceinline__ float row_sum(const Partial<Q>& p, int lane) {
+  if constexpr (Q == 0) {
+    float v[QR];
+#pragma unroll
+    for (int r = 0; r < QR; ++r) {
+      float lo, hi;
+      f2_unpack(p.p[r], lo, hi);
+      v[r] = __fadd_rn(lo, hi);
+    }
+    // lanes 16 apart take two rows each, lanes 8 apart one of these
+    const bool up = lane & 16, odd = lane & 8;
+    const float a0 = __shfl_xor_sync(FULL, up ? v[0] : v[2], 16), a1 = __shfl_xor_sync(FULL, up ? v[1] : v[3], 16);
+    const float k0 = __fadd_rn(up ? v[2] : v[0], a0), k1 = __fadd_rn(up ? v[3] : v[1], a1);
+    float s = __fadd_rn(odd ? k1 : k0, __shfl_xor_sync(FULL, odd ? k0 : k1, 8));
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1) s = __fadd_rn(s, __shfl_xor_sync(FULL, s, o));
+    return s;
+  } else {
+    float v = p.p + __shfl_down_sync(FULL, p.p, 4);
+    return v + __shfl_down_sync(FULL, v, 2);
+  }
 }
 
 template <int Q, bool GLU>
@@ -192,14 +251,6 @@ __global__ void __launch_bounds__(NW * 32, 1) moe_kernel(const MoeArgs a) {
   const int quads = GLU ? np * per : per;
   const int q0 = (int)((long)quads * blockIdx.x / gridDim.x), q1 = (int)((long)quads * (blockIdx.x + 1) / gridDim.x);
   const int nq = q1 - q0, items = GLU ? nq : nq * np;
-  struct Cursor {
-    int item, c;  // item, slice
-  };
-  auto next = [&](Cursor& s) {
-    if (++s.c < a.nsl) return;
-    s.c = 0;
-    s.item += NW;
-  };
   // an item's pair (of those that are there) and its first output row
   auto place = [&](int item, int& i, int& row) {
     if (GLU) {
@@ -210,12 +261,20 @@ __global__ void __launch_bounds__(NW * 32, 1) moe_kernel(const MoeArgs a) {
       row = 4 * (q0 + item - i * nq);
     }
   };
+  struct Cursor {
+    int item, c;  // item, slice
+    int i, row;   // the item's place
+  };
+  auto next = [&](Cursor& s) {
+    if (++s.c < a.nsl) return;
+    s.c = 0;
+    s.item += NW;
+    if (s.item < items) place(s.item, s.i, s.row);
+  };
   const int nb = a.K >> 5;
   // matrix row r of the quad: its row in the stack
   auto stack_row = [&](const Cursor& s, int r) -> long {
-    int i, row;
-    place(s.item, i, row);
-    return (long)expert_of[i] * a.rows + row + (GLU ? r & 1 : r);
+    return (long)expert_of[s.i] * a.rows + s.row + (GLU ? r & 1 : r);
   };
   auto issue = [&](const Cursor& s, int slot) {
     const int k0 = s.c * a.tk, len = a.K - k0 < a.tk ? a.K - k0 : a.tk;
@@ -236,8 +295,9 @@ __global__ void __launch_bounds__(NW * 32, 1) moe_kernel(const MoeArgs a) {
       bulk(st + a.s_off + r * a.srow, (up ? a.sb : a.sa) + (off & ~15ull), slen, bar, 0);
     __syncwarp();
   };
-  typedef typename part_t<Q>::t P;
-  Cursor head{warp, 0}, at = head;
+  Cursor head{warp, 0, 0, 0};
+  if (warp < items) place(warp, head.i, head.row);
+  Cursor at = head;
   const int total = warp < items ? ((items - 1 - warp) / NW + 1) * a.nsl : 0;
   int issued = 0;
   for (; issued < total && issued < a.depth; ++issued, next(head)) issue(head, issued);
@@ -249,7 +309,8 @@ __global__ void __launch_bounds__(NW * 32, 1) moe_kernel(const MoeArgs a) {
   __syncthreads();
 
   bool ok = true;
-  P p = (P)0;
+  Partial<Q> p;
+  p.clear();
   int n = 0, slot = 0;
   unsigned phase = 0;
   for (; n < total; ++n) {
@@ -264,8 +325,7 @@ __global__ void __launch_bounds__(NW * 32, 1) moe_kernel(const MoeArgs a) {
 #pragma unroll
     for (int r = 0; r < 2; ++r)
       sh[r] = (unsigned)((((unsigned long long)stack_row(at, r) * nb + (k0 >> 5)) * 2) & 15);
-    int i, row;
-    place(at.item, i, row);
+    const int i = at.i, row = at.row;
     quad_stage<Q>(p, st, a, k0, len, sh, smem + (GLU ? 0 : i * act_bytes<Q>(a.K)), lane);
     __syncwarp();
     if (issued < total) {
@@ -275,8 +335,8 @@ __global__ void __launch_bounds__(NW * 32, 1) moe_kernel(const MoeArgs a) {
       ++issued;
     }
     if (at.c == a.nsl - 1) {
-      const float v = row_sum(p);
-      p = (P)0;
+      const float v = row_sum<Q>(p, lane);
+      p.clear();
       if (GLU) {
         const float u = __shfl_down_sync(FULL, v, 16);
         if (lane == 0 || lane == 8) a.out[(t * a.k + pair_of[i]) * a.rows + row + (lane >> 3)] = swiglu(v, u);
@@ -343,7 +403,7 @@ bool fit(MoeArgs& a, int mode, int rows_held, int products, int smem_optin, int*
   const int room = smem_optin - kStatic - (int)a.ring_off;
   int best = 0;
   for (int n = (a.K + SLICE - 1) / SLICE; n <= a.K / 128; ++n) {
-    const int tk = ((a.K + n - 1) / n + 127) & ~127;
+    const int unit = mode == 0 ? 256 : 128, tk = ((a.K + n - 1) / n + unit - 1) & ~(unit - 1);
     const unsigned srow = (tk / 16u + 23u) & ~15u;  // a row's scales and half of 16 bytes, to 16
     const unsigned bytes = (4u * tk + 4u * srow + 127u) & ~127u;
     int depth = room / (int)(NW * bytes);
