@@ -8,6 +8,12 @@
 // rows' arithmetic is lk_gemv_q8's (8 lanes to a row, lane pair b mod 4 with
 // block b's exact dot, (p0 + p2) + (p1 + p3)), so each product has its bits.
 //
+// Stages are few and large: the copy engine starts a bulk copy in 16 to 23 cycles whatever
+// its size, and a warp takes as long again around each stage (gate/up of 8 rows, 4096 x 1024:
+// slices of 512 170 us, 1024 107, 2048 85, whole rows 83).  So rows that are whole in a
+// stage are one copy of neighbouring rows (gate/up two), up to four quads of short
+// rows, and the scales come by the lanes' own asynchronous copies.
+//
 // Gate/up: a quad is the gate rows and the up rows of two neighbouring outputs
 // of one pair, so the warp that has them has what the SwiGLU needs.  A row's
 // pairs lie one after the other, and its blocks share their outputs evenly.  The
@@ -30,7 +36,7 @@ namespace {
 constexpr int NW = 12;             // warps of a block
 constexpr int SLICE = 4096;        // bytes of K in a stage at most
 constexpr int DEPTH = 8;           // stages of a warp at most
-constexpr int kStatic = 2048;      // static shared memory, at most
+constexpr int kStatic = 1536;      // static shared memory, at most
 constexpr int kProducts = 16384;   // down: bytes of a block's products, about
 
 template <int Q>
@@ -110,14 +116,15 @@ __device__ __forceinline__ void levels4(unsigned u, f32x2& w01, f32x2& w23) {
   w23 = f2_add(f2_pack(i8_bits_f32(u, 2), i8_bits_f32(u, 3)), neg);
 }
 
-// A stage's part of four rows against the activation at `act` (K its whole length).
+// A stage's part of four rows against the activation at `act` (K its whole length); row r
+// of the four is row base + (r & 1) + hop * (r >> 1) of the stage.
 // Dequant: lane l has values 8l .. 8l + 7 of a stretch of 256, of one block, of all four rows
 // (4l .. 4l + 3 of a last 128); the stage's sums are added to the item's, so a row of K
 // values has K / 256 + slices + 15 roundings at most in a chain, all in f32: within
 // 5e-6 of sum |w x| up to K 16384.
 template <int Q>
 __device__ __forceinline__ void quad_stage(Partial<Q>& p, const unsigned char* st, const MoeArgs& a, int k0, int len,
-                                           const unsigned (&sh)[2], const unsigned char* act, int lane) {
+                                           int base, int hop, const unsigned char* act, int lane) {
   if constexpr (Q == 0) {
     const float* X = (const float*)act + k0 + 4 * lane;
     const unsigned char* S = st + a.s_off;
@@ -130,8 +137,9 @@ __device__ __forceinline__ void quad_stage(Partial<Q>& p, const unsigned char* s
       const float4 xa = *(const float4*)(X + 256 * s), xb = *(const float4*)(X + 256 * s + 128);
 #pragma unroll
       for (int r = 0; r < QR; ++r) {
-        const uint2 u = *(const uint2*)(st + r * a.tk + 256 * s + 8 * lane);
-        const float ws = __half2float(*(const __half*)(S + r * a.srow + sh[r & 1] + 16 * s + 2 * (lane >> 2)));
+        const int row = base + (r & 1) + hop * (r >> 1);
+        const uint2 u = *(const uint2*)(st + row * a.ld + 256 * s + 8 * lane);
+        const float ws = __half2float(*(const __half*)(S + row * a.srow + 16 * s + 2 * (lane >> 2)));
         f32x2 w0, w1, w2, w3;
         levels4(u.x ^ 0x80808080u, w0, w1);
         levels4(u.y ^ 0x80808080u, w2, w3);
@@ -146,8 +154,9 @@ __device__ __forceinline__ void quad_stage(Partial<Q>& p, const unsigned char* s
       const float4 xx = *(const float4*)(X + 256 * n);
 #pragma unroll
       for (int r = 0; r < QR; ++r) {
-        const unsigned u = *(const unsigned*)(st + r * a.tk + 256 * n + 4 * lane);
-        const float ws = __half2float(*(const __half*)(S + r * a.srow + sh[r & 1] + 16 * n + 2 * (lane >> 3)));
+        const int row = base + (r & 1) + hop * (r >> 1);
+        const unsigned u = *(const unsigned*)(st + row * a.ld + 256 * n + 4 * lane);
+        const float ws = __half2float(*(const __half*)(S + row * a.srow + 16 * n + 2 * (lane >> 3)));
         f32x2 w0, w1;
         levels4(u ^ 0x80808080u, w0, w1);
         const f32x2 d = f2_fma(w1, f2_pack(xx.z, xx.w), f2_mul(w0, f2_pack(xx.x, xx.y)));
@@ -158,9 +167,9 @@ __device__ __forceinline__ void quad_stage(Partial<Q>& p, const unsigned char* s
     for (int r = 0; r < QR; ++r) p.p[r] = f2_add(p.p[r], acc[r]);
   } else {
     const int nseg = len >> 7;
-    const int rr = lane >> 3, j = lane & 7, q = j >> 1;
-    const unsigned char* W = st + rr * a.tk + 16 * j;
-    const unsigned char* S = st + a.s_off + rr * a.srow + sh[rr & 1] + 2 * q;
+    const int rr = lane >> 3, j = lane & 7, q = j >> 1, row = base + (rr & 1) + hop * (rr >> 1);
+    const unsigned char* W = st + row * a.ld + 16 * j;
+    const unsigned char* S = st + a.s_off + row * a.srow + 2 * q;
     const unsigned char* XQ = act + k0 + 16 * j;
     const float* XS = (const float*)(act + (size_t)a.K * Q) + (k0 >> 5) + q;
 #pragma unroll 8
@@ -220,7 +229,7 @@ __global__ void __launch_bounds__(NW * 32, 1) moe_kernel(const MoeArgs a) {
   unsigned char* ring = smem + a.ring_off + (size_t)warp * a.depth * a.stage_bytes;
   const unsigned full0 = smem_u32(bars + warp * DEPTH);
   if (lane == 0)
-    for (int s = 0; s < a.depth; ++s) mbar_init(full0 + 8 * s, 1);
+    for (int s = 0; s < a.depth; ++s) mbar_init(full0 + 8 * s, 33);  // the bulk copies', and each lane's
   if (threadIdx.x == 0) {
     aborted = 0;
     asm volatile("griddepcontrol.launch_dependents;" :::);
@@ -246,57 +255,71 @@ __global__ void __launch_bounds__(NW * 32, 1) moe_kernel(const MoeArgs a) {
   ActLoad<Q> act(a, row_of, GLU ? np > 0 : np);
   act.load(0);
 
-  // this block's quads: gate/up, of all pairs' outputs; down, of its rows of all pairs
+  // this block's quads: gate/up, of all pairs' outputs; down, of its rows of all pairs.  An
+  // item is up to G of them side by side (gate/up: blocks begin at whole items)
+  const int G = a.group;
   const int per = GLU ? a.rows / 2 : a.rows / 4;  // quads of a pair
-  const int quads = GLU ? np * per : per;
-  const int q0 = (int)((long)quads * blockIdx.x / gridDim.x), q1 = (int)((long)quads * (blockIdx.x + 1) / gridDim.x);
-  const int nq = q1 - q0, items = GLU ? nq : nq * np;
-  // an item's pair (of those that are there) and its first output row
-  auto place = [&](int item, int& i, int& row) {
-    if (GLU) {
-      i = (q0 + item) / per;
-      row = 2 * (q0 + item - i * per);
-    } else {
-      i = item / nq;
-      row = 4 * (q0 + item - i * nq);
-    }
-  };
+  const int units = GLU ? np * per / G : per;
+  const int q0 = (int)((long)units * blockIdx.x / gridDim.x) * (GLU ? G : 1);
+  const int q1 = (int)((long)units * (blockIdx.x + 1) / gridDim.x) * (GLU ? G : 1);
+  const int nq = q1 - q0, ipp = (nq + G - 1) / G, items = GLU ? ipp : ipp * np;
   struct Cursor {
-    int item, c;  // item, slice
-    int i, row;   // the item's place
+    int item, c;   // item, slice
+    int i, q, n;   // the item's pair (of those that are there), its first quad (gate/up: of the pair's; down:
+                   // of the block's), its quads
+  };
+  auto place = [&](Cursor& s) {
+    if (GLU) {
+      const int q = q0 + s.item * G;
+      s.i = q / per;
+      s.q = q - s.i * per;
+      s.n = G;
+    } else {
+      s.i = s.item / ipp;
+      s.q = (s.item - s.i * ipp) * G;
+      s.n = min(G, nq - s.q);
+    }
   };
   auto next = [&](Cursor& s) {
     if (++s.c < a.nsl) return;
     s.c = 0;
     s.item += NW;
-    if (s.item < items) place(s.item, s.i, s.row);
+    if (s.item < items) place(s);
   };
-  const int nb = a.K >> 5;
-  // matrix row r of the quad: its row in the stack
-  auto stack_row = [&](const Cursor& s, int r) -> long {
-    return (long)expert_of[s.i] * a.rows + s.row + (GLU ? r & 1 : r);
-  };
+  const int nb = a.K >> 5, odd = (nb >> 2) & 1;  // odd: rows of scales begin at 8 bytes in turn
+  const int hop = GLU ? 2 * G : 2;               // (quad_stage; gate/up: up rows behind the gate rows)
   auto issue = [&](const Cursor& s, int slot) {
     const int k0 = s.c * a.tk, len = a.K - k0 < a.tk ? a.K - k0 : a.tk;
     const unsigned bar = full0 + 8 * slot;
     unsigned char* st = ring + (size_t)slot * a.stage_bytes;
-    const int r = lane & 3;
-    const long row = lane < 8 ? stack_row(s, r) : 0;
-    const bool up = GLU && r >= 2;
-    const unsigned long long off = ((unsigned long long)row * nb + (k0 >> 5)) * 2;
-    const unsigned slen = ((unsigned)len / 16 + (unsigned)(off & 15) + 15u) & ~15u;  // 16-byte superset
-    unsigned mine = lane < 4 ? (unsigned)len : lane < 8 ? slen : 0u;
-    mine = __reduce_add_sync(FULL, mine);
-    if (lane == 0) mbar_arrive_expect_tx(bar, mine);
+    const int rows = 4 * s.n, half = 2 * s.n;  // of the stage; gate/up: of each matrix
+    const long row0 = (long)expert_of[s.i] * a.rows + (GLU ? 2 * s.q : 4 * (q0 + s.q));
+    // row i of the item: its row in the stage
+    auto at = [&](int i) { return GLU && i >= half ? i - half + hop : i; };
+    if (lane == 0) mbar_arrive_expect_tx(bar, (unsigned)rows * len);
     __syncwarp();
-    if (lane < 4)
-      bulk(st + r * a.tk, (up ? a.wb : a.wa) + row * a.K + k0, len, bar, 0);
-    else if (lane < 8)
-      bulk(st + a.s_off + r * a.srow, (up ? a.sb : a.sa) + (off & ~15ull), slen, bar, 0);
+    if (a.nsl == 1) {
+      if (lane < (GLU ? 2 : 1))
+        bulk_g2s_nohint(st + (size_t)lane * hop * a.ld, (lane ? a.wb : a.wa) + row0 * a.K, (GLU ? half : rows) * a.K, bar);
+    } else if (lane < 4) {
+      const bool up = GLU && lane >= 2;
+      bulk_g2s_nohint(st + lane * a.ld, (up ? a.wb : a.wa) + (row0 + (up ? lane - 2 : lane)) * a.K + k0, len, bar);
+    }
+    // the scales, 2 bytes a block, 16 or (where rows begin at 8) 8 at a time
+    const int size = odd || len % 256 ? 8 : 16, per_row = len / 16 / size;
+    for (int c = lane; c < rows * per_row; c += 32) {
+      const int i = c / per_row, off = size * (c - i * per_row);
+      const bool up = GLU && i >= half;
+      const unsigned char* from = (up ? a.sb : a.sa) + ((row0 + (up ? i - half : i)) * nb + (k0 >> 5)) * 2 + off;
+      unsigned char* to = st + a.s_off + at(i) * a.srow + off;
+      if (size == 16) copy16(to, from);
+      else copy8(to, from);
+    }
+    arrive_with_copies(bar);
     __syncwarp();
   };
-  Cursor head{warp, 0, 0, 0};
-  if (warp < items) place(warp, head.i, head.row);
+  Cursor head{warp, 0, 0, 0, 0};
+  if (warp < items) place(head);
   Cursor at = head;
   const int total = warp < items ? ((items - 1 - warp) / NW + 1) * a.nsl : 0;
   int issued = 0;
@@ -321,28 +344,26 @@ __global__ void __launch_bounds__(NW * 32, 1) moe_kernel(const MoeArgs a) {
     }
     const int k0 = at.c * a.tk, len = a.K - k0 < a.tk ? a.K - k0 : a.tk;
     unsigned char* st = ring + (size_t)slot * a.stage_bytes;
-    unsigned sh[2];
-#pragma unroll
-    for (int r = 0; r < 2; ++r)
-      sh[r] = (unsigned)((((unsigned long long)stack_row(at, r) * nb + (k0 >> 5)) * 2) & 15);
-    const int i = at.i, row = at.row;
-    quad_stage<Q>(p, st, a, k0, len, sh, smem + (GLU ? 0 : i * act_bytes<Q>(a.K)), lane);
+    const unsigned char* x = smem + (GLU ? 0 : at.i * act_bytes<Q>(a.K));
+    for (int q = 0; q < at.n; ++q) {
+      quad_stage<Q>(p, st, a, k0, len, (GLU ? 2 : 4) * q, hop, x, lane);
+      if (at.c < a.nsl - 1) break;  // (a slice: one quad, its sums go on)
+      const float v = row_sum<Q>(p, lane);
+      p.clear();
+      if (GLU) {
+        const float u = __shfl_down_sync(FULL, v, 16);
+        if (lane == 0 || lane == 8)
+          a.out[(t * a.k + pair_of[at.i]) * a.rows + 2 * (at.q + q) + (lane >> 3)] = swiglu(v, u);
+      } else if ((lane & 7) == 0) {
+        products[4 * (at.i * nq + at.q + q) + (lane >> 3)] = v;
+      }
+    }
     __syncwarp();
     if (issued < total) {
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       issue(head, slot);
       next(head);
       ++issued;
-    }
-    if (at.c == a.nsl - 1) {
-      const float v = row_sum<Q>(p, lane);
-      p.clear();
-      if (GLU) {
-        const float u = __shfl_down_sync(FULL, v, 16);
-        if (lane == 0 || lane == 8) a.out[(t * a.k + pair_of[i]) * a.rows + row + (lane >> 3)] = swiglu(v, u);
-      } else if ((lane & 7) == 0) {
-        products[4 * at.item + (lane >> 3)] = v;
-      }
     }
     next(at);
     if (++slot == a.depth) {
@@ -392,35 +413,45 @@ __global__ void __launch_bounds__(NW * 32, 1) moe_kernel(const MoeArgs a) {
 
 // ---- host --------------------------------------------------------------------------
 
-// Stages: rows in equal slices of at most SLICE bytes, a multiple of 128, and as
-// many stages a warp as fit; more, shorter slices only where clearly more bytes
-// are in flight with them.
-bool fit(MoeArgs& a, int mode, int rows_held, int products, int smem_optin, int* smem) {
+// Stages: whole rows up to SLICE bytes, else the fewest equal slices, and up to four quads of
+// short rows; `quads` of them come to a warp.  Where these are few, two smaller stages a warp
+// instead of one, so that its copies go on while it computes (8 experts of 1024 x 4096 for one
+// row: 15.0 us against 17.0; 64 pairs: 85 against 83).
+bool fit(MoeArgs& a, int mode, int rows_held, int products, long quads, int smem_optin, int* smem) {
   const unsigned act = mode == 0 ? 4u * a.K : (unsigned)a.K * mode + a.K / 8u;
   if ((unsigned long long)act * rows_held > 200000u) return false;
   a.s_products = act * rows_held;  // (a multiple of 16)
   a.ring_off = (a.s_products + 4u * products + 127u) & ~127u;
   const int room = smem_optin - kStatic - (int)a.ring_off;
-  int best = 0;
+  const int unit = mode == 0 ? 256 : 128;
+  bool found = false;
   for (int n = (a.K + SLICE - 1) / SLICE; n <= a.K / 128; ++n) {
-    const int unit = mode == 0 ? 256 : 128, tk = ((a.K + n - 1) / n + unit - 1) & ~(unit - 1);
-    const unsigned srow = (tk / 16u + 23u) & ~15u;  // a row's scales and half of 16 bytes, to 16
-    const unsigned bytes = (4u * tk + 4u * srow + 127u) & ~127u;
-    int depth = room / (int)(NW * bytes);
-    if (depth > DEPTH) depth = DEPTH;
-    // (two stages a warp: one is used while the other's copy is under way)
-    const int score = depth * tk + (depth > 1 ? tk / 2 : 0);
-    if (score <= best + best / 8) continue;
-    best = score;
-    a.tk = tk;
-    a.nsl = (a.K + tk - 1) / tk;
-    a.srow = srow;
-    a.s_off = 4u * tk;
-    a.stage_bytes = bytes;
-    a.depth = depth;
-    *smem = (int)a.ring_off + NW * depth * (int)bytes;
+    const int tk = ((a.K + n - 1) / n + unit - 1) & ~(unit - 1);
+    int group = 1;
+    while (n == 1 && group < 4 && 8 * group * a.K <= 4 * SLICE && quads >= 8 * group) group *= 2;
+    for (; group > 0; group /= 2) {
+      const int ld = n == 1 ? a.K : tk;
+      const unsigned srow = (tk / 16u + 31u) & ~15u;  // (padded: the rows of a quad in different banks)
+      const unsigned bytes = (4u * group * (ld + srow) + 127u) & ~127u;
+      int depth = room / (int)(NW * bytes);
+      if (depth > DEPTH) depth = DEPTH;
+      if (depth < 1 || (found && depth < 2)) continue;
+      found = true;
+      a.tk = tk;
+      a.nsl = (a.K + tk - 1) / tk;
+      a.ld = ld;
+      a.group = group;
+      a.srow = srow;
+      a.s_off = 4u * group * ld;
+      a.stage_bytes = bytes;
+      a.depth = depth;
+      *smem = (int)a.ring_off + NW * depth * (int)bytes;
+      break;
+    }
+    // large enough, or as deep as it gets
+    if (found && (a.depth >= 2 || quads >= 4 || 2 * tk < SLICE)) break;
   }
-  return best > 0;
+  return found;
 }
 
 template <int Q, bool GLU>
@@ -458,7 +489,8 @@ lk_status launch_moe(MoeArgs& a, int mode, int M, int held, const lk_launch_cfg*
     if (gx > a.rows / 4) gx = a.rows / 4;
   }
   const int products = GLU ? 0 : a.k * 4 * ((a.rows / 4 + gx - 1) / gx);
-  if (!fit(a, mode, held, products, d->smem_optin, &smem)) return LK_ERR_SHAPE;
+  const long quads = (GLU ? (long)a.k * a.rows / 2 : (long)a.k * a.rows / 4) / gx / NW;  // of a warp, about
+  if (!fit(a, mode, held, products, quads, d->smem_optin, &smem)) return LK_ERR_SHAPE;
   const dim3 grid(gx, M);
   const int pdl = cfg_pdl(cfg);
   return mode == 0   ? run<0, GLU>(a, grid, smem, d->smem_optin, pdl, stream)

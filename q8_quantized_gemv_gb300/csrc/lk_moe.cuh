@@ -28,6 +28,7 @@ struct MoeArgs {
   float* hs;
   int* cnt;
   int tk, nsl;                 // bytes of K in a stage, stages of a row
+  int ld, group;               // single rows: bytes between a stage's rows, quads of an item
   int depth;                   // stages of a warp
   unsigned srow, s_off, stage_bytes, ring_off, s_products;
   unsigned long long wait_ns;
@@ -56,6 +57,17 @@ lk_status launch_moe_kernel(void (*f)(A), std::atomic<int> (&done)[lkh::kMaxDevi
   cfg.attrs = attr;
   cfg.numAttrs = pdl ? 1 : 0;
   return cudaLaunchKernelEx(&cfg, f, a) == cudaSuccess ? LK_OK : LK_ERR_CUDA;
+}
+
+// A lane's own copies, and its arrival at `bar` when they are there.
+__device__ __forceinline__ void copy16(void* to, const void* from) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(lkring::smem_u32(to)), "l"(from) : "memory");
+}
+__device__ __forceinline__ void copy8(void* to, const void* from) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(lkring::smem_u32(to)), "l"(from) : "memory");
+}
+__device__ __forceinline__ void arrive_with_copies(unsigned bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
 }
 
 // The quantized modes for several rows (lk_moe_rows.cu).

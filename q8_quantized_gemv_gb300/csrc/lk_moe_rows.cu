@@ -69,17 +69,6 @@ __device__ __forceinline__ void dot_bits(int (&d)[4], const unsigned (&w)[4], un
 }
 __device__ __forceinline__ float dot_of(int bits) { return __fadd_rn(__int_as_float(bits), -12582912.0f); }
 
-// A lane's own copies, and its arrival at `bar` when they are there.
-__device__ __forceinline__ void copy16(void* to, const void* from) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(to)), "l"(from) : "memory");
-}
-__device__ __forceinline__ void copy8(void* to, const void* from) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(smem_u32(to)), "l"(from) : "memory");
-}
-__device__ __forceinline__ void arrive_with_copies(unsigned bar) {
-  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
-}
-
 // A bundle: expert, its first place in the sorted pairs, pairs.
 __device__ __forceinline__ unsigned bundle_of(int e, int start, int n) {
   return (unsigned)e | (unsigned)start << 10 | (unsigned)(n - 1) << 21;
