@@ -461,12 +461,16 @@ lk_status run(const MoeArgs& a, dim3 grid, int smem, int optin, int pdl, cudaStr
 }
 
 // Whether the tensor-core kernel, which reads a shared expert once, is faster than
-// single rows at the copy rate.  Measured (gate/up, down; single rows against tensor cores,
-// us): 128 experts 4096 x 1024, k 8, Int8Act 8 rows 84 / 96 and 54 / 61, 16 rows 163 / 147 and
-// 104 / 89; TwoPass 8 rows 87 / 98 and 66 / 61; 60 experts 2048 x 1408, k 4, 16 rows 58 / 58 and
-// 38 / 38, TwoPass 8 rows 36 / 39 and 24 / 26; 8 experts, k 2, 4 rows 23 / 32 and 13 / 18,
-// 8 rows 40 / 36 and 23 / 20.
-bool rows_favoured(int E, int pairs, int mode) { return 16 * pairs >= (mode == 1 ? 15 : 9) * E + 96; }
+// single rows at the copy rate.  Measured (single rows against tensor cores, us; gate/up, down):
+// 128 experts 4096 x 1024, k 8, Int8Act 8 rows 80 / 87 and 42 / 56, 16 rows 153 / 133 and
+// 84 / 81, 32 rows 266 / 170 and 179 / 113; TwoPass 8 rows 83 / 88 and 50 / 56, 16 rows 162 / 136
+// and 96 / 81; 60 experts 2048 x 1408, k 4, Int8Act 8 rows 30 / 36 and 18 / 26, 16 rows 52 / 52 and
+// 31 / 37, TwoPass 34 / 37 and 21 / 25, 61 / 54 and 38 / 37; 8 experts 4096 x 2048, k 2, Int8Act 8
+// rows 35 / 34 and 18 / 19, TwoPass 42 / 35 and 22 / 19.
+bool rows_favoured(int E, int pairs, int mode, bool glu) {
+  const int least = mode == 1 ? (glu ? 10 * E + 200 : 15 * E + 160) : (glu ? 8 * E + 96 : 10 * E + 96);
+  return 16 * pairs >= least;
+}
 
 template <bool GLU>
 lk_status launch_moe(MoeArgs& a, int mode, int M, int held, const lk_launch_cfg* cfg, cudaStream_t stream) {
@@ -477,7 +481,7 @@ lk_status launch_moe(MoeArgs& a, int mode, int M, int held, const lk_launch_cfg*
   if (!a.err) return LK_ERR_CUDA;
   const int path = cfg ? cfg->path : 0;
   if (path == 1 || (path == 3 && mode == 0)) return LK_ERR_SHAPE;
-  if (path == 3 || (path == 0 && mode != 0 && rows_favoured(a.E, M * a.k, mode)))
+  if (path == 3 || (path == 0 && mode != 0 && rows_favoured(a.E, M * a.k, mode, GLU)))
     return moe_rows(a, GLU, mode, M, cfg_pdl(cfg), stream);
   int smem = 0;
   // blocks of a row of activations; down: enough that a block's products are few

@@ -88,6 +88,7 @@ __global__ void __launch_bounds__(NW * 32, 1) moe_rows_kernel(const RowsArgs ra)
   short* ids = (short*)(smem + ra.o_ids);
   unsigned short* rank = (unsigned short*)(smem + ra.o_rank);
   unsigned short* order = (unsigned short*)(smem + ra.o_order);
+  const unsigned short* from = GLU ? rank : order;  // later: the activation row of order's pairs
   unsigned short* cnt = (unsigned short*)(smem + ra.o_cnt);
   unsigned short* off = (unsigned short*)(smem + ra.o_off);  // first place, first bundle of an expert
   unsigned* bundle = (unsigned*)(smem + ra.o_bundle);
@@ -166,6 +167,10 @@ __global__ void __launch_bounds__(NW * 32, 1) moe_rows_kernel(const RowsArgs ra)
   for (int p = threadIdx.x; p < ra.P; p += blockDim.x)
     if (ids[p] >= 0) order[off[ids[p]] + rank[p]] = (unsigned short)p;
   __syncthreads();
+  if (GLU) {
+    for (int i = threadIdx.x; i < ra.P; i += blockDim.x) rank[i] = (unsigned short)(order[i] / a.k);
+    __syncthreads();
+  }
   const int nbu = n_bundles;
 
   const int nb = a.K >> 5, odd = (nb >> 2) & 1;  // odd: rows of scales begin at 8 bytes in turn
@@ -177,6 +182,9 @@ __global__ void __launch_bounds__(NW * 32, 1) moe_rows_kernel(const RowsArgs ra)
   const int t_hi = GLU ? (int)((long)nbu * per * (blockIdx.x + 1) / G) : 0;
   const unsigned a_row = (lane & 15) * ra.rs + (lane >> 4) * 16;
   const unsigned b_row = (lane & 7) * ra.ars + (lane >> 3) * 16;
+  // the matrix of a lane's weight row, of its activation row
+  const int8_t* const w_of = GLU && lane >= 8 ? a.wb : a.wa;
+  const int8_t* const x_of = Q == 2 && (lane & 1) ? a.xl : a.xq;
   int slot = 0;
   unsigned phase = 0;
   bool ok = true;
@@ -186,61 +194,67 @@ __global__ void __launch_bounds__(NW * 32, 1) moe_rows_kernel(const RowsArgs ra)
     const int rt = GLU ? per : (rn + TR - 1) / TR;
     const int lo = GLU ? t_lo : 0, hi = GLU ? t_hi : nbu * rt;
     struct Cursor {
-      int tile, c;
+      int v, w, c;  // bundle, its tile, slice
+      unsigned bu;
     };
+    const int dv = nw / rt, dw = nw - dv * rt;  // (a division a stage was a good part of a stage's time)
     auto next = [&](Cursor& s) {
-      if (++s.c == a.nsl) {
-        s.c = 0;
-        s.tile += nw;
+      if (++s.c < a.nsl) return;
+      s.c = 0;
+      s.v += dv;
+      s.w += dw;
+      if (s.w >= rt) {
+        s.w -= rt;
+        ++s.v;
       }
+      if (s.v < nbu) s.bu = bundle[s.v];
     };
     auto issue = [&](const Cursor& s, int to) {
-      const int v = s.tile / rt, w = s.tile - v * rt;
-      const unsigned bu = bundle[v];
-      const int e = bu & 1023, start = (bu >> 10) & 2047, n = (int)(bu >> 21) + 1;
+      const int e = s.bu & 1023, start = (s.bu >> 10) & 2047, n = (int)(s.bu >> 21) + 1;
       const int k0 = s.c * a.tk, len = a.K - k0 < a.tk ? a.K - k0 : a.tk;
       const unsigned bar = full0 + 8 * to;
       unsigned char* st = ring + (size_t)to * a.stage_bytes;
-      const int rows = GLU ? TR : min(TR, rn - TR * w);
-      auto stack_row = [&](int i) { return (long)e * a.rows + (GLU ? 8 * w + (i & 7) : r0 + TR * w + i); };
+      const int rows = GLU ? TR : min(TR, rn - TR * s.w);
+      const long row0 = (long)e * a.rows + (GLU ? 8 * s.w : r0 + TR * s.w);
+      auto stack_row = [&](int i) { return row0 + (GLU ? i & 7 : i); };
       if (lane == 0) mbar_arrive_expect_tx(bar, (unsigned)len * (rows + Q * n));
       __syncwarp();
       if (lane < 16) {
-        if (lane < rows) {
-          const bool up = GLU && lane >= 8;
-          bulk_g2s_nohint(st + lane * ra.rs, (up ? a.wb : a.wa) + stack_row(lane) * a.K + k0, len, bar);
-        }
+        if (lane < rows) bulk_g2s_nohint(st + lane * ra.rs, w_of + stack_row(lane) * a.K + k0, len, bar);
       } else if (lane < 16 + Q * n) {
-        const int x = (lane - 16) / Q, low = Q == 2 ? lane & 1 : 0, p = order[start + x];
-        const long xr = GLU ? p / a.k : p;
-        bulk_g2s_nohint(st + ra.x_off + (lane - 16) * ra.ars, (low ? a.xl : a.xq) + xr * a.K + k0, len, bar);
+        bulk_g2s_nohint(st + ra.x_off + (lane - 16) * ra.ars, x_of + (long)from[start + (lane - 16) / Q] * a.K + k0, len, bar);
       }
-      // scales: 2 bytes a block of a weight row, 16 or (where rows begin at 8) 8 at a time
-      if (!odd && len % 256 == 0) {
-        const int per_row = len / 256;
-        for (int c = lane; c < rows * per_row; c += 32) {
-          const int i = c / per_row, at = 16 * (c - i * per_row);
-          copy16(st + a.s_off + i * ra.srs + at, (GLU && i >= 8 ? a.sb : a.sa) + (stack_row(i) * nb + (k0 >> 5)) * 2 + at);
-        }
-      } else {
-        const int per_row = len / 128;
-        for (int c = lane; c < rows * per_row; c += 32) {
-          const int i = c / per_row, at = 8 * (c - i * per_row);
-          copy8(st + a.s_off + i * ra.srs + at, (GLU && i >= 8 ? a.sb : a.sa) + (stack_row(i) * nb + (k0 >> 5)) * 2 + at);
-        }
-      }
+      // scales: 2 bytes a block of a weight row, 16 or (where rows begin at 8) 8 at a time,
       // and 4 bytes a block of an activation row
-      const int per_row = len / 128;
-      for (int c = lane; c < n * per_row; c += 32) {
-        const int x = c / per_row, at = 4 * (c - x * per_row), p = order[start + x];
-        const long xr = GLU ? p / a.k : p;
-        copy16(st + ra.xs_off + x * ra.xsr + 4 * at, a.xs + xr * nb + (k0 >> 5) + at);
+      auto scale16 = [&](int i, int at) {
+        copy16(st + a.s_off + i * ra.srs + at, (GLU && i >= 8 ? a.sb : a.sa) + (stack_row(i) * nb + (k0 >> 5)) * 2 + at);
+      };
+      auto act_scale = [&](int x, int at) {
+        copy16(st + ra.xs_off + x * ra.xsr + 4 * at, a.xs + (long)from[start + x] * nb + (k0 >> 5) + at);
+      };
+      if (len == 512 && !odd) {
+        if (lane >> 1 < rows) scale16(lane >> 1, 16 * (lane & 1));
+        if (lane >> 2 < n) act_scale(lane >> 2, 4 * (lane & 3));
+      } else {
+        const int per_row = len / 128, half = per_row / 2;
+        if (!odd && len % 256 == 0) {
+          for (int c = lane; c < rows * half; c += 32) scale16(c / half, 16 * (c % half));
+        } else {
+          for (int c = lane; c < rows * per_row; c += 32) {
+            const int i = c / per_row, at = 8 * (c - i * per_row);
+            copy8(st + a.s_off + i * ra.srs + at, (GLU && i >= 8 ? a.sb : a.sa) + (stack_row(i) * nb + (k0 >> 5)) * 2 + at);
+          }
+        }
+        for (int c = lane; c < n * per_row; c += 32) act_scale(c / per_row, 4 * (c % per_row));
       }
       arrive_with_copies(bar);
       __syncwarp();
     };
-    Cursor head{lo + warp, 0}, at = head;
-    const int total = ok && lo + warp < hi ? ((hi - 1 - lo - warp) / nw + 1) * a.nsl : 0;
+    const int first = lo + warp;
+    Cursor head{first / rt, first % rt, 0, 0}, at;
+    if (first < hi) head.bu = bundle[head.v];
+    at = head;
+    const int total = ok && first < hi ? ((hi - 1 - first) / nw + 1) * a.nsl : 0;
     int issued = 0;
     for (int s = slot; issued < total && issued < a.depth; ++issued, next(head)) {
       issue(head, s);
@@ -266,7 +280,6 @@ __global__ void __launch_bounds__(NW * 32, 1) moe_rows_kernel(const RowsArgs ra)
       const int k0 = at.c * a.tk, len = a.K - k0 < a.tk ? a.K - k0 : a.tk;
       unsigned char* st = ring + (size_t)slot * a.stage_bytes;
       const unsigned W = smem_u32(st) + a_row, X = smem_u32(st + ra.x_off) + b_row;
-      const int v = at.tile / rt, w = at.tile - v * rt;
       const unsigned char* S = st + a.s_off + g * ra.srs;
       const unsigned char* XS = st + ra.xs_off + LP * t4 * ra.xsr;
       const int groups = len >> 7;
@@ -328,8 +341,7 @@ __global__ void __launch_bounds__(NW * 32, 1) moe_rows_kernel(const RowsArgs ra)
         ++issued;
       }
       if (at.c == a.nsl - 1) {
-        const unsigned bu = bundle[v];
-        const int start = (bu >> 10) & 2047, np = (int)(bu >> 21) + 1;
+        const int w = at.w, start = (at.bu >> 10) & 2047, np = (int)(at.bu >> 21) + 1;
 #pragma unroll
         for (int c = 0; c < LP; ++c) {
           float y[2];
