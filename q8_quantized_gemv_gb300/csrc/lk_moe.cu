@@ -8,8 +8,8 @@
 // rows' arithmetic is lk_gemv_q8's (8 lanes to a row, lane pair b mod 4 with
 // block b's exact dot, (p0 + p2) + (p1 + p3)), so each product has its bits.
 //
-// Stages are few and large: the copy engine starts a bulk copy in 16 to 23 cycles whatever
-// its size, and a warp takes as long again around each stage (gate/up of 8 rows, 4096 x 1024:
+// Stages are few and large: a bulk copy goes out in about 20 cycles whatever its size, one
+// lane at a time, and a warp takes as long again around each stage (gate/up of 8 rows, 4096 x 1024:
 // slices of 512 170 us, 1024 107, 2048 85, whole rows 83).  So rows that are whole in a
 // stage are one copy of neighbouring rows (gate/up two), up to four quads of short
 // rows, and the scales come by the lanes' own asynchronous copies.
@@ -462,14 +462,13 @@ lk_status run(const MoeArgs& a, dim3 grid, int smem, int optin, int pdl, cudaStr
 
 // Whether the tensor-core kernel, which reads a shared expert once, is faster than
 // single rows at the copy rate.  Measured (single rows against tensor cores, us; gate/up, down):
-// 128 experts 4096 x 1024, k 8, Int8Act 8 rows 80 / 87 and 42 / 56, 16 rows 153 / 133 and
-// 84 / 81, 32 rows 266 / 170 and 179 / 113; TwoPass 8 rows 83 / 88 and 50 / 56, 16 rows 162 / 136
-// and 96 / 81; 60 experts 2048 x 1408, k 4, Int8Act 8 rows 30 / 36 and 18 / 26, 16 rows 52 / 52 and
-// 31 / 37, TwoPass 34 / 37 and 21 / 25, 61 / 54 and 38 / 37; 8 experts 4096 x 2048, k 2, Int8Act 8
-// rows 35 / 34 and 18 / 19, TwoPass 42 / 35 and 22 / 19.
+// 128 experts 4096 x 1024, k 8, Int8Act 8 rows 80 / 82 and 41 / 50, 16 rows 152 / 130 and
+// 84 / 72, 32 rows 267 / 167 and 179 / 100; TwoPass 8 rows 83 / 87 and 50 / 50, 16 rows 162 / 132
+// and 97 / 73; 60 experts 2048 x 1408, k 4, Int8Act 8 rows 30 / 35 and 18 / 24, 16 rows 52 / 52 and
+// 32 / 35, TwoPass 34 / 38 and 21 / 24, 61 / 54 and 38 / 34; 8 experts 4096 x 2048, k 2, Int8Act 8
+// rows 35 / 36 and 18 / 18, TwoPass 42 / 39 and 23 / 19.
 bool rows_favoured(int E, int pairs, int mode, bool glu) {
-  const int least = mode == 1 ? (glu ? 10 * E + 200 : 15 * E + 160) : (glu ? 8 * E + 96 : 10 * E + 96);
-  return 16 * pairs >= least;
+  return 16 * pairs >= (mode == 1 ? (glu ? 10 * E + 200 : 12 * E + 190) : 8 * E + 128);
 }
 
 template <bool GLU>

@@ -8,9 +8,11 @@
 // weights come from HBM once (more pairs: again from L2).  A tile is 16 weight
 // rows x 8 columns, a column a pair's words (TwoPass: neighbouring columns its high and low
 // words, which the same lane then has the dots of); a warp streams its tiles through its
-// own shared-memory stages, each one slice of K: bulk copies of the 16 rows and of the
-// bundle's activation rows, and the lanes' own asynchronous copies of their scales (bulk copies
-// of 32 bytes kept the copy engine, which starts one in about 16 cycles, from the rest).
+// own shared-memory stages, each one slice of K of the 16 rows and of the bundle's activation
+// rows, by the lanes' own asynchronous copies: a bulk copy a row goes out one lane at a
+// time, about 20 cycles each, and 24 of them were a good part of a stage's time (64 rows down
+// 145 us against 128).  Slices are as large as 16 warps have room for: halves of it, two
+// stages a warp, took 159 us.
 // Each row is 16 bytes longer than its slice, which keeps ldmatrix's eight rows in
 // different banks.  A 32-block is one mma m16n8k32 of int8
 // levels with the exact dots as result, combined in f32 as every other kernel
@@ -96,7 +98,7 @@ __global__ void __launch_bounds__(NW * 32, 1) moe_rows_kernel(const RowsArgs ra)
   unsigned char* ring = smem + ra.o_ring + (size_t)warp * a.depth * a.stage_bytes;
   const unsigned full0 = smem_u32(bars + warp * DEPTH);
   if (lane == 0)
-    for (int s = 0; s < a.depth; ++s) mbar_init(full0 + 8 * s, 33);  // the bulk copies', and each lane's
+    for (int s = 0; s < a.depth; ++s) mbar_init(full0 + 8 * s, 32);
   for (int e = threadIdx.x; e < a.E; e += blockDim.x) cnt[e] = 0;
   if (threadIdx.x == 0) {
     aborted = 0;
@@ -182,9 +184,6 @@ __global__ void __launch_bounds__(NW * 32, 1) moe_rows_kernel(const RowsArgs ra)
   const int t_hi = GLU ? (int)((long)nbu * per * (blockIdx.x + 1) / G) : 0;
   const unsigned a_row = (lane & 15) * ra.rs + (lane >> 4) * 16;
   const unsigned b_row = (lane & 7) * ra.ars + (lane >> 3) * 16;
-  // the matrix of a lane's weight row, of its activation row
-  const int8_t* const w_of = GLU && lane >= 8 ? a.wb : a.wa;
-  const int8_t* const x_of = Q == 2 && (lane & 1) ? a.xl : a.xq;
   int slot = 0;
   unsigned phase = 0;
   bool ok = true;
@@ -217,12 +216,27 @@ __global__ void __launch_bounds__(NW * 32, 1) moe_rows_kernel(const RowsArgs ra)
       const int rows = GLU ? TR : min(TR, rn - TR * s.w);
       const long row0 = (long)e * a.rows + (GLU ? 8 * s.w : r0 + TR * s.w);
       auto stack_row = [&](int i) { return row0 + (GLU ? i & 7 : i); };
-      if (lane == 0) mbar_arrive_expect_tx(bar, (unsigned)len * (rows + Q * n));
-      __syncwarp();
-      if (lane < 16) {
-        if (lane < rows) bulk_g2s_nohint(st + lane * ra.rs, w_of + stack_row(lane) * a.K + k0, len, bar);
-      } else if (lane < 16 + Q * n) {
-        bulk_g2s_nohint(st + ra.x_off + (lane - 16) * ra.ars, x_of + (long)from[start + (lane - 16) / Q] * a.K + k0, len, bar);
+      if (16 * lane < len) {
+        unsigned char* to_w = st + 16 * lane;
+        const int8_t* w = a.wa + row0 * a.K + k0 + 16 * lane;
+        if (GLU) {
+          const int8_t* u = a.wb + row0 * a.K + k0 + 16 * lane;
+#pragma unroll
+          for (int i = 0; i < 8; ++i, w += a.K) copy16(to_w + i * ra.rs, w);
+#pragma unroll
+          for (int i = 8; i < TR; ++i, u += a.K) copy16(to_w + i * ra.rs, u);
+        } else {
+#pragma unroll
+          for (int i = 0; i < TR; ++i, w += a.K)
+            if (i < rows) copy16(to_w + i * ra.rs, w);
+        }
+#pragma unroll
+        for (int x = 0; x < TC / Q; ++x) {
+          if (x >= n) break;
+          const long at = (long)from[start + x] * a.K + k0 + 16 * lane;
+          copy16(to_w + ra.x_off + Q * x * ra.ars, a.xq + at);
+          if (Q == 2) copy16(to_w + ra.x_off + (Q * x + 1) * ra.ars, a.xl + at);
+        }
       }
       // scales: 2 bytes a block of a weight row, 16 or (where rows begin at 8) 8 at a time,
       // and 4 bytes a block of an activation row
@@ -335,7 +349,6 @@ __global__ void __launch_bounds__(NW * 32, 1) moe_rows_kernel(const RowsArgs ra)
       }
       __syncwarp();
       if (issued < total) {
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         issue(head, slot);
         next(head);
         ++issued;
