@@ -492,6 +492,26 @@ static __device__ __forceinline__ void run(const SampleArgs& a, unsigned char* s
     sum.flush();
     return weigh ? sum.all : number;
   };
+  // this lane's sum of all weights of min_p at least, where no border is (without its keys: 64 rows of
+  // 151936 37.6 -> 34.6 us)
+  auto sum_all = [&](float min_p) {
+    Sum sum;
+    int turns = 0;
+    mine.again([&](const float (&l)[4], int) {
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        float small;
+        const float big = w.parts(l[q], small);
+        if (w.depth(l[q]) < REACH && (min_p == 0.0f || Weights::enough(big, small, min_p))) sum.add(Split(big, small));
+      }
+      if (++turns == (int)GRID / 4) {
+        turns = 0;
+        sum.flush();
+      }
+    });
+    sum.flush();
+    return sum.all;
+  };
 
   if (by_k || by_p) {
     // ---- the order in bins ----
@@ -872,7 +892,7 @@ static __device__ __forceinline__ void run(const SampleArgs& a, unsigned char* s
     }
   }
   if (!summed) {
-    u64 part = sum_up_to(last, true, mp);
+    u64 part = last == ~0ull ? sum_all(mp) : sum_up_to(last, true, mp);
     part = warp_sum(part);
     if (lane == 0) cl.map_shared_rank(&s, 0)->drawn[slot] = part;
   }
