@@ -25,7 +25,7 @@
  *
  * Experts.  Matrix n of a stack [E][rows][K] is a Q8_0 matrix as everywhere
  * (levels int8, f16 scales [E][rows][K/32]), 16-byte aligned both.  rows and K
- * are multiples of 128, E <= LK_MOE_MAX_E.
+ * are multiples of 128, E <= LK_MOE_MAX_E, E * rows < 2^31, k * rows < 2^29.
  *
  * What a call writes must not overlap what it reads or anything else it writes
  * (LK_ERR_ARG).

@@ -507,8 +507,8 @@ lk_status check_shape(int E, int rows, int K, lk_mode mode, int M, int k, const 
   if (E < 1 || E > LK_MOE_MAX_E || rows < 128 || rows % 128 || K < 128 || K % 128 || M < 0 || M > LK_MAX_BATCH ||
       k < 1 || k > LK_MOE_MAX_K)
     return LK_ERR_SHAPE;
-  // rows of a stack, and quads of a row's pairs, are 32-bit numbers
-  if ((long)E * rows > 0x7fffffffL || (long)k * rows > 0x3fffffffL) return LK_ERR_SHAPE;
+  // rows of a stack, and tiles of all pairs, are 32-bit numbers
+  if ((long)E * rows > 0x7fffffffL || (long)k * rows > 0x1fffffffL) return LK_ERR_SHAPE;
   return LK_OK;
 }
 // Activation rows by mode: present and aligned.

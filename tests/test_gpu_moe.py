@@ -320,6 +320,27 @@ def test_kernels_agree(lk, mode, M, E, k, F, K):
         assert err.value.status == -3
 
 
+@pytest.mark.parametrize("mode", ["dequant", "int8act", "twopass"])
+@pytest.mark.parametrize("M,E,k,rows,K", [(40, 6, 8, 640, 384), (40, 6, 8, 640, 2048), (50, 4, 2, 1280, 1152),
+                                          (7, 5, 3, 256, 4224), (7, 5, 3, 256, 4352), (1, 5, 3, 128, 4096)])
+def test_single_rows_stages(lk, mode, M, E, k, rows, K):
+    """The kernel for single rows with several groups of short rows in a stage (the last of a
+    block with fewer), and with long rows in slices whose scales begin at 8 or 16 bytes."""
+    mode, cfg = lk.MODES[mode], lk.launch_cfg(path=2)
+    a, b = experts(E, rows, K, 1, DEV), experts(E, rows, K, 2, DEV)
+    ids = make_ids(M, E, k, 3)
+    there = ((ids >= 0) & (ids < E)).flatten()
+    acts, h = acts_of(x_rows(M, K, 4), mode), torch.full((M * k, rows), 7.0, device=DEV)
+    lk.lk_moe_glu_q8(lk.Experts(gate=a, up=b), mode, ids, h, cfg=cfg, **acts)
+    want, tol = glu_ref(a, b, acts, mode, ids, E)
+    assert bool(((h.double() - want).abs() <= tol)[there].all()) and bool((h[~there] == 7).all())
+    hidden, w = acts_of(x_rows(M * k, K, 5), mode), torch.rand((M, k), device=DEV)
+    y = torch.full((M, rows), math.nan, device=DEV)
+    lk.lk_moe_down_q8(lk.Experts(down=a), mode, ids, w, y, cfg=cfg, **as_h(hidden))
+    want, tol = down_ref(a, hidden, mode, ids, w, E)
+    assert bool(((y.double() - want).abs() <= tol).all())
+
+
 def test_two_streams_at_once(lk):
     """Calls on two streams, each with its own outputs and counters."""
     M, E, k, F, K, mode = 8, 12, 4, 256, 768, lk.LK_INT8ACT

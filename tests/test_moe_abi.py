@@ -106,6 +106,7 @@ def test_glu_refusals(lib):
         for m in (1, 2, 3, 4, 5, 6, 7, 8):
             assert glu(lib, **{n: m}) == -1, (n, m)
     assert glu(lib, hq=9) == -1 and glu(lib, hs=FAKE + 10 * BIG + 496) == -1 and glu(lib, cnt=12) == -1
+    assert glu(lib, E=1, k=1, F=1 << 29) == -3 and glu(lib, E=1, k=2, F=1 << 28) == -3
     assert glu(lib, M=0, wg=None) == 0
 
 
