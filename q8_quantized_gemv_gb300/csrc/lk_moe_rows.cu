@@ -4,8 +4,9 @@
 // Rows that chose the same expert share the read of its weights.  Every block
 // sorts the pairs by expert (the same sort in all of them: it takes about a
 // microsecond, nothing is handed on) into bundles of one expert's up to 8 pairs
-// (TwoPass 4), and takes its share of all bundles' weight rows in order, so an expert's
-// weights come from HBM once (more pairs: again from L2).  A tile is 16 weight
+// (TwoPass 4), and takes its share of all bundles' weight rows, the same rows of an expert's
+// bundles one after the other: an expert's weights come from HBM once, for more bundles again
+// from L2 (bundle after bundle TwoPass took 262 us for 64 rows gate/up of 128 experts, so 234).  A tile is 16 weight
 // rows x 8 columns, a column a pair's words (TwoPass: neighbouring columns its high and low
 // words, which the same lane then has the dots of); a warp streams its tiles through its
 // own shared-memory stages, each one slice of K of the 16 rows and of the bundle's activation
@@ -182,6 +183,24 @@ __global__ void __launch_bounds__(NW * 32, 1) moe_rows_kernel(const RowsArgs ra)
   const int r_lo = GLU ? 0 : (int)((long)a.rows * blockIdx.x / G), r_hi = GLU ? 0 : (int)((long)a.rows * (blockIdx.x + 1) / G);
   const int t_lo = GLU ? (int)((long)nbu * per * blockIdx.x / G) : 0;
   const int t_hi = GLU ? (int)((long)nbu * per * (blockIdx.x + 1) / G) : 0;
+  // Gate/up: tiles (and groups of four, for the words) go expert by expert, of an expert by its
+  // rows, the same rows of its bundles one after the other: they come from HBM once.
+  struct Place {
+    int first, n;  // the expert's first bundle, its bundles
+    int step, v;   // its rows' tile (group), bundle
+  };
+  auto place_of = [&](int i, int each) {
+    Place s;
+    const int v0 = i / each;
+    const unsigned bu = bundle[v0];
+    const int e = bu & 1023;
+    s.n = (cnt[e] + TP - 1) / TP;
+    s.first = v0 - ((int)((bu >> 10) & 2047) - off[e]) / TP;
+    const int r = i - s.first * each;
+    s.step = s.n == 1 ? r : r / s.n;
+    s.v = s.first + r - s.step * s.n;
+    return s;
+  };
   const unsigned a_row = (lane & 15) * ra.rs + (lane >> 4) * 16;
   const unsigned b_row = (lane & 7) * ra.ars + (lane >> 3) * 16;
   int slot = 0;
@@ -193,20 +212,31 @@ __global__ void __launch_bounds__(NW * 32, 1) moe_rows_kernel(const RowsArgs ra)
     const int rt = GLU ? per : (rn + TR - 1) / TR;
     const int lo = GLU ? t_lo : 0, hi = GLU ? t_hi : nbu * rt;
     struct Cursor {
-      int v, w, c;  // bundle, its tile, slice
-      unsigned bu;
+      int tile, c;  // gate/up: tile, down: bundle; slice
+      int w;        // the tile's rows
+      unsigned bu;  // its bundle
     };
-    const int dv = nw / rt, dw = nw - dv * rt;  // (a division a stage was a good part of a stage's time)
-    auto next = [&](Cursor& s) {
+    const int dv = nw / rt, dw = nw - dv * rt;
+    auto place = [&](Cursor& s) {
+      const Place at = place_of(s.tile, per);
+      s.w = at.step;
+      s.bu = bundle[at.v];
+    };
+    auto next = [&](Cursor& s) {  // (no divisions but a gate/up tile's)
       if (++s.c < a.nsl) return;
       s.c = 0;
-      s.v += dv;
-      s.w += dw;
-      if (s.w >= rt) {
-        s.w -= rt;
-        ++s.v;
+      if (GLU) {
+        s.tile += nw;
+        if (s.tile < hi) place(s);
+      } else {
+        s.tile += dv;
+        s.w += dw;
+        if (s.w >= rt) {
+          s.w -= rt;
+          ++s.tile;
+        }
+        if (s.tile < nbu) s.bu = bundle[s.tile];
       }
-      if (s.v < nbu) s.bu = bundle[s.v];
     };
     auto issue = [&](const Cursor& s, int to) {
       const int e = s.bu & 1023, start = (s.bu >> 10) & 2047, n = (int)(s.bu >> 21) + 1;
@@ -265,9 +295,12 @@ __global__ void __launch_bounds__(NW * 32, 1) moe_rows_kernel(const RowsArgs ra)
       __syncwarp();
     };
     const int first = lo + warp;
-    Cursor head{first / rt, first % rt, 0, 0}, at;
-    if (first < hi) head.bu = bundle[head.v];
-    at = head;
+    Cursor head{GLU ? first : first / rt, 0, first % rt, 0};
+    if (first < hi) {
+      if (GLU) place(head);
+      else head.bu = bundle[head.tile];
+    }
+    Cursor at = head;
     const int total = ok && first < hi ? ((hi - 1 - first) / nw + 1) * a.nsl : 0;
     int issued = 0;
     for (int s = slot; issued < total && issued < a.depth; ++issued, next(head)) {
@@ -410,17 +443,25 @@ __global__ void __launch_bounds__(NW * 32, 1) moe_rows_kernel(const RowsArgs ra)
     __syncthreads();
     if (*abort_flag || t_hi <= t_lo) return;
     const int groups = a.rows / 32;  // of a pair
-    for (int x = t_lo / 4 + warp; x <= (t_hi - 1) / 4; x += nw) {
-      const int lo = t_lo > 4 * x ? t_lo : 4 * x, hi = t_hi < 4 * x + 4 ? t_hi : 4 * x + 4;
-      if (hi - lo < 4) {
+    // the expert's groups of the same rows as the first tile's, to those of the last one's
+    const Place from_tile = place_of(t_lo, per), to_tile = place_of(t_hi - 1, per);
+    const int x0 = from_tile.first * groups + from_tile.step / 4 * from_tile.n;
+    const int x1 = to_tile.first * groups + (to_tile.step / 4 + 1) * to_tile.n;
+    for (int x = x0 + warp; x < x1; x += nw) {
+      const Place at = place_of(x, groups);
+      const int gi = at.step, t0 = at.first * per + 4 * gi * at.n + at.v - at.first;  // its first tile of four
+      int mine = 0;
+      for (int i = 0; i < 4; ++i) mine += t0 + i * at.n >= t_lo && t0 + i * at.n < t_hi;
+      if (mine == 0) continue;
+      if (mine < 4) {
         int old = 0;
-        if (lane == 0) old = atomicAdd(a.cnt + x, hi - lo);
+        if (lane == 0) old = atomicAdd(a.cnt + x, mine);
         old = __shfl_sync(FULL, old, 0);
-        if (old + hi - lo != 4) continue;  // another block finishes it
+        if (old + mine != 4) continue;  // another block finishes it
         if (lane == 0) a.cnt[x] = 0;
         __threadfence();  // the others' h after their counts
       }
-      const int v = x / groups, gi = x - v * groups;
+      const int v = at.v;
       const unsigned bu = bundle[v];
       const int start = (bu >> 10) & 2047, np = (int)(bu >> 21) + 1;
       for (int c = 0; c < np; ++c) {
