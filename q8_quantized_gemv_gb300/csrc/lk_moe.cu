@@ -264,29 +264,23 @@ __global__ void __launch_bounds__(NW * 32, 1) moe_kernel(const MoeArgs a) {
   const int q1 = (int)((long)units * (blockIdx.x + 1) / gridDim.x) * (GLU ? G : 1);
   const int nq = q1 - q0, ipp = (nq + G - 1) / G, items = GLU ? ipp : ipp * np;
   struct Cursor {
-    int item, c;   // item, slice
+    int c;         // slice
     int i, q, n;   // the item's pair (of those that are there), its first quad (gate/up: of the pair's; down:
                    // of the block's), its quads
   };
-  auto place = [&](Cursor& s) {
-    if (GLU) {
-      const int q = q0 + s.item * G;
-      s.i = q / per;
-      s.q = q - s.i * per;
-      s.n = G;
-    } else {
-      s.i = s.item / ipp;
-      s.q = (s.item - s.i * ipp) * G;
-      s.n = min(G, nq - s.q);
-    }
-  };
+  const int whole = ipp * G, di = GLU || !ipp ? 0 : NW / ipp, dq = (NW - di * ipp) * G;
   auto next = [&](Cursor& s) {
     if (++s.c < a.nsl) return;
     s.c = 0;
-    s.item += NW;
-    if (s.item < items) place(s);
+    s.i += di;
+    s.q += GLU ? NW * G : dq;
+    if (s.q >= (GLU ? per : whole)) {  // (gate/up: a pair has at least 64 quads, a round at most 48)
+      s.q -= GLU ? per : whole;
+      ++s.i;
+    }
+    if (!GLU) s.n = min(G, nq - s.q);
   };
-  const int nb = a.K >> 5, odd = (nb >> 2) & 1;  // odd: rows of scales begin at 8 bytes in turn
+  const int nb = a.K >> 5;
   const int hop = GLU ? 2 * G : 2;               // (quad_stage; gate/up: up rows behind the gate rows)
   auto issue = [&](const Cursor& s, int slot) {
     const int k0 = s.c * a.tk, len = a.K - k0 < a.tk ? a.K - k0 : a.tk;
@@ -294,8 +288,6 @@ __global__ void __launch_bounds__(NW * 32, 1) moe_kernel(const MoeArgs a) {
     unsigned char* st = ring + (size_t)slot * a.stage_bytes;
     const int rows = 4 * s.n, half = 2 * s.n;  // of the stage; gate/up: of each matrix
     const long row0 = (long)expert_of[s.i] * a.rows + (GLU ? 2 * s.q : 4 * (q0 + s.q));
-    // row i of the item: its row in the stage
-    auto at = [&](int i) { return GLU && i >= half ? i - half + hop : i; };
     if (lane == 0) mbar_arrive_expect_tx(bar, (unsigned)rows * len);
     __syncwarp();
     if (a.nsl == 1) {
@@ -305,21 +297,30 @@ __global__ void __launch_bounds__(NW * 32, 1) moe_kernel(const MoeArgs a) {
       const bool up = GLU && lane >= 2;
       bulk_g2s_nohint(st + lane * a.ld, (up ? a.wb : a.wa) + (row0 + (up ? lane - 2 : lane)) * a.K + k0, len, bar);
     }
-    // the scales, 2 bytes a block, 16 or (where rows begin at 8) 8 at a time
-    const int size = odd || len % 256 ? 8 : 16, per_row = len / 16 / size;
-    for (int c = lane; c < rows * per_row; c += 32) {
-      const int i = c / per_row, off = size * (c - i * per_row);
-      const bool up = GLU && i >= half;
-      const unsigned char* from = (up ? a.sb : a.sa) + ((row0 + (up ? i - half : i)) * nb + (k0 >> 5)) * 2 + off;
-      unsigned char* to = st + a.s_off + at(i) * a.srow + off;
-      if (size == 16) copy16(to, from);
-      else copy8(to, from);
+    // the scales, 2 bytes a block: a row has up to 256 bytes and begins at a multiple of 8
+    if (8 * lane < len / 16) {
+      const long at = 2 * (row0 * nb + (k0 >> 5)) + 8 * lane;
+      unsigned char* to = st + a.s_off + 8 * lane;
+#pragma unroll 1
+      for (int i = 0; i < (GLU ? half : rows); i += 2) {
+        copy8(to + i * a.srow, a.sa + at + 2 * i * nb);
+        copy8(to + (i + 1) * a.srow, a.sa + at + 2 * (i + 1) * nb);
+        if (GLU) {
+          copy8(to + (hop + i) * a.srow, a.sb + at + 2 * i * nb);
+          copy8(to + (hop + i + 1) * a.srow, a.sb + at + 2 * (i + 1) * nb);
+        }
+      }
     }
     arrive_with_copies(bar);
     __syncwarp();
   };
-  Cursor head{warp, 0, 0, 0, 0};
-  if (warp < items) place(head);
+  const int first = GLU ? q0 + warp * G : warp;
+  Cursor head{0, 0, 0, G};
+  if (warp < items) {
+    head.i = first / (GLU ? per : ipp);
+    head.q = GLU ? first - head.i * per : (first - head.i * ipp) * G;
+    if (!GLU) head.n = min(G, nq - head.q);
+  }
   Cursor at = head;
   const int total = warp < items ? ((items - 1 - warp) / NW + 1) * a.nsl : 0;
   int issued = 0;
