@@ -194,12 +194,14 @@ class Sampling:
 
     State after the stack is built: u float32 [batch], the random numbers in
     [0, 1) of the next token, which the caller writes; prob float32 [batch], the
-    drawn tokens' probabilities."""
+    drawn tokens' probabilities.  It belongs to one stack."""
 
     def __init__(self, temperature=None, top_k=None, top_p=None, min_p=None):
         self.given = dict(temperature=temperature, top_k=top_k, top_p=top_p, min_p=min_p)
 
     def build(self, batch, dev):
+        if hasattr(self, "set"):
+            raise ValueError("this Sampling has the numbers of another stack")
         self.set = {}
         for n, v in self.given.items():
             if v is not None:

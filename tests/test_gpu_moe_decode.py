@@ -104,3 +104,7 @@ def test_refusals(lk):
     with pytest.raises(ValueError):
         DecodeStack(**SIZE, moe=moe)
     assert st.launches_per_token() == 1 + 2 * (4 + 1 + 4) + 2
+    draw = Sampling(top_k=3)
+    DecodeStack(**SIZE, sample=draw)
+    with pytest.raises(ValueError):
+        DecodeStack(**SIZE, sample=draw)
