@@ -185,7 +185,6 @@ struct SampleArgs {
   float* prob;
 };
 
-constexpr int MAX_C = 8;           // blocks of a row at most
 constexpr int CAP = 4096;          // tokens near the borders that are sorted
 constexpr int HELD = 32768;        // tokens of a block in shared memory at most
 
@@ -195,9 +194,10 @@ __device__ __forceinline__ u64 warp_sum(u64 v) {
   return v;
 }
 
-// A row's blocks, of NW warps each.  Few tokens go with few warps: most of what a block
-// runs through is run through by all of its warps, whatever they have to do.
-template <int NW>
+// A row's blocks, up to MAX_C (8 or 16) of NW warps each.  Few tokens go with few warps: most of
+// what a block runs through is run through by all of its warps, whatever they have to do.
+// (Loops over 16 blocks cost rows of fewer 2 %, so those have kernels of their own.)
+template <int NW, int MAX_C>
 struct Rows {
 static constexpr int THREADS = 32 * NW;
 static constexpr int NB = 64 * NW;                  // bins of the order
@@ -967,17 +967,17 @@ static __device__ __forceinline__ void run(const SampleArgs& a, unsigned char* s
 
 };
 
-template <int NW>
+template <int NW, int MAX_C>
 __global__ void __launch_bounds__(32 * NW) sample_kernel(const SampleArgs a) {
   extern __shared__ __align__(128) unsigned char smem[];
-  Rows<NW>::run(a, smem);
+  Rows<NW, MAX_C>::run(a, smem);
 }
 
 constexpr int LARGE = 32768, SMALL = 6144;  // tokens of a block above which it has 32 (16) warps
 
-template <int NW>
+template <int NW, int MAX_C>
 lk_status launch_rows(SampleArgs a, int M, int dev, int pdl, cudaStream_t stream) {
-  typedef Rows<NW> R;
+  typedef Rows<NW, MAX_C> R;
   cudaLaunchConfig_t lc = {};
   lc.blockDim = dim3(R::THREADS);
   lc.stream = stream;
@@ -990,10 +990,12 @@ lk_status launch_rows(SampleArgs a, int M, int dev, int pdl, cudaStream_t stream
   lc.numAttrs = pdl ? 2 : 1;
   static std::atomic<int> done[kMaxDevices];
   if (!done[dev].load(std::memory_order_acquire)) {
-    if (cudaFuncSetAttribute(sample_kernel<NW>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             (int)(sizeof(typename R::Shared) + HELD * 4)) != cudaSuccess)
+    if (cudaFuncSetAttribute(sample_kernel<NW, MAX_C>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             (int)(sizeof(typename R::Shared) + HELD * 4)) != cudaSuccess ||
+        (MAX_C > 8 &&
+         cudaFuncSetAttribute(sample_kernel<NW, MAX_C>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess))
       return LK_ERR_CUDA;
-    carveout_max_shared(sample_kernel<NW>);
+    carveout_max_shared(sample_kernel<NW, MAX_C>);
     done[dev].store(1, std::memory_order_release);
   }
   const int parts = a.C * NW;
@@ -1002,17 +1004,19 @@ lk_status launch_rows(SampleArgs a, int M, int dev, int pdl, cudaStream_t stream
   lc.gridDim = dim3(M * a.C);
   lc.dynamicSmemBytes = sizeof(typename R::Shared) + (size_t)NW * a.held * 4;
   attr[0].val.clusterDim.x = a.C;
-  return cudaLaunchKernelEx(&lc, sample_kernel<NW>, a) == cudaSuccess ? LK_OK : LK_ERR_CUDA;
+  return cudaLaunchKernelEx(&lc, sample_kernel<NW, MAX_C>, a) == cudaSuccess ? LK_OK : LK_ERR_CUDA;
 }
 
-// Clusters of 2, 4 and 8 blocks that the device takes at once, 10 bits each (0: an error).
+// Clusters of 2, 4, 8 and 16 blocks that the device takes at once, 8 bits each (0: an error).
 int clusters_at_once(int dev) {
   static std::atomic<int> known[kMaxDevices];
   int fits = known[dev].load(std::memory_order_acquire);
   if (fits) return fits;
-  typedef Rows<32> R;
+  typedef Rows<32, 16> R;
   const size_t most = sizeof(typename R::Shared) + HELD * 4;
-  if (cudaFuncSetAttribute(sample_kernel<32>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most) != cudaSuccess) return 0;
+  if (cudaFuncSetAttribute(sample_kernel<32, 16>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most) != cudaSuccess ||
+      cudaFuncSetAttribute(sample_kernel<32, 16>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
+    return 0;
   cudaLaunchConfig_t lc = {};
   lc.blockDim = dim3(R::THREADS);
   lc.dynamicSmemBytes = most;
@@ -1021,12 +1025,12 @@ int clusters_at_once(int dev) {
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   lc.attrs = attr;
   lc.numAttrs = 1;
-  for (int i = 0; i < 3; ++i) {
+  for (int i = 0; i < 4; ++i) {
     int n = 0;
     attr[0].val.clusterDim.x = 2u << i;
     lc.gridDim = dim3(2u << i);
-    if (cudaOccupancyMaxActiveClusters(&n, sample_kernel<32>, &lc) != cudaSuccess) return 0;
-    fits |= (n < 1023 ? n : 1023) << (10 * i);
+    if (cudaOccupancyMaxActiveClusters(&n, sample_kernel<32, 16>, &lc) != cudaSuccess) return 0;
+    fits |= (n < 127 ? n : 127) << (8 * i);
   }
   known[dev].store(fits, std::memory_order_release);
   return fits;
@@ -1053,11 +1057,16 @@ extern "C" lk_status lk_sample(const float* logits, int M, int N, const float* t
   const int fits = clusters_at_once(dev);
   if (!fits) return LK_ERR_CUDA;
   // blocks of a row: as many as are on the SMs at once with all rows', none with less than 2048 tokens
+  // (one row of 151936 in 16 blocks, not 8: top_p 31 -> 24 us, top_k 50 and top_p 17 -> 15)
   int C = 1;
-  for (int i = 0; i < 3 && M <= ((fits >> (10 * i)) & 1023) && N >= C * 4096; ++i) C *= 2;
+  for (int i = 0; i < 4 && M <= ((fits >> (8 * i)) & 127) && N >= C * 4096; ++i) C *= 2;
   const SampleArgs a = {logits, N, C, 0, 0, temperature, top_k, top_p, min_p, u, idx, prob};
   const int pdl = cfg_pdl(cfg), tokens = N / C;
-  return tokens > LARGE   ? launch_rows<32>(a, M, dev, pdl, stream)
-         : tokens > SMALL ? launch_rows<16>(a, M, dev, pdl, stream)
-                          : launch_rows<8>(a, M, dev, pdl, stream);
+  if (C == 16)
+    return tokens > LARGE   ? launch_rows<32, 16>(a, M, dev, pdl, stream)
+           : tokens > SMALL ? launch_rows<16, 16>(a, M, dev, pdl, stream)
+                            : launch_rows<8, 16>(a, M, dev, pdl, stream);
+  return tokens > LARGE   ? launch_rows<32, 8>(a, M, dev, pdl, stream)
+         : tokens > SMALL ? launch_rows<16, 8>(a, M, dev, pdl, stream)
+                          : launch_rows<8, 8>(a, M, dev, pdl, stream);
 }

@@ -199,6 +199,20 @@ def test_rows_of_any_alignment(lk, M):
         assert near <= 1
 
 
+@pytest.mark.parametrize("N", [32767, 32768, 50001, 98305, 600011])
+@pytest.mark.parametrize("M", [1, 3])
+def test_few_rows_in_many_blocks(lk, M, N):
+    """Rows that most blocks share, from the fewest tokens a block to the most warps."""
+    logits = vocab(M, N, N)
+    logits[:, ::5] = np.round(logits[:, ::5])
+    r = np.random.default_rng(N)
+    u, one = r.random(M), np.ones(M)
+    check(lk, logits, u, near=1)
+    check(lk, logits, u, near=1, top_k=40 * one, top_p=0.9 * one)
+    check(lk, logits, u, near=1, top_k=(N // 2) * one, min_p=1e-4 * one)
+    check(lk, logits, u, near=1, top_p=0.97 * one, temperature=1.3 * one)
+
+
 def test_largest_row(lk):
     """As many logits as a row may have, and tokens a bin too many to count."""
     N = 1 << 21
