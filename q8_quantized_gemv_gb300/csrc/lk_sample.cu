@@ -385,6 +385,9 @@ static __device__ __forceinline__ void run(const SampleArgs& a, unsigned char* s
     if (C == 1) __syncthreads();
     else cl.sync();
   };
+  // A block's shared memory may be written by another once it has begun, which its arrival here
+  // tells; the wait lies behind the row's read, which hides it (nothing is handed over: relaxed).
+  if (C > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" :::);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   if (threadIdx.x == 0) {
     s.listed = 0;
@@ -434,6 +437,7 @@ static __device__ __forceinline__ void run(const SampleArgs& a, unsigned char* s
       s.fwarp[warp] = low;
     }
     __syncthreads();
+    if (C > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
     if (warp == 0) {
       first = ~warp_max_u64(lane < NW ? ~s.warp[lane] : 0ull);
       low = lane < NW ? s.fwarp[lane] : INFINITY;
