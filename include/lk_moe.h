@@ -25,7 +25,7 @@
  *
  * Experts.  Matrix n of a stack [E][rows][K] is a Q8_0 matrix as everywhere
  * (levels int8, f16 scales [E][rows][K/32]), 16-byte aligned both.  rows and K
- * are multiples of 128, E <= LK_MOE_MAX_E, E * rows < 2^31, k * rows < 2^29.
+ * are multiples of 128, E <= LK_MOE_MAX_E, K <= LK_MOE_MAX_LEN, E * rows < 2^31, k * rows < 2^29.
  *
  * What a call writes must not overlap what it reads or anything else it writes
  * (LK_ERR_ARG).
@@ -42,6 +42,7 @@ extern "C" {
 #define LK_MOE_MAX_E 1024  /* experts */
 #define LK_MOE_MAX_K 32    /* experts of a row */
 #define LK_MOE_MAX_GROUPS 32
+#define LK_MOE_MAX_LEN (1 << 30) /* values of a matrix's row */
 
 typedef enum { LK_SCORE_SOFTMAX = 0, LK_SCORE_SIGMOID = 1 } lk_score;
 

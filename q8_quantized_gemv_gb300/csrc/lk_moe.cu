@@ -414,14 +414,19 @@ __global__ void __launch_bounds__(NW * 32, 1) moe_kernel(const MoeArgs a) {
 
 // ---- host --------------------------------------------------------------------------
 
+// Bytes of `rows` activation rows in a block's shared memory (past 32 bits for rows of 2^30), and
+// as many as leave the stages room.
+constexpr unsigned long long kHeld = 200000;
+unsigned long long held_bytes(int mode, int K, int rows) {
+  return (mode == 0 ? 4ull * K : (unsigned long long)K * mode + K / 8u) * rows;
+}
+
 // Stages: whole rows up to SLICE bytes, else the fewest equal slices, and up to four quads of
 // short rows; `quads` of them come to a warp.  Where these are few, two smaller stages a warp
 // instead of one, so that its copies go on while it computes (8 experts of 1024 x 4096 for one
 // row: 15.0 us against 17.0; 64 pairs: 85 against 83).
 bool fit(MoeArgs& a, int mode, int rows_held, int products, long quads, int smem_optin, int* smem) {
-  const unsigned act = mode == 0 ? 4u * a.K : (unsigned)a.K * mode + a.K / 8u;
-  if ((unsigned long long)act * rows_held > 200000u) return false;
-  a.s_products = act * rows_held;  // (a multiple of 16)
+  a.s_products = (unsigned)held_bytes(mode, a.K, rows_held);  // (a multiple of 16)
   a.ring_off = (a.s_products + 4u * products + 127u) & ~127u;
   const int room = smem_optin - kStatic - (int)a.ring_off;
   const int unit = mode == 0 ? 256 : 128;
@@ -474,15 +479,16 @@ bool rows_favoured(int E, int pairs, int mode, bool glu) {
 
 template <bool GLU>
 lk_status launch_moe(MoeArgs& a, int mode, int M, int held, const lk_launch_cfg* cfg, cudaStream_t stream) {
+  const int path = cfg ? cfg->path : 0;
+  if (path == 1 || (path == 3 && mode == 0)) return LK_ERR_SHAPE;
+  const bool rows = path == 3 || (path == 0 && mode != 0 && rows_favoured(a.E, M * a.k, mode, GLU));
+  if (!rows && held_bytes(mode, a.K, held) > kHeld) return LK_ERR_SHAPE;
   const DeviceInfo* d = device_info(nullptr);
   if (!d) return LK_ERR_CUDA;
   a.wait_ns = opt_wait_us > 0 ? (unsigned long long)opt_wait_us * 1000ull : 2000000000ull;
   a.err = error_word_ptr();
   if (!a.err) return LK_ERR_CUDA;
-  const int path = cfg ? cfg->path : 0;
-  if (path == 1 || (path == 3 && mode == 0)) return LK_ERR_SHAPE;
-  if (path == 3 || (path == 0 && mode != 0 && rows_favoured(a.E, M * a.k, mode, GLU)))
-    return moe_rows(a, GLU, mode, M, cfg_pdl(cfg), stream);
+  if (rows) return moe_rows(a, GLU, mode, M, cfg_pdl(cfg), stream);
   int smem = 0;
   // blocks of a row of activations; down: enough that a block's products are few
   int gx = d->sm_count / M;  // (all of them on the SMs at once: a second wave of blocks doubled the time)
@@ -505,7 +511,7 @@ lk_status launch_moe(MoeArgs& a, int mode, int M, int held, const lk_launch_cfg*
 // Checks that both calls make of a stack's shape, the mode, the rows and k.
 lk_status check_shape(int E, int rows, int K, lk_mode mode, int M, int k, const lk_launch_cfg* cfg) {
   if (mode < LK_DEQUANT || mode > LK_TWOPASS || check_launch_cfg(cfg)) return LK_ERR_ARG;
-  if (E < 1 || E > LK_MOE_MAX_E || rows < 128 || rows % 128 || K < 128 || K % 128 || M < 0 || M > LK_MAX_BATCH ||
+  if (E < 1 || E > LK_MOE_MAX_E || rows < 128 || rows % 128 || K < 128 || K % 128 || K > LK_MOE_MAX_LEN || M < 0 || M > LK_MAX_BATCH ||
       k < 1 || k > LK_MOE_MAX_K)
     return LK_ERR_SHAPE;
   // rows of a stack, and tiles of all pairs, are 32-bit numbers
