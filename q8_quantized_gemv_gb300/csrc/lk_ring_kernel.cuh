@@ -733,11 +733,14 @@ __device__ __forceinline__ void finish_quad(typename part_t<Q>::t (&p)[M], const
   }
 }
 
-// Bounded wait on `bar` that ignores the abort flag (used to drain copies).
+// Bounded wait on `bar` that ignores the abort flag, for copies in flight when a
+// block gives up: they would land in shared memory that is another block's by
+// then, so it is a second at least, however short the waits' limit is.
+constexpr unsigned long long kDrainNs = 1000000000ull;
 __device__ __forceinline__ void drain_wait(unsigned bar, unsigned parity, unsigned long long limit_ns, int* err) {
-  const unsigned long long t0 = gtimer();
+  const unsigned long long t0 = gtimer(), limit = limit_ns > kDrainNs ? limit_ns : kDrainNs;
   while (!mbar_try(bar, parity)) {
-    if (gtimer() - t0 > limit_ns) {
+    if (gtimer() - t0 > limit) {
       atomicOr(err, ERR_DRAIN);
       break;
     }
