@@ -85,7 +85,7 @@ lk_status lk_moe_route(const float* logits, const float* bias, int M, int E, lk_
  *        every completed call leaves it zeroed (after LK_ERR_DEVICE_TIMEOUT zero it
  *        again).  Calls that may run at the same time need separate ones
  * LK_ERR_SHAPE where the row of x does not fit in shared memory (K up to 32768
- * always does).
+ * always does): LK_DEQUANT, and with path 2 (the library's choice is path 3 then).
  */
 lk_status lk_moe_glu_q8(const int8_t* wg, const uint16_t* wsg, const int8_t* wu, const uint16_t* wsu, int E, int F,
                         int K, lk_mode mode, const float* x, const int8_t* xq, const int8_t* xl, const float* xs, int M,
@@ -102,7 +102,7 @@ lk_status lk_moe_glu_q8(const int8_t* wg, const uint16_t* wsg, const int8_t* wu,
  *             16-byte aligned
  *   weights   f32 [M][k];  y  f32 [M][N], 16-byte aligned
  * LK_ERR_SHAPE where a row's k activations do not fit in shared memory (k * F up to
- * 32768 always do).
+ * 32768 always do): LK_DEQUANT, and with path 2 (the library's choice is path 3 then).
  */
 lk_status lk_moe_down_q8(const int8_t* wd, const uint16_t* wsd, int E, int N, int F, lk_mode mode, const float* h,
                          const int8_t* hq, const int8_t* hl, const float* hs, int M, const int32_t* ids,

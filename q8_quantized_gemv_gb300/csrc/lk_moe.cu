@@ -481,8 +481,10 @@ template <bool GLU>
 lk_status launch_moe(MoeArgs& a, int mode, int M, int held, const lk_launch_cfg* cfg, cudaStream_t stream) {
   const int path = cfg ? cfg->path : 0;
   if (path == 1 || (path == 3 && mode == 0)) return LK_ERR_SHAPE;
-  const bool rows = path == 3 || (path == 0 && mode != 0 && rows_favoured(a.E, M * a.k, mode, GLU));
-  if (!rows && held_bytes(mode, a.K, held) > kHeld) return LK_ERR_SHAPE;
+  const bool held_fits = held_bytes(mode, a.K, held) <= kHeld;
+  // (the tensor-core kernel streams the activation with the weights: it takes any length)
+  const bool rows = path == 3 || (path == 0 && mode != 0 && (!held_fits || rows_favoured(a.E, M * a.k, mode, GLU)));
+  if (!rows && !held_fits) return LK_ERR_SHAPE;
   const DeviceInfo* d = device_info(nullptr);
   if (!d) return LK_ERR_CUDA;
   a.wait_ns = opt_wait_us > 0 ? (unsigned long long)opt_wait_us * 1000ull : 2000000000ull;

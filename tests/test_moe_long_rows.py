@@ -52,3 +52,14 @@ def test_lengths_that_slices_of_it_would_pass(lib, call, mode, path):
     """The tensor-core kernel takes rows in slices, whose number is rounded up from the length."""
     for K in ((1 << 30) + 128, (1 << 31) - 384, (1 << 31) - 128):
         assert call(lib, mode, K, path) == SHAPE
+
+
+@pytest.mark.parametrize("call", [glu, down])
+@pytest.mark.parametrize("mode,K", [(1, 180000 // 128 * 128), (1, 196608), (2, 102400), (2, 1 << 20), (1, 1 << 20)])
+def test_the_library_takes_them_to_the_kernel_that_holds_none(lib, call, mode, K):
+    """Quantized rows of any length are taken by the library's own choice: the
+    shape is not what a call without a device fails for."""
+    if torch.cuda.is_available():
+        pytest.skip("the addresses are of no memory")
+    assert call(lib, mode, K, 0) != SHAPE
+    assert (call(lib, mode, K, 2) == SHAPE) == (mode * K + K // 8 > 200000)
