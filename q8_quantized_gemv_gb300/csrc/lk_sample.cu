@@ -6,8 +6,8 @@
 // |q| < 2^-6.5, from a quartic in f32 (a table-driven exponential after P. T. P. Tang, ACM
 // TOMS 15(2), 1989): relative error below 2^-29.  Each lane has a copy of the table in its
 // own banks.  Single weights are whole numbers of 2^-39 (the largest is exactly 2^39);
-// a lane's sum over its part of a row is kept as two f32 sums, of the weights'
-// multiples of a grid that makes them exact and of the rests (whole numbers of 64 bits
+// a lane's sum over its part of a row is kept as three f32 sums, of the weights'
+// multiples of two grids that make them exact and of the rests (whole numbers of 64 bits
 // cost three times the instructions), then rounded to a whole number: what is summed over
 // lanes and blocks does not depend on their order.
 //
@@ -122,27 +122,35 @@ struct Weights {
 };
 static_assert(TAB == 64, "parts() shifts by this");
 
-// A weight as a multiple of GRID / 2^23 and what it is more than that.
-constexpr float GRID = 256.0f;
+// A weight as a multiple of GRID / 2^23 = 2^-15, one of FINE_GRID / 2^23 = 2^-31 (2^-16 at most),
+// and what it is more than these: 2^-32 at most, and 2^-25 of the weight.
+constexpr float GRID = 256.0f, FINE_GRID = 0x1p-8f;
 struct Split {
-  float multiple, rest;
+  float multiple, fine, rest;
   __device__ __forceinline__ Split(float big, float small) {
     const float r = __fmul_rn(big, small), hi = __fadd_rn(big, r), lo = __fsub_rn(r, __fsub_rn(hi, big));
     multiple = __fsub_rn(__fadd_rn(hi, 1.5f * GRID), 1.5f * GRID);
-    rest = __fadd_rn(__fsub_rn(hi, multiple), lo);
+    const float more = __fsub_rn(hi, multiple);
+    fine = __fsub_rn(__fadd_rn(more, 1.5f * FINE_GRID), 1.5f * FINE_GRID);
+    rest = __fadd_rn(__fsub_rn(more, fine), lo);
   }
 };
-// A lane's sum of up to GRID of them: of the multiples exactly.
+// A lane's sum of up to GRID of them: of both multiples exactly, and the rests of 256 weights
+// come to 2^-24 at most, so what f32 loses of these is below 2^-41 (one grid only lost
+// 2^-26 where all weights were alike and below 2^-16).
 struct Sum {
-  float high = 0.f, low = 0.f;
+  float high = 0.f, middle = 0.f, low = 0.f;
   u64 all = 0;
   __device__ __forceinline__ void add(const Split& v) {
     high = __fadd_rn(high, v.multiple);
+    middle = __fadd_rn(middle, v.fine);
     low = __fadd_rn(low, v.rest);
   }
   __device__ __forceinline__ void flush() {
-    all += (u64)(__float2ll_rn(__fmul_rn(high, (float)(1ull << ONE))) + __float2ll_rn(__fmul_rn(low, (float)(1ull << ONE))));
-    high = low = 0.f;
+    constexpr float one = (float)(1ull << ONE);
+    all += (u64)(__float2ll_rn(__fmul_rn(high, one)) + __float2ll_rn(__fmul_rn(middle, one)) +
+                 __float2ll_rn(__fmul_rn(low, one)));
+    high = middle = low = 0.f;
   }
 };
 
@@ -674,224 +682,240 @@ static __device__ __forceinline__ void run(const SampleArgs& a, unsigned char* s
       safe = by_p ? min(p_lo, bk) : bk;  // bins before it stay whole
     }
     __syncthreads();
+    // bins by their first places, as place() has them before it takes the whole number out
+    auto from = [&](int b) { return 8388608.0f + (float)(PLACES * b); };
+    // What min_p keeps is a beginning of the order too.  Where it ends in bins that stay whole under
+    // top_k and top_p, it is what is kept, and their borders need not be found; where it ends behind
+    // these bins, they stay whole under it as well (a sum of its own for it took registers: 64 rows of
+    // 151936 with top_p 82 us against 77).  2^-12: log2f's error and the depth's, many times.
+    bool ends_before = false, unsure = false;
+    if (mp > 0.0f && !few && !full) {
+      const float d = -log2f(mp);
+      ends_before = __fadd_rn(__fmul_rn(d + 0x1p-12f, bins.scale), 8388608.0f) < from(safe) - 1.0f;
+      unsure = !ends_before && __fadd_rn(__fmul_rn(d - 0x1p-12f, bins.scale), 8388608.0f) < from(safe);
+    }
     // ---- the sums beside the windows, the tokens in them ----
-    u64 part = 0, kept = 0, mid = 0;
-    if (few) {
-      // (a loop of its own, so short that fetching its code does not count)
-      const float t_k1 = 8388608.0f + (float)(PLACES * (bk + 1));
-      mine.again([&](const float (&l)[4], int i) {
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const float d = w.depth(l[q]);
-          if (d < REACH && __fadd_rn(__fmul_rn(d, bins.scale), 8388608.0f) < t_k1) {
-            const unsigned n = atomicAdd(&s.listed, 1u);
-            if (n < CAP) s.list[n] = key_of(l[q], i + q);
-          }
-        }
-      });
-    } else if (!full) {
-      Sum sum_kept, sum_part, sum_mid;
-      // bins by their first places, as place() has them before it takes the whole number out
-      auto from = [&](int b) { return 8388608.0f + (float)(PLACES * b); };
-      const float t_safe = from(safe), t_lo = from(p_lo), t_hi = from(p_hi + 1), t_k = from(bk), t_k1 = from(bk + 1);
-      int turns = 0;
-      mine.again([&](const float (&l)[4], int i) {
-        // (without branches: the four tokens' chains of dependent steps interleave)
-        float at[4];
-        bool near[4], some = false, sums = false;
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const float d = w.depth(l[q]);
-          at[q] = d < REACH ? __fadd_rn(__fmul_rn(d, bins.scale), 8388608.0f) : INFINITY;
-          near[q] = (at[q] >= t_lo && at[q] < t_hi) || (at[q] >= t_k && at[q] < t_k1);
-          some = some || near[q];
-          sums = sums || (at[q] < t_k && !near[q]);
-        }
-        if (__any_sync(FULL, sums)) {
+    if (!ends_before) {
+      u64 kept = 0, mid = 0;
+      if (few) {
+        // (a loop of its own, so short that fetching its code does not count)
+        const float t_k1 = 8388608.0f + (float)(PLACES * (bk + 1));
+        mine.again([&](const float (&l)[4], int i) {
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
-            float small;
-            const float big = w.parts(l[q], small);
-            const Split e(big, small);
-            if (at[q] < t_safe) sum_kept.add(e);
-            else if (at[q] < t_k && !near[q]) sum_mid.add(e);
-            if (mp > 0.0f && at[q] < t_safe && Weights::enough(big, small, mp)) sum_part.add(e);
-          }
-          if (++turns == (int)GRID / 4) {
-            turns = 0;
-            sum_kept.flush();
-            sum_part.flush();
-            sum_mid.flush();
-          }
-        }
-        if (some)
-#pragma unroll
-          for (int q = 0; q < 4; ++q)
-            if (near[q]) {
+            const float d = w.depth(l[q]);
+            if (d < REACH && __fadd_rn(__fmul_rn(d, bins.scale), 8388608.0f) < t_k1) {
               const unsigned n = atomicAdd(&s.listed, 1u);
               if (n < CAP) s.list[n] = key_of(l[q], i + q);
             }
-      });
-      sum_kept.flush();
-      sum_part.flush();
-      sum_mid.flush();
-      kept = sum_kept.all;
-      mid = sum_mid.all;
-      part = mp > 0.0f ? sum_part.all : kept;
-    }
-    part = warp_sum(part);
-    if (lane == 0) cl.map_shared_rank(&s, 0)->drawn[slot] = part;
-    kept = block_sum(kept, s);
-    mid = block_sum(mid, s);
-    if (threadIdx.x < C) {
-      Shared* to = cl.map_shared_rank(&s, threadIdx.x);
-      to->n_list[me] = s.listed;
-      to->kept[me] = kept;
-      to->mid[me] = mid;
-    }
-    meet();
-    unsigned listed = 0;
-    for (int q = 0; q < C; ++q) listed += s.n_list[q];
-    if (listed <= CAP && !full) {
-      summed = true;
-      if (me == 0) {
-        kept = mid = 0;
-        for (int q = 0; q < C; ++q) {
-          kept += s.kept[q];
-          mid += s.mid[q];
-        }
-        for (unsigned i = threadIdx.x; i < listed; i += THREADS) {
-          unsigned j = i;
-          int q = 0;
-          while (j >= s.n_list[q]) j -= s.n_list[q++];
-          s.sorted[i] = cl.map_shared_rank(&s, q)->list[j];
-        }
-        __syncthreads();
-        if (listed <= THREADS) {
-          // a key a thread; neighbours below 32 meet by shuffles
-          const unsigned i = threadIdx.x;
-          unsigned pad = 32;
-          while (pad < listed) pad *= 2;
-          u64 v = i < listed ? s.sorted[i] : ~0ull;
-#pragma unroll 1
-          for (unsigned k = 2; k <= pad; k *= 2)
-#pragma unroll 1
-            for (unsigned j = k / 2; j > 0; j /= 2) {
-              u64 o;
-              if (j >= 32) {
-                __syncthreads();
-                s.sorted[i] = v;
-                __syncthreads();
-                o = s.sorted[i ^ j];
-              } else {
-                o = __shfl_xor_sync(FULL, v, j);
-              }
-              v = (((i & j) == 0) == ((i & k) == 0)) == (o < v) ? o : v;
-            }
-          __syncthreads();
-          s.sorted[i] = v;
-        } else {
-          unsigned pad = THREADS;
-          while (pad < listed) pad *= 2;
-          for (unsigned i = listed + threadIdx.x; i < pad; i += THREADS) s.sorted[i] = ~0ull;
-          __syncthreads();
-#pragma unroll 1
-          for (unsigned k = 2; k <= pad; k *= 2)
-#pragma unroll 1
-            for (unsigned j = k / 2; j > 0; j /= 2) {
-              for (unsigned i = threadIdx.x; i < pad / 2; i += THREADS) {
-                const unsigned p = 2 * i - (i & (j - 1)), q = p + j;
-                const u64 y = s.sorted[p], z = s.sorted[q];
-                if ((y > z) == !(p & k)) {
-                  s.sorted[p] = z;
-                  s.sorted[q] = y;
-                }
-              }
-              __syncthreads();
-            }
-        }
-        __syncthreads();
-        // the border among them: of top_k the nk-th of its bin, of top_p the first whose sum reaches
-        u64* weight = s.list;  // of the sorted keys (the block's own list is in sorted[] now)
-        const bool k_there = by_k && bk < NB;
-#pragma unroll 1
-        for (unsigned i = threadIdx.x; i < listed; i += THREADS) weight[i] = w.of(value_of(s.sorted[i]));
-        __syncthreads();
-        if (warp == 0) {
-          unsigned stay = listed;
-          if (k_there) {
-            unsigned before = 0;  // of the keys, those before the top_k bin
-            if (!few)
-              for (unsigned i = lane; i < listed; i += 32)
-                before += (int)(bins.place(w.depth(value_of(s.sorted[i]))) / PLACES) < bk;
-            stay = __reduce_add_sync(FULL, before) + nk;
           }
-          u64 key = stay ? s.sorted[stay - 1] : 0ull;
-          if (by_p) {
-            u64 z = 0;
-#pragma unroll 1
-            for (unsigned i = lane; i < stay; i += 32) z += weight[i];
-            z = warp_sum(z) + kept + mid;
-            const u64 want = share_up(fmaxf(tp, 0.f), z), goal = want ? want : 1ull;
-            u64 run = kept;
-#pragma unroll 1
-            for (unsigned i0 = 0; i0 < stay; i0 += 32) {
-              u64 inc = i0 + lane < stay ? weight[i0 + lane] : 0ull;
+        });
+      } else if (!full) {
+        Sum sum_kept, sum_mid;
+        const float t_safe = from(safe), t_lo = from(p_lo), t_hi = from(p_hi + 1), t_k = from(bk), t_k1 = from(bk + 1);
+        int turns = 0;
+        mine.again([&](const float (&l)[4], int i) {
+          // (without branches: the four tokens' chains of dependent steps interleave)
+          float at[4];
+          bool near[4], some = false, sums = false;
 #pragma unroll
-              for (int o = 1; o < 32; o <<= 1) {
-                const u64 y = __shfl_up_sync(FULL, inc, o);
-                if (lane >= o) inc += y;
-              }
-              const unsigned there = __ballot_sync(FULL, run + inc >= goal);
-              if (there) {
-                const unsigned i = i0 + __ffs(there) - 1;
-                key = s.sorted[i < stay ? i : stay - 1];
-                break;
-              }
-              run += __shfl_sync(FULL, inc, 31);
+          for (int q = 0; q < 4; ++q) {
+            const float d = w.depth(l[q]);
+            at[q] = d < REACH ? __fadd_rn(__fmul_rn(d, bins.scale), 8388608.0f) : INFINITY;
+            near[q] = (at[q] >= t_lo && at[q] < t_hi) || (at[q] >= t_k && at[q] < t_k1);
+            some = some || near[q];
+            sums = sums || (at[q] < t_k && !near[q]);
+          }
+          if (__any_sync(FULL, sums)) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              float small;
+              const float big = w.parts(l[q], small);
+              const Split e(big, small);
+              if (at[q] < t_safe) sum_kept.add(e);
+              else if (at[q] < t_k && !near[q]) sum_mid.add(e);
+            }
+            if (++turns == (int)GRID / 4) {
+              turns = 0;
+              sum_kept.flush();
+              sum_mid.flush();
             }
           }
-          // all keys where no border is in the bins
-          if (lane == 0) s.last = !by_p && !k_there ? ~0ull : key;
-        }
-        __syncthreads();
-        last = s.last;
-#pragma unroll 1
-        for (unsigned i = threadIdx.x; i < listed; i += THREADS)
-          if (s.sorted[i] <= last && (mp == 0.0f || w.enough(value_of(s.sorted[i]), mp)))
-            atomicAdd(&s.drawn[((unsigned)(s.sorted[i] & 0xFFFFFFFFu) + skew) / (unsigned)a.part], weight[i]);
-        __syncthreads();
+          if (some)
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+              if (near[q]) {
+                const unsigned n = atomicAdd(&s.listed, 1u);
+                if (n < CAP) s.list[n] = key_of(l[q], i + q);
+              }
+        });
+        sum_kept.flush();
+        sum_mid.flush();
+        kept = sum_kept.all;
+        mid = sum_mid.all;
       }
-    } else {
-      // too many tokens near a border (equal ones, as a rule): by halving the keys
-      int turn = 0;
-      auto whole = [&](u64 v) {
-        v = block_sum(v, s);
-        if (threadIdx.x < C) cl.map_shared_rank(&s, threadIdx.x)->sums[turn][me] = v;
-        meet();
-        u64 r = 0;
-        for (int q = 0; q < C; ++q) r += s.sums[turn][q];
-        turn ^= 1;
-        return r;
-      };
-      auto upto = [&](u64 key, bool weigh) {
-        return whole(sum_up_to(key, weigh, 0.0f));
-      };
-      auto border = [&](bool weigh, u64 want, u64 top) {
-        u64 bottom = first;
-        while (bottom < top) {
-          const u64 half = bottom + (top - bottom) / 2;
-          if (upto(half, weigh) >= want) top = half;
-          else bottom = half + 1;
+      const u64 part = warp_sum(kept);
+      if (lane == 0) cl.map_shared_rank(&s, 0)->drawn[slot] = part;
+      kept = block_sum(kept, s);
+      mid = block_sum(mid, s);
+      if (threadIdx.x < C) {
+        Shared* to = cl.map_shared_rank(&s, threadIdx.x);
+        to->n_list[me] = s.listed;
+        to->kept[me] = kept;
+        to->mid[me] = mid;
+      }
+      meet();
+      unsigned listed = 0;
+      for (int q = 0; q < C; ++q) listed += s.n_list[q];
+      if (listed <= CAP && !full) {
+        summed = !unsure;
+        if (me == 0) {
+          kept = mid = 0;
+          for (int q = 0; q < C; ++q) {
+            kept += s.kept[q];
+            mid += s.mid[q];
+          }
+          for (unsigned i = threadIdx.x; i < listed; i += THREADS) {
+            unsigned j = i;
+            int q = 0;
+            while (j >= s.n_list[q]) j -= s.n_list[q++];
+            s.sorted[i] = cl.map_shared_rank(&s, q)->list[j];
+          }
+          __syncthreads();
+          if (listed <= THREADS) {
+            // a key a thread; neighbours below 32 meet by shuffles
+            const unsigned i = threadIdx.x;
+            unsigned pad = 32;
+            while (pad < listed) pad *= 2;
+            u64 v = i < listed ? s.sorted[i] : ~0ull;
+#pragma unroll 1
+            for (unsigned k = 2; k <= pad; k *= 2)
+#pragma unroll 1
+              for (unsigned j = k / 2; j > 0; j /= 2) {
+                u64 o;
+                if (j >= 32) {
+                  __syncthreads();
+                  s.sorted[i] = v;
+                  __syncthreads();
+                  o = s.sorted[i ^ j];
+                } else {
+                  o = __shfl_xor_sync(FULL, v, j);
+                }
+                v = (((i & j) == 0) == ((i & k) == 0)) == (o < v) ? o : v;
+              }
+            __syncthreads();
+            s.sorted[i] = v;
+          } else {
+            unsigned pad = THREADS;
+            while (pad < listed) pad *= 2;
+            for (unsigned i = listed + threadIdx.x; i < pad; i += THREADS) s.sorted[i] = ~0ull;
+            __syncthreads();
+#pragma unroll 1
+            for (unsigned k = 2; k <= pad; k *= 2)
+#pragma unroll 1
+              for (unsigned j = k / 2; j > 0; j /= 2) {
+                for (unsigned i = threadIdx.x; i < pad / 2; i += THREADS) {
+                  const unsigned p = 2 * i - (i & (j - 1)), q = p + j;
+                  const u64 y = s.sorted[p], z = s.sorted[q];
+                  if ((y > z) == !(p & k)) {
+                    s.sorted[p] = z;
+                    s.sorted[q] = y;
+                  }
+                }
+                __syncthreads();
+              }
+          }
+          __syncthreads();
+          // the border among them: of top_k the nk-th of its bin, of top_p the first whose sum reaches
+          u64* weight = s.list;  // of the sorted keys (the block's own list is in sorted[] now)
+          const bool k_there = by_k && bk < NB;
+#pragma unroll 1
+          for (unsigned i = threadIdx.x; i < listed; i += THREADS) weight[i] = w.of(value_of(s.sorted[i]));
+          __syncthreads();
+          if (warp == 0) {
+            unsigned stay = listed;
+            if (k_there) {
+              unsigned before = 0;  // of the keys, those before the top_k bin
+              if (!few)
+                for (unsigned i = lane; i < listed; i += 32)
+                  before += (int)(bins.place(w.depth(value_of(s.sorted[i]))) / PLACES) < bk;
+              stay = __reduce_add_sync(FULL, before) + nk;
+            }
+            u64 key = stay ? s.sorted[stay - 1] : 0ull;
+            if (by_p) {
+              u64 z = 0;
+#pragma unroll 1
+              for (unsigned i = lane; i < stay; i += 32) z += weight[i];
+              z = warp_sum(z) + kept + mid;
+              const u64 want = share_up(fmaxf(tp, 0.f), z), goal = want ? want : 1ull;
+              u64 run = kept;
+#pragma unroll 1
+              for (unsigned i0 = 0; i0 < stay; i0 += 32) {
+                u64 inc = i0 + lane < stay ? weight[i0 + lane] : 0ull;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                  const u64 y = __shfl_up_sync(FULL, inc, o);
+                  if (lane >= o) inc += y;
+                }
+                const unsigned there = __ballot_sync(FULL, run + inc >= goal);
+                if (there) {
+                  const unsigned i = i0 + __ffs(there) - 1;
+                  key = s.sorted[i < stay ? i : stay - 1];
+                  break;
+                }
+                run += __shfl_sync(FULL, inc, 31);
+              }
+            }
+            // all keys where no border is in the bins
+            if (lane == 0) s.last = !by_p && !k_there ? ~0ull : key;
+          }
+          __syncthreads();
+          last = s.last;
+          if (unsure) {
+            if (threadIdx.x < C) cl.map_shared_rank(&s, threadIdx.x)->last = last;
+          } else {
+#pragma unroll 1
+            for (unsigned i = threadIdx.x; i < listed; i += THREADS)
+              if (s.sorted[i] <= last && (mp == 0.0f || w.enough(value_of(s.sorted[i]), mp)))
+                atomicAdd(&s.drawn[((unsigned)(s.sorted[i] & 0xFFFFFFFFu) + skew) / (unsigned)a.part], weight[i]);
+          }
+          __syncthreads();
         }
-        return bottom;
-      };
-      const u64 end = key_of(low, (unsigned)N);
-      last = end;
-      if (by_k && upto(end, false) >= (u64)tk) last = border(false, tk, end);
-      if (by_p) {
-        const u64 want = share_up(fmaxf(tp, 0.f), upto(last, true));
-        last = border(true, want ? want : 1ull, last);
+        if (unsure) {  // (the sums of all blocks' tokens up to the border, below)
+          meet();
+          last = s.last;
+        }
+      } else {
+        // too many tokens near a border (equal ones, as a rule): by halving the keys
+        int turn = 0;
+        auto whole = [&](u64 v) {
+          v = block_sum(v, s);
+          if (threadIdx.x < C) cl.map_shared_rank(&s, threadIdx.x)->sums[turn][me] = v;
+          meet();
+          u64 r = 0;
+          for (int q = 0; q < C; ++q) r += s.sums[turn][q];
+          turn ^= 1;
+          return r;
+        };
+        auto upto = [&](u64 key, bool weigh) {
+          return whole(sum_up_to(key, weigh, 0.0f));
+        };
+        auto border = [&](bool weigh, u64 want, u64 top) {
+          u64 bottom = first;
+          while (bottom < top) {
+            const u64 half = bottom + (top - bottom) / 2;
+            if (upto(half, weigh) >= want) top = half;
+            else bottom = half + 1;
+          }
+          return bottom;
+        };
+        const u64 end = key_of(low, (unsigned)N);
+        last = end;
+        if (by_k && upto(end, false) >= (u64)tk) last = border(false, tk, end);
+        if (by_p) {
+          const u64 want = share_up(fmaxf(tp, 0.f), upto(last, true));
+          last = border(true, want ? want : 1ull, last);
+        }
       }
     }
   }
