@@ -30,13 +30,15 @@ extern "C" {
  *   min_p > 0    of these the ones with e_i >= min(min_p, 1)
  *   idx          the lowest index i such that the sum of e over the tokens that
  *                stay, from the lowest index up to i, exceeds u times their sum
- *                (u >= 1: the last of them with e above 0)
- *   prob         optional f32 [M]: e_idx over that sum
+ *                (u >= 1: as the largest number below 1)
+ *   prob         optional f32 [M]: e_idx over that sum, to 2^-22 relatively
  * A logit of NaN counts as -inf (never drawn), +inf as the largest f32; a row
- * without any other gets idx -1, prob 0.  The e are formed to 2^-29 relatively
- * and summed to about 2^-37 of the largest: the token differs from the exact one only
- * where u or top_p lies within about 2^-28 of a border between tokens (min_p within
- * 2^-29 of a token's e).  The same call gives the same bits; the same row among others
+ * without any other gets idx -1, prob 0.  A difference of logits past f32's range is an
+ * infinite one.  The e are formed to 2^-29 relatively; those below 2^-48.5 count
+ * as 0, all of them together less than N 2^-48.5; sums are within 2^-28 but for
+ * these: the token differs from the exact one only where u or top_p lies within 2^-27 (N
+ * above 2^18: 2^-26) of a border between tokens, or min_p within 2^-29 of a
+ * token's e, relatively.  The same call gives the same bits; the same row among others
  * (M, or another alignment of its logits) the same token but for such borders.
  *   u    f32 [M], >= 0 (below 0 or NaN: 0);  idx int32 [M]
  * What is written must not overlap what is read (LK_ERR_ARG).

@@ -5,7 +5,9 @@
 // 2^(frac) comes from a table of 64, and the remaining factor, 1 + q with
 // |q| < 2^-6.5, from a quartic in f32 (a table-driven exponential after P. T. P. Tang, ACM
 // TOMS 15(2), 1989): relative error below 2^-29.  Each lane has a copy of the table in its
-// own banks.  Single weights are whole numbers of 2^-39 (the largest is exactly 2^39);
+// own banks.  Weights below 2^-REACH of the largest count as nothing, N of them for N 2^-48.5 of
+// it.  Sums are whole numbers of 2^-42 (all of a row's fit in 64 bits), and those of a warp's
+// part, in which the token is found, of 2^-48, so that no weight that counts is rounded to 0;
 // a lane's sum over its part of a row is kept as three f32 sums, of the weights'
 // multiples of two grids that make them exact and of the rests (whole numbers of 64 bits
 // cost three times the instructions), then rounded to a whole number: what is summed over
@@ -31,12 +33,13 @@ namespace {
 
 typedef unsigned long long u64;
 
-constexpr int ONE = 39;                         // a weight of 1 is 2^39
+constexpr int ONE = 42;                         // a weight of 1 is 2^42,
+constexpr int FINE = 48;                        // within a part 2^48
 
 // ---- the weights -------------------------------------------------------------------
 
 constexpr int TAB = 64;                         // entries of the table
-constexpr float REACH = 41.0f;                  // 2^-REACH of the largest and below is nothing
+constexpr float REACH = 48.5f;                  // 2^-REACH of the largest and below is nothing
 
 // 2^(j/TAB): as a float, and what it is more than that, relatively (exp's series in f64 on
 // the host, of which an f32 rest keeps enough)
@@ -99,17 +102,17 @@ struct Weights {
     small = fmaf(f, fmaf(f, fmaf(f, fmaf(f, 0.0096181291f, 0.055504109f), 0.24022651f), 0.69314718f), t.y);
     return __int_as_float(__float_as_int(t.x) + (k >> 6) * (1 << 23));
   }
-  // as a whole number of 2^-ONE, rounded to nearest
-  __device__ __forceinline__ u64 of(float l, float depth) const {
+  // as a whole number of 2^-BITS, rounded to nearest
+  template <int BITS>
+  __device__ __forceinline__ u64 of(float l) const {
     float small;
     const float big = parts(l, small);
-    // big is a multiple of 2^-64 2^-ONE, so in two steps: its integer (exact or nearest), and the rest
-    const float scaled = __fmul_rn(big, (float)(1ull << ONE)), rest = __fmul_rn(scaled, small);
+    // in two steps: the integer of big (exact or nearest), and the rest
+    const float scaled = __fmul_rn(big, (float)(1ull << BITS)), rest = __fmul_rn(scaled, small);
     const long long whole = __float2ll_rn(scaled);
     const float left = __fadd_rn(__fsub_rn(scaled, __ll2float_rn(whole)), rest);
-    return depth < REACH ? (u64)(whole + __float2ll_rn(left)) : 0ull;
+    return depth(l) < REACH ? (u64)(whole + __float2ll_rn(left)) : 0ull;
   }
-  __device__ __forceinline__ u64 of(float l) const { return of(l, depth(l)); }
   // e >= min_p, the same answer wherever it is asked
   static __device__ __forceinline__ bool enough(float big, float small, float min_p) {
     return __fmaf_rn(big, small, __fsub_rn(big, min_p)) >= 0.0f;
@@ -213,9 +216,9 @@ static constexpr int PLACES = 32768 / NB;           // places in a bin
 static constexpr int POS_BITS = NW == 32 ? 18 : NW == 16 ? 19 : 20;  // a bin's word: the sum of its tokens' places, above it
                                                     // their number, below 2^(32 - POS_BITS)
 // Of the bins' estimated sums.  A bin's sum of weights is estimated from its tokens' mean
-// place: within (ln2 * width)^2 / 8 of it (width 41 / NB at most: 2.4e-5, 1e-4 or 3.9e-4), half a
-// place's rounding (4.4e-4) and the f32 sums.
-static constexpr float SLACK = NW == 8 ? 1e-3f : 6e-4f;
+// place: within (ln2 * width)^2 / 8 of it (width REACH / (NB - 1) at most: 3.4e-5, 1.4e-4 or 5.4e-4),
+// half a place's rounding (5.2e-4) and the f32 sums.
+static constexpr float SLACK = NW == 8 ? 1.3e-3f : 8e-4f;
 
 struct alignas(16) Shared {
   float2 table[TAB * 32];
@@ -830,7 +833,7 @@ static __device__ __forceinline__ void run(const SampleArgs& a, unsigned char* s
           u64* weight = s.list;  // of the sorted keys (the block's own list is in sorted[] now)
           const bool k_there = by_k && bk < NB;
 #pragma unroll 1
-          for (unsigned i = threadIdx.x; i < listed; i += THREADS) weight[i] = w.of(value_of(s.sorted[i]));
+          for (unsigned i = threadIdx.x; i < listed; i += THREADS) weight[i] = w.template of<ONE>(value_of(s.sorted[i]));
           __syncthreads();
           if (warp == 0) {
             unsigned stay = listed;
@@ -962,8 +965,8 @@ static __device__ __forceinline__ void run(const SampleArgs& a, unsigned char* s
   const u64 goal = s.goal, total = s.kept[0];
   const int begin = max(0, s.at * a.part - skew), end = min(N, (s.at + 1) * a.part - skew);
   // (The part's sum was rounded lane by lane: should the goal lie past what its tokens come
-  // to here, the second turn takes the last of them.)
-  u64 run = 0, want = goal;
+  // to here, the second turn takes the last of them.  A part with a sum has tokens that count.)
+  u64 run = 0, want = goal << (FINE - ONE);
 #pragma unroll 1
   for (int turn = 0; turn < 2; ++turn) {
     run = 0;
@@ -971,7 +974,7 @@ static __device__ __forceinline__ void run(const SampleArgs& a, unsigned char* s
     for (int i0 = begin; i0 < end && run <= want; i0 += THREADS) {
       const int i = i0 + threadIdx.x;
       const float l = i < end ? clean(__ldcg(x + i)) : -INFINITY;
-      u64 e = i < end && key_of(l, i) <= last && (mp == 0.0f || w.enough(l, mp)) ? w.of(l) : 0ull;
+      u64 e = i < end && key_of(l, i) <= last && (mp == 0.0f || w.enough(l, mp)) ? w.template of<FINE>(l) : 0ull;
       u64 all;
       const u64 r = run + block_before(e, all, s);
       if (r <= want && r + e > want) {
@@ -984,12 +987,8 @@ static __device__ __forceinline__ void run(const SampleArgs& a, unsigned char* s
       }
       run += all;
     }
-    if (run > want || run == 0) break;
+    if (run > want) break;
     want = run - 1;
-  }
-  if (run == 0 && threadIdx.x == 0) {  // nothing but weights that single tokens round to 0: the first
-    a.idx[row] = (int)(first & 0xFFFFFFFFu);
-    if (a.prob) a.prob[row] = __fdiv_rn((float)(1ull << ONE), __ull2float_rn(total));
   }
 }
 
@@ -1002,6 +1001,8 @@ __global__ void __launch_bounds__(32 * NW) sample_kernel(const SampleArgs a) {
 }
 
 constexpr int LARGE = 32768, SMALL = 6144;  // tokens of a block above which it has 32 (16) warps
+constexpr int MOST = 1 << 20;               // tokens of a block: more would pass 64 bits in a part's sum
+static_assert(((unsigned long long)MOST / 32 + 128) <= (~0ull >> FINE), "a part's sum");
 
 template <int NW, int MAX_C>
 lk_status launch_rows(SampleArgs a, int M, int dev, int pdl, cudaStream_t stream) {
@@ -1087,7 +1088,7 @@ extern "C" lk_status lk_sample(const float* logits, int M, int N, const float* t
   // blocks of a row: as many as are on the SMs at once with all rows', none with less than 2048 tokens
   // (one row of 151936 in 16 blocks, not 8: top_p 31 -> 24 us, top_k 50 and top_p 17 -> 15)
   int C = 1;
-  for (int i = 0; i < 4 && M <= ((fits >> (8 * i)) & 127) && N >= C * 4096; ++i) C *= 2;
+  for (int i = 0; i < 4 && ((M <= ((fits >> (8 * i)) & 127) && N >= C * 4096) || N > C * MOST); ++i) C *= 2;
   const SampleArgs a = {logits, N, C, 0, 0, temperature, top_k, top_p, min_p, u, idx, prob};
   const int pdl = cfg_pdl(cfg), tokens = N / C;
   if (C == 16)
