@@ -602,8 +602,10 @@ static __device__ __forceinline__ void run(const SampleArgs& a, unsigned char* s
       }
       __syncthreads();
     };
+    // bins by their first places, as place() has them before it takes the whole number out
+    auto from = [&](int b) { return 8388608.0f + (float)(PLACES * b); };
     int bk = NB, nk = 0, p_lo = NB, p_hi = -1, safe = 0;
-    bool full = false;
+    bool full = false, ends_before = false, unsure = false;
     if (few) {
       if (top > -INFINITY) count(top);
       merge();
@@ -683,20 +685,17 @@ static __device__ __forceinline__ void run(const SampleArgs& a, unsigned char* s
         p_lo = min(mark[2], p_hi);
       }
       safe = by_p ? min(p_lo, bk) : bk;  // bins before it stay whole
+      // What min_p keeps is a beginning of the order too.  Where it ends in bins that stay whole under
+      // top_k and top_p, it is what is kept, and their borders need not be found; where it ends behind
+      // these bins, they stay whole under it as well (a sum of its own for it took registers: 64 rows of
+      // 151936 with top_p 82 us against 77).  2^-12: log2f's error and the depth's, many times.
+      if (mp > 0.0f && !full) {
+        const float d = -log2f(mp);
+        ends_before = __fadd_rn(__fmul_rn(d + 0x1p-12f, bins.scale), 8388608.0f) < from(safe) - 1.0f;
+        unsure = !ends_before && __fadd_rn(__fmul_rn(d - 0x1p-12f, bins.scale), 8388608.0f) < from(safe);
+      }
     }
     __syncthreads();
-    // bins by their first places, as place() has them before it takes the whole number out
-    auto from = [&](int b) { return 8388608.0f + (float)(PLACES * b); };
-    // What min_p keeps is a beginning of the order too.  Where it ends in bins that stay whole under
-    // top_k and top_p, it is what is kept, and their borders need not be found; where it ends behind
-    // these bins, they stay whole under it as well (a sum of its own for it took registers: 64 rows of
-    // 151936 with top_p 82 us against 77).  2^-12: log2f's error and the depth's, many times.
-    bool ends_before = false, unsure = false;
-    if (mp > 0.0f && !few && !full) {
-      const float d = -log2f(mp);
-      ends_before = __fadd_rn(__fmul_rn(d + 0x1p-12f, bins.scale), 8388608.0f) < from(safe) - 1.0f;
-      unsure = !ends_before && __fadd_rn(__fmul_rn(d - 0x1p-12f, bins.scale), 8388608.0f) < from(safe);
-    }
     // ---- the sums beside the windows, the tokens in them ----
     if (!ends_before) {
       u64 kept = 0, mid = 0;
