@@ -73,7 +73,8 @@ lk_status lk_moe_route(const float* logits, const float* bias, int M, int E, lk_
  * The gate and up products of every pair and their SwiGLU: with e = ids[t][j],
  *   h[t*k + j] = swiglu(Wg_e x_t, Wu_e x_t),
  * each product as lk_gemv_q8 forms it in this mode (the same bits in the
- * quantized modes), the SwiGLU as lk_swiglu_quant.  An absent pair's rows are
+ * quantized modes; LK_DEQUANT within 1e-5 of sum |w x|, its f32 sums over
+ * 4096 values at most added without loss), the SwiGLU as lk_swiglu_quant.  An absent pair's rows are
  * left as they are.
  *   wg, wsg / wu, wsu   stacks [E][F][K]
  *   x, xq, xl, xs       the M rows by mode, as lk_gemv_q8's, 16-byte aligned

@@ -94,7 +94,7 @@ struct ActLoad {
 };
 
 // What a lane has of its item's four rows: under Dequant its part of each row, in packed
-// halves; else partial (lane & 7) / 2 of row lane / 8, in the even lanes.
+// halves, and for rows in several slices what rounding took off it; else partial (lane & 7) / 2 of row lane / 8, in the even lanes.
 template <int Q>
 struct Partial {
   float p;
@@ -102,10 +102,10 @@ struct Partial {
 };
 template <>
 struct Partial<0> {
-  f32x2 p[QR];
+  f32x2 p[QR], rest[QR];
   __device__ __forceinline__ void clear() {
 #pragma unroll
-    for (int r = 0; r < QR; ++r) p[r] = f2_pack(0.f, 0.f);
+    for (int r = 0; r < QR; ++r) p[r] = rest[r] = f2_pack(0.f, 0.f);
   }
 };
 
@@ -119,10 +119,12 @@ __device__ __forceinline__ void levels4(unsigned u, f32x2& w01, f32x2& w23) {
 // A stage's part of four rows against the activation at `act` (K its whole length); row r
 // of the four is row base + (r & 1) + hop * (r >> 1) of the stage.
 // Dequant: lane l has values 8l .. 8l + 7 of a stretch of 256, of one block, of all four rows
-// (4l .. 4l + 3 of a last 128); the stage's sums are added to the item's, so a row of K
-// values has K / 256 + slices + 15 roundings at most in a chain, all in f32: within
-// 5e-6 of sum |w x| up to K 16384.
-template <int Q>
+// (4l .. 4l + 3 of a last 128).  The stage's sums are f32, over 16 steps at most; what is
+// rounded off when they are added to the item's is kept beside these (D. E. Knuth's two-sum), so a
+// value passes 16 + 4 roundings, and 7 behind: within 2e-6 of sum |w x| whatever the number of slices
+// (in f32 alone the chain was as long as the slices are many: 195 at most, 1.2e-5).
+// (SLICED: rows in several slices.  The two-sum of rows in one took 2 %.)
+template <int Q, bool SLICED>
 __device__ __forceinline__ void quad_stage(Partial<Q>& p, const unsigned char* st, const MoeArgs& a, int k0, int len,
                                            int base, int hop, const unsigned char* act, int lane) {
   if constexpr (Q == 0) {
@@ -164,7 +166,14 @@ __device__ __forceinline__ void quad_stage(Partial<Q>& p, const unsigned char* s
       }
     }
 #pragma unroll
-    for (int r = 0; r < QR; ++r) p.p[r] = f2_add(p.p[r], acc[r]);
+    for (int r = 0; r < QR; ++r) {
+      const f32x2 a0 = p.p[r], minus = f2_pack(-1.f, -1.f), sum = f2_add(a0, acc[r]);
+      p.p[r] = sum;
+      if constexpr (!SLICED) continue;
+      auto less = [&](f32x2 x, f32x2 y) { return f2_fma(y, minus, x); };  // x - y
+      const f32x2 b = less(sum, a0);
+      p.rest[r] = f2_add(p.rest[r], f2_add(less(a0, less(sum, b)), less(acc[r], b)));
+    }
   } else {
     const int nseg = len >> 7;
     const int rr = lane >> 3, j = lane & 7, q = j >> 1, row = base + (rr & 1) + hop * (rr >> 1);
@@ -190,7 +199,7 @@ __device__ __forceinline__ void quad_stage(Partial<Q>& p, const unsigned char* s
 
 // The product of each row r, in lane 8 r: Dequant the sum over the lanes, else
 // (p0 + p2) + (p1 + p3).
-template <int Q>
+template <int Q, bool SLICED>
 __device__ __forceinline__ float row_sum(const Partial<Q>& p, int lane) {
   if constexpr (Q == 0) {
     float v[QR];
@@ -199,6 +208,14 @@ __device__ __forceinline__ float row_sum(const Partial<Q>& p, int lane) {
       float lo, hi;
       f2_unpack(p.p[r], lo, hi);
       v[r] = __fadd_rn(lo, hi);
+    }
+    if constexpr (SLICED) {
+#pragma unroll
+      for (int r = 0; r < QR; ++r) {
+        float lo, hi;
+        f2_unpack(p.rest[r], lo, hi);
+        if (v[r] - v[r] == 0.f) v[r] = __fadd_rn(v[r], __fadd_rn(lo, hi));  // (not finite: it has no rest)
+      }
     }
     // lanes 16 apart take two rows each, lanes 8 apart one of these
     const bool up = lane & 16, odd = lane & 8;
@@ -214,7 +231,7 @@ __device__ __forceinline__ float row_sum(const Partial<Q>& p, int lane) {
   }
 }
 
-template <int Q, bool GLU>
+template <int Q, bool GLU, bool SLICED>
 __global__ void __launch_bounds__(NW * 32, 1) moe_kernel(const MoeArgs a) {
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ unsigned long long bars[NW * DEPTH];
@@ -347,9 +364,9 @@ __global__ void __launch_bounds__(NW * 32, 1) moe_kernel(const MoeArgs a) {
     unsigned char* st = ring + (size_t)slot * a.stage_bytes;
     const unsigned char* x = smem + (GLU ? 0 : at.i * act_bytes<Q>(a.K));
     for (int q = 0; q < at.n; ++q) {
-      quad_stage<Q>(p, st, a, k0, len, (GLU ? 2 : 4) * q, hop, x, lane);
+      quad_stage<Q, SLICED>(p, st, a, k0, len, (GLU ? 2 : 4) * q, hop, x, lane);
       if (at.c < a.nsl - 1) break;  // (a slice: one quad, its sums go on)
-      const float v = row_sum<Q>(p, lane);
+      const float v = row_sum<Q, SLICED>(p, lane);
       p.clear();
       if (GLU) {
         const float u = __shfl_down_sync(FULL, v, 16);
@@ -460,10 +477,10 @@ bool fit(MoeArgs& a, int mode, int rows_held, int products, long quads, int smem
   return found;
 }
 
-template <int Q, bool GLU>
+template <int Q, bool GLU, bool SLICED = false>
 lk_status run(const MoeArgs& a, dim3 grid, int smem, int optin, int pdl, cudaStream_t stream) {
   static std::atomic<int> done[kMaxDevices];
-  return launch_moe_kernel(moe_kernel<Q, GLU>, done, grid, NW * 32, smem, optin - kStatic, pdl, stream, a);
+  return launch_moe_kernel(moe_kernel<Q, GLU, SLICED>, done, grid, NW * 32, smem, optin - kStatic, pdl, stream, a);
 }
 
 // Whether the tensor-core kernel, which reads a shared expert once, is faster than
@@ -505,7 +522,8 @@ lk_status launch_moe(MoeArgs& a, int mode, int M, int held, const lk_launch_cfg*
   if (!fit(a, mode, held, products, quads, d->smem_optin, &smem)) return LK_ERR_SHAPE;
   const dim3 grid(gx, M);
   const int pdl = cfg_pdl(cfg);
-  return mode == 0   ? run<0, GLU>(a, grid, smem, d->smem_optin, pdl, stream)
+  return mode == 0   ? (a.nsl > 1 ? run<0, GLU, true>(a, grid, smem, d->smem_optin, pdl, stream)
+                                  : run<0, GLU>(a, grid, smem, d->smem_optin, pdl, stream))
          : mode == 1 ? run<1, GLU>(a, grid, smem, d->smem_optin, pdl, stream)
                      : run<2, GLU>(a, grid, smem, d->smem_optin, pdl, stream);
 }

@@ -58,3 +58,55 @@ def test_gate_up_where_the_row_does_not_fit(lk, mode):
     lk.lk_moe_glu_q8(lk.Experts(gate=gate, up=up), m, ids, h, **acts)
     want, tol = glu_ref(gate, up, acts, m, ids, E)
     assert bool(((h.double() - want).abs() <= tol).all())
+
+
+def test_dequant_sums_over_many_slices(lk):
+    """Equal products, so that every slice's sum is the same and rounds the same way when
+    it is added: 4 x, 8 x and a lane's sums of them, and those of the lanes, are exact in
+    f32, the sum over the 98 slices is not (plain f32: 25 half steps off).  One rounding
+    is left where its rest is kept."""
+    F, N = 49920, 128
+    x = 0x29CBF8 * 2.0 ** -21
+    h = torch.full((1, F), x, device=DEV)
+    down = (torch.ones((1, N, F), dtype=torch.int8, device=DEV), torch.ones((1, N, F // 32), dtype=torch.float16, device=DEV))
+    ids, w, y = torch.zeros((1, 1), dtype=torch.int32, device=DEV), torch.ones((1, 1), device=DEV), torch.empty((1, N), device=DEV)
+    lk.lk_moe_down_q8(lk.Experts(down=down), "dequant", ids, w, y, h=h)
+    assert float((y.double() / (F * x) - 1).abs().max()) <= 2 * 2.0 ** -24
+    gate = (torch.ones((1, N, F), dtype=torch.int8, device=DEV), down[1])
+    hh = torch.empty((1, N), device=DEV)
+    lk.lk_moe_glu_q8(lk.Experts(gate=gate, up=gate), "dequant", ids, hh, x=h * 2.0 ** -17)
+    g = torch.tensor(F * x * 2.0 ** -17, dtype=torch.float64)
+    want = float(g * torch.sigmoid(g) * g)
+    # (the two products, an exponential of 2 units, three operations)
+    assert float((hh.double() / want - 1).abs().max()) <= 12 * 2.0 ** -24
+
+
+@pytest.mark.parametrize("K", [4224, 8192, 16384, 24704, 32768, 40064, 49920])
+def test_dequant_of_one_sign(lk, K):
+    """Products of one sign, where roundings add up: within 1e-5 of the sum, as lk_gemv_q8's."""
+    E, k, R = 2, 1, 256
+    gate, up, down = (experts(E, R, K, s, DEV) for s in (1, 2, 3))
+    for q, s in (gate, up, down):
+        q.abs_()
+    ids, w = torch.tensor([[1]], dtype=torch.int32, device=DEV), torch.ones((1, 1), device=DEV)
+    x = rows(1, K, K).abs()
+    h, y = torch.empty((1, R), device=DEV), torch.empty((1, R), device=DEV)
+    lk.lk_moe_glu_q8(lk.Experts(gate=gate, up=up), "dequant", ids, h, x=x)
+    want, tol = glu_ref(gate, up, {"x": x}, lk.LK_DEQUANT, ids, E)
+    assert bool(((h.double() - want).abs() <= tol).all())
+    lk.lk_moe_down_q8(lk.Experts(down=down), "dequant", ids, w, y, h=x)
+    want, tol = down_ref(down, {"x": x}, lk.LK_DEQUANT, ids, w, E)
+    assert bool(((y.double() - want).abs() <= tol).all())
+
+
+@pytest.mark.parametrize("K", [1024, 8192])
+def test_dequant_past_f32(lk, K):
+    """Sums that pass f32's range are infinite, whether a row is one slice or several."""
+    q = torch.ones((1, 128, K), dtype=torch.int8, device=DEV)
+    s = torch.ones((1, 128, K // 32), dtype=torch.float16, device=DEV)
+    ids, w, y = torch.zeros((1, 1), dtype=torch.int32, device=DEV), torch.ones((1, 1), device=DEV), torch.empty((1, 128), device=DEV)
+    h = torch.full((1, K), 1e36, device=DEV)
+    lk.lk_moe_down_q8(lk.Experts(down=(q, s)), "dequant", ids, w, y, h=h)
+    assert bool((y == math.inf).all())
+    lk.lk_moe_down_q8(lk.Experts(down=(q, s)), "dequant", ids, w, y, h=-h)
+    assert bool((y == -math.inf).all())
