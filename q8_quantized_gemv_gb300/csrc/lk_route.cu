@@ -6,11 +6,14 @@
 // give the next, and its lane drops it.  What this costs is latency (a launch,
 // one read, k + 1 rounds of two warp reductions); there are no bytes to speak of.
 //
-// Which experts are taken is decided in f32 where f32 can.  A score is within
-// 2^-20 of the row's largest (exp's argument is rounded to 2^-24 of |l - max|, exp to two
-// places, and e^-x (x + 16) 2^-24 is at most that; a sigmoid is within 2^-21), so values
-// further apart than twice that (and 2^-22 of themselves, for the rounding of
-// s + bias) are in the right order.  Where two neighbours of the order taken are nearer
+// Which experts are taken is decided in f32 where f32 can.  With u = 2^-24, of a softmax (e =
+// exp(-x), x = max - l) each e is within e (x + 4) u <= 4 u (the argument's rounding, exp to two
+// places), and a rounding of s takes u more: two scores are 10 u of the largest off each
+// other.  The sum is off by (V + 4) u of itself for its additions, V in a lane and 5 between them,
+// and by 8 u for its terms (the most that up to 1023 terms e (x + 4) beside a 1 come to), its
+// reciprocal by u: all scores by the same factor, so a difference of two by (V + 13) u of
+// the largest at most.  A sigmoid is within 2^-21.  So values further apart than (V + 24) u of the largest score
+// (2^-20), and 2^-22 of themselves, for the rounding of s + bias, are in the right order.  Where two neighbours of the order taken are nearer
 // (one row in some hundreds), f64 decides, whose exp is slow on this GPU's narrow
 // f64 pipe: for sigmoids of the experts in question alone, one a lane; with a
 // softmax, whose sum takes all of them, or where it is about groups, of the whole row (some
@@ -93,7 +96,7 @@ __device__ __forceinline__ int route_row(const RouteArgs& a, const float (&l)[V]
     const bool there = l[v] > -INFINITY && b[v] - b[v] == 0.0f;
     c[v] = !there ? none : by_logit ? (T)l[v] : p[v] + (T)b[v];
   }
-  const T slack = F32 ? (a.sigmoid ? (T)0x1p-20f : (T)0x1p-19f * pmax) : (T)0, part = F32 ? (T)0x1p-22f : (T)0;
+  const T slack = F32 ? (a.sigmoid ? (T)0x1p-20f : (T)((V + 24) * 0x1p-24f) * pmax) : (T)0, part = F32 ? (T)0x1p-22f : (T)0;
   bool sure = true;
 
   if (a.n_group > 1) {
