@@ -13,7 +13,8 @@
 // and by 8 u for its terms (the most that up to 1023 terms e (x + 4) beside a 1 come to), its
 // reciprocal by u: all scores by the same factor, so a difference of two by (V + 13) u of
 // the largest at most.  A sigmoid is within 2^-21.  So values further apart than (V + 24) u of the largest score
-// (2^-20), and 2^-22 of themselves, for the rounding of s + bias, are in the right order.  Where two neighbours of the order taken are nearer
+// (2^-20), and 2^-22 of themselves, for the rounding of s + bias, are in the right order; groups' sums of
+// two twice that, of the largest of what they are sums of.  Where two neighbours of the order taken are nearer
 // (one row in some hundreds), f64 decides, whose exp is slow on this GPU's narrow
 // f64 pipe: for sigmoids of the experts in question alone, one a lane; with a
 // softmax, whose sum takes all of them, or where it is about groups, of the whole row (some
@@ -115,7 +116,8 @@ __device__ __forceinline__ int route_row(const RouteArgs& a, const float (&l)[V]
         t2 = x > t1 ? t1 : x > t2 ? x : t2;
         t1 = x > t1 ? x : t1;
       }
-    const T val = sums && t2 > none ? t1 + t2 : t1;
+    const bool two = sums && t2 > none;
+    const T val = two ? t1 + t2 : t1;
     int rank = 0;
     for (int g = 0; g < a.n_group; ++g) {
       const T w = __shfl_sync(FULL, val, g);
@@ -123,10 +125,13 @@ __device__ __forceinline__ int route_row(const RouteArgs& a, const float (&l)[V]
     }
     const unsigned stay = __ballot_sync(FULL, lane < a.n_group && val > none && rank < a.top_group);
     if (F32 && !(by_logit && !sums)) {
+      // the largest of what the sums are of: the two may cancel
+      const float size = val > none ? fabsf((float)t1) + (two ? fabsf((float)t2) : 0.f) : 0.f;
+      const float most = __uint_as_float(__reduce_max_sync(FULL, __float_as_uint(size)));
       for (int g = 0; g < a.n_group; ++g) {
         const T w = __shfl_sync(FULL, val, g);
         if (lane < a.n_group && val > none && w > none && (((stay >> g) ^ (stay >> lane)) & 1u))
-          sure = sure && fabsf((float)(w - val)) > 2.0f * (float)slack + 2.0f * (float)part * fabsf((float)val);
+          sure = sure && fabsf((float)(w - val)) > 2.0f * (float)slack + 2.0f * (float)part * most;
       }
       if (!__all_sync(FULL, sure)) return ALL;
     }

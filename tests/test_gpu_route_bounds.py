@@ -59,3 +59,27 @@ def test_softmax_whose_sum_loses_the_most(lk, where):
     for k in (1, 2):
         ids, _ = route(lk, l, bias, k)
         assert ids[0].tolist() == want[0, :k].tolist()
+
+
+def test_group_sums_of_biases_of_both_signs(lk):
+    """A group's value is small, what it is the sum of is not: s + bias is rounded at the
+    bias's size."""
+    # equal scores, 2^-10 each; 1 + 2^-11 and odd half steps more: rounded down, rounded up
+    E = 1024
+    l, bias = np.zeros((1, E), np.float32), np.full(E, -5.0, np.float32)
+    b = -round(0.99 * 2.0 ** 24) * U
+    bias[[0, 1]] = 1 - 2.0 ** -11 + U, b + 3 * U
+    bias[[512, 513]] = 1 - 2.0 ** -11 + 3 * U, b
+    s = 2.0 ** -10 + bias.astype(np.float64)
+    assert s[0] + s[1] == s[512] + s[513] + U
+    ids, _ = route(lk, l, bias, 2, n_group=2, top_group=1, group_sum=2)
+    assert ids[0].tolist() == [0, 1]
+    # sigmoids; the f32 sums (a step of 100 is 2^-17) are off by more than they differ
+    for l in ([-0.33351847529411316, -0.1987764537334442, 0.09946588426828384, -0.6499243974685669],
+              [1.0161256790161133, 0.02421480044722557, -0.8853384852409363, 2.907092809677124],
+              [-0.3497023582458496, 0.5829254984855652, 0.22258533537387848, -0.0008985933382064104]):
+        l, bias = np.array([l], np.float32), np.float32([100, -100, 100, -100])
+        want, _, gap = route_ref(l, bias, "sigmoid", 2, 1, 2, 2, True, 1.0)
+        assert gap > 1e-9 and want[0].tolist() == [0, 1]
+        ids, _ = route(lk, l, bias, 2, score="sigmoid", n_group=2, top_group=1, group_sum=2)
+        assert ids[0].tolist() == [0, 1]
