@@ -58,7 +58,9 @@ typedef enum { LK_SCORE_SOFTMAX = 0, LK_SCORE_SIGMOID = 1 } lk_score;
  *   ids: the k experts of the largest c, the largest first (equal values: the
  *   lower number); weights: scale * s, with renorm nonzero over the sum of the k.
  * Choices are those of s, c and the groups' sums in f64: where f32 does not
- * decide, f64 does.  Weights are f32, within 2^-15 of their values relatively.
+ * decide, f64 does.  Weights are f32, within 2^-15 of their values relatively (2^-126 below
+ * f32's normal range); with renorm they are 0 where no sigmoid of the k is in
+ * that of f64 (logits below -708).
  * An expert whose logit is NaN or -inf, or whose bias is not finite, is out; a
  * logit of +inf counts as the largest f32.  Where fewer than k are left, the rest
  * are -1 with weight 0.

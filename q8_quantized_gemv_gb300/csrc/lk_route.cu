@@ -223,11 +223,10 @@ __device__ __forceinline__ int route_row(const RouteArgs& a, const float (&l)[V]
 
   T w = id >= 0 ? pmine : (T)0;
   if (a.renorm) {
-    if (!a.sigmoid) {
-      // from the chosen logits alone: the row's largest may be in no chosen group
-      const T lm = warp_max(id >= 0 ? (T)lmine : none);
-      w = id >= 0 ? exp_of((T)lmine - lm) : (T)0;
-    }
+    // from the chosen logits alone: the row's largest may be in no chosen group; below -40 a
+    // sigmoid is exp(l) to 2^-57, and f64 may not hold the smaller ones (none from -708 on)
+    const T lm = !F32 || !a.sigmoid ? warp_max(id >= 0 ? (T)lmine : none) : (T)0;
+    if (!a.sigmoid || lm < (T)-40) w = id >= 0 && (!a.sigmoid || lm >= (T)-708) ? exp_of((T)lmine - lm) : (T)0;
     T sum = w;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(FULL, sum, o);
