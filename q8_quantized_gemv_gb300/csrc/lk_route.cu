@@ -222,17 +222,23 @@ __device__ __forceinline__ int route_row(const RouteArgs& a, const float (&l)[V]
   }
 
   T w = id >= 0 ? pmine : (T)0;
+  bool low = F32 && id >= 0 && w < (T)0x1p-126f;
   if (a.renorm) {
     // from the chosen logits alone: the row's largest may be in no chosen group; below -40 a
     // sigmoid is exp(l) to 2^-57, and f64 may not hold the smaller ones (none from -708 on)
     const T lm = !F32 || !a.sigmoid ? warp_max(id >= 0 ? (T)lmine : none) : (T)0;
     if (!a.sigmoid || lm < (T)-40) w = id >= 0 && (!a.sigmoid || lm >= (T)-708) ? exp_of((T)lmine - lm) : (T)0;
+    low = F32 && id >= 0 && w < (T)0x1p-126f;
     T sum = w;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(FULL, sum, o);
-    // sigmoids this small: their quotient needs f64's range
-    if (F32 && sum < (T)1e-30f && __any_sync(FULL, id >= 0)) return ALL;
     w = sum > (T)0 ? w / sum : (T)0;
+  }
+  // Scores below f32's range whose weights need not be, for their sum or for the scale: f64 has them.
+  // (exp(-88) is below 2^-126; masked experts that fill up a row are far below)
+  if (F32 && __any_sync(FULL, low)) {
+    const float most = warp_max(id >= 0 ? lmine : -INFINITY), from = a.sigmoid ? fminf(most, 0.f) : most;
+    if (__any_sync(FULL, low && lmine - from > -88.0f - fmaxf(logf(fabsf(a.scale)), 0.f))) return ALL;
   }
   weight = (float)(w * (T)a.scale);
   return SURE;

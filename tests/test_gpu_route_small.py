@@ -33,7 +33,7 @@ def near(got, want):
     return np.all(np.abs(got - want) <= 2.0 ** -15 * np.abs(want) + 2.0 ** -126)
 
 
-@pytest.mark.parametrize("top", [-90.0, -150.0, -700.0, -707.5])
+@pytest.mark.parametrize("top", [-30.0, -90.0, -150.0, -700.0, -707.5])
 def test_sigmoids_over_their_sum(lk, top):
     """Of the k chosen, by their logits' differences: exp(l) / (1 + exp(l)) is as good as exp(l)
     there, and its quotients need no range."""
@@ -60,3 +60,21 @@ def test_sigmoids_below_64_bits(lk):
     ids, w = route(lk, logits, 3, score="sigmoid")
     e = np.exp(np.float64([0, -9, -20]))
     assert ids[0].tolist() == [3, 0, 1] and near(w[0], e / e.sum())
+
+
+@pytest.mark.parametrize("score,renorm", [("softmax", False), ("softmax", True), ("sigmoid", False), ("sigmoid", True)])
+@pytest.mark.parametrize("scale", [1.0, 2.5, 1e10, -1e20, 1e30])
+def test_scores_below_32_bits_times_a_scale(lk, score, renorm, scale):
+    """scale brings scores that f32 does not hold back into its range."""
+    logits = np.float32([[1.0, -60.0, -86.0, -88.0, -92.0, -100.0, -120.0, -145.0, -1e4, np.finfo(np.float32).min]])
+    l = logits[0].astype(np.float64)
+    if score == "softmax":
+        s = np.exp(l - l.max())
+        s /= s.sum()
+    else:
+        s = np.array([1 / (1 + math.exp(-x)) if x > -700 else 0.0 for x in l])
+    if renorm:
+        s /= s.sum()
+    ids, w = route(lk, logits, 10, score=score, renorm=renorm, scale=scale)
+    assert ids[0].tolist() == list(range(10))
+    assert near(w[0], float(np.float32(scale)) * s)
