@@ -37,7 +37,6 @@ constexpr int NW = 12;             // warps of a block
 constexpr int SLICE = 4096;        // bytes of K in a stage at most
 constexpr int DEPTH = 8;           // stages of a warp at most
 constexpr int kStatic = 1536;      // static shared memory, at most
-constexpr int kProducts = 16384;   // down: bytes of a block's products, about
 
 template <int Q>
 __host__ __device__ constexpr unsigned act_bytes(unsigned len) {
@@ -483,40 +482,23 @@ lk_status run(const MoeArgs& a, dim3 grid, int smem, int optin, int pdl, cudaStr
   return launch_moe_kernel(moe_kernel<Q, GLU, SLICED>, done, grid, NW * 32, smem, optin - kStatic, pdl, stream, a);
 }
 
-// Whether the tensor-core kernel, which reads a shared expert once, is faster than
-// single rows at the copy rate.  Measured (single rows against tensor cores, us; gate/up, down):
-// 128 experts 4096 x 1024, k 8, Int8Act 8 rows 80 / 82 and 41 / 50, 16 rows 152 / 130 and
-// 84 / 72, 32 rows 267 / 167 and 179 / 100; TwoPass 8 rows 83 / 87 and 50 / 50, 16 rows 162 / 132
-// and 97 / 73; 60 experts 2048 x 1408, k 4, Int8Act 8 rows 30 / 35 and 18 / 24, 16 rows 52 / 52 and
-// 32 / 35, TwoPass 34 / 38 and 21 / 24, 61 / 54 and 38 / 34; 8 experts 4096 x 2048, k 2, Int8Act 8
-// rows 35 / 36 and 18 / 18, TwoPass 42 / 39 and 23 / 19.
-bool rows_favoured(int E, int pairs, int mode, bool glu) {
-  return 16 * pairs >= (mode == 1 ? (glu ? 10 * E + 200 : 12 * E + 190) : 8 * E + 128);
-}
-
 template <bool GLU>
 lk_status launch_moe(MoeArgs& a, int mode, int M, int held, const lk_launch_cfg* cfg, cudaStream_t stream) {
   const int path = cfg ? cfg->path : 0;
   if (path == 1 || (path == 3 && mode == 0)) return LK_ERR_SHAPE;
   const bool held_fits = held_bytes(mode, a.K, held) <= kHeld;
   // (the tensor-core kernel streams the activation with the weights: it takes any length)
-  const bool rows = path == 3 || (path == 0 && mode != 0 && (!held_fits || rows_favoured(a.E, M * a.k, mode, GLU)));
+  bool rows = path == 3 || (path == 0 && mode != 0 && !held_fits);
   if (!rows && !held_fits) return LK_ERR_SHAPE;
   const DeviceInfo* d = device_info(nullptr);
   if (!d) return LK_ERR_CUDA;
   a.wait_ns = opt_wait_us > 0 ? (unsigned long long)opt_wait_us * 1000ull : 2000000000ull;
   a.err = error_word_ptr();
   if (!a.err) return LK_ERR_CUDA;
+  if (path == 0 && mode != 0 && !rows) rows = rows_favoured(a.E, a.rows, a.K, a.k, M, mode, GLU, d->sm_count);
   if (rows) return moe_rows(a, GLU, mode, M, cfg_pdl(cfg), stream);
   int smem = 0;
-  // blocks of a row of activations; down: enough that a block's products are few
-  int gx = d->sm_count / M;  // (all of them on the SMs at once: a second wave of blocks doubled the time)
-  if (gx < 1) gx = 1;
-  if (!GLU) {
-    const int least = (int)(((long)a.k * a.rows * 4 + kProducts - 1) / kProducts);
-    if (gx < least) gx = least;
-    if (gx > a.rows / 4) gx = a.rows / 4;
-  }
+  const int gx = row_blocks(a.rows, a.k, M, d->sm_count, GLU);
   const int products = GLU ? 0 : a.k * 4 * ((a.rows / 4 + gx - 1) / gx);
   const long quads = (GLU ? (long)a.k * a.rows / 2 : (long)a.k * a.rows / 4) / gx / NW;  // of a warp, about
   if (!fit(a, mode, held, products, quads, d->smem_optin, &smem)) return LK_ERR_SHAPE;
