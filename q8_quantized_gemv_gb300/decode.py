@@ -181,6 +181,9 @@ class Mixture:
         """Layer l's experts on the normed rows `act`, summed into y."""
         lk.lk_gemv_q8(*self.routers[l], mode, self.logits, M=self.ids.shape[0], cfg=cfg, **act)
         lk.lk_moe_route(self.logits, self.ids, self.weights, bias=self.biases[l], cfg=cfg, **self.how)
+        # the stack's path names a GEMV kernel; these have kernels of their own
+        cfg = lk.LkLaunchCfg.from_buffer_copy(cfg)
+        cfg.path = 0
         to = dict(self.words, cnt=self.cnt) if self.words else {}
         act = {n: t for n, t in act.items() if t is not None}
         lk.lk_moe_glu_q8(self.stacks[l], mode, self.ids, self.h, cfg=cfg, **act, **to)
