@@ -149,9 +149,12 @@ class Mixture:
         self.how = dict(score=score, n_group=n_group, top_group=top_group, group_sum=group_sum, renorm=renorm,
                         scale=scale)
 
-    def build(self, layers, hidden, batch, mode, seed, dev):
+    def check(self):
         if hasattr(self, "stacks"):
             raise ValueError("this Mixture has the experts of another stack")
+
+    def build(self, layers, hidden, batch, mode, seed, dev):
+        self.check()
         E, F, n = self.E, self.F, batch * self.k
 
         def stack(rows, K, s):
@@ -202,9 +205,12 @@ class Sampling:
     def __init__(self, temperature=None, top_k=None, top_p=None, min_p=None):
         self.given = dict(temperature=temperature, top_k=top_k, top_p=top_p, min_p=min_p)
 
-    def build(self, batch, dev):
+    def check(self):
         if hasattr(self, "set"):
             raise ValueError("this Sampling has the numbers of another stack")
+
+    def build(self, batch, dev):
+        self.check()
         self.set = {}
         for n, v in self.given.items():
             if v is not None:
@@ -238,19 +244,20 @@ class DecodeStack:
         # the gated pair runs as one fused launch; the chain and fused-prologue
         # forms keep the projections-alone dataflow
         self.glu = bool(glu) and not chain and not fused
-        self.attn = attn
+        self.attn, self.moe, self.sample = attn, moe, sample
+        # (all that is refused before anything is built: the parts stay free for another stack)
+        if attn is not None and (not self.glu or not fused_qkv):
+            raise ValueError("attn needs the decoder dataflow (glu=True) and the fused q|k|v matrix")
+        for name, part in (("moe", moe), ("sample", sample)):
+            if part is not None:
+                if not self.glu:
+                    raise ValueError(f"{name} needs the decoder dataflow (glu=True)")
+                part.check()
         if attn is not None:
-            if not self.glu or not fused_qkv:
-                raise ValueError("attn needs the decoder dataflow (glu=True) and the fused q|k|v matrix")
             attn.build(layers, q_dim, kv_dim, batch, s + 777_000, dev)
-        self.moe, self.sample = moe, sample
         if moe is not None:
-            if not self.glu:
-                raise ValueError("moe needs the decoder dataflow (glu=True)")
             moe.build(layers, hidden, batch, self.mode, s + 888_000, dev)
         if sample is not None:
-            if not self.glu:
-                raise ValueError("sample needs the decoder dataflow (glu=True)")
             sample.build(batch, dev)
         self.shapes = {"q": (q_dim, hidden), "k": (kv_dim, hidden), "v": (kv_dim, hidden),
                        "o": (hidden, q_dim), "gu": (2 * ffn, hidden), "down": (hidden, ffn)}
