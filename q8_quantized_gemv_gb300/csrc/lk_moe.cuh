@@ -56,23 +56,24 @@ inline int row_blocks(int rows, int k, int M, int sms, bool glu) {
 // By the bytes that each reads, in us (MB by TB/s): single rows a pair's matrices for each of
 // the pairs, from HBM or L2, wave after wave of blocks; the tensor cores those of the experts
 // touched, as uniform routing has it (absent pairs count: the host does not know them), and
-// a start and an end that grow with a matrix.  The constants are fitted to the times of 66
-// shapes in both modes (4 to 512 experts, matrices of 35 KB to 62 MB): the kernel chosen takes
-// 0.3 to 0.7 % more than the better one on the mean, 15 % at the worst.  Single rows against
-// tensor cores, us, gate/up and down: 128 experts 4096 x 1024, k 8, Int8Act 8 rows 79 / 84 and
-// 42 / 50, 16 rows 150 / 132 and 84 / 72, TwoPass 8 rows 83 / 87 and 50 / 51; 60 experts
-// 2048 x 1408, k 4, Int8Act 16 rows 51 / 52 and 30 / 35, 32 rows 97 / 66 and 59 / 45; 256
-// experts 4096 x 1024, k 8, Int8Act 16 rows 159 / 156 and 85 / 86, 20 rows 194 / 175 and 178
-// (two waves) / 98; 4 experts 1024 x 1024, k 1, 32 rows 16 / 9 and 10 / 9.
+// a start and an end that grow with a matrix.  The constants are fitted to the times of 90
+// shapes in both modes (1 to 64 rows, 4 to 512 experts, matrices of 35 KB to 62 MB): the kernel
+// chosen takes 0.3 to 0.7 % more than the better one on the mean, 19 % at the worst.  Single
+// rows against tensor cores, us, gate/up and down: 128 experts 4096 x 1024, k 8, Int8Act 8 rows
+// 79 / 84 and 42 / 50, 16 rows 150 / 132 and 84 / 72, TwoPass 8 rows 83 / 87 and 50 / 51; 60
+// experts 2048 x 1408, k 4, Int8Act 16 rows 51 / 52 and 30 / 35, 32 rows 97 / 66 and 59 / 45;
+// 256 experts 4096 x 1024, k 8, Int8Act 16 rows 159 / 156 and 85 / 86, 20 rows 194 / 175 and
+// 178 (two waves) / 98; 4 experts 1024 x 1024, k 1, 32 rows 16 / 9 and 10 / 9; 8 experts
+// 4096 x 14336, k 2, 1 row 41 / 56 and 33 / 59.
 inline bool rows_favoured(int E, int rows, int K, int k, int M, int mode, bool glu, int sms) {
   const double mb = (double)rows * K * (glu ? 2 : 1) * 1.0625e-6, pairs = (double)M * k;
-  const double touched = E * (1.0 - exp(-pairs / E));
+  const double touched = k < E ? E * (1.0 - pow(1.0 - (double)k / E, M)) : E;  // (a row's are different ones)
   const int waves = (int)(((long)row_blocks(rows, k, M, sms, glu) * M + sms - 1) / sms);
   struct Fit {
     double rate, start, grows, to;  // TB/s; us, us a MB, up to so many
   };
-  constexpr Fit fits[2][2] = {{{7.6, 1.0, 2.5, 3.0}, {7.4, 0.5, 3.25, 9.0}},   // Int8Act: down, gate/up
-                              {{6.2, 1.5, 1.25, 5.0}, {7.6, 1.0, 1.0, 9.0}}};  // TwoPass
+  constexpr Fit fits[2][2] = {{{7.4, 2.0, 1.75, 6.0}, {7.8, 0.0, 1.25, 20.0}},   // Int8Act: down, gate/up
+                              {{4.4, 2.0, 4.75, 3.0}, {7.2, 1.0, 1.0, 12.0}}};  // TwoPass
   const Fit& f = fits[mode - 1][glu];
   return waves * pairs * mb / f.rate >= touched * mb / 6.0 + f.start + f.grows * (mb < f.to ? mb : f.to);
 }

@@ -16,11 +16,11 @@ def test_the_kernel_chosen_is_about_the_faster(tmp_path):
         lines = [x for x in f if not x.startswith("#")]
     r = subprocess.run([exe], input="".join(lines), capture_output=True, text=True, timeout=60, check=True)
     chosen = [int(x) for x in r.stdout.split()]
-    assert len(chosen) == len(lines) >= 100
+    assert len(chosen) == len(lines) >= 300
     lost = {}
     for line, rows in zip(lines, chosen):
         *_, mode, op, t1, t2 = line.split()
         t = (float(t1), float(t2))
         lost.setdefault((mode, op), []).append(t[rows] / min(t) - 1)
     for of, v in lost.items():
-        assert max(v) <= 0.15 and sum(v) / len(v) <= 0.01, (of, max(v), sum(v) / len(v))
+        assert max(v) <= 0.2 and sum(v) / len(v) <= 0.01, (of, max(v), sum(v) / len(v))
