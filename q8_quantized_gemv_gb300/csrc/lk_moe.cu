@@ -93,7 +93,8 @@ struct ActLoad {
 };
 
 // What a lane has of its item's four rows: under Dequant its part of each row, in packed
-// halves, and for rows in several slices what rounding took off it; else partial (lane & 7) / 2 of row lane / 8, in the even lanes.
+// halves, and for rows in several slices what rounding took off it; else partial (lane & 7) / 2
+// of row lane / 8, in the even lanes.
 template <int Q>
 struct Partial {
   float p;
@@ -513,8 +514,8 @@ lk_status launch_moe(MoeArgs& a, int mode, int M, int held, const lk_launch_cfg*
 // Checks that both calls make of a stack's shape, the mode, the rows and k.
 lk_status check_shape(int E, int rows, int K, lk_mode mode, int M, int k, const lk_launch_cfg* cfg) {
   if (mode < LK_DEQUANT || mode > LK_TWOPASS || check_launch_cfg(cfg)) return LK_ERR_ARG;
-  if (E < 1 || E > LK_MOE_MAX_E || rows < 128 || rows % 128 || K < 128 || K % 128 || K > LK_MOE_MAX_LEN || M < 0 || M > LK_MAX_BATCH ||
-      k < 1 || k > LK_MOE_MAX_K)
+  if (E < 1 || E > LK_MOE_MAX_E || rows < 128 || rows % 128 || K < 128 || K % 128 || K > LK_MOE_MAX_LEN || M < 0 ||
+      M > LK_MAX_BATCH || k < 1 || k > LK_MOE_MAX_K)
     return LK_ERR_SHAPE;
   // rows of a stack, and tiles of all pairs, are 32-bit numbers
   if ((long)E * rows > 0x7fffffffL || (long)k * rows > 0x1fffffffL) return LK_ERR_SHAPE;

@@ -12,10 +12,10 @@
 // other.  The sum is off by (V + 4) u of itself for its additions, V in a lane and 5 between them,
 // and by 8 u for its terms (the most that up to 1023 terms e (x + 4) beside a 1 come to), its
 // reciprocal by u: all scores by the same factor, so a difference of two by (V + 13) u of
-// the largest at most.  A sigmoid is within 2^-21.  So values further apart than (V + 24) u of the largest score
-// (2^-20), and 2^-22 of themselves, for the rounding of s + bias, are in the right order; groups' sums of
-// two twice that, of the largest of what they are sums of.  Where two neighbours of the order taken are nearer
-// (one row in some hundreds), f64 decides, whose exp is slow on this GPU's narrow
+// the largest at most.  A sigmoid is within 2^-21.  So values further apart than (V + 24) u of
+// the largest score (2^-20), and 2^-22 of themselves, for the rounding of s + bias, are in the
+// right order; groups' sums of two twice that, of the largest of what they are sums of.  Where
+// two neighbours of the order taken are nearer (one row in some hundreds), f64 decides, whose exp is slow on this GPU's narrow
 // f64 pipe: for sigmoids of the experts in question alone, one a lane; with a
 // softmax, whose sum takes all of them, or where it is about groups, of the whole row (some
 // 8 us for 256 experts).  Without a bias the order is the logits' own, and exact.
@@ -97,7 +97,8 @@ __device__ __forceinline__ int route_row(const RouteArgs& a, const float (&l)[V]
     const bool there = l[v] > -INFINITY && b[v] - b[v] == 0.0f;
     c[v] = !there ? none : by_logit ? (T)l[v] : p[v] + (T)b[v];
   }
-  const T slack = F32 ? (a.sigmoid ? (T)0x1p-20f : (T)((V + 24) * 0x1p-24f) * pmax) : (T)0, part = F32 ? (T)0x1p-22f : (T)0;
+  const T slack = F32 ? (a.sigmoid ? (T)0x1p-20f : (T)((V + 24) * 0x1p-24f) * pmax) : (T)0;
+  const T part = F32 ? (T)0x1p-22f : (T)0;
   bool sure = true;
 
   if (a.n_group > 1) {

@@ -832,7 +832,8 @@ static __device__ __forceinline__ void run(const SampleArgs& a, unsigned char* s
           u64* weight = s.list;  // of the sorted keys (the block's own list is in sorted[] now)
           const bool k_there = by_k && bk < NB;
 #pragma unroll 1
-          for (unsigned i = threadIdx.x; i < listed; i += THREADS) weight[i] = w.template of<ONE>(value_of(s.sorted[i]));
+          for (unsigned i = threadIdx.x; i < listed; i += THREADS)
+            weight[i] = w.of<ONE>(value_of(s.sorted[i]));
           __syncthreads();
           if (warp == 0) {
             unsigned stay = listed;
@@ -973,7 +974,7 @@ static __device__ __forceinline__ void run(const SampleArgs& a, unsigned char* s
     for (int i0 = begin; i0 < end && run <= want; i0 += THREADS) {
       const int i = i0 + threadIdx.x;
       const float l = i < end ? clean(__ldcg(x + i)) : -INFINITY;
-      u64 e = i < end && key_of(l, i) <= last && (mp == 0.0f || w.enough(l, mp)) ? w.template of<FINE>(l) : 0ull;
+      u64 e = i < end && key_of(l, i) <= last && (mp == 0.0f || w.enough(l, mp)) ? w.of<FINE>(l) : 0ull;
       u64 all;
       const u64 r = run + block_before(e, all, s);
       if (r <= want && r + e > want) {

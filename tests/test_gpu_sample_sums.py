@@ -111,3 +111,19 @@ def test_min_p_at_every_place_of_the_order(lk, M, N):
     # (min_p at a token's weight rounded to f32 is 2^-25 from it on the mean, one case in four within
     # the margin: of the six pairs of twelve that are such, and hardly any other)
     assert undecided < drawn / 4
+
+
+@pytest.mark.parametrize("M", [1, 64])
+def test_the_largest_sums(lk, M):
+    """2^21 equal logits, whose sum is the most that whole numbers of 64 bits are asked
+    to hold, in many blocks and in as few as there are: the token is u's share of the row, exactly."""
+    N = 1 << 21
+    logits = torch.full((M, N), 2.5, device=DEV)
+    logits[::2] = -7
+    idx, prob = torch.zeros((M,), dtype=torch.int32, device=DEV), torch.zeros((M,), device=DEV)
+    for r in range(3):
+        u = (torch.arange(M, device=DEV, dtype=torch.float64) * 0.0153 + 0.31 * r).float()
+        u[-1] = (0.0, 0.5, 1 - 2.0 ** -24)[r]
+        lk.lk_sample(logits, u, idx, prob=prob)
+        assert torch.equal(idx.long(), (u.double() * N).floor().long().clamp(max=N - 1))
+        assert float((prob.double() * N - 1).abs().max()) <= 2.0 ** -22
